@@ -13,6 +13,16 @@ struct CompactLayers {
   void* v[E3_MAX_LAYERS];
 };
 
+// Per-layer pointers of a 4-bit cache (kernel parameter).
+struct Kv4Layers {
+  void* k[E3_MAX_LAYERS];
+  void* v[E3_MAX_LAYERS];
+  void* ks[E3_MAX_LAYERS];
+  void* vs[E3_MAX_LAYERS];
+  float k_unit[E3_MAX_LAYERS];
+  float v_unit[E3_MAX_LAYERS];
+};
+
 e3_status launch_expand(const float* logits, int B, int F, int V, int k, int W, float inv_temp,
                         const float* parent_score, const int32_t* parent_id, int depth, int cand_offset,
                         const e3_cand& c, int32_t* next_id, float* next_score, bool sampled, uint64_t seed,
@@ -74,5 +84,27 @@ e3_status launch_accept_sampled(const int32_t* tok, const int32_t* parent, const
 
 e3_status launch_compact(const CompactLayers& layers, const e3_kv_layer& geo, int L, int B, const int32_t* path,
                          const int32_t* acc_len, int D, int32_t* kv_len, int32_t* dev_err, cudaStream_t s);
+
+e3_status launch_qkv_append(const void* qkv, size_t ld, int B, int R, const int32_t* n_rows, int H, const float* q_norm,
+                            const float* k_norm, float eps, const e3_rope* rope, const int32_t* pos, void* Q,
+                            const e3_kv_layer& kv, const int32_t* kv_len, int32_t* dev_err, cudaStream_t s);
+e3_status launch_kv4_append(const Kv4Layers& l4, const e3_kv4_layer& geo, const CompactLayers& src,
+                            const e3_kv_layer& sgeo, int L, int B, int max_rows, const int32_t* rows,
+                            const int32_t* n_rows, int n_add, const int32_t* kv_len, int32_t* kv_len_next,
+                            int32_t* dev_err, cudaStream_t s);
+e3_status launch_kv4_read(const Kv4Layers& l4, const e3_kv4_layer& geo, const CompactLayers& dst,
+                          const e3_kv_layer& dgeo, int L, int B, int max_rows, const int32_t* first,
+                          const int32_t* n_rows, int32_t* dev_err, cudaStream_t s);
+size_t verify4_workspace_bytes(int B, int R, int H, int KVH, int hd, int max_kv_len);
+e3_status launch_verify4(const void* Q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
+                         const uint64_t* mask, int B, int R, int H, int max_kv_len, float sm_scale, void* O, float* lse,
+                         int32_t* dev_err, void* ws, size_t ws_bytes, cudaStream_t s);
+e3_status launch_logits_process(const float* logits, int B, int R, int V, const float* temp, const uint16_t* counts,
+                                const int32_t* tok, const int32_t* parent, const float* pen, const int32_t* bias_tok,
+                                const float* bias_val, int n_bias, const uint32_t* allow, const int32_t* allow_row,
+                                int n_allow, float* out, float* row_max, uint64_t* row_Q, int32_t* row_argmax,
+                                int32_t* dev_err, cudaStream_t s);
+e3_status launch_token_counts(uint16_t* counts, int V, int B, const int32_t* tokens, const int32_t* n, int n_add,
+                              int max_n, int prompt, cudaStream_t s);
 
 }  // namespace e3

@@ -15,9 +15,10 @@ LIB_PATH = os.path.join(_HERE, "_build", "libeagle3.so")
 
 E3_OK = 0
 E3_F32, E3_BF16 = 0, 1
-E3_DEV_ERR_NONFINITE, E3_DEV_ERR_CAPACITY, E3_DEV_ERR_TIMEOUT = 1, 2, 4
+E3_DEV_ERR_NONFINITE, E3_DEV_ERR_CAPACITY, E3_DEV_ERR_TIMEOUT, E3_DEV_ERR_MASKED = 1, 2, 4, 8
 E3_ACCEPT_TREE_DET, E3_ACCEPT_SAMPLED = 0, 1
 E3_KV_PREFIX_STABLE = 1
+E3_ROPE_PLAIN, E3_ROPE_LINEAR, E3_ROPE_WAVELEN, E3_ROPE_YARN = 0, 1, 2, 3
 E3_KV_SELFTEST_STALL = 0x40000000  # failure-detection self-test only
 STATUS_NAMES = {0: "E3_OK", 1: "E3_ERR_INVALID_ARG", 2: "E3_ERR_SHAPE", 3: "E3_ERR_UNSUPPORTED",
                 4: "E3_ERR_CAPACITY", 5: "E3_ERR_NONFINITE", 6: "E3_ERR_CUDA", 7: "E3_ERR_TIMEOUT"}
@@ -25,6 +26,8 @@ SYMBOLS = ["eagle3_fuse", "eagle3_fuse_workspace_bytes", "eagle3_fuse_noalloc",
            "eagle3_fuse_noalloc_max_scratch_bytes", "eagle3_expand", "eagle3_expand_sampled", "tree_build_mask",
            "tree_verify_attn", "eagle3_verify_workspace_bytes", "lmhead_logits", "spec_accept",
            "spec_accept_sampled", "kv_compact", "eagle3_draft_step", "eagle3_draft_workspace_bytes",
+           "eagle3_rope_init", "tree_qkv_append", "kv4_append", "kv4_read", "tree_verify_attn4",
+           "eagle3_verify4_workspace_bytes", "tree_logits_process", "token_counts_add",
            "eagle3_budget_init", "eagle3_budget_update", "eagle3_last_error",
            "eagle3_abi_version", "eagle3_launch_count"]
 MAX_BUDGET_LEVELS = 16
@@ -54,6 +57,25 @@ class e3_kv_layer(ctypes.Structure):
                 ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
                 ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int), ("dt", ctypes.c_int),
                 ("flags", ctypes.c_int)]
+
+
+class e3_kv4_layer(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("k_unit", ctypes.c_float), ("v_unit", ctypes.c_float),
+                ("flags", ctypes.c_int)]
+
+
+class e3_rope_spec(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("scaling", ctypes.c_int),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("orig_len", ctypes.c_double), ("amp", ctypes.c_double)]
+
+
+class e3_rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("amp", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * 128)]
 
 
 class e3_drafter(ctypes.Structure):
@@ -102,6 +124,16 @@ def _load() -> ctypes.CDLL:
         "eagle3_draft_step": (I, [ctypes.POINTER(e3_drafter), ctypes.POINTER(e3_kv_layer), P, I, I, I, I, P, I, I,
                                   P, I, I, ctypes.POINTER(e3_cand), P, P, P, P, P, P, P, P, P, S, P, P]),
         "eagle3_draft_workspace_bytes": (S, [ctypes.POINTER(e3_drafter), I, I, I, I]),
+        "eagle3_rope_init": (I, [ctypes.POINTER(e3_rope_spec), ctypes.POINTER(e3_rope)]),
+        "tree_qkv_append": (I, [P, S, I, I, P, I, P, P, F, ctypes.POINTER(e3_rope), P, P, ctypes.POINTER(e3_kv_layer),
+                                P, P, P]),
+        "kv4_append": (I, [ctypes.POINTER(e3_kv4_layer), ctypes.POINTER(e3_kv_layer), I, I, I, P, P, I, P, P, P, P]),
+        "kv4_read": (I, [ctypes.POINTER(e3_kv4_layer), ctypes.POINTER(e3_kv_layer), I, I, I, P, P, P, P]),
+        "tree_verify_attn4": (I, [P, ctypes.POINTER(e3_kv4_layer), ctypes.POINTER(e3_kv_layer), P, P, I, I, I, I, F, P, P,
+                                  P, P, S, P]),
+        "eagle3_verify4_workspace_bytes": (S, [I, I, I, I, I, I]),
+        "tree_logits_process": (I, [P, I, I, I, P, P, P, P, P, P, P, I, P, P, I, P, P, P, P, P, P]),
+        "token_counts_add": (I, [P, I, I, P, P, I, I, I, P]),
         "eagle3_budget_init": (I, [ctypes.POINTER(e3_budget_policy), P, I]),
         "eagle3_budget_update": (I, [ctypes.POINTER(e3_budget_policy), P, I, P, F, F, P]),
         "eagle3_last_error": (ctypes.c_char_p, []),
@@ -152,6 +184,12 @@ def make_cand(tok, parent, score, depth, cap: int) -> e3_cand:
 def make_kv_layer(k, v, page_table, n_pages, page_size, max_pages, n_kv_heads, head_dim, dt, flags=0) -> e3_kv_layer:
     return e3_kv_layer(ptr(k), ptr(v), ptr(page_table), n_pages, page_size, max_pages, n_kv_heads, head_dim, dt,
                        flags)
+
+
+def make_kv4_layer(k, v, k_scale, v_scale, page_table, n_pages, page_size, max_pages, n_kv_heads, head_dim, k_unit=1.0,
+                   v_unit=1.0, flags=0) -> e3_kv4_layer:
+    return e3_kv4_layer(ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), ptr(page_table), n_pages, page_size, max_pages,
+                        n_kv_heads, head_dim, k_unit, v_unit, flags)
 
 
 def abi_version() -> int:
@@ -248,6 +286,70 @@ def kv_compact(layers, B, path, acc_len, D, kv_len, dev_err=None, stream=None):
     arr = (e3_kv_layer * len(layers))(*layers)
     _check("kv_compact", _lib.kv_compact(arr, len(layers), B, ptr(path), ptr(acc_len), D, ptr(kv_len),
                                          ptr(dev_err), _stream(stream)))
+
+
+def eagle3_rope_init(rot_dim, base, interleaved=False, scaling=E3_ROPE_PLAIN, factor=1.0, low=1.0, high=4.0,
+                     orig_len=8192.0, amp=0.0) -> e3_rope:
+    """The rotary frequencies of a head (host struct) for tree_qkv_append."""
+    spec = e3_rope_spec(rot_dim, int(interleaved), scaling, base, factor, low, high, orig_len, amp)
+    rope = e3_rope()
+    _check("eagle3_rope_init", _lib.eagle3_rope_init(ctypes.byref(spec), ctypes.byref(rope)))
+    return rope
+
+
+def tree_qkv_append(qkv, ld, B, R, n_rows, n_q_heads, q_norm, k_norm, eps, rope: e3_rope | None, pos, Q,
+                    kv: e3_kv_layer, kv_len, dev_err=None, stream=None):
+    """ld: elements from one qkv row to the next; kv_len None: rows go to slots 0 .. R-1 (a tree tail)."""
+    _check("tree_qkv_append",
+           _lib.tree_qkv_append(ptr(qkv), ld, B, R, ptr(n_rows), n_q_heads, ptr(q_norm), ptr(k_norm), eps,
+                                None if rope is None else ctypes.byref(rope), ptr(pos), ptr(Q), ctypes.byref(kv),
+                                ptr(kv_len), ptr(dev_err), _stream(stream)))
+
+
+def _layer_arrays(fn, layers, others):
+    if len(layers) != len(others):
+        raise ValueError(f"{fn}: {len(layers)} 4-bit layers and {len(others)} 16-bit ones")
+    return (e3_kv4_layer * len(layers))(*layers), (e3_kv_layer * len(others))(*others)
+
+
+def kv4_append(layers, src, B, max_rows, rows, n_rows, n_add, kv_len, kv_len_next, dev_err=None, stream=None):
+    """layers/src: sequences of e3_kv4_layer / bf16 e3_kv_layer, one per layer."""
+    a4, a16 = _layer_arrays("kv4_append", layers, src)
+    _check("kv4_append", _lib.kv4_append(a4, a16, len(a4), B, max_rows, ptr(rows), ptr(n_rows), n_add, ptr(kv_len),
+                                         ptr(kv_len_next), ptr(dev_err), _stream(stream)))
+
+
+def kv4_read(layers, dst, B, max_rows, first, n_rows, dev_err=None, stream=None):
+    """layers/dst: sequences of e3_kv4_layer / bf16 e3_kv_layer, one per layer."""
+    a4, a16 = _layer_arrays("kv4_read", layers, dst)
+    _check("kv4_read", _lib.kv4_read(a4, a16, len(a4), B, max_rows, ptr(first), ptr(n_rows), ptr(dev_err),
+                                     _stream(stream)))
+
+
+def eagle3_verify4_workspace_bytes(B, R, n_q_heads, n_kv_heads, head_dim, max_kv_len) -> int:
+    return int(_lib.eagle3_verify4_workspace_bytes(B, R, n_q_heads, n_kv_heads, head_dim, max_kv_len))
+
+
+def tree_verify_attn4(Q, kv: e3_kv4_layer, tail: e3_kv_layer, kv_len, mask, B, R, n_q_heads, max_kv_len, sm_scale, O,
+                      lse, dev_err=None, ws=None, ws_bytes=0, stream=None):
+    _check("tree_verify_attn4",
+           _lib.tree_verify_attn4(ptr(Q), ctypes.byref(kv), ctypes.byref(tail), ptr(kv_len), ptr(mask), B, R, n_q_heads,
+                                  max_kv_len, sm_scale, ptr(O), ptr(lse), ptr(dev_err), ptr(ws), ws_bytes,
+                                  _stream(stream)))
+
+
+def tree_logits_process(logits, B, R, V, temp_per_row, counts, tok, parent, pen, bias_tok, bias_val, n_bias, allow,
+                        allow_row, n_allow, out, row_max, row_Q, row_argmax, dev_err=None, stream=None):
+    _check("tree_logits_process",
+           _lib.tree_logits_process(ptr(logits), B, R, V, ptr(temp_per_row), ptr(counts), ptr(tok), ptr(parent),
+                                    ptr(pen), ptr(bias_tok), ptr(bias_val), n_bias, ptr(allow), ptr(allow_row), n_allow,
+                                    ptr(out), ptr(row_max), ptr(row_Q), ptr(row_argmax), ptr(dev_err),
+                                    _stream(stream)))
+
+
+def token_counts_add(counts, V, B, tokens, n, n_add, max_n, prompt=False, stream=None):
+    _check("token_counts_add", _lib.token_counts_add(ptr(counts), V, B, ptr(tokens), ptr(n), n_add, max_n,
+                                                     int(bool(prompt)), _stream(stream)))
 
 
 def budget_policy(levels, min_level=0, max_level=None, base_level=0, alpha=0.5, low=0.25, high=0.75, spread=0.25,

@@ -85,6 +85,7 @@ typedef enum { E3_F32 = 0, E3_BF16 = 1 } e3_dtype;
                                   compaction); an internal candidate list of
                                   eagle3_expand overflowed (not expected) */
 #define E3_DEV_ERR_TIMEOUT 4   /* a bounded on-device wait ran out; outputs invalid */
+#define E3_DEV_ERR_MASKED 8    /* tree_logits_process: a row with no token left */
 
 /* Limits of this build. */
 #define E3_MAX_TOPK 32     /* k of eagle3_expand */
@@ -369,6 +370,212 @@ E3_API e3_status spec_accept_sampled(const int32_t* tok, const int32_t* parent,
 E3_API e3_status kv_compact(const e3_kv_layer* layers, int L, int B, const int32_t* path,
                      const int32_t* acc_len, int D, int32_t* kv_len, int32_t* dev_err,
                      e3_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * eagle3_rope_init (host): the rotary frequencies of a head, for tree_qkv_append.
+ * rot_dim (even, 2..256) leading dimensions of a head rotate; pair i < rot_dim/2 is
+ *   (x[i], x[i + rot_dim/2]), or (x[2i], x[2i+1]) with interleaved != 0, and turns by
+ *   pos * f_i:  (a, b) -> amp * (a cos - b sin, b cos + a sin).
+ * f_i = base^(-2i/rot_dim), then by `scaling`:
+ *   E3_ROPE_PLAIN    f_i;                                    amp = 1
+ *   E3_ROPE_LINEAR   f_i / factor;                           amp = 1
+ *   E3_ROPE_WAVELEN  by the turns n = orig_len f_i / (2 pi) of the trained length,
+ *                    w = clamp((n - low)/(high - low), 0, 1):
+ *                    f_i ((1 - w)/factor + w);               amp = 1
+ *   E3_ROPE_YARN     by the pair's index, the ramp running between the pairs that make
+ *                    `high` and `low` turns in the trained length: with
+ *                    d(n) = rot_dim ln(orig_len/(2 pi n)) / (2 ln base),
+ *                    a = max(floor(d(high)), 0), e = min(ceil(d(low)), rot_dim - 1),
+ *                    w = clamp((i - a)/max(e - a, 0.001), 0, 1):
+ *                    f_i (w/factor + 1 - w);                 amp = 0.1 ln(factor) + 1
+ * amp > 0 in the spec replaces that factor (0: the scaling's own).
+ * Frequencies are computed in double and held as 64-bit fractions of a turn, so that
+ * pos * f_i modulo a turn is one integer product that rounds nothing, however far
+ * the position.
+ * The struct is plain data: keep it, copy it, use it from several threads.
+ * ------------------------------------------------------------------------- */
+typedef enum { E3_ROPE_PLAIN = 0, E3_ROPE_LINEAR = 1, E3_ROPE_WAVELEN = 2, E3_ROPE_YARN = 3 } e3_rope_scaling;
+typedef struct {
+  int rot_dim;
+  int interleaved;
+  int scaling;     /* e3_rope_scaling */
+  double base;     /* > 1 */
+  double factor;   /* > 0; scalings other than PLAIN */
+  double low;      /* turns; WAVELEN and YARN, 0 < low < high */
+  double high;
+  double orig_len; /* trained length; WAVELEN and YARN, > 0 */
+  double amp;      /* 0: the scaling's own */
+} e3_rope_spec;
+typedef struct {
+  int rot_dim;
+  int interleaved;
+  float amp;
+  uint64_t turns[128]; /* f_i / (2 pi) in units of 2^-64 turns */
+} e3_rope;
+E3_API e3_status eagle3_rope_init(const e3_rope_spec* spec /* host */, e3_rope* rope /* host */);
+
+/* ---------------------------------------------------------------------------
+ * tree_qkv_append: from one layer's projected rows to its attention's inputs --
+ * norms of each query and key head, rotary positions, and the append of K and V
+ * to the paged cache, in one pass.  It writes what tree_verify_attn and
+ * tree_verify_attn4 read ("Thinking Budget 与 EAGLE-3", 一棵候选树怎样被验证: the
+ * nodes' K/V are temporary entries behind the prefix; "EAGLE 系列与 DFlash", §二
+ * 关键新增步骤①: a node's position follows from its depth).
+ * Row r < n_rows[b] of request b (n_rows NULL: all R; values are clamped to
+ * [0, R]): qkv row b*R + r starts at qkv + (b*R + r)*ld elements and holds
+ * [n_q_heads | n_kv_heads | n_kv_heads] heads of head_dim values: q, k, v.
+ *   q_norm/k_norm (fp32 [head_dim], NULL: none): x = x / sqrt(mean(x^2) + eps) * norm
+ *   rope (host, NULL: none): rotation at pos[b*R + r] (any int32)
+ *   q -> Q[b][r], k and v -> logical slot kv_len[b] + r of the cache (kv_len NULL:
+ *   slot r, the layout of a tree tail).
+ * All arithmetic in fp32, one rounding to kv->dt at the end; v is copied.
+ * Rows r >= n_rows[b] and their slots are left as they were.  A row whose slot has
+ * no page (past max_pages, a page id out of range, kv_len[b] < 0) sets
+ * E3_DEV_ERR_CAPACITY; its Q is written, its K and V are not.
+ * qkv, Q: dtype kv->dt, 16-byte aligned rows take the vector path, others a
+ * scalar one.  The output buffers must not overlap qkv.
+ * Limits: rope->rot_dim <= head_dim; ld >= (n_q_heads + 2 n_kv_heads) head_dim;
+ * B*R < 2^31; kv->flags 0 or E3_KV_PREFIX_STABLE (ignored).
+ * ------------------------------------------------------------------------- */
+E3_API e3_status tree_qkv_append(const void* qkv, size_t ld, int B, int R, const int32_t* n_rows, int n_q_heads,
+                                 const float* q_norm, const float* k_norm, float eps, const e3_rope* rope,
+                                 const int32_t* pos, void* Q, const e3_kv_layer* kv /* host struct */,
+                                 const int32_t* kv_len, int32_t* dev_err, e3_stream_t stream);
+
+/* One layer's paged KV cache held in 4 bits.  Each group of 16 consecutive head
+ * dimensions of a row shares a scale e (fp8 e4m3) and holds 4-bit values c (e2m1:
+ * +-{0, 0.5, 1, 1.5, 2, 3, 4, 6}); the value is c * e * unit.  c * e has at most six
+ * significant bits, so it is exact in bf16 and fp16.
+ * k, v: [n_pages][n_kv_heads][page_size][head_dim/2] bytes, byte i of a row = dims 2i
+ *   (low four bits) and 2i+1;  k_scale, v_scale: [n_pages][n_kv_heads][page_size]
+ *   [head_dim/16] bytes.  Slots as in e3_kv_layer.
+ * k_unit, v_unit: one factor per layer, a power of two in [2^-60, 2^60] (1 suits
+ *   values between about 0.01 and 2000 in magnitude); being a power of two it keeps
+ *   the grid exact. */
+typedef struct {
+  void* k;
+  void* v;
+  void* k_scale;
+  void* v_scale;
+  const int32_t* page_table; /* [B][max_pages], device */
+  int n_pages;
+  int page_size;             /* a multiple of 16 */
+  int max_pages;
+  int n_kv_heads;
+  int head_dim;              /* 64 or 128 */
+  float k_unit;
+  float v_unit;
+  int flags;                 /* 0 or E3_KV_PREFIX_STABLE (see tree_verify_attn4) */
+} e3_kv4_layer;
+
+/* ---------------------------------------------------------------------------
+ * kv4_append: rows of a bf16 cache to the end of the 4-bit cache, all layers -- the
+ * commit of a round whose tree K/V live in a bf16 tail (only the accepted path is
+ * ever quantized; kv_compact's counterpart), or of a prompt.
+ * Request b appends n = n_rows[b] + n_add rows (n <= 0: none): row j < n is logical
+ * slot rows[b*max_rows + j] of src (rows NULL: slot j) and goes to logical slot
+ * kv_len[b] + j of the 4-bit cache; kv_len_next[b] = kv_len[b] + max(n, 0)
+ * (kv_len_next NULL: not written; it may be kv_len itself).
+ * After spec_accept: rows = path, n_rows = acc_len, n_add = 1, max_rows = D + 1.
+ * Each group of 16 values x:  e = e4m3(min(max|x| / (6 unit), 448)) to nearest even,
+ *   c = the nearest e2m1 value to x / (e unit), ties to the even code, +-6 beyond
+ *   (e = 0: c = 0), the sign of x kept.  NaN is stored as 0 and +-Inf as the largest
+ *   finite bf16; both set E3_DEV_ERR_NONFINITE.
+ * n > max_rows, or rows beyond the 4-bit cache's pages, set E3_DEV_ERR_CAPACITY and
+ * leave the request as it was (its length too); a page id out of range (either side)
+ * sets it and skips that row.
+ * layers, src: host arrays of L descriptors of one geometry each (as kv_compact);
+ * src bf16.  The two caches must not overlap.
+ * Limits: 1 <= L <= E3_MAX_LAYERS, 1 <= B <= 65535, max_rows >= 1.
+ * ------------------------------------------------------------------------- */
+E3_API e3_status kv4_append(const e3_kv4_layer* layers, const e3_kv_layer* src, int L, int B, int max_rows,
+                            const int32_t* rows, const int32_t* n_rows, int n_add, const int32_t* kv_len,
+                            int32_t* kv_len_next, int32_t* dev_err, e3_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * kv4_read: rows of the 4-bit cache back to bf16 values (handing a request to a
+ * bf16 cache): logical slots first[b] + j, j < n_rows[b] <= max_rows, of every layer
+ * go to logical slots j of dst.  Exact (see e3_kv4_layer) where the value is a normal
+ * bf16 number.  first NULL: from slot 0.  Errors as kv4_append.
+ * ------------------------------------------------------------------------- */
+E3_API e3_status kv4_read(const e3_kv4_layer* layers, const e3_kv_layer* dst, int L, int B, int max_rows,
+                          const int32_t* first, const int32_t* n_rows, int32_t* dev_err, e3_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * tree_verify_attn4: tree_verify_attn over a prefix held in 4 bits.
+ * For request b (P = kv_len[b]), node i < R, query head h < n_q_heads:
+ *   keys = prefix [0, P) of the 4-bit cache, and slots j < R of the bf16 tail with
+ *   bit j of mask[b][i];  o = softmax(sm_scale * q . k) v,  lse = ln(sum exp(...)).
+ * The tail (host struct, bf16, same KV heads and head_dim; its page table has a row
+ * per request) holds the nodes' K/V at logical slots 0 .. R-1 (tree_qkv_append with
+ * kv_len NULL writes it there); they are read at full precision.
+ * Q, O: [B][R][n_q_heads][head_dim] bf16; lse: [B][R][n_q_heads] fp32.
+ * A row that sees no key (empty prefix and mask) gets o = 0, lse = -Inf.  Slots that
+ * a row does not see have no effect on it, whatever they hold; a row that sees a
+ * tail node with a NaN or Inf in V gets NaN in all of o.
+ * kv_len[b] outside [0, max_kv_len] or beyond the pages sets E3_DEV_ERR_CAPACITY and
+ * leaves the request's outputs unwritten; a page id out of range sets it and makes
+ * the request's outputs unspecified.
+ * Limits: head_dim 64 or 128; R <= 256; n_q_heads % n_kv_heads == 0; tail pages hold R
+ *   slots.  E3_KV_PREFIX_STABLE in kv->flags: the promise of tree_verify_attn.
+ * ws: eagle3_verify4_workspace_bytes(...) bytes of device scratch, 16-byte aligned;
+ *   calls that may overlap on the GPU need scratch of their own.
+ * ------------------------------------------------------------------------- */
+E3_API e3_status tree_verify_attn4(const void* Q, const e3_kv4_layer* kv /* host struct */,
+                                   const e3_kv_layer* tail /* host struct */, const int32_t* kv_len,
+                                   const uint64_t* mask, int B, int R, int n_q_heads, int max_kv_len, float sm_scale,
+                                   void* O, float* lse, int32_t* dev_err, void* ws, size_t ws_bytes,
+                                   e3_stream_t stream);
+E3_API size_t eagle3_verify4_workspace_bytes(int B, int R, int n_q_heads, int n_kv_heads, int head_dim,
+                                             int max_kv_len);
+
+/* ---------------------------------------------------------------------------
+ * tree_logits_process: penalties, biases and grammar masks on the node logits, and
+ * the statistics that spec_accept reads; between lmhead_logits and spec_accept.
+ * Row i of request b predicts the token after node i, so the tokens of its path
+ * (node i and its ancestors, without the root: the root is the answer's last token
+ * and is in counts) count as part of the answer.  For token v, in this order, each
+ * operation rounded to fp32:
+ *   c = (counts[b][v] & 32767) + occurrences of v on the path;
+ *   seen: c > 0, or bit 15 of counts[b][v] (v occurs in the prompt);
+ *   z = logits;  seen: z = z > 0 ? z / rep : z * rep;
+ *   c > 0: z = (z - freq * c) - pres;
+ *   z = z + (the biases of v, summed in list order);
+ *   z = -Inf where the grammar does not allow v.
+ * out[row][v] = z, and with T = temp_per_row[row] (as lmhead_logits) s = z * (1/T):
+ *   row_max, row_argmax (lowest id on ties), row_Q = sum floor(2^40 E(s - row_max)).
+ * A -Inf logit means a token that is ruled out.  NaN or +Inf in a z sets
+ * E3_DEV_ERR_NONFINITE, a row that is -Inf throughout E3_DEV_ERR_MASKED; both give
+ * row_max = NaN, row_Q = 0, row_argmax = -1, which spec_accept reports in status.
+ * counts [B][V] uint16, kept by token_counts_add (NULL: no token seen).  tok, parent:
+ * [B][R] from tree_build_mask (NULL both: no paths, R independent rows); tokens
+ * outside [0, V) are skipped.  pen: [B][3] fp32 {rep > 0, freq, pres} (NULL: 1, 0, 0).
+ * bias_tok/bias_val: [B][n_bias] (NULL with n_bias = 0); entries with a token outside
+ * [0, V) are skipped; a bias of -Inf rules the token out.
+ * allow: [n_allow][ceil(V/32)] uint32, bit v % 32 of word v / 32 (NULL: no grammar);
+ * allow_row: [B][R], the row of allow that node follows, outside [0, n_allow): all
+ * allowed (NULL: row b*R + i).
+ * out may be logits itself.  With sampled drafts the accept step stays exact: it reads
+ * the processed rows as the target's.
+ * Limits: n_bias <= 1024; R <= 256; every path has at most E3_MAX_DEPTH nodes beside
+ * the root; V >= 1, V < 2^30.
+ * ------------------------------------------------------------------------- */
+E3_API e3_status tree_logits_process(const float* logits, int B, int R, int V, const float* temp_per_row,
+                                     const uint16_t* counts, const int32_t* tok, const int32_t* parent,
+                                     const float* pen, const int32_t* bias_tok, const float* bias_val, int n_bias,
+                                     const uint32_t* allow, const int32_t* allow_row, int n_allow, float* out,
+                                     float* row_max, uint64_t* row_Q, int32_t* row_argmax, int32_t* dev_err,
+                                     e3_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * token_counts_add: adds tokens [b][0 .. min(n[b] + n_add, max_n)) to counts [B][V]
+ * (the low 15 bits count the answer's occurrences, saturating at 32767); prompt != 0
+ * sets bit 15 instead.  After spec_accept: tokens = out_tok, n = acc_len, n_add = 1,
+ * max_n = D + 1.  Tokens outside [0, V) are skipped.  counts must be 4-byte aligned and
+ * hold B*V rounded up to an even number of entries.
+ * ------------------------------------------------------------------------- */
+E3_API e3_status token_counts_add(uint16_t* counts, int V, int B, const int32_t* tokens, const int32_t* n, int n_add,
+                                  int max_n, int prompt, e3_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * eagle3_draft_step: one step of the drafter -- a single decoder layer -- for
