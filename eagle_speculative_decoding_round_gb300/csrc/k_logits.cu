@@ -7,19 +7,32 @@
 // before the accept step, each node with the tokens of its own path.
 //
 // Bound: memory (the row in, the row out).
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <atomic>
+
 #include "e3_common.cuh"
 #include "e3_kernels.h"
 
 namespace e3 {
 
+namespace cg = cooperative_groups;
+
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 256;
+constexpr int kBatch = 8;  // pieces of a thread whose loads are in flight together
 constexpr int kMaxBias = 1024;
+constexpr int kMaxR = E3_MAX_NODES + 1;
+constexpr int kPer = 16384;     // tokens of a CTA at three CTAs an SM (64 KB of the row each)
+constexpr int kSeenCap = 1024;  // seen tokens of a CTA's part that its list holds
 
 struct LogitsArgs {
   const float* logits;
   int R, V;
+  int per;   // tokens of a CTA (a multiple of 4, at most 2 kPer)
+  int rows;  // rows of a cluster
   const float* temp;
   const uint16_t* counts;
   const int32_t* tok;
@@ -36,38 +49,439 @@ struct LogitsArgs {
   uint64_t* row_Q;
   int32_t* row_argmax;
   int32_t* dev_err;
+  float one;  // 1.0f (see MassSum)
 };
 
-__global__ void __launch_bounds__(kThreads)
+// maximum that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+// z after the penalties of a token that occurs c times in the answer (rounded step by step)
+__device__ __forceinline__ float penalize(float z, int c, bool prompt, float rep, float freq, float pres) {
+  if (c > 0 || prompt) z = z > 0.0f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+  if (c > 0) z = __fsub_rn(__fsub_rn(z, __fmul_rn(freq, static_cast<float>(c))), pres);
+  return z;
+}
+
+// Sum of the masses floor(2^40 E(s - m)) of pairs of values, bit for bit those of fx_mass:
+// the same rounded steps, in packed pairs.  A sum of a product is a fused a * one + b with
+// `one` a kernel argument: the compiler cannot contract it with the product, which is
+// rounded by itself.  s - m is held at -64 from below, where the mass is 0 as it is
+// below -32.  y = E 2^40 is split without a 64-bit shift: hi = floor(y
+// / 2^20) and lo = floor(y - 2^20 hi) are the low mantissa bits of truncated sums with
+// 2^23, and the bit patterns themselves are summed; their common 0x4B000000 leaves with
+// total().  A thread adds fewer than 2^11 values, so neither 32-bit sum wraps past it.
+struct MassSum {
+  uint32_t hi = 0u, lo = 0u, n = 0u;
+  __device__ __forceinline__ void add(float2 z, float2 it, float2 neg_m, float2 one) {
+    float2 x = __ffma2_rn(__fmul2_rn(z, it), one, neg_m);
+    x = make_float2(fmaxf(x.x, -64.0f), fmaxf(x.y, -64.0f));
+    const float2 t = __fmul2_rn(x, make_float2(0x1.715476p+0f, 0x1.715476p+0f));
+    const float2 tm = __ffma2_rn(t, one, make_float2(0x1.8p23f, 0x1.8p23f));
+    const float2 nn = __ffma2_rn(tm, make_float2(-1.0f, -1.0f), make_float2(0x1.8p23f, 0x1.8p23f));  // -n
+    float2 r = __ffma2_rn(nn, make_float2(0x1.62e4p-1f, 0x1.62e4p-1f), x);
+    r = __ffma2_rn(nn, make_float2(0x1.7f7d1cp-20f, 0x1.7f7d1cp-20f), r);
+    float2 p = make_float2(0x1.a01a02p-13f, 0x1.a01a02p-13f);
+    p = __ffma2_rn(p, r, make_float2(0x1.6c16c2p-10f, 0x1.6c16c2p-10f));
+    p = __ffma2_rn(p, r, make_float2(0x1.111112p-7f, 0x1.111112p-7f));
+    p = __ffma2_rn(p, r, make_float2(0x1.555556p-5f, 0x1.555556p-5f));
+    p = __ffma2_rn(p, r, make_float2(0x1.555556p-3f, 0x1.555556p-3f));
+    p = __ffma2_rn(p, r, make_float2(0.5f, 0.5f));
+    p = __ffma2_rn(p, r, make_float2(1.0f, 1.0f));
+    p = __ffma2_rn(p, r, make_float2(1.0f, 1.0f));
+    // 2^(n + 40): the low mantissa bits of tm are n (its high ones leave with the shift)
+    const float2 sc = make_float2(__uint_as_float((__float_as_uint(tm.x) << 23) + (167u << 23)),
+                                  __uint_as_float((__float_as_uint(tm.y) << 23) + (167u << 23)));
+    const float2 y = __fmul2_rn(p, sc);  // exact
+    const float2 big = make_float2(8388608.0f, 8388608.0f);
+    const float2 h = __ffma2_rz(y, make_float2(0x1p-20f, 0x1p-20f), big);
+    const float2 hf = __ffma2_rn(h, one, make_float2(-8388608.0f, -8388608.0f));
+    const float2 rem = __ffma2_rn(hf, make_float2(-0x1p20f, -0x1p20f), y);  // exact, in [0, 2^20)
+    const float2 l = __ffma2_rz(rem, one, big);
+    hi += __float_as_uint(h.x) + __float_as_uint(h.y);
+    lo += __float_as_uint(l.x) + __float_as_uint(l.y);
+    n += 2u;
+  }
+  __device__ __forceinline__ unsigned long long total() const {
+    const uint32_t h = hi - n * 0x4B000000u, l = lo - n * 0x4B000000u;
+    return (static_cast<unsigned long long>(h) << 20) + l;
+  }
+};
+
+__device__ __forceinline__ uint32_t su32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+// Dynamic shared memory: the CTA's part of the row, its seen tokens, its biases and a bit
+// per token that has one.
+struct LogitsSmem {
+  int z, list, allow, btok, bval, bits, total;  // byte offsets
+};
+__host__ __device__ inline LogitsSmem logits_smem(int per, int n_bias) {
+  LogitsSmem s;
+  s.z = 0;
+  s.list = (per * 4 + 15) / 16 * 16;
+  s.allow = s.list + kSeenCap * 4;
+  s.btok = s.allow + (per / 32 + 2) * 4;
+  s.bval = s.btok + n_bias * 4;
+  s.bits = s.bval + n_bias * 4;
+  s.total = s.bits + (n_bias ? (per + 31) / 32 * 4 : 0);
+  return s;
+}
+
+// One cluster per group of a request's rows; a CTA owns `per` consecutive tokens of each.
+// What does not change from row to row is laid out once: the tokens of the CTA's part
+// that the request has seen (a list; most of the vocabulary has none), and its biases in
+// list order.  Per row: the part arrives in shared memory by one bulk copy; the few seen,
+// path and bias tokens are changed in place; one pass applies the grammar and takes the
+// maximum, another the masses; the part leaves by one bulk copy.  The row is read once
+// and written once, the CTAs of the cluster exchange one maximum and one sum per row.
+// Three CTAs share an SM, so that one's copies and barriers pass under the others' sums.
+// Rows off the 16-byte grid (VEC = false) are copied by plain loads and stores.
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads, 3)
 logits_process_kernel(LogitsArgs a) {
-  __shared__ int s_path[E3_MAX_DEPTH];
-  __shared__ int s_npath;
-  __shared__ int s_btok[kMaxBias];
-  __shared__ float s_bval[kMaxBias];
+  extern __shared__ __align__(128) unsigned char dyn[];
+  __shared__ int s_tok[kMaxR], s_par[kMaxR];
+  __shared__ int s_path[E3_MAX_DEPTH], s_npath, s_nbias, s_nseen;
+  __shared__ float s_red[kThreads / 32];
+  __shared__ unsigned long long s_sum[kThreads / 32];
+  __shared__ float s_max[2][8];             // by row parity, one per CTA of the cluster
+  __shared__ unsigned long long s_Q[2][8];  // (CTA 0)
+  __shared__ int s_arg[2][8];               // (CTA 0)
+  __shared__ int s_first;
+  __shared__ __align__(8) uint64_t bar;
+  const LogitsSmem lay = logits_smem(a.per, a.n_bias);
+  float* zs = reinterpret_cast<float*>(dyn);
+  uint32_t* list = reinterpret_cast<uint32_t*>(dyn + lay.list);
+  uint32_t* s_ok = reinterpret_cast<uint32_t*>(dyn + lay.allow);  // the row's mask words of this part
+  int* btok = reinterpret_cast<int*>(dyn + lay.btok);
+  float* bval = reinterpret_cast<float*>(dyn + lay.bval);
+  uint32_t* bbits = reinterpret_cast<uint32_t*>(dyn + lay.bits);
+  cg::cluster_group cluster = cg::this_cluster();
+  const int CL = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+  const int groups = (a.R + a.rows - 1) / a.rows, grp = blockIdx.x / CL;
+  const int b = grp / groups, i0 = (grp % groups) * a.rows, i1 = min(a.R, i0 + a.rows);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int v0 = min(a.V, rank * a.per), nv = min(a.V - v0, a.per);
+  if (tid == 0) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(su32(&bar)));
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    s_npath = s_nbias = s_nseen = 0;
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // this CTA runs: peers may store to it
+  pdl_wait();
+  pdl_trigger();
+  auto load_row = [&](int i) {  // thread 0 (VEC)
+    const uint32_t bytes = static_cast<uint32_t>(nv) * 4u;
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(&bar)), "r"(bytes) : "memory");
+    if (bytes)
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(su32(zs)),
+                   "l"(a.logits + (static_cast<size_t>(b) * a.R + i) * a.V + v0), "r"(bytes), "r"(su32(&bar))
+                   : "memory");
+  };
+  if (VEC && tid == 0) load_row(i0);
+  const float rep = a.pen ? a.pen[3 * b] : 1.0f, freq = a.pen ? a.pen[3 * b + 1] : 0.0f, pres = a.pen ? a.pen[3 * b + 2] : 0.0f;
+  const uint16_t* cnt = a.counts ? a.counts + static_cast<size_t>(b) * a.V + v0 : nullptr;
+  if (a.n_bias)
+    for (int k = tid; k < (a.per + 31) / 32; k += kThreads) bbits[k] = 0u;
+  if (a.tok)
+    for (int k = tid; k < a.R; k += kThreads) {
+      s_tok[k] = a.tok[static_cast<size_t>(b) * a.R + k];
+      s_par[k] = a.parent[static_cast<size_t>(b) * a.R + k];
+    }
+  __syncthreads();
+  // seen tokens of this part: (token, count word); their order does not matter
+  if (cnt) {
+    for (int k0 = warp * 128; k0 < nv; k0 += 4 * kThreads * kBatch) {
+      uint2 x[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {  // every load of the batch before its first use
+        const int t = k0 + 4 * kThreads * u + (VEC ? 4 * lane : lane);
+        if (VEC) {
+          x[u] = t < nv ? *reinterpret_cast<const uint2*>(cnt + t) : make_uint2(0u, 0u);
+        } else {
+          x[u].x = (t < nv ? cnt[t] : 0u) | (t + 32 < nv ? static_cast<uint32_t>(cnt[t + 32]) << 16 : 0u);
+          x[u].y = (t + 64 < nv ? cnt[t + 64] : 0u) | (t + 96 < nv ? static_cast<uint32_t>(cnt[t + 96]) << 16 : 0u);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int t = k0 + 4 * kThreads * u + (VEC ? 4 * lane : lane);
+        const uint32_t cw[4] = {x[u].x & 0xFFFFu, x[u].x >> 16, x[u].y & 0xFFFFu, x[u].y >> 16};
+        if (!__any_sync(0xFFFFFFFFu, (x[u].x | x[u].y) != 0u)) continue;
+        unsigned m[4];
+        int n = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          m[j] = __ballot_sync(0xFFFFFFFFu, cw[j] != 0u);
+          n += __popc(m[j]);
+        }
+        int base = 0;
+        if (lane == 0) base = atomicAdd(&s_nseen, n);
+        base = __shfl_sync(0xFFFFFFFFu, base, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int p = base + __popc(m[j] & ((1u << lane) - 1u));
+          if (cw[j] != 0u && p < kSeenCap) list[p] = (static_cast<uint32_t>(t + (VEC ? j : 32 * j)) << 16) | cw[j];
+          base += __popc(m[j]);
+        }
+      }
+    }
+  }
+  if (warp == kThreads / 32 - 1 && a.n_bias) {  // the list's entries within this part, in order
+    int n = 0;
+    for (int k0 = 0; k0 < a.n_bias; k0 += 32) {
+      const int k = k0 + lane;
+      const int t = k < a.n_bias ? a.bias_tok[static_cast<size_t>(b) * a.n_bias + k] : -1;
+      const bool in = t >= v0 && t - v0 < nv;
+      const unsigned m = __ballot_sync(0xFFFFFFFFu, in);
+      if (in) {
+        const int p = n + __popc(m & ((1u << lane) - 1u));
+        btok[p] = t - v0;
+        bval[p] = a.bias_val[static_cast<size_t>(b) * a.n_bias + k];
+        atomicOr(&bbits[(t - v0) >> 5], 1u << ((t - v0) & 31));
+      }
+      n += __popc(m);
+    }
+    if (lane == 0) s_nbias = n;
+  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // thread 0 of CTA 0 writes a row's results one barrier later, when every sum has come
+  float last_mx = 0.0f;
+  bool last_ok = false;
+  auto finish = [&](int i) {
+    const int par = (i - i0) & 1;
+    const size_t row = static_cast<size_t>(b) * a.R + i;
+    unsigned long long Q = 0;
+    int first = 0x7FFFFFFF;
+    for (int c = 0; c < CL; ++c) {
+      Q += s_Q[par][c];
+      first = min(first, s_arg[par][c]);
+    }
+    a.row_max[row] = last_ok ? last_mx : __int_as_float(0x7FC00000);
+    a.row_Q[row] = last_ok ? Q : 0ull;
+    a.row_argmax[row] = last_ok ? first : -1;
+  };
+  for (int i = i0; i < i1; ++i) {
+    const int par = (i - i0) & 1;
+    const size_t row = static_cast<size_t>(b) * a.R + i;
+    const float it = inv_temp(a.temp[row]);
+    const uint32_t* allow = nullptr;
+    if (a.allow) {
+      const int ar = a.allow_row ? a.allow_row[row] : static_cast<int>(row);
+      if (ar >= 0 && ar < a.n_allow) allow = a.allow + static_cast<size_t>(ar) * ((a.V + 31) / 32);
+    }
+    const int w0 = v0 >> 5;
+    if (allow)
+      for (int w = w0 + tid; 32 * w < v0 + nv; w += kThreads) s_ok[w - w0] = allow[w];
+    if (tid == 0) {
+      int n = 0, u = a.tok ? i : 0;
+      while (u > 0 && u < a.R && n < E3_MAX_DEPTH) {
+        const int t = s_tok[u] - v0;
+        if (s_tok[u] >= 0 && t >= 0 && t < nv) s_path[n++] = t;
+        u = s_par[u] < u ? s_par[u] : -1;  // parents come first
+      }
+      s_npath = n;
+      s_first = 0x7FFFFFFF;
+    }
+    if (VEC) {
+      if (tid == 0) {  // the copy has landed (bounded)
+        bool ok = false;
+        uint64_t t0 = 0;
+        for (int n = 0; !ok; ++n) {
+          uint32_t done;
+          asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                       : "=r"(done)
+                       : "r"(su32(&bar)), "r"(par)
+                       : "memory");
+          ok = done != 0;
+          uint64_t t;
+          asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+          if (n == 0) t0 = t;
+          if (!ok && t - t0 > 1000000000ull) {
+            dev_flag(a.dev_err, E3_DEV_ERR_TIMEOUT);
+            break;
+          }
+        }
+      }
+    } else {
+      const float* src = a.logits + row * a.V + v0;
+      for (int t = tid; t < nv; t += kThreads) zs[t] = src[t];
+    }
+    __syncthreads();
+    const int npath = s_npath, nbias = s_nbias, nseen = s_nseen;
+    auto biased = [&](int t) { return nbias > 0 && ((bbits[t >> 5] >> (t & 31)) & 1u); };
+    auto on_path = [&](int t) {
+      int c = 0;
+      for (int k = 0; k < npath; ++k) c += s_path[k] == t;
+      return c;
+    };
+    // seen tokens that neither the path nor a bias touches
+    if (nseen <= kSeenCap) {
+      for (int e = tid; e < nseen; e += kThreads) {
+        const uint32_t w = list[e];
+        const int t = static_cast<int>(w >> 16);
+        if (!biased(t) && on_path(t) == 0)
+          zs[t] = penalize(zs[t], static_cast<int>(w & 32767u), (w & 32768u) != 0u, rep, freq, pres);
+      }
+    } else {  // more than the list holds: the counts themselves
+      for (int t = tid; t < nv; t += kThreads) {
+        const uint32_t w = cnt[t];
+        if (w != 0u && !biased(t) && on_path(t) == 0)
+          zs[t] = penalize(zs[t], static_cast<int>(w & 32767u), (w & 32768u) != 0u, rep, freq, pres);
+      }
+    }
+    // tokens of the path and of the biases: each once, at its first entry of the two lists
+    for (int e = tid; e < npath + nbias; e += kThreads) {
+      const int t = e < npath ? s_path[e] : btok[e - npath];
+      bool again = false;
+      for (int k = 0; k < e && !again; ++k) again = (k < npath ? s_path[k] : btok[k - npath]) == t;
+      if (again) continue;
+      const uint32_t w = cnt ? cnt[t] : 0u;
+      float z = penalize(zs[t], static_cast<int>(w & 32767u) + on_path(t), (w & 32768u) != 0u, rep, freq, pres);
+      float add = 0.0f;
+      bool any = false;
+      for (int k = max(0, e - npath); k < nbias; ++k)
+        if (btok[k] == t) {
+          add = any ? __fadd_rn(add, bval[k]) : bval[k];
+          any = true;
+        }
+      if (any) z = __fadd_rn(z, add);
+      zs[t] = z;
+    }
+    __syncthreads();
+    // grammar and maximum
+    float best = -INFINITY;
+#pragma unroll 4
+    for (int k = tid; 4 * k < nv; k += kThreads) {
+      float4 x = reinterpret_cast<float4*>(zs)[k];
+      if (!VEC) {  // the part may end inside the group
+        if (4 * k + 1 >= nv) x.y = -INFINITY;
+        if (4 * k + 2 >= nv) x.z = -INFINITY;
+        if (4 * k + 3 >= nv) x.w = -INFINITY;
+      }
+      if (allow) {
+        const int v = v0 + 4 * k;  // a multiple of four
+        const uint32_t ok = s_ok[(v >> 5) - w0] >> (v & 31);
+        if (!(ok & 1u)) x.x = -INFINITY;
+        if (!(ok & 2u)) x.y = -INFINITY;
+        if (!(ok & 4u)) x.z = -INFINITY;
+        if (!(ok & 8u)) x.w = -INFINITY;
+      }
+      if (allow || !VEC) reinterpret_cast<float4*>(zs)[k] = x;
+      best = max_nan(max_nan(best, x.x, x.y), x.z, x.w);
+    }
+    const float mine = best;
+    best = warp_reduce(best, [](float p, float q) { return max_nan(p, q); });
+    if (lane == 0) s_red[warp] = best;
+    if (VEC) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the pass's stores, before the copy out
+    __syncthreads();
+    if (warp == 0) {
+      best = warp_reduce(lane < kThreads / 32 ? s_red[lane] : -INFINITY, [](float p, float q) { return max_nan(p, q); });
+      if (lane < CL) *cluster.map_shared_rank(&s_max[par][rank], lane) = best;
+      if (VEC && lane == 0 && nv > 0) {
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(a.out + row * a.V + v0),
+                     "r"(su32(zs)), "r"(static_cast<uint32_t>(nv) * 4u)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+    }
+    if (!VEC) {
+      float* dst = a.out + row * a.V + v0;
+      for (int t = tid; t < nv; t += kThreads) dst[t] = zs[t];
+    }
+    cluster.sync();
+    if (rank == 0 && tid == 0 && i > i0) finish(i - 1);
+    float zm = s_max[par][0];
+    for (int c = 1; c < CL; ++c) zm = max_nan(zm, s_max[par][c]);
+    const float mx = __fadd_rn(__fmul_rn(zm, it), 0.0f);
+    const bool none = zm == -INFINITY, bad = !none && !(fabsf(mx) <= 3.402823466e38f);
+    last_mx = mx;
+    last_ok = !none && !bad;
+    unsigned long long Q = 0;
+    if (last_ok) {
+      // the lowest token that reaches the maximum (rounding is monotone: a thread that
+      // holds one has its own largest logit among them)
+      if (__fmul_rn(mine, it) == mx) {
+        int first = 0x7FFFFFFF;
+        for (int k = tid; 4 * k < nv; k += kThreads) {
+          const float4 x = reinterpret_cast<const float4*>(zs)[k];
+          const float e[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int j = 3; j >= 0; --j)
+            if (__fmul_rn(e[j], it) == mx) first = min(first, v0 + 4 * k + j);
+        }
+        atomicMin(&s_first, first);
+      }
+      MassSum sum;
+      const float2 it2 = make_float2(it, it), nm = make_float2(-mx, -mx), one = make_float2(a.one, a.one);
+#pragma unroll 4
+      for (int k = tid; 4 * k < nv; k += kThreads) {
+        const float4 x = reinterpret_cast<const float4*>(zs)[k];
+        sum.add(make_float2(x.x, x.y), it2, nm, one);
+        sum.add(make_float2(x.z, x.w), it2, nm, one);
+      }
+      Q = sum.total();
+    } else if (rank == 0 && tid == 0) {
+      dev_flag(a.dev_err, bad ? E3_DEV_ERR_NONFINITE : E3_DEV_ERR_MASKED);
+    }
+    Q = warp_reduce(static_cast<uint64_t>(Q), SumU64());
+    if (lane == 0) s_sum[warp] = Q;
+    __syncthreads();  // also: every thread is done with the row
+    if (tid == 0) {
+      Q = 0;
+      for (int w = 0; w < kThreads / 32; ++w) Q += s_sum[w];
+      *cluster.map_shared_rank(&s_Q[par][rank], 0) = Q;
+      *cluster.map_shared_rank(&s_arg[par][rank], 0) = s_first;
+      if (VEC) {
+        // the copy out has read the part, then the next row may take its place
+        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        if (i + 1 < i1) load_row(i + 1);
+      }
+    }
+    // (thread 0 resets s_first and s_npath before the next __syncthreads, which every
+    // thread reaches after this row's last read of them)
+  }
+  cluster.sync();
+  if (rank == 0 && tid == 0) finish(i1 - 1);
+  if (VEC && tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+// Vocabularies that a cluster's shared memory does not hold (V > 262144): one CTA per row in
+// two passes, the second over the processed row.
+__global__ void __launch_bounds__(kThreads)
+logits_process_wide_kernel(LogitsArgs a) {
+  __shared__ int s_path[E3_MAX_DEPTH], s_npath;
+  __shared__ int btok[kMaxBias];
+  __shared__ float bval[kMaxBias];
   __shared__ uint64_t red64[32];
   __shared__ int redi[32];
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.x, b = row / a.R, i = row - b * a.R;
+  const int row = blockIdx.x, b = row / a.R, node = row - b * a.R;
   if (threadIdx.x == 0) {
-    int n = 0;
-    if (a.tok) {
-      int u = i;
-      while (u > 0 && u < a.R && n < E3_MAX_DEPTH) {
-        s_path[n++] = a.tok[static_cast<size_t>(b) * a.R + u];
-        u = a.parent[static_cast<size_t>(b) * a.R + u];
-      }
+    int n = 0, u = a.tok ? node : 0;
+    while (u > 0 && u < a.R && n < E3_MAX_DEPTH) {
+      s_path[n++] = a.tok[static_cast<size_t>(b) * a.R + u];
+      const int p = a.parent[static_cast<size_t>(b) * a.R + u];
+      u = p < u ? p : -1;
     }
     s_npath = n;
   }
   for (int k = threadIdx.x; k < a.n_bias; k += kThreads) {
-    s_btok[k] = a.bias_tok[static_cast<size_t>(b) * a.n_bias + k];
-    s_bval[k] = a.bias_val[static_cast<size_t>(b) * a.n_bias + k];
+    btok[k] = a.bias_tok[static_cast<size_t>(b) * a.n_bias + k];
+    bval[k] = a.bias_val[static_cast<size_t>(b) * a.n_bias + k];
   }
   __syncthreads();
-  const int npath = s_npath;
   const float rep = a.pen ? a.pen[3 * b] : 1.0f, freq = a.pen ? a.pen[3 * b + 1] : 0.0f, pres = a.pen ? a.pen[3 * b + 2] : 0.0f;
-  const float* z = a.logits + static_cast<size_t>(row) * a.V;
+  const float* zin = a.logits + static_cast<size_t>(row) * a.V;
   float* out = a.out + static_cast<size_t>(row) * a.V;
   const uint16_t* cnt = a.counts ? a.counts + static_cast<size_t>(b) * a.V : nullptr;
   const uint32_t* allow = nullptr;
@@ -79,24 +493,23 @@ logits_process_kernel(LogitsArgs a) {
   uint64_t best = 0ull;
   int bad = 0;
   for (int v = threadIdx.x; v < a.V; v += kThreads) {
-    float x = z[v];
-    const uint32_t cw = cnt ? cnt[v] : 0u;
-    int c = static_cast<int>(cw & 32767u);
-    for (int k = 0; k < npath; ++k) c += s_path[k] == v;
-    if (c > 0 || (cw & 32768u)) x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
-    if (c > 0) x = __fsub_rn(__fsub_rn(x, __fmul_rn(freq, static_cast<float>(c))), pres);
+    const uint32_t w = cnt ? cnt[v] : 0u;
+    int c = static_cast<int>(w & 32767u);
+    for (int k = 0; k < s_npath; ++k) c += s_path[k] == v;
+    float x = penalize(zin[v], c, (w & 32768u) != 0u, rep, freq, pres);
     float add = 0.0f;
-    bool biased = false;
+    bool any = false;
     for (int k = 0; k < a.n_bias; ++k)
-      if (s_btok[k] == v) {
-        add = biased ? __fadd_rn(add, s_bval[k]) : s_bval[k];
-        biased = true;
+      if (btok[k] == v) {
+        add = any ? __fadd_rn(add, bval[k]) : bval[k];
+        any = true;
       }
-    if (biased) x = __fadd_rn(x, add);
+    if (any) x = __fadd_rn(x, add);
     if (allow && !((allow[v >> 5] >> (v & 31)) & 1u)) x = -INFINITY;
     out[v] = x;
-    bad |= !(x <= 3.402823466e38f);  // NaN or +Inf
-    const uint64_t key = x == -INFINITY ? 0ull : pack_best(__fmul_rn(x, it), static_cast<uint32_t>(v));
+    const float s = __fmul_rn(x, it);
+    bad |= !(s <= 3.402823466e38f);  // NaN or +Inf
+    const uint64_t key = x == -INFINITY ? 0ull : pack_best(s, static_cast<uint32_t>(v));
     best = key > best ? key : best;
   }
   bad = block_reduce(bad, OrI(), redi);
@@ -111,12 +524,12 @@ logits_process_kernel(LogitsArgs a) {
     return;
   }
   const float mx = unord_f32(static_cast<uint32_t>(best >> 32));
-  uint64_t Qs = 0;
-  for (int v = threadIdx.x; v < a.V; v += kThreads) Qs += fx_mass(__fmul_rn(out[v], it), mx);
-  Qs = block_reduce(Qs, SumU64(), red64);
+  uint64_t Q = 0;
+  for (int v = threadIdx.x; v < a.V; v += kThreads) Q += fx_mass(__fmul_rn(out[v], it), mx);
+  Q = block_reduce(Q, SumU64(), red64);
   if (threadIdx.x == 0) {
     a.row_max[row] = mx;
-    a.row_Q[row] = Qs;
+    a.row_Q[row] = Q;
     a.row_argmax[row] = static_cast<int32_t>(packed_id(best));
   }
 }
@@ -154,9 +567,44 @@ e3_status launch_logits_process(const float* logits, int B, int R, int V, const 
                                 const float* bias_val, int n_bias, const uint32_t* allow, const int32_t* allow_row,
                                 int n_allow, float* out, float* row_max, uint64_t* row_Q, int32_t* row_argmax,
                                 int32_t* dev_err, cudaStream_t s) {
-  const LogitsArgs a{logits, R,     V,         temp,    counts, tok,     parent, pen,        bias_tok, bias_val,
-                     n_bias, allow, allow_row, n_allow, out,    row_max, row_Q,  row_argmax, dev_err};
-  const cudaError_t e = launch_pdl(logits_process_kernel, dim3(B * R), dim3(kThreads), 0, s, 1, a);
+  LogitsArgs a{logits,   R,      V,     0,         1,       temp, counts,  tok,   parent,     pen,    bias_tok,
+               bias_val, n_bias, allow, allow_row, n_allow, out,  row_max, row_Q, row_argmax, dev_err,
+               1.0f};
+  if (V > 8 * 2 * kPer) {
+    const cudaError_t e = launch_pdl(logits_process_wide_kernel, dim3(B * R), dim3(kThreads), 0, s, 1, a);
+    return e == cudaSuccess ? E3_OK : cuda_status(e, "logits_process_wide_kernel");
+  }
+  // CTAs of a row: as many as hold it, and more (down to 2048 tokens each) while the rows
+  // leave SMs empty.  Rows of a cluster: several of one request, so that the request's lists are
+  // built less often, as the rounds of clusters allow
+  const int sms = 152;
+  int CL = 1;
+  while (CL < 8 && (CL * kPer < V || (static_cast<long>(B) * R * CL < sms && V > 2048 * CL))) CL *= 2;
+  a.per = ((V + CL - 1) / CL + 3) / 4 * 4;
+  const long places = std::max(1, 408 / CL);  // clusters that three CTAs an SM leave room for (51 of eight, as the occupancy query answers)
+  a.rows = 1;
+  long cost = 0;
+  for (int n = 1; n <= 16 && n <= R; ++n) {  // rounds of clusters x (their rows + the lists, about a row's time)
+    const long rounds = (static_cast<long>(B) * ((R + n - 1) / n) + places - 1) / places, c = rounds * (n + 1);
+    if (n == 1 || c < cost) {
+      cost = c;
+      a.rows = n;
+    }
+  }
+  const int smem = logits_smem(a.per, n_bias).total;
+  static std::atomic<bool> attr_done{false};
+  if (!attr_done.load(std::memory_order_acquire)) {
+    const int most = logits_smem(2 * kPer, kMaxBias).total;
+    cudaError_t e = cudaFuncSetAttribute(logits_process_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(logits_process_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    if (e != cudaSuccess) return cuda_status(e, "logits_process_kernel smem attribute");
+    attr_done.store(true, std::memory_order_release);
+  }
+  const bool vec = V % 4 == 0 && aligned16(logits) && aligned16(out) && (reinterpret_cast<uintptr_t>(counts) & 7u) == 0;
+  const dim3 grid(static_cast<unsigned>(B) * ((R + a.rows - 1) / a.rows) * CL), block(kThreads);
+  const cudaError_t e = vec ? launch_pdl(logits_process_kernel<true>, grid, block, smem, s, CL, a)
+                            : launch_pdl(logits_process_kernel<false>, grid, block, smem, s, CL, a);
   return e == cudaSuccess ? E3_OK : cuda_status(e, "logits_process_kernel");
 }
 

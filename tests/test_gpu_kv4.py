@@ -508,6 +508,9 @@ LOGITS = [
     (1, 9, 4097, 1024, True, True, False, True, True),
     (2, 3, 33000, 0, False, False, False, False, False),
     (1, 2, 150001, 5, True, True, True, True, False),
+    (1, 3, 200000, 5, True, True, True, True, True),
+    (1, 2, 262148, 9, True, True, True, True, False),   # wider than a cluster holds
+    (40, 8, 2052, 2, True, True, True, True, False),    # many rows
 ]
 
 
