@@ -79,7 +79,7 @@ static e3_status gather_layers(const char* fn, const e3_kv4_layer* layers, const
   E3_REQUIRE(other[0].dt == E3_BF16, E3_ERR_UNSUPPORTED, "%s: the 16-bit side must be bf16", fn);
   E3_REQUIRE(other[0].n_kv_heads == layers[0].n_kv_heads && other[0].head_dim == layers[0].head_dim, E3_ERR_SHAPE,
              "%s: heads or head_dim of the two caches differ", fn);
-  E3_REQUIRE(static_cast<long long>(layers[0].n_kv_heads) * max_rows * (layers[0].head_dim / 16) <= (1ll << 38), E3_ERR_SHAPE,
+  E3_REQUIRE(static_cast<long long>(layers[0].n_kv_heads) * max_rows * (layers[0].head_dim / 16) < (1ll << 31), E3_ERR_SHAPE,
              "%s: max_rows=%d", fn, max_rows);
   return E3_OK;
 }

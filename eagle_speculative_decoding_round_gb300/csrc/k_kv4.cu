@@ -11,6 +11,8 @@
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "e3_common.cuh"
 #include "e3_kernels.h"
 
@@ -22,19 +24,19 @@ constexpr int kThreads = 256;
 
 // index of (page, head 0, slot) of logical slot t in rows, or -1
 __device__ __forceinline__ long long slot_row(const int32_t* table, int max_pages, int n_pages, int page_size, int KVH,
-                                              int b, long long t) {
+                                              int b, int t) {
   if (t < 0) return -1;
-  const long long pi = t / page_size;
+  const int pi = t / page_size;
   if (pi >= max_pages) return -1;
   const int page = table[static_cast<size_t>(b) * max_pages + pi];
   if (page < 0 || page >= n_pages) return -1;
-  return static_cast<long long>(page) * KVH * page_size + t % page_size;
+  return static_cast<long long>(page) * KVH * page_size + (t - pi * page_size);
 }
 
 // Rows request b appends, or -1 if they do not fit.
 __device__ __forceinline__ int append_count(int n, int max_rows, long long P, long long cap) {
   if (n <= 0) return 0;
-  return (n > max_rows || P < 0 || P + n > cap) ? -1 : n;
+  return (n > max_rows || P < 0 || P + n > cap || P + n > 0x7FFFFFFFll) ? -1 : n;
 }
 
 // One group of 16 bf16 values -> 8 bytes of codes, the scale byte.  `unit` is a power
@@ -44,77 +46,124 @@ __device__ __forceinline__ int append_count(int n, int max_rows, long long P, lo
 // one correction step is exact on midpoints and within 2^-22 elsewhere, so the
 // conversion's rounding is that of the true quotient.
 __device__ __forceinline__ uint2 quantize16(const uint32_t (&w)[8], float unit, uint8_t* scale, bool* bad) {
-  float x[16];
-  float amax = 0.0f;
+  uint32_t m = w[0] & 0x7FFF7FFFu;  // largest magnitudes of the low and the high halves, as bf16 bits
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    float y = __uint_as_float((i & 1) ? (w[i >> 1] & 0xFFFF0000u) : (w[i >> 1] << 16));
-    if (!(fabsf(y) <= 3.3895314e38f)) {  // NaN or Inf
-      *bad = true;
-      y = y != y ? 0.0f : copysignf(3.3895314e38f, y);
-    }
-    x[i] = y;
-    amax = fmaxf(amax, fabsf(y));
+  for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+  m = max(m & 0xFFFFu, m >> 16);
+  const bool odd = m >= 0x7F80u;  // a NaN or an Inf
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
-  const float want = fminf(__fdiv_rn(amax, 6.0f * unit), 448.0f);
-  const __nv_fp8_storage_t e8 = __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
+  if (odd) {
+    *bad = true;
+    m = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (x[i] != x[i]) x[i] = 0.0f;
+      x[i] = fminf(fmaxf(x[i], -3.3895314e38f), 3.3895314e38f);
+      m = max(m, __float_as_uint(fabsf(x[i])) >> 16);
+    }
+  }
+  const float want = __fdiv_rn(__uint_as_float(m << 16), 6.0f * unit);
+  const __nv_fp8_storage_t e8 = __nv_cvt_float_to_fp8(fminf(want, 448.0f), __NV_SATFINITE, __NV_E4M3);
   *scale = e8;
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(e8, __NV_E4M3))) * unit;
-  const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+  float y[16];
+  if (want <= 448.0f && s > 0.0f) {  // quotients of at most 9: e is at worst half a step off a subnormal scale
+    const float r = __frcp_rn(s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 a = make_float2(x[2 * i], x[2 * i + 1]), rr = make_float2(r, r);
+      const float2 q = __fmul2_rn(a, rr);
+      const float2 d = __ffma2_rn(__ffma2_rn(q, make_float2(-s, -s), a), rr, q);
+      y[2 * i] = d.x == 0.0f ? a.x * 0.0f : d.x;  // (the sign of a zero value is kept)
+      y[2 * i + 1] = d.y == 0.0f ? a.y * 0.0f : d.y;
+    }
+  } else {  // a scale at its bound or of 0
+    const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float a = fabsf(x[i]), q = fminf(a * r, 16.0f);
+      y[i] = copysignf(s > 0.0f ? fminf(fmaf(fmaf(-q, s, a), r, q), 16.0f) : 0.0f, x[i]);
+    }
+  }
   uint32_t out[2] = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    float y[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float a = fabsf(x[2 * i + h]);
-      const float q = fminf(a * r, 16.0f);
-      y[h] = copysignf(s > 0.0f ? fminf(fmaf(fmaf(-q, s, a), r, q), 16.0f) : 0.0f, x[2 * i + h]);
-    }
-    const uint32_t c = __nv_cvt_float2_to_fp4x2(make_float2(y[0], y[1]), __NV_E2M1, cudaRoundNearest);
+    const uint32_t c = __nv_cvt_float2_to_fp4x2(make_float2(y[2 * i], y[2 * i + 1]), __NV_E2M1, cudaRoundNearest);
     out[i >> 2] |= c << (8 * (i & 3));
   }
   return make_uint2(out[0], out[1]);
 }
 
+// Where a thread's group lies: row j, KV head and group of its request; the same in every
+// layer and for K and V, so the tables are looked up once.
+struct RowItem {
+  int j, kvh, g;
+};
+__device__ __forceinline__ RowItem row_item(const e3_kv4_layer& geo, int max_rows) {
+  // groups fastest, then rows, then heads: a warp's groups are neighbours in a page
+  const unsigned sh = geo.head_dim == 128 ? 3u : 2u;
+  const unsigned jt = (blockIdx.x * kThreads + threadIdx.x) >> sh;
+  return RowItem{static_cast<int>(jt % static_cast<unsigned>(max_rows)), static_cast<int>(jt / static_cast<unsigned>(max_rows)),
+                 static_cast<int>(threadIdx.x & ((1u << sh) - 1u))};
+}
+
 __global__ void __launch_bounds__(kThreads)
-kv4_append_kernel(Kv4Layers L4, e3_kv4_layer geo, CompactLayers src, e3_kv_layer sgeo, int L, int max_rows,
-                  const int32_t* __restrict__ rows, const int32_t* __restrict__ n_rows, int n_add,
-                  const int32_t* __restrict__ kv_len, int32_t* kv_len_next, int32_t* dev_err) {
+kv4_append_kernel(const __grid_constant__ Kv4Layers L4, e3_kv4_layer geo, const __grid_constant__ CompactLayers src,
+                  e3_kv_layer sgeo, int L, int per, int max_rows, const int32_t* __restrict__ rows,
+                  const int32_t* __restrict__ n_rows, int n_add, const int32_t* __restrict__ kv_len,
+                  int32_t* kv_len_next, int32_t* dev_err) {
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.z, lw = blockIdx.y, l = lw >> 1, which = lw & 1;
+  const int b = blockIdx.z;
   const long long P = kv_len[b];
-  const int given = n_rows[b] + n_add;
-  const int n = append_count(given, max_rows, P, static_cast<long long>(geo.max_pages) * geo.page_size);
-  if (blockIdx.x == 0 && lw == 0 && threadIdx.x == 0) {
+  const int n = append_count(n_rows[b] + n_add, max_rows, P, static_cast<long long>(geo.max_pages) * geo.page_size);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
     if (n < 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
     if (kv_len_next) kv_len_next[b] = static_cast<int32_t>(P + max(n, 0));
   }
-  const int gpr = geo.head_dim / 16;
-  const long long it = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  const int g = static_cast<int>(it % gpr);
-  const long long rest = it / gpr;
-  const int j = static_cast<int>(rest % max_rows);
-  const long long kvh = rest / max_rows;
-  if (kvh >= geo.n_kv_heads || j >= n) return;
-  const int from = rows ? rows[static_cast<size_t>(b) * max_rows + j] : j;
+  const RowItem it = row_item(geo, max_rows);
+  if (it.kvh >= geo.n_kv_heads || it.j >= n) return;
+  const int from = rows ? rows[static_cast<size_t>(b) * max_rows + it.j] : it.j;
   const long long sr = slot_row(sgeo.page_table, sgeo.max_pages, sgeo.n_pages, sgeo.page_size, sgeo.n_kv_heads, b, from);
-  const long long dr = slot_row(geo.page_table, geo.max_pages, geo.n_pages, geo.page_size, geo.n_kv_heads, b, P + j);
+  const long long dr =
+      slot_row(geo.page_table, geo.max_pages, geo.n_pages, geo.page_size, geo.n_kv_heads, b, static_cast<int>(P) + it.j);
   if (sr < 0 || dr < 0) {
     dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
     return;
   }
-  const size_t so = (static_cast<size_t>(sr + kvh * sgeo.page_size) * gpr + g) * 2;  // in 16-byte units
-  const size_t dq = static_cast<size_t>(dr + kvh * geo.page_size) * gpr + g;        // in groups
-  const uint4* p = static_cast<const uint4*>(which ? src.v[l] : src.k[l]) + so;
-  const uint4 x0 = p[0], x1 = p[1];
-  const uint32_t w[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-  uint8_t e;
+  const int gpr = geo.head_dim / 16;
+  const size_t so = (static_cast<size_t>(sr + static_cast<long long>(it.kvh) * sgeo.page_size) * gpr + it.g) * 2;  // 16-byte units
+  const size_t dq = static_cast<size_t>(dr + static_cast<long long>(it.kvh) * geo.page_size) * gpr + it.g;         // groups
+  const int l0 = blockIdx.y * per, l1 = min(L, l0 + per);
   bool bad = false;
-  const uint2 c = quantize16(w, which ? L4.v_unit[l] : L4.k_unit[l], &e, &bad);
-  static_cast<uint2*>(which ? L4.v[l] : L4.k[l])[dq] = c;
-  static_cast<uint8_t*>(which ? L4.vs[l] : L4.ks[l])[dq] = e;
+  uint4 x[4];
+  auto load = [&](int l) {
+    const uint4* pk = static_cast<const uint4*>(src.k[l]) + so;
+    const uint4* pv = static_cast<const uint4*>(src.v[l]) + so;
+    x[0] = pk[0], x[1] = pk[1], x[2] = pv[0], x[3] = pv[1];
+  };
+  load(l0);
+  for (int l = l0; l < l1; ++l) {
+    uint32_t w[2][8];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      w[h >> 1][4 * (h & 1)] = x[h].x;
+      w[h >> 1][4 * (h & 1) + 1] = x[h].y;
+      w[h >> 1][4 * (h & 1) + 2] = x[h].z;
+      w[h >> 1][4 * (h & 1) + 3] = x[h].w;
+    }
+    if (l + 1 < l1) load(l + 1);  // the next layer's group is in flight meanwhile
+    uint8_t e;
+    static_cast<uint2*>(L4.k[l])[dq] = quantize16(w[0], L4.k_unit[l], &e, &bad);
+    static_cast<uint8_t*>(L4.ks[l])[dq] = e;
+    static_cast<uint2*>(L4.v[l])[dq] = quantize16(w[1], L4.v_unit[l], &e, &bad);
+    static_cast<uint8_t*>(L4.vs[l])[dq] = e;
+  }
   if (bad) dev_flag(dev_err, E3_DEV_ERR_NONFINITE);
 }
 
@@ -127,35 +176,8 @@ __global__ void kv4_len_kernel(int B, int max_rows, const int32_t* __restrict__ 
   if (b < B) kv_len[b] += max(append_count(n_rows[b] + n_add, max_rows, kv_len[b], cap), 0);
 }
 
-__global__ void __launch_bounds__(kThreads)
-kv4_read_kernel(Kv4Layers L4, e3_kv4_layer geo, CompactLayers dst, e3_kv_layer dgeo, int L, int max_rows,
-                const int32_t* __restrict__ first, const int32_t* __restrict__ n_rows, int32_t* dev_err) {
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.z, lw = blockIdx.y, l = lw >> 1, which = lw & 1;
-  const int n = n_rows[b];
-  if (n > max_rows) {
-    if (blockIdx.x == 0 && lw == 0 && threadIdx.x == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
-    return;
-  }
-  const int gpr = geo.head_dim / 16;
-  const long long it = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
-  const int g = static_cast<int>(it % gpr);
-  const long long rest = it / gpr;
-  const int j = static_cast<int>(rest % max_rows);
-  const long long kvh = rest / max_rows;
-  if (kvh >= geo.n_kv_heads || j >= n) return;
-  const long long t = (first ? static_cast<long long>(first[b]) : 0ll) + j;
-  const long long sr = slot_row(geo.page_table, geo.max_pages, geo.n_pages, geo.page_size, geo.n_kv_heads, b, t);
-  const long long dr = slot_row(dgeo.page_table, dgeo.max_pages, dgeo.n_pages, dgeo.page_size, dgeo.n_kv_heads, b, j);
-  if (sr < 0 || dr < 0) {
-    dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
-    return;
-  }
-  const size_t sq = static_cast<size_t>(sr + kvh * geo.page_size) * gpr + g;
-  const uint2 c = static_cast<const uint2*>(which ? L4.v[l] : L4.k[l])[sq];
-  const uint8_t e = static_cast<const uint8_t*>(which ? L4.vs[l] : L4.ks[l])[sq];
-  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(e, __NV_E4M3))) * (which ? L4.v_unit[l] : L4.k_unit[l]);
+__device__ __forceinline__ void dequantize16(uint2 c, uint8_t e, float unit, uint4* out) {
+  const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(e, __NV_E4M3))) * unit;
   uint32_t o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -164,15 +186,61 @@ kv4_read_kernel(Kv4Layers L4, e3_kv4_layer geo, CompactLayers dst, e3_kv_layer d
     const float2 f = __half22float2(h);
     o[i] = pack2_bf16(f.x * s, f.y * s);
   }
-  uint4* p = static_cast<uint4*>(which ? dst.v[l] : dst.k[l]) +
-             (static_cast<size_t>(dr + kvh * dgeo.page_size) * gpr + g) * 2;
-  p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
+  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-dim3 row_grid(const e3_kv4_layer& geo, int L, int B, int max_rows) {
+__global__ void __launch_bounds__(kThreads)
+kv4_read_kernel(const __grid_constant__ Kv4Layers L4, e3_kv4_layer geo, const __grid_constant__ CompactLayers dst,
+                e3_kv_layer dgeo, int L, int per, int max_rows, const int32_t* __restrict__ first,
+                const int32_t* __restrict__ n_rows, int32_t* dev_err) {
+  pdl_wait();
+  pdl_trigger();
+  const int b = blockIdx.z;
+  const int n = n_rows[b];
+  if (n > max_rows) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+    return;
+  }
+  const RowItem it = row_item(geo, max_rows);
+  if (it.kvh >= geo.n_kv_heads || it.j >= n) return;
+  const long long t = (first ? static_cast<long long>(first[b]) : 0ll) + it.j;
+  const long long sr = slot_row(geo.page_table, geo.max_pages, geo.n_pages, geo.page_size, geo.n_kv_heads, b,
+                                t < 0 || t > 0x7FFFFFFF ? -1 : static_cast<int>(t));
+  const long long dr = slot_row(dgeo.page_table, dgeo.max_pages, dgeo.n_pages, dgeo.page_size, dgeo.n_kv_heads, b, it.j);
+  if (sr < 0 || dr < 0) {
+    dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+    return;
+  }
+  const int gpr = geo.head_dim / 16;
+  const size_t sq = static_cast<size_t>(sr + static_cast<long long>(it.kvh) * geo.page_size) * gpr + it.g;
+  const size_t dq = (static_cast<size_t>(dr + static_cast<long long>(it.kvh) * dgeo.page_size) * gpr + it.g) * 2;
+  const int l0 = blockIdx.y * per, l1 = min(L, l0 + per);
+  uint2 c[2];
+  uint8_t e[2];
+  auto load = [&](int l) {
+    c[0] = static_cast<const uint2*>(L4.k[l])[sq];
+    e[0] = static_cast<const uint8_t*>(L4.ks[l])[sq];
+    c[1] = static_cast<const uint2*>(L4.v[l])[sq];
+    e[1] = static_cast<const uint8_t*>(L4.vs[l])[sq];
+  };
+  load(l0);
+  for (int l = l0; l < l1; ++l) {
+    const uint2 ck = c[0], cv = c[1];
+    const uint8_t ek = e[0], ev = e[1];
+    if (l + 1 < l1) load(l + 1);
+    dequantize16(ck, ek, L4.k_unit[l], static_cast<uint4*>(dst.k[l]) + dq);
+    dequantize16(cv, ev, L4.v_unit[l], static_cast<uint4*>(dst.v[l]) + dq);
+  }
+}
+
+// Grid over (groups of a request, layers in parts of `per`, requests): several layers
+// per thread, as far as eight CTAs remain for every SM.
+dim3 row_grid(const e3_kv4_layer& geo, int L, int B, int max_rows, int* per) {
   const long long items = static_cast<long long>(geo.n_kv_heads) * max_rows * (geo.head_dim / 16);
-  return dim3(static_cast<unsigned>((items + kThreads - 1) / kThreads), 2 * L, B);
+  const long long x = (items + kThreads - 1) / kThreads;
+  *per = static_cast<int>(std::min<long long>(L, std::max<long long>(1, x * B * L / (8 * 152))));
+  return dim3(static_cast<unsigned>(x), (L + *per - 1) / *per, B);
 }
 
 }  // namespace
@@ -182,8 +250,10 @@ e3_status launch_kv4_append(const Kv4Layers& l4, const e3_kv4_layer& geo, const 
                             const int32_t* n_rows, int n_add, const int32_t* kv_len, int32_t* kv_len_next,
                             int32_t* dev_err, cudaStream_t s) {
   const bool in_place = kv_len_next == kv_len;
-  cudaError_t e = launch_pdl(kv4_append_kernel, row_grid(geo, L, B, max_rows), dim3(kThreads), 0, s, 1, l4, geo, src,
-                             sgeo, L, max_rows, rows, n_rows, n_add, kv_len, in_place ? nullptr : kv_len_next, dev_err);
+  int per = 1;
+  const dim3 grid = row_grid(geo, L, B, max_rows, &per);
+  cudaError_t e = launch_pdl(kv4_append_kernel, grid, dim3(kThreads), 0, s, 1, l4, geo, src, sgeo, L, per, max_rows, rows,
+                             n_rows, n_add, kv_len, in_place ? nullptr : kv_len_next, dev_err);
   if (e != cudaSuccess) return cuda_status(e, "kv4_append_kernel");
   if (in_place) {
     e = launch_pdl(kv4_len_kernel, dim3((B + 255) / 256), dim3(256), 0, s, 1, B, max_rows, n_rows, n_add,
@@ -196,8 +266,10 @@ e3_status launch_kv4_append(const Kv4Layers& l4, const e3_kv4_layer& geo, const 
 e3_status launch_kv4_read(const Kv4Layers& l4, const e3_kv4_layer& geo, const CompactLayers& dst,
                           const e3_kv_layer& dgeo, int L, int B, int max_rows, const int32_t* first,
                           const int32_t* n_rows, int32_t* dev_err, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(kv4_read_kernel, row_grid(geo, L, B, max_rows), dim3(kThreads), 0, s, 1, l4, geo, dst,
-                                   dgeo, L, max_rows, first, n_rows, dev_err);
+  int per = 1;
+  const dim3 grid = row_grid(geo, L, B, max_rows, &per);
+  const cudaError_t e = launch_pdl(kv4_read_kernel, grid, dim3(kThreads), 0, s, 1, l4, geo, dst, dgeo, L, per, max_rows,
+                                   first, n_rows, dev_err);
   return e == cudaSuccess ? E3_OK : cuda_status(e, "kv4_read_kernel");
 }
 

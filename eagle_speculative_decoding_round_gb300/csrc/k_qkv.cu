@@ -18,7 +18,7 @@ namespace e3 {
 namespace {
 
 constexpr int kQkvThreads = 256;
-constexpr int kPieces = 3;  // 8-value pieces a thread holds at once (48 heads of 128: one pass)
+constexpr int kItems = 2;  // heads of a thread in flight (16 values of each)
 
 struct QkvArgs {
   const void* qkv;
@@ -83,92 +83,115 @@ __device__ __forceinline__ void st8(__nv_bfloat16* p, const float (&v)[8]) {
       make_uint4(pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3]), pack2_bf16(v[4], v[5]), pack2_bf16(v[6], v[7]));
 }
 
-// Vector kernel: head_dim HD in {32, 64, 128, 256}, 16-byte rows, rotated pieces whole
-// (rot_dim a multiple of 16, or of 8 when interleaved).  HD/8 lanes hold a head.
-template <typename T, int HD>
-__global__ void __launch_bounds__(kQkvThreads)
+// Vector kernel: head_dim HD in {32, 64, 128, 256}, 16-byte rows, rot_dim a multiple of
+// 16.  HD/16 lanes hold a head; lane p owns two 8-value pieces that rotate with each
+// other (p and its partner half the rotated part away; neighbours when interleaved; the
+// lanes past the rotated part own plain pieces), so no value crosses lanes and a lane's
+// eight cosines and sines serve every head it handles.
+template <typename T, int HD, bool INTER>
+__global__ void __launch_bounds__(kQkvThreads, 3)
 qkv_append_kernel(QkvArgs a, const __grid_constant__ e3_rope rope) {
-  constexpr int LPH = HD / 8;
+  constexpr int LPH = HD / 16;
+  constexpr int HPP = kQkvThreads / LPH;  // heads of a pass
   __shared__ float2 s_cs[128];
+  __shared__ __align__(16) float s_w[2][HD];
   pdl_wait();
   pdl_trigger();
   const int row = blockIdx.x;
   const int b = row / a.R, r = row - b * a.R;
   if (a.n_rows && r >= a.n_rows[b]) return;
+  const int heads = a.H + 2 * a.KVH;
+  const int p = threadIdx.x % LPH, h0 = threadIdx.x / LPH;
+  const int half = rope.rot_dim >> 1, turning = rope.rot_dim / 16;
+  const bool turns = p < turning;
+  const int dA = INTER ? 16 * p : (turns ? 8 * p : rope.rot_dim + 16 * (p - turning));
+  const int dB = (INTER || !turns) ? dA + 8 : dA + half;
   const T* src = static_cast<const T*>(a.qkv) + static_cast<size_t>(row) * a.ld;
-  const int heads = a.H + 2 * a.KVH, np = heads * LPH;
-  long long dst = -1;
-  const int half = rope.rot_dim >> 1;
-  for (int p0 = 0; p0 < np; p0 += kQkvThreads * kPieces) {
-    float v[kPieces][8];
+  float v[kItems][16];
+  auto load = [&](int hb) {
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int p = p0 + u * kQkvThreads + threadIdx.x;
-      if (p < np) {
-        ld8<T>(src + static_cast<size_t>(p) * 8, v[u]);
+    for (int u = 0; u < kItems; ++u) {
+      const int h = hb + u * HPP + h0;
+      if (h < heads) {
+        ld8<T>(src + static_cast<size_t>(h) * HD + dA, *reinterpret_cast<float(*)[8]>(&v[u][0]));
+        ld8<T>(src + static_cast<size_t>(h) * HD + dB, *reinterpret_cast<float(*)[8]>(&v[u][8]));
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[u][j] = 0.0f;
+        for (int j = 0; j < 16; ++j) v[u][j] = 0.0f;
       }
     }
-    if (p0 == 0) {
-      if (threadIdx.x < half) s_cs[threadIdx.x] = rope_cs(rope, threadIdx.x, a.pos[row]);
-      dst = append_row(a, b, r);
-      if (dst < 0 && threadIdx.x == 0) dev_flag(a.dev_err, E3_DEV_ERR_CAPACITY);
-      __syncthreads();
+  };
+  load(0);
+  if (threadIdx.x < half) s_cs[threadIdx.x] = rope_cs(rope, threadIdx.x, a.pos[row]);
+  if (a.q_norm)
+    for (int d = threadIdx.x; d < HD; d += kQkvThreads) s_w[0][d] = a.q_norm[d];
+  if (a.k_norm)
+    for (int d = threadIdx.x; d < HD; d += kQkvThreads) s_w[1][d] = a.k_norm[d];
+  const long long dst = append_row(a, b, r);
+  if (dst < 0 && threadIdx.x == 0) dev_flag(a.dev_err, E3_DEV_ERR_CAPACITY);
+  __syncthreads();
+  float2 c[4], s[4];  // cosines and sines of pairs 8p .. 8p + 7, two at a time
+  if (turns) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 x = *reinterpret_cast<const float4*>(&s_cs[8 * p + 2 * j]);
+      c[j] = make_float2(x.x, x.z);
+      s[j] = make_float2(x.y, x.w);
     }
+  }
+  for (int hb = 0; hb < heads; hb += kItems * HPP) {
+    if (hb > 0) load(hb);
 #pragma unroll
-    for (int u = 0; u < kPieces; ++u) {
-      const int p = p0 + u * kQkvThreads + threadIdx.x;
-      const int h = p / LPH, d0 = (p % LPH) * 8;
+    for (int u = 0; u < kItems; ++u) {
+      const int h = hb + u * HPP + h0;
       const bool is_q = h < a.H, is_k = !is_q && h < a.H + a.KVH;
-      const float* norm = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
-      if (a.q_norm || a.k_norm) {  // the head's lanes are one aligned group of a warp; every lane takes part
-        float ss = 0.0f;
+      float2* x = reinterpret_cast<float2*>(v[u]);  // x[0..3] piece A, x[4..7] piece B
+      if (a.q_norm || a.k_norm) {  // (every lane of the head's group takes part in the sum)
+        float2 ss = __fmul2_rn(x[0], x[0]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(v[u][j], v[u][j], ss);
+        for (int j = 1; j < 8; ++j) ss = __ffma2_rn(x[j], x[j], ss);
+        float t = ss.x + ss.y;
 #pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-        if (norm) {
-          const float inv = 1.0f / sqrtf(ss * (1.0f / HD) + a.eps);
+        for (int o = LPH / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+        if ((is_q && a.q_norm) || (is_k && a.k_norm)) {
+          const float inv = 1.0f / sqrtf(t * (1.0f / HD) + a.eps);
+          const float* w = s_w[is_q ? 0 : 1];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[u][j] *= inv * norm[d0 + j];
+          for (int j = 0; j < 4; ++j) {
+            const float4 y = *reinterpret_cast<const float4*>(w + (j < 2 ? dA : dB) + 4 * (j & 1));
+            x[2 * j] = __fmul2_rn(x[2 * j], __fmul2_rn(make_float2(y.x, y.y), make_float2(inv, inv)));
+            x[2 * j + 1] = __fmul2_rn(x[2 * j + 1], __fmul2_rn(make_float2(y.z, y.w), make_float2(inv, inv)));
+          }
         }
       }
-      if (half > 0) {
-        const bool turns = (is_q || is_k) && d0 < rope.rot_dim;
-        if (rope.interleaved) {
-          if (turns) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 cs = s_cs[(d0 >> 1) + j];
-              const float x = v[u][2 * j], y = v[u][2 * j + 1];
-              v[u][2 * j] = x * cs.x - y * cs.y;
-              v[u][2 * j + 1] = y * cs.x + x * cs.y;
-            }
-          }
-        } else {
-          // the partner piece is half/8 lanes up or down within the head
-          const bool low = d0 < half;
-          const int lane = threadIdx.x & 31;
-          const int from = turns ? (low ? lane + (half >> 3) : lane - (half >> 3)) : lane;
+      if (turns && (is_q || is_k)) {
+        if (INTER) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float y = __shfl_sync(0xFFFFFFFFu, v[u][j], from);
-            if (turns) {
-              const float2 cs = s_cs[(low ? d0 : d0 - half) + j];
-              v[u][j] = low ? v[u][j] * cs.x - y * cs.y : v[u][j] * cs.x + y * cs.y;
-            }
+            const float cc = (j & 1) ? c[j >> 1].y : c[j >> 1].x, sn = (j & 1) ? s[j >> 1].y : s[j >> 1].x;
+            x[j] = __ffma2_rn(x[j], make_float2(cc, cc), __fmul2_rn(make_float2(x[j].y, x[j].x), make_float2(-sn, sn)));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = x[j], z = x[4 + j];
+            x[j] = __ffma2_rn(y, c[j], __fmul2_rn(z, make_float2(-s[j].x, -s[j].y)));
+            x[4 + j] = __ffma2_rn(z, c[j], __fmul2_rn(y, s[j]));
           }
         }
       }
-      if (p < np) {
+      if (h < heads) {
+        T* out = nullptr;
         if (is_q) {
-          st8(static_cast<T*>(a.Q) + (static_cast<size_t>(row) * a.H + h) * HD + d0, v[u]);
+          out = static_cast<T*>(a.Q) + (static_cast<size_t>(row) * a.H + h) * HD;
         } else if (dst >= 0) {
           const int kvh = is_k ? h - a.H : h - a.H - a.KVH;
-          T* base = static_cast<T*>(is_k ? a.kv.k : a.kv.v);
-          st8(base + static_cast<size_t>(dst + static_cast<long long>(kvh) * a.kv.page_size) * HD + d0, v[u]);
+          out = static_cast<T*>(is_k ? a.kv.k : a.kv.v) +
+                static_cast<size_t>(dst + static_cast<long long>(kvh) * a.kv.page_size) * HD;
+        }
+        if (out) {
+          st8(out + dA, *reinterpret_cast<const float(*)[8]>(&v[u][0]));
+          st8(out + dB, *reinterpret_cast<const float(*)[8]>(&v[u][8]));
         }
       }
     }
@@ -235,14 +258,14 @@ qkv_append_any_kernel(QkvArgs a, const __grid_constant__ e3_rope rope) {
   }
 }
 
-template <typename T>
+template <typename T, bool INTER>
 cudaError_t launch_qkv(const QkvArgs& a, const e3_rope& rope, int rows, bool vec, cudaStream_t s) {
   const dim3 grid(rows), block(kQkvThreads);
   if (vec) switch (a.hd) {
-      case 32: return launch_pdl(qkv_append_kernel<T, 32>, grid, block, 0, s, 1, a, rope);
-      case 64: return launch_pdl(qkv_append_kernel<T, 64>, grid, block, 0, s, 1, a, rope);
-      case 128: return launch_pdl(qkv_append_kernel<T, 128>, grid, block, 0, s, 1, a, rope);
-      case 256: return launch_pdl(qkv_append_kernel<T, 256>, grid, block, 0, s, 1, a, rope);
+      case 32: return launch_pdl(qkv_append_kernel<T, 32, INTER>, grid, block, 0, s, 1, a, rope);
+      case 64: return launch_pdl(qkv_append_kernel<T, 64, INTER>, grid, block, 0, s, 1, a, rope);
+      case 128: return launch_pdl(qkv_append_kernel<T, 128, INTER>, grid, block, 0, s, 1, a, rope);
+      case 256: return launch_pdl(qkv_append_kernel<T, 256, INTER>, grid, block, 0, s, 1, a, rope);
       default: break;
     }
   return launch_pdl(qkv_append_any_kernel<T>, grid, block, 0, s, 1, a, rope);
@@ -257,9 +280,12 @@ e3_status launch_qkv_append(const void* qkv, size_t ld, int B, int R, const int3
   const e3_rope& rp = rope ? *rope : none;
   const QkvArgs a{qkv, ld, R, H, kv.n_kv_heads, kv.head_dim, n_rows, q_norm, k_norm, eps, pos, Q, kv, kv_len, dev_err};
   const int esz = kv.dt == E3_F32 ? 4 : 2;
-  const bool vec = aligned16(qkv) && aligned16(Q) && (ld * esz) % 16 == 0 && rp.rot_dim % (rp.interleaved ? 8 : 16) == 0;
-  const cudaError_t e = kv.dt == E3_F32 ? launch_qkv<float>(a, rp, B * R, vec, s)
-                                        : launch_qkv<__nv_bfloat16>(a, rp, B * R, vec, s);
+  const bool vec = aligned16(qkv) && aligned16(Q) && (ld * esz) % 16 == 0 && rp.rot_dim % 16 == 0;
+  const cudaError_t e =
+      kv.dt == E3_F32 ? (rp.interleaved ? launch_qkv<float, true>(a, rp, B * R, vec, s)
+                                        : launch_qkv<float, false>(a, rp, B * R, vec, s))
+                      : (rp.interleaved ? launch_qkv<__nv_bfloat16, true>(a, rp, B * R, vec, s)
+                                        : launch_qkv<__nv_bfloat16, false>(a, rp, B * R, vec, s));
   return e == cudaSuccess ? E3_OK : cuda_status(e, "qkv_append_kernel");
 }
 

@@ -309,7 +309,9 @@ def tree_qkv_append(qkv, ld, B, R, n_rows, n_q_heads, q_norm, k_norm, eps, rope:
 def _layer_arrays(fn, layers, others):
     if len(layers) != len(others):
         raise ValueError(f"{fn}: {len(layers)} 4-bit layers and {len(others)} 16-bit ones")
-    return (e3_kv4_layer * len(layers))(*layers), (e3_kv_layer * len(others))(*others)
+    # one copy of the descriptors' bytes (filling a ctypes array element by element takes longer than the launch)
+    return ((e3_kv4_layer * len(layers)).from_buffer_copy(b"".join(layers)),
+            (e3_kv_layer * len(others)).from_buffer_copy(b"".join(others)))
 
 
 def kv4_append(layers, src, B, max_rows, rows, n_rows, n_add, kv_len, kv_len_next, dev_err=None, stream=None):

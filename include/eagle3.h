@@ -486,7 +486,8 @@ typedef struct {
  * sets it and skips that row.
  * layers, src: host arrays of L descriptors of one geometry each (as kv_compact);
  * src bf16.  The two caches must not overlap.
- * Limits: 1 <= L <= E3_MAX_LAYERS, 1 <= B <= 65535, max_rows >= 1.
+ * Limits: 1 <= L <= E3_MAX_LAYERS, 1 <= B <= 65535, max_rows >= 1,
+ *   n_kv_heads * max_rows * head_dim / 16 < 2^31.
  * ------------------------------------------------------------------------- */
 E3_API e3_status kv4_append(const e3_kv4_layer* layers, const e3_kv_layer* src, int L, int B, int max_rows,
                             const int32_t* rows, const int32_t* n_rows, int n_add, const int32_t* kv_len,
