@@ -163,10 +163,19 @@ def ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_torch_c = None
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # torch's current stream as its handle; the call without the Stream object costs
+        # a thirtieth of torch.cuda.current_stream() (2.9 us, as long as a small launch)
+        global _torch_c
+        if _torch_c is None:
+            import torch
+            torch.cuda.current_stream()  # initializes CUDA on first use
+            _torch_c = torch._C
+        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
