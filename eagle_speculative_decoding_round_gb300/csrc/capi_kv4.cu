@@ -160,6 +160,7 @@ E3_API e3_status tree_verify_attn4(const void* Q, const e3_kv4_layer* kv, const 
   E3_REQUIRE(B >= 1 && B <= 65535 && R >= 1 && R <= E3_MAX_NODES + 1, E3_ERR_SHAPE, "%s: B=%d R=%d", fn, B, R);
   E3_REQUIRE(n_q_heads >= 1 && n_q_heads <= 65535 && n_q_heads % kv->n_kv_heads == 0, E3_ERR_SHAPE,
              "%s: n_q_heads %d not a multiple of n_kv_heads %d", fn, n_q_heads, kv->n_kv_heads);
+  E3_REQUIRE(static_cast<long long>(B) * R * n_q_heads < (1ll << 31), E3_ERR_SHAPE, "%s: B*R*n_q_heads too large", fn);
   E3_REQUIRE(max_kv_len >= 0 && max_kv_len <= (1 << 30), E3_ERR_SHAPE, "%s: max_kv_len=%d", fn, max_kv_len);
   E3_REQUIRE(max_kv_len <= static_cast<long long>(kv->max_pages) * kv->page_size, E3_ERR_CAPACITY,
              "%s: max_kv_len %d exceeds the pages", fn, max_kv_len);

@@ -4,9 +4,9 @@
 // 三步走): the 4-bit prefix is split across CTAs, the tree nodes' bf16 tail joins the
 // last segment, partial (o, m, l) records are merged by their log-sum-exp.
 //
-// verify4_mma_kernel: one CTA = (16 query rows, segment) of one KV head; its warps take
-// 16-key granules in turn, each with a running softmax of its own, merged at the end.
-// A granule's codes and scales reach the warp's ring in shared memory by cp.async.  The
+// verify4_mma_kernel: a warp works alone on 16 query rows of one KV head and a run of
+// 16-key granules, whose codes and scales reach its ring in shared memory by cp.async.
+// Warps share nothing: one's waits pass under the others' arithmetic.  The
 // codes become fp16 matrix operands in registers: a value c * e (e2m1 times e4m3) has at
 // most six significant bits and lies in [2^-10, 2688], so the fp16 product is exact; Q
 // is scaled by a power of two per row (its largest magnitude to [1, 2)), so that its
@@ -17,7 +17,7 @@
 //
 // The dims of a head and the keys of a granule may be taken in any order by the
 // contractions.  K: thread (g, c) = (lane / 4, lane % 4) reads hd/4 consecutive dims of
-// one key, its k-slots of every 16-dim step.  V: it reads hd/8 consecutive dims of four
+// two keys, its k-slots of every 16-dim step.  V: it reads hd/8 consecutive dims of four
 // keys; codes of two keys are interleaved as integers so that one conversion gives the
 // (key, key') pair that the operand wants.
 #include <cuda_fp16.h>
@@ -27,6 +27,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "e3_common.cuh"
 #include "e3_kernels.h"
@@ -45,11 +46,69 @@ constexpr int kStages = 4;  // granules in a warp's ring
 // fp16's subnormal step is 2^-32 of a row's largest weight.
 constexpr float kHead = 7.0f, kTop = 15.0f;
 
+// How the work is shared.  A pair is (request, KV head, tile of `rows` query rows); its
+// units are granules of `keys` prefix keys and then of `keys` tree nodes.  All pairs' units in a
+// row, request by request, are cut into equal shares, one per worker (a warp), whatever
+// the requests' lengths: a worker may end one pair and begin the next.  The part of pair
+// p that worker c computed is record p + c (both only grow along the row, so no two
+// coincide).
 struct V4Geom {
-  int B, R, H, KVH, G, RG;
-  int S, chunk;  // prefix segments of `chunk` keys; the last also takes the tail
+  int B, R, H, KVH, G;
+  int rows;     // query rows of a tile
+  int RG;       // row tiles of a KV head
+  int workers;  // shares
+  int min_share;
   int max_kv_len;
 };
+
+// Units of request b's pairs, 0 if its length is out of bounds.
+template <int KEYS>
+__device__ __forceinline__ int pair_units(const V4Geom& g, const e3_kv4_layer& kv, int P) {
+  if (P < 0 || P > g.max_kv_len || P > static_cast<long long>(kv.max_pages) * kv.page_size) return 0;
+  return (P + KEYS - 1) / KEYS + (g.R + KEYS - 1) / KEYS;
+}
+
+// Where a worker begins in the row of units.  Every lane of the warp calls it and gets the
+// same answer.
+struct V4Place {
+  long long share, before;  // units of a share; units before request b
+  int b;                    // the request that holds the share's first unit (B: none)
+};
+template <int KEYS>
+__device__ __forceinline__ V4Place find_place(const V4Geom& g, const e3_kv4_layer& kv, const int32_t* kv_len, int worker) {
+  const int lane = threadIdx.x & 31;
+  const long long Q = static_cast<long long>(g.KVH) * g.RG;
+  long long total = 0;
+  for (int b0 = 0; b0 < g.B; b0 += 32) {
+    const int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv, kv_len[b0 + lane]) : 0;
+    total += __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(u));
+  }
+  V4Place f;
+  f.share = max((total * Q + g.workers - 1) / g.workers, static_cast<long long>(g.min_share));
+  const long long at = f.share * worker;
+  long long base = 0;
+  f.b = g.B;
+  f.before = total * Q;
+  for (int b0 = 0; b0 < g.B; b0 += 32) {
+    const int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv, kv_len[b0 + lane]) : 0;
+    unsigned incl = static_cast<unsigned>(u);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const long long end = (base + incl) * Q;
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, end > at);
+    if (hit) {
+      const int k = __ffs(hit) - 1;
+      f.b = b0 + k;
+      f.before = (base + __shfl_sync(0xFFFFFFFFu, incl, k) - __shfl_sync(0xFFFFFFFFu, static_cast<unsigned>(u), k)) * Q;
+      break;
+    }
+    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  return f;
+}
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
@@ -73,15 +132,28 @@ __device__ __forceinline__ void mma_b16(float (&c)[4], const uint32_t (&a)[4], u
 }
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
-// byte `i` of w (two 4-bit values, low first) as an fp16 pair
-__device__ __forceinline__ __half2 cvt4(uint32_t w, int i) {
-  return __half2(__half2_raw(__nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(w >> (8 * i)), __NV_E2M1)));
+// the four bytes of w (two 4-bit values each, low first) as fp16 pairs
+__device__ __forceinline__ void cvt4(uint32_t w, __half2 (&h)[4]) {
+  uint32_t r[4];
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = u2h(r[i]);
 }
 // two e4m3 bytes (low first) as an fp16 pair
 __device__ __forceinline__ __half2 cvt8(uint32_t w) {
   return __half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3)));
 }
-// key of column j of score tile t within a granule: columns 2c and 2c + 1 hold keys c
+// the transpose of an 8 x 8 matrix of 16-bit values, thread (g, c) holding row g, columns 2c, 2c + 1
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// key of row j of the score tile's half t within a granule: rows 2c and 2c + 1 hold keys c
 // and 4 + (c ^ 1), so that the keys read together lie in different shared-memory banks
 __device__ __forceinline__ int key_of(int t, int j) { return 8 * t + ((j & 1) ? 4 + ((j >> 1) ^ 1) : (j >> 1)); }
 
@@ -92,10 +164,7 @@ struct V4Cfg {
   static constexpr int CODES = kGran * ROWB;          // bytes per operand and granule
   static constexpr int SCALES = kGran * SCB;
   static constexpr int STAGE = 2 * (CODES + SCALES);  // K codes, V codes, K scales, V scales
-  static constexpr int RING = kWarps * kStages * STAGE;
-  static constexpr int PITCH = HD + 4;                // floats per merge row
-  static constexpr int MERGE = kWarps * 16 * (PITCH + 2) * 4;
-  static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+  static constexpr int SMEM = kWarps * kStages * STAGE;
 };
 
 // 16-byte piece `ch` of key `key`'s codes within a granule: for 64-byte rows every
@@ -105,439 +174,517 @@ __device__ __forceinline__ int code_off(int key, int ch) {
   return HD == 128 ? key * 64 + ((ch ^ (((key >> 1) & 1) << 1)) << 4) : key * 32 + (ch << 4);
 }
 
-template <int HD>
-__global__ void __launch_bounds__(kWarps * 32, 3)
-verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, e3_kv4_layer kv, e3_kv_layer tail,
-                   const int32_t* __restrict__ kv_len, const uint64_t* __restrict__ mask, V4Geom g, float sm_scale,
-                   float* __restrict__ ws_o, float2* __restrict__ ws_ml, int32_t* dev_err) {
+// NR: tiles of eight query rows (1 or 2).  K is the first operand of S^T = K Q^T (16 keys x
+// 8 rows) and V^T the first of O^T = V^T P^T (16 dims x 8 rows), so a few query rows cost
+// few instructions and few accumulators; the probabilities change their place between
+// the two by a register transpose (movmatrix).
+template <int HD, int NR>
+__global__ void __launch_bounds__(kWarps * 32, NR == 1 ? 4 : 2)
+verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e3_kv4_layer kv,
+                   const __grid_constant__ e3_kv_layer tail, const int32_t* __restrict__ kv_len,
+                   const uint64_t* __restrict__ mask, const __grid_constant__ V4Geom g, float sm_scale,
+                   float* __restrict__ ws_o, float2* __restrict__ ws_ml, int32_t* __restrict__ ends, int32_t* dev_err) {
   using C = V4Cfg<HD>;
-  constexpr int KS = HD / 16;   // 16-dim steps of Q K^T
-  constexpr int NT = HD / 8;    // 8-dim output tiles
+  constexpr int ROWS = 8 * NR;
+  constexpr int KS = HD / 16;   // 16-dim steps of K Q^T
+  constexpr int MT = HD / 16;   // 16-dim tiles of O^T
   constexpr int DK = HD / 4;    // dims of a key that a thread's K operand holds
   constexpr int DV = HD / 8;    // dims that a thread's V operand holds
   extern __shared__ __align__(16) unsigned char smem[];
   pdl_wait();
   pdl_trigger();
-  const int rg = blockIdx.x % g.RG, s = blockIdx.x / g.RG;
-  const int kvh = blockIdx.y, b = blockIdx.z;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gq = lane >> 2, tq = lane & 3;
-  const int P = kv_len[b];
-  if (P < 0 || P > g.max_kv_len || P > static_cast<long long>(kv.max_pages) * kv.page_size) {
-    if (threadIdx.x == 0 && blockIdx.x == 0 && kvh == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
-    return;
-  }
-  const int k0 = min(P, s * g.chunk), k1 = min(P, k0 + g.chunk);
-  const int ngran = (k1 - k0 + kGran - 1) / kGran;
+  const int worker = blockIdx.x * kWarps + warp, Qn = g.KVH * g.RG;
+  if (blockIdx.x == 0)  // requests whose length is out of bounds
+    for (int b = threadIdx.x; b < g.B; b += kWarps * 32)
+      if (pair_units<kGran>(g, kv, kv_len[b]) == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+  const V4Place at = find_place<kGran>(g, kv, kv_len, worker);
+  int b = at.b;
+  if (b >= g.B) return;
+  long long todo = at.share;
+  int units = pair_units<kGran>(g, kv, kv_len[b]);
+  int pq = static_cast<int>((at.share * worker - at.before) / units);  // the pair within the request
+  int x0 = static_cast<int>(at.share * worker - at.before - static_cast<long long>(pq) * units);
   unsigned char* ring = smem + warp * kStages * C::STAGE;
+  for (;;) {
+    // one pair's part of this share: units [x0, x1)
+    const int P = kv_len[b];
+    const int x1 = static_cast<int>(min(static_cast<long long>(units), x0 + todo));
+    const int kvh = pq / g.RG, rg = pq - kvh * g.RG;
+    const int NG = (P + kGran - 1) / kGran;
+    const int ga = x0, ngran = max(0, min(x1, NG) - x0);  // the prefix granules
 
-  // granule `gi` of this segment into ring stage `st`
-  auto load_granule = [&](int gi, int st) {
-    if (gi < ngran) {
-      const int t = k0 + gi * kGran;
-      const int page = kv.page_table[static_cast<size_t>(b) * kv.max_pages + t / kv.page_size];
+    // granules are loaded in order: this lane's addresses move along a page, the next
+    // page's id is read a page ahead
+    const int32_t* table = kv.page_table + static_cast<size_t>(b) * kv.max_pages;
+    int lpi = ga * kGran / kv.page_size, lslot = ga * kGran - lpi * kv.page_size, lgi = 0;
+    int npage = ngran > 0 ? table[lpi] : 0;
+    const unsigned char *lk = nullptr, *lv = nullptr, *ls = nullptr;
+    int lbytes = 0;
+    constexpr int NS = C::SCALES / 16;  // 16-byte pieces of one operand's scales
+    auto enter_page = [&](int page, int slot) {
       const bool ok = page >= 0 && page < kv.n_pages;
       if (!ok && lane == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
-      const size_t row = ok ? (static_cast<size_t>(page) * g.KVH + kvh) * kv.page_size + t % kv.page_size : 0;
-      const int bytes = ok ? 16 : 0;
-      const uint32_t base = su32(ring + st * C::STAGE);
-      const unsigned char* kc = static_cast<const unsigned char*>(kv.k) + row * C::ROWB;
-      const unsigned char* vc = static_cast<const unsigned char*>(kv.v) + row * C::ROWB;
-#pragma unroll
-      for (int i = 0; i < C::CODES / 512; ++i) {
-        const int p = i * 32 + lane;  // piece within the granule
-        const int off = code_off<HD>(p / (C::ROWB / 16), p % (C::ROWB / 16));
-        cp16(base + off, kc + p * 16, bytes);
-        cp16(base + C::CODES + off, vc + p * 16, bytes);
-      }
-      constexpr int NS = C::SCALES / 16;  // pieces of one operand's scales
-      if (lane < 2 * NS) {
-        const unsigned char* sc = static_cast<const unsigned char*>(lane < NS ? kv.k_scale : kv.v_scale) + row * C::SCB;
-        cp16(base + 2 * C::CODES + lane * 16, sc + (lane % NS) * 16, bytes);
-      }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) load_granule(warp + i * kWarps, i);
-
-  // Q rows of this thread (gq and gq + 8 of the tile): dims [DK tq, DK (tq + 1))
-  uint32_t qa[KS][4];
-  const int rows = g.G * g.R;
-  int node[2], head[2];
-  bool rowv[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = rg * 16 + gq + 8 * h;
-    rowv[h] = r < rows;
-    node[h] = rowv[h] ? r / g.G : 0;
-    head[h] = kvh * g.G + (rowv[h] ? r % g.G : 0);
-    const uint2* qp =
-        reinterpret_cast<const uint2*>(Q + ((static_cast<size_t>(b) * g.R + node[h]) * g.H + head[h]) * HD + DK * tq);
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const uint2 x = rowv[h] ? qp[ks] : make_uint2(0u, 0u);
-      qa[ks][h] = x.x;
-      qa[ks][2 + h] = x.y;
-    }
-  }
-  float o[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
-  bool poison[2] = {false, false};  // the row sees a tail node with a non-finite V
-
-  // running softmax over one granule's scores (already scaled, -Inf where unseen):
-  // probabilities replace the scores; o and l follow the moved base
-  auto softmax = [&](float (&sc)[2][4]) {
-    float bm[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      bm[h] = fmaxf(fmaxf(sc[0][2 * h], sc[0][2 * h + 1]), fmaxf(sc[1][2 * h], sc[1][2 * h + 1]));
-      bm[h] = fmaxf(bm[h], __shfl_xor_sync(0xFFFFFFFFu, bm[h], 1));
-      bm[h] = fmaxf(bm[h], __shfl_xor_sync(0xFFFFFFFFu, bm[h], 2));
-    }
-    const bool move = bm[0] > m[0] + kTop || bm[1] > m[1] + kTop;
-    if (__any_sync(0xFFFFFFFFu, move)) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float nm = fmaxf(m[h], bm[h] - kHead);
-        const float corr = nm == -INFINITY ? 1.0f : ex2(m[h] - nm);
-        m[h] = nm;
-        l[h] *= corr;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          o[n][2 * h] *= corr;
-          o[n][2 * h + 1] *= corr;
-        }
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float sub = m[h] == -INFINITY ? 0.0f : m[h];
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          sc[t][2 * h + e] = ex2(sc[t][2 * h + e] - sub);
-          l[h] += sc[t][2 * h + e];
-        }
-    }
-  };
-
-  // the tree tail (last segment): granules of 16 nodes, warps in turn, bf16
-  if (s == g.S - 1) {
-    const float c2 = sm_scale * kLog2e;
-    const int words = (g.R + 63) >> 6;
-    const __nv_bfloat16* tk = static_cast<const __nv_bfloat16*>(tail.k);
-    const __nv_bfloat16* tv = static_cast<const __nv_bfloat16*>(tail.v);
-    auto tail_row = [&](int j) -> long long {  // row of tail slot j, -1 beyond R or on a bad page
-      if (j >= g.R) return -1;
-      const int page = tail.page_table[static_cast<size_t>(b) * tail.max_pages + j / tail.page_size];
-      if (page < 0 || page >= tail.n_pages) {
-        dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
-        return -1;
-      }
-      return (static_cast<long long>(page) * g.KVH + kvh) * tail.page_size + j % tail.page_size;
+      const size_t row = ok ? (static_cast<size_t>(page) * g.KVH + kvh) * kv.page_size + slot : 0;
+      lbytes = ok ? 16 : 0;  // (zeros instead of a bad page's bytes)
+      lk = static_cast<const unsigned char*>(kv.k) + row * C::ROWB + lane * 16;
+      lv = static_cast<const unsigned char*>(kv.v) + row * C::ROWB + lane * 16;
+      ls = static_cast<const unsigned char*>(lane < NS ? kv.k_scale : kv.v_scale) + row * C::SCB + (lane % NS) * 16;
     };
-    for (int j0 = warp * kGran; j0 < g.R; j0 += kWarps * kGran) {
-      float sc[2][4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
-        const long long row = tail_row(j0 + key_of(t, gq));
-        const uint2* kp = reinterpret_cast<const uint2*>(tk + max(row, 0ll) * HD + DK * tq);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint2 x = row >= 0 ? kp[ks] : make_uint2(0u, 0u);
-          mma_b16(sc[t], qa[ks], x.x, x.y);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint64_t* mr = mask + (static_cast<size_t>(b) * g.R + node[h]) * words;
-        const uint64_t bits = mr[j0 >> 6];  // a granule lies within one word
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int j = j0 + key_of(t, 2 * tq + e);
-            const bool see = rowv[h] && j < g.R && ((bits >> (j & 63)) & 1ull);
-            sc[t][2 * h + e] = see ? sc[t][2 * h + e] * c2 : -INFINITY;
-          }
-      }
-      softmax(sc);
-      uint32_t pa[4];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        pa[2 * t] = pack2_bf16(sc[t][0], sc[t][1]);
-        pa[2 * t + 1] = pack2_bf16(sc[t][2], sc[t][3]);
-      }
-      uint32_t raw[4][DV / 2];  // keys (tile 0: two, tile 1: two), DV dims each
-      uint32_t badk = 0u;       // keys of the granule with a non-finite V, as bits
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = key_of(i >> 1, 2 * tq + (i & 1));
-        const long long row = tail_row(j0 + j);
-        const uint2* vp = reinterpret_cast<const uint2*>(tv + max(row, 0ll) * HD + DV * gq);
-        bool bad = false;
-#pragma unroll
-        for (int d = 0; d < DV / 4; ++d) {
-          const uint2 x = row >= 0 ? vp[d] : make_uint2(0u, 0u);
-          raw[i][2 * d] = x.x;
-          raw[i][2 * d + 1] = x.y;
-          bad |= (x.x & 0x7F80u) == 0x7F80u || (x.x & 0x7F800000u) == 0x7F800000u || (x.y & 0x7F80u) == 0x7F80u ||
-                 (x.y & 0x7F800000u) == 0x7F800000u;
-        }
-        if (bad) {  // rows that do not see the node must not meet it in 0 * Inf
-          badk |= 1u << j;
-#pragma unroll
-          for (int d = 0; d < DV / 2; ++d) raw[i][d] = 0u;
-        }
-      }
-      badk = __reduce_or_sync(0xFFFFFFFFu, badk);
-      if (badk) {
-        // a key's other dims may sit in another thread: drop the whole node everywhere
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if ((badk >> key_of(i >> 1, 2 * tq + (i & 1))) & 1u)
-#pragma unroll
-            for (int d = 0; d < DV / 2; ++d) raw[i][d] = 0u;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint64_t bits = mask[(static_cast<size_t>(b) * g.R + node[h]) * words + (j0 >> 6)];
-          poison[h] |= ((bits >> (j0 & 63)) & badk) != 0ull;
-        }
-      }
-#pragma unroll
-      for (int d = 0; d < DV / 2; ++d) {
-        const uint32_t lo0 = __byte_perm(raw[0][d], raw[1][d], 0x5410), hi0 = __byte_perm(raw[0][d], raw[1][d], 0x7632);
-        const uint32_t lo1 = __byte_perm(raw[2][d], raw[3][d], 0x5410), hi1 = __byte_perm(raw[2][d], raw[3][d], 0x7632);
-        mma_b16(o[2 * d], pa, lo0, lo1);
-        mma_b16(o[2 * d + 1], pa, hi0, hi1);
-      }
+    auto read_ahead = [&]() { npage = lpi + 1 < kv.max_pages ? table[lpi + 1] : -1; };
+    if (ngran > 0) {
+      enter_page(npage, lslot);
+      read_ahead();
     }
-  }
+    auto load_granule = [&](int st) {  // the next granule into ring stage `st`
+      if (lgi < ngran) {
+        if (lslot == kv.page_size) {
+          lslot = 0;
+          ++lpi;
+          enter_page(npage, 0);
+          read_ahead();
+        }
+        const uint32_t base = su32(ring + st * C::STAGE);
+#pragma unroll
+        for (int i = 0; i < C::CODES / 512; ++i) {
+          const int p = i * 32 + lane;  // piece within the granule
+          const int off = code_off<HD>(p / (C::ROWB / 16), p % (C::ROWB / 16));
+          cp16(base + off, lk + i * 512, lbytes);
+          cp16(base + C::CODES + off, lv + i * 512, lbytes);
+        }
+        if (lane < 2 * NS) cp16(base + 2 * C::CODES + lane * 16, ls, lbytes);
+        const int step = lbytes ? 1 : 0;  // (a bad page's addresses stay where they are)
+        lk += step * C::CODES;
+        lv += step * C::CODES;
+        ls += step * C::SCALES;
+        ++lgi;
+        lslot += kGran;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) load_granule(i);
 
-  // Q to fp16, each row's largest magnitude scaled to [1, 2); the scores' factor follows
-  float c2[2];
+    // Q as the second operand: thread (gq, tq) holds row gq of each tile, dims [DK tq, DK (tq + 1))
+    uint32_t qb[NR][KS][2];
+    const int rows = g.G * g.R;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t am = 0u;  // largest magnitude as bf16 bits
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t w = qa[ks][2 * x + h];
-        am = max(am, max(w & 0x7FFFu, (w >> 16) & 0x7FFFu));
-      }
-    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-    am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-    const int ex = max(static_cast<int>(am >> 7), 1) - 127;  // exponent of the largest magnitude
-    // 2^-ex in two factors (ex reaches 128 for Inf and NaN, -126 for subnormals)
-    const float f0 = __uint_as_float(static_cast<uint32_t>(127 - ex / 2) << 23);
-    const float f1 = __uint_as_float(static_cast<uint32_t>(127 - (ex - ex / 2)) << 23);
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint32_t w = qa[ks][2 * x + h];
-        const float lo = __uint_as_float(w << 16) * f0 * f1, hi = __uint_as_float(w & 0xFFFF0000u) * f0 * f1;
-        qa[ks][2 * x + h] = h2u(__floats2half2_rn(lo, hi));
-      }
-    c2[h] = sm_scale * kLog2e * kv.k_unit * __uint_as_float(static_cast<uint32_t>(127 + ex / 2) << 23) *
-            __uint_as_float(static_cast<uint32_t>(127 + (ex - ex / 2)) << 23);
-  }
-  // o holds V values in units of v_unit from here on
-  const float inv_vu = 1.0f / kv.v_unit;
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[n][e] *= inv_vu;
-
-  for (int i = 0; warp + i * kWarps < ngran; ++i) {
-    load_granule(warp + (i + kStages - 1) * kWarps, (i + kStages - 1) % kStages);
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-    __syncwarp();
-    const unsigned char* st = ring + (i % kStages) * C::STAGE;
-    const int left = k1 - (k0 + (warp + i * kWarps) * kGran);  // keys of the granule below k1
-    float sc[2][4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.0f;
-      const int key = key_of(t, gq);
-      uint32_t w[DK / 8];
-      if (HD == 128) {
-        const uint4 x = *reinterpret_cast<const uint4*>(st + code_off<HD>(key, tq));
-        w[0] = x.x, w[1] = x.y, w[DK / 8 - 2] = x.z, w[DK / 8 - 1] = x.w;
-      } else {
-        const uint2 x = *reinterpret_cast<const uint2*>(st + key * C::ROWB + 8 * tq);
-        w[0] = x.x, w[1] = x.y;
-      }
-      const unsigned char* sp = st + 2 * C::CODES + key * C::SCB;
-      __half2 e2[DK / 16];  // the scale of each 16 dims, in both halves
-      if (HD == 128) {
-        const uint32_t e = h2u(cvt8(*reinterpret_cast<const uint16_t*>(sp + 2 * tq)));
-        e2[0] = u2h(__byte_perm(e, e, 0x1010));
-        e2[DK / 16 - 1] = u2h(__byte_perm(e, e, 0x3232));
-      } else {
-        const uint32_t e = h2u(cvt8(sp[tq]));
-        e2[0] = u2h(__byte_perm(e, e, 0x1010));
-      }
+    for (int nr = 0; nr < NR; ++nr) {
+      const int r = rg * ROWS + 8 * nr + gq;
+      const bool in = r < rows;
+      const int node = in ? r / g.G : 0, head = kvh * g.G + (in ? r - node * g.G : 0);
+      const uint2* qp = reinterpret_cast<const uint2*>(Q + ((static_cast<size_t>(b) * g.R + node) * g.H + head) * HD + DK * tq);
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        const __half2 x0 = __hmul2(cvt4(w[ks >> 1], 2 * (ks & 1)), e2[ks >> 2]);
-        const __half2 x1 = __hmul2(cvt4(w[ks >> 1], 2 * (ks & 1) + 1), e2[ks >> 2]);
-        mma_f16(sc[t], qa[ks], h2u(x0), h2u(x1));
+        const uint2 x = in ? qp[ks] : make_uint2(0u, 0u);
+        qb[nr][ks][0] = x.x;
+        qb[nr][ks][1] = x.y;
       }
     }
+    // O^T: tile j's accumulators are dims DV gq + 2j and + 1 (rows gq and gq + 8) of query
+    // rows 2 tq and 2 tq + 1 of each row tile
+    float o[NR][MT][4];
+    float m[NR][2], l[NR][2];   // base and sum of query rows 2 tq, 2 tq + 1
+    bool poison[NR][2];         // the row sees a tail node with a non-finite V
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sc[t][e] = key_of(t, 2 * tq + (e & 1)) < left ? sc[t][e] * c2[e >> 1] : -INFINITY;
-    softmax(sc);
-    uint32_t pa[4];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      pa[2 * t] = h2u(__floats2half2_rn(sc[t][0], sc[t][1]));
-      pa[2 * t + 1] = h2u(__floats2half2_rn(sc[t][2], sc[t][3]));
+      for (int j = 0; j < MT; ++j) o[nr][j][0] = o[nr][j][1] = o[nr][j][2] = o[nr][j][3] = 0.0f;
+      m[nr][0] = m[nr][1] = -INFINITY;
+      l[nr][0] = l[nr][1] = 0.0f;
+      poison[nr][0] = poison[nr][1] = false;
     }
-    // V: words of DV dims of the four keys, and the scale pair of each two keys (0 where
-    // the key is beyond the prefix: whatever its slot holds, it adds 0)
-    uint32_t vw[4][DV / 8];
-    uint32_t ve[4];
+
+    // running softmax over one granule's scores (already scaled, -Inf where unseen): sc[nr]
+    // holds keys gq (0, 1) and gq + 8 (2, 3) of query rows 2 tq, 2 tq + 1; probabilities
+    // replace the scores; o and l follow the moved base
+    auto softmax = [&](float (&sc)[NR][4]) {
+      float bm[NR][2];
+      bool move = false;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int key = key_of(x >> 1, 2 * tq + (x & 1));
-      if (HD == 128) {
-        const uint2 y = *reinterpret_cast<const uint2*>(st + C::CODES + code_off<HD>(key, gq >> 1) + 8 * (gq & 1));
-        vw[x][0] = y.x, vw[x][DV / 8 - 1] = y.y;
-      } else {
-        vw[x][0] = *reinterpret_cast<const uint32_t*>(st + C::CODES + key * C::ROWB + 4 * gq);
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float x = fmaxf(sc[nr][e], sc[nr][2 + e]);
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+          bm[nr][e] = x;
+          move |= x > m[nr][e] + kTop;
+        }
+      if (__any_sync(0xFFFFFFFFu, move)) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float nm = fmaxf(m[nr][e], bm[nr][e] - kHead);
+            const float corr = nm == -INFINITY ? 1.0f : ex2(m[nr][e] - nm);
+            m[nr][e] = nm;
+            l[nr][e] *= corr;
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+              o[nr][j][e] *= corr;
+              o[nr][j][2 + e] *= corr;
+            }
+          }
       }
-      ve[x] = st[2 * C::CODES + C::SCALES + key * C::SCB + (DV * gq) / 16];
-      if (key >= left) ve[x] = 0u;
-    }
-    const __half2 e01 = cvt8(ve[0] | (ve[1] << 8)), e23 = cvt8(ve[2] | (ve[3] << 8));
 #pragma unroll
-    for (int w = 0; w < DV / 8; ++w) {
-      constexpr uint32_t kLo = 0x0F0F0F0Fu;
-      const uint32_t ev0 = (vw[0][w] & kLo) | ((vw[1][w] << 4) & ~kLo), od0 = ((vw[0][w] >> 4) & kLo) | (vw[1][w] & ~kLo);
-      const uint32_t ev1 = (vw[2][w] & kLo) | ((vw[3][w] << 4) & ~kLo), od1 = ((vw[2][w] >> 4) & kLo) | (vw[3][w] & ~kLo);
+      for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-      for (int d = 0; d < 4; ++d) {
-        mma_f16(o[8 * w + 2 * d], pa, h2u(__hmul2(cvt4(ev0, d), e01)), h2u(__hmul2(cvt4(ev1, d), e23)));
-        mma_f16(o[8 * w + 2 * d + 1], pa, h2u(__hmul2(cvt4(od0, d), e01)), h2u(__hmul2(cvt4(od1, d), e23)));
+        for (int e = 0; e < 2; ++e) {
+          const float sub = m[nr][e] == -INFINITY ? 0.0f : m[nr][e];
+          sc[nr][e] = ex2(sc[nr][e] - sub);
+          sc[nr][2 + e] = ex2(sc[nr][2 + e] - sub);
+          l[nr][e] += sc[nr][e] + sc[nr][2 + e];
+        }
+    };
+
+    // this part's granules of 16 tree nodes, in bf16
+    if (x1 > NG) {
+      const float c2 = sm_scale * kLog2e;
+      const int words = (g.R + 63) >> 6;
+      const __nv_bfloat16* tk = static_cast<const __nv_bfloat16*>(tail.k);
+      const __nv_bfloat16* tv = static_cast<const __nv_bfloat16*>(tail.v);
+      auto tail_row = [&](int j) -> long long {  // row of tail slot j, -1 beyond R or on a bad page
+        if (j >= g.R) return -1;
+        const int page = tail.page_table[static_cast<size_t>(b) * tail.max_pages + j / tail.page_size];
+        if (page < 0 || page >= tail.n_pages) {
+          dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+          return -1;
+        }
+        return (static_cast<long long>(page) * g.KVH + kvh) * tail.page_size + j % tail.page_size;
+      };
+#pragma unroll 1
+      for (int j0 = (max(x0, NG) - NG) * kGran; j0 < (x1 - NG) * kGran; j0 += kGran) {
+        // (V is loaded after the scores: both at once would cost the main loop its registers)
+        uint2 kr[2][KS];
+        uint32_t raw[4][DV / 2];  // V of keys (tile 0: two, tile 1: two), DV dims each
+        uint64_t bits[NR][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const long long row = tail_row(j0 + key_of(t, gq));
+          const uint2* kp = reinterpret_cast<const uint2*>(tk + max(row, 0ll) * HD + DK * tq);
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) kr[t][ks] = row >= 0 ? kp[ks] : make_uint2(0u, 0u);
+        }
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // (a granule lies within one mask word)
+            const int r = rg * ROWS + 8 * nr + 2 * tq + e;
+            bits[nr][e] = r < rows ? mask[(static_cast<size_t>(b) * g.R + r / g.G) * words + (j0 >> 6)] >> (j0 & 63) : 0ull;
+          }
+        float sc[NR][4];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          sc[nr][0] = sc[nr][1] = sc[nr][2] = sc[nr][3] = 0.0f;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const uint32_t a[4] = {kr[0][ks].x, kr[1][ks].x, kr[0][ks].y, kr[1][ks].y};
+            mma_b16(sc[nr], a, qb[nr][ks][0], qb[nr][ks][1]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = key_of(e >> 1, gq);
+            const bool see = j0 + j < g.R && ((bits[nr][e & 1] >> j) & 1ull);
+            sc[nr][e] = see ? sc[nr][e] * c2 : -INFINITY;
+          }
+        }
+        softmax(sc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const long long row = tail_row(j0 + key_of(i >> 1, 2 * tq + (i & 1)));
+          const uint2* vp = reinterpret_cast<const uint2*>(tv + max(row, 0ll) * HD + DV * gq);
+#pragma unroll
+          for (int d = 0; d < DV / 4; ++d) {
+            const uint2 x = row >= 0 ? vp[d] : make_uint2(0u, 0u);
+            raw[i][2 * d] = x.x;
+            raw[i][2 * d + 1] = x.y;
+          }
+        }
+        uint32_t badk = 0u;  // keys of the granule with a non-finite V, as bits
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          bool bad = false;
+#pragma unroll
+          for (int d = 0; d < DV / 2; ++d)
+            bad |= (raw[i][d] & 0x7F80u) == 0x7F80u || (raw[i][d] & 0x7F800000u) == 0x7F800000u;
+          if (bad) badk |= 1u << key_of(i >> 1, 2 * tq + (i & 1));
+        }
+        badk = __reduce_or_sync(0xFFFFFFFFu, badk);
+        if (badk) {
+          // rows that do not see such a node must not meet it in 0 * Inf: it leaves the
+          // product (its dims sit in several threads), rows that see it get NaN below
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((badk >> key_of(i >> 1, 2 * tq + (i & 1))) & 1u)
+#pragma unroll
+              for (int d = 0; d < DV / 2; ++d) raw[i][d] = 0u;
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) poison[nr][e] |= (bits[nr][e] & badk) != 0ull;
+        }
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          const uint32_t p0 = transpose8(pack2_bf16(sc[nr][0], sc[nr][1])), p1 = transpose8(pack2_bf16(sc[nr][2], sc[nr][3]));
+#pragma unroll
+          for (int d = 0; d < DV / 2; ++d) {
+            const uint32_t a[4] = {__byte_perm(raw[0][d], raw[1][d], 0x5410), __byte_perm(raw[0][d], raw[1][d], 0x7632),
+                                   __byte_perm(raw[2][d], raw[3][d], 0x5410), __byte_perm(raw[2][d], raw[3][d], 0x7632)};
+            mma_b16(o[nr][d], a, p0, p1);
+          }
+        }
       }
     }
-    __syncwarp();  // the stage may be refilled
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
+
+    // Q to fp16, each row's largest magnitude scaled to [1, 2); the scores' factor follows
+    float c2[NR][2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 1);
-    l[h] += __shfl_xor_sync(0xFFFFFFFFu, l[h], 2);
-    // poison is the same in a row's four threads (one mask word and one badk per granule)
-    if (poison[h])
+    for (int nr = 0; nr < NR; ++nr) {
+      uint32_t am = 0u;  // largest magnitude of row gq as bf16 bits
 #pragma unroll
-      for (int n = 0; n < NT; ++n) o[n][2 * h] = o[n][2 * h + 1] = __int_as_float(0x7FC00000);
-  }
-  // merge of the warps: every warp's (o, m, l) to shared memory, then each row by its threads
-  __syncthreads();
-  float* so = reinterpret_cast<float*>(smem);                  // [warp][16][PITCH]
-  float2* sml = reinterpret_cast<float2*>(so + kWarps * 16 * C::PITCH);  // [warp][16]
+      for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float* dst = so + (warp * 16 + gq + 8 * h) * C::PITCH;
-    // output column n' of tile n is dim DV n' + n: this thread has n' = 2 tq, 2 tq + 1
+        for (int x = 0; x < 2; ++x) am = __vmaxu2(am, qb[nr][ks][x] & 0x7FFF7FFFu);
+      am = max(am & 0xFFFFu, am >> 16);
+      am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+      am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+      const int ex = max(static_cast<int>(am >> 7), 1) - 127;  // exponent of the largest magnitude
+      // 2^-ex in two factors (ex reaches 128 for Inf and NaN, -126 for subnormals)
+      const float f0 = __uint_as_float(static_cast<uint32_t>(127 - ex / 2) << 23);
+      const float f1 = __uint_as_float(static_cast<uint32_t>(127 - (ex - ex / 2)) << 23);
 #pragma unroll
-    for (int e = 0; e < 2; ++e)
+      for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int n = 0; n < NT; n += 4)
-        *reinterpret_cast<float4*>(dst + DV * (2 * tq + e) + n) =
-            make_float4(o[n][2 * h + e], o[n + 1][2 * h + e], o[n + 2][2 * h + e], o[n + 3][2 * h + e]);
-    if (tq == 0) sml[warp * 16 + gq + 8 * h] = make_float2(m[h], l[h]);
-  }
-  __syncthreads();
-  constexpr int PER = HD / 8;  // dims of a thread: eight threads per row
-  const int rr = threadIdx.x >> 3, d0 = (threadIdx.x & 7) * PER;
-  const int r = rg * 16 + rr;
-  if (r >= rows) return;
-  float M = -INFINITY, L = 0.0f, wgt[kWarps];
+        for (int x = 0; x < 2; ++x) {
+          const uint32_t w = qb[nr][ks][x];
+          const float lo = __uint_as_float(w << 16) * f0 * f1, hi = __uint_as_float(w & 0xFFFF0000u) * f0 * f1;
+          qb[nr][ks][x] = h2u(__floats2half2_rn(lo, hi));
+        }
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sml[w * 16 + rr].y != 0.0f ? sml[w * 16 + rr].x : -INFINITY);
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const float2 ml = sml[w * 16 + rr];
-    wgt[w] = ml.y != 0.0f ? ex2(ml.x - M) : 0.0f;  // (a NaN sum stays one)
-    L += ml.y * wgt[w];
-  }
-  const float inv = L != 0.0f ? kv.v_unit / L : 0.0f;
-  const size_t rec =
-      ((static_cast<size_t>(b) * g.S + s) * g.R + r / g.G) * g.H + kvh * g.G + r % g.G;
-  float* dst = ws_o + rec * HD + d0;
-#pragma unroll
-  for (int d = 0; d < PER; d += 4) {
-    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float4 x = *reinterpret_cast<const float4*>(so + (w * 16 + rr) * C::PITCH + d0 + d);
-      a.x = fmaf(wgt[w], x.x, a.x);
-      a.y = fmaf(wgt[w], x.y, a.y);
-      a.z = fmaf(wgt[w], x.z, a.z);
-      a.w = fmaf(wgt[w], x.w, a.w);
+      for (int e = 0; e < 2; ++e) {  // row 2 tq + e is held by lanes 4 (2 tq + e) ..
+        const int er = __shfl_sync(0xFFFFFFFFu, ex, 4 * (2 * tq + e));
+        c2[nr][e] = sm_scale * kLog2e * kv.k_unit * __uint_as_float(static_cast<uint32_t>(127 + er / 2) << 23) *
+                    __uint_as_float(static_cast<uint32_t>(127 + (er - er / 2)) << 23);
+      }
     }
-    *reinterpret_cast<float4*>(dst + d) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    if (x1 > NG) {  // o holds V values in units of v_unit from here on
+      const float inv_vu = 1.0f / kv.v_unit;
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nr][j][e] *= inv_vu;
+    }
+
+#pragma unroll 1
+    for (int i = 0; i < ngran; ++i) {
+      load_granule((i + kStages - 1) % kStages);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      __syncwarp();
+      const unsigned char* st = ring + (i % kStages) * C::STAGE;
+      const int left = P - (ga + i) * kGran;  // keys below P from the granule's first
+      float sc[NR][4];
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) sc[nr][0] = sc[nr][1] = sc[nr][2] = sc[nr][3] = 0.0f;
+      uint32_t w[2][DK / 8];
+      __half2 e2[2][DK / 16];  // the scale of each 16 dims, in both halves
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int key = key_of(t, gq);
+        const unsigned char* sp = st + 2 * C::CODES + key * C::SCB;
+        if (HD == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(st + code_off<HD>(key, tq));
+          w[t][0] = x.x, w[t][1] = x.y, w[t][DK / 8 - 2] = x.z, w[t][DK / 8 - 1] = x.w;
+          const uint32_t e = h2u(cvt8(*reinterpret_cast<const uint16_t*>(sp + 2 * tq)));
+          e2[t][0] = u2h(__byte_perm(e, e, 0x1010));
+          e2[t][DK / 16 - 1] = u2h(__byte_perm(e, e, 0x3232));
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(st + key * C::ROWB + 8 * tq);
+          w[t][0] = x.x, w[t][1] = x.y;
+          const uint32_t e = h2u(cvt8(sp[tq]));
+          e2[t][0] = u2h(__byte_perm(e, e, 0x1010));
+        }
+      }
+#pragma unroll
+      for (int k2 = 0; k2 < KS / 2; ++k2) {
+        __half2 x[4], y[4];
+        cvt4(w[0][k2], x);
+        cvt4(w[1][k2], y);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t a[4] = {h2u(__hmul2(x[2 * k], e2[0][k2 >> 1])), h2u(__hmul2(y[2 * k], e2[1][k2 >> 1])),
+                                 h2u(__hmul2(x[2 * k + 1], e2[0][k2 >> 1])), h2u(__hmul2(y[2 * k + 1], e2[1][k2 >> 1]))};
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) mma_f16(sc[nr], a, qb[nr][2 * k2 + k][0], qb[nr][2 * k2 + k][1]);
+        }
+      }
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nr][e] = sc[nr][e] * c2[nr][e & 1];
+      if (left < kGran) {  // keys beyond the prefix
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key_of(e >> 1, gq) >= left) sc[nr][e] = -INFINITY;
+      }
+      softmax(sc);
+      uint32_t pb[NR][2];
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        pb[nr][0] = transpose8(h2u(__floats2half2_rn(sc[nr][0], sc[nr][1])));
+        pb[nr][1] = transpose8(h2u(__floats2half2_rn(sc[nr][2], sc[nr][3])));
+      }
+      // V: words of DV dims of the four keys, and the scale pair of each two keys (0 where
+      // the key is beyond the prefix: whatever its slot holds, it adds 0)
+      uint32_t vw[4][DV / 8];
+      uint32_t ve[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int key = key_of(x >> 1, 2 * tq + (x & 1));
+        if (HD == 128) {
+          const uint2 y = *reinterpret_cast<const uint2*>(st + C::CODES + code_off<HD>(key, gq >> 1) + 8 * (gq & 1));
+          vw[x][0] = y.x, vw[x][DV / 8 - 1] = y.y;
+        } else {
+          vw[x][0] = *reinterpret_cast<const uint32_t*>(st + C::CODES + key * C::ROWB + 4 * gq);
+        }
+        ve[x] = st[2 * C::CODES + C::SCALES + key * C::SCB + (DV * gq) / 16];
+      }
+      if (left < kGran)
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (key_of(x >> 1, 2 * tq + (x & 1)) >= left) ve[x] = 0u;
+      const __half2 e01 = cvt8(__byte_perm(ve[0], ve[1], 0x40)), e23 = cvt8(__byte_perm(ve[2], ve[3], 0x40));
+#pragma unroll
+      for (int x = 0; x < DV / 8; ++x) {
+        constexpr uint32_t kLo = 0x0F0F0F0Fu;
+        __half2 a0[4], a1[4], b0[4], b1[4];  // even and odd dims of the key pairs
+        cvt4((vw[0][x] & kLo) | ((vw[1][x] << 4) & ~kLo), a0);
+        cvt4(((vw[0][x] >> 4) & kLo) | (vw[1][x] & ~kLo), b0);
+        cvt4((vw[2][x] & kLo) | ((vw[3][x] << 4) & ~kLo), a1);
+        cvt4(((vw[2][x] >> 4) & kLo) | (vw[3][x] & ~kLo), b1);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const uint32_t a[4] = {h2u(__hmul2(a0[d], e01)), h2u(__hmul2(b0[d], e01)), h2u(__hmul2(a1[d], e23)),
+                                 h2u(__hmul2(b1[d], e23))};
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) mma_f16(o[nr][4 * x + d], a, pb[nr][0], pb[nr][1]);
+        }
+      }
+      __syncwarp();  // the stage may be refilled
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    // this part's record: o normalized by its own sum, the base and the sum
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float s = l[nr][e];
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 4);
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+        const int rr = 8 * nr + 2 * tq + e;
+        if (rg * ROWS + rr < rows) {
+          const size_t rec = (static_cast<size_t>(b) * Qn + pq + worker) * ROWS + rr;
+          // (poison is the same in all threads of a row: one mask word and one badk per granule)
+          const float inv = poison[nr][e] ? __int_as_float(0x7FC00000) : s != 0.0f ? kv.v_unit / s : 0.0f;
+          float* dst = ws_o + rec * HD + DV * gq;
+#pragma unroll
+          for (int j = 0; j < MT; j += 2)
+            *reinterpret_cast<float4*>(dst + 2 * j) = make_float4(o[nr][j][e] * inv, o[nr][j][2 + e] * inv,
+                                                                   o[nr][j + 1][e] * inv, o[nr][j + 1][2 + e] * inv);
+          if (gq == 0) ws_ml[rec] = make_float2(m[nr][e], s);
+        }
+      }
+    if (lane == 0) {
+      int32_t* e = ends + 2 * (static_cast<size_t>(b) * Qn + pq);
+      if (x0 == 0) e[0] = worker;
+      if (x1 == units) e[1] = worker;
+    }
+    // the next pair of this share
+    todo -= x1 - x0;
+    if (todo <= 0) break;
+    x0 = 0;
+    if (++pq == Qn) {
+      pq = 0;
+      for (++b; b < g.B; ++b) {
+        units = pair_units<kGran>(g, kv, kv_len[b]);
+        if (units > 0) break;
+      }
+      if (b >= g.B) break;
+    }
   }
-  if ((threadIdx.x & 7) == 0) ws_ml[rec] = make_float2(M, L);
 }
 
-// Merge of the segments' records: one warp per (b, i, h) row.
-template <int HD>
-__global__ void __launch_bounds__(256)
-verify4_merge_kernel(e3_kv4_layer kv, const int32_t* __restrict__ kv_len, V4Geom g, const float* __restrict__ ws_o,
-                     const float2* __restrict__ ws_ml, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
+// Merge of a pair's records: one warp per (b, i, h) row, hd/32 dims a lane.  ROWS: the
+// row tile of the kernel that wrote them.  The workers that began and ended the pair left
+// their numbers in `ends`, so the records are found without the search; the first
+// records' values are requested together with their weights.
+template <int HD, int ROWS, int KEYS>
+__global__ void __launch_bounds__(128)
+verify4_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __restrict__ kv_len,
+                     const __grid_constant__ V4Geom g, const float* __restrict__ ws_o, const float2* __restrict__ ws_ml,
+                     const int32_t* __restrict__ ends, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
   constexpr int PER = HD / 32;
+  constexpr int AHEAD = 8;
+  const int lane = threadIdx.x & 31;
+  const unsigned row = blockIdx.x * 4u + (threadIdx.x >> 5);
+  const unsigned stride = static_cast<unsigned>(g.R) * g.H;
+  const int b = static_cast<int>(row / stride);
+  if (b >= g.B) {
+    pdl_wait();
+    return;
+  }
+  const int ih = static_cast<int>(row - b * stride), i = ih / g.H, h = ih - i * g.H;
+  const int kvh = h / g.G, r = i * g.G + h - kvh * g.G, rt = r / ROWS;
+  const size_t pair = static_cast<size_t>(b) * g.KVH * g.RG + kvh * g.RG + rt;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  const long long stride = static_cast<long long>(g.R) * g.H;
-  if (row >= stride * g.B) return;
-  const int b = static_cast<int>(row / stride);
-  const int P = kv_len[b];
-  if (P < 0 || P > g.max_kv_len || P > static_cast<long long>(kv.max_pages) * kv.page_size) return;
-  const size_t base = static_cast<size_t>(b) * g.S * stride + row % stride;
-  // segments with keys: those the prefix reaches, and the last (the tail)
-  const int np = min(g.S - 1, (P + g.chunk - 1) / g.chunk);
-  auto seg = [&](int q) { return q < np ? q : g.S - 1; };
-  float M = -INFINITY;
-  for (int q = lane; q <= np; q += 32) {
-    const float2 ml = ws_ml[base + seg(q) * stride];
-    if (ml.y != 0.0f) M = fmaxf(M, ml.x);
+  const int P = kv_len[b], c0 = ends[2 * pair], c1 = ends[2 * pair + 1];
+  if (pair_units<KEYS>(g, kv, P) == 0) return;
+  const int n = c1 - c0 + 1;
+  const size_t base = (pair + c0) * ROWS + (r - rt * ROWS);  // then ROWS apart
+  using Vec = typename std::conditional<PER == 4, float4, float2>::type;
+  auto value = [&](int q) { return reinterpret_cast<const Vec*>(ws_o + (base + static_cast<size_t>(q) * ROWS) * HD)[lane]; };
+  Vec x[AHEAD];
+#pragma unroll
+  for (int q = 0; q < AHEAD; ++q)
+    if (q < n) x[q] = value(q);
+  float2 ml = lane < n ? ws_ml[base + static_cast<size_t>(lane) * ROWS] : make_float2(-INFINITY, 0.0f);
+  float M = ml.y != 0.0f ? ml.x : -INFINITY;
+  for (int q = lane + 32; q < n; q += 32) {
+    const float2 y = ws_ml[base + static_cast<size_t>(q) * ROWS];
+    if (y.y != 0.0f) M = fmaxf(M, y.x);
   }
   M = warp_reduce(M, MaxF());
   float acc[PER];
 #pragma unroll
   for (int u = 0; u < PER; ++u) acc[u] = 0.0f;
   float den = 0.0f;
-  for (int q0 = 0; q0 <= np; q0 += 32) {
-    float w = 0.0f;
-    if (q0 + lane <= np) {
-      const float2 ml = ws_ml[base + seg(q0 + lane) * stride];
-      w = ml.y != 0.0f ? ml.y * ex2(ml.x - M) : 0.0f;
-    }
+  for (int q0 = 0; q0 < n; q0 += 32) {
+    if (q0 > 0) ml = q0 + lane < n ? ws_ml[base + static_cast<size_t>(q0 + lane) * ROWS] : make_float2(-INFINITY, 0.0f);
+    const float w = ml.y != 0.0f ? ml.y * ex2(ml.x - M) : 0.0f;
     den += w;
-    const int nq = min(32, np + 1 - q0);
-#pragma unroll 4
-    for (int j = 0; j < nq; ++j) {
-      const float wj = __shfl_sync(0xFFFFFFFFu, w, j);
-      const float* src = ws_o + (base + seg(q0 + j) * stride) * HD + lane * PER;
+    const int nq = min(32, n - q0);
+    for (int j0 = 0; j0 < nq; j0 += AHEAD) {
 #pragma unroll
-      for (int u = 0; u < PER; ++u) acc[u] = fmaf(wj, src[u], acc[u]);
+      for (int j = 0; j < AHEAD; ++j) {
+        const float wj = __shfl_sync(0xFFFFFFFFu, w, (j0 + j) & 31);
+        if (j0 + j < nq) {
+          const float* v = reinterpret_cast<const float*>(&x[j]);
+#pragma unroll
+          for (int u = 0; u < PER; ++u) acc[u] = fmaf(wj, v[u], acc[u]);
+        }
+        if (q0 + j0 + AHEAD + j < n) x[j] = value(q0 + j0 + AHEAD + j);
+      }
     }
   }
-  den = warp_reduce(den, [](float a, float c) { return a + c; });
+  den = warp_reduce(den, [](float p, float q) { return p + q; });
   const float inv = den != 0.0f ? 1.0f / den : 0.0f;
   __nv_bfloat16* out = O + static_cast<size_t>(row) * HD + lane * PER;
 #pragma unroll
@@ -556,6 +703,8 @@ int num_sms() {
   return n_once;
 }
 
+// Shares of the granule kernel: every warp that is resident, none below four granules.
+// Query rows in tiles of eight while they fit one, else of sixteen.
 V4Geom make_geom(int B, int R, int H, int KVH, int max_kv_len) {
   V4Geom g{};
   g.B = B;
@@ -563,24 +712,39 @@ V4Geom make_geom(int B, int R, int H, int KVH, int max_kv_len) {
   g.H = H;
   g.KVH = KVH;
   g.G = H / KVH;
-  g.RG = (g.G * R + 15) / 16;
+  g.rows = g.G * R <= 8 ? 8 : 16;
+  g.RG = (g.G * R + g.rows - 1) / g.rows;
   g.max_kv_len = max_kv_len;
-  const long natural = static_cast<long>(B) * KVH * g.RG;
-  const long splits = std::max(1L, (3L * num_sms() + natural - 1) / natural);
-  const int unit = kWarps * kGran;
-  long chunk = ((static_cast<long>(max_kv_len) + splits - 1) / splits + unit - 1) / unit * unit;
-  chunk = std::max(chunk, 2L * unit);
-  g.chunk = static_cast<int>(chunk);
-  g.S = static_cast<int>(std::max(1L, (max_kv_len + chunk - 1) / chunk));
+  g.workers = (g.rows == 8 ? 4 : 2) * num_sms() * kWarps;
+  g.min_share = 4;
   return g;
+}
+
+size_t pairs(const V4Geom& g) { return static_cast<size_t>(g.B) * g.KVH * g.RG; }
+size_t records(const V4Geom& g) { return pairs(g) + g.workers; }
+
+template <int HD, int NR>
+cudaError_t launch_mma(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
+                       const uint64_t* mask, const V4Geom& g, float sm_scale, float* ws_o, float2* ws_ml, int32_t* ends,
+                       __nv_bfloat16* o, float* lse, int32_t* dev_err, cudaStream_t s) {
+  static std::atomic<bool> attr_done{false};
+  if (!attr_done.load(std::memory_order_acquire)) {  // room for the rings of every resident CTA
+    cudaFuncSetAttribute(verify4_mma_kernel<HD, NR>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    attr_done.store(true, std::memory_order_release);
+  }
+  const cudaError_t e = launch_pdl(verify4_mma_kernel<HD, NR>, dim3(g.workers / kWarps), dim3(kWarps * 32), V4Cfg<HD>::SMEM, s,
+                                   1, q, kv, tail, kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, dev_err);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(verify4_merge_kernel<HD, 8 * NR, kGran>, dim3(static_cast<unsigned>((static_cast<long>(g.B) * g.R * g.H + 3) / 4)),
+                    dim3(128), 0, s, 1, kv, kv_len, g, static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml),
+                    static_cast<const int32_t*>(ends), o, lse);
 }
 
 }  // namespace
 
 size_t verify4_workspace_bytes(int B, int R, int H, int KVH, int hd, int max_kv_len) {
   const V4Geom g = make_geom(B, R, H, KVH, max_kv_len);
-  const size_t recs = static_cast<size_t>(B) * g.S * R * H;
-  return recs * (hd * sizeof(float) + sizeof(float2));
+  return records(g) * g.rows * (hd * sizeof(float) + sizeof(float2)) + pairs(g) * 2 * sizeof(int32_t);
 }
 
 e3_status launch_verify4(const void* Q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
@@ -590,28 +754,19 @@ e3_status launch_verify4(const void* Q, const e3_kv4_layer& kv, const e3_kv_laye
   const size_t need = verify4_workspace_bytes(B, R, H, kv.n_kv_heads, kv.head_dim, max_kv_len);
   E3_REQUIRE(ws_bytes >= need, E3_ERR_CAPACITY, "tree_verify_attn4: workspace of %zu bytes needed, %zu given", need,
              ws_bytes);
-  const size_t recs = static_cast<size_t>(B) * g.S * R * H;
   float* ws_o = static_cast<float*>(ws);
-  float2* ws_ml = reinterpret_cast<float2*>(ws_o + recs * kv.head_dim);
-  const dim3 grid(g.RG * g.S, kv.n_kv_heads, B);
-  const dim3 mgrid(static_cast<unsigned>((static_cast<long>(B) * R * H + 7) / 8));
+  float2* ws_ml = reinterpret_cast<float2*>(ws_o + records(g) * g.rows * kv.head_dim);
+  int32_t* ends = reinterpret_cast<int32_t*>(ws_ml + records(g) * g.rows);
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(Q);
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(O);
   cudaError_t e;
   if (kv.head_dim == 128)
-    e = launch_pdl(verify4_mma_kernel<128>, grid, dim3(kWarps * 32), V4Cfg<128>::SMEM, s, 1, q, kv, tail, kv_len, mask, g,
-                   sm_scale, ws_o, ws_ml, dev_err);
+    e = g.rows == 8 ? launch_mma<128, 1>(q, kv, tail, kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, o, lse, dev_err, s)
+                    : launch_mma<128, 2>(q, kv, tail, kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, o, lse, dev_err, s);
   else
-    e = launch_pdl(verify4_mma_kernel<64>, grid, dim3(kWarps * 32), V4Cfg<64>::SMEM, s, 1, q, kv, tail, kv_len, mask, g,
-                   sm_scale, ws_o, ws_ml, dev_err);
-  if (e != cudaSuccess) return cuda_status(e, "verify4_mma_kernel");
-  if (kv.head_dim == 128)
-    e = launch_pdl(verify4_merge_kernel<128>, mgrid, dim3(256), 0, s, 1, kv, kv_len, g, static_cast<const float*>(ws_o),
-                   static_cast<const float2*>(ws_ml), o, lse);
-  else
-    e = launch_pdl(verify4_merge_kernel<64>, mgrid, dim3(256), 0, s, 1, kv, kv_len, g, static_cast<const float*>(ws_o),
-                   static_cast<const float2*>(ws_ml), o, lse);
-  return e == cudaSuccess ? E3_OK : cuda_status(e, "verify4_merge_kernel");
+    e = g.rows == 8 ? launch_mma<64, 1>(q, kv, tail, kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, o, lse, dev_err, s)
+                    : launch_mma<64, 2>(q, kv, tail, kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, o, lse, dev_err, s);
+  return e == cudaSuccess ? E3_OK : cuda_status(e, "verify4 kernels");
 }
 
 }  // namespace e3
