@@ -99,6 +99,11 @@ size_t verify4_workspace_bytes(int B, int R, int H, int KVH, int hd, int max_kv_
 e3_status launch_verify4(const void* Q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
                          const uint64_t* mask, int B, int R, int H, int max_kv_len, float sm_scale, void* O, float* lse,
                          int32_t* dev_err, void* ws, size_t ws_bytes, cudaStream_t s);
+bool verify4_uses_tc(int R, int H, int KVH, int hd);
+size_t verify4_tc_workspace_bytes(int B, int R, int H, int KVH, int max_kv_len);
+e3_status launch_verify4_tc(const void* Q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
+                            const uint64_t* mask, int B, int R, int H, int max_kv_len, float sm_scale, void* O, float* lse,
+                            int32_t* dev_err, void* ws, cudaStream_t s);
 e3_status launch_logits_process(const float* logits, int B, int R, int V, const float* temp, const uint16_t* counts,
                                 const int32_t* tok, const int32_t* parent, const float* pen, const int32_t* bias_tok,
                                 const float* bias_val, int n_bias, const uint32_t* allow, const int32_t* allow_row,

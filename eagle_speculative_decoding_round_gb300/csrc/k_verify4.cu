@@ -31,93 +31,19 @@
 
 #include "e3_common.cuh"
 #include "e3_kernels.h"
+#include "verify4.cuh"
 
 namespace e3 {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kGran = 16;   // keys of a granule
 constexpr int kWarps = 4;
 constexpr int kStages = 4;  // granules in a warp's ring
-// The softmax base m is kept kHead below the running maximum it was set from and moves
-// when a score passes it by more than kTop (log2): weights stay below 2^15 in fp16, and
-// fp16's subnormal step is 2^-32 of a row's largest weight.
-constexpr float kHead = 7.0f, kTop = 15.0f;
-
-// How the work is shared.  A pair is (request, KV head, tile of `rows` query rows); its
-// units are granules of `keys` prefix keys and then of `keys` tree nodes.  All pairs' units in a
-// row, request by request, are cut into equal shares, one per worker (a warp), whatever
-// the requests' lengths: a worker may end one pair and begin the next.  The part of pair
-// p that worker c computed is record p + c (both only grow along the row, so no two
-// coincide).
-struct V4Geom {
-  int B, R, H, KVH, G;
-  int rows;     // query rows of a tile
-  int RG;       // row tiles of a KV head
-  int workers;  // shares
-  int min_share;
-  int max_kv_len;
-};
-
-// Units of request b's pairs, 0 if its length is out of bounds.
-template <int KEYS>
-__device__ __forceinline__ int pair_units(const V4Geom& g, const e3_kv4_layer& kv, int P) {
-  if (P < 0 || P > g.max_kv_len || P > static_cast<long long>(kv.max_pages) * kv.page_size) return 0;
-  return (P + KEYS - 1) / KEYS + (g.R + KEYS - 1) / KEYS;
-}
-
-// Where a worker begins in the row of units.  Every lane of the warp calls it and gets the
-// same answer.
-struct V4Place {
-  long long share, before;  // units of a share; units before request b
-  int b;                    // the request that holds the share's first unit (B: none)
-};
-template <int KEYS>
-__device__ __forceinline__ V4Place find_place(const V4Geom& g, const e3_kv4_layer& kv, const int32_t* kv_len, int worker) {
-  const int lane = threadIdx.x & 31;
-  const long long Q = static_cast<long long>(g.KVH) * g.RG;
-  long long total = 0;
-  for (int b0 = 0; b0 < g.B; b0 += 32) {
-    const int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv, kv_len[b0 + lane]) : 0;
-    total += __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(u));
-  }
-  V4Place f;
-  f.share = max((total * Q + g.workers - 1) / g.workers, static_cast<long long>(g.min_share));
-  const long long at = f.share * worker;
-  long long base = 0;
-  f.b = g.B;
-  f.before = total * Q;
-  for (int b0 = 0; b0 < g.B; b0 += 32) {
-    const int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv, kv_len[b0 + lane]) : 0;
-    unsigned incl = static_cast<unsigned>(u);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    const long long end = (base + incl) * Q;
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, end > at);
-    if (hit) {
-      const int k = __ffs(hit) - 1;
-      f.b = b0 + k;
-      f.before = (base + __shfl_sync(0xFFFFFFFFu, incl, k) - __shfl_sync(0xFFFFFFFFu, static_cast<unsigned>(u), k)) * Q;
-      break;
-    }
-    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
-  }
-  return f;
-}
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 // D += A B, m16n8k16, fp32 accumulators
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -451,8 +377,9 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
       am = max(am & 0xFFFFu, am >> 16);
       am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
       am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-      const int ex = max(static_cast<int>(am >> 7), 1) - 127;  // exponent of the largest magnitude
-      // 2^-ex in two factors (ex reaches 128 for Inf and NaN, -126 for subnormals)
+      // exponent of the largest magnitude (below 2^-64 a row's scores are as good as zero)
+      const int ex = max(static_cast<int>(am >> 7) - 127, -64);
+      // 2^-ex in two factors (ex reaches 128 for Inf and NaN)
       const float f0 = __uint_as_float(static_cast<uint32_t>(127 - ex / 2) << 23);
       const float f1 = __uint_as_float(static_cast<uint32_t>(127 - (ex - ex / 2)) << 23);
 #pragma unroll
@@ -621,88 +548,6 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
   }
 }
 
-// Merge of a pair's records: one warp per (b, i, h) row, hd/32 dims a lane.  ROWS: the
-// row tile of the kernel that wrote them.  The workers that began and ended the pair left
-// their numbers in `ends`, so the records are found without the search; the first
-// records' values are requested together with their weights.
-template <int HD, int ROWS, int KEYS>
-__global__ void __launch_bounds__(128)
-verify4_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __restrict__ kv_len,
-                     const __grid_constant__ V4Geom g, const float* __restrict__ ws_o, const float2* __restrict__ ws_ml,
-                     const int32_t* __restrict__ ends, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
-  constexpr int PER = HD / 32;
-  constexpr int AHEAD = 8;
-  const int lane = threadIdx.x & 31;
-  const unsigned row = blockIdx.x * 4u + (threadIdx.x >> 5);
-  const unsigned stride = static_cast<unsigned>(g.R) * g.H;
-  const int b = static_cast<int>(row / stride);
-  if (b >= g.B) {
-    pdl_wait();
-    return;
-  }
-  const int ih = static_cast<int>(row - b * stride), i = ih / g.H, h = ih - i * g.H;
-  const int kvh = h / g.G, r = i * g.G + h - kvh * g.G, rt = r / ROWS;
-  const size_t pair = static_cast<size_t>(b) * g.KVH * g.RG + kvh * g.RG + rt;
-  pdl_wait();
-  pdl_trigger();
-  const int P = kv_len[b], c0 = ends[2 * pair], c1 = ends[2 * pair + 1];
-  if (pair_units<KEYS>(g, kv, P) == 0) return;
-  const int n = c1 - c0 + 1;
-  const size_t base = (pair + c0) * ROWS + (r - rt * ROWS);  // then ROWS apart
-  using Vec = typename std::conditional<PER == 4, float4, float2>::type;
-  auto value = [&](int q) { return reinterpret_cast<const Vec*>(ws_o + (base + static_cast<size_t>(q) * ROWS) * HD)[lane]; };
-  Vec x[AHEAD];
-#pragma unroll
-  for (int q = 0; q < AHEAD; ++q)
-    if (q < n) x[q] = value(q);
-  float2 ml = lane < n ? ws_ml[base + static_cast<size_t>(lane) * ROWS] : make_float2(-INFINITY, 0.0f);
-  float M = ml.y != 0.0f ? ml.x : -INFINITY;
-  for (int q = lane + 32; q < n; q += 32) {
-    const float2 y = ws_ml[base + static_cast<size_t>(q) * ROWS];
-    if (y.y != 0.0f) M = fmaxf(M, y.x);
-  }
-  M = warp_reduce(M, MaxF());
-  float acc[PER];
-#pragma unroll
-  for (int u = 0; u < PER; ++u) acc[u] = 0.0f;
-  float den = 0.0f;
-  for (int q0 = 0; q0 < n; q0 += 32) {
-    if (q0 > 0) ml = q0 + lane < n ? ws_ml[base + static_cast<size_t>(q0 + lane) * ROWS] : make_float2(-INFINITY, 0.0f);
-    const float w = ml.y != 0.0f ? ml.y * ex2(ml.x - M) : 0.0f;
-    den += w;
-    const int nq = min(32, n - q0);
-    for (int j0 = 0; j0 < nq; j0 += AHEAD) {
-#pragma unroll
-      for (int j = 0; j < AHEAD; ++j) {
-        const float wj = __shfl_sync(0xFFFFFFFFu, w, (j0 + j) & 31);
-        if (j0 + j < nq) {
-          const float* v = reinterpret_cast<const float*>(&x[j]);
-#pragma unroll
-          for (int u = 0; u < PER; ++u) acc[u] = fmaf(wj, v[u], acc[u]);
-        }
-        if (q0 + j0 + AHEAD + j < n) x[j] = value(q0 + j0 + AHEAD + j);
-      }
-    }
-  }
-  den = warp_reduce(den, [](float p, float q) { return p + q; });
-  const float inv = den != 0.0f ? 1.0f / den : 0.0f;
-  __nv_bfloat16* out = O + static_cast<size_t>(row) * HD + lane * PER;
-#pragma unroll
-  for (int u = 0; u < PER; u += 2)
-    *reinterpret_cast<uint32_t*>(out + u) = pack2_bf16(acc[u] * inv, acc[u + 1] * inv);
-  if (lane == 0) lse[row] = den != 0.0f ? (M + log2f(den)) * kLn2 : -INFINITY;
-}
-
-int num_sms() {
-  static const int n_once = [] {  // queried once, thread-safely (152 on GB300 if the query fails)
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-    return n;
-  }();
-  return n_once;
-}
-
 // Shares of the granule kernel: every warp that is resident, none below four granules.
 // Query rows in tiles of eight while they fit one, else of sixteen.
 V4Geom make_geom(int B, int R, int H, int KVH, int max_kv_len) {
@@ -735,7 +580,7 @@ cudaError_t launch_mma(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_
   const cudaError_t e = launch_pdl(verify4_mma_kernel<HD, NR>, dim3(g.workers / kWarps), dim3(kWarps * 32), V4Cfg<HD>::SMEM, s,
                                    1, q, kv, tail, kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, dev_err);
   if (e != cudaSuccess) return e;
-  return launch_pdl(verify4_merge_kernel<HD, 8 * NR, kGran>, dim3(static_cast<unsigned>((static_cast<long>(g.B) * g.R * g.H + 3) / 4)),
+  return launch_pdl(verify4_merge_kernel<HD, 8 * NR, kGran, 1>, dim3(static_cast<unsigned>((static_cast<long>(g.B) * g.R * g.H + 3) / 4)),
                     dim3(128), 0, s, 1, kv, kv_len, g, static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml),
                     static_cast<const int32_t*>(ends), o, lse);
 }
@@ -743,6 +588,7 @@ cudaError_t launch_mma(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_
 }  // namespace
 
 size_t verify4_workspace_bytes(int B, int R, int H, int KVH, int hd, int max_kv_len) {
+  if (verify4_uses_tc(R, H, KVH, hd)) return verify4_tc_workspace_bytes(B, R, H, KVH, max_kv_len);
   const V4Geom g = make_geom(B, R, H, KVH, max_kv_len);
   return records(g) * g.rows * (hd * sizeof(float) + sizeof(float2)) + pairs(g) * 2 * sizeof(int32_t);
 }
@@ -750,10 +596,12 @@ size_t verify4_workspace_bytes(int B, int R, int H, int KVH, int hd, int max_kv_
 e3_status launch_verify4(const void* Q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
                          const uint64_t* mask, int B, int R, int H, int max_kv_len, float sm_scale, void* O, float* lse,
                          int32_t* dev_err, void* ws, size_t ws_bytes, cudaStream_t s) {
-  const V4Geom g = make_geom(B, R, H, kv.n_kv_heads, max_kv_len);
   const size_t need = verify4_workspace_bytes(B, R, H, kv.n_kv_heads, kv.head_dim, max_kv_len);
   E3_REQUIRE(ws_bytes >= need, E3_ERR_CAPACITY, "tree_verify_attn4: workspace of %zu bytes needed, %zu given", need,
              ws_bytes);
+  if (verify4_uses_tc(R, H, kv.n_kv_heads, kv.head_dim))
+    return launch_verify4_tc(Q, kv, tail, kv_len, mask, B, R, H, max_kv_len, sm_scale, O, lse, dev_err, ws, s);
+  const V4Geom g = make_geom(B, R, H, kv.n_kv_heads, max_kv_len);
   float* ws_o = static_cast<float*>(ws);
   float2* ws_ml = reinterpret_cast<float2*>(ws_o + records(g) * g.rows * kv.head_dim);
   int32_t* ends = reinterpret_cast<int32_t*>(ws_ml + records(g) * g.rows);

@@ -1,0 +1,898 @@
+// k_verify4_tc.cu -- tree_verify_attn4 on the 5th-generation tensor cores (head_dim 128,
+// more than 16 query rows per KV head).
+//
+// Work is cut as in verify4.cuh: a pair is (request, KV head, tile of RT * 128 query rows),
+// its units are tiles of 128 prefix keys and then of 128 tree nodes; one CTA per SM takes
+// an equal share of all units.  A tile goes through the CTA like this:
+//   producer (warp 0)      the tile's codes and scales by bulk copies into a ring
+//   dequantizers (4 warps) codes -> fp16 operands in 128-byte-swizzled shared memory: a
+//                          value c * e is exact in fp16 (see k_verify4.cu).  Tree nodes are
+//                          read from the bf16 tail and scaled by powers of two instead
+//                          (per key for K, per tile for V), which keeps their bits
+//   S = Q K^T              tcgen05.mma kind::f16, M = 128 rows, N = 128 keys, into the S
+//                          buffer of the row's softmax group
+//   softmax (2 x 4 warps)  one thread per row: maximum, exponentials, P (fp16) over S
+//   O += P V               A = P from TMEM, V in place as an MN-major operand; O stays in
+//                          TMEM, rescaled only when a base moves by more than 2^15
+// The two softmax groups alternate, so that one's exponentials run while the tensor core
+// works for the other.  RT = 2: a group per 128 rows, both use every tile, which is
+// dequantized once for 256 rows.  RT = 1 (at most 128 rows): the groups take the tiles in
+// turn, each with an O of its own, and leave two records per part.
+// Bound: shared-memory bandwidth.  Per 128 keys and SM in 128-byte cycles (RT = 2): raw
+// tile in and out 288, operands written 512, Q and K read by S 2 x 512, V by O 2 x 256.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "e3_common.cuh"
+#include "e3_kernels.h"
+#include "verify4.cuh"
+
+namespace e3 {
+
+namespace {
+
+constexpr int kRows = 128;   // query rows of a softmax group
+constexpr int kKeys = 128;   // keys of a tile
+constexpr int kHD = 128;
+constexpr int kHalfB = 16384;            // bytes of a 64-dim half of an operand: [128 rows][128 B]
+constexpr int kOpB = 2 * kHalfB;         // bytes of an operand
+constexpr int kCodeB = kKeys * kHD / 2;  // bytes of a tile's codes, per operand
+constexpr int kScaleB = kKeys * kHD / 16;
+constexpr int kRawB = 2 * (kCodeB + kScaleB);
+constexpr int kRaw = 3;                  // raw stages
+constexpr int kTailRing = 8;             // tiles of tree nodes whose factors are kept (at most five are in flight)
+// Warpgroups: 0 = producer and MMA issuer (and two idle warps), 1 and 2 = softmax, 3 =
+// dequantizers.  Registers move from the first and the last to the softmax groups, which
+// hold half a row of scores: 56 + 2 x 168 + 80 = 472 of the 4 x 128 that the launch gives
+// each quarter of a warpgroup set.
+constexpr int kThreads = 512;
+constexpr int kSoftmax0 = 4, kDeq0 = 12;
+constexpr int kRegsIssue = 56, kRegsSoftmax = 168, kRegsDeq = 80;
+static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsDeq <= 4 * 120, "the split stays below the launch's registers");
+constexpr unsigned long long kWaitNs = 1000000000ull;
+
+template <int RT>
+struct Cfg {
+  static constexpr int NV = RT == 2 ? 1 : 2;  // V stages
+  static constexpr int Q = 0, K = RT * kOpB, V = K + 2 * kOpB, RAW = V + NV * kOpB, FAC = RAW + kRaw * kRawB;
+  static constexpr int BARS = FAC + kTailRing * kKeys * 4, END = BARS + 512;
+  static constexpr int SMEM = END + 1024;  // (base rounded up to 1024)
+};
+static_assert(Cfg<1>::SMEM <= 232448 && Cfg<2>::SMEM <= 232448, "shared memory of a CTA");
+
+__device__ __forceinline__ uint32_t su32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ uint64_t gtimer() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ void bar_init(uint64_t* b, uint32_t n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(su32(b)), "r"(n));
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(su32(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(su32(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t par) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(su32(b)), "r"(par)
+               : "memory");
+  return ok != 0;
+}
+// Bounded wait: about a second, or until another role has given up.
+__device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t par, volatile int* abort) {
+  if (bar_try(b, par)) return true;
+  const uint64_t t0 = gtimer();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (bar_try(b, par)) return true;
+    if (*abort) return false;
+    if (gtimer() - t0 > kWaitNs) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(su32(bar))
+               : "memory");
+}
+// 128-byte-swizzled smem descriptor; lbo/sbo in bytes.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+// kind::f16 instruction descriptor: f16 x f16 -> f32, M = N = 128, the second operand's major.
+__host__ __device__ constexpr uint32_t idesc_f16(int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(128 >> 3) << 17) |
+         (static_cast<uint32_t>(128 >> 4) << 24);
+}
+__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::
+                   "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc));
+}
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::
+                   "r"(d), "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
+}
+__device__ __forceinline__ void umma_commit(uint64_t* b) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(b)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+#define E3_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), "=r"(r[o + 6]), "=r"(r[o + 7])
+// 32 consecutive 32-bit TMEM columns of this thread's lane; tmem_wait() before their use
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : E3_R8(r, 0), E3_R8(r, 8), E3_R8(r, 16), E3_R8(r, 24)
+      : "r"(taddr));
+}
+#undef E3_R8
+__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  tmem_ld32(taddr, r);
+  tmem_ld32(taddr + 32, r + 32);
+  tmem_wait();
+}
+#define E3_V8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      E3_V8(v, 0), E3_V8(v, 8), E3_V8(v, 16), E3_V8(v, 24)
+      : "memory");
+}
+#undef E3_V8
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ float fmax3f(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+// 2^e for any int e a float's exponent can meet here (|e| <= 252), as a product of two normals
+__device__ __forceinline__ float pow2f(int e) {
+  const int a = e / 2;
+  return __uint_as_float(static_cast<uint32_t>(127 + a) << 23) * __uint_as_float(static_cast<uint32_t>(127 + e - a) << 23);
+}
+
+// The parts of one CTA's share, one after another; every role walks the same list.
+struct Parts {
+  long long todo;
+  int b, pq, x0, x1, units;
+  int P, NT;  // the request's length, its prefix tiles
+  __device__ __forceinline__ void take() {
+    x1 = static_cast<int>(min(static_cast<long long>(units), x0 + todo));
+    NT = (P + kKeys - 1) / kKeys;
+  }
+  __device__ __forceinline__ int tiles() const { return x1 - x0; }
+  // the next part; false at the end of the share
+  __device__ __forceinline__ bool next(const V4Geom& g, const e3_kv4_layer& kv, const int32_t* kv_len) {
+    todo -= x1 - x0;
+    if (todo <= 0) return false;
+    x0 = 0;
+    if (++pq == g.KVH * g.RG) {
+      pq = 0;
+      for (++b; b < g.B; ++b) {
+        P = kv_len[b];
+        units = pair_units<kKeys>(g, kv, P);
+        if (units > 0) break;
+      }
+      if (b >= g.B) return false;
+    }
+    take();
+    return true;
+  }
+};
+
+// 4-bit values of four words (32 dims of a key) -> fp16 pairs, eight per call: word w, scale e
+__device__ __forceinline__ uint4 decode8(uint32_t w, __half2 e) {
+  uint32_t r[4];
+  asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+  return make_uint4(h2u(__hmul2(u2h(r[0]), e)), h2u(__hmul2(u2h(r[1]), e)), h2u(__hmul2(u2h(r[2]), e)),
+                    h2u(__hmul2(u2h(r[3]), e)));
+}
+
+template <int RT>
+__global__ void __launch_bounds__(kThreads, 1)
+verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e3_kv4_layer kv,
+                  const __grid_constant__ e3_kv_layer tail, const int32_t* __restrict__ kv_len,
+                  const uint64_t* __restrict__ mask, const __grid_constant__ V4Geom g, float sm_scale,
+                  float* __restrict__ ws_o, float2* __restrict__ ws_ml, int32_t* __restrict__ ends, int32_t* dev_err) {
+  using C = Cfg<RT>;
+  constexpr int NV = C::NV;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V, *sRaw = sm + C::RAW;
+  float* s_fac = reinterpret_cast<float*>(sm + C::FAC);  // [kTailRing][128] factor of each tree node's scores
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BARS);
+  uint64_t* raw_full = bars;        // [kRaw]
+  uint64_t* raw_empty = bars + 3;   // [kRaw]
+  uint64_t* k_full = bars + 6;      // [2]
+  uint64_t* k_empty = bars + 8;     // [2]
+  uint64_t* v_full = bars + 10;     // [NV]
+  uint64_t* v_empty = bars + 12;    // [NV]
+  uint64_t* s_full = bars + 14;     // [2] by softmax group, as the following
+  uint64_t* p_full = bars + 16;
+  uint64_t* o_done = bars + 18;
+  uint64_t* q_full = bars + 20;
+  uint64_t* q_free = bars + 22;     // (RT = 1) both groups are done with the shared Q
+  int* s_ue = reinterpret_cast<int*>(bars + 24);                    // [kTailRing] exponent of V's unit in a tile of nodes
+  uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_ue + kTailRing);  // [kTailRing][4] nodes with a non-finite V
+  uint32_t* tmem_slot = s_bad + 4 * kTailRing;
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kRaw; ++i) {
+      bar_init(&raw_full[i], 1);
+      bar_init(&raw_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&k_full[i], 4);
+      bar_init(&k_empty[i], 1);
+      bar_init(&v_full[i], 4);
+      bar_init(&v_empty[i], 1);
+      bar_init(&s_full[i], 1);
+      bar_init(&p_full[i], 4);
+      bar_init(&o_done[i], 1);
+      bar_init(&q_full[i], 4);
+    }
+    bar_init(q_free, 8);
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  if (cta == 0)  // requests whose length is out of bounds
+    for (int b = threadIdx.x; b < g.B; b += kThreads)
+      if (pair_units<kKeys>(g, kv, kv_len[b]) == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+  const V4Place at = find_place<kKeys>(g, kv, kv_len, cta);
+  const bool work = at.b < g.B;
+  Parts first{};
+  if (work) {
+    first.b = at.b;
+    first.P = kv_len[at.b];
+    first.todo = at.share;
+    first.units = pair_units<kKeys>(g, kv, first.P);
+    const long long off = at.share * cta - at.before;
+    first.pq = static_cast<int>(off / first.units);
+    first.x0 = static_cast<int>(off - static_cast<long long>(first.pq) * first.units);
+    first.take();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  pdl_trigger();
+  const uint32_t tmem = *tmem_slot;
+  // TMEM columns: S (and P) of group w at 128 w, O of group w at 256 + 128 w
+  const int Qn = g.KVH * g.RG;
+  const int vu_exp = static_cast<int>(__float_as_uint(kv.v_unit) >> 23) - 127;
+  int T_raw = 0;  // (producer) tiles issued
+
+  if (warp < kSoftmax0) {
+    regs_dec<kRegsIssue>();
+    if (warp == 0 && work) {
+      Parts p = first;
+      int ntail = 0;
+      bool live = true;
+      do {
+        const int kvh = p.pq / g.RG;
+        for (int x = p.x0; live && x < p.x1; ++x) {
+          const int st = T_raw % kRaw;
+          if (!bar_wait(&raw_empty[st], ((T_raw / kRaw) & 1) ^ 1, abort)) {
+            live = false;
+            break;
+          }
+          __syncwarp();
+          ++T_raw;
+          if (x < p.NT) {
+            // runs of keys within a page, lane / 4 = run, lane % 4 = what (K, V, their scales)
+            const int t0 = x * kKeys, keys = min(kKeys, (p.P - t0 + 15) & ~15);
+            uint32_t bytes = 0;
+            unsigned char* base = sRaw + st * kRawB;
+            // up to eight 16-key granules form runs: each lane finds the run that starts at its granule
+            const int gr = lane >> 2, what = lane & 3;
+            const int t = t0 + 16 * gr;
+            int run = 0;
+            const unsigned char* src = nullptr;
+            if (16 * gr < keys) {
+              const int pi = t / kv.page_size, slot = t - pi * kv.page_size;
+              if (gr == 0 || slot == 0) {
+                run = min(keys - 16 * gr, kv.page_size - slot);
+                const int page = kv.page_table[static_cast<size_t>(p.b) * kv.max_pages + pi];
+                if (page < 0 || page >= kv.n_pages) {
+                  dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+                  run = 0;
+                } else {
+                  const size_t row = (static_cast<size_t>(page) * g.KVH + kvh) * kv.page_size + slot;
+                  const void* from = what == 0 ? kv.k : what == 1 ? kv.v : what == 2 ? kv.k_scale : kv.v_scale;
+                  src = static_cast<const unsigned char*>(from) + row * (what < 2 ? kHD / 2 : kHD / 16);
+                }
+              }
+            }
+            bytes = static_cast<uint32_t>(run) * (what < 2 ? kHD / 2 : kHD / 16);
+            const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes);
+            if (lane == 0) bar_expect(&raw_full[st], total);
+            __syncwarp();
+            if (bytes) {
+              const int at_b = what == 0 ? 16 * gr * (kHD / 2) : what == 1 ? kCodeB + 16 * gr * (kHD / 2)
+                               : 2 * kCodeB + (what == 3 ? kScaleB : 0) + 16 * gr * (kHD / 16);
+              bulk_copy(su32(base + at_b), src, bytes, &raw_full[st]);
+            }
+          } else {
+            // a tile of tree nodes: the exponent of its largest finite V
+            const int j0 = (x - p.NT) * kKeys, nj = min(kKeys, g.R - j0);
+            uint32_t am = 0u;
+            for (int i = lane; i < nj * 16; i += 32) {
+              const int j = j0 + (i >> 4), pi = j / tail.page_size;
+              const int page = tail.page_table[static_cast<size_t>(p.b) * tail.max_pages + pi];
+              if (page < 0 || page >= tail.n_pages) continue;
+              const size_t row = (static_cast<size_t>(page) * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size);
+              const uint4 y = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(tail.v) + row * kHD)[i & 15];
+              const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t lo = w[c] & 0x7FFFu, hi = (w[c] >> 16) & 0x7FFFu;
+                if (lo < 0x7F80u) am = max(am, lo);
+                if (hi < 0x7F80u) am = max(am, hi);
+              }
+            }
+            am = __reduce_max_sync(0xFFFFFFFFu, am);
+            if (lane == 0) {
+              // (not so far below v_unit that O would overflow in it)
+              s_ue[ntail % kTailRing] = max(static_cast<int>(am >> 7) - 127, vu_exp - 40);
+              bar_arrive(&raw_full[st]);
+            }
+            ++ntail;
+          }
+        }
+      } while (live && p.next(g, kv, kv_len));
+    }
+    if (warp == 1 && lane == 0 && work) {
+      constexpr uint32_t idS = idesc_f16(0), idO = idesc_f16(1);
+      const uint64_t q_desc = desc_sw128(su32(sQ), 16, 1024);
+      const uint64_t k_desc = desc_sw128(su32(sK), 16, 1024);
+      const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
+      // jobs in order: RT = 2: (tile, group 0), (tile, group 1), ...; RT = 1: the tiles of a
+      // part, groups in turn.  Two cursors: S runs one job ahead of O
+      struct Cursor {
+        Parts p;
+        int i, n, T, part;  // job of the part, jobs of the part, tile number, part number
+        bool on;
+      };
+      auto start = [&](Cursor& c) { c.n = c.p.tiles() * RT, c.i = 0; };
+      auto advance = [&](Cursor& c) {
+        if (RT == 1 || (c.i & 1)) ++c.T;
+        if (++c.i == c.n) {
+          c.on = c.p.next(g, kv, kv_len);
+          ++c.part;
+          if (c.on) start(c);
+        }
+      };
+      Cursor s{first, 0, 0, 0, 0, true}, o{first, 0, 0, 0, 0, true};
+      start(s);
+      start(o);
+      int ns[2] = {0, 0}, no[2] = {0, 0};  // S and O products issued per group
+      bool ok = true;
+      auto issue_S = [&]() {
+        const int w = s.i & 1, st = s.T & 1;
+        ok = ok && bar_wait(&k_full[st], (s.T >> 1) & 1, abort);
+        if (s.i < 2) ok = ok && bar_wait(&q_full[RT == 1 ? 0 : w], s.part & 1, abort);
+        if (ns[w] > 0) ok = ok && bar_wait(&o_done[w], (ns[w] - 1) & 1, abort);  // P of the group's last job has been read
+        if (!ok) return;
+        fence_after();
+        const uint64_t qd = q_desc + static_cast<uint64_t>(((RT == 1 ? 0 : w) * kOpB) >> 4);
+        const uint64_t kd = k_desc + static_cast<uint64_t>((st * kOpB) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < kHD / 16; ++kk) {
+          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kHalfB + (kk & 3) * 32) >> 4);
+          umma(tmem + w * 128, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[w]);
+        if (RT == 1 || w == 1) umma_commit(&k_empty[st]);
+        ++ns[w];
+        advance(s);
+      };
+      auto issue_O = [&]() {
+        const int w = o.i & 1, st = o.T % NV;
+        ok = ok && bar_wait(&p_full[w], no[w] & 1, abort);
+        ok = ok && bar_wait(&v_full[st], (o.T / NV) & 1, abort);
+        if (!ok) return;
+        fence_after();
+        const uint64_t vd = v_desc + static_cast<uint64_t>((st * kOpB) >> 4);
+        const uint32_t acc0 = o.i >= 2 ? 1u : 0u;  // the group's first job of a part starts its O
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          umma_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), idO,
+                  kk > 0 ? 1u : acc0);
+        umma_commit(&o_done[w]);
+        if (RT == 1 || w == 1) umma_commit(&v_empty[st]);
+        ++no[w];
+        advance(o);
+      };
+      issue_S();
+      while (ok && o.on) {
+        // the next S goes first where it waits for nothing that this O product leads to:
+        // the other group's, in the same part
+        const bool ahead = s.on && s.part == o.part && (s.i & 1) != (o.i & 1);
+        if (ahead) issue_S();
+        if (ok) issue_O();
+        if (!ahead && ok && s.on) issue_S();
+      }
+    }
+  } else if (warp >= kDeq0) {
+    regs_dec<kRegsDeq>();
+    if (work) {
+      const int dw = warp - kDeq0, q = lane & 3;
+      Parts p = first;
+      int T = 0, ntail = 0;
+      bool live = true;
+      do {
+        const int kvh = p.pq / g.RG;
+        for (int x = p.x0; live && x < p.x1; ++x, ++T) {
+          const int st = T % kRaw;
+          if (!bar_wait(&raw_full[st], (T / kRaw) & 1, abort)) {
+            live = false;
+            break;
+          }
+          const unsigned char* raw = sRaw + st * kRawB;
+          const bool nodes = x >= p.NT;
+          const int left = nodes ? g.R - (x - p.NT) * kKeys : p.P - x * kKeys;  // keys that exist
+          const int slot = ntail % kTailRing;
+#pragma unroll 1
+          for (int op = 0; op < 2; ++op) {  // K, then V
+            const int dst_st = op ? T % NV : T & 1;
+            uint64_t* empty = op ? &v_empty[dst_st] : &k_empty[dst_st];
+            uint64_t* full = op ? &v_full[dst_st] : &k_full[dst_st];
+            if (!bar_wait(empty, (op ? ((T / NV) & 1) : ((T >> 1) & 1)) ^ 1, abort)) {
+              live = false;
+              break;
+            }
+            unsigned char* dst = (op ? sV : sK) + dst_st * kOpB;
+            if (!nodes) {
+              const unsigned char* codes = raw + op * kCodeB;
+              const unsigned char* scales = raw + 2 * kCodeB + op * kScaleB;
+              uint4 w4[4];
+              uint32_t e4[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = dw * 32 + i * 8 + (lane >> 2);
+                w4[i] = *reinterpret_cast<const uint4*>(codes + key * (kHD / 2) + q * 16);
+                e4[i] = *reinterpret_cast<const uint16_t*>(scales + key * (kHD / 16) + 2 * q);
+                if (key >= left) e4[i] = 0u;  // beyond the prefix: adds 0 whatever the slot holds
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = dw * 32 + i * 8 + (lane >> 2);
+                const uint32_t e = h2u(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(e4[i]), __NV_E4M3))));
+                uint32_t ea = __byte_perm(e, e, 0x1010), eb = __byte_perm(e, e, 0x3232);
+                uint32_t w[4] = {w4[i].x, w4[i].y, w4[i].z, w4[i].w};
+                // the four 16-byte pieces in an order that differs between the lanes which
+                // store together, so that their banks do
+                const int flip = ((q >> 1) & 1) | ((key & 1) << 1);
+                if (flip & 1) {
+                  const uint32_t a = w[0], b = w[2];
+                  w[0] = w[1], w[1] = a, w[2] = w[3], w[3] = b;
+                }
+                if (flip & 2) {
+                  uint32_t a = w[0], b = w[1];
+                  w[0] = w[2], w[1] = w[3], w[2] = a, w[3] = b;
+                  a = ea, ea = eb, eb = a;
+                }
+                unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int chunk = 4 * (q & 1) + (k ^ flip);
+                  *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = decode8(w[k], u2h(k < 2 ? ea : eb));
+                }
+              }
+            } else {
+              const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(op ? tail.v : tail.k);
+              uint32_t bad_v = 0u;  // this warp's keys with a non-finite V
+#pragma unroll 1
+              for (int i = 0; i < 4; ++i) {
+                const int key = dw * 32 + i * 8 + (lane >> 2), j = (x - p.NT) * kKeys + key;
+                uint4 y[4] = {};
+                if (key < left) {
+                  const int pi = j / tail.page_size;
+                  const int page = tail.page_table[static_cast<size_t>(p.b) * tail.max_pages + pi];
+                  if (page >= 0 && page < tail.n_pages) {
+                    const size_t row = (static_cast<size_t>(page) * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) y[c] = reinterpret_cast<const uint4*>(from + row * kHD + 32 * q)[c];
+                  } else {
+                    dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+                  }
+                }
+                uint32_t w[16];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) w[4 * c] = y[c].x, w[4 * c + 1] = y[c].y, w[4 * c + 2] = y[c].z, w[4 * c + 3] = y[c].w;
+                uint32_t am = 0u;
+#pragma unroll
+                for (int c = 0; c < 16; ++c) am = __vmaxu2(am, w[c] & 0x7FFF7FFFu);
+                am = max(am & 0xFFFFu, am >> 16);
+                am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+                am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));  // the key's four lanes
+                const bool bad = am >= 0x7F80u;
+                // a node with a NaN or an Inf leaves the product: its scores get a NaN factor,
+                // rows that see its V are marked
+                const int ex = op ? s_ue[slot] : max(static_cast<int>(am >> 7), 1) - 127;
+                if (op == 0 && q == 0) s_fac[slot * kKeys + key] = bad ? __int_as_float(0x7FC00000) : pow2f(ex);
+                if (bad) bad_v |= 1u << (key & 31);
+                const int na = -ex / 2;
+                const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
+                const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
+                unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  uint32_t h[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const uint32_t z = bad ? 0u : w[4 * c + k];
+                    h[k] = h2u(__floats2half2_rn(__uint_as_float(z << 16) * f0 * f1, __uint_as_float(z & 0xFFFF0000u) * f0 * f1));
+                  }
+                  const int chunk = 4 * (q & 1) + c;
+                  *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+              }
+              bad_v = __reduce_or_sync(0xFFFFFFFFu, bad_v);
+              if (op == 1 && lane == 0) s_bad[slot * 4 + dw] = bad_v;
+            }
+            fence_async_smem();  // generic-proxy writes -> tensor core
+            __syncwarp();
+            if (lane == 0) bar_arrive(full);
+          }
+          if (!live) break;
+          if (nodes) ++ntail;
+          __syncwarp();
+          if (lane == 0) bar_arrive(&raw_empty[st]);
+        }
+      } while (live && p.next(g, kv, kv_len));
+    }
+  } else {
+    regs_inc<kRegsSoftmax>();
+    // softmax: warp w of group grp reads TMEM lane quarter warp % 4 (rows 32 quarter ..)
+    const int grp = (warp - kSoftmax0) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + grp * 128 + lane_base, tO = tmem + 256 + grp * 128 + lane_base;
+    if (work) {
+      Parts p = first;
+      int n_job = 0, ntail = 0, n_part = 0;
+      bool live = true;
+      do {
+        const int kvh = p.pq / g.RG, rg = p.pq - kvh * g.RG;
+        const int gr = (rg * RT + (RT == 2 ? grp : 0)) * kRows + r;  // row of the KV head
+        const bool row_ok = gr < g.G * g.R;
+        const int node = row_ok ? gr / g.G : 0, head = kvh * g.G + (row_ok ? gr - node * g.G : 0);
+        // Q of the row to fp16, its largest magnitude scaled to [1, 2)
+        float c2;
+        {
+          const uint4* qp = reinterpret_cast<const uint4*>(Q + ((static_cast<size_t>(p.b) * g.R + node) * g.H + head) * kHD);
+          uint4 y[16];
+          uint32_t am = 0u;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            y[c] = row_ok ? qp[c] : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int c = 0; c < 16; ++c)
+            am = __vmaxu2(am, __vmaxu2(__vmaxu2(y[c].x & 0x7FFF7FFFu, y[c].y & 0x7FFF7FFFu),
+                                       __vmaxu2(y[c].z & 0x7FFF7FFFu, y[c].w & 0x7FFF7FFFu)));
+          am = max(am & 0xFFFFu, am >> 16);
+          // (below 2^-64 a row's scores are as good as zero, and its factor would underflow)
+          const int ex = max(static_cast<int>(am >> 7) - 127, -64);
+          c2 = fmaxf(sm_scale * kLog2e * pow2f(ex), 1e-37f);
+          if (RT == 2 || grp == 0) {
+            // (RT = 1: the other group's products of the last part have read the shared Q)
+            if (RT == 1 && n_part > 0 && !bar_wait(q_free, (n_part - 1) & 1, abort)) live = false;
+            const int na = -ex / 2;
+            const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
+            const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
+            unsigned char* row = sQ + (RT == 2 ? grp : 0) * kOpB + r * 128;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const uint32_t w[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                h[k] = h2u(__floats2half2_rn(__uint_as_float(w[k] << 16) * f0 * f1, __uint_as_float(w[k] & 0xFFFF0000u) * f0 * f1));
+              *reinterpret_cast<uint4*>(row + (c >> 3) * kHalfB + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&q_full[grp]);
+          }
+        }
+        const float c2p = c2 * kv.k_unit;
+        float m = -INFINITY, l = 0.0f;
+        int ue = vu_exp, mine = 0;  // exponent of O's unit; this group's jobs of the part
+        const int tail0 = ntail;
+        const int words = (g.R + 63) >> 6;
+        const uint64_t* mrow = mask + (static_cast<size_t>(p.b) * g.R + node) * words;
+        for (int x = p.x0; x < p.x1; ++x) {
+          const bool nodes = x >= p.NT;
+          const int slot = ntail % kTailRing;
+          if (nodes) ++ntail;
+          if (RT == 1 && ((x - p.x0) & 1) != grp) continue;
+          if (!live) break;
+          const int left = nodes ? g.R - (x - p.NT) * kKeys : p.P - x * kKeys;
+          // keys the row sees: all, those that exist, or the ancestors among the nodes
+          uint64_t see[2] = {~0ull, ~0ull};
+          const bool full = !nodes && left >= kKeys;
+          if (!full) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int n = left - 64 * h;
+              see[h] = n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+              if (nodes) {
+                const int wd = 2 * (x - p.NT) + h;
+                see[h] &= wd < words && row_ok ? mrow[wd] : 0ull;
+              }
+            }
+          }
+          if (!bar_wait(&s_full[grp], n_job & 1, abort)) {
+            live = false;
+            break;
+          }
+          __syncwarp();
+          fence_after();
+          const int tile_ue = nodes ? s_ue[slot] : vu_exp;
+          const float c = full ? c2p : c2;  // (the other tiles' factors are applied to the scores)
+          float v[64];
+          auto factors = [&](int h) {  // scores of half h: factor and -Inf where unseen
+            const float* fac = s_fac + slot * kKeys + 64 * h;
+#pragma unroll
+            for (int j = 0; j < 64; ++j) v[j] = ((see[h] >> j) & 1ull) ? v[j] * (nodes ? fac[j] : kv.k_unit) : -INFINITY;
+          };
+          auto most = [&]() {
+            float a0 = fmax3f(v[0], v[1], v[2]), a1 = fmax3f(v[3], v[4], v[5]);
+            float a2 = fmax3f(v[6], v[7], v[8]), a3 = fmax3f(v[9], v[10], v[11]);
+#pragma unroll
+            for (int j = 12; j + 8 <= 60; j += 8) {
+              a0 = fmax3f(a0, v[j], v[j + 1]);
+              a1 = fmax3f(a1, v[j + 2], v[j + 3]);
+              a2 = fmax3f(a2, v[j + 4], v[j + 5]);
+              a3 = fmax3f(a3, v[j + 6], v[j + 7]);
+            }
+            return fmax3f(fmax3f(a0, v[60], v[61]), fmax3f(a1, v[62], v[63]), fmaxf(a2, a3));
+          };
+          tmem_ld64(tS, v);
+          if (!full) factors(0);
+          float tmax = most();
+          tmem_ld64(tS + 64, v);
+          if (!full) factors(1);
+          tmax = fmaxf(tmax, most()) * c;
+          // the base moves when passed by more than 2^15; O's unit when the tile's V has another
+          const bool move = tmax > m + kTop;
+          const bool unit = tile_ue != ue && mine > 0;
+          float corr = 1.0f;
+          if (move) {
+            const float nm = fmaxf(m, tmax - kHead);
+            corr = ex2(m - nm);
+            l *= corr;
+            m = nm;
+          }
+          if (unit) corr *= pow2f(ue - tile_ue);
+          ue = tile_ue;
+          if (mine > 0 && __any_sync(0xFFFFFFFFu, move || unit)) {
+            if (!bar_wait(&o_done[grp], (n_job - 1) & 1, abort)) {
+              live = false;
+              break;
+            }
+            __syncwarp();
+            fence_after();
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+              uint32_t y[32];
+              tmem_ld32(tO + 32 * h, y);
+              tmem_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
+              tmem_st32(tO + 32 * h, y);
+              tmem_st_wait();
+            }
+          }
+          const float2 cv = make_float2(c, c);
+          const float sub = m == -INFINITY ? 0.0f : m;
+          const float2 nv = make_float2(-sub, -sub);
+          float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          auto probs = [&](int h, uint32_t (&pk)[32]) {
+#pragma unroll
+            for (int j = 0; j < 64; j += 2) {
+              const float2 a = __ffma2_rn(make_float2(v[j], v[j + 1]), cv, nv);
+              float e0 = ex2(a.x), e1 = ex2(a.y);
+              if (!full) {
+                e0 = ((see[h] >> j) & 1ull) ? e0 : 0.0f;
+                e1 = ((see[h] >> (j + 1)) & 1ull) ? e1 : 0.0f;
+              }
+              sum[(j >> 1) & 3] = __fadd2_rn(sum[(j >> 1) & 3], make_float2(e0, e1));
+              pk[j >> 1] = h2u(__floats2half2_rn(e0, e1));
+            }
+          };
+          uint32_t pk1[32], pk0[32];
+          probs(1, pk1);
+          tmem_ld64(tS, v);  // the first half again: P overwrites it below
+          if (!full) factors(0);
+          probs(0, pk0);
+          tmem_st32(tS, pk0);
+          tmem_st32(tS + 32, pk1);
+          tmem_st_wait();
+          const float2 s01 = __fadd2_rn(sum[0], sum[1]), s23 = __fadd2_rn(sum[2], sum[3]);
+          const float2 st = __fadd2_rn(s01, s23);
+          l += st.x + st.y;
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&p_full[grp]);
+          ++n_job;
+          ++mine;
+        }
+        if (!live) break;
+        if (RT == 1) {  // this group's S products have read Q
+          __syncwarp();
+          if (lane == 0) bar_arrive(q_free);
+        }
+        // the part's record: o normalized by its own sum, the base and the sum
+        if (mine > 0) {
+          if (!bar_wait(&o_done[grp], (n_job - 1) & 1, abort)) {
+            live = false;
+            break;
+          }
+          __syncwarp();
+          fence_after();
+        }
+        // a row that sees a node with a non-finite V gets NaN (the marks are complete: the
+        // products with V are)
+        bool poison = false;
+        for (int x = max(p.x0, p.NT); x < p.x1; ++x) {
+          if (RT == 1 && ((x - p.x0) & 1) != grp) continue;
+          const uint32_t* bad = s_bad + (tail0 + x - max(p.x0, p.NT)) % kTailRing * 4;
+          const int wd = 2 * (x - p.NT);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (row_ok && wd + h < words)
+              poison |= (mrow[wd + h] & (bad[2 * h] | (static_cast<uint64_t>(bad[2 * h + 1]) << 32))) != 0ull;
+        }
+        const size_t rec = (static_cast<size_t>(p.b) * Qn + p.pq + cta) * (RT == 1 ? 2 : 1) + (RT == 1 ? grp : 0);
+        const size_t rrow = rec * (RT * kRows) + (RT == 2 ? grp * kRows : 0) + r;
+        if (mine > 0) {
+          const float inv = poison ? __int_as_float(0x7FC00000) : l != 0.0f ? pow2f(ue) / l : 0.0f;
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            uint32_t y[32];
+            tmem_ld32(tO + 32 * h, y);
+            tmem_wait();
+            if (row_ok) {
+              float4* dst = reinterpret_cast<float4*>(ws_o + rrow * kHD + 32 * h);
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                dst[j] = make_float4(__uint_as_float(y[4 * j]) * inv, __uint_as_float(y[4 * j + 1]) * inv,
+                                     __uint_as_float(y[4 * j + 2]) * inv, __uint_as_float(y[4 * j + 3]) * inv);
+            }
+          }
+          fence_before();
+        }
+        if (row_ok) ws_ml[rrow] = make_float2(m, l);
+        if (grp == 0 && r == 0) {
+          int32_t* e = ends + 2 * (static_cast<size_t>(p.b) * Qn + p.pq);
+          if (p.x0 == 0) e[0] = cta;
+          if (p.x1 == p.units) e[1] = cta;
+        }
+        ++n_part;
+      } while (p.next(g, kv, kv_len));
+    }
+  }
+  fence_before();
+  if (__syncthreads_or(*abort != 0)) {
+    // after a wait that ran out, the copies still in flight land (bounded) before the
+    // shared memory goes
+    if (warp == 0) {
+      const uint64_t t0 = gtimer();
+      for (int t = max(0, T_raw - kRaw); t < T_raw; ++t)
+        while (!bar_try(&raw_full[t % kRaw], (t / kRaw) & 1) && gtimer() - t0 < kWaitNs) {
+        }
+      if (lane == 0) dev_flag(dev_err, E3_DEV_ERR_TIMEOUT);
+    }
+    __syncthreads();
+  }
+  fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+V4Geom make_geom_tc(int B, int R, int H, int KVH, int max_kv_len) {
+  V4Geom g{};
+  g.B = B;
+  g.R = R;
+  g.H = H;
+  g.KVH = KVH;
+  g.G = H / KVH;
+  g.rows = g.G * R <= kRows ? kRows : 2 * kRows;
+  g.RG = (g.G * R + g.rows - 1) / g.rows;
+  g.max_kv_len = max_kv_len;
+  g.workers = num_sms();
+  g.min_share = 1;
+  return g;
+}
+
+// records: one per part (two where the softmax groups take the tiles in turn)
+size_t record_rows(const V4Geom& g) {
+  return (static_cast<size_t>(g.B) * g.KVH * g.RG + g.workers) * 2 * kRows;
+}
+
+template <int RT>
+cudaError_t launch_tc(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
+                      const uint64_t* mask, const V4Geom& g, float sm_scale, float* ws_o, float2* ws_ml, int32_t* ends,
+                      __nv_bfloat16* o, float* lse, int32_t* dev_err, cudaStream_t s) {
+  static std::atomic<bool> attr_done{false};
+  if (!attr_done.load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(verify4_tc_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<RT>::SMEM);
+    if (e != cudaSuccess) return e;
+    attr_done.store(true, std::memory_order_release);
+  }
+  const cudaError_t e = launch_pdl(verify4_tc_kernel<RT>, dim3(g.workers), dim3(kThreads), Cfg<RT>::SMEM, s, 1, q, kv, tail,
+                                   kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, dev_err);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(verify4_merge_kernel<kHD, RT * kRows, kKeys, RT == 1 ? 2 : 1>,
+                    dim3(static_cast<unsigned>((static_cast<long>(g.B) * g.R * g.H + 3) / 4)), dim3(128), 0, s, 1, kv, kv_len, g,
+                    static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml), static_cast<const int32_t*>(ends), o,
+                    lse);
+}
+
+}  // namespace
+
+bool verify4_uses_tc(int R, int H, int KVH, int hd) { return hd == kHD && H / KVH * R > 16; }
+
+size_t verify4_tc_workspace_bytes(int B, int R, int H, int KVH, int max_kv_len) {
+  const V4Geom g = make_geom_tc(B, R, H, KVH, max_kv_len);
+  return record_rows(g) * (kHD * sizeof(float) + sizeof(float2)) +
+         static_cast<size_t>(g.B) * g.KVH * g.RG * 2 * sizeof(int32_t);
+}
+
+e3_status launch_verify4_tc(const void* Q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
+                            const uint64_t* mask, int B, int R, int H, int max_kv_len, float sm_scale, void* O, float* lse,
+                            int32_t* dev_err, void* ws, cudaStream_t s) {
+  const V4Geom g = make_geom_tc(B, R, H, kv.n_kv_heads, max_kv_len);
+  float* ws_o = static_cast<float*>(ws);
+  float2* ws_ml = reinterpret_cast<float2*>(ws_o + record_rows(g) * kHD);
+  int32_t* ends = reinterpret_cast<int32_t*>(ws_ml + record_rows(g));
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(Q);
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(O);
+  const cudaError_t e = g.rows == kRows ? launch_tc<1>(q, kv, tail, kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, o, lse, dev_err, s)
+                                        : launch_tc<2>(q, kv, tail, kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, o, lse, dev_err, s);
+  return e == cudaSuccess ? E3_OK : cuda_status(e, "verify4_tc kernels");
+}
+
+}  // namespace e3

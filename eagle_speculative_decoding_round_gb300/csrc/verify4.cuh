@@ -1,0 +1,175 @@
+// verify4.cuh -- what the kernels of tree_verify_attn4 share: how the work is cut, and the
+// merge of the parts.
+#pragma once
+#include <math.h>
+
+#include <type_traits>
+
+#include "e3_common.cuh"
+
+namespace e3 {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// The softmax base m is kept kHead below the running maximum it was set from and moves
+// when a score passes it by more than kTop (log2): weights stay below 2^15 in fp16, and
+// fp16's subnormal step is 2^-32 of a row's largest weight.
+constexpr float kHead = 7.0f, kTop = 15.0f;
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// How the work is shared.  A pair is (request, KV head, tile of `rows` query rows); its
+// units are granules of `keys` prefix keys and then of `keys` tree nodes.  All pairs' units in a
+// row, request by request, are cut into equal shares, one per worker (a warp), whatever
+// the requests' lengths: a worker may end one pair and begin the next.  The part of pair
+// p that worker c computed is record p + c (both only grow along the row, so no two
+// coincide).
+struct V4Geom {
+  int B, R, H, KVH, G;
+  int rows;     // query rows of a tile
+  int RG;       // row tiles of a KV head
+  int workers;  // shares
+  int min_share;
+  int max_kv_len;
+};
+
+// Units of request b's pairs, 0 if its length is out of bounds.
+template <int KEYS>
+__device__ __forceinline__ int pair_units(const V4Geom& g, const e3_kv4_layer& kv, int P) {
+  if (P < 0 || P > g.max_kv_len || P > static_cast<long long>(kv.max_pages) * kv.page_size) return 0;
+  return (P + KEYS - 1) / KEYS + (g.R + KEYS - 1) / KEYS;
+}
+
+// Where a worker begins in the row of units.  Every lane of the warp calls it and gets the
+// same answer.
+struct V4Place {
+  long long share, before;  // units of a share; units before request b
+  int b;                    // the request that holds the share's first unit (B: none)
+};
+template <int KEYS>
+__device__ __forceinline__ V4Place find_place(const V4Geom& g, const e3_kv4_layer& kv, const int32_t* kv_len, int worker) {
+  const int lane = threadIdx.x & 31;
+  const long long Q = static_cast<long long>(g.KVH) * g.RG;
+  long long total = 0;
+  for (int b0 = 0; b0 < g.B; b0 += 32) {
+    const int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv, kv_len[b0 + lane]) : 0;
+    total += __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(u));
+  }
+  V4Place f;
+  f.share = max((total * Q + g.workers - 1) / g.workers, static_cast<long long>(g.min_share));
+  const long long at = f.share * worker;
+  long long base = 0;
+  f.b = g.B;
+  f.before = total * Q;
+  for (int b0 = 0; b0 < g.B; b0 += 32) {
+    const int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv, kv_len[b0 + lane]) : 0;
+    unsigned incl = static_cast<unsigned>(u);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const long long end = (base + incl) * Q;
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, end > at);
+    if (hit) {
+      const int k = __ffs(hit) - 1;
+      f.b = b0 + k;
+      f.before = (base + __shfl_sync(0xFFFFFFFFu, incl, k) - __shfl_sync(0xFFFFFFFFu, static_cast<unsigned>(u), k)) * Q;
+      break;
+    }
+    base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  return f;
+}
+
+// Merge of a pair's records: one warp per (b, i, h) row, hd/32 dims a lane.  ROWS: the
+// row tile of the kernel that wrote them.  The workers that began and ended the pair left
+// their numbers in `ends`, so the records are found without the search; the first
+// records' values are requested together with their weights.
+template <int HD, int ROWS, int KEYS, int SPLIT>
+__global__ void __launch_bounds__(128)
+verify4_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __restrict__ kv_len,
+                     const __grid_constant__ V4Geom g, const float* __restrict__ ws_o, const float2* __restrict__ ws_ml,
+                     const int32_t* __restrict__ ends, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
+  constexpr int PER = HD / 32;
+  constexpr int AHEAD = 8;
+  const int lane = threadIdx.x & 31;
+  const unsigned row = blockIdx.x * 4u + (threadIdx.x >> 5);
+  const unsigned stride = static_cast<unsigned>(g.R) * g.H;
+  const int b = static_cast<int>(row / stride);
+  if (b >= g.B) {
+    pdl_wait();
+    return;
+  }
+  const int ih = static_cast<int>(row - b * stride), i = ih / g.H, h = ih - i * g.H;
+  const int kvh = h / g.G, r = i * g.G + h - kvh * g.G, rt = r / ROWS;
+  const size_t pair = static_cast<size_t>(b) * g.KVH * g.RG + kvh * g.RG + rt;
+  pdl_wait();
+  pdl_trigger();
+  const int P = kv_len[b], c0 = ends[2 * pair], c1 = ends[2 * pair + 1];
+  if (pair_units<KEYS>(g, kv, P) == 0) return;
+  const int n = (c1 - c0 + 1) * SPLIT;
+  const size_t base = (pair + c0) * SPLIT * ROWS + (r - rt * ROWS);  // then ROWS apart
+  using Vec = typename std::conditional<PER == 4, float4, float2>::type;
+  auto value = [&](int q) { return reinterpret_cast<const Vec*>(ws_o + (base + static_cast<size_t>(q) * ROWS) * HD)[lane]; };
+  Vec x[AHEAD];
+#pragma unroll
+  for (int q = 0; q < AHEAD; ++q)
+    if (q < n) x[q] = value(q);
+  float2 ml = lane < n ? ws_ml[base + static_cast<size_t>(lane) * ROWS] : make_float2(-INFINITY, 0.0f);
+  float M = ml.y != 0.0f ? ml.x : -INFINITY;
+  for (int q = lane + 32; q < n; q += 32) {
+    const float2 y = ws_ml[base + static_cast<size_t>(q) * ROWS];
+    if (y.y != 0.0f) M = fmaxf(M, y.x);
+  }
+  M = warp_reduce(M, MaxF());
+  float acc[PER];
+#pragma unroll
+  for (int u = 0; u < PER; ++u) acc[u] = 0.0f;
+  float den = 0.0f;
+  for (int q0 = 0; q0 < n; q0 += 32) {
+    if (q0 > 0) ml = q0 + lane < n ? ws_ml[base + static_cast<size_t>(q0 + lane) * ROWS] : make_float2(-INFINITY, 0.0f);
+    // (-1: a record without keys, whose values were never written; a NaN sum stays one)
+    const float w = ml.y != 0.0f ? ml.y * ex2(ml.x - M) : -1.0f;
+    den += w == -1.0f ? 0.0f : w;
+    const int nq = min(32, n - q0);
+    for (int j0 = 0; j0 < nq; j0 += AHEAD) {
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        const float wj = __shfl_sync(0xFFFFFFFFu, w, (j0 + j) & 31);
+        if (j0 + j < nq && wj != -1.0f) {
+          const float* v = reinterpret_cast<const float*>(&x[j]);
+#pragma unroll
+          for (int u = 0; u < PER; ++u) acc[u] = fmaf(wj, v[u], acc[u]);
+        }
+        if (q0 + j0 + AHEAD + j < n) x[j] = value(q0 + j0 + AHEAD + j);
+      }
+    }
+  }
+  den = warp_reduce(den, [](float p, float q) { return p + q; });
+  const float inv = den != 0.0f ? 1.0f / den : 0.0f;
+  __nv_bfloat16* out = O + static_cast<size_t>(row) * HD + lane * PER;
+#pragma unroll
+  for (int u = 0; u < PER; u += 2)
+    *reinterpret_cast<uint32_t*>(out + u) = pack2_bf16(acc[u] * inv, acc[u + 1] * inv);
+  if (lane == 0) lse[row] = den != 0.0f ? (M + log2f(den)) * kLn2 : -INFINITY;
+}
+
+int num_sms() {
+  static const int n_once = [] {  // queried once, thread-safely (152 on GB300 if the query fails)
+    int dev = 0, n = 0;
+    cudaGetDevice(&dev);
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
+    return n;
+  }();
+  return n_once;
+}
+
+}  // namespace
+
+}  // namespace e3
