@@ -26,6 +26,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "e3_common.cuh"
 #include "e3_kernels.h"
@@ -46,20 +47,18 @@ constexpr int kRawB = 2 * (kCodeB + kScaleB);
 constexpr int kRaw = 3;                  // raw stages
 constexpr int kTailRing = 8;             // tiles of tree nodes whose factors are kept (at most five are in flight)
 // Warpgroups: 0 = producer and MMA issuer (and two idle warps), 1 and 2 = softmax, 3 =
-// dequantizers.  Registers move from the first and the last to the softmax groups, which
-// hold half a row of scores: 56 + 2 x 168 + 80 = 472 of the 4 x 128 that the launch gives
-// each quarter of a warpgroup set.
+// dequantizers.  Registers move from the first and the last to the softmax groups, whose
+// threads hold a row of scores each; launch_tc checks that the launch brings the sum.
 constexpr int kThreads = 512;
 constexpr int kSoftmax0 = 4, kDeq0 = 12;
-constexpr int kRegsIssue = 56, kRegsSoftmax = 168, kRegsDeq = 80;
-static_assert(kRegsIssue + 2 * kRegsSoftmax + kRegsDeq <= 4 * 120, "the split stays below the launch's registers");
+constexpr int kRegsIssue = 48, kRegsSoftmax = 184, kRegsDeq = 88;
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
 template <int RT>
 struct Cfg {
   static constexpr int NV = RT == 2 ? 1 : 2;  // V stages
   static constexpr int Q = 0, K = RT * kOpB, V = K + 2 * kOpB, RAW = V + NV * kOpB, FAC = RAW + kRaw * kRawB;
-  static constexpr int BARS = FAC + kTailRing * kKeys * 4, END = BARS + 512;
+  static constexpr int BARS = FAC + kTailRing * kKeys * 4, END = BARS + 640;
   static constexpr int SMEM = END + 1024;  // (base rounded up to 1024)
 };
 static_assert(Cfg<1>::SMEM <= 232448 && Cfg<2>::SMEM <= 232448, "shared memory of a CTA");
@@ -143,11 +142,33 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
 }
 #undef E3_R8
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// 64 columns of this thread's lane as 32 register pairs (so that the packed arithmetic
+// needs no moves), one load instruction and its wait
 __device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  tmem_ld32(taddr, r);
-  tmem_ld32(taddr + 32, r + 32);
-  tmem_wait();
+  unsigned long long q[32];
+#define E3_Q4(o) "=l"(q[o]), "=l"(q[o + 1]), "=l"(q[o + 2]), "=l"(q[o + 3])
+#define E3_M(i, a, b) " mov.b64 %" #i ", {t" #a ", t" #b "};\n"
+  asm volatile(
+      "{\n .reg .b32 t<64>;\n"
+      " tcgen05.ld.sync.aligned.32x32b.x64.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,t16,t17,t18,t19,t20,"
+      "t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31,t32,t33,t34,t35,t36,t37,t38,t39,t40,t41,t42,t43,t44,t45,t46,t47,t48,t49,"
+      "t50,t51,t52,t53,t54,t55,t56,t57,t58,t59,t60,t61,t62,t63}, [%32];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      E3_M(0, 0, 1) E3_M(1, 2, 3) E3_M(2, 4, 5) E3_M(3, 6, 7) E3_M(4, 8, 9) E3_M(5, 10, 11) E3_M(6, 12, 13) E3_M(7, 14, 15)
+      E3_M(8, 16, 17) E3_M(9, 18, 19) E3_M(10, 20, 21) E3_M(11, 22, 23) E3_M(12, 24, 25) E3_M(13, 26, 27) E3_M(14, 28, 29)
+      E3_M(15, 30, 31) E3_M(16, 32, 33) E3_M(17, 34, 35) E3_M(18, 36, 37) E3_M(19, 38, 39) E3_M(20, 40, 41)
+      E3_M(21, 42, 43) E3_M(22, 44, 45) E3_M(23, 46, 47) E3_M(24, 48, 49) E3_M(25, 50, 51) E3_M(26, 52, 53)
+      E3_M(27, 54, 55) E3_M(28, 56, 57) E3_M(29, 58, 59) E3_M(30, 60, 61) E3_M(31, 62, 63) "}\n"
+      : E3_Q4(0), E3_Q4(4), E3_Q4(8), E3_Q4(12), E3_Q4(16), E3_Q4(20), E3_Q4(24), E3_Q4(28)
+      : "r"(taddr)
+      : "memory");
+#undef E3_Q4
+#undef E3_M
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[2 * i] = __uint_as_float(static_cast<uint32_t>(q[i]));
+    v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(q[i] >> 32));
+  }
 }
 #define E3_V8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
@@ -158,6 +179,23 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       : "memory");
 }
 #undef E3_V8
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n"
+      " tcgen05.wait::st.sync.aligned;\n" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+      "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void regs_inc() {
@@ -245,8 +283,8 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   uint64_t* o_done = bars + 18;
   uint64_t* q_full = bars + 20;
   uint64_t* q_free = bars + 22;     // (RT = 1) both groups are done with the shared Q
-  int* s_ue = reinterpret_cast<int*>(bars + 24);                    // [kTailRing] exponent of V's unit in a tile of nodes
-  uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_ue + kTailRing);  // [kTailRing][4] nodes with a non-finite V
+  int* s_ue = reinterpret_cast<int*>(bars + 24);                        // [kTailRing][4] exponent of V's unit in a tile of nodes, by dequantizer warp
+  uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_ue + 4 * kTailRing);  // [kTailRing][4] nodes with a non-finite V
   uint32_t* tmem_slot = s_bad + 4 * kTailRing;
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -306,7 +344,6 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
     regs_dec<kRegsIssue>();
     if (warp == 0 && work) {
       Parts p = first;
-      int ntail = 0;
       bool live = true;
       do {
         const int kvh = p.pq / g.RG;
@@ -353,30 +390,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
               bulk_copy(su32(base + at_b), src, bytes, &raw_full[st]);
             }
           } else {
-            // a tile of tree nodes: the exponent of its largest finite V
-            const int j0 = (x - p.NT) * kKeys, nj = min(kKeys, g.R - j0);
-            uint32_t am = 0u;
-            for (int i = lane; i < nj * 16; i += 32) {
-              const int j = j0 + (i >> 4), pi = j / tail.page_size;
-              const int page = tail.page_table[static_cast<size_t>(p.b) * tail.max_pages + pi];
-              if (page < 0 || page >= tail.n_pages) continue;
-              const size_t row = (static_cast<size_t>(page) * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size);
-              const uint4 y = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(tail.v) + row * kHD)[i & 15];
-              const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t lo = w[c] & 0x7FFFu, hi = (w[c] >> 16) & 0x7FFFu;
-                if (lo < 0x7F80u) am = max(am, lo);
-                if (hi < 0x7F80u) am = max(am, hi);
-              }
-            }
-            am = __reduce_max_sync(0xFFFFFFFFu, am);
-            if (lane == 0) {
-              // (not so far below v_unit that O would overflow in it)
-              s_ue[ntail % kTailRing] = max(static_cast<int>(am >> 7) - 127, vu_exp - 40);
-              bar_arrive(&raw_full[st]);
-            }
-            ++ntail;
+            if (lane == 0) bar_arrive(&raw_full[st]);  // tree nodes: read by the dequantizers
           }
         }
       } while (live && p.next(g, kv, kv_len));
@@ -520,52 +534,94 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
                 }
               }
             } else {
-              const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(op ? tail.v : tail.k);
-              uint32_t bad_v = 0u;  // this warp's keys with a non-finite V
-#pragma unroll 1
-              for (int i = 0; i < 4; ++i) {
+              // 32 dims of a node's row (zeros where there is none), this lane's quarter
+              auto load_row = [&](const void* from, int i, uint4 (&y)[4]) {
                 const int key = dw * 32 + i * 8 + (lane >> 2), j = (x - p.NT) * kKeys + key;
-                uint4 y[4] = {};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[c] = make_uint4(0u, 0u, 0u, 0u);
                 if (key < left) {
                   const int pi = j / tail.page_size;
                   const int page = tail.page_table[static_cast<size_t>(p.b) * tail.max_pages + pi];
                   if (page >= 0 && page < tail.n_pages) {
                     const size_t row = (static_cast<size_t>(page) * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) y[c] = reinterpret_cast<const uint4*>(from + row * kHD + 32 * q)[c];
+                    for (int c = 0; c < 4; ++c)
+                      y[c] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(from) + row * kHD + 32 * q)[c];
                   } else {
                     dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
                   }
                 }
-                uint32_t w[16];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) w[4 * c] = y[c].x, w[4 * c + 1] = y[c].y, w[4 * c + 2] = y[c].z, w[4 * c + 3] = y[c].w;
+              };
+              // largest magnitude of the node's row as bf16 bits, the same in its four lanes
+              auto row_max = [&](const uint4 (&y)[4]) {
                 uint32_t am = 0u;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) am = __vmaxu2(am, w[c] & 0x7FFF7FFFu);
+                for (int c = 0; c < 4; ++c)
+                  am = __vmaxu2(am, __vmaxu2(__vmaxu2(y[c].x & 0x7FFF7FFFu, y[c].y & 0x7FFF7FFFu),
+                                             __vmaxu2(y[c].z & 0x7FFF7FFFu, y[c].w & 0x7FFF7FFFu)));
                 am = max(am & 0xFFFFu, am >> 16);
                 am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-                am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));  // the key's four lanes
-                const bool bad = am >= 0x7F80u;
-                // a node with a NaN or an Inf leaves the product: its scores get a NaN factor,
-                // rows that see its V are marked
-                const int ex = op ? s_ue[slot] : max(static_cast<int>(am >> 7), 1) - 127;
-                if (op == 0 && q == 0) s_fac[slot * kKeys + key] = bad ? __int_as_float(0x7FC00000) : pow2f(ex);
-                if (bad) bad_v |= 1u << (key & 31);
-                const int na = -ex / 2;
-                const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
-                const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
-                unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
+                return max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+              };
+              int vu = vu_exp - 40;  // (not so far below v_unit that O would overflow in it)
+              if (op == 0) {
+                // V's unit: the exponent of the tile's largest node without NaN or Inf.  Each
+                // warp leaves that of its nodes with its K
+                uint32_t top = 0u;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  uint32_t h[4];
+                for (int i0 = 0; i0 < 4; i0 += 2) {
+                  if (dw * 32 + i0 * 8 >= left) break;
+                  uint4 y[2][4];
+                  load_row(tail.v, i0, y[0]);
+                  load_row(tail.v, i0 + 1, y[1]);
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const uint32_t z = bad ? 0u : w[4 * c + k];
-                    h[k] = h2u(__floats2half2_rn(__uint_as_float(z << 16) * f0 * f1, __uint_as_float(z & 0xFFFF0000u) * f0 * f1));
+                  for (int h = 0; h < 2; ++h) {
+                    const uint32_t am = row_max(y[h]);
+                    if (am < 0x7F80u) top = max(top, am);
                   }
-                  const int chunk = 4 * (q & 1) + c;
-                  *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                }
+                top = __reduce_max_sync(0xFFFFFFFFu, top);
+                if (lane == 0) s_ue[slot * 4 + dw] = max(static_cast<int>(top >> 7) - 127, vu);
+              } else {
+                if (!bar_wait(&k_full[T & 1], (T >> 1) & 1, abort)) {  // every warp has left its own
+                  live = false;
+                  break;
+                }
+                __syncwarp();
+                vu = max(max(s_ue[slot * 4], s_ue[slot * 4 + 1]), max(s_ue[slot * 4 + 2], s_ue[slot * 4 + 3]));
+              }
+              uint32_t bad_v = 0u;  // this warp's keys with a non-finite V
+#pragma unroll 1
+              for (int i0 = 0; i0 < 4; i0 += 2) {
+                uint4 y[2][4];
+                load_row(op ? tail.v : tail.k, i0, y[0]);
+                load_row(op ? tail.v : tail.k, i0 + 1, y[1]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const int key = dw * 32 + (i0 + h) * 8 + (lane >> 2);
+                  const uint32_t am = row_max(y[h]);
+                  const bool bad = am >= 0x7F80u;
+                  // a node with a NaN or an Inf leaves the product: its scores get a NaN
+                  // factor, rows that see its V are marked
+                  const int ex = op ? vu : max(static_cast<int>(am >> 7), 1) - 127;
+                  if (op == 0 && q == 0) s_fac[slot * kKeys + key] = bad ? __int_as_float(0x7FC00000) : pow2f(ex);
+                  if (bad) bad_v |= 1u << (key & 31);
+                  const int na = -ex / 2;
+                  const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
+                  const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
+                  unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) {
+                    const uint32_t w[4] = {y[h][c].x, y[h][c].y, y[h][c].z, y[h][c].w};
+                    uint32_t hh[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                      const uint32_t z = bad ? 0u : w[k];
+                      hh[k] = h2u(__floats2half2_rn(__uint_as_float(z << 16) * f0 * f1, __uint_as_float(z & 0xFFFF0000u) * f0 * f1));
+                    }
+                    const int chunk = 4 * (q & 1) + c;
+                    *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+                  }
                 }
               }
               bad_v = __reduce_or_sync(0xFFFFFFFFu, bad_v);
@@ -669,90 +725,92 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           }
           __syncwarp();
           fence_after();
-          const int tile_ue = nodes ? s_ue[slot] : vu_exp;
-          const float c = full ? c2p : c2;  // (the other tiles' factors are applied to the scores)
-          float v[64];
-          auto factors = [&](int h) {  // scores of half h: factor and -Inf where unseen
-            const float* fac = s_fac + slot * kKeys + 64 * h;
+          const int tile_ue = nodes ? max(max(s_ue[slot * 4], s_ue[slot * 4 + 1]), max(s_ue[slot * 4 + 2], s_ue[slot * 4 + 3])) : vu_exp;
+          // One tile's scores to probabilities; ALL: every key is seen and the factor is the
+          // cache's (the other tiles' factors and masks are applied element by element).
+          // False: a wait ran out.
+          auto tile = [&](auto all) -> bool {
+            constexpr bool ALL = decltype(all)::value;
+            const float c = ALL ? c2p : c2;
+            float v[2][64];
+            auto factors = [&](int h) {  // scores of half h: factor and -Inf where unseen
+              const float* fac = s_fac + slot * kKeys + 64 * h;
 #pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] = ((see[h] >> j) & 1ull) ? v[j] * (nodes ? fac[j] : kv.k_unit) : -INFINITY;
-          };
-          auto most = [&]() {
-            float a0 = fmax3f(v[0], v[1], v[2]), a1 = fmax3f(v[3], v[4], v[5]);
-            float a2 = fmax3f(v[6], v[7], v[8]), a3 = fmax3f(v[9], v[10], v[11]);
+              for (int j = 0; j < 64; ++j) v[h][j] = ((see[h] >> j) & 1ull) ? v[h][j] * (nodes ? fac[j] : kv.k_unit) : -INFINITY;
+            };
+            auto most = [&](const float (&y)[64]) {
+              float a0 = fmax3f(y[0], y[1], y[2]), a1 = fmax3f(y[3], y[4], y[5]);
+              float a2 = fmax3f(y[6], y[7], y[8]), a3 = fmax3f(y[9], y[10], y[11]);
 #pragma unroll
-            for (int j = 12; j + 8 <= 60; j += 8) {
-              a0 = fmax3f(a0, v[j], v[j + 1]);
-              a1 = fmax3f(a1, v[j + 2], v[j + 3]);
-              a2 = fmax3f(a2, v[j + 4], v[j + 5]);
-              a3 = fmax3f(a3, v[j + 6], v[j + 7]);
-            }
-            return fmax3f(fmax3f(a0, v[60], v[61]), fmax3f(a1, v[62], v[63]), fmaxf(a2, a3));
-          };
-          tmem_ld64(tS, v);
-          if (!full) factors(0);
-          float tmax = most();
-          tmem_ld64(tS + 64, v);
-          if (!full) factors(1);
-          tmax = fmaxf(tmax, most()) * c;
-          // the base moves when passed by more than 2^15; O's unit when the tile's V has another
-          const bool move = tmax > m + kTop;
-          const bool unit = tile_ue != ue && mine > 0;
-          float corr = 1.0f;
-          if (move) {
-            const float nm = fmaxf(m, tmax - kHead);
-            corr = ex2(m - nm);
-            l *= corr;
-            m = nm;
-          }
-          if (unit) corr *= pow2f(ue - tile_ue);
-          ue = tile_ue;
-          if (mine > 0 && __any_sync(0xFFFFFFFFu, move || unit)) {
-            if (!bar_wait(&o_done[grp], (n_job - 1) & 1, abort)) {
-              live = false;
-              break;
-            }
-            __syncwarp();
-            fence_after();
-#pragma unroll 1
-            for (int h = 0; h < 4; ++h) {
-              uint32_t y[32];
-              tmem_ld32(tO + 32 * h, y);
-              tmem_wait();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
-              tmem_st32(tO + 32 * h, y);
-              tmem_st_wait();
-            }
-          }
-          const float2 cv = make_float2(c, c);
-          const float sub = m == -INFINITY ? 0.0f : m;
-          const float2 nv = make_float2(-sub, -sub);
-          float2 sum[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          auto probs = [&](int h, uint32_t (&pk)[32]) {
-#pragma unroll
-            for (int j = 0; j < 64; j += 2) {
-              const float2 a = __ffma2_rn(make_float2(v[j], v[j + 1]), cv, nv);
-              float e0 = ex2(a.x), e1 = ex2(a.y);
-              if (!full) {
-                e0 = ((see[h] >> j) & 1ull) ? e0 : 0.0f;
-                e1 = ((see[h] >> (j + 1)) & 1ull) ? e1 : 0.0f;
+              for (int j = 12; j + 8 <= 60; j += 8) {
+                a0 = fmax3f(a0, y[j], y[j + 1]);
+                a1 = fmax3f(a1, y[j + 2], y[j + 3]);
+                a2 = fmax3f(a2, y[j + 4], y[j + 5]);
+                a3 = fmax3f(a3, y[j + 6], y[j + 7]);
               }
-              sum[(j >> 1) & 3] = __fadd2_rn(sum[(j >> 1) & 3], make_float2(e0, e1));
-              pk[j >> 1] = h2u(__floats2half2_rn(e0, e1));
+              return fmax3f(fmax3f(a0, y[60], y[61]), fmax3f(a1, y[62], y[63]), fmaxf(a2, a3));
+            };
+            tmem_ld64(tS, v[0]);
+            if (!ALL) factors(0);
+            float tmax = most(v[0]);
+            tmem_ld64(tS + 64, v[1]);
+            if (!ALL) factors(1);
+            tmax = fmaxf(tmax, most(v[1])) * c;
+            // the base moves when passed by more than 2^15; O's unit when the tile's V has another
+            const bool move = tmax > m + kTop;
+            const bool unit = tile_ue != ue && mine > 0;
+            float corr = 1.0f;
+            if (move) {
+              const float nm = fmaxf(m, tmax - kHead);
+              corr = ex2(m - nm);
+              l *= corr;
+              m = nm;
             }
+            if (unit) corr *= pow2f(ue - tile_ue);
+            ue = tile_ue;
+            const bool rescale = mine > 0 && __any_sync(0xFFFFFFFFu, move || unit);
+            const float2 cv = make_float2(c, c);
+            const float sub = ALL ? m : m == -INFINITY ? 0.0f : m;
+            const float2 nv = make_float2(-sub, -sub);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // P of half h goes over columns [32 h, 32 h + 32): scores already read
+              uint32_t pk[32];
+#pragma unroll
+              for (int j = 0; j < 64; j += 2) {
+                const float2 a = __ffma2_rn(make_float2(v[h][j], v[h][j + 1]), cv, nv);
+                float e0 = ex2(a.x), e1 = ex2(a.y);
+                if (!ALL) {
+                  e0 = ((see[h] >> j) & 1ull) ? e0 : 0.0f;
+                  e1 = ((see[h] >> (j + 1)) & 1ull) ? e1 : 0.0f;
+                }
+                sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], make_float2(e0, e1));
+                pk[j >> 1] = h2u(__floats2half2_rn(e0, e1));
+              }
+              tmem_st32(tS + 32 * h, pk);
+            }
+            const float2 st = __fadd2_rn(sum[0], sum[1]);
+            l += st.x + st.y;
+            if (rescale) {
+              if (!bar_wait(&o_done[grp], (n_job - 1) & 1, abort)) return false;
+              __syncwarp();
+              fence_after();
+#pragma unroll 1
+              for (int h = 0; h < 8; ++h) {  // in 16-column steps, to keep register pressure low
+                uint32_t y[16];
+                tmem_ld16(tO + 16 * h, y);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
+                tmem_st16(tO + 16 * h, y);
+              }
+            }
+            tmem_st_wait();
+            return true;
           };
-          uint32_t pk1[32], pk0[32];
-          probs(1, pk1);
-          tmem_ld64(tS, v);  // the first half again: P overwrites it below
-          if (!full) factors(0);
-          probs(0, pk0);
-          tmem_st32(tS, pk0);
-          tmem_st32(tS + 32, pk1);
-          tmem_st_wait();
-          const float2 s01 = __fadd2_rn(sum[0], sum[1]), s23 = __fadd2_rn(sum[2], sum[3]);
-          const float2 st = __fadd2_rn(s01, s23);
-          l += st.x + st.y;
+          if (!(full ? tile(std::true_type{}) : tile(std::false_type{}))) {
+            live = false;
+            break;
+          }
           fence_before();
           __syncwarp();
           if (lane == 0) bar_arrive(&p_full[grp]);
@@ -857,9 +915,13 @@ cudaError_t launch_tc(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_k
                       __nv_bfloat16* o, float* lse, int32_t* dev_err, cudaStream_t s) {
   static std::atomic<bool> attr_done{false};
   if (!attr_done.load(std::memory_order_acquire)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(verify4_tc_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<RT>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(verify4_tc_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<RT>::SMEM);
     if (e != cudaSuccess) return e;
+    // a warpgroup that asked for registers which the launch did not bring would wait for ever
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, verify4_tc_kernel<RT>);
+    if (e != cudaSuccess) return e;
+    if (4 * fa.numRegs < kRegsIssue + 2 * kRegsSoftmax + kRegsDeq) return cudaErrorLaunchOutOfResources;
     attr_done.store(true, std::memory_order_release);
   }
   const cudaError_t e = launch_pdl(verify4_tc_kernel<RT>, dim3(g.workers), dim3(kThreads), Cfg<RT>::SMEM, s, 1, q, kv, tail,
