@@ -9,7 +9,7 @@
 //                          value c * e is exact in fp16 (see k_verify4.cu).  Tree nodes are
 //                          read from the bf16 tail and scaled by powers of two instead
 //                          (per key for K, per tile for V), which keeps their bits
-//   S = Q K^T              tcgen05.mma kind::f16, M = 128 rows, N = 128 keys, into the S
+//   S = Q K^T              (warps 1 and 2, one per softmax group) tcgen05.mma kind::f16, M = 128 rows, N = 128 keys, into the S
 //                          buffer of the row's softmax group
 //   softmax (2 x 4 warps)  one thread per row: maximum, exponentials, P (fp16) over S
 //   O += P V               A = P from TMEM, V in place as an MN-major operand; O stays in
@@ -46,7 +46,7 @@ constexpr int kScaleB = kKeys * kHD / 16;
 constexpr int kRawB = 2 * (kCodeB + kScaleB);
 constexpr int kRaw = 3;                  // raw stages
 constexpr int kTailRing = 8;             // tiles of tree nodes whose factors are kept (at most five are in flight)
-// Warpgroups: 0 = producer and MMA issuer (and two idle warps), 1 and 2 = softmax, 3 =
+// Warpgroups: 0 = producer and the MMA issuers (and an idle warp), 1 and 2 = softmax, 3 =
 // dequantizers.  Registers move from the first and the last to the softmax groups, whose
 // threads hold a row of scores each; launch_tc checks that the launch brings the sum.
 constexpr int kThreads = 512;
@@ -297,9 +297,9 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(&k_full[i], 4);
-      bar_init(&k_empty[i], 1);
+      bar_init(&k_empty[i], RT);  // one commit per group that uses the tile
       bar_init(&v_full[i], 4);
-      bar_init(&v_empty[i], 1);
+      bar_init(&v_empty[i], RT);
       bar_init(&s_full[i], 1);
       bar_init(&p_full[i], 4);
       bar_init(&o_done[i], 1);
@@ -395,77 +395,49 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         }
       } while (live && p.next(g, kv, kv_len));
     }
-    if (warp == 1 && lane == 0 && work) {
+    // one issuing thread per softmax group: neither group's products wait behind the other
+    // group's barriers
+    if ((warp == 1 || warp == 2) && lane == 0 && work) {
       constexpr uint32_t idS = idesc_f16(0), idO = idesc_f16(1);
-      const uint64_t q_desc = desc_sw128(su32(sQ), 16, 1024);
+      const int w = warp - 1;
+      const uint64_t q_desc = desc_sw128(su32(sQ) + (RT == 2 ? w : 0) * kOpB, 16, 1024);
       const uint64_t k_desc = desc_sw128(su32(sK), 16, 1024);
       const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
-      // jobs in order: RT = 2: (tile, group 0), (tile, group 1), ...; RT = 1: the tiles of a
-      // part, groups in turn.  Two cursors: S runs one job ahead of O
-      struct Cursor {
-        Parts p;
-        int i, n, T, part;  // job of the part, jobs of the part, tile number, part number
-        bool on;
-      };
-      auto start = [&](Cursor& c) { c.n = c.p.tiles() * RT, c.i = 0; };
-      auto advance = [&](Cursor& c) {
-        if (RT == 1 || (c.i & 1)) ++c.T;
-        if (++c.i == c.n) {
-          c.on = c.p.next(g, kv, kv_len);
-          ++c.part;
-          if (c.on) start(c);
-        }
-      };
-      Cursor s{first, 0, 0, 0, 0, true}, o{first, 0, 0, 0, 0, true};
-      start(s);
-      start(o);
-      int ns[2] = {0, 0}, no[2] = {0, 0};  // S and O products issued per group
-      bool ok = true;
-      auto issue_S = [&]() {
-        const int w = s.i & 1, st = s.T & 1;
-        ok = ok && bar_wait(&k_full[st], (s.T >> 1) & 1, abort);
-        if (s.i < 2) ok = ok && bar_wait(&q_full[RT == 1 ? 0 : w], s.part & 1, abort);
-        if (ns[w] > 0) ok = ok && bar_wait(&o_done[w], (ns[w] - 1) & 1, abort);  // P of the group's last job has been read
-        if (!ok) return;
-        fence_after();
-        const uint64_t qd = q_desc + static_cast<uint64_t>(((RT == 1 ? 0 : w) * kOpB) >> 4);
-        const uint64_t kd = k_desc + static_cast<uint64_t>((st * kOpB) >> 4);
+      const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
+      Parts p = first;
+      int T = 0, n = 0, part = 0;  // tiles, this group's jobs, parts
+      bool live = true;
+      do {
+        const int tiles = p.tiles();
+        for (int i = 0; live && i < tiles; ++i, ++T) {
+          if (RT == 1 && (i & 1) != w) continue;
+          const uint32_t acc0 = i >= 2 || (RT == 2 && i > 0) ? 1u : 0u;  // the group's first job of a part starts its O
+          live = bar_wait(&k_full[T & 1], (T >> 1) & 1, abort);
+          if (acc0 == 0u) live = live && bar_wait(&q_full[RT == 1 ? 0 : w], part & 1, abort);
+          if (n > 0) live = live && bar_wait(&o_done[w], (n - 1) & 1, abort);  // P of the last job, under S, has been read
+          if (!live) break;
+          fence_after();
+          const uint64_t kd = k_desc + static_cast<uint64_t>(((T & 1) * kOpB) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kHD / 16; ++kk) {
-          const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kHalfB + (kk & 3) * 32) >> 4);
-          umma(tmem + w * 128, qd + off, kd + off, idS, kk > 0 ? 1u : 0u);
-        }
-        umma_commit(&s_full[w]);
-        if (RT == 1 || w == 1) umma_commit(&k_empty[st]);
-        ++ns[w];
-        advance(s);
-      };
-      auto issue_O = [&]() {
-        const int w = o.i & 1, st = o.T % NV;
-        ok = ok && bar_wait(&p_full[w], no[w] & 1, abort);
-        ok = ok && bar_wait(&v_full[st], (o.T / NV) & 1, abort);
-        if (!ok) return;
-        fence_after();
-        const uint64_t vd = v_desc + static_cast<uint64_t>((st * kOpB) >> 4);
-        const uint32_t acc0 = o.i >= 2 ? 1u : 0u;  // the group's first job of a part starts its O
+          for (int kk = 0; kk < kHD / 16; ++kk) {
+            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kHalfB + (kk & 3) * 32) >> 4);
+            umma(tS, q_desc + off, kd + off, idS, kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[w]);
+          umma_commit(&k_empty[T & 1]);
+          live = bar_wait(&v_full[T % NV], (T / NV) & 1, abort) && bar_wait(&p_full[w], n & 1, abort);
+          if (!live) break;
+          fence_after();
+          const uint64_t vd = v_desc + static_cast<uint64_t>(((T % NV) * kOpB) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          umma_ts(tmem + 256 + w * 128, tmem + w * 128 + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), idO,
-                  kk > 0 ? 1u : acc0);
-        umma_commit(&o_done[w]);
-        if (RT == 1 || w == 1) umma_commit(&v_empty[st]);
-        ++no[w];
-        advance(o);
-      };
-      issue_S();
-      while (ok && o.on) {
-        // the next S goes first where it waits for nothing that this O product leads to:
-        // the other group's, in the same part
-        const bool ahead = s.on && s.part == o.part && (s.i & 1) != (o.i & 1);
-        if (ahead) issue_S();
-        if (ok) issue_O();
-        if (!ahead && ok && s.on) issue_S();
-      }
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            umma_ts(tO, tS + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), idO, kk > 0 ? 1u : acc0);
+          umma_commit(&o_done[w]);
+          umma_commit(&v_empty[T % NV]);
+          ++n;
+        }
+        ++part;
+      } while (live && p.next(g, kv, kv_len));
     }
   } else if (warp >= kDeq0) {
     regs_dec<kRegsDeq>();
