@@ -51,7 +51,7 @@ constexpr int kTailRing = 8;             // tiles of tree nodes whose factors ar
 // threads hold a row of scores each; launch_tc checks that the launch brings the sum.
 constexpr int kThreads = 512;
 constexpr int kSoftmax0 = 4, kDeq0 = 12;
-constexpr int kRegsIssue = 48, kRegsSoftmax = 184, kRegsDeq = 88;
+constexpr int kRegsIssue = 64, kRegsSoftmax = 176, kRegsDeq = 88;
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
 template <int RT>
@@ -401,40 +401,51 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       constexpr uint32_t idS = idesc_f16(0), idO = idesc_f16(1);
       const int w = warp - 1;
       const uint64_t q_desc = desc_sw128(su32(sQ) + (RT == 2 ? w : 0) * kOpB, 16, 1024);
-      const uint64_t k_desc = desc_sw128(su32(sK), 16, 1024);
-      const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
+      const uint64_t k_desc0 = desc_sw128(su32(sK), 16, 1024);
+      const uint64_t v_desc0 = desc_sw128(su32(sV), kHalfB, 1024);
       const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
+      uint64_t* const sf = &s_full[w];
+      uint64_t* const pf = &p_full[w];
+      uint64_t* const od = &o_done[w];
+      uint64_t* const qf = &q_full[RT == 1 ? 0 : w];
       Parts p = first;
-      int T = 0, n = 0, part = 0;  // tiles, this group's jobs, parts
+      uint32_t T = 0, n = 0, part = 0;  // tiles, this group's jobs, parts
       bool live = true;
       do {
-        const int tiles = p.tiles();
-        for (int i = 0; live && i < tiles; ++i, ++T) {
-          if (RT == 1 && (i & 1) != w) continue;
-          const uint32_t acc0 = i >= 2 || (RT == 2 && i > 0) ? 1u : 0u;  // the group's first job of a part starts its O
-          live = bar_wait(&k_full[T & 1], (T >> 1) & 1, abort);
-          if (acc0 == 0u) live = live && bar_wait(&q_full[RT == 1 ? 0 : w], part & 1, abort);
-          if (n > 0) live = live && bar_wait(&o_done[w], (n - 1) & 1, abort);  // P of the last job, under S, has been read
+        const uint32_t tiles = static_cast<uint32_t>(p.tiles());
+        // the group's first tile of the part, then every tile (RT = 2) or every second
+        uint32_t t = T + (RT == 1 ? w : 0);
+        const uint32_t end = T + tiles;
+        T = end;
+        if (t < end) live = bar_wait(qf, part & 1, abort);
+        uint32_t acc0 = 0u;  // the first job of a part starts O
+        for (; live && t < end; t += RT == 1 ? 2 : 1) {
+          const uint32_t ks = t & 1, vs = NV == 2 ? t & 1 : 0;
+          const uint64_t kd = k_desc0 + static_cast<uint64_t>(ks * (kOpB >> 4)), vd = v_desc0 + static_cast<uint64_t>(vs * (kOpB >> 4));
+          if (!bar_wait(&k_full[ks], (t >> 1) & 1, abort)) live = false;
+          if (n > 0 && !bar_wait(od, (n - 1) & 1, abort)) live = false;  // P of the last job, under S, has been read
           if (!live) break;
           fence_after();
-          const uint64_t kd = k_desc + static_cast<uint64_t>(((T & 1) * kOpB) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kHD / 16; ++kk) {
-            const uint64_t off = static_cast<uint64_t>(((kk >> 2) * kHalfB + (kk & 3) * 32) >> 4);
+            constexpr uint64_t kStep = 32 >> 4;
+            const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kHalfB >> 4)) + (kk & 3) * kStep;
             umma(tS, q_desc + off, kd + off, idS, kk > 0 ? 1u : 0u);
           }
-          umma_commit(&s_full[w]);
-          umma_commit(&k_empty[T & 1]);
-          live = bar_wait(&v_full[T % NV], (T / NV) & 1, abort) && bar_wait(&p_full[w], n & 1, abort);
-          if (!live) break;
+          umma_commit(sf);
+          umma_commit(&k_empty[ks]);
+          if (!bar_wait(&v_full[vs], (NV == 2 ? t >> 1 : t) & 1, abort) || !bar_wait(pf, n & 1, abort)) {
+            live = false;
+            break;
+          }
           fence_after();
-          const uint64_t vd = v_desc + static_cast<uint64_t>(((T % NV) * kOpB) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
             umma_ts(tO, tS + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), idO, kk > 0 ? 1u : acc0);
-          umma_commit(&o_done[w]);
-          umma_commit(&v_empty[T % NV]);
+          umma_commit(od);
+          umma_commit(&v_empty[vs]);
           ++n;
+          acc0 = 1u;
         }
         ++part;
       } while (live && p.next(g, kv, kv_len));
