@@ -101,6 +101,11 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t par, volatile int
     }
   }
 }
+// The same for a whole warp: every lane gets the same answer (the warp stays together
+// where some lanes saw the phase and others the end)
+__device__ __forceinline__ bool warp_wait(uint64_t* b, uint32_t par, volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, bar_wait(b, par, abort));
+}
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
                "r"(bytes), "r"(su32(bar))
@@ -142,43 +147,37 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
 }
 #undef E3_R8
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// 64 columns of this thread's lane as 32 register pairs (so that the packed arithmetic
-// needs no moves), one load instruction and its wait
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float (&v)[64]) {
-  unsigned long long q[32];
+// 128 columns of this thread's lane as register pairs (so that the packed arithmetic needs
+// no moves): four loads in flight, one wait
+__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float2 (&v)[64]) {
+  unsigned long long q[64];
 #define E3_Q4(o) "=l"(q[o]), "=l"(q[o + 1]), "=l"(q[o + 2]), "=l"(q[o + 3])
 #define E3_M(i, a, b) " mov.b64 %" #i ", {t" #a ", t" #b "};\n"
   asm volatile(
-      "{\n .reg .b32 t<64>;\n"
-      " tcgen05.ld.sync.aligned.32x32b.x64.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,t16,t17,t18,t19,t20,"
-      "t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31,t32,t33,t34,t35,t36,t37,t38,t39,t40,t41,t42,t43,t44,t45,t46,t47,t48,t49,"
-      "t50,t51,t52,t53,t54,t55,t56,t57,t58,t59,t60,t61,t62,t63}, [%32];\n"
+      "{\n .reg .b32 t<128>;\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31}, [%64];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {t32,t33,t34,t35,t36,t37,t38,t39,t40,t41,t42,t43,t44,t45,t46,t47,t48,t49,t50,t51,t52,t53,t54,t55,t56,t57,t58,t59,t60,t61,t62,t63}, [%65];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {t64,t65,t66,t67,t68,t69,t70,t71,t72,t73,t74,t75,t76,t77,t78,t79,t80,t81,t82,t83,t84,t85,t86,t87,t88,t89,t90,t91,t92,t93,t94,t95}, [%66];\n"
+      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {t96,t97,t98,t99,t100,t101,t102,t103,t104,t105,t106,t107,t108,t109,t110,t111,t112,t113,t114,t115,t116,t117,t118,t119,t120,t121,t122,t123,t124,t125,t126,t127}, [%67];\n"
       " tcgen05.wait::ld.sync.aligned;\n"
       E3_M(0, 0, 1) E3_M(1, 2, 3) E3_M(2, 4, 5) E3_M(3, 6, 7) E3_M(4, 8, 9) E3_M(5, 10, 11) E3_M(6, 12, 13) E3_M(7, 14, 15)
-      E3_M(8, 16, 17) E3_M(9, 18, 19) E3_M(10, 20, 21) E3_M(11, 22, 23) E3_M(12, 24, 25) E3_M(13, 26, 27) E3_M(14, 28, 29)
-      E3_M(15, 30, 31) E3_M(16, 32, 33) E3_M(17, 34, 35) E3_M(18, 36, 37) E3_M(19, 38, 39) E3_M(20, 40, 41)
-      E3_M(21, 42, 43) E3_M(22, 44, 45) E3_M(23, 46, 47) E3_M(24, 48, 49) E3_M(25, 50, 51) E3_M(26, 52, 53)
-      E3_M(27, 54, 55) E3_M(28, 56, 57) E3_M(29, 58, 59) E3_M(30, 60, 61) E3_M(31, 62, 63) "}\n"
-      : E3_Q4(0), E3_Q4(4), E3_Q4(8), E3_Q4(12), E3_Q4(16), E3_Q4(20), E3_Q4(24), E3_Q4(28)
-      : "r"(taddr)
+       E3_M(8, 16, 17) E3_M(9, 18, 19) E3_M(10, 20, 21) E3_M(11, 22, 23) E3_M(12, 24, 25) E3_M(13, 26, 27) E3_M(14, 28, 29) E3_M(15, 30, 31)
+       E3_M(16, 32, 33) E3_M(17, 34, 35) E3_M(18, 36, 37) E3_M(19, 38, 39) E3_M(20, 40, 41) E3_M(21, 42, 43) E3_M(22, 44, 45) E3_M(23, 46, 47)
+       E3_M(24, 48, 49) E3_M(25, 50, 51) E3_M(26, 52, 53) E3_M(27, 54, 55) E3_M(28, 56, 57) E3_M(29, 58, 59) E3_M(30, 60, 61) E3_M(31, 62, 63)
+       E3_M(32, 64, 65) E3_M(33, 66, 67) E3_M(34, 68, 69) E3_M(35, 70, 71) E3_M(36, 72, 73) E3_M(37, 74, 75) E3_M(38, 76, 77) E3_M(39, 78, 79)
+       E3_M(40, 80, 81) E3_M(41, 82, 83) E3_M(42, 84, 85) E3_M(43, 86, 87) E3_M(44, 88, 89) E3_M(45, 90, 91) E3_M(46, 92, 93) E3_M(47, 94, 95)
+       E3_M(48, 96, 97) E3_M(49, 98, 99) E3_M(50, 100, 101) E3_M(51, 102, 103) E3_M(52, 104, 105) E3_M(53, 106, 107) E3_M(54, 108, 109) E3_M(55, 110, 111)
+       E3_M(56, 112, 113) E3_M(57, 114, 115) E3_M(58, 116, 117) E3_M(59, 118, 119) E3_M(60, 120, 121) E3_M(61, 122, 123) E3_M(62, 124, 125) E3_M(63, 126, 127)
+      "}\n"
+      : E3_Q4(0), E3_Q4(4), E3_Q4(8), E3_Q4(12), E3_Q4(16), E3_Q4(20), E3_Q4(24), E3_Q4(28), E3_Q4(32), E3_Q4(36), E3_Q4(40), E3_Q4(44), E3_Q4(48), E3_Q4(52), E3_Q4(56), E3_Q4(60)
+      : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
       : "memory");
 #undef E3_Q4
 #undef E3_M
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[2 * i] = __uint_as_float(static_cast<uint32_t>(q[i]));
-    v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(q[i] >> 32));
-  }
+  for (int i = 0; i < 64; ++i)
+    v[i] = make_float2(__uint_as_float(static_cast<uint32_t>(q[i])), __uint_as_float(static_cast<uint32_t>(q[i] >> 32)));
 }
-#define E3_V8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
-      E3_V8(v, 0), E3_V8(v, 8), E3_V8(v, 16), E3_V8(v, 24)
-      : "memory");
-}
-#undef E3_V8
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
@@ -190,8 +189,7 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n"
-      " tcgen05.wait::st.sync.aligned;\n" ::"r"(taddr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
       "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
@@ -283,6 +281,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   uint64_t* o_done = bars + 18;
   uint64_t* q_full = bars + 20;
   uint64_t* q_free = bars + 22;     // (RT = 1) both groups are done with the shared Q
+  uint64_t* go = bars + 23;         // (RT = 2) the second group may start a part
   int* s_ue = reinterpret_cast<int*>(bars + 24);                        // [kTailRing][4] exponent of V's unit in a tile of nodes, by dequantizer warp
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_ue + 4 * kTailRing);  // [kTailRing][4] nodes with a non-finite V
   uint32_t* tmem_slot = s_bad + 4 * kTailRing;
@@ -306,6 +305,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       bar_init(&q_full[i], 4);
     }
     bar_init(q_free, 8);
+    bar_init(go, 1);
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -349,7 +349,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         const int kvh = p.pq / g.RG;
         for (int x = p.x0; live && x < p.x1; ++x) {
           const int st = T_raw % kRaw;
-          if (!bar_wait(&raw_empty[st], ((T_raw / kRaw) & 1) ^ 1, abort)) {
+          if (!warp_wait(&raw_empty[st], ((T_raw / kRaw) & 1) ^ 1, abort)) {
             live = false;
             break;
           }
@@ -409,7 +409,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       uint64_t* const od = &o_done[w];
       uint64_t* const qf = &q_full[RT == 1 ? 0 : w];
       Parts p = first;
-      uint32_t T = 0, n = 0, part = 0;  // tiles, this group's jobs, parts
+      uint32_t T = 0, n = 0, part = 0, n_go = 0;  // tiles, this group's jobs, parts, staggered parts
       bool live = true;
       do {
         const uint32_t tiles = static_cast<uint32_t>(p.tiles());
@@ -418,6 +418,12 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         const uint32_t end = T + tiles;
         T = end;
         if (t < end) live = bar_wait(qf, part & 1, abort);
+        // the second group starts half a turn later, so that one group's exponentials run
+        // beside the other's products (started together they stay together): at the first
+        // group's first P of the part.  That group cannot be a part ahead, since the V
+        // stage waits for both
+        const bool stagger = RT == 2 && tiles >= 4;
+        if (stagger && w == 1) live = live && bar_wait(go, n_go & 1, abort);
         uint32_t acc0 = 0u;  // the first job of a part starts O
         for (; live && t < end; t += RT == 1 ? 2 : 1) {
           const uint32_t ks = t & 1, vs = NV == 2 ? t & 1 : 0;
@@ -438,6 +444,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
             live = false;
             break;
           }
+          if (stagger && w == 0 && acc0 == 0u) bar_arrive(go);
           fence_after();
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
@@ -448,178 +455,184 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           acc0 = 1u;
         }
         ++part;
+        if (stagger) ++n_go;
       } while (live && p.next(g, kv, kv_len));
     }
   } else if (warp >= kDeq0) {
     regs_dec<kRegsDeq>();
     if (work) {
       const int dw = warp - kDeq0, q = lane & 3;
-      Parts p = first;
-      int T = 0, ntail = 0;
-      bool live = true;
-      do {
+      // One operand (0: K, 1: V) of a tile.  K runs a tile ahead of V: the next tile's K does
+      // not wait for this tile's V stage, which both groups' O products have to leave first.
+      struct Cursor {
+        Parts p;
+        int x, T, ntail;
+        bool on;
+      };
+      auto advance = [&](Cursor& c) {
+        if (c.x >= c.p.NT) ++c.ntail;
+        ++c.T;
+        if (++c.x == c.p.x1) {
+          c.on = c.p.next(g, kv, kv_len);
+          c.x = c.p.x0;
+        }
+      };
+      auto convert = [&](const int op, const Cursor& cur) -> bool {
+        const Parts& p = cur.p;
+        const int x = cur.x, T = cur.T, st = T % kRaw, slot = cur.ntail % kTailRing;
         const int kvh = p.pq / g.RG;
-        for (int x = p.x0; live && x < p.x1; ++x, ++T) {
-          const int st = T % kRaw;
-          if (!bar_wait(&raw_full[st], (T / kRaw) & 1, abort)) {
-            live = false;
-            break;
+        if (op == 0 && !warp_wait(&raw_full[st], (T / kRaw) & 1, abort)) return false;
+        const int dst_st = op ? T % NV : T & 1;
+        if (!warp_wait(op ? &v_empty[dst_st] : &k_empty[dst_st], (op ? ((T / NV) & 1) : ((T >> 1) & 1)) ^ 1, abort)) return false;
+        const unsigned char* raw = sRaw + st * kRawB;
+        const bool nodes = x >= p.NT;
+        const int left = nodes ? g.R - (x - p.NT) * kKeys : p.P - x * kKeys;  // keys that exist
+        unsigned char* dst = (op ? sV : sK) + dst_st * kOpB;
+        if (!nodes) {
+          const unsigned char* codes = raw + op * kCodeB;
+          const unsigned char* scales = raw + 2 * kCodeB + op * kScaleB;
+          uint4 w4[4];
+          uint32_t e4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = dw * 32 + i * 8 + (lane >> 2);
+            w4[i] = *reinterpret_cast<const uint4*>(codes + key * (kHD / 2) + q * 16);
+            e4[i] = *reinterpret_cast<const uint16_t*>(scales + key * (kHD / 16) + 2 * q);
+            if (key >= left) e4[i] = 0u;  // beyond the prefix: adds 0 whatever the slot holds
           }
-          const unsigned char* raw = sRaw + st * kRawB;
-          const bool nodes = x >= p.NT;
-          const int left = nodes ? g.R - (x - p.NT) * kKeys : p.P - x * kKeys;  // keys that exist
-          const int slot = ntail % kTailRing;
-#pragma unroll 1
-          for (int op = 0; op < 2; ++op) {  // K, then V
-            const int dst_st = op ? T % NV : T & 1;
-            uint64_t* empty = op ? &v_empty[dst_st] : &k_empty[dst_st];
-            uint64_t* full = op ? &v_full[dst_st] : &k_full[dst_st];
-            if (!bar_wait(empty, (op ? ((T / NV) & 1) : ((T >> 1) & 1)) ^ 1, abort)) {
-              live = false;
-              break;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = dw * 32 + i * 8 + (lane >> 2);
+            const uint32_t e = h2u(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(e4[i]), __NV_E4M3))));
+            uint32_t ea = __byte_perm(e, e, 0x1010), eb = __byte_perm(e, e, 0x3232);
+            uint32_t w[4] = {w4[i].x, w4[i].y, w4[i].z, w4[i].w};
+            // the four 16-byte pieces in an order that differs between the lanes which
+            // store together, so that their banks do
+            const int flip = ((q >> 1) & 1) | ((key & 1) << 1);
+            if (flip & 1) {
+              const uint32_t a = w[0], b = w[2];
+              w[0] = w[1], w[1] = a, w[2] = w[3], w[3] = b;
             }
-            unsigned char* dst = (op ? sV : sK) + dst_st * kOpB;
-            if (!nodes) {
-              const unsigned char* codes = raw + op * kCodeB;
-              const unsigned char* scales = raw + 2 * kCodeB + op * kScaleB;
-              uint4 w4[4];
-              uint32_t e4[4];
+            if (flip & 2) {
+              uint32_t a = w[0], b = w[1];
+              w[0] = w[2], w[1] = w[3], w[2] = a, w[3] = b;
+              a = ea, ea = eb, eb = a;
+            }
+            unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int key = dw * 32 + i * 8 + (lane >> 2);
-                w4[i] = *reinterpret_cast<const uint4*>(codes + key * (kHD / 2) + q * 16);
-                e4[i] = *reinterpret_cast<const uint16_t*>(scales + key * (kHD / 16) + 2 * q);
-                if (key >= left) e4[i] = 0u;  // beyond the prefix: adds 0 whatever the slot holds
-              }
+            for (int k = 0; k < 4; ++k) {
+              const int chunk = 4 * (q & 1) + (k ^ flip);
+              *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = decode8(w[k], u2h(k < 2 ? ea : eb));
+            }
+          }
+        } else {
+          // 32 dims of a node's row (zeros where there is none), this lane's quarter
+          auto load_row = [&](const void* from, int i, uint4 (&y)[4]) {
+            const int key = dw * 32 + i * 8 + (lane >> 2), j = (x - p.NT) * kKeys + key;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int key = dw * 32 + i * 8 + (lane >> 2);
-                const uint32_t e = h2u(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(e4[i]), __NV_E4M3))));
-                uint32_t ea = __byte_perm(e, e, 0x1010), eb = __byte_perm(e, e, 0x3232);
-                uint32_t w[4] = {w4[i].x, w4[i].y, w4[i].z, w4[i].w};
-                // the four 16-byte pieces in an order that differs between the lanes which
-                // store together, so that their banks do
-                const int flip = ((q >> 1) & 1) | ((key & 1) << 1);
-                if (flip & 1) {
-                  const uint32_t a = w[0], b = w[2];
-                  w[0] = w[1], w[1] = a, w[2] = w[3], w[3] = b;
-                }
-                if (flip & 2) {
-                  uint32_t a = w[0], b = w[1];
-                  w[0] = w[2], w[1] = w[3], w[2] = a, w[3] = b;
-                  a = ea, ea = eb, eb = a;
-                }
-                unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const int chunk = 4 * (q & 1) + (k ^ flip);
-                  *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = decode8(w[k], u2h(k < 2 ? ea : eb));
-                }
-              }
-            } else {
-              // 32 dims of a node's row (zeros where there is none), this lane's quarter
-              auto load_row = [&](const void* from, int i, uint4 (&y)[4]) {
-                const int key = dw * 32 + i * 8 + (lane >> 2), j = (x - p.NT) * kKeys + key;
-#pragma unroll
-                for (int c = 0; c < 4; ++c) y[c] = make_uint4(0u, 0u, 0u, 0u);
-                if (key < left) {
-                  const int pi = j / tail.page_size;
-                  const int page = tail.page_table[static_cast<size_t>(p.b) * tail.max_pages + pi];
-                  if (page >= 0 && page < tail.n_pages) {
-                    const size_t row = (static_cast<size_t>(page) * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                      y[c] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(from) + row * kHD + 32 * q)[c];
-                  } else {
-                    dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
-                  }
-                }
-              };
-              // largest magnitude of the node's row as bf16 bits, the same in its four lanes
-              auto row_max = [&](const uint4 (&y)[4]) {
-                uint32_t am = 0u;
+            for (int c = 0; c < 4; ++c) y[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (key < left) {
+              const int pi = j / tail.page_size;
+              const int page = tail.page_table[static_cast<size_t>(p.b) * tail.max_pages + pi];
+              if (page >= 0 && page < tail.n_pages) {
+                const size_t row = (static_cast<size_t>(page) * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size);
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                  am = __vmaxu2(am, __vmaxu2(__vmaxu2(y[c].x & 0x7FFF7FFFu, y[c].y & 0x7FFF7FFFu),
-                                             __vmaxu2(y[c].z & 0x7FFF7FFFu, y[c].w & 0x7FFF7FFFu)));
-                am = max(am & 0xFFFFu, am >> 16);
-                am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-                return max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-              };
-              int vu = vu_exp - 40;  // (not so far below v_unit that O would overflow in it)
-              if (op == 0) {
-                // V's unit: the exponent of the tile's largest node without NaN or Inf.  Each
-                // warp leaves that of its nodes with its K
-                uint32_t top = 0u;
-#pragma unroll
-                for (int i0 = 0; i0 < 4; i0 += 2) {
-                  if (dw * 32 + i0 * 8 >= left) break;
-                  uint4 y[2][4];
-                  load_row(tail.v, i0, y[0]);
-                  load_row(tail.v, i0 + 1, y[1]);
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    const uint32_t am = row_max(y[h]);
-                    if (am < 0x7F80u) top = max(top, am);
-                  }
-                }
-                top = __reduce_max_sync(0xFFFFFFFFu, top);
-                if (lane == 0) s_ue[slot * 4 + dw] = max(static_cast<int>(top >> 7) - 127, vu);
+                  y[c] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(from) + row * kHD + 32 * q)[c];
               } else {
-                if (!bar_wait(&k_full[T & 1], (T >> 1) & 1, abort)) {  // every warp has left its own
-                  live = false;
-                  break;
-                }
-                __syncwarp();
-                vu = max(max(s_ue[slot * 4], s_ue[slot * 4 + 1]), max(s_ue[slot * 4 + 2], s_ue[slot * 4 + 3]));
+                dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
               }
-              uint32_t bad_v = 0u;  // this warp's keys with a non-finite V
-#pragma unroll 1
-              for (int i0 = 0; i0 < 4; i0 += 2) {
-                uint4 y[2][4];
-                load_row(op ? tail.v : tail.k, i0, y[0]);
-                load_row(op ? tail.v : tail.k, i0 + 1, y[1]);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const int key = dw * 32 + (i0 + h) * 8 + (lane >> 2);
-                  const uint32_t am = row_max(y[h]);
-                  const bool bad = am >= 0x7F80u;
-                  // a node with a NaN or an Inf leaves the product: its scores get a NaN
-                  // factor, rows that see its V are marked
-                  const int ex = op ? vu : max(static_cast<int>(am >> 7), 1) - 127;
-                  if (op == 0 && q == 0) s_fac[slot * kKeys + key] = bad ? __int_as_float(0x7FC00000) : pow2f(ex);
-                  if (bad) bad_v |= 1u << (key & 31);
-                  const int na = -ex / 2;
-                  const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
-                  const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
-                  unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
-#pragma unroll
-                  for (int c = 0; c < 4; ++c) {
-                    const uint32_t w[4] = {y[h][c].x, y[h][c].y, y[h][c].z, y[h][c].w};
-                    uint32_t hh[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                      const uint32_t z = bad ? 0u : w[k];
-                      hh[k] = h2u(__floats2half2_rn(__uint_as_float(z << 16) * f0 * f1, __uint_as_float(z & 0xFFFF0000u) * f0 * f1));
-                    }
-                    const int chunk = 4 * (q & 1) + c;
-                    *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
-                  }
-                }
-              }
-              bad_v = __reduce_or_sync(0xFFFFFFFFu, bad_v);
-              if (op == 1 && lane == 0) s_bad[slot * 4 + dw] = bad_v;
             }
-            fence_async_smem();  // generic-proxy writes -> tensor core
-            __syncwarp();
-            if (lane == 0) bar_arrive(full);
+          };
+          // largest magnitude of the node's row as bf16 bits, the same in its four lanes
+          auto row_max = [&](const uint4 (&y)[4]) {
+            uint32_t am = 0u;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              am = __vmaxu2(am, __vmaxu2(__vmaxu2(y[c].x & 0x7FFF7FFFu, y[c].y & 0x7FFF7FFFu),
+                                         __vmaxu2(y[c].z & 0x7FFF7FFFu, y[c].w & 0x7FFF7FFFu)));
+            am = max(am & 0xFFFFu, am >> 16);
+            am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+            return max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+          };
+          int vu = vu_exp - 40;  // (not so far below v_unit that O would overflow in it)
+          if (op == 0) {
+            // V's unit: the exponent of the tile's largest node without NaN or Inf.  Each
+            // warp leaves that of its nodes with its K
+            uint32_t top = 0u;
+#pragma unroll
+            for (int i0 = 0; i0 < 4; i0 += 2) {
+              if (dw * 32 + i0 * 8 >= left) break;
+              uint4 y[2][4];
+              load_row(tail.v, i0, y[0]);
+              load_row(tail.v, i0 + 1, y[1]);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t am = row_max(y[h]);
+                if (am < 0x7F80u) top = max(top, am);
+              }
+            }
+            top = __reduce_max_sync(0xFFFFFFFFu, top);
+            if (lane == 0) s_ue[slot * 4 + dw] = max(static_cast<int>(top >> 7) - 127, vu);
+          } else {
+            if (!warp_wait(&k_full[T & 1], (T >> 1) & 1, abort)) return false;  // every warp has left its own
+            vu = max(max(s_ue[slot * 4], s_ue[slot * 4 + 1]), max(s_ue[slot * 4 + 2], s_ue[slot * 4 + 3]));
           }
-          if (!live) break;
-          if (nodes) ++ntail;
-          __syncwarp();
-          if (lane == 0) bar_arrive(&raw_empty[st]);
+          uint32_t bad_v = 0u;  // this warp's keys with a non-finite V
+#pragma unroll 1
+          for (int i0 = 0; i0 < 4; i0 += 2) {
+            uint4 y[2][4];
+            load_row(op ? tail.v : tail.k, i0, y[0]);
+            load_row(op ? tail.v : tail.k, i0 + 1, y[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int key = dw * 32 + (i0 + h) * 8 + (lane >> 2);
+              const uint32_t am = row_max(y[h]);
+              const bool bad = am >= 0x7F80u;
+              // a node with a NaN or an Inf leaves the product: its scores get a NaN
+              // factor, rows that see its V are marked
+              const int ex = op ? vu : max(static_cast<int>(am >> 7), 1) - 127;
+              if (op == 0 && q == 0) s_fac[slot * kKeys + key] = bad ? __int_as_float(0x7FC00000) : pow2f(ex);
+              if (bad) bad_v |= 1u << (key & 31);
+              const int na = -ex / 2;
+              const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
+              const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
+              unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t w[4] = {y[h][c].x, y[h][c].y, y[h][c].z, y[h][c].w};
+                uint32_t hh[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t z = bad ? 0u : w[k];
+                  hh[k] = h2u(__floats2half2_rn(__uint_as_float(z << 16) * f0 * f1, __uint_as_float(z & 0xFFFF0000u) * f0 * f1));
+                }
+                const int chunk = 4 * (q & 1) + c;
+                *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+              }
+            }
+          }
+          bad_v = __reduce_or_sync(0xFFFFFFFFu, bad_v);
+          if (op == 1 && lane == 0) s_bad[slot * 4 + dw] = bad_v;
         }
-      } while (live && p.next(g, kv, kv_len));
+        fence_async_smem();  // generic-proxy writes -> tensor core
+        __syncwarp();
+        if (lane == 0) bar_arrive(op ? &v_full[dst_st] : &k_full[dst_st]);
+        return true;
+      };
+      Cursor k{first, first.x0, 0, 0, true}, v{first, first.x0, 0, 0, true};
+      bool live = convert(0, k);
+      advance(k);
+      while (live && v.on) {
+        if (k.on) {
+          if (!convert(0, k)) break;
+          advance(k);
+        }
+        if (!convert(1, v)) break;
+        __syncwarp();
+        if (lane == 0) bar_arrive(&raw_empty[v.T % kRaw]);
+        advance(v);
+      }
     }
   } else {
     regs_inc<kRegsSoftmax>();
@@ -656,7 +669,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           c2 = fmaxf(sm_scale * kLog2e * pow2f(ex), 1e-37f);
           if (RT == 2 || grp == 0) {
             // (RT = 1: the other group's products of the last part have read the shared Q)
-            if (RT == 1 && n_part > 0 && !bar_wait(q_free, (n_part - 1) & 1, abort)) live = false;
+            if (RT == 1 && n_part > 0 && !warp_wait(q_free, (n_part - 1) & 1, abort)) live = false;
             const int na = -ex / 2;
             const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
             const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
@@ -702,7 +715,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
               }
             }
           }
-          if (!bar_wait(&s_full[grp], n_job & 1, abort)) {
+          if (!warp_wait(&s_full[grp], n_job & 1, abort)) {
             live = false;
             break;
           }
@@ -715,30 +728,26 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           auto tile = [&](auto all) -> bool {
             constexpr bool ALL = decltype(all)::value;
             const float c = ALL ? c2p : c2;
-            float v[2][64];
-            auto factors = [&](int h) {  // scores of half h: factor and -Inf where unseen
-              const float* fac = s_fac + slot * kKeys + 64 * h;
+            float2 v[64];
+            tmem_ld128(tS, v);
+            if (!ALL) {  // factors, and -Inf where unseen
+              const float* fac = s_fac + slot * kKeys;
 #pragma unroll
-              for (int j = 0; j < 64; ++j) v[h][j] = ((see[h] >> j) & 1ull) ? v[h][j] * (nodes ? fac[j] : kv.k_unit) : -INFINITY;
-            };
-            auto most = [&](const float (&y)[64]) {
-              float a0 = fmax3f(y[0], y[1], y[2]), a1 = fmax3f(y[3], y[4], y[5]);
-              float a2 = fmax3f(y[6], y[7], y[8]), a3 = fmax3f(y[9], y[10], y[11]);
-#pragma unroll
-              for (int j = 12; j + 8 <= 60; j += 8) {
-                a0 = fmax3f(a0, y[j], y[j + 1]);
-                a1 = fmax3f(a1, y[j + 2], y[j + 3]);
-                a2 = fmax3f(a2, y[j + 4], y[j + 5]);
-                a3 = fmax3f(a3, y[j + 6], y[j + 7]);
+              for (int j = 0; j < 64; ++j) {
+                const uint64_t s2 = see[j >> 5] >> ((2 * j) & 63);
+                v[j].x = (s2 & 1ull) ? v[j].x * (nodes ? fac[2 * j] : kv.k_unit) : -INFINITY;
+                v[j].y = (s2 & 2ull) ? v[j].y * (nodes ? fac[2 * j + 1] : kv.k_unit) : -INFINITY;
               }
-              return fmax3f(fmax3f(a0, y[60], y[61]), fmax3f(a1, y[62], y[63]), fmaxf(a2, a3));
-            };
-            tmem_ld64(tS, v[0]);
-            if (!ALL) factors(0);
-            float tmax = most(v[0]);
-            tmem_ld64(tS + 64, v[1]);
-            if (!ALL) factors(1);
-            tmax = fmaxf(tmax, most(v[1])) * c;
+            }
+            float a0 = fmaxf(v[0].x, v[0].y), a1 = fmaxf(v[1].x, v[1].y), a2 = fmaxf(v[2].x, v[2].y), a3 = fmaxf(v[3].x, v[3].y);
+#pragma unroll
+            for (int j = 4; j < 64; j += 4) {
+              a0 = fmax3f(a0, v[j].x, v[j].y);
+              a1 = fmax3f(a1, v[j + 1].x, v[j + 1].y);
+              a2 = fmax3f(a2, v[j + 2].x, v[j + 2].y);
+              a3 = fmax3f(a3, v[j + 3].x, v[j + 3].y);
+            }
+            const float tmax = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * c;
             // the base moves when passed by more than 2^15; O's unit when the tile's V has another
             const bool move = tmax > m + kTop;
             const bool unit = tile_ue != ue && mine > 0;
@@ -757,25 +766,26 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
             const float2 nv = make_float2(-sub, -sub);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {  // P of half h goes over columns [32 h, 32 h + 32): scores already read
-              uint32_t pk[32];
+            for (int h = 0; h < 4; ++h) {  // P of 32 keys goes over 16 columns: the scores are in registers
+              uint32_t pk[16];
 #pragma unroll
-              for (int j = 0; j < 64; j += 2) {
-                const float2 a = __ffma2_rn(make_float2(v[h][j], v[h][j + 1]), cv, nv);
-                float e0 = ex2(a.x), e1 = ex2(a.y);
+              for (int j = 0; j < 16; ++j) {
+                const float2 a = __ffma2_rn(v[16 * h + j], cv, nv);
+                float2 e = make_float2(ex2(a.x), ex2(a.y));
                 if (!ALL) {
-                  e0 = ((see[h] >> j) & 1ull) ? e0 : 0.0f;
-                  e1 = ((see[h] >> (j + 1)) & 1ull) ? e1 : 0.0f;
+                  const uint64_t s2 = see[h >> 1] >> ((32 * h + 2 * j) & 63);
+                  e.x = (s2 & 1ull) ? e.x : 0.0f;
+                  e.y = (s2 & 2ull) ? e.y : 0.0f;
                 }
-                sum[(j >> 1) & 1] = __fadd2_rn(sum[(j >> 1) & 1], make_float2(e0, e1));
-                pk[j >> 1] = h2u(__floats2half2_rn(e0, e1));
+                sum[j & 1] = __fadd2_rn(sum[j & 1], e);
+                pk[j] = h2u(__float22half2_rn(e));
               }
-              tmem_st32(tS + 32 * h, pk);
+              tmem_st16(tS + 16 * h, pk);
             }
             const float2 st = __fadd2_rn(sum[0], sum[1]);
             l += st.x + st.y;
             if (rescale) {
-              if (!bar_wait(&o_done[grp], (n_job - 1) & 1, abort)) return false;
+              if (!warp_wait(&o_done[grp], (n_job - 1) & 1, abort)) return false;
               __syncwarp();
               fence_after();
 #pragma unroll 1
@@ -785,6 +795,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
 #pragma unroll
                 for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
                 tmem_st16(tO + 16 * h, y);
+                tmem_st_wait();
               }
             }
             tmem_st_wait();
@@ -807,7 +818,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         }
         // the part's record: o normalized by its own sum, the base and the sum
         if (mine > 0) {
-          if (!bar_wait(&o_done[grp], (n_job - 1) & 1, abort)) {
+          if (!warp_wait(&o_done[grp], (n_job - 1) & 1, abort)) {
             live = false;
             break;
           }

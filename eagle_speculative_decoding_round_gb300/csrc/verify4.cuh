@@ -112,7 +112,8 @@ verify4_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __r
   pdl_wait();
   pdl_trigger();
   const int P = kv_len[b], c0 = ends[2 * pair], c1 = ends[2 * pair + 1];
-  if (pair_units<KEYS>(g, kv, P) == 0) return;
+  // (a worker that gave up, its error word set, may not have left its number)
+  if (pair_units<KEYS>(g, kv, P) == 0 || c0 < 0 || c1 < c0 || c1 >= g.workers) return;
   const int n = (c1 - c0 + 1) * SPLIT;
   const size_t base = (pair + c0) * SPLIT * ROWS + (r - rt * ROWS);  // then ROWS apart
   using Vec = typename std::conditional<PER == 4, float4, float2>::type;
