@@ -4,7 +4,7 @@
 // Work is cut as in verify4.cuh: a pair is (request, KV head, tile of RT * 128 query rows),
 // its units are tiles of 128 prefix keys and then of 128 tree nodes; one CTA per SM takes
 // an equal share of all units.  A tile goes through the CTA like this:
-//   producer (warp 0)      the tile's codes and scales by bulk copies into a ring
+//   producers (warps 0, 3) the tile's codes and scales by bulk copies into rings, K and V
 //   dequantizers (4 warps) codes -> fp16 operands in 128-byte-swizzled shared memory: a
 //                          value c * e is exact in fp16 (see k_verify4.cu).  Tree nodes are
 //                          read from the bf16 tail and scaled by powers of two instead
@@ -43,10 +43,9 @@ constexpr int kHalfB = 16384;            // bytes of a 64-dim half of an operand
 constexpr int kOpB = 2 * kHalfB;         // bytes of an operand
 constexpr int kCodeB = kKeys * kHD / 2;  // bytes of a tile's codes, per operand
 constexpr int kScaleB = kKeys * kHD / 16;
-constexpr int kRawB = 2 * (kCodeB + kScaleB);
-constexpr int kRaw = 3;                  // raw stages
+constexpr int kRawB = kCodeB + kScaleB;  // of one operand
 constexpr int kTailRing = 8;             // tiles of tree nodes whose factors are kept (at most five are in flight)
-// Warpgroups: 0 = producer and the MMA issuers (and an idle warp), 1 and 2 = softmax, 3 =
+// Warpgroups: 0 = producers and MMA issuers, 1 and 2 = softmax, 3 =
 // dequantizers.  Registers move from the first and the last to the softmax groups, whose
 // threads hold a row of scores each; launch_tc checks that the launch brings the sum.
 constexpr int kThreads = 512;
@@ -56,9 +55,9 @@ constexpr unsigned long long kWaitNs = 1000000000ull;
 
 template <int RT>
 struct Cfg {
-  static constexpr int NV = RT == 2 ? 1 : 2;  // V stages
-  static constexpr int Q = 0, K = RT * kOpB, V = K + 2 * kOpB, RAW = V + NV * kOpB, FAC = RAW + kRaw * kRawB;
-  static constexpr int BARS = FAC + kTailRing * kKeys * 4, END = BARS + 640;
+  static constexpr int RK = RT == 2 ? 2 : 3, RV = RT == 2 ? 1 : 3;  // raw stages of K and V
+  static constexpr int Q = 0, K = RT * kOpB, V = K + 2 * kOpB, RAW = V + 2 * kOpB, FAC = RAW + (RK + RV) * kRawB;
+  static constexpr int BARS = FAC + kTailRing * kKeys * 4, END = BARS + 768;
   static constexpr int SMEM = END + 1024;  // (base rounded up to 1024)
 };
 static_assert(Cfg<1>::SMEM <= 232448 && Cfg<2>::SMEM <= 232448, "shared memory of a CTA");
@@ -264,25 +263,24 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
                   const uint64_t* __restrict__ mask, const __grid_constant__ V4Geom g, float sm_scale,
                   float* __restrict__ ws_o, float2* __restrict__ ws_ml, int32_t* __restrict__ ends, int32_t* dev_err) {
   using C = Cfg<RT>;
-  constexpr int NV = C::NV;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V, *sRaw = sm + C::RAW;
   float* s_fac = reinterpret_cast<float*>(sm + C::FAC);  // [kTailRing][128] factor of each tree node's scores
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BARS);
-  uint64_t* raw_full = bars;        // [kRaw]
-  uint64_t* raw_empty = bars + 3;   // [kRaw]
-  uint64_t* k_full = bars + 6;      // [2]
-  uint64_t* k_empty = bars + 8;     // [2]
-  uint64_t* v_full = bars + 10;     // [NV]
-  uint64_t* v_empty = bars + 12;    // [NV]
-  uint64_t* s_full = bars + 14;     // [2] by softmax group, as the following
-  uint64_t* p_full = bars + 16;
-  uint64_t* o_done = bars + 18;
-  uint64_t* q_full = bars + 20;
-  uint64_t* q_free = bars + 22;     // (RT = 1) both groups are done with the shared Q
-  uint64_t* go = bars + 23;         // (RT = 2) the second group may start a part
-  int* s_ue = reinterpret_cast<int*>(bars + 24);                        // [kTailRing][4] exponent of V's unit in a tile of nodes, by dequantizer warp
+  uint64_t* raw_full = bars;        // [K, V][3]
+  uint64_t* raw_empty = bars + 6;   // [K, V][3]
+  uint64_t* k_full = bars + 12;     // [2]
+  uint64_t* k_empty = bars + 14;    // [2]
+  uint64_t* v_full = bars + 16;     // [2]
+  uint64_t* v_empty = bars + 18;    // [2]
+  uint64_t* s_full = bars + 20;     // [2] by softmax group, as the following
+  uint64_t* p_full = bars + 22;
+  uint64_t* o_done = bars + 24;
+  uint64_t* q_full = bars + 26;
+  uint64_t* q_free = bars + 28;     // (RT = 1) both groups are done with the shared Q
+  uint64_t* go = bars + 29;         // (RT = 2) the second group may start a part
+  int* s_ue = reinterpret_cast<int*>(bars + 30);                        // [kTailRing][4] exponent of V's unit in a tile of nodes, by dequantizer warp
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_ue + 4 * kTailRing);  // [kTailRing][4] nodes with a non-finite V
   uint32_t* tmem_slot = s_bad + 4 * kTailRing;
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -290,7 +288,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRaw; ++i) {
+    for (int i = 0; i < 6; ++i) {
       bar_init(&raw_full[i], 1);
       bar_init(&raw_empty[i], 4);
     }
@@ -338,59 +336,60 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   // TMEM columns: S (and P) of group w at 128 w, O of group w at 256 + 128 w
   const int Qn = g.KVH * g.RG;
   const int vu_exp = static_cast<int>(__float_as_uint(kv.v_unit) >> 23) - 127;
-  int T_raw = 0;  // (producer) tiles issued
+  int T_raw = 0;  // (producers) tiles issued
 
   if (warp < kSoftmax0) {
     regs_dec<kRegsIssue>();
-    if (warp == 0 && work) {
+    if ((warp == 0 || warp == 3) && work) {
+      const int op = warp == 0 ? 0 : 1, stages = op ? C::RV : C::RK;  // warp 0 brings K, warp 3 V
+      const unsigned char* codes = static_cast<const unsigned char*>(op ? kv.v : kv.k);
+      const unsigned char* scales = static_cast<const unsigned char*>(op ? kv.v_scale : kv.k_scale);
+      unsigned char* ring = sRaw + (op ? C::RK * kRawB : 0);
       Parts p = first;
       bool live = true;
+      int st = 0;
+      uint32_t par = 1u;  // parity of the stages' last release (a fresh barrier counts as released)
       do {
         const int kvh = p.pq / g.RG;
         for (int x = p.x0; live && x < p.x1; ++x) {
-          const int st = T_raw % kRaw;
-          if (!warp_wait(&raw_empty[st], ((T_raw / kRaw) & 1) ^ 1, abort)) {
+          uint64_t* full = &raw_full[3 * op + st];
+          if (!warp_wait(&raw_empty[3 * op + st], par, abort)) {
             live = false;
             break;
           }
-          __syncwarp();
           ++T_raw;
           if (x < p.NT) {
-            // runs of keys within a page, lane / 4 = run, lane % 4 = what (K, V, their scales)
+            // granules of 16 keys form runs within a page: lane / 2 is the granule, a lane
+            // whose granule begins a run copies the run's codes (even) or scales (odd)
             const int t0 = x * kKeys, keys = min(kKeys, (p.P - t0 + 15) & ~15);
+            const int gr = lane >> 1, what = lane & 1;
             uint32_t bytes = 0;
-            unsigned char* base = sRaw + st * kRawB;
-            // up to eight 16-key granules form runs: each lane finds the run that starts at its granule
-            const int gr = lane >> 2, what = lane & 3;
-            const int t = t0 + 16 * gr;
-            int run = 0;
             const unsigned char* src = nullptr;
             if (16 * gr < keys) {
-              const int pi = t / kv.page_size, slot = t - pi * kv.page_size;
+              const int t = t0 + 16 * gr, pi = t / kv.page_size, slot = t - pi * kv.page_size;
               if (gr == 0 || slot == 0) {
-                run = min(keys - 16 * gr, kv.page_size - slot);
+                const int run = min(keys - 16 * gr, kv.page_size - slot);
                 const int page = kv.page_table[static_cast<size_t>(p.b) * kv.max_pages + pi];
                 if (page < 0 || page >= kv.n_pages) {
                   dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
-                  run = 0;
                 } else {
                   const size_t row = (static_cast<size_t>(page) * g.KVH + kvh) * kv.page_size + slot;
-                  const void* from = what == 0 ? kv.k : what == 1 ? kv.v : what == 2 ? kv.k_scale : kv.v_scale;
-                  src = static_cast<const unsigned char*>(from) + row * (what < 2 ? kHD / 2 : kHD / 16);
+                  src = what ? scales + row * (kHD / 16) : codes + row * (kHD / 2);
+                  bytes = static_cast<uint32_t>(run) * (what ? kHD / 16 : kHD / 2);
                 }
               }
             }
-            bytes = static_cast<uint32_t>(run) * (what < 2 ? kHD / 2 : kHD / 16);
             const uint32_t total = __reduce_add_sync(0xFFFFFFFFu, bytes);
-            if (lane == 0) bar_expect(&raw_full[st], total);
+            if (lane == 0) bar_expect(full, total);
             __syncwarp();
-            if (bytes) {
-              const int at_b = what == 0 ? 16 * gr * (kHD / 2) : what == 1 ? kCodeB + 16 * gr * (kHD / 2)
-                               : 2 * kCodeB + (what == 3 ? kScaleB : 0) + 16 * gr * (kHD / 16);
-              bulk_copy(su32(base + at_b), src, bytes, &raw_full[st]);
-            }
+            if (bytes)
+              bulk_copy(su32(ring + st * kRawB + (what ? kCodeB + 16 * gr * (kHD / 16) : 16 * gr * (kHD / 2))), src, bytes, full);
           } else {
-            if (lane == 0) bar_arrive(&raw_full[st]);  // tree nodes: read by the dequantizers
+            if (lane == 0) bar_arrive(full);  // tree nodes: read by the dequantizers
+          }
+          if (++st == stages) {
+            st = 0;
+            par ^= 1u;
           }
         }
       } while (live && p.next(g, kv, kv_len));
@@ -421,12 +420,12 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         // the second group starts half a turn later, so that one group's exponentials run
         // beside the other's products (started together they stay together): at the first
         // group's first P of the part.  That group cannot be a part ahead, since the V
-        // stage waits for both
+        // stages wait for both and the part has more tiles
         const bool stagger = RT == 2 && tiles >= 4;
         if (stagger && w == 1) live = live && bar_wait(go, n_go & 1, abort);
         uint32_t acc0 = 0u;  // the first job of a part starts O
         for (; live && t < end; t += RT == 1 ? 2 : 1) {
-          const uint32_t ks = t & 1, vs = NV == 2 ? t & 1 : 0;
+          const uint32_t ks = t & 1, vs = t & 1;
           const uint64_t kd = k_desc0 + static_cast<uint64_t>(ks * (kOpB >> 4)), vd = v_desc0 + static_cast<uint64_t>(vs * (kOpB >> 4));
           if (!bar_wait(&k_full[ks], (t >> 1) & 1, abort)) live = false;
           if (n > 0 && !bar_wait(od, (n - 1) & 1, abort)) live = false;  // P of the last job, under S, has been read
@@ -440,7 +439,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           }
           umma_commit(sf);
           umma_commit(&k_empty[ks]);
-          if (!bar_wait(&v_full[vs], (NV == 2 ? t >> 1 : t) & 1, abort) || !bar_wait(pf, n & 1, abort)) {
+          if (!bar_wait(&v_full[vs], (t >> 1) & 1, abort) || !bar_wait(pf, n & 1, abort)) {
             live = false;
             break;
           }
@@ -479,18 +478,18 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       };
       auto convert = [&](const int op, const Cursor& cur) -> bool {
         const Parts& p = cur.p;
-        const int x = cur.x, T = cur.T, st = T % kRaw, slot = cur.ntail % kTailRing;
+        const int x = cur.x, T = cur.T, slot = cur.ntail % kTailRing;
+        const int st = op ? T % C::RV : T % C::RK;
         const int kvh = p.pq / g.RG;
-        if (op == 0 && !warp_wait(&raw_full[st], (T / kRaw) & 1, abort)) return false;
-        const int dst_st = op ? T % NV : T & 1;
-        if (!warp_wait(op ? &v_empty[dst_st] : &k_empty[dst_st], (op ? ((T / NV) & 1) : ((T >> 1) & 1)) ^ 1, abort)) return false;
-        const unsigned char* raw = sRaw + st * kRawB;
+        if (!warp_wait(&raw_full[3 * op + st], (op ? T / C::RV : T / C::RK) & 1, abort)) return false;
+        const int dst_st = T & 1;
+        if (!warp_wait(op ? &v_empty[dst_st] : &k_empty[dst_st], ((T >> 1) & 1) ^ 1, abort)) return false;
+        const unsigned char* raw = sRaw + (op ? C::RK + st : st) * kRawB;
         const bool nodes = x >= p.NT;
         const int left = nodes ? g.R - (x - p.NT) * kKeys : p.P - x * kKeys;  // keys that exist
         unsigned char* dst = (op ? sV : sK) + dst_st * kOpB;
         if (!nodes) {
-          const unsigned char* codes = raw + op * kCodeB;
-          const unsigned char* scales = raw + 2 * kCodeB + op * kScaleB;
+          const unsigned char *codes = raw, *scales = raw + kCodeB;
           uint4 w4[4];
           uint32_t e4[4];
 #pragma unroll
@@ -617,7 +616,10 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         }
         fence_async_smem();  // generic-proxy writes -> tensor core
         __syncwarp();
-        if (lane == 0) bar_arrive(op ? &v_full[dst_st] : &k_full[dst_st]);
+        if (lane == 0) {
+          bar_arrive(op ? &v_full[dst_st] : &k_full[dst_st]);
+          bar_arrive(&raw_empty[3 * op + st]);
+        }
         return true;
       };
       Cursor k{first, first.x0, 0, 0, true}, v{first, first.x0, 0, 0, true};
@@ -629,8 +631,6 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           advance(k);
         }
         if (!convert(1, v)) break;
-        __syncwarp();
-        if (lane == 0) bar_arrive(&raw_empty[v.T % kRaw]);
         advance(v);
       }
     }
@@ -870,10 +870,11 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   if (__syncthreads_or(*abort != 0)) {
     // after a wait that ran out, the copies still in flight land (bounded) before the
     // shared memory goes
-    if (warp == 0) {
+    if (warp == 0 || warp == 3) {
       const uint64_t t0 = gtimer();
-      for (int t = max(0, T_raw - kRaw); t < T_raw; ++t)
-        while (!bar_try(&raw_full[t % kRaw], (t / kRaw) & 1) && gtimer() - t0 < kWaitNs) {
+      const int op = warp == 0 ? 0 : 1, stages = op ? C::RV : C::RK;
+      for (int t = max(0, T_raw - stages); t < T_raw; ++t)
+        while (!bar_try(&raw_full[3 * op + t % stages], (t / stages) & 1) && gtimer() - t0 < kWaitNs) {
         }
       if (lane == 0) dev_flag(dev_err, E3_DEV_ERR_TIMEOUT);
     }
