@@ -9,17 +9,18 @@
 //                          value c * e is exact in fp16 (see k_verify4.cu).  Tree nodes are
 //                          read from the bf16 tail and scaled by powers of two instead
 //                          (per key for K, per tile for V), which keeps their bits
-//   S = Q K^T              (warps 1 and 2, one per softmax group) tcgen05.mma kind::f16, M = 128 rows, N = 128 keys, into the S
-//                          buffer of the row's softmax group
+//   S = Q K^T              (warps 1 and 2, one per softmax group) tcgen05.mma kind::f16, M =
+//                          128 rows, N = 64 keys, into one of the group's two S buffers
 //   softmax (2 x 4 warps)  one thread per row: maximum, exponentials, P (fp16) over S
 //   O += P V               A = P from TMEM, V in place as an MN-major operand; O stays in
 //                          TMEM, rescaled only when a base moves by more than 2^15
-// The two softmax groups alternate, so that one's exponentials run while the tensor core
-// works for the other.  RT = 2: a group per 128 rows, both use every tile, which is
+// A group's next scores are there when it has written its last P: S of a step runs under
+// the exponentials of the step before it, and the two groups fill each other's gaps.  RT = 2: a group per 128 rows, both use every tile, which is
 // dequantized once for 256 rows.  RT = 1 (at most 128 rows): the groups take the tiles in
 // turn, each with an O of its own, and leave two records per part.
 // Bound: shared-memory bandwidth.  Per 128 keys and SM in 128-byte cycles (RT = 2): raw
-// tile in and out 288, operands written 512, Q and K read by S 2 x 512, V by O 2 x 256.
+// tile in and out 288, operands written 512, Q and K read by S 2 x 768, V by O 2 x 256;
+// its tensor core needs 2048 cycles for them.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
@@ -38,6 +39,7 @@ namespace {
 
 constexpr int kRows = 128;   // query rows of a softmax group
 constexpr int kKeys = 128;   // keys of a tile
+constexpr int kStep = 64;    // keys of a step
 constexpr int kHD = 128;
 constexpr int kHalfB = 16384;            // bytes of a 64-dim half of an operand: [128 rows][128 B]
 constexpr int kOpB = 2 * kHalfB;         // bytes of an operand
@@ -116,9 +118,9 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
          (static_cast<uint64_t>(2) << 61);
 }
-// kind::f16 instruction descriptor: f16 x f16 -> f32, M = N = 128, the second operand's major.
-__host__ __device__ constexpr uint32_t idesc_f16(int b_mn) {
-  return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(128 >> 3) << 17) |
+// kind::f16 instruction descriptor: f16 x f16 -> f32, M = 128, N, the second operand's major.
+__host__ __device__ constexpr uint32_t idesc_f16(int N, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(128 >> 4) << 24);
 }
 __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
@@ -146,35 +148,29 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
 }
 #undef E3_R8
 __device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// 128 columns of this thread's lane as register pairs (so that the packed arithmetic needs
-// no moves): four loads in flight, one wait
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float2 (&v)[64]) {
-  unsigned long long q[64];
+// 64 columns of this thread's lane as register pairs (so that the packed arithmetic needs
+// no moves), one load and its wait
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float2 (&v)[32]) {
+  unsigned long long q[32];
 #define E3_Q4(o) "=l"(q[o]), "=l"(q[o + 1]), "=l"(q[o + 2]), "=l"(q[o + 3])
 #define E3_M(i, a, b) " mov.b64 %" #i ", {t" #a ", t" #b "};\n"
   asm volatile(
-      "{\n .reg .b32 t<128>;\n"
-      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31}, [%64];\n"
-      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {t32,t33,t34,t35,t36,t37,t38,t39,t40,t41,t42,t43,t44,t45,t46,t47,t48,t49,t50,t51,t52,t53,t54,t55,t56,t57,t58,t59,t60,t61,t62,t63}, [%65];\n"
-      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {t64,t65,t66,t67,t68,t69,t70,t71,t72,t73,t74,t75,t76,t77,t78,t79,t80,t81,t82,t83,t84,t85,t86,t87,t88,t89,t90,t91,t92,t93,t94,t95}, [%66];\n"
-      " tcgen05.ld.sync.aligned.32x32b.x32.b32 {t96,t97,t98,t99,t100,t101,t102,t103,t104,t105,t106,t107,t108,t109,t110,t111,t112,t113,t114,t115,t116,t117,t118,t119,t120,t121,t122,t123,t124,t125,t126,t127}, [%67];\n"
+      "{\n .reg .b32 t<64>;\n"
+      " tcgen05.ld.sync.aligned.32x32b.x64.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31,t3"
+      "2,t33,t34,t35,t36,t37,t38,t39,t40,t41,t42,t43,t44,t45,t46,t47,t48,t49,t50,t51,t52,t53,t54,t55,t56,t57,t58,t59,t60,t61,t62,t63}, [%32];\n"
       " tcgen05.wait::ld.sync.aligned;\n"
       E3_M(0, 0, 1) E3_M(1, 2, 3) E3_M(2, 4, 5) E3_M(3, 6, 7) E3_M(4, 8, 9) E3_M(5, 10, 11) E3_M(6, 12, 13) E3_M(7, 14, 15)
        E3_M(8, 16, 17) E3_M(9, 18, 19) E3_M(10, 20, 21) E3_M(11, 22, 23) E3_M(12, 24, 25) E3_M(13, 26, 27) E3_M(14, 28, 29) E3_M(15, 30, 31)
        E3_M(16, 32, 33) E3_M(17, 34, 35) E3_M(18, 36, 37) E3_M(19, 38, 39) E3_M(20, 40, 41) E3_M(21, 42, 43) E3_M(22, 44, 45) E3_M(23, 46, 47)
        E3_M(24, 48, 49) E3_M(25, 50, 51) E3_M(26, 52, 53) E3_M(27, 54, 55) E3_M(28, 56, 57) E3_M(29, 58, 59) E3_M(30, 60, 61) E3_M(31, 62, 63)
-       E3_M(32, 64, 65) E3_M(33, 66, 67) E3_M(34, 68, 69) E3_M(35, 70, 71) E3_M(36, 72, 73) E3_M(37, 74, 75) E3_M(38, 76, 77) E3_M(39, 78, 79)
-       E3_M(40, 80, 81) E3_M(41, 82, 83) E3_M(42, 84, 85) E3_M(43, 86, 87) E3_M(44, 88, 89) E3_M(45, 90, 91) E3_M(46, 92, 93) E3_M(47, 94, 95)
-       E3_M(48, 96, 97) E3_M(49, 98, 99) E3_M(50, 100, 101) E3_M(51, 102, 103) E3_M(52, 104, 105) E3_M(53, 106, 107) E3_M(54, 108, 109) E3_M(55, 110, 111)
-       E3_M(56, 112, 113) E3_M(57, 114, 115) E3_M(58, 116, 117) E3_M(59, 118, 119) E3_M(60, 120, 121) E3_M(61, 122, 123) E3_M(62, 124, 125) E3_M(63, 126, 127)
       "}\n"
-      : E3_Q4(0), E3_Q4(4), E3_Q4(8), E3_Q4(12), E3_Q4(16), E3_Q4(20), E3_Q4(24), E3_Q4(28), E3_Q4(32), E3_Q4(36), E3_Q4(40), E3_Q4(44), E3_Q4(48), E3_Q4(52), E3_Q4(56), E3_Q4(60)
-      : "r"(taddr), "r"(taddr + 32), "r"(taddr + 64), "r"(taddr + 96)
+      : E3_Q4(0), E3_Q4(4), E3_Q4(8), E3_Q4(12), E3_Q4(16), E3_Q4(20), E3_Q4(24), E3_Q4(28)
+      : "r"(taddr)
       : "memory");
 #undef E3_Q4
 #undef E3_M
 #pragma unroll
-  for (int i = 0; i < 64; ++i)
+  for (int i = 0; i < 32; ++i)
     v[i] = make_float2(__uint_as_float(static_cast<uint32_t>(q[i])), __uint_as_float(static_cast<uint32_t>(q[i] >> 32)));
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -224,7 +220,8 @@ struct Parts {
     x1 = static_cast<int>(min(static_cast<long long>(units), x0 + todo));
     NT = (P + kKeys - 1) / kKeys;
   }
-  __device__ __forceinline__ int tiles() const { return x1 - x0; }
+  // keys of tile x that exist (more than 128 where it is not the last of its kind)
+  __device__ __forceinline__ int left(const V4Geom& g, int x) const { return x >= NT ? g.R - (x - NT) * kKeys : P - x * kKeys; }
   // the next part; false at the end of the share
   __device__ __forceinline__ bool next(const V4Geom& g, const e3_kv4_layer& kv, const int32_t* kv_len) {
     todo -= x1 - x0;
@@ -274,13 +271,13 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   uint64_t* k_empty = bars + 14;    // [2]
   uint64_t* v_full = bars + 16;     // [2]
   uint64_t* v_empty = bars + 18;    // [2]
-  uint64_t* s_full = bars + 20;     // [2] by softmax group, as the following
-  uint64_t* p_full = bars + 22;
-  uint64_t* o_done = bars + 24;
-  uint64_t* q_full = bars + 26;
-  uint64_t* q_free = bars + 28;     // (RT = 1) both groups are done with the shared Q
-  uint64_t* go = bars + 29;         // (RT = 2) the second group may start a part
-  int* s_ue = reinterpret_cast<int*>(bars + 30);                        // [kTailRing][4] exponent of V's unit in a tile of nodes, by dequantizer warp
+  uint64_t* s_full = bars + 20;     // [softmax group][2 buffers], as p_full
+  uint64_t* p_full = bars + 24;
+  uint64_t* o_done = bars + 28;     // [softmax group], as q_full
+  uint64_t* q_full = bars + 30;
+  uint64_t* o_last = bars + 32;     // [softmax group] the last O product of a part
+  uint64_t* q_free = bars + 34;     // (RT = 1) both groups are done with the shared Q
+  int* s_ue = reinterpret_cast<int*>(bars + 36);                        // [kTailRing][4] exponent of V's unit in a tile of nodes, by dequantizer warp
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_ue + 4 * kTailRing);  // [kTailRing][4] nodes with a non-finite V
   uint32_t* tmem_slot = s_bad + 4 * kTailRing;
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -297,13 +294,15 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       bar_init(&k_empty[i], RT);  // one commit per group that uses the tile
       bar_init(&v_full[i], 4);
       bar_init(&v_empty[i], RT);
-      bar_init(&s_full[i], 1);
-      bar_init(&p_full[i], 4);
+      bar_init(&s_full[2 * i], 1);
+      bar_init(&s_full[2 * i + 1], 1);
+      bar_init(&p_full[2 * i], 4);
+      bar_init(&p_full[2 * i + 1], 4);
       bar_init(&o_done[i], 1);
+      bar_init(&o_last[i], 1);
       bar_init(&q_full[i], 4);
     }
     bar_init(q_free, 8);
-    bar_init(go, 1);
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -394,68 +393,104 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         }
       } while (live && p.next(g, kv, kv_len));
     }
-    // one issuing thread per softmax group: neither group's products wait behind the other
-    // group's barriers
+    // One issuing thread per softmax group: neither group's products wait behind the other
+    // group's barriers.  S runs a step (64 keys) ahead of O within a part.
     if ((warp == 1 || warp == 2) && lane == 0 && work) {
-      constexpr uint32_t idS = idesc_f16(0), idO = idesc_f16(1);
+      constexpr uint32_t idS = idesc_f16(kStep, 0), idO = idesc_f16(kHD, 1);
       const int w = warp - 1;
       const uint64_t q_desc = desc_sw128(su32(sQ) + (RT == 2 ? w : 0) * kOpB, 16, 1024);
-      const uint64_t k_desc0 = desc_sw128(su32(sK), 16, 1024);
-      const uint64_t v_desc0 = desc_sw128(su32(sV), kHalfB, 1024);
+      const uint64_t k_desc = desc_sw128(su32(sK), 16, 1024);
+      const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
       const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
-      uint64_t* const sf = &s_full[w];
-      uint64_t* const pf = &p_full[w];
-      uint64_t* const od = &o_done[w];
-      uint64_t* const qf = &q_full[RT == 1 ? 0 : w];
-      Parts p = first;
-      uint32_t T = 0, n = 0, part = 0, n_go = 0;  // tiles, this group's jobs, parts, staggered parts
-      bool live = true;
-      do {
-        const uint32_t tiles = static_cast<uint32_t>(p.tiles());
-        // the group's first tile of the part, then every tile (RT = 2) or every second
-        uint32_t t = T + (RT == 1 ? w : 0);
-        const uint32_t end = T + tiles;
-        T = end;
-        if (t < end) live = bar_wait(qf, part & 1, abort);
-        // the second group starts half a turn later, so that one group's exponentials run
-        // beside the other's products (started together they stay together): at the first
-        // group's first P of the part.  That group cannot be a part ahead, since the V
-        // stages wait for both and the part has more tiles
-        const bool stagger = RT == 2 && tiles >= 4;
-        if (stagger && w == 1) live = live && bar_wait(go, n_go & 1, abort);
-        uint32_t acc0 = 0u;  // the first job of a part starts O
-        for (; live && t < end; t += RT == 1 ? 2 : 1) {
-          const uint32_t ks = t & 1, vs = t & 1;
-          const uint64_t kd = k_desc0 + static_cast<uint64_t>(ks * (kOpB >> 4)), vd = v_desc0 + static_cast<uint64_t>(vs * (kOpB >> 4));
-          if (!bar_wait(&k_full[ks], (t >> 1) & 1, abort)) live = false;
-          if (n > 0 && !bar_wait(od, (n - 1) & 1, abort)) live = false;  // P of the last job, under S, has been read
-          if (!live) break;
-          fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kHD / 16; ++kk) {
-            constexpr uint64_t kStep = 32 >> 4;
-            const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kHalfB >> 4)) + (kk & 3) * kStep;
-            umma(tS, q_desc + off, kd + off, idS, kk > 0 ? 1u : 0u);
-          }
-          umma_commit(sf);
-          umma_commit(&k_empty[ks]);
-          if (!bar_wait(&v_full[vs], (t >> 1) & 1, abort) || !bar_wait(pf, n & 1, abort)) {
-            live = false;
-            break;
-          }
-          if (stagger && w == 0 && acc0 == 0u) bar_arrive(go);
-          fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            umma_ts(tO, tS + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), idO, kk > 0 ? 1u : acc0);
-          umma_commit(od);
-          umma_commit(&v_empty[vs]);
-          ++n;
-          acc0 = 1u;
+      struct Cursor {
+        Parts p;
+        int x;              // tile of the pair
+        uint32_t t;         // tile of the CTA
+        uint32_t n, part;   // steps of the group before this one, parts before this one
+        bool half, fresh;   // second half of the tile; first step of the part
+        bool on;
+      };
+      // the group's first tile at or after the part's start (RT = 1: it may have none)
+      auto enter = [&](Cursor& c) {
+        c.fresh = true;
+        c.half = false;
+        for (;;) {
+          c.x = c.p.x0;
+          if (RT == 1 && w == 1) ++c.x, ++c.t;
+          if (c.x < c.p.x1) return;
+          c.t -= static_cast<uint32_t>(c.x - c.p.x1);
+          c.on = c.p.next(g, kv, kv_len);
+          ++c.part;
+          if (!c.on) return;
         }
-        ++part;
-        if (stagger) ++n_go;
-      } while (live && p.next(g, kv, kv_len));
+      };
+      auto last_half = [&](const Cursor& c) { return c.half || c.p.left(g, c.x) <= kStep; };
+      auto advance = [&](Cursor& c) {
+        ++c.n;
+        c.fresh = false;
+        if (!last_half(c)) {
+          c.half = true;
+          return;
+        }
+        c.half = false;
+        c.x += RT == 1 ? 2 : 1;
+        c.t += RT == 1 ? 2 : 1;
+        if (c.x >= c.p.x1) {
+          c.t -= static_cast<uint32_t>(c.x - c.p.x1);
+          c.on = c.p.next(g, kv, kv_len);
+          ++c.part;
+          if (c.on) enter(c);
+        }
+      };
+      Cursor s{first, 0, 0u, 0u, 0u, false, true, true};
+      enter(s);
+      Cursor o = s;
+      bool live = true;
+      auto issue_S = [&]() {
+        const uint32_t ks = s.t & 1, buf = s.n & 1;
+        if (!s.half) live = bar_wait(&k_full[ks], (s.t >> 1) & 1, abort);
+        if (s.fresh) live = live && bar_wait(&q_full[RT == 1 ? 0 : w], s.part & 1, abort);
+        // P of step n - 2, in this buffer, has been read.  (Where S does not run ahead, O of
+        // step n - 1 is on its way too and may end first: that one is waited for.)
+        const uint32_t behind = s.n == o.n ? 1u : 2u;
+        if (s.n >= behind) live = live && bar_wait(&o_done[w], (s.n - behind) & 1, abort);
+        if (!live) return;
+        fence_after();
+        const uint64_t kd = k_desc + static_cast<uint64_t>(ks * (kOpB >> 4) + (s.half ? kStep * 128 >> 4 : 0));
+#pragma unroll
+        for (int kk = 0; kk < kHD / 16; ++kk) {
+          const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kHalfB >> 4) + (kk & 3) * 2);
+          umma(tS + buf * kStep, q_desc + off, kd + off, idS, kk > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[2 * w + buf]);
+        if (last_half(s)) umma_commit(&k_empty[ks]);
+        advance(s);
+      };
+      auto issue_O = [&]() {
+        const uint32_t vs = o.t & 1, buf = o.n & 1;
+        if (!o.half) live = bar_wait(&v_full[vs], (o.t >> 1) & 1, abort);
+        live = live && bar_wait(&p_full[2 * w + buf], (o.n >> 1) & 1, abort);
+        if (!live) return;
+        fence_after();
+        const uint64_t vd = v_desc + static_cast<uint64_t>(vs * (kOpB >> 4) + (o.half ? kStep * 128 >> 4 : 0));
+#pragma unroll
+        for (int kk = 0; kk < kStep / 16; ++kk)
+          umma_ts(tO, tS + buf * kStep + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), idO,
+                  kk > 0 || !o.fresh ? 1u : 0u);  // the first step of a part starts O
+        umma_commit(&o_done[w]);
+        if (last_half(o)) umma_commit(&v_empty[vs]);
+        const uint32_t part = o.part;
+        advance(o);
+        if (o.part != part) umma_commit(&o_last[w]);
+      };
+      if (s.on) issue_S();
+      while (live && o.on) {
+        // (the first S of a part needs the new Q, which its group writes after the last O)
+        const bool ahead = s.on && s.part == o.part && s.n == o.n + 1;
+        if (ahead) issue_S();
+        if (live) issue_O();
+        if (live && s.on && s.n == o.n) issue_S();
+      }
     }
   } else if (warp >= kDeq0) {
     regs_dec<kRegsDeq>();
@@ -486,7 +521,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         if (!warp_wait(op ? &v_empty[dst_st] : &k_empty[dst_st], ((T >> 1) & 1) ^ 1, abort)) return false;
         const unsigned char* raw = sRaw + (op ? C::RK + st : st) * kRawB;
         const bool nodes = x >= p.NT;
-        const int left = nodes ? g.R - (x - p.NT) * kKeys : p.P - x * kKeys;  // keys that exist
+        const int left = p.left(g, x);
         unsigned char* dst = (op ? sV : sK) + dst_st * kOpB;
         if (!nodes) {
           const unsigned char *codes = raw, *scales = raw + kCodeB;
@@ -642,7 +677,8 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
     const uint32_t tS = tmem + grp * 128 + lane_base, tO = tmem + 256 + grp * 128 + lane_base;
     if (work) {
       Parts p = first;
-      int n_job = 0, ntail = 0, n_part = 0;
+      uint32_t n_step = 0, n_last = 0;
+      int ntail = 0, n_part = 0;
       bool live = true;
       do {
         const int kvh = p.pq / g.RG, rg = p.pq - kvh * g.RG;
@@ -688,128 +724,128 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
             if (lane == 0) bar_arrive(&q_full[grp]);
           }
         }
+        // (RT = 1: the groups begin a part together, so that neither frees the shared Q twice
+        // while the other is a part behind)
+        if (RT == 1 && grp == 1 && !warp_wait(&q_full[0], n_part & 1, abort)) live = false;
         const float c2p = c2 * kv.k_unit;
         float m = -INFINITY, l = 0.0f;
-        int ue = vu_exp, mine = 0;  // exponent of O's unit; this group's jobs of the part
+        int ue = vu_exp, mine = 0;  // exponent of O's unit; this group's steps of the part
         const int tail0 = ntail;
         const int words = (g.R + 63) >> 6;
         const uint64_t* mrow = mask + (static_cast<size_t>(p.b) * g.R + node) * words;
-        for (int x = p.x0; x < p.x1; ++x) {
+        for (int x = p.x0; live && x < p.x1; ++x) {
           const bool nodes = x >= p.NT;
           const int slot = ntail % kTailRing;
           if (nodes) ++ntail;
           if (RT == 1 && ((x - p.x0) & 1) != grp) continue;
-          if (!live) break;
-          const int left = nodes ? g.R - (x - p.NT) * kKeys : p.P - x * kKeys;
-          // keys the row sees: all, those that exist, or the ancestors among the nodes
-          uint64_t see[2] = {~0ull, ~0ull};
-          const bool full = !nodes && left >= kKeys;
-          if (!full) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int n = left - 64 * h;
-              see[h] = n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+          const int left = p.left(g, x);
+          int tile_ue = vu_exp;
+#pragma unroll 1
+          for (int h = 0; h < 2 && left > kStep * h; ++h) {
+            // keys the row sees: all, those that exist, or the ancestors among the nodes
+            uint64_t see = ~0ull;
+            const bool full = !nodes && left >= kStep * (h + 1);
+            if (!full) {
+              const int n = left - kStep * h;
+              see = n >= 64 ? ~0ull : (1ull << n) - 1ull;
               if (nodes) {
                 const int wd = 2 * (x - p.NT) + h;
-                see[h] &= wd < words && row_ok ? mrow[wd] : 0ull;
+                see &= wd < words && row_ok ? mrow[wd] : 0ull;
               }
             }
-          }
-          if (!warp_wait(&s_full[grp], n_job & 1, abort)) {
-            live = false;
-            break;
-          }
-          __syncwarp();
-          fence_after();
-          const int tile_ue = nodes ? max(max(s_ue[slot * 4], s_ue[slot * 4 + 1]), max(s_ue[slot * 4 + 2], s_ue[slot * 4 + 3])) : vu_exp;
-          // One tile's scores to probabilities; ALL: every key is seen and the factor is the
-          // cache's (the other tiles' factors and masks are applied element by element).
-          // False: a wait ran out.
-          auto tile = [&](auto all) -> bool {
-            constexpr bool ALL = decltype(all)::value;
-            const float c = ALL ? c2p : c2;
-            float2 v[64];
-            tmem_ld128(tS, v);
-            if (!ALL) {  // factors, and -Inf where unseen
-              const float* fac = s_fac + slot * kKeys;
-#pragma unroll
-              for (int j = 0; j < 64; ++j) {
-                const uint64_t s2 = see[j >> 5] >> ((2 * j) & 63);
-                v[j].x = (s2 & 1ull) ? v[j].x * (nodes ? fac[2 * j] : kv.k_unit) : -INFINITY;
-                v[j].y = (s2 & 2ull) ? v[j].y * (nodes ? fac[2 * j + 1] : kv.k_unit) : -INFINITY;
-              }
+            const uint32_t buf = n_step & 1;
+            if (!warp_wait(&s_full[2 * grp + buf], (n_step >> 1) & 1, abort)) {
+              live = false;
+              break;
             }
-            float a0 = fmaxf(v[0].x, v[0].y), a1 = fmaxf(v[1].x, v[1].y), a2 = fmaxf(v[2].x, v[2].y), a3 = fmaxf(v[3].x, v[3].y);
+            fence_after();
+            if (nodes) tile_ue = max(max(s_ue[slot * 4], s_ue[slot * 4 + 1]), max(s_ue[slot * 4 + 2], s_ue[slot * 4 + 3]));
+            // One step's scores to probabilities; ALL: every key is seen and the factor is
+            // the cache's (the other steps' factors and masks are applied element by
+            // element).  False: a wait ran out.
+            auto step = [&](auto all) -> bool {
+              constexpr bool ALL = decltype(all)::value;
+              const float c = ALL ? c2p : c2;
+              float2 v[32];
+              tmem_ld64(tS + buf * kStep, v);
+              if (!ALL) {  // factors, and -Inf where unseen
+                const float* fac = s_fac + slot * kKeys + kStep * h;
 #pragma unroll
-            for (int j = 4; j < 64; j += 4) {
-              a0 = fmax3f(a0, v[j].x, v[j].y);
-              a1 = fmax3f(a1, v[j + 1].x, v[j + 1].y);
-              a2 = fmax3f(a2, v[j + 2].x, v[j + 2].y);
-              a3 = fmax3f(a3, v[j + 3].x, v[j + 3].y);
-            }
-            const float tmax = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * c;
-            // the base moves when passed by more than 2^15; O's unit when the tile's V has another
-            const bool move = tmax > m + kTop;
-            const bool unit = tile_ue != ue && mine > 0;
-            float corr = 1.0f;
-            if (move) {
-              const float nm = fmaxf(m, tmax - kHead);
-              corr = ex2(m - nm);
-              l *= corr;
-              m = nm;
-            }
-            if (unit) corr *= pow2f(ue - tile_ue);
-            ue = tile_ue;
-            const bool rescale = mine > 0 && __any_sync(0xFFFFFFFFu, move || unit);
-            const float2 cv = make_float2(c, c);
-            const float sub = ALL ? m : m == -INFINITY ? 0.0f : m;
-            const float2 nv = make_float2(-sub, -sub);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {  // P of 32 keys goes over 16 columns: the scores are in registers
-              uint32_t pk[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float2 a = __ffma2_rn(v[16 * h + j], cv, nv);
-                float2 e = make_float2(ex2(a.x), ex2(a.y));
-                if (!ALL) {
-                  const uint64_t s2 = see[h >> 1] >> ((32 * h + 2 * j) & 63);
-                  e.x = (s2 & 1ull) ? e.x : 0.0f;
-                  e.y = (s2 & 2ull) ? e.y : 0.0f;
+                for (int j = 0; j < 32; ++j) {
+                  v[j].x = ((see >> (2 * j)) & 1ull) ? v[j].x * (nodes ? fac[2 * j] : kv.k_unit) : -INFINITY;
+                  v[j].y = ((see >> (2 * j + 1)) & 1ull) ? v[j].y * (nodes ? fac[2 * j + 1] : kv.k_unit) : -INFINITY;
                 }
-                sum[j & 1] = __fadd2_rn(sum[j & 1], e);
-                pk[j] = h2u(__float22half2_rn(e));
               }
-              tmem_st16(tS + 16 * h, pk);
-            }
-            const float2 st = __fadd2_rn(sum[0], sum[1]);
-            l += st.x + st.y;
-            if (rescale) {
-              if (!warp_wait(&o_done[grp], (n_job - 1) & 1, abort)) return false;
-              __syncwarp();
-              fence_after();
-#pragma unroll 1
-              for (int h = 0; h < 8; ++h) {  // in 16-column steps, to keep register pressure low
-                uint32_t y[16];
-                tmem_ld16(tO + 16 * h, y);
+              float a0 = fmaxf(v[0].x, v[0].y), a1 = fmaxf(v[1].x, v[1].y), a2 = fmaxf(v[2].x, v[2].y), a3 = fmaxf(v[3].x, v[3].y);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
-                tmem_st16(tO + 16 * h, y);
-                tmem_st_wait();
+              for (int j = 4; j < 32; j += 4) {
+                a0 = fmax3f(a0, v[j].x, v[j].y);
+                a1 = fmax3f(a1, v[j + 1].x, v[j + 1].y);
+                a2 = fmax3f(a2, v[j + 2].x, v[j + 2].y);
+                a3 = fmax3f(a3, v[j + 3].x, v[j + 3].y);
               }
+              const float tmax = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * c;
+              // the base moves when passed by more than 2^15; O's unit when the tile's V has another
+              const bool move = tmax > m + kTop;
+              const bool unit = tile_ue != ue && mine > 0;
+              float corr = 1.0f;
+              if (move) {
+                const float nm = fmaxf(m, tmax - kHead);
+                corr = ex2(m - nm);
+                l *= corr;
+                m = nm;
+              }
+              if (unit) corr *= pow2f(ue - tile_ue);
+              ue = tile_ue;
+              const bool rescale = mine > 0 && __any_sync(0xFFFFFFFFu, move || unit);
+              const float2 cv = make_float2(c, c);
+              const float sub = ALL ? m : m == -INFINITY ? 0.0f : m;
+              const float2 nv = make_float2(-sub, -sub);
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {  // P of 32 keys goes over 16 columns: the scores are in registers
+                uint32_t pk[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const float2 a = __ffma2_rn(v[16 * q + j], cv, nv);
+                  float2 e = make_float2(ex2(a.x), ex2(a.y));
+                  if (!ALL) {
+                    e.x = ((see >> (32 * q + 2 * j)) & 1ull) ? e.x : 0.0f;
+                    e.y = ((see >> (32 * q + 2 * j + 1)) & 1ull) ? e.y : 0.0f;
+                  }
+                  sum[j & 1] = __fadd2_rn(sum[j & 1], e);
+                  pk[j] = h2u(__float22half2_rn(e));
+                }
+                tmem_st16(tS + buf * kStep + 16 * q, pk);
+              }
+              const float2 st = __fadd2_rn(sum[0], sum[1]);
+              l += st.x + st.y;
+              if (rescale) {
+                if (!warp_wait(&o_done[grp], (n_step - 1) & 1, abort)) return false;
+                fence_after();
+#pragma unroll 1
+                for (int d = 0; d < 8; ++d) {  // in 16-column steps, to keep register pressure low
+                  uint32_t y[16];
+                  tmem_ld16(tO + 16 * d, y);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
+                  tmem_st16(tO + 16 * d, y);
+                  tmem_st_wait();
+                }
+              }
+              tmem_st_wait();
+              return true;
+            };
+            if (!(full ? step(std::true_type{}) : step(std::false_type{}))) {
+              live = false;
+              break;
             }
-            tmem_st_wait();
-            return true;
-          };
-          if (!(full ? tile(std::true_type{}) : tile(std::false_type{}))) {
-            live = false;
-            break;
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&p_full[2 * grp + buf]);
+            ++n_step;
+            ++mine;
           }
-          fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&p_full[grp]);
-          ++n_job;
-          ++mine;
         }
         if (!live) break;
         if (RT == 1) {  // this group's S products have read Q
@@ -818,7 +854,8 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         }
         // the part's record: o normalized by its own sum, the base and the sum
         if (mine > 0) {
-          if (!warp_wait(&o_done[grp], (n_job - 1) & 1, abort)) {
+          // (a barrier of its own: up to two of the steps' phases may be open here)
+          if (!warp_wait(&o_last[grp], n_last++ & 1, abort)) {
             live = false;
             break;
           }
@@ -876,6 +913,8 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       for (int t = max(0, T_raw - stages); t < T_raw; ++t)
         while (!bar_try(&raw_full[3 * op + t % stages], (t / stages) & 1) && gtimer() - t0 < kWaitNs) {
         }
+      while (gtimer() - t0 < 50000) {  // and so have the products
+      }
       if (lane == 0) dev_flag(dev_err, E3_DEV_ERR_TIMEOUT);
     }
     __syncthreads();
