@@ -53,13 +53,14 @@ constexpr int kTailRing = 8;             // tiles of tree nodes whose factors ar
 constexpr int kThreads = 512;
 constexpr int kSoftmax0 = 4, kDeq0 = 12;
 constexpr int kRegsIssue = 64, kRegsSoftmax = 176, kRegsDeq = 88;
+constexpr int kNodeExp = 24;  // > kTop: a node's weight times a row of V sums below 2^(15 - 24 + 8) of it
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
 template <int RT>
 struct Cfg {
   static constexpr int RK = RT == 2 ? 2 : 3, RV = RT == 2 ? 1 : 3;  // raw stages of K and V
   static constexpr int Q = 0, K = RT * kOpB, V = K + 2 * kOpB, RAW = V + 2 * kOpB, FAC = RAW + (RK + RV) * kRawB;
-  static constexpr int BARS = FAC + kTailRing * kKeys * 4, END = BARS + 768;
+  static constexpr int BARS = FAC + kTailRing * kKeys * 4, END = BARS + 1536;
   static constexpr int SMEM = END + 1024;  // (base rounded up to 1024)
 };
 static_assert(Cfg<1>::SMEM <= 232448 && Cfg<2>::SMEM <= 232448, "shared memory of a CTA");
@@ -87,18 +88,21 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t par) {
                : "memory");
   return ok != 0;
 }
-// Bounded wait: about a second, or until another role has given up.
+// Bounded wait: about a second, or until another role has given up.  (The timer is read
+// once in 32 probes, each of which the hardware may suspend for a while.)
 __device__ __forceinline__ bool bar_wait(uint64_t* b, uint32_t par, volatile int* abort) {
-  if (bar_try(b, par)) return true;
-  const uint64_t t0 = gtimer();
-  for (;;) {
+  uint64_t t0 = 0;
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (bar_try(b, par)) return true;
-    if (*abort) return false;
-    if (gtimer() - t0 > kWaitNs) {
-      *abort = 1;
-      return false;
+  for (uint32_t n = 1;; ++n) {
+    if (bar_try(b, par)) return true;
+    if ((n & 31u) == 0u) {
+      if (*abort) return false;
+      const uint64_t now = gtimer();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitNs) {
+        *abort = 1;
+        return false;
+      }
     }
   }
 }
@@ -118,9 +122,9 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo, uint
          (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
          (static_cast<uint64_t>(2) << 61);
 }
-// kind::f16 instruction descriptor: f16 x f16 -> f32, M = 128, N, the second operand's major.
-__host__ __device__ constexpr uint32_t idesc_f16(int N, int b_mn) {
-  return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+// kind::f16 instruction descriptor: f16 or bf16 operands -> f32, M = 128, N, the second operand's major.
+__host__ __device__ constexpr uint32_t idesc_16(int N, int b_mn, bool bf16) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(128 >> 4) << 24);
 }
 __device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
@@ -277,9 +281,9 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   uint64_t* q_full = bars + 30;
   uint64_t* o_last = bars + 32;     // [softmax group] the last O product of a part
   uint64_t* q_free = bars + 34;     // (RT = 1) both groups are done with the shared Q
-  int* s_ue = reinterpret_cast<int*>(bars + 36);                        // [kTailRing][4] exponent of V's unit in a tile of nodes, by dequantizer warp
-  uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_ue + 4 * kTailRing);  // [kTailRing][4] nodes with a non-finite V
-  uint32_t* tmem_slot = s_bad + 4 * kTailRing;
+  uint32_t* s_bad = reinterpret_cast<uint32_t*>(bars + 36);  // [kTailRing][4] nodes with a non-finite V
+  int* s_ex = reinterpret_cast<int*>(s_bad + 4 * kTailRing);  // [8 softmax warps][32] exponents of the rows of Q
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_ex + 256);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -396,7 +400,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
     // One issuing thread per softmax group: neither group's products wait behind the other
     // group's barriers.  S runs a step (64 keys) ahead of O within a part.
     if ((warp == 1 || warp == 2) && lane == 0 && work) {
-      constexpr uint32_t idS = idesc_f16(kStep, 0), idO = idesc_f16(kHD, 1);
+      constexpr uint32_t idS = idesc_16(kStep, 0, false);
       const int w = warp - 1;
       const uint64_t q_desc = desc_sw128(su32(sQ) + (RT == 2 ? w : 0) * kOpB, 16, 1024);
       const uint64_t k_desc = desc_sw128(su32(sK), 16, 1024);
@@ -473,6 +477,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         if (!live) return;
         fence_after();
         const uint64_t vd = v_desc + static_cast<uint64_t>(vs * (kOpB >> 4) + (o.half ? kStep * 128 >> 4 : 0));
+        const uint32_t idO = o.x >= o.p.NT ? idesc_16(kHD, 1, true) : idesc_16(kHD, 1, false);  // tree nodes' V stays bf16
 #pragma unroll
         for (int kk = 0; kk < kStep / 16; ++kk)
           umma_ts(tO, tS + buf * kStep + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), idO,
@@ -560,72 +565,49 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
             }
           }
         } else {
-          // 32 dims of a node's row (zeros where there is none), this lane's quarter
-          auto load_row = [&](const void* from, int i, uint4 (&y)[4]) {
-            const int key = dw * 32 + i * 8 + (lane >> 2), j = (x - p.NT) * kKeys + key;
+          // tree nodes: K to fp16, each key's largest magnitude scaled to [1, 2) (its scores
+          // get the factor back); V as it is stored, its product runs in bf16
+          const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(op ? tail.v : tail.k);
+          long long rows[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] = make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < 4; ++i) {  // the pages of all rows at once
+            const int key = dw * 32 + i * 8 + (lane >> 2), j = (x - p.NT) * kKeys + key;
+            rows[i] = -1;
             if (key < left) {
               const int pi = j / tail.page_size;
               const int page = tail.page_table[static_cast<size_t>(p.b) * tail.max_pages + pi];
-              if (page >= 0 && page < tail.n_pages) {
-                const size_t row = (static_cast<size_t>(page) * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size);
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  y[c] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(from) + row * kHD + 32 * q)[c];
-              } else {
+              if (page >= 0 && page < tail.n_pages)
+                rows[i] = (static_cast<long long>(page) * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size);
+              else
                 dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
-              }
             }
-          };
-          // largest magnitude of the node's row as bf16 bits, the same in its four lanes
-          auto row_max = [&](const uint4 (&y)[4]) {
-            uint32_t am = 0u;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              am = __vmaxu2(am, __vmaxu2(__vmaxu2(y[c].x & 0x7FFF7FFFu, y[c].y & 0x7FFF7FFFu),
-                                         __vmaxu2(y[c].z & 0x7FFF7FFFu, y[c].w & 0x7FFF7FFFu)));
-            am = max(am & 0xFFFFu, am >> 16);
-            am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-            return max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-          };
-          int vu = vu_exp - 40;  // (not so far below v_unit that O would overflow in it)
-          if (op == 0) {
-            // V's unit: the exponent of the tile's largest node without NaN or Inf.  Each
-            // warp leaves that of its nodes with its K
-            uint32_t top = 0u;
-#pragma unroll
-            for (int i0 = 0; i0 < 4; i0 += 2) {
-              if (dw * 32 + i0 * 8 >= left) break;
-              uint4 y[2][4];
-              load_row(tail.v, i0, y[0]);
-              load_row(tail.v, i0 + 1, y[1]);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t am = row_max(y[h]);
-                if (am < 0x7F80u) top = max(top, am);
-              }
-            }
-            top = __reduce_max_sync(0xFFFFFFFFu, top);
-            if (lane == 0) s_ue[slot * 4 + dw] = max(static_cast<int>(top >> 7) - 127, vu);
-          } else {
-            if (!warp_wait(&k_full[T & 1], (T >> 1) & 1, abort)) return false;  // every warp has left its own
-            vu = max(max(s_ue[slot * 4], s_ue[slot * 4 + 1]), max(s_ue[slot * 4 + 2], s_ue[slot * 4 + 3]));
           }
           uint32_t bad_v = 0u;  // this warp's keys with a non-finite V
 #pragma unroll 1
           for (int i0 = 0; i0 < 4; i0 += 2) {
             uint4 y[2][4];
-            load_row(op ? tail.v : tail.k, i0, y[0]);
-            load_row(op ? tail.v : tail.k, i0 + 1, y[1]);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const long long row = i0 ? rows[2 + h] : rows[h];
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                y[h][c] = row >= 0 ? reinterpret_cast<const uint4*>(from + row * kHD + 32 * q)[c] : make_uint4(0u, 0u, 0u, 0u);
+            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const int key = dw * 32 + (i0 + h) * 8 + (lane >> 2);
-              const uint32_t am = row_max(y[h]);
+              uint32_t am = 0u;  // largest magnitude of the node's row as bf16 bits, the same in its four lanes
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                am = __vmaxu2(am, __vmaxu2(__vmaxu2(y[h][c].x & 0x7FFF7FFFu, y[h][c].y & 0x7FFF7FFFu),
+                                           __vmaxu2(y[h][c].z & 0x7FFF7FFFu, y[h][c].w & 0x7FFF7FFFu)));
+              am = max(am & 0xFFFFu, am >> 16);
+              am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+              am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+              // a node with a NaN or an Inf leaves the product: its scores get a NaN factor,
+              // rows that see its V are marked
               const bool bad = am >= 0x7F80u;
-              // a node with a NaN or an Inf leaves the product: its scores get a NaN
-              // factor, rows that see its V are marked
-              const int ex = op ? vu : max(static_cast<int>(am >> 7), 1) - 127;
+              const int ex = max(static_cast<int>(am >> 7), 1) - 127;
               if (op == 0 && q == 0) s_fac[slot * kKeys + key] = bad ? __int_as_float(0x7FC00000) : pow2f(ex);
               if (bad) bad_v |= 1u << (key & 31);
               const int na = -ex / 2;
@@ -634,15 +616,15 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
               unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
-                const uint32_t w[4] = {y[h][c].x, y[h][c].y, y[h][c].z, y[h][c].w};
-                uint32_t hh[4];
+                uint32_t w[4] = {y[h][c].x, y[h][c].y, y[h][c].z, y[h][c].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                  const uint32_t z = bad ? 0u : w[k];
-                  hh[k] = h2u(__floats2half2_rn(__uint_as_float(z << 16) * f0 * f1, __uint_as_float(z & 0xFFFF0000u) * f0 * f1));
+                  if (op == 0)
+                    w[k] = h2u(__floats2half2_rn(__uint_as_float(w[k] << 16) * f0 * f1, __uint_as_float(w[k] & 0xFFFF0000u) * f0 * f1));
+                  if (bad) w[k] = 0u;
                 }
                 const int chunk = 4 * (q & 1) + c;
-                *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+                *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
               }
             }
           }
@@ -657,16 +639,15 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         }
         return true;
       };
-      Cursor k{first, first.x0, 0, 0, true}, v{first, first.x0, 0, 0, true};
-      bool live = convert(0, k);
-      advance(k);
-      while (live && v.on) {
-        if (k.on) {
-          if (!convert(0, k)) break;
-          advance(k);
+      Cursor cur[2] = {{first, first.x0, 0, 0, true}, {first, first.x0, 0, 0, true}};
+      // K, then K and V in turn until both have ended (one call: the code is long)
+      int op = 0;
+      while (cur[1].on) {
+        if (cur[op].on) {
+          if (!convert(op, cur[op])) break;
+          advance(cur[op]);
         }
-        if (!convert(1, v)) break;
-        advance(v);
+        op = op == 0 && cur[1].T < cur[0].T - (cur[0].on ? 1 : 0) ? 1 : 0;
       }
     }
   } else {
@@ -685,49 +666,54 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         const int gr = (rg * RT + (RT == 2 ? grp : 0)) * kRows + r;  // row of the KV head
         const bool row_ok = gr < g.G * g.R;
         const int node = row_ok ? gr / g.G : 0, head = kvh * g.G + (row_ok ? gr - node * g.G : 0);
-        // Q of the row to fp16, its largest magnitude scaled to [1, 2)
-        float c2;
-        {
-          const uint4* qp = reinterpret_cast<const uint4*>(Q + ((static_cast<size_t>(p.b) * g.R + node) * g.H + head) * kHD);
-          uint4 y[16];
-          uint32_t am = 0u;
+        // Q to fp16, each row's largest magnitude scaled to [1, 2): half a warp to a row, so
+        // that rows are read and written in whole lines; the exponents meet their rows in s_ex
+        int* ex_rows = s_ex + (RT == 2 ? grp : 0) * kRows + quarter * 32;
+        if (RT == 2 || grp == 0) {
+          const int own = row_ok ? node * g.H + head : -1;
+          const int chunk = lane & 15;
+          const uint4* qb = reinterpret_cast<const uint4*>(Q + static_cast<size_t>(p.b) * g.R * g.H * kHD) + chunk;
+          unsigned char* to = sQ + (RT == 2 ? grp : 0) * kOpB + (chunk >> 3) * kHalfB + quarter * 32 * 128;
+#pragma unroll 1
+          for (int i0 = 0; i0 < 16; i0 += 8) {
+            uint4 y[8];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            y[c] = row_ok ? qp[c] : make_uint4(0u, 0u, 0u, 0u);
-          }
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            am = __vmaxu2(am, __vmaxu2(__vmaxu2(y[c].x & 0x7FFF7FFFu, y[c].y & 0x7FFF7FFFu),
-                                       __vmaxu2(y[c].z & 0x7FFF7FFFu, y[c].w & 0x7FFF7FFFu)));
-          am = max(am & 0xFFFFu, am >> 16);
-          // (below 2^-64 a row's scores are as good as zero, and its factor would underflow)
-          const int ex = max(static_cast<int>(am >> 7) - 127, -64);
-          c2 = fmaxf(sm_scale * kLog2e * pow2f(ex), 1e-37f);
-          if (RT == 2 || grp == 0) {
+            for (int i = 0; i < 8; ++i) {
+              const int at = __shfl_sync(0xFFFFFFFFu, own, 2 * (i0 + i) + (lane >> 4));
+              y[i] = at >= 0 ? qb[static_cast<size_t>(at) * (kHD / 8)] : make_uint4(0u, 0u, 0u, 0u);
+            }
             // (RT = 1: the other group's products of the last part have read the shared Q)
-            if (RT == 1 && n_part > 0 && !warp_wait(q_free, (n_part - 1) & 1, abort)) live = false;
-            const int na = -ex / 2;
-            const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
-            const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
-            unsigned char* row = sQ + (RT == 2 ? grp : 0) * kOpB + r * 128;
+            if (RT == 1 && i0 == 0 && n_part > 0 && !warp_wait(q_free, (n_part - 1) & 1, abort)) live = false;
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              const uint32_t w[4] = {y[c].x, y[c].y, y[c].z, y[c].w};
+            for (int i = 0; i < 8; ++i) {
+              const int rr = 2 * (i0 + i) + (lane >> 4);
+              uint32_t am = __vmaxu2(__vmaxu2(y[i].x & 0x7FFF7FFFu, y[i].y & 0x7FFF7FFFu),
+                                     __vmaxu2(y[i].z & 0x7FFF7FFFu, y[i].w & 0x7FFF7FFFu));
+#pragma unroll
+              for (int o = 8; o > 0; o >>= 1) am = __vmaxu2(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+              am = max(am & 0xFFFFu, am >> 16);
+              // (below 2^-64 a row's scores are as good as zero, and its factor would underflow)
+              const int ex = max(static_cast<int>(am >> 7) - 127, -64);
+              if (chunk == 0) ex_rows[rr] = ex;
+              const int na = -ex / 2;
+              const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
+              const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
+              const uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
               uint32_t h[4];
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 h[k] = h2u(__floats2half2_rn(__uint_as_float(w[k] << 16) * f0 * f1, __uint_as_float(w[k] & 0xFFFF0000u) * f0 * f1));
-              *reinterpret_cast<uint4*>(row + (c >> 3) * kHalfB + (((c & 7) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(to + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&q_full[grp]);
           }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&q_full[grp]);
         }
         // (RT = 1: the groups begin a part together, so that neither frees the shared Q twice
         // while the other is a part behind)
         if (RT == 1 && grp == 1 && !warp_wait(&q_full[0], n_part & 1, abort)) live = false;
-        const float c2p = c2 * kv.k_unit;
+        const float c2 = fmaxf(sm_scale * kLog2e * pow2f(ex_rows[lane]), 1e-37f), c2p = c2 * kv.k_unit;
         float m = -INFINITY, l = 0.0f;
         int ue = vu_exp, mine = 0;  // exponent of O's unit; this group's steps of the part
         const int tail0 = ntail;
@@ -739,7 +725,9 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           if (nodes) ++ntail;
           if (RT == 1 && ((x - p.x0) & 1) != grp) continue;
           const int left = p.left(g, x);
-          int tile_ue = vu_exp;
+          // O's unit: the cache's under the prefix; the nodes' weights carry 2^-kNodeExp, so that
+          // products with any finite V stay finite
+          const int tile_ue = nodes ? kNodeExp : vu_exp;
 #pragma unroll 1
           for (int h = 0; h < 2 && left > kStep * h; ++h) {
             // keys the row sees: all, those that exist, or the ancestors among the nodes
@@ -759,7 +747,6 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
               break;
             }
             fence_after();
-            if (nodes) tile_ue = max(max(s_ue[slot * 4], s_ue[slot * 4 + 1]), max(s_ue[slot * 4 + 2], s_ue[slot * 4 + 3]));
             // One step's scores to probabilities; ALL: every key is seen and the factor is
             // the cache's (the other steps' factors and masks are applied element by
             // element).  False: a wait ran out.
@@ -768,12 +755,16 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
               const float c = ALL ? c2p : c2;
               float2 v[32];
               tmem_ld64(tS + buf * kStep, v);
-              if (!ALL) {  // factors, and -Inf where unseen
-                const float* fac = s_fac + slot * kKeys + kStep * h;
+              if (!ALL) {  // factors, and -Inf where unseen (whose exponential is 0)
+                const float2* fac = reinterpret_cast<const float2*>(s_fac + slot * kKeys + kStep * h);
+                const uint32_t s0 = static_cast<uint32_t>(see), s1 = static_cast<uint32_t>(see >> 32);
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                  v[j].x = ((see >> (2 * j)) & 1ull) ? v[j].x * (nodes ? fac[2 * j] : kv.k_unit) : -INFINITY;
-                  v[j].y = ((see >> (2 * j + 1)) & 1ull) ? v[j].y * (nodes ? fac[2 * j + 1] : kv.k_unit) : -INFINITY;
+                  if (j % 8 == 0) asm volatile("" ::: "memory");  // (few factors at a time in registers)
+                  const float2 f = nodes ? fac[j] : make_float2(kv.k_unit, kv.k_unit);
+                  const uint32_t sb = j < 16 ? s0 : s1;
+                  v[j].x = sb & (1u << (2 * j & 31)) ? v[j].x * f.x : -INFINITY;
+                  v[j].y = sb & (2u << (2 * j & 31)) ? v[j].y * f.y : -INFINITY;
                 }
               }
               float a0 = fmaxf(v[0].x, v[0].y), a1 = fmaxf(v[1].x, v[1].y), a2 = fmaxf(v[2].x, v[2].y), a3 = fmaxf(v[3].x, v[3].y);
@@ -799,7 +790,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
               ue = tile_ue;
               const bool rescale = mine > 0 && __any_sync(0xFFFFFFFFu, move || unit);
               const float2 cv = make_float2(c, c);
-              const float sub = ALL ? m : m == -INFINITY ? 0.0f : m;
+              const float sub = ALL ? m : (m == -INFINITY ? 0.0f : m) + (nodes ? kNodeExp : 0);
               const float2 nv = make_float2(-sub, -sub);
               float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -808,18 +799,14 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
                   const float2 a = __ffma2_rn(v[16 * q + j], cv, nv);
-                  float2 e = make_float2(ex2(a.x), ex2(a.y));
-                  if (!ALL) {
-                    e.x = ((see >> (32 * q + 2 * j)) & 1ull) ? e.x : 0.0f;
-                    e.y = ((see >> (32 * q + 2 * j + 1)) & 1ull) ? e.y : 0.0f;
-                  }
+                  const float2 e = make_float2(ex2(a.x), ex2(a.y));
                   sum[j & 1] = __fadd2_rn(sum[j & 1], e);
-                  pk[j] = h2u(__float22half2_rn(e));
+                  pk[j] = !ALL && nodes ? pack2_bf16(e.x, e.y) : h2u(__float22half2_rn(e));
                 }
                 tmem_st16(tS + buf * kStep + 16 * q, pk);
               }
               const float2 st = __fadd2_rn(sum[0], sum[1]);
-              l += st.x + st.y;
+              l += ALL || !nodes ? st.x + st.y : (st.x + st.y) * pow2f(kNodeExp);
               if (rescale) {
                 if (!warp_wait(&o_done[grp], (n_step - 1) & 1, abort)) return false;
                 fence_after();
@@ -875,25 +862,25 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
               poison |= (mrow[wd + h] & (bad[2 * h] | (static_cast<uint64_t>(bad[2 * h + 1]) << 32))) != 0ull;
         }
         const size_t rec = (static_cast<size_t>(p.b) * Qn + p.pq + cta) * (RT == 1 ? 2 : 1) + (RT == 1 ? grp : 0);
-        const size_t rrow = rec * (RT * kRows) + (RT == 2 ? grp * kRows : 0) + r;
+        const int rrow = (RT == 2 ? grp * kRows : 0) + r;
         if (mine > 0) {
           const float inv = poison ? __int_as_float(0x7FC00000) : l != 0.0f ? pow2f(ue) / l : 0.0f;
+          float4* dst = reinterpret_cast<float4*>(ws_o + rec * (RT * kRows * kHD)) + rrow;
 #pragma unroll 1
           for (int h = 0; h < 4; ++h) {
             uint32_t y[32];
             tmem_ld32(tO + 32 * h, y);
             tmem_wait();
             if (row_ok) {
-              float4* dst = reinterpret_cast<float4*>(ws_o + rrow * kHD + 32 * h);
 #pragma unroll
               for (int j = 0; j < 8; ++j)
-                dst[j] = make_float4(__uint_as_float(y[4 * j]) * inv, __uint_as_float(y[4 * j + 1]) * inv,
-                                     __uint_as_float(y[4 * j + 2]) * inv, __uint_as_float(y[4 * j + 3]) * inv);
+                dst[(8 * h + j) * (RT * kRows)] = make_float4(__uint_as_float(y[4 * j]) * inv, __uint_as_float(y[4 * j + 1]) * inv,
+                                                              __uint_as_float(y[4 * j + 2]) * inv, __uint_as_float(y[4 * j + 3]) * inv);
             }
           }
           fence_before();
         }
-        if (row_ok) ws_ml[rrow] = make_float2(m, l);
+        if (row_ok) ws_ml[rec * (RT * kRows) + rrow] = make_float2(m, l);
         if (grp == 0 && r == 0) {
           int32_t* e = ends + 2 * (static_cast<size_t>(p.b) * Qn + p.pq);
           if (p.x0 == 0) e[0] = cta;
@@ -921,6 +908,77 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   }
   fence_after();
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+// Merge of a pair's records.  A record holds its values as [dims / 4][rows][4], so that the
+// threads of the kernel above, a row each, write whole lines; here a block takes 8 rows of a
+// pair, a warp 32 dims of each: lane % 8 is the row, lane / 8 and lane / 8 + 4 the dims' quads.
+template <int RT>
+__global__ void __launch_bounds__(128)
+verify4_tc_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __restrict__ kv_len,
+                        const __grid_constant__ V4Geom g, const float* __restrict__ ws_o, const float2* __restrict__ ws_ml,
+                        const int32_t* __restrict__ ends, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
+  constexpr int ROWS = RT * kRows, SPLIT = RT == 1 ? 2 : 1, AHEAD = 8;
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) * 8 + (lane >> 3);
+  const int strips = (g.G * g.R + 7) / 8;  // of a KV head (8 divides ROWS: none crosses a tile)
+  const int b = blockIdx.x / (g.KVH * strips), in = blockIdx.x - b * (g.KVH * strips), kvh = in / strips;
+  const int r = (in - kvh * strips) * 8 + (lane & 7), rt = r / ROWS;  // row of the KV head
+  const bool ok = r < g.G * g.R;
+  const size_t pair = (static_cast<size_t>(b) * g.KVH + kvh) * g.RG + rt;
+  const int i = ok ? r / g.G : 0;
+  const size_t row = (static_cast<size_t>(b) * g.R + i) * g.H + kvh * g.G + (ok ? r - i * g.G : 0);
+  pdl_wait();
+  pdl_trigger();
+  const int c0 = ends[2 * pair], c1 = ends[2 * pair + 1];
+  // (a worker that gave up, its error word set, may not have left its number)
+  if (pair_units<kKeys>(g, kv, kv_len[b]) == 0 || c0 < 0 || c1 < c0 || c1 >= g.workers) return;
+  const int n = ok ? (c1 - c0 + 1) * SPLIT : 0;
+  const size_t rec = (pair + c0) * SPLIT;
+  const float2* ml = ws_ml + rec * ROWS + (r - rt * ROWS);
+  const float4* val = reinterpret_cast<const float4*>(ws_o + rec * (ROWS * kHD)) + quad * ROWS + (r - rt * ROWS);
+  float M = -INFINITY;
+  for (int q0 = lane >> 3; q0 < n; q0 += 4 * AHEAD) {
+    float2 y[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) y[u] = q0 + 4 * u < n ? ml[(q0 + 4 * u) * ROWS] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (y[u].y != 0.0f) M = fmaxf(M, y[u].x);
+  }
+  M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, 8));
+  M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, 16));
+  float acc[8], den = 0.0f;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) acc[u] = 0.0f;
+  for (int q0 = 0; q0 < n; q0 += AHEAD) {
+    float2 y[AHEAD];
+    float4 x[AHEAD][2];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      y[u] = make_float2(0.0f, 0.0f);
+      if (q0 + u < n) {
+        y[u] = ml[(q0 + u) * ROWS];
+        x[u][0] = val[static_cast<size_t>(q0 + u) * (ROWS * kHD / 4)];
+        x[u][1] = val[static_cast<size_t>(q0 + u) * (ROWS * kHD / 4) + 4 * ROWS];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (y[u].y != 0.0f) {  // (0: a record without keys, whose values were never written; a NaN sum stays one)
+        const float w = y[u].y * ex2(y[u].x - M);
+        den += w;
+        acc[0] = fmaf(w, x[u][0].x, acc[0]), acc[1] = fmaf(w, x[u][0].y, acc[1]);
+        acc[2] = fmaf(w, x[u][0].z, acc[2]), acc[3] = fmaf(w, x[u][0].w, acc[3]);
+        acc[4] = fmaf(w, x[u][1].x, acc[4]), acc[5] = fmaf(w, x[u][1].y, acc[5]);
+        acc[6] = fmaf(w, x[u][1].z, acc[6]), acc[7] = fmaf(w, x[u][1].w, acc[7]);
+      }
+  }
+  if (!ok) return;
+  const float inv = den != 0.0f ? 1.0f / den : 0.0f;
+  uint2* out = reinterpret_cast<uint2*>(O + row * kHD) + quad;
+  out[0] = make_uint2(pack2_bf16(acc[0] * inv, acc[1] * inv), pack2_bf16(acc[2] * inv, acc[3] * inv));
+  out[4] = make_uint2(pack2_bf16(acc[4] * inv, acc[5] * inv), pack2_bf16(acc[6] * inv, acc[7] * inv));
+  if (quad == 0) lse[row] = den != 0.0f ? (M + log2f(den)) * kLn2 : -INFINITY;
 }
 
 V4Geom make_geom_tc(int B, int R, int H, int KVH, int max_kv_len) {
@@ -961,10 +1019,9 @@ cudaError_t launch_tc(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_k
   const cudaError_t e = launch_pdl(verify4_tc_kernel<RT>, dim3(g.workers), dim3(kThreads), Cfg<RT>::SMEM, s, 1, q, kv, tail,
                                    kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, dev_err);
   if (e != cudaSuccess) return e;
-  return launch_pdl(verify4_merge_kernel<kHD, RT * kRows, kKeys, RT == 1 ? 2 : 1>,
-                    dim3(static_cast<unsigned>((static_cast<long>(g.B) * g.R * g.H + 3) / 4)), dim3(128), 0, s, 1, kv, kv_len, g,
-                    static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml), static_cast<const int32_t*>(ends), o,
-                    lse);
+  return launch_pdl(verify4_tc_merge_kernel<RT>, dim3(static_cast<unsigned>(g.B) * g.KVH * ((g.G * g.R + 7) / 8)), dim3(128), 0, s, 1,
+                    kv, kv_len, g, static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml),
+                    static_cast<const int32_t*>(ends), o, lse);
 }
 
 }  // namespace
