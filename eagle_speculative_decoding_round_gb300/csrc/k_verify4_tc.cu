@@ -257,6 +257,56 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 e) {
                     h2u(__hmul2(u2h(r[3]), e)));
 }
 
+// 32 rows of 256 bytes in a swizzled operand (the first row a multiple of 8): half a warp to
+// a row, lane % 16 the 16-byte piece.  (Loops, not straight code: an instruction that runs
+// once a part costs its fetch.)
+__device__ __forceinline__ unsigned char* row_chunk(unsigned char* slab, int rr, int c) {
+  return slab + (c >> 3) * kHalfB + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
+}
+// rows `own` (a lane's own row, -1: zeros) of `from` into the slab
+__device__ __forceinline__ void bring_rows(const __nv_bfloat16* from, int own, unsigned char* slab, int lane) {
+  const int c = lane & 15;
+#pragma unroll 2
+  for (int i = 0; i < 16; ++i) {
+    const int rr = 2 * i + (lane >> 4);
+    const int at = __shfl_sync(0xFFFFFFFFu, own, rr);
+    const __nv_bfloat16* src = from + static_cast<size_t>(max(at, 0)) * kHD + c * 8;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(su32(row_chunk(slab, rr, c))), "l"(src), "r"(at >= 0 ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+// magnitudes' bits: the larger of the even and of the odd elements
+__device__ __forceinline__ uint32_t max_bits(const uint4& y) {
+  return __vmaxu2(__vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu), __vmaxu2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu));
+}
+// the slab's rows from bf16 to fp16 in place, each row's largest magnitude scaled to [1, 2)
+// (which keeps its bits down to 2^-24 of it); factor(row, its magnitude's bits, the power).  A
+// row with a NaN or an Inf becomes zeros.
+template <class F>
+__device__ __forceinline__ void rows_to_half(unsigned char* slab, int lane, F factor) {
+#pragma unroll 2
+  for (int i = 0; i < 16; ++i) {
+    const int rr = 2 * i + (lane >> 4);
+    uint4* at = reinterpret_cast<uint4*>(row_chunk(slab, rr, lane & 15));
+    const uint4 y = *at;
+    uint32_t am = max_bits(y);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) am = __vmaxu2(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
+    am = max(am & 0xFFFFu, am >> 16);
+    const int ex = max(static_cast<int>(am >> 7), 1) - 127;
+    if ((lane & 15) == 0) factor(rr, am, ex);
+    const int na = -ex / 2;
+    const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
+    const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
+    uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      w[k] = am < 0x7F80u ? h2u(__floats2half2_rn(__uint_as_float(w[k] << 16) * f0 * f1, __uint_as_float(w[k] & 0xFFFF0000u) * f0 * f1)) : 0u;
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 template <int RT>
 __global__ void __launch_bounds__(kThreads, 1)
 verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e3_kv4_layer kv,
@@ -275,13 +325,12 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   uint64_t* k_empty = bars + 14;    // [2]
   uint64_t* v_full = bars + 16;     // [2]
   uint64_t* v_empty = bars + 18;    // [2]
-  uint64_t* s_full = bars + 20;     // [softmax group][2 buffers], as p_full
-  uint64_t* p_full = bars + 24;
-  uint64_t* o_done = bars + 28;     // [softmax group], as q_full
-  uint64_t* q_full = bars + 30;
-  uint64_t* o_last = bars + 32;     // [softmax group] the last O product of a part
-  uint64_t* q_free = bars + 34;     // (RT = 1) both groups are done with the shared Q
-  uint32_t* s_bad = reinterpret_cast<uint32_t*>(bars + 36);  // [kTailRing][4] nodes with a non-finite V
+  uint64_t* s_full = bars + 20;     // [softmax group], as the following
+  uint64_t* p_full = bars + 22;     // [softmax group][half of the tile]
+  uint64_t* o_done = bars + 26;
+  uint64_t* q_full = bars + 28;
+  uint64_t* q_free = bars + 30;     // (RT = 1) both groups are done with the shared Q
+  uint32_t* s_bad = reinterpret_cast<uint32_t*>(bars + 32);  // [kTailRing][4] nodes with a non-finite V
   int* s_ex = reinterpret_cast<int*>(s_bad + 4 * kTailRing);  // [8 softmax warps][32] exponents of the rows of Q
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_ex + 256);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -298,12 +347,10 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       bar_init(&k_empty[i], RT);  // one commit per group that uses the tile
       bar_init(&v_full[i], 4);
       bar_init(&v_empty[i], RT);
-      bar_init(&s_full[2 * i], 1);
-      bar_init(&s_full[2 * i + 1], 1);
+      bar_init(&s_full[i], 1);
       bar_init(&p_full[2 * i], 4);
       bar_init(&p_full[2 * i + 1], 4);
       bar_init(&o_done[i], 1);
-      bar_init(&o_last[i], 1);
       bar_init(&q_full[i], 4);
     }
     bar_init(q_free, 8);
@@ -336,7 +383,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   fence_after();
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;
-  // TMEM columns: S (and P) of group w at 128 w, O of group w at 256 + 128 w
+  // TMEM columns: S of group w at 128 w, its P over S's first half, O of group w at 256 + 128 w
   const int Qn = g.KVH * g.RG;
   const int vu_exp = static_cast<int>(__float_as_uint(kv.v_unit) >> 23) - 127;
   int T_raw = 0;  // (producers) tiles issued
@@ -398,104 +445,62 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       } while (live && p.next(g, kv, kv_len));
     }
     // One issuing thread per softmax group: neither group's products wait behind the other
-    // group's barriers.  S runs a step (64 keys) ahead of O within a part.
+    // group's barriers.
     if ((warp == 1 || warp == 2) && lane == 0 && work) {
-      constexpr uint32_t idS = idesc_16(kStep, 0, false);
+      constexpr uint32_t idS = idesc_16(kKeys, 0, false);
       const int w = warp - 1;
       const uint64_t q_desc = desc_sw128(su32(sQ) + (RT == 2 ? w : 0) * kOpB, 16, 1024);
       const uint64_t k_desc = desc_sw128(su32(sK), 16, 1024);
       const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
       const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
-      struct Cursor {
-        Parts p;
-        int x;              // tile of the pair
-        uint32_t t;         // tile of the CTA
-        uint32_t n, part;   // steps of the group before this one, parts before this one
-        bool half, fresh;   // second half of the tile; first step of the part
-        bool on;
-      };
-      // the group's first tile at or after the part's start (RT = 1: it may have none)
-      auto enter = [&](Cursor& c) {
-        c.fresh = true;
-        c.half = false;
-        for (;;) {
-          c.x = c.p.x0;
-          if (RT == 1 && w == 1) ++c.x, ++c.t;
-          if (c.x < c.p.x1) return;
-          c.t -= static_cast<uint32_t>(c.x - c.p.x1);
-          c.on = c.p.next(g, kv, kv_len);
-          ++c.part;
-          if (!c.on) return;
-        }
-      };
-      auto last_half = [&](const Cursor& c) { return c.half || c.p.left(g, c.x) <= kStep; };
-      auto advance = [&](Cursor& c) {
-        ++c.n;
-        c.fresh = false;
-        if (!last_half(c)) {
-          c.half = true;
-          return;
-        }
-        c.half = false;
-        c.x += RT == 1 ? 2 : 1;
-        c.t += RT == 1 ? 2 : 1;
-        if (c.x >= c.p.x1) {
-          c.t -= static_cast<uint32_t>(c.x - c.p.x1);
-          c.on = c.p.next(g, kv, kv_len);
-          ++c.part;
-          if (c.on) enter(c);
-        }
-      };
-      Cursor s{first, 0, 0u, 0u, 0u, false, true, true};
-      enter(s);
-      Cursor o = s;
+      Parts p = first;
+      uint32_t t0 = 0, n = 0, part = 0;  // tiles of the CTA before the part; the group's tiles; parts
       bool live = true;
-      auto issue_S = [&]() {
-        const uint32_t ks = s.t & 1, buf = s.n & 1;
-        if (!s.half) live = bar_wait(&k_full[ks], (s.t >> 1) & 1, abort);
-        if (s.fresh) live = live && bar_wait(&q_full[RT == 1 ? 0 : w], s.part & 1, abort);
-        // P of step n - 2, in this buffer, has been read.  (Where S does not run ahead, O of
-        // step n - 1 is on its way too and may end first: that one is waited for.)
-        const uint32_t behind = s.n == o.n ? 1u : 2u;
-        if (s.n >= behind) live = live && bar_wait(&o_done[w], (s.n - behind) & 1, abort);
-        if (!live) return;
-        fence_after();
-        const uint64_t kd = k_desc + static_cast<uint64_t>(ks * (kOpB >> 4) + (s.half ? kStep * 128 >> 4 : 0));
+      do {
+        const int x_first = p.x0 + (RT == 1 ? w : 0);
+        for (int x = x_first; live && x < p.x1; x += RT == 1 ? 2 : 1, ++n) {
+          const uint32_t t = t0 + static_cast<uint32_t>(x - p.x0), st = t & 1;
+          // S over the P that the last O product has read.  (Q is waited for behind K: where
+          // RT = 1 and the second group had no tile in the parts before, K's stage says that
+          // their Q has been used, so that the barrier is in this part's phase.)
+          live = bar_wait(&k_full[st], (t >> 1) & 1, abort) && (x > x_first || bar_wait(&q_full[RT == 1 ? 0 : w], part & 1, abort)) &&
+                 (n == 0 || bar_wait(&o_done[w], (n - 1) & 1, abort));
+          if (!live) break;
+          fence_after();
+          const uint64_t kd = k_desc + static_cast<uint64_t>(st * (kOpB >> 4));
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
 #pragma unroll
-        for (int kk = 0; kk < kHD / 16; ++kk) {
-          const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kHalfB >> 4) + (kk & 3) * 2);
-          umma(tS + buf * kStep, q_desc + off, kd + off, idS, kk > 0 ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t off = static_cast<uint64_t>(half * (kHalfB >> 4) + kk * 2);
+              umma(tS, q_desc + off, kd + off, idS, half + kk > 0 ? 1u : 0u);
+            }
+          }
+          umma_commit(&s_full[w]);
+          umma_commit(&k_empty[st]);
+          live = bar_wait(&v_full[st], (t >> 1) & 1, abort);
+          const uint64_t vd = v_desc + static_cast<uint64_t>(st * (kOpB >> 4));
+          const bool two = p.left(g, x) > kStep;
+          const uint32_t idO = x >= p.NT ? idesc_16(kHD, 1, true) : idesc_16(kHD, 1, false);  // tree nodes' V stays bf16
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            live = live && bar_wait(&p_full[2 * w + half], n & 1, abort);
+            if (!live) break;
+            fence_after();
+            if (half == 0 || two) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_ts(tO, tS + half * 32 + kk * 8, vd + static_cast<uint64_t>(((half * kStep + kk * 16) * 128) >> 4), idO,
+                        half + kk > 0 || x > x_first ? 1u : 0u);  // the first of a part starts O
+            }
+          }
+          if (!live) break;
+          umma_commit(&o_done[w]);
+          umma_commit(&v_empty[st]);
         }
-        umma_commit(&s_full[2 * w + buf]);
-        if (last_half(s)) umma_commit(&k_empty[ks]);
-        advance(s);
-      };
-      auto issue_O = [&]() {
-        const uint32_t vs = o.t & 1, buf = o.n & 1;
-        if (!o.half) live = bar_wait(&v_full[vs], (o.t >> 1) & 1, abort);
-        live = live && bar_wait(&p_full[2 * w + buf], (o.n >> 1) & 1, abort);
-        if (!live) return;
-        fence_after();
-        const uint64_t vd = v_desc + static_cast<uint64_t>(vs * (kOpB >> 4) + (o.half ? kStep * 128 >> 4 : 0));
-        const uint32_t idO = o.x >= o.p.NT ? idesc_16(kHD, 1, true) : idesc_16(kHD, 1, false);  // tree nodes' V stays bf16
-#pragma unroll
-        for (int kk = 0; kk < kStep / 16; ++kk)
-          umma_ts(tO, tS + buf * kStep + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), idO,
-                  kk > 0 || !o.fresh ? 1u : 0u);  // the first step of a part starts O
-        umma_commit(&o_done[w]);
-        if (last_half(o)) umma_commit(&v_empty[vs]);
-        const uint32_t part = o.part;
-        advance(o);
-        if (o.part != part) umma_commit(&o_last[w]);
-      };
-      if (s.on) issue_S();
-      while (live && o.on) {
-        // (the first S of a part needs the new Q, which its group writes after the last O)
-        const bool ahead = s.on && s.part == o.part && s.n == o.n + 1;
-        if (ahead) issue_S();
-        if (live) issue_O();
-        if (live && s.on && s.n == o.n) issue_S();
-      }
+        t0 += static_cast<uint32_t>(p.x1 - p.x0);
+        ++part;
+      } while (live && p.next(g, kv, kv_len));
     }
   } else if (warp >= kDeq0) {
     regs_dec<kRegsDeq>();
@@ -530,106 +535,76 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         unsigned char* dst = (op ? sV : sK) + dst_st * kOpB;
         if (!nodes) {
           const unsigned char *codes = raw, *scales = raw + kCodeB;
-          uint4 w4[4];
-          uint32_t e4[4];
+#pragma unroll 1
+          for (int i0 = 0; i0 < 4; i0 += 2) {
+            uint4 w4[2];
+            uint32_t e4[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = dw * 32 + i * 8 + (lane >> 2);
-            w4[i] = *reinterpret_cast<const uint4*>(codes + key * (kHD / 2) + q * 16);
-            e4[i] = *reinterpret_cast<const uint16_t*>(scales + key * (kHD / 16) + 2 * q);
-            if (key >= left) e4[i] = 0u;  // beyond the prefix: adds 0 whatever the slot holds
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = dw * 32 + i * 8 + (lane >> 2);
-            const uint32_t e = h2u(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(e4[i]), __NV_E4M3))));
-            uint32_t ea = __byte_perm(e, e, 0x1010), eb = __byte_perm(e, e, 0x3232);
-            uint32_t w[4] = {w4[i].x, w4[i].y, w4[i].z, w4[i].w};
-            // the four 16-byte pieces in an order that differs between the lanes which
-            // store together, so that their banks do
-            const int flip = ((q >> 1) & 1) | ((key & 1) << 1);
-            if (flip & 1) {
-              const uint32_t a = w[0], b = w[2];
-              w[0] = w[1], w[1] = a, w[2] = w[3], w[3] = b;
+            for (int i = 0; i < 2; ++i) {
+              const int key = dw * 32 + (i0 + i) * 8 + (lane >> 2);
+              w4[i] = *reinterpret_cast<const uint4*>(codes + key * (kHD / 2) + q * 16);
+              e4[i] = *reinterpret_cast<const uint16_t*>(scales + key * (kHD / 16) + 2 * q);
+              if (key >= left) e4[i] = 0u;  // beyond the prefix: adds 0 whatever the slot holds
             }
-            if (flip & 2) {
-              uint32_t a = w[0], b = w[1];
-              w[0] = w[2], w[1] = w[3], w[2] = a, w[3] = b;
-              a = ea, ea = eb, eb = a;
-            }
-            unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int chunk = 4 * (q & 1) + (k ^ flip);
-              *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = decode8(w[k], u2h(k < 2 ? ea : eb));
+            for (int i = 0; i < 2; ++i) {
+              const int key = dw * 32 + (i0 + i) * 8 + (lane >> 2);
+              const uint32_t e = h2u(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(e4[i]), __NV_E4M3))));
+              uint32_t ea = __byte_perm(e, e, 0x1010), eb = __byte_perm(e, e, 0x3232);
+              uint32_t w[4] = {w4[i].x, w4[i].y, w4[i].z, w4[i].w};
+              // the four 16-byte pieces in an order that differs between the lanes which
+              // store together, so that their banks do
+              const int flip = ((q >> 1) & 1) | ((key & 1) << 1);
+              if (flip & 1) {
+                const uint32_t a = w[0], b = w[2];
+                w[0] = w[1], w[1] = a, w[2] = w[3], w[3] = b;
+              }
+              if (flip & 2) {
+                uint32_t a = w[0], b = w[1];
+                w[0] = w[2], w[1] = w[3], w[2] = a, w[3] = b;
+                a = ea, ea = eb, eb = a;
+              }
+              unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int chunk = 4 * (q & 1) + (k ^ flip);
+                *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = decode8(w[k], u2h(k < 2 ? ea : eb));
+              }
             }
           }
         } else {
           // tree nodes: K to fp16, each key's largest magnitude scaled to [1, 2) (its scores
           // get the factor back); V as it is stored, its product runs in bf16
-          const __nv_bfloat16* from = static_cast<const __nv_bfloat16*>(op ? tail.v : tail.k);
-          long long rows[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {  // the pages of all rows at once
-            const int key = dw * 32 + i * 8 + (lane >> 2), j = (x - p.NT) * kKeys + key;
-            rows[i] = -1;
-            if (key < left) {
-              const int pi = j / tail.page_size;
-              const int page = tail.page_table[static_cast<size_t>(p.b) * tail.max_pages + pi];
-              if (page >= 0 && page < tail.n_pages)
-                rows[i] = (static_cast<long long>(page) * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size);
-              else
-                dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
-            }
+          int own = -1;  // this lane's row of the warp's 32
+          if (dw * 32 + lane < left) {
+            const int j = (x - p.NT) * kKeys + dw * 32 + lane, pi = j / tail.page_size;
+            const int page = tail.page_table[static_cast<size_t>(p.b) * tail.max_pages + pi];
+            if (page >= 0 && page < tail.n_pages)
+              own = (page * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size);
+            else
+              dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
           }
-          uint32_t bad_v = 0u;  // this warp's keys with a non-finite V
-#pragma unroll 1
-          for (int i0 = 0; i0 < 4; i0 += 2) {
-            uint4 y[2][4];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const long long row = i0 ? rows[2 + h] : rows[h];
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                y[h][c] = row >= 0 ? reinterpret_cast<const uint4*>(from + row * kHD + 32 * q)[c] : make_uint4(0u, 0u, 0u, 0u);
+          unsigned char* slab = dst + dw * 32 * 128;
+          bring_rows(static_cast<const __nv_bfloat16*>(op ? tail.v : tail.k), own, slab, lane);
+          // a node with a NaN or an Inf leaves the product: its scores get a NaN factor, rows
+          // that see its V are marked
+          if (op == 0) {
+            rows_to_half(slab, lane, [&](int rr, uint32_t am, int ex) {
+              s_fac[slot * kKeys + dw * 32 + rr] = am >= 0x7F80u ? __int_as_float(0x7FC00000) : pow2f(ex);
+            });
+          } else {
+            uint32_t bad_v = 0u;
+#pragma unroll 2
+            for (int i = 0; i < 16; ++i) {
+              uint4* at = reinterpret_cast<uint4*>(row_chunk(slab, 2 * i + (lane >> 4), lane & 15));
+              const uint32_t am = max_bits(*at);
+              const bool bad = max(am & 0xFFFFu, am >> 16) >= 0x7F80u;
+              if (bad) *at = make_uint4(0u, 0u, 0u, 0u);
+              const uint32_t hit = __ballot_sync(0xFFFFFFFFu, bad);
+              bad_v |= ((hit & 0xFFFFu) ? 1u << (2 * i) : 0u) | (hit >> 16 ? 2u << (2 * i) : 0u);
             }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int key = dw * 32 + (i0 + h) * 8 + (lane >> 2);
-              uint32_t am = 0u;  // largest magnitude of the node's row as bf16 bits, the same in its four lanes
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                am = __vmaxu2(am, __vmaxu2(__vmaxu2(y[h][c].x & 0x7FFF7FFFu, y[h][c].y & 0x7FFF7FFFu),
-                                           __vmaxu2(y[h][c].z & 0x7FFF7FFFu, y[h][c].w & 0x7FFF7FFFu)));
-              am = max(am & 0xFFFFu, am >> 16);
-              am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-              am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-              // a node with a NaN or an Inf leaves the product: its scores get a NaN factor,
-              // rows that see its V are marked
-              const bool bad = am >= 0x7F80u;
-              const int ex = max(static_cast<int>(am >> 7), 1) - 127;
-              if (op == 0 && q == 0) s_fac[slot * kKeys + key] = bad ? __int_as_float(0x7FC00000) : pow2f(ex);
-              if (bad) bad_v |= 1u << (key & 31);
-              const int na = -ex / 2;
-              const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
-              const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
-              unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                uint32_t w[4] = {y[h][c].x, y[h][c].y, y[h][c].z, y[h][c].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  if (op == 0)
-                    w[k] = h2u(__floats2half2_rn(__uint_as_float(w[k] << 16) * f0 * f1, __uint_as_float(w[k] & 0xFFFF0000u) * f0 * f1));
-                  if (bad) w[k] = 0u;
-                }
-                const int chunk = 4 * (q & 1) + c;
-                *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            }
+            if (lane == 0) s_bad[slot * 4 + dw] = bad_v;
           }
-          bad_v = __reduce_or_sync(0xFFFFFFFFu, bad_v);
-          if (op == 1 && lane == 0) s_bad[slot * 4 + dw] = bad_v;
         }
         fence_async_smem();  // generic-proxy writes -> tensor core
         __syncwarp();
@@ -658,7 +633,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
     const uint32_t tS = tmem + grp * 128 + lane_base, tO = tmem + 256 + grp * 128 + lane_base;
     if (work) {
       Parts p = first;
-      uint32_t n_step = 0, n_last = 0;
+      uint32_t n_tile = 0;
       int ntail = 0, n_part = 0;
       bool live = true;
       do {
@@ -666,46 +641,16 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         const int gr = (rg * RT + (RT == 2 ? grp : 0)) * kRows + r;  // row of the KV head
         const bool row_ok = gr < g.G * g.R;
         const int node = row_ok ? gr / g.G : 0, head = kvh * g.G + (row_ok ? gr - node * g.G : 0);
-        // Q to fp16, each row's largest magnitude scaled to [1, 2): half a warp to a row, so
-        // that rows are read and written in whole lines; the exponents meet their rows in s_ex
+        // Q to fp16; the rows' powers of two meet them in s_ex
         int* ex_rows = s_ex + (RT == 2 ? grp : 0) * kRows + quarter * 32;
         if (RT == 2 || grp == 0) {
-          const int own = row_ok ? node * g.H + head : -1;
-          const int chunk = lane & 15;
-          const uint4* qb = reinterpret_cast<const uint4*>(Q + static_cast<size_t>(p.b) * g.R * g.H * kHD) + chunk;
-          unsigned char* to = sQ + (RT == 2 ? grp : 0) * kOpB + (chunk >> 3) * kHalfB + quarter * 32 * 128;
-#pragma unroll 1
-          for (int i0 = 0; i0 < 16; i0 += 8) {
-            uint4 y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int at = __shfl_sync(0xFFFFFFFFu, own, 2 * (i0 + i) + (lane >> 4));
-              y[i] = at >= 0 ? qb[static_cast<size_t>(at) * (kHD / 8)] : make_uint4(0u, 0u, 0u, 0u);
-            }
-            // (RT = 1: the other group's products of the last part have read the shared Q)
-            if (RT == 1 && i0 == 0 && n_part > 0 && !warp_wait(q_free, (n_part - 1) & 1, abort)) live = false;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int rr = 2 * (i0 + i) + (lane >> 4);
-              uint32_t am = __vmaxu2(__vmaxu2(y[i].x & 0x7FFF7FFFu, y[i].y & 0x7FFF7FFFu),
-                                     __vmaxu2(y[i].z & 0x7FFF7FFFu, y[i].w & 0x7FFF7FFFu));
-#pragma unroll
-              for (int o = 8; o > 0; o >>= 1) am = __vmaxu2(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-              am = max(am & 0xFFFFu, am >> 16);
-              // (below 2^-64 a row's scores are as good as zero, and its factor would underflow)
-              const int ex = max(static_cast<int>(am >> 7) - 127, -64);
-              if (chunk == 0) ex_rows[rr] = ex;
-              const int na = -ex / 2;
-              const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
-              const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
-              const uint32_t w[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
-              uint32_t h[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                h[k] = h2u(__floats2half2_rn(__uint_as_float(w[k] << 16) * f0 * f1, __uint_as_float(w[k] & 0xFFFF0000u) * f0 * f1));
-              *reinterpret_cast<uint4*>(to + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-          }
+          // (RT = 1: the other group's products of the last part have read the shared Q)
+          if (RT == 1 && n_part > 0 && !warp_wait(q_free, (n_part - 1) & 1, abort)) live = false;
+          unsigned char* slab = sQ + (RT == 2 ? grp : 0) * kOpB + quarter * 32 * 128;
+          bring_rows(Q + static_cast<size_t>(p.b) * g.R * g.H * kHD, row_ok ? node * g.H + head : -1, slab, lane);
+          // (a row with a NaN or an Inf: a NaN factor.  Below 2^-64 a row's scores are as good
+          // as zero, and their factor would underflow)
+          rows_to_half(slab, lane, [&](int rr, uint32_t am, int ex) { ex_rows[rr] = am >= 0x7F80u ? 128 : max(ex, -64); });
           fence_async_smem();
           __syncwarp();
           if (lane == 0) bar_arrive(&q_full[grp]);
@@ -713,9 +658,10 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         // (RT = 1: the groups begin a part together, so that neither frees the shared Q twice
         // while the other is a part behind)
         if (RT == 1 && grp == 1 && !warp_wait(&q_full[0], n_part & 1, abort)) live = false;
-        const float c2 = fmaxf(sm_scale * kLog2e * pow2f(ex_rows[lane]), 1e-37f), c2p = c2 * kv.k_unit;
+        const int q_ex = ex_rows[lane];
+        const float c2 = q_ex == 128 ? __int_as_float(0x7FC00000) : fmaxf(sm_scale * kLog2e * pow2f(q_ex), 1e-37f);
         float m = -INFINITY, l = 0.0f;
-        int ue = vu_exp, mine = 0;  // exponent of O's unit; this group's steps of the part
+        int ue = vu_exp, mine = 0;  // exponent of O's unit; this group's tiles of the part
         const int tail0 = ntail;
         const int words = (g.R + 63) >> 6;
         const uint64_t* mrow = mask + (static_cast<size_t>(p.b) * g.R + node) * words;
@@ -724,115 +670,121 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           const int slot = ntail % kTailRing;
           if (nodes) ++ntail;
           if (RT == 1 && ((x - p.x0) & 1) != grp) continue;
-          const int left = p.left(g, x);
+          const int left = p.left(g, x), halves = left > kStep ? 2 : 1;
+          const bool all = !nodes && left >= kKeys;
+          // keys the row sees: those that exist, or the ancestors among the nodes
+          uint64_t see[2] = {left >= 64 ? ~0ull : (1ull << left) - 1ull, left >= 128 ? ~0ull : left > 64 ? (1ull << (left - 64)) - 1ull : 0ull};
+          if (nodes) {
+            const int wd = 2 * (x - p.NT);
+            see[0] &= row_ok ? mrow[wd] : 0ull;
+            see[1] &= row_ok && wd + 1 < words ? mrow[wd + 1] : 0ull;
+          }
           // O's unit: the cache's under the prefix; the nodes' weights carry 2^-kNodeExp, so that
           // products with any finite V stay finite
           const int tile_ue = nodes ? kNodeExp : vu_exp;
+          const float c = nodes ? c2 : c2 * kv.k_unit;
+          if (!warp_wait(&s_full[grp], n_tile & 1, abort)) {
+            live = false;
+            break;
+          }
+          fence_after();
+          if (!all) {  // the nodes' factors, and -Inf where unseen (whose exponential is 0)
 #pragma unroll 1
-          for (int h = 0; h < 2 && left > kStep * h; ++h) {
-            // keys the row sees: all, those that exist, or the ancestors among the nodes
-            uint64_t see = ~0ull;
-            const bool full = !nodes && left >= kStep * (h + 1);
-            if (!full) {
-              const int n = left - kStep * h;
-              see = n >= 64 ? ~0ull : (1ull << n) - 1ull;
-              if (nodes) {
-                const int wd = 2 * (x - p.NT) + h;
-                see &= wd < words && row_ok ? mrow[wd] : 0ull;
+            for (int d = 0; d < 4 * halves; ++d) {
+              uint32_t y[16];
+              tmem_ld16(tS + 16 * d, y);
+              const uint32_t sb = static_cast<uint32_t>((d < 4 ? see[0] : see[1]) >> (16 * (d & 3)));
+              const float4* fac = reinterpret_cast<const float4*>(s_fac + slot * kKeys + 16 * d);
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) {
+                const float4 f = nodes ? fac[j / 4] : make_float4(1.f, 1.f, 1.f, 1.f);
+                y[j] = sb & (1u << j) ? __float_as_uint(__uint_as_float(y[j]) * f.x) : 0xFF800000u;
+                y[j + 1] = sb & (2u << j) ? __float_as_uint(__uint_as_float(y[j + 1]) * f.y) : 0xFF800000u;
+                y[j + 2] = sb & (4u << j) ? __float_as_uint(__uint_as_float(y[j + 2]) * f.z) : 0xFF800000u;
+                y[j + 3] = sb & (8u << j) ? __float_as_uint(__uint_as_float(y[j + 3]) * f.w) : 0xFF800000u;
               }
+              tmem_st16(tS + 16 * d, y);
             }
-            const uint32_t buf = n_step & 1;
-            if (!warp_wait(&s_full[2 * grp + buf], (n_step >> 1) & 1, abort)) {
-              live = false;
-              break;
+            tmem_st_wait();
+          }
+          float tmax = -INFINITY;
+#pragma unroll 1
+          for (int h = 0; h < halves; ++h) {
+            float2 v[32];
+            tmem_ld64(tS + kStep * h, v);
+            float a0 = fmaxf(v[0].x, v[0].y), a1 = fmaxf(v[1].x, v[1].y), a2 = fmaxf(v[2].x, v[2].y), a3 = fmaxf(v[3].x, v[3].y);
+#pragma unroll
+            for (int j = 4; j < 32; j += 4) {
+              a0 = fmax3f(a0, v[j].x, v[j].y);
+              a1 = fmax3f(a1, v[j + 1].x, v[j + 1].y);
+              a2 = fmax3f(a2, v[j + 2].x, v[j + 2].y);
+              a3 = fmax3f(a3, v[j + 3].x, v[j + 3].y);
             }
-            fence_after();
-            // One step's scores to probabilities; ALL: every key is seen and the factor is
-            // the cache's (the other steps' factors and masks are applied element by
-            // element).  False: a wait ran out.
-            auto step = [&](auto all) -> bool {
-              constexpr bool ALL = decltype(all)::value;
-              const float c = ALL ? c2p : c2;
+            tmax = fmax3f(tmax, fmaxf(a0, a1), fmaxf(a2, a3));
+          }
+          tmax *= c;
+          // the base moves when passed by more than 2^15; O's unit when the tile's V has another
+          const bool move = tmax > m + kTop;
+          const bool unit = tile_ue != ue && mine > 0;
+          float corr = 1.0f;
+          if (move) {
+            const float nm = fmaxf(m, tmax - kHead);
+            corr = ex2(m - nm);
+            l *= corr;
+            m = nm;
+          }
+          if (unit) corr *= pow2f(ue - tile_ue);
+          ue = tile_ue;
+          if (mine > 0 && __any_sync(0xFFFFFFFFu, move || unit)) {
+            // (O of the last tile is done: S of this one was issued after it)
+#pragma unroll 1
+            for (int d = 0; d < 8; ++d) {
+              uint32_t y[16];
+              tmem_ld16(tO + 16 * d, y);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
+              tmem_st16(tO + 16 * d, y);
+            }
+          }
+          const float2 cv = make_float2(c, c);
+          const float sub = (m == -INFINITY ? 0.0f : m) + static_cast<float>(nodes ? kNodeExp : 0);
+          const float2 nv = make_float2(-sub, -sub);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          // P of 64 keys goes over 32 columns of S's first half, whose scores have been read
+          // when the second half's P comes
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (h < halves) {
               float2 v[32];
-              tmem_ld64(tS + buf * kStep, v);
-              if (!ALL) {  // factors, and -Inf where unseen (whose exponential is 0)
-                const float2* fac = reinterpret_cast<const float2*>(s_fac + slot * kKeys + kStep * h);
-                const uint32_t s0 = static_cast<uint32_t>(see), s1 = static_cast<uint32_t>(see >> 32);
+              tmem_ld64(tS + kStep * h, v);
+              auto probs = [&](auto pack) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                  if (j % 8 == 0) asm volatile("" ::: "memory");  // (few factors at a time in registers)
-                  const float2 f = nodes ? fac[j] : make_float2(kv.k_unit, kv.k_unit);
-                  const uint32_t sb = j < 16 ? s0 : s1;
-                  v[j].x = sb & (1u << (2 * j & 31)) ? v[j].x * f.x : -INFINITY;
-                  v[j].y = sb & (2u << (2 * j & 31)) ? v[j].y * f.y : -INFINITY;
+                for (int q = 0; q < 2; ++q) {
+                  uint32_t pk[16];
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) {
+                    const float2 a = __ffma2_rn(v[16 * q + j], cv, nv);
+                    const float2 e = make_float2(ex2(a.x), ex2(a.y));
+                    sum[j & 1] = __fadd2_rn(sum[j & 1], e);
+                    pk[j] = pack(e);
+                  }
+                  tmem_st16(tS + 32 * h + 16 * q, pk);
                 }
-              }
-              float a0 = fmaxf(v[0].x, v[0].y), a1 = fmaxf(v[1].x, v[1].y), a2 = fmaxf(v[2].x, v[2].y), a3 = fmaxf(v[3].x, v[3].y);
-#pragma unroll
-              for (int j = 4; j < 32; j += 4) {
-                a0 = fmax3f(a0, v[j].x, v[j].y);
-                a1 = fmax3f(a1, v[j + 1].x, v[j + 1].y);
-                a2 = fmax3f(a2, v[j + 2].x, v[j + 2].y);
-                a3 = fmax3f(a3, v[j + 3].x, v[j + 3].y);
-              }
-              const float tmax = fmaxf(fmaxf(a0, a1), fmaxf(a2, a3)) * c;
-              // the base moves when passed by more than 2^15; O's unit when the tile's V has another
-              const bool move = tmax > m + kTop;
-              const bool unit = tile_ue != ue && mine > 0;
-              float corr = 1.0f;
-              if (move) {
-                const float nm = fmaxf(m, tmax - kHead);
-                corr = ex2(m - nm);
-                l *= corr;
-                m = nm;
-              }
-              if (unit) corr *= pow2f(ue - tile_ue);
-              ue = tile_ue;
-              const bool rescale = mine > 0 && __any_sync(0xFFFFFFFFu, move || unit);
-              const float2 cv = make_float2(c, c);
-              const float sub = ALL ? m : (m == -INFINITY ? 0.0f : m) + (nodes ? kNodeExp : 0);
-              const float2 nv = make_float2(-sub, -sub);
-              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {  // P of 32 keys goes over 16 columns: the scores are in registers
-                uint32_t pk[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const float2 a = __ffma2_rn(v[16 * q + j], cv, nv);
-                  const float2 e = make_float2(ex2(a.x), ex2(a.y));
-                  sum[j & 1] = __fadd2_rn(sum[j & 1], e);
-                  pk[j] = !ALL && nodes ? pack2_bf16(e.x, e.y) : h2u(__float22half2_rn(e));
-                }
-                tmem_st16(tS + buf * kStep + 16 * q, pk);
-              }
-              const float2 st = __fadd2_rn(sum[0], sum[1]);
-              l += ALL || !nodes ? st.x + st.y : (st.x + st.y) * pow2f(kNodeExp);
-              if (rescale) {
-                if (!warp_wait(&o_done[grp], (n_step - 1) & 1, abort)) return false;
-                fence_after();
-#pragma unroll 1
-                for (int d = 0; d < 8; ++d) {  // in 16-column steps, to keep register pressure low
-                  uint32_t y[16];
-                  tmem_ld16(tO + 16 * d, y);
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
-                  tmem_st16(tO + 16 * d, y);
-                  tmem_st_wait();
-                }
-              }
+              };
+              if (nodes)
+                probs([](float2 e) { return pack2_bf16(e.x, e.y); });
+              else
+                probs([](float2 e) { return h2u(__float22half2_rn(e)); });
               tmem_st_wait();
-              return true;
-            };
-            if (!(full ? step(std::true_type{}) : step(std::false_type{}))) {
-              live = false;
-              break;
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(&p_full[2 * grp + buf]);
-            ++n_step;
-            ++mine;
+            if (lane == 0) bar_arrive(&p_full[2 * grp + h]);
           }
+          const float2 st = __fadd2_rn(sum[0], sum[1]);
+          l += (st.x + st.y) * (nodes ? pow2f(kNodeExp) : 1.0f);
+          ++n_tile;
+          ++mine;
         }
         if (!live) break;
         if (RT == 1) {  // this group's S products have read Q
@@ -841,8 +793,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         }
         // the part's record: o normalized by its own sum, the base and the sum
         if (mine > 0) {
-          // (a barrier of its own: up to two of the steps' phases may be open here)
-          if (!warp_wait(&o_last[grp], n_last++ & 1, abort)) {
+          if (!warp_wait(&o_done[grp], (n_tile - 1) & 1, abort)) {
             live = false;
             break;
           }
