@@ -47,13 +47,14 @@ constexpr int kCodeB = kKeys * kHD / 2;  // bytes of a tile's codes, per operand
 constexpr int kScaleB = kKeys * kHD / 16;
 constexpr int kRawB = kCodeB + kScaleB;  // of one operand
 constexpr int kTailRing = 8;             // tiles of tree nodes whose factors are kept (at most five are in flight)
-// Warpgroups: 0 = producers and MMA issuers, 1 and 2 = softmax, 3 =
-// dequantizers.  Registers move from the first and the last to the softmax groups, whose
-// threads hold a row of scores each; launch_tc checks that the launch brings the sum.
-constexpr int kThreads = 512;
+// Warpgroups: 0 = producers and MMA issuers, 1 and 2 = softmax, 3 and 4 = dequantizers of K
+// and of V.  Registers move from the others to the softmax groups; launch_tc checks that the
+// launch brings the sum.
+constexpr int kThreads = 640;
 constexpr int kSoftmax0 = 4, kDeq0 = 12;
-constexpr int kRegsIssue = 64, kRegsSoftmax = 176, kRegsDeq = 88;
+constexpr int kRegsIssue = 56, kRegsSoftmax = 136, kRegsDeq = 72;
 constexpr int kNodeExp = 24;  // > kTop: a node's weight times a row of V sums below 2^(15 - 24 + 8) of it
+constexpr int kStagger = 0;
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
 template <int RT>
@@ -466,6 +467,9 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           live = bar_wait(&k_full[st], (t >> 1) & 1, abort) && (x > x_first || bar_wait(&q_full[RT == 1 ? 0 : w], part & 1, abort)) &&
                  (n == 0 || bar_wait(&o_done[w], (n - 1) & 1, abort));
           if (!live) break;
+          if (RT == 2 && w == 1 && x == x_first)
+            for (const long long c0 = clock64(); clock64() - c0 < kStagger;) {
+            }
           fence_after();
           const uint64_t kd = k_desc + static_cast<uint64_t>(st * (kOpB >> 4));
 #pragma unroll 1
@@ -505,31 +509,17 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   } else if (warp >= kDeq0) {
     regs_dec<kRegsDeq>();
     if (work) {
-      const int dw = warp - kDeq0, q = lane & 3;
-      // One operand (0: K, 1: V) of a tile.  K runs a tile ahead of V: the next tile's K does
-      // not wait for this tile's V stage, which both groups' O products have to leave first.
-      struct Cursor {
-        Parts p;
-        int x, T, ntail;
-        bool on;
-      };
-      auto advance = [&](Cursor& c) {
-        if (c.x >= c.p.NT) ++c.ntail;
-        ++c.T;
-        if (++c.x == c.p.x1) {
-          c.on = c.p.next(g, kv, kv_len);
-          c.x = c.p.x0;
-        }
-      };
-      auto convert = [&](const int op, const Cursor& cur) -> bool {
-        const Parts& p = cur.p;
-        const int x = cur.x, T = cur.T, slot = cur.ntail % kTailRing;
-        const int st = op ? T % C::RV : T % C::RK;
-        const int kvh = p.pq / g.RG;
-        if (!warp_wait(&raw_full[3 * op + st], (op ? T / C::RV : T / C::RK) & 1, abort)) return false;
-        const int dst_st = T & 1;
-        if (!warp_wait(op ? &v_empty[dst_st] : &k_empty[dst_st], ((T >> 1) & 1) ^ 1, abort)) return false;
-        const unsigned char* raw = sRaw + (op ? C::RK + st : st) * kRawB;
+      const int op = (warp - kDeq0) >> 2, dw = warp & 3, q = lane & 3;  // 0: K, 1: V
+      const int stages = op ? C::RV : C::RK;
+      Parts p = first;
+      int x = p.x0, ntail = 0;
+      uint32_t st = 0, raw_par = 0;  // raw stage and its parity
+      for (uint32_t T = 0;; ++T) {
+        const int slot = ntail % kTailRing, kvh = p.pq / g.RG;
+        if (!warp_wait(&raw_full[3 * op + st], raw_par, abort)) break;
+        const uint32_t dst_st = T & 1;
+        if (!warp_wait(op ? &v_empty[dst_st] : &k_empty[dst_st], ((T >> 1) & 1) ^ 1, abort)) break;
+        const unsigned char* raw = sRaw + (op * C::RK + st) * kRawB;
         const bool nodes = x >= p.NT;
         const int left = p.left(g, x);
         unsigned char* dst = (op ? sV : sK) + dst_st * kOpB;
@@ -612,17 +602,15 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           bar_arrive(op ? &v_full[dst_st] : &k_full[dst_st]);
           bar_arrive(&raw_empty[3 * op + st]);
         }
-        return true;
-      };
-      Cursor cur[2] = {{first, first.x0, 0, 0, true}, {first, first.x0, 0, 0, true}};
-      // K, then K and V in turn until both have ended (one call: the code is long)
-      int op = 0;
-      while (cur[1].on) {
-        if (cur[op].on) {
-          if (!convert(op, cur[op])) break;
-          advance(cur[op]);
+        if (nodes) ++ntail;
+        if (++st == static_cast<uint32_t>(stages)) {
+          st = 0;
+          raw_par ^= 1u;
         }
-        op = op == 0 && cur[1].T < cur[0].T - (cur[0].on ? 1 : 0) ? 1 : 0;
+        if (++x == p.x1) {
+          if (!p.next(g, kv, kv_len)) break;
+          x = p.x0;
+        }
       }
     }
   } else {
@@ -964,7 +952,7 @@ cudaError_t launch_tc(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_k
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, verify4_tc_kernel<RT>);
     if (e != cudaSuccess) return e;
-    if (4 * fa.numRegs < kRegsIssue + 2 * kRegsSoftmax + kRegsDeq) return cudaErrorLaunchOutOfResources;
+    if (kThreads / 128 * fa.numRegs < kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsDeq) return cudaErrorLaunchOutOfResources;
     attr_done.store(true, std::memory_order_release);
   }
   const cudaError_t e = launch_pdl(verify4_tc_kernel<RT>, dim3(g.workers), dim3(kThreads), Cfg<RT>::SMEM, s, 1, q, kv, tail,
