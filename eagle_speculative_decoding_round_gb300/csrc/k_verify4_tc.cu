@@ -857,7 +857,7 @@ __global__ void __launch_bounds__(128)
 verify4_tc_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __restrict__ kv_len,
                         const __grid_constant__ V4Geom g, const float* __restrict__ ws_o, const float2* __restrict__ ws_ml,
                         const int32_t* __restrict__ ends, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
-  constexpr int ROWS = RT * kRows, SPLIT = RT == 1 ? 2 : 1, AHEAD = 8;
+  constexpr int ROWS = RT * kRows, SPLIT = RT == 1 ? 2 : 1, AHEAD = 4;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) * 8 + (lane >> 3);
   const int strips = (g.G * g.R + 7) / 8;  // of a KV head (8 divides ROWS: none crosses a tile)
   const int b = blockIdx.x / (g.KVH * strips), in = blockIdx.x - b * (g.KVH * strips), kvh = in / strips;
@@ -875,18 +875,8 @@ verify4_tc_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* 
   const size_t rec = (pair + c0) * SPLIT;
   const float2* ml = ws_ml + rec * ROWS + (r - rt * ROWS);
   const float4* val = reinterpret_cast<const float4*>(ws_o + rec * (ROWS * kHD)) + quad * ROWS + (r - rt * ROWS);
-  float M = -INFINITY;
-  for (int q0 = lane >> 3; q0 < n; q0 += 4 * AHEAD) {
-    float2 y[AHEAD];
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) y[u] = q0 + 4 * u < n ? ml[(q0 + 4 * u) * ROWS] : make_float2(-INFINITY, 0.0f);
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u)
-      if (y[u].y != 0.0f) M = fmaxf(M, y[u].x);
-  }
-  M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, 8));
-  M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, 16));
-  float acc[8], den = 0.0f;
+  // the weights are kept relative to the largest base so far
+  float M = -INFINITY, acc[8], den = 0.0f;
 #pragma unroll
   for (int u = 0; u < 8; ++u) acc[u] = 0.0f;
   for (int q0 = 0; q0 < n; q0 += AHEAD) {
@@ -894,12 +884,23 @@ verify4_tc_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* 
     float4 x[AHEAD][2];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
-      y[u] = make_float2(0.0f, 0.0f);
+      y[u] = make_float2(-INFINITY, 0.0f);
       if (q0 + u < n) {
         y[u] = ml[(q0 + u) * ROWS];
         x[u][0] = val[static_cast<size_t>(q0 + u) * (ROWS * kHD / 4)];
         x[u][1] = val[static_cast<size_t>(q0 + u) * (ROWS * kHD / 4) + 4 * ROWS];
       }
+    }
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (y[u].y != 0.0f) top = fmaxf(top, y[u].x);
+    if (top > M) {
+      const float f = ex2(M - top);
+      M = top;
+      den *= f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) acc[u] *= f;
     }
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
