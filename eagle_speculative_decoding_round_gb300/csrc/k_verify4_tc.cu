@@ -219,25 +219,27 @@ __device__ __forceinline__ float pow2f(int e) {
 // The parts of one CTA's share, one after another; every role walks the same list.
 struct Parts {
   long long todo;
-  int b, pq, x0, x1, units;
-  int P, NT;  // the request's length, its prefix tiles
+  int b, pq, x0, x1;  // the pair; the part's tiles
+  int real, w1;       // the pair's tiles; the end of the part in units, where a pair has `extra` more of them
+  int P, NT, extra;   // the request's length, its prefix tiles
   __device__ __forceinline__ void take() {
-    x1 = static_cast<int>(min(static_cast<long long>(units), x0 + todo));
+    w1 = static_cast<int>(min(static_cast<long long>(real + extra), x0 + todo));
+    x1 = min(w1, real);
     NT = (P + kKeys - 1) / kKeys;
   }
   // keys of tile x that exist (more than 128 where it is not the last of its kind)
   __device__ __forceinline__ int left(const V4Geom& g, int x) const { return x >= NT ? g.R - (x - NT) * kKeys : P - x * kKeys; }
   // the next part; false at the end of the share
   __device__ __forceinline__ bool next(const V4Geom& g, const e3_kv4_layer& kv, const int32_t* kv_len) {
-    todo -= x1 - x0;
+    todo -= w1 - x0;
     if (todo <= 0) return false;
     x0 = 0;
     if (++pq == g.KVH * g.RG) {
       pq = 0;
       for (++b; b < g.B; ++b) {
         P = kv_len[b];
-        units = pair_units<kKeys>(g, kv, P);
-        if (units > 0) break;
+        real = pair_units<kKeys>(g, kv, P);
+        if (real > 0) break;
       }
       if (b >= g.B) return false;
     }
@@ -267,7 +269,7 @@ __device__ __forceinline__ unsigned char* row_chunk(unsigned char* slab, int rr,
 // rows `own` (a lane's own row, -1: zeros) of `from` into the slab
 __device__ __forceinline__ void bring_rows(const __nv_bfloat16* from, int own, unsigned char* slab, int lane) {
   const int c = lane & 15;
-#pragma unroll 2
+#pragma unroll 4
   for (int i = 0; i < 16; ++i) {
     const int rr = 2 * i + (lane >> 4);
     const int at = __shfl_sync(0xFFFFFFFFu, own, rr);
@@ -286,7 +288,7 @@ __device__ __forceinline__ uint32_t max_bits(const uint4& y) {
 // row with a NaN or an Inf becomes zeros.
 template <class F>
 __device__ __forceinline__ void rows_to_half(unsigned char* slab, int lane, F factor) {
-#pragma unroll 2
+#pragma unroll 4
   for (int i = 0; i < 16; ++i) {
     const int rr = 2 * i + (lane >> 4);
     uint4* at = reinterpret_cast<uint4*>(row_chunk(slab, rr, lane & 15));
@@ -367,17 +369,19 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
     for (int b = threadIdx.x; b < g.B; b += kThreads)
       if (pair_units<kKeys>(g, kv, kv_len[b]) == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
   const V4Place at = find_place<kKeys>(g, kv, kv_len, cta);
-  const bool work = at.b < g.B;
+  bool work = at.b < g.B;
   Parts first{};
   if (work) {
     first.b = at.b;
     first.P = kv_len[at.b];
     first.todo = at.share;
-    first.units = pair_units<kKeys>(g, kv, first.P);
+    first.real = pair_units<kKeys>(g, kv, first.P);
+    first.extra = at.extra;
     const long long off = at.share * cta - at.before;
-    first.pq = static_cast<int>(off / first.units);
-    first.x0 = static_cast<int>(off - static_cast<long long>(first.pq) * first.units);
+    first.pq = static_cast<int>(off / (first.real + at.extra));
+    first.x0 = static_cast<int>(off - static_cast<long long>(first.pq) * (first.real + at.extra));
     first.take();
+    if (first.x1 <= first.x0) work = first.next(g, kv, kv_len);
   }
   fence_before();
   __syncthreads();
@@ -584,7 +588,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
             });
           } else {
             uint32_t bad_v = 0u;
-#pragma unroll 2
+#pragma unroll 4
             for (int i = 0; i < 16; ++i) {
               uint4* at = reinterpret_cast<uint4*>(row_chunk(slab, 2 * i + (lane >> 4), lane & 15));
               const uint32_t am = max_bits(*at);
@@ -823,7 +827,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         if (grp == 0 && r == 0) {
           int32_t* e = ends + 2 * (static_cast<size_t>(p.b) * Qn + p.pq);
           if (p.x0 == 0) e[0] = cta;
-          if (p.x1 == p.units) e[1] = cta;
+          if (p.x1 == p.real) e[1] = cta;
         }
         ++n_part;
       } while (p.next(g, kv, kv_len));
@@ -851,14 +855,17 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
 
 // Merge of a pair's records.  A record holds its values as [dims / 4][rows][4], so that the
 // threads of the kernel above, a row each, write whole lines; here a block takes 8 rows of a
-// pair, a warp 32 dims of each: lane % 8 is the row, lane / 8 and lane / 8 + 4 the dims' quads.
-template <int RT>
-__global__ void __launch_bounds__(128)
+// pair, a warp NQ * 16 dims of each: lane % 8 is the row, lane / 8 the four dims (the second
+// four 16 dims on).  NQ = 1 has more loads in flight where a pair has many records, NQ = 2
+// less to set up where there are many rows: 1 and 32 requests' 61 nodes, whole calls, us:
+// NQ = 1 21.3 and 314, NQ = 2 24.7 and 296.
+template <int RT, int NQ>
+__global__ void __launch_bounds__(256 / NQ)
 verify4_tc_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __restrict__ kv_len,
                         const __grid_constant__ V4Geom g, const float* __restrict__ ws_o, const float2* __restrict__ ws_ml,
                         const int32_t* __restrict__ ends, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
-  constexpr int ROWS = RT * kRows, SPLIT = RT == 1 ? 2 : 1, AHEAD = 4;
-  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) * 8 + (lane >> 3);
+  constexpr int ROWS = RT * kRows, SPLIT = RT == 1 ? 2 : 1, AHEAD = 8 / NQ;
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) * (4 * NQ) + (lane >> 3);
   const int strips = (g.G * g.R + 7) / 8;  // of a KV head (8 divides ROWS: none crosses a tile)
   const int b = blockIdx.x / (g.KVH * strips), in = blockIdx.x - b * (g.KVH * strips), kvh = in / strips;
   const int r = (in - kvh * strips) * 8 + (lane & 7), rt = r / ROWS;  // row of the KV head
@@ -876,19 +883,19 @@ verify4_tc_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* 
   const float2* ml = ws_ml + rec * ROWS + (r - rt * ROWS);
   const float4* val = reinterpret_cast<const float4*>(ws_o + rec * (ROWS * kHD)) + quad * ROWS + (r - rt * ROWS);
   // the weights are kept relative to the largest base so far
-  float M = -INFINITY, acc[8], den = 0.0f;
+  float M = -INFINITY, acc[4 * NQ], den = 0.0f;
 #pragma unroll
-  for (int u = 0; u < 8; ++u) acc[u] = 0.0f;
+  for (int u = 0; u < 4 * NQ; ++u) acc[u] = 0.0f;
   for (int q0 = 0; q0 < n; q0 += AHEAD) {
     float2 y[AHEAD];
-    float4 x[AHEAD][2];
+    float4 x[AHEAD][NQ];
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u) {
       y[u] = make_float2(-INFINITY, 0.0f);
       if (q0 + u < n) {
         y[u] = ml[(q0 + u) * ROWS];
-        x[u][0] = val[static_cast<size_t>(q0 + u) * (ROWS * kHD / 4)];
-        x[u][1] = val[static_cast<size_t>(q0 + u) * (ROWS * kHD / 4) + 4 * ROWS];
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) x[u][k] = val[static_cast<size_t>(q0 + u) * (ROWS * kHD / 4) + 4 * k * ROWS];
       }
     }
     float top = M;
@@ -900,24 +907,26 @@ verify4_tc_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* 
       M = top;
       den *= f;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) acc[u] *= f;
+      for (int u = 0; u < 4 * NQ; ++u) acc[u] *= f;
     }
 #pragma unroll
     for (int u = 0; u < AHEAD; ++u)
       if (y[u].y != 0.0f) {  // (0: a record without keys, whose values were never written; a NaN sum stays one)
         const float w = y[u].y * ex2(y[u].x - M);
         den += w;
-        acc[0] = fmaf(w, x[u][0].x, acc[0]), acc[1] = fmaf(w, x[u][0].y, acc[1]);
-        acc[2] = fmaf(w, x[u][0].z, acc[2]), acc[3] = fmaf(w, x[u][0].w, acc[3]);
-        acc[4] = fmaf(w, x[u][1].x, acc[4]), acc[5] = fmaf(w, x[u][1].y, acc[5]);
-        acc[6] = fmaf(w, x[u][1].z, acc[6]), acc[7] = fmaf(w, x[u][1].w, acc[7]);
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) {
+          acc[4 * k] = fmaf(w, x[u][k].x, acc[4 * k]), acc[4 * k + 1] = fmaf(w, x[u][k].y, acc[4 * k + 1]);
+          acc[4 * k + 2] = fmaf(w, x[u][k].z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(w, x[u][k].w, acc[4 * k + 3]);
+        }
       }
   }
   if (!ok) return;
   const float inv = den != 0.0f ? 1.0f / den : 0.0f;
-  uint2* out = reinterpret_cast<uint2*>(O + row * kHD) + quad;
-  out[0] = make_uint2(pack2_bf16(acc[0] * inv, acc[1] * inv), pack2_bf16(acc[2] * inv, acc[3] * inv));
-  out[4] = make_uint2(pack2_bf16(acc[4] * inv, acc[5] * inv), pack2_bf16(acc[6] * inv, acc[7] * inv));
+#pragma unroll
+  for (int k = 0; k < NQ; ++k)
+    reinterpret_cast<uint2*>(O + row * kHD)[quad + 4 * k] =
+        make_uint2(pack2_bf16(acc[4 * k] * inv, acc[4 * k + 1] * inv), pack2_bf16(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
   if (quad == 0) lse[row] = den != 0.0f ? (M + log2f(den)) * kLn2 : -INFINITY;
 }
 
@@ -933,6 +942,10 @@ V4Geom make_geom_tc(int B, int R, int H, int KVH, int max_kv_len) {
   g.max_kv_len = max_kv_len;
   g.workers = num_sms();
   g.min_share = 1;
+  // A part costs about four tiles by itself (Q, the nodes, a record): counted, they even out
+  // the shares where requests differ in length.  32 requests of 512 to 8192 keys, us: 298
+  // without, 249, 241, 222, 221, 224 with 1, 2, 3, 4, 6.
+  g.extra = 4;
   return g;
 }
 
@@ -959,9 +972,13 @@ cudaError_t launch_tc(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_k
   const cudaError_t e = launch_pdl(verify4_tc_kernel<RT>, dim3(g.workers), dim3(kThreads), Cfg<RT>::SMEM, s, 1, q, kv, tail,
                                    kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, dev_err);
   if (e != cudaSuccess) return e;
-  return launch_pdl(verify4_tc_merge_kernel<RT>, dim3(static_cast<unsigned>(g.B) * g.KVH * ((g.G * g.R + 7) / 8)), dim3(128), 0, s, 1,
-                    kv, kv_len, g, static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml),
-                    static_cast<const int32_t*>(ends), o, lse);
+  const unsigned blocks = static_cast<unsigned>(g.B) * g.KVH * ((g.G * g.R + 7) / 8);
+  const float* co = ws_o;
+  const float2* cml = ws_ml;
+  const int32_t* ce = ends;
+  if (blocks > 4u * g.workers)
+    return launch_pdl(verify4_tc_merge_kernel<RT, 2>, dim3(blocks), dim3(128), 0, s, 1, kv, kv_len, g, co, cml, ce, o, lse);
+  return launch_pdl(verify4_tc_merge_kernel<RT, 1>, dim3(blocks), dim3(256), 0, s, 1, kv, kv_len, g, co, cml, ce, o, lse);
 }
 
 }  // namespace

@@ -35,6 +35,7 @@ struct V4Geom {
   int RG;       // row tiles of a KV head
   int workers;  // shares
   int min_share;
+  int extra;  // units that a pair counts beyond its own, for what a part costs by itself
   int max_kv_len;
 };
 
@@ -50,24 +51,30 @@ __device__ __forceinline__ int pair_units(const V4Geom& g, const e3_kv4_layer& k
 struct V4Place {
   long long share, before;  // units of a share; units before request b
   int b;                    // the request that holds the share's first unit (B: none)
+  int extra;                // a pair's further units: none where shares are small
 };
 template <int KEYS>
 __device__ __forceinline__ V4Place find_place(const V4Geom& g, const e3_kv4_layer& kv, const int32_t* kv_len, int worker) {
   const int lane = threadIdx.x & 31;
   const long long Q = static_cast<long long>(g.KVH) * g.RG;
   long long total = 0;
+  int live = 0;
   for (int b0 = 0; b0 < g.B; b0 += 32) {
     const int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv, kv_len[b0 + lane]) : 0;
     total += __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(u));
+    live += __popc(__ballot_sync(0xFFFFFFFFu, u > 0));
   }
   V4Place f;
+  f.extra = total * Q >= 8ll * g.workers ? g.extra : 0;
+  total += static_cast<long long>(live) * f.extra;
   f.share = max((total * Q + g.workers - 1) / g.workers, static_cast<long long>(g.min_share));
   const long long at = f.share * worker;
   long long base = 0;
   f.b = g.B;
   f.before = total * Q;
   for (int b0 = 0; b0 < g.B; b0 += 32) {
-    const int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv, kv_len[b0 + lane]) : 0;
+    int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv, kv_len[b0 + lane]) : 0;
+    if (u > 0) u += f.extra;
     unsigned incl = static_cast<unsigned>(u);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
