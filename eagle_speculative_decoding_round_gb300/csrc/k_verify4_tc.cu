@@ -152,31 +152,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
       : "r"(taddr));
 }
 #undef E3_R8
-__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// 64 columns of this thread's lane as register pairs (so that the packed arithmetic needs
-// no moves), one load and its wait
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, float2 (&v)[32]) {
-  unsigned long long q[32];
-#define E3_Q4(o) "=l"(q[o]), "=l"(q[o + 1]), "=l"(q[o + 2]), "=l"(q[o + 3])
-#define E3_M(i, a, b) " mov.b64 %" #i ", {t" #a ", t" #b "};\n"
-  asm volatile(
-      "{\n .reg .b32 t<64>;\n"
-      " tcgen05.ld.sync.aligned.32x32b.x64.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31,t3"
-      "2,t33,t34,t35,t36,t37,t38,t39,t40,t41,t42,t43,t44,t45,t46,t47,t48,t49,t50,t51,t52,t53,t54,t55,t56,t57,t58,t59,t60,t61,t62,t63}, [%32];\n"
-      " tcgen05.wait::ld.sync.aligned;\n"
-      E3_M(0, 0, 1) E3_M(1, 2, 3) E3_M(2, 4, 5) E3_M(3, 6, 7) E3_M(4, 8, 9) E3_M(5, 10, 11) E3_M(6, 12, 13) E3_M(7, 14, 15)
-       E3_M(8, 16, 17) E3_M(9, 18, 19) E3_M(10, 20, 21) E3_M(11, 22, 23) E3_M(12, 24, 25) E3_M(13, 26, 27) E3_M(14, 28, 29) E3_M(15, 30, 31)
-       E3_M(16, 32, 33) E3_M(17, 34, 35) E3_M(18, 36, 37) E3_M(19, 38, 39) E3_M(20, 40, 41) E3_M(21, 42, 43) E3_M(22, 44, 45) E3_M(23, 46, 47)
-       E3_M(24, 48, 49) E3_M(25, 50, 51) E3_M(26, 52, 53) E3_M(27, 54, 55) E3_M(28, 56, 57) E3_M(29, 58, 59) E3_M(30, 60, 61) E3_M(31, 62, 63)
-      "}\n"
-      : E3_Q4(0), E3_Q4(4), E3_Q4(8), E3_Q4(12), E3_Q4(16), E3_Q4(20), E3_Q4(24), E3_Q4(28)
-      : "r"(taddr)
-      : "memory");
-#undef E3_Q4
-#undef E3_M
-#pragma unroll
-  for (int i = 0; i < 32; ++i)
-    v[i] = make_float2(__uint_as_float(static_cast<uint32_t>(q[i])), __uint_as_float(static_cast<uint32_t>(q[i] >> 32)));
+// waits for this thread's loads, of which `r` was one
+__device__ __forceinline__ void tmem_wait32(uint32_t* r) {
+#define E3_RW8(o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), "+r"(r[o + 6]), "+r"(r[o + 7])
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : E3_RW8(0), E3_RW8(8), E3_RW8(16), E3_RW8(24)::"memory");
+#undef E3_RW8
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -332,8 +312,9 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   uint64_t* p_full = bars + 22;     // [softmax group][half of the tile]
   uint64_t* o_done = bars + 26;
   uint64_t* q_full = bars + 28;
-  uint64_t* q_free = bars + 30;     // (RT = 1) both groups are done with the shared Q
-  uint32_t* s_bad = reinterpret_cast<uint32_t*>(bars + 32);  // [kTailRing][4] nodes with a non-finite V
+  uint64_t* o_half = bars + 30;     // the product with the tile's first half
+  uint64_t* q_free = bars + 32;     // (RT = 1) both groups are done with the shared Q
+  uint32_t* s_bad = reinterpret_cast<uint32_t*>(bars + 34);  // [kTailRing][4] nodes with a non-finite V
   int* s_ex = reinterpret_cast<int*>(s_bad + 4 * kTailRing);  // [8 softmax warps][32] exponents of the rows of Q
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_ex + 256);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -354,6 +335,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       bar_init(&p_full[2 * i], 4);
       bar_init(&p_full[2 * i + 1], 4);
       bar_init(&o_done[i], 1);
+      bar_init(&o_half[i], 1);
       bar_init(&q_full[i], 4);
     }
     bar_init(q_free, 8);
@@ -501,6 +483,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
                 umma_ts(tO, tS + half * 32 + kk * 8, vd + static_cast<uint64_t>(((half * kStep + kk * 16) * 128) >> 4), idO,
                         half + kk > 0 || x > x_first ? 1u : 0u);  // the first of a part starts O
             }
+            if (half == 0) umma_commit(&o_half[w]);
           }
           if (!live) break;
           umma_commit(&o_done[w]);
@@ -699,82 +682,96 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
             }
             tmem_st_wait();
           }
-          float tmax = -INFINITY;
-#pragma unroll 1
-          for (int h = 0; h < halves; ++h) {
-            float2 v[32];
-            tmem_ld64(tS + kStep * h, v);
-            float a0 = fmaxf(v[0].x, v[0].y), a1 = fmaxf(v[1].x, v[1].y), a2 = fmaxf(v[2].x, v[2].y), a3 = fmaxf(v[3].x, v[3].y);
-#pragma unroll
-            for (int j = 4; j < 32; j += 4) {
-              a0 = fmax3f(a0, v[j].x, v[j].y);
-              a1 = fmax3f(a1, v[j + 1].x, v[j + 1].y);
-              a2 = fmax3f(a2, v[j + 2].x, v[j + 2].y);
-              a3 = fmax3f(a3, v[j + 3].x, v[j + 3].y);
-            }
-            tmax = fmax3f(tmax, fmaxf(a0, a1), fmaxf(a2, a3));
-          }
-          tmax *= c;
-          // the base moves when passed by more than 2^15; O's unit when the tile's V has another
-          const bool move = tmax > m + kTop;
-          const bool unit = tile_ue != ue && mine > 0;
-          float corr = 1.0f;
-          if (move) {
-            const float nm = fmaxf(m, tmax - kHead);
-            corr = ex2(m - nm);
-            l *= corr;
-            m = nm;
-          }
-          if (unit) corr *= pow2f(ue - tile_ue);
-          ue = tile_ue;
-          if (mine > 0 && __any_sync(0xFFFFFFFFu, move || unit)) {
-            // (O of the last tile is done: S of this one was issued after it)
+          auto scale_o = [&](float f) {  // O times f
 #pragma unroll 1
             for (int d = 0; d < 8; ++d) {
               uint32_t y[16];
               tmem_ld16(tO + 16 * d, y);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
+              for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
               tmem_st16(tO + 16 * d, y);
             }
+            tmem_st_wait();
+          };
+          if (tile_ue != ue) {  // (O of the last tile is done: S of this one was issued after it)
+            if (mine > 0) scale_o(pow2f(ue - tile_ue));
+            ue = tile_ue;
           }
-          const float2 cv = make_float2(c, c);
-          const float sub = (m == -INFINITY ? 0.0f : m) + static_cast<float>(nodes ? kNodeExp : 0);
-          const float2 nv = make_float2(-sub, -sub);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          const float back = nodes ? pow2f(kNodeExp) : 1.0f;
           // P of 64 keys goes over 32 columns of S's first half, whose scores have been read
           // when the second half's P comes
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
-            if (h < halves) {
-              float2 v[32];
-              tmem_ld64(tS + kStep * h, v);
+            // Exponentials against the base so far.  Where a row's sum passes 2^kTop (or it has
+            // no base yet) its maximum is looked for, the base moved and the half done again:
+            // no pass over the scores for their maximum is made otherwise.
+#pragma unroll 1
+            for (int turn = 0; h < halves && turn < 2; ++turn) {
+              const float sub = (m == -INFINITY ? 0.0f : m) + static_cast<float>(nodes ? kNodeExp : 0);
+              const float2 cv = make_float2(c, c), nv = make_float2(-sub, -sub);
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+              uint32_t pk[2][16];
               auto probs = [&](auto pack) {
+                uint32_t y[2][32];
+                tmem_ld32(tS + kStep * h, y[0]);
+                tmem_wait32(y[0]);
+                tmem_ld32(tS + kStep * h + 32, y[1]);
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                  uint32_t pk[16];
+                  if (q == 1) tmem_wait32(y[1]);
 #pragma unroll
                   for (int j = 0; j < 16; ++j) {
-                    const float2 a = __ffma2_rn(v[16 * q + j], cv, nv);
+                    const float2 a = __ffma2_rn(make_float2(__uint_as_float(y[q][2 * j]), __uint_as_float(y[q][2 * j + 1])), cv, nv);
                     const float2 e = make_float2(ex2(a.x), ex2(a.y));
                     sum[j & 1] = __fadd2_rn(sum[j & 1], e);
-                    pk[j] = pack(e);
+                    pk[q][j] = pack(e);
                   }
-                  tmem_st16(tS + 32 * h + 16 * q, pk);
                 }
               };
               if (nodes)
                 probs([](float2 e) { return pack2_bf16(e.x, e.y); });
               else
                 probs([](float2 e) { return h2u(__float22half2_rn(e)); });
-              tmem_st_wait();
+              const float2 s2 = __fadd2_rn(sum[0], sum[1]);
+              const float s = (s2.x + s2.y) * back;
+              const bool move = !(s <= 32768.0f) || m == -INFINITY;
+              if (turn == 1 || !__any_sync(0xFFFFFFFFu, move)) {
+                l += s;
+                tmem_st16(tS + 32 * h, pk[0]);
+                tmem_st16(tS + 32 * h + 16, pk[1]);
+                tmem_st_wait();
+                break;
+              }
+              float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll 1
+              for (int d = 0; d < 4; ++d) {
+                uint32_t y[16];
+                tmem_ld16(tS + kStep * h + 16 * d, y);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                  a0 = fmax3f(a0, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                  a1 = fmax3f(a1, __uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
+                }
+              }
+              const float nm = move ? fmaxf(m, fmaxf(a0, a1) * c - kHead) : m;
+              const float corr = nm == m ? 1.0f : ex2(m - nm);
+              l *= corr;
+              m = nm;
+              if (h == 1 && !warp_wait(&o_half[grp], n_tile & 1, abort)) {
+                live = false;
+                break;
+              }
+              if (mine > 0 || h == 1) {
+                fence_after();
+                scale_o(corr);
+              }
             }
+            if (!live) break;
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(&p_full[2 * grp + h]);
           }
-          const float2 st = __fadd2_rn(sum[0], sum[1]);
-          l += (st.x + st.y) * (nodes ? pow2f(kNodeExp) : 1.0f);
+          if (!live) break;
           ++n_tile;
           ++mine;
         }
@@ -813,7 +810,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           for (int h = 0; h < 4; ++h) {
             uint32_t y[32];
             tmem_ld32(tO + 32 * h, y);
-            tmem_wait();
+            tmem_wait32(y);
             if (row_ok) {
 #pragma unroll
               for (int j = 0; j < 8; ++j)
