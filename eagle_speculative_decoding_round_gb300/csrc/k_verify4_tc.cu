@@ -83,9 +83,9 @@ __device__ __forceinline__ void bar_expect(uint64_t* b, uint32_t bytes) {
 }
 __device__ __forceinline__ bool bar_try(uint64_t* b, uint32_t par) {
   uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+  asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
                : "=r"(ok)
-               : "r"(su32(b)), "r"(par)
+               : "r"(su32(b)), "r"(par), "n"(20000)  // (ns that the hardware may suspend the probe for)
                : "memory");
   return ok != 0;
 }
