@@ -496,7 +496,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   } else if (warp >= kDeq0) {
     regs_dec<kRegsDeq>();
     if (work) {
-      const int op = (warp - kDeq0) >> 2, dw = warp & 3, q = lane & 3;  // 0: K, 1: V
+      const int op = (warp - kDeq0) >> 2, dw = warp & 3;  // 0: K, 1: V
       const int stages = op ? C::RV : C::RK;
       Parts p = first;
       int x = p.x0, ntail = 0;
@@ -511,42 +511,27 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         const int left = p.left(g, x);
         unsigned char* dst = (op ? sV : sK) + dst_st * kOpB;
         if (!nodes) {
-          const unsigned char *codes = raw, *scales = raw + kCodeB;
+          // eight lanes to a key, 16 dims (a scale) each.  The lanes of the second half's dims
+          // store their two 16-byte pieces in the other order, so that the banks of the eight
+          // lanes that store together differ
+          const int j = lane & 7, kr = lane >> 3, flip = j >> 2;
+          const uint32_t codes = su32(raw) + (dw * 32 + kr) * (kHD / 2) + j * 8;
+          const uint32_t scales = su32(raw) + kCodeB + (dw * 32 + kr) * (kHD / 16) + j;
+          const uint32_t out = su32(dst) + flip * kHalfB + (dw * 32 + kr) * 128 + (((2 * (j & 3) + flip) ^ kr) << 4);
+          const int lim = left - (dw * 32 + kr);
 #pragma unroll 1
-          for (int i0 = 0; i0 < 4; i0 += 2) {
-            uint4 w4[2];
-            uint32_t e4[2];
+          for (int i0 = 0; i0 < 8; i0 += 4) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int key = dw * 32 + (i0 + i) * 8 + (lane >> 2);
-              w4[i] = *reinterpret_cast<const uint4*>(codes + key * (kHD / 2) + q * 16);
-              e4[i] = *reinterpret_cast<const uint16_t*>(scales + key * (kHD / 16) + 2 * q);
-              if (key >= left) e4[i] = 0u;  // beyond the prefix: adds 0 whatever the slot holds
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int key = dw * 32 + (i0 + i) * 8 + (lane >> 2);
-              const uint32_t e = h2u(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(e4[i]), __NV_E4M3))));
-              uint32_t ea = __byte_perm(e, e, 0x1010), eb = __byte_perm(e, e, 0x3232);
-              uint32_t w[4] = {w4[i].x, w4[i].y, w4[i].z, w4[i].w};
-              // the four 16-byte pieces in an order that differs between the lanes which
-              // store together, so that their banks do
-              const int flip = ((q >> 1) & 1) | ((key & 1) << 1);
-              if (flip & 1) {
-                const uint32_t a = w[0], b = w[2];
-                w[0] = w[1], w[1] = a, w[2] = w[3], w[3] = b;
-              }
-              if (flip & 2) {
-                uint32_t a = w[0], b = w[1];
-                w[0] = w[2], w[1] = w[3], w[2] = a, w[3] = b;
-                a = ea, ea = eb, eb = a;
-              }
-              unsigned char* row = dst + (q >> 1) * kHalfB + key * 128;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int chunk = 4 * (q & 1) + (k ^ flip);
-                *reinterpret_cast<uint4*>(row + ((chunk ^ (key & 7)) << 4)) = decode8(w[k], u2h(k < 2 ? ea : eb));
-              }
+            for (int i = 0; i < 4; ++i) {  // keys 4 (i0 + i) on; their rows' swizzle: 4 (i % 2) more
+              uint32_t w[2], e;
+              asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(codes + i0 * 256 + i * 256));
+              asm volatile("ld.shared.u8 %0, [%1];" : "=r"(e) : "r"(scales + i0 * 32 + i * 32));
+              if (4 * (i0 + i) >= lim) e = 0u;  // beyond the prefix: adds 0 whatever the slot holds
+              const __half2 es = __half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(e * 0x101u), __NV_E4M3)));
+              const uint4 a = decode8(flip ? w[1] : w[0], es), b = decode8(flip ? w[0] : w[1], es);
+              const uint32_t at = (out ^ ((i & 1) << 6)) + i0 * 512 + i * 512;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w) : "memory");
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16u), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w) : "memory");
             }
           }
         } else {
