@@ -52,9 +52,8 @@ constexpr int kTailRing = 8;             // tiles of tree nodes whose factors ar
 // launch brings the sum.
 constexpr int kThreads = 640;
 constexpr int kSoftmax0 = 4, kDeq0 = 12;
-constexpr int kRegsIssue = 56, kRegsSoftmax = 136, kRegsDeq = 72;
+constexpr int kRegsIssue = 80, kRegsSoftmax = 120, kRegsDeq = 80;
 constexpr int kNodeExp = 24;  // > kTop: a node's weight times a row of V sums below 2^(15 - 24 + 8) of it
-constexpr int kStagger = 0;
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
 template <int RT>
@@ -313,8 +312,9 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   uint64_t* o_done = bars + 26;
   uint64_t* q_full = bars + 28;
   uint64_t* o_half = bars + 30;     // the product with the tile's first half
-  uint64_t* q_free = bars + 32;     // (RT = 1) both groups are done with the shared Q
-  uint32_t* s_bad = reinterpret_cast<uint32_t*>(bars + 34);  // [kTailRing][4] nodes with a non-finite V
+  uint64_t* turn = bars + 32;       // (RT = 2) [softmax group] the group has its scores
+  uint64_t* q_free = bars + 34;     // (RT = 1) both groups are done with the shared Q
+  uint32_t* s_bad = reinterpret_cast<uint32_t*>(bars + 36);  // [kTailRing][4] nodes with a non-finite V
   int* s_ex = reinterpret_cast<int*>(s_bad + 4 * kTailRing);  // [8 softmax warps][32] exponents of the rows of Q
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_ex + 256);
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -337,6 +337,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       bar_init(&o_done[i], 1);
       bar_init(&o_half[i], 1);
       bar_init(&q_full[i], 4);
+      bar_init(&turn[i], 4);
     }
     bar_init(q_free, 8);
     *abort = 0;
@@ -451,11 +452,12 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           // RT = 1 and the second group had no tile in the parts before, K's stage says that
           // their Q has been used, so that the barrier is in this part's phase.)
           live = bar_wait(&k_full[st], (t >> 1) & 1, abort) && (x > x_first || bar_wait(&q_full[RT == 1 ? 0 : w], part & 1, abort)) &&
-                 (n == 0 || bar_wait(&o_done[w], (n - 1) & 1, abort));
+                 (n == 0 || bar_wait(&o_done[w], (n - 1) & 1, abort)) &&
+                 // RT = 2: the groups' scores come in turn, each when the other group has its own:
+                 // left alone the groups fall into step, and the tensor core idles under their
+                 // softmax (132 rows, 65536 keys: 90 us, in turn 87)
+                 (RT == 1 || (w == 0 && n == 0) || bar_wait(&turn[w ^ 1], (w == 0 ? n - 1 : n) & 1, abort));
           if (!live) break;
-          if (RT == 2 && w == 1 && x == x_first)
-            for (const long long c0 = clock64(); clock64() - c0 < kStagger;) {
-            }
           fence_after();
           const uint64_t kd = k_desc + static_cast<uint64_t>(st * (kOpB >> 4));
 #pragma unroll 1
@@ -682,6 +684,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
             if (mine > 0) scale_o(pow2f(ue - tile_ue));
             ue = tile_ue;
           }
+          if (RT == 2 && lane == 0) bar_arrive(&turn[grp]);
           const float back = nodes ? pow2f(kNodeExp) : 1.0f;
           // P of 64 keys goes over 32 columns of S's first half, whose scores have been read
           // when the second half's P comes
@@ -691,7 +694,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
             // no base yet) its maximum is looked for, the base moved and the half done again:
             // no pass over the scores for their maximum is made otherwise.
 #pragma unroll 1
-            for (int turn = 0; h < halves && turn < 2; ++turn) {
+            for (int again = 0; h < halves && again < 2; ++again) {
               const float sub = (m == -INFINITY ? 0.0f : m) + static_cast<float>(nodes ? kNodeExp : 0);
               const float2 cv = make_float2(c, c), nv = make_float2(-sub, -sub);
               float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -720,7 +723,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
               const float2 s2 = __fadd2_rn(sum[0], sum[1]);
               const float s = (s2.x + s2.y) * back;
               const bool move = !(s <= 32768.0f) || m == -INFINITY;
-              if (turn == 1 || !__any_sync(0xFFFFFFFFu, move)) {
+              if (again == 1 || !__any_sync(0xFFFFFFFFu, move)) {
                 l += s;
                 tmem_st16(tS + 32 * h, pk[0]);
                 tmem_st16(tS + 32 * h + 16, pk[1]);
