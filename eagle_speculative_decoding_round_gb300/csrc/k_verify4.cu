@@ -40,6 +40,7 @@ namespace {
 constexpr int kGran = 16;   // keys of a granule
 constexpr int kWarps = 4;
 constexpr int kStages = 4;  // granules in a warp's ring
+constexpr int kStep = 2;    // granules of a step
 
 __device__ __forceinline__ uint32_t su32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
@@ -190,7 +191,7 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) load_granule(i);
+    for (int i = 0; i < kStages - kStep; ++i) load_granule(i);
 
     // Q as the second operand: thread (gq, tq) holds row gq of each tile, dims [DK tq, DK (tq + 1))
     uint32_t qb[NR][KS][2];
@@ -222,17 +223,20 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
       poison[nr][0] = poison[nr][1] = false;
     }
 
-    // running softmax over one granule's scores (already scaled, -Inf where unseen): sc[nr]
-    // holds keys gq (0, 1) and gq + 8 (2, 3) of query rows 2 tq, 2 tq + 1; probabilities
-    // replace the scores; o and l follow the moved base
-    auto softmax = [&](float (&sc)[NR][4]) {
+    // running softmax over the scores of NGR granules (already scaled, -Inf where unseen):
+    // sc[.][nr] holds keys gq (0, 1) and gq + 8 (2, 3) of query rows 2 tq, 2 tq + 1;
+    // probabilities replace the scores; o and l follow the moved base
+    auto softmax = [&](auto& sc) {
+      constexpr int NGR = std::extent<std::remove_reference_t<decltype(sc)>, 0>::value;
       float bm[NR][2];
       bool move = false;
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float x = fmaxf(sc[nr][e], sc[nr][2 + e]);
+          float x = fmaxf(sc[0][nr][e], sc[0][nr][2 + e]);
+#pragma unroll
+          for (int u = 1; u < NGR; ++u) x = fmaxf(x, fmaxf(sc[u][nr][e], sc[u][nr][2 + e]));
           x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
@@ -260,9 +264,12 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float sub = m[nr][e] == -INFINITY ? 0.0f : m[nr][e];
-          sc[nr][e] = ex2(sc[nr][e] - sub);
-          sc[nr][2 + e] = ex2(sc[nr][2 + e] - sub);
-          l[nr][e] += sc[nr][e] + sc[nr][2 + e];
+#pragma unroll
+          for (int u = 0; u < NGR; ++u) {
+            sc[u][nr][e] = ex2(sc[u][nr][e] - sub);
+            sc[u][nr][2 + e] = ex2(sc[u][nr][2 + e] - sub);
+            l[nr][e] += sc[u][nr][e] + sc[u][nr][2 + e];
+          }
         }
     };
 
@@ -301,20 +308,20 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
             const int r = rg * ROWS + 8 * nr + 2 * tq + e;
             bits[nr][e] = r < rows ? mask[(static_cast<size_t>(b) * g.R + r / g.G) * words + (j0 >> 6)] >> (j0 & 63) : 0ull;
           }
-        float sc[NR][4];
+        float sc[1][NR][4];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-          sc[nr][0] = sc[nr][1] = sc[nr][2] = sc[nr][3] = 0.0f;
+          sc[0][nr][0] = sc[0][nr][1] = sc[0][nr][2] = sc[0][nr][3] = 0.0f;
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
             const uint32_t a[4] = {kr[0][ks].x, kr[1][ks].x, kr[0][ks].y, kr[1][ks].y};
-            mma_b16(sc[nr], a, qb[nr][ks][0], qb[nr][ks][1]);
+            mma_b16(sc[0][nr], a, qb[nr][ks][0], qb[nr][ks][1]);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = key_of(e >> 1, gq);
             const bool see = j0 + j < g.R && ((bits[nr][e & 1] >> j) & 1ull);
-            sc[nr][e] = see ? sc[nr][e] * c2 : -INFINITY;
+            sc[0][nr][e] = see ? sc[0][nr][e] * c2 : -INFINITY;
           }
         }
         softmax(sc);
@@ -354,7 +361,7 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
         }
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-          const uint32_t p0 = transpose8(pack2_bf16(sc[nr][0], sc[nr][1])), p1 = transpose8(pack2_bf16(sc[nr][2], sc[nr][3]));
+          const uint32_t p0 = transpose8(pack2_bf16(sc[0][nr][0], sc[0][nr][1])), p1 = transpose8(pack2_bf16(sc[0][nr][2], sc[0][nr][3]));
 #pragma unroll
           for (int d = 0; d < DV / 2; ++d) {
             const uint32_t a[4] = {__byte_perm(raw[0][d], raw[1][d], 0x5410), __byte_perm(raw[0][d], raw[1][d], 0x7632),
@@ -407,103 +414,117 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
           for (int e = 0; e < 4; ++e) o[nr][j][e] *= inv_vu;
     }
 
+    // a step: kStep granules, whose products do not wait for one another.  (Keys beyond the
+    // prefix, and the granules that a last step lacks: -Inf for a score, 0 for V's scale.)
 #pragma unroll 1
-    for (int i = 0; i < ngran; ++i) {
-      load_granule((i + kStages - 1) % kStages);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    for (int i = 0; i < ngran; i += kStep) {
+#pragma unroll
+      for (int u = 0; u < kStep; ++u) load_granule((i + kStages - kStep + u) % kStages);
+      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - kStep) : "memory");
       __syncwarp();
-      const unsigned char* st = ring + (i % kStages) * C::STAGE;
-      const int left = P - (ga + i) * kGran;  // keys below P from the granule's first
-      float sc[NR][4];
+      float sc[kStep][NR][4];
+      const int left0 = min(P - (ga + i) * kGran, (ngran - i) * kGran);  // keys from the step's first
 #pragma unroll
-      for (int nr = 0; nr < NR; ++nr) sc[nr][0] = sc[nr][1] = sc[nr][2] = sc[nr][3] = 0.0f;
-      uint32_t w[2][DK / 8];
-      __half2 e2[2][DK / 16];  // the scale of each 16 dims, in both halves
+      for (int u = 0; u < kStep; ++u) {
+        const unsigned char* st = ring + (i + u) % kStages * C::STAGE;
+        const int left = left0 - u * kGran;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int key = key_of(t, gq);
-        const unsigned char* sp = st + 2 * C::CODES + key * C::SCB;
-        if (HD == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(st + code_off<HD>(key, tq));
-          w[t][0] = x.x, w[t][1] = x.y, w[t][DK / 8 - 2] = x.z, w[t][DK / 8 - 1] = x.w;
-          const uint32_t e = h2u(cvt8(*reinterpret_cast<const uint16_t*>(sp + 2 * tq)));
-          e2[t][0] = u2h(__byte_perm(e, e, 0x1010));
-          e2[t][DK / 16 - 1] = u2h(__byte_perm(e, e, 0x3232));
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(st + key * C::ROWB + 8 * tq);
-          w[t][0] = x.x, w[t][1] = x.y;
-          const uint32_t e = h2u(cvt8(sp[tq]));
-          e2[t][0] = u2h(__byte_perm(e, e, 0x1010));
+        for (int nr = 0; nr < NR; ++nr) sc[u][nr][0] = sc[u][nr][1] = sc[u][nr][2] = sc[u][nr][3] = 0.0f;
+        uint32_t w[2][DK / 8];
+        __half2 e2[2][DK / 16];  // the scale of each 16 dims, in both halves
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int key = key_of(t, gq);
+          const unsigned char* sp = st + 2 * C::CODES + key * C::SCB;
+          if (HD == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(st + code_off<HD>(key, tq));
+            w[t][0] = x.x, w[t][1] = x.y, w[t][DK / 8 - 2] = x.z, w[t][DK / 8 - 1] = x.w;
+            const uint32_t e = h2u(cvt8(*reinterpret_cast<const uint16_t*>(sp + 2 * tq)));
+            e2[t][0] = u2h(__byte_perm(e, e, 0x1010));
+            e2[t][DK / 16 - 1] = u2h(__byte_perm(e, e, 0x3232));
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(st + key * C::ROWB + 8 * tq);
+            w[t][0] = x.x, w[t][1] = x.y;
+            const uint32_t e = h2u(cvt8(sp[tq]));
+            e2[t][0] = u2h(__byte_perm(e, e, 0x1010));
+          }
         }
-      }
 #pragma unroll
-      for (int k2 = 0; k2 < KS / 2; ++k2) {
-        __half2 x[4], y[4];
-        cvt4(w[0][k2], x);
-        cvt4(w[1][k2], y);
+        for (int k2 = 0; k2 < KS / 2; ++k2) {
+          __half2 x[4], y[4];
+          cvt4(w[0][k2], x);
+          cvt4(w[1][k2], y);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t a[4] = {h2u(__hmul2(x[2 * k], e2[0][k2 >> 1])), h2u(__hmul2(y[2 * k], e2[1][k2 >> 1])),
-                                 h2u(__hmul2(x[2 * k + 1], e2[0][k2 >> 1])), h2u(__hmul2(y[2 * k + 1], e2[1][k2 >> 1]))};
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t a[4] = {h2u(__hmul2(x[2 * k], e2[0][k2 >> 1])), h2u(__hmul2(y[2 * k], e2[1][k2 >> 1])),
+                                   h2u(__hmul2(x[2 * k + 1], e2[0][k2 >> 1])), h2u(__hmul2(y[2 * k + 1], e2[1][k2 >> 1]))};
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr) mma_f16(sc[nr], a, qb[nr][2 * k2 + k][0], qb[nr][2 * k2 + k][1]);
+            for (int nr = 0; nr < NR; ++nr) mma_f16(sc[u][nr], a, qb[nr][2 * k2 + k][0], qb[nr][2 * k2 + k][1]);
+          }
         }
-      }
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[nr][e] = sc[nr][e] * c2[nr][e & 1];
-      if (left < kGran) {  // keys beyond the prefix
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key_of(e >> 1, gq) >= left) sc[nr][e] = -INFINITY;
+          for (int e = 0; e < 4; ++e) sc[u][nr][e] = sc[u][nr][e] * c2[nr][e & 1];
+        if (left < kGran) {
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key_of(e >> 1, gq) >= left) sc[u][nr][e] = -INFINITY;
+        }
       }
       softmax(sc);
-      uint32_t pb[NR][2];
+      uint32_t pb[kStep][NR][2];
 #pragma unroll
-      for (int nr = 0; nr < NR; ++nr) {
-        pb[nr][0] = transpose8(h2u(__floats2half2_rn(sc[nr][0], sc[nr][1])));
-        pb[nr][1] = transpose8(h2u(__floats2half2_rn(sc[nr][2], sc[nr][3])));
-      }
-      // V: words of DV dims of the four keys, and the scale pair of each two keys (0 where
-      // the key is beyond the prefix: whatever its slot holds, it adds 0)
-      uint32_t vw[4][DV / 8];
-      uint32_t ve[4];
+      for (int u = 0; u < kStep; ++u)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int key = key_of(x >> 1, 2 * tq + (x & 1));
-        if (HD == 128) {
-          const uint2 y = *reinterpret_cast<const uint2*>(st + C::CODES + code_off<HD>(key, gq >> 1) + 8 * (gq & 1));
-          vw[x][0] = y.x, vw[x][DV / 8 - 1] = y.y;
-        } else {
-          vw[x][0] = *reinterpret_cast<const uint32_t*>(st + C::CODES + key * C::ROWB + 4 * gq);
+        for (int nr = 0; nr < NR; ++nr) {
+          pb[u][nr][0] = transpose8(h2u(__floats2half2_rn(sc[u][nr][0], sc[u][nr][1])));
+          pb[u][nr][1] = transpose8(h2u(__floats2half2_rn(sc[u][nr][2], sc[u][nr][3])));
         }
-        ve[x] = st[2 * C::CODES + C::SCALES + key * C::SCB + (DV * gq) / 16];
-      }
-      if (left < kGran)
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (key_of(x >> 1, 2 * tq + (x & 1)) >= left) ve[x] = 0u;
-      const __half2 e01 = cvt8(__byte_perm(ve[0], ve[1], 0x40)), e23 = cvt8(__byte_perm(ve[2], ve[3], 0x40));
+      for (int u = 0; u < kStep; ++u) {
+        // V: words of DV dims of the four keys, and the scale pair of each two keys (0 where
+        // the key is beyond the prefix: whatever its slot holds, it adds 0)
+        const unsigned char* st = ring + (i + u) % kStages * C::STAGE;
+        const int left = left0 - u * kGran;
+        uint32_t vw[4][DV / 8];
+        uint32_t ve[4];
 #pragma unroll
-      for (int x = 0; x < DV / 8; ++x) {
-        constexpr uint32_t kLo = 0x0F0F0F0Fu;
-        __half2 a0[4], a1[4], b0[4], b1[4];  // even and odd dims of the key pairs
-        cvt4((vw[0][x] & kLo) | ((vw[1][x] << 4) & ~kLo), a0);
-        cvt4(((vw[0][x] >> 4) & kLo) | (vw[1][x] & ~kLo), b0);
-        cvt4((vw[2][x] & kLo) | ((vw[3][x] << 4) & ~kLo), a1);
-        cvt4(((vw[2][x] >> 4) & kLo) | (vw[3][x] & ~kLo), b1);
+        for (int x = 0; x < 4; ++x) {
+          const int key = key_of(x >> 1, 2 * tq + (x & 1));
+          if (HD == 128) {
+            const uint2 y = *reinterpret_cast<const uint2*>(st + C::CODES + code_off<HD>(key, gq >> 1) + 8 * (gq & 1));
+            vw[x][0] = y.x, vw[x][DV / 8 - 1] = y.y;
+          } else {
+            vw[x][0] = *reinterpret_cast<const uint32_t*>(st + C::CODES + key * C::ROWB + 4 * gq);
+          }
+          ve[x] = st[2 * C::CODES + C::SCALES + key * C::SCB + (DV * gq) / 16];
+        }
+        if (left < kGran)
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const uint32_t a[4] = {h2u(__hmul2(a0[d], e01)), h2u(__hmul2(b0[d], e01)), h2u(__hmul2(a1[d], e23)),
-                                 h2u(__hmul2(b1[d], e23))};
+          for (int x = 0; x < 4; ++x)
+            if (key_of(x >> 1, 2 * tq + (x & 1)) >= left) ve[x] = 0u;
+        const __half2 e01 = cvt8(__byte_perm(ve[0], ve[1], 0x40)), e23 = cvt8(__byte_perm(ve[2], ve[3], 0x40));
 #pragma unroll
-          for (int nr = 0; nr < NR; ++nr) mma_f16(o[nr][4 * x + d], a, pb[nr][0], pb[nr][1]);
+        for (int x = 0; x < DV / 8; ++x) {
+          constexpr uint32_t kLo = 0x0F0F0F0Fu;
+          __half2 a0[4], a1[4], b0[4], b1[4];  // even and odd dims of the key pairs
+          cvt4((vw[0][x] & kLo) | ((vw[1][x] << 4) & ~kLo), a0);
+          cvt4(((vw[0][x] >> 4) & kLo) | (vw[1][x] & ~kLo), b0);
+          cvt4((vw[2][x] & kLo) | ((vw[3][x] << 4) & ~kLo), a1);
+          cvt4(((vw[2][x] >> 4) & kLo) | (vw[3][x] & ~kLo), b1);
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const uint32_t a[4] = {h2u(__hmul2(a0[d], e01)), h2u(__hmul2(b0[d], e01)), h2u(__hmul2(a1[d], e23)),
+                                   h2u(__hmul2(b1[d], e23))};
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) mma_f16(o[nr][4 * x + d], a, pb[u][nr][0], pb[u][nr][1]);
+          }
         }
       }
-      __syncwarp();  // the stage may be refilled
+      __syncwarp();  // the stages may be refilled
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     // this part's record: o normalized by its own sum, the base and the sum
