@@ -21,7 +21,7 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
 constexpr int kBatch = 8;  // pieces of a thread whose loads are in flight together
 constexpr int kMaxBias = 1024;
 constexpr int kMaxR = E3_MAX_NODES + 1;
@@ -293,6 +293,11 @@ logits_process_kernel(LogitsArgs a) {
     }
     if (VEC) {
       if (tid == 0) {  // the copy has landed (bounded)
+        // the next row comes into L2 under this one's work: its copy waits for this part's place
+        if (i + 1 < i1 && nv > 0)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a.logits + (row + 1) * a.V + v0),
+                       "r"(static_cast<uint32_t>(nv) * 4u)
+                       : "memory");
         bool ok = false;
         uint64_t t0 = 0;
         for (int n = 0; !ok; ++n) {
