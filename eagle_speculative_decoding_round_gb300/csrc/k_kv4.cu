@@ -20,7 +20,7 @@ namespace e3 {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // index of (page, head 0, slot) of logical slot t in rows, or -1
 __device__ __forceinline__ long long slot_row(const int32_t* table, int max_pages, int n_pages, int page_size, int KVH,

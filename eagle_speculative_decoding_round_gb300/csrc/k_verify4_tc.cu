@@ -339,7 +339,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       bar_init(&q_full[i], 4);
       bar_init(&turn[i], 4);
     }
-    bar_init(q_free, 8);
+    bar_init(q_free, 9);  // the softmax warps, and the second group's issuer
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -442,17 +442,18 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
       const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
       Parts p = first;
-      uint32_t t0 = 0, n = 0, part = 0;  // tiles of the CTA before the part; the group's tiles; parts
+      uint32_t n = 0, part = 0;  // the group's tiles; parts
       bool live = true;
       do {
         const int x_first = p.x0 + (RT == 1 ? w : 0);
+        // (the second group of RT = 1 sees every part's Q come, also where it has no tile of
+        // the part: a phase that it missed would let it take the next for one behind)
+        live = bar_wait(&q_full[RT == 1 ? 0 : w], part++ & 1, abort);
+        if (RT == 1 && w == 1 && live) bar_arrive(q_free);
         for (int x = x_first; live && x < p.x1; x += RT == 1 ? 2 : 1, ++n) {
-          const uint32_t t = t0 + static_cast<uint32_t>(x - p.x0), st = t & 1;
-          // S over the P that the last O product has read.  (Q is waited for behind K: where
-          // RT = 1 and the second group had no tile in the parts before, K's stage says that
-          // their Q has been used, so that the barrier is in this part's phase.)
-          live = bar_wait(&k_full[st], (t >> 1) & 1, abort) && (x > x_first || bar_wait(&q_full[RT == 1 ? 0 : w], part & 1, abort)) &&
-                 (n == 0 || bar_wait(&o_done[w], (n - 1) & 1, abort)) &&
+          const uint32_t st = RT == 1 ? w : n & 1, par = RT == 1 ? n & 1 : (n >> 1) & 1;
+          // S over the P that the last O product has read
+          live = bar_wait(&k_full[st], par, abort) && (n == 0 || bar_wait(&o_done[w], (n - 1) & 1, abort)) &&
                  // RT = 2: the groups' scores come in turn, each when the other group has its own:
                  // left alone the groups fall into step, and the tensor core idles under their
                  // softmax (132 rows, 65536 keys: 90 us, in turn 87)
@@ -470,7 +471,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           }
           umma_commit(&s_full[w]);
           umma_commit(&k_empty[st]);
-          live = bar_wait(&v_full[st], (t >> 1) & 1, abort);
+          live = bar_wait(&v_full[st], par, abort);
           const uint64_t vd = v_desc + static_cast<uint64_t>(st * (kOpB >> 4));
           const bool two = p.left(g, x) > kStep;
           const uint32_t idO = x >= p.NT ? idesc_16(kHD, 1, true) : idesc_16(kHD, 1, false);  // tree nodes' V stays bf16
@@ -491,8 +492,6 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           umma_commit(&o_done[w]);
           umma_commit(&v_empty[st]);
         }
-        t0 += static_cast<uint32_t>(p.x1 - p.x0);
-        ++part;
       } while (live && p.next(g, kv, kv_len));
     }
   } else if (warp >= kDeq0) {
@@ -503,11 +502,14 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       Parts p = first;
       int x = p.x0, ntail = 0;
       uint32_t st = 0, raw_par = 0;  // raw stage and its parity
+      uint32_t used[2] = {0u, 0u};  // uses of the two stages so far
       for (uint32_t T = 0;; ++T) {
         const int slot = ntail % kTailRing, kvh = p.pq / g.RG;
         if (!warp_wait(&raw_full[3 * op + st], raw_par, abort)) break;
-        const uint32_t dst_st = T & 1;
-        if (!warp_wait(op ? &v_empty[dst_st] : &k_empty[dst_st], ((T >> 1) & 1) ^ 1, abort)) break;
+        // RT = 2: the stages in turn.  RT = 1: a stage per softmax group, which then sees each
+        // of its phases
+        const uint32_t dst_st = RT == 1 ? (x - p.x0) & 1 : T & 1, use = dst_st ? used[1]++ : used[0]++;
+        if (!warp_wait(op ? &v_empty[dst_st] : &k_empty[dst_st], (use & 1) ^ 1, abort)) break;
         const unsigned char* raw = sRaw + (op * C::RK + st) * kRawB;
         const bool nodes = x >= p.NT;
         const int left = p.left(g, x);

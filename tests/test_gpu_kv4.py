@@ -496,6 +496,110 @@ def test_verify_attn4_on_streams_and_in_a_graph():
     attn_check(a, *out)
 
 
+@pytest.mark.parametrize("B,R,H,KVH,hd,most", [
+    (48, 17, 32, 8, 128, 300),    # 68 rows a KV head: parts of one tile and of several
+    (48, 17, 32, 8, 128, 40),     # no more than the nodes' tile and one of the prefix
+    (40, 61, 32, 8, 128, 900),    # 244 rows
+    (24, 200, 16, 4, 128, 500),   # several row tiles, two tiles of nodes
+    (64, 3, 16, 4, 64, 700),
+])
+def test_verify_attn4_many_requests_of_differing_length(B, R, H, KVH, hd, most):
+    """Shares that end inside a request, hold several, or begin behind one's last tile."""
+    rng = np.random.default_rng(B + R + most)
+    lens = [int(x) for x in np.where(rng.random(B) < 0.15, 0, rng.integers(1, most + 1, B))]
+    lens[1] = 12 * most
+    d = attn_inputs(R, B, R, H, KVH, hd, lens, 16)
+    dev = {}
+    O, lse, err = attn_call(d, dev=dev)
+    O2, lse2, _ = attn_call(d, dev=dev, err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    assert not torch.any(O == 55.0) and not torch.any(lse == 55.0)
+    attn_check(d, O, lse, requests=[0, 1, 2, B // 2, B - 1])
+
+
+@pytest.mark.parametrize("R,H,KVH", [(9, 8, 4), (21, 16, 4), (40, 16, 4)])
+def test_a_round_in_a_graph(R, H, KVH):
+    """The round's calls captured once and replayed on other inputs: bit for bit the eager calls' results."""
+    B, hd, V, D, page, lens = 2, 128, 2048, 4, 16, [130, 77]
+    rng = np.random.default_rng(R)
+    mp = 16
+    pt = i32(rng.permutation(B * mp).reshape(B, mp))
+    width = (H + 2 * KVH) * hd
+
+    def values(seed):
+        r = np.random.default_rng(seed)
+        par = np.stack([random_tree(r, R, D)[0] for _ in range(B)]).astype(np.int32)
+        path = np.zeros((B, D + 1), np.int32)
+        acc = np.zeros(B, np.int32)
+        for b in range(B):
+            u, up = R - 1, []
+            while u > 0:
+                up.append(u)
+                u = int(par[b, u])
+            acc[b] = len(up)
+            path[b, 1:len(up) + 1] = up[::-1]
+        return dict(qkv=to_dev(synth.to_bf16_f32(r.normal(size=(B * R, width)).astype(np.float32)), torch.bfloat16),
+                    pos=i32(r.integers(0, 9000, (B, R))), mask=mask_of(np.stack([ancestors(q) for q in par])),
+                    par=i32(par), tok=i32(r.integers(0, V, (B, R))), path=i32(path), acc=i32(acc),
+                    z=to_dev(r.normal(size=(B * R, V)).astype(np.float32) * 4.0))
+
+    def state():
+        r = np.random.default_rng(5)
+        s = dict(q4=[torch.from_numpy(r.integers(0, 256, (B * mp, KVH, page, hd // 2), dtype=np.uint8)).cuda() for _ in range(2)],
+                 e4=[torch.from_numpy(r.integers(40, 60, (B * mp, KVH, page, hd // 16), dtype=np.uint8)).cuda() for _ in range(2)],
+                 tail=[torch.zeros((B, KVH, 64, hd), dtype=torch.bfloat16, device="cuda") for _ in range(2)], tpt=i32([[0], [1]]),
+                 lens=i32(lens), Q=torch.zeros((B, R, H, hd), dtype=torch.bfloat16, device="cuda"),
+                 counts=torch.zeros(B * V, dtype=torch.int16, device="cuda"), err=err_word(),
+                 back=[torch.zeros((B * mp, KVH, page, hd), dtype=torch.bfloat16, device="cuda") for _ in range(2)],
+                 out=torch.zeros((B * R, V), device="cuda"), mx=torch.zeros(B * R, device="cuda"),
+                 Qs=torch.zeros(B * R, dtype=torch.int64, device="cuda"), am=torch.zeros(B * R, dtype=torch.int32, device="cuda"),
+                 O=torch.zeros((B, R, H, hd), dtype=torch.bfloat16, device="cuda"), lse=torch.zeros((B, R, H), device="cuda"))
+        s["need"] = e3.eagle3_verify4_workspace_bytes(B, R, H, KVH, hd, mp * page)
+        s["ws"] = torch.full((s["need"],), 255, dtype=torch.uint8, device="cuda")
+        return s
+
+    rope = e3.eagle3_rope_init(hd, 10000.0)
+    temp = torch.full((B * R,), 0.8, device="cuda")
+    pen = to_dev(np.array([[1.2, 0.1, 0.1], [1.5, 0.0, 0.3]], np.float32))
+
+    def run(s, x):
+        kv = e3.make_kv4_layer(*s["q4"], *s["e4"], pt, B * mp, page, mp, KVH, hd)
+        tail = e3.make_kv_layer(*s["tail"], s["tpt"], B, 64, 1, KVH, hd, e3.E3_BF16)
+        back = e3.make_kv_layer(*s["back"], pt, B * mp, page, mp, KVH, hd, e3.E3_BF16)
+        e3.tree_qkv_append(x["qkv"], width, B, R, None, H, None, None, 0.0, rope, x["pos"], s["Q"], tail, None, s["err"])
+        e3.tree_verify_attn4(s["Q"], kv, tail, s["lens"], x["mask"], B, R, H, mp * page, hd ** -0.5, s["O"], s["lse"], s["err"],
+                             s["ws"], s["need"])
+        e3.tree_logits_process(x["z"], B, R, V, temp, s["counts"], x["tok"], x["par"], pen, None, None, 0, None, None, 0, s["out"],
+                               s["mx"], s["Qs"], s["am"], s["err"])
+        e3.kv4_append([kv], [tail], B, D + 1, x["path"], x["acc"], 1, s["lens"], s["lens"], s["err"])
+        e3.token_counts_add(s["counts"], V, B, x["path"], x["acc"], 1, D + 1)
+        e3.kv4_read([kv], [back], B, mp * page, None, s["lens"], s["err"])
+
+    eager, held = state(), state()
+    x = values(0)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):  # (first calls set kernel attributes)
+        run(state(), x)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(held, x)
+    for seed in (1, 2):
+        y = values(seed)
+        for k in x:
+            x[k].copy_(y[k])
+        run(eager, y)
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(eager["err"].item()) == 0 and int(held["err"].item()) == 0
+        for k in ("lens", "Q", "counts", "out", "mx", "Qs", "am", "O", "lse"):
+            assert torch.equal(eager[k], held[k]), k
+        for k in ("q4", "e4", "tail", "back"):
+            assert all(torch.equal(a, b) for a, b in zip(eager[k], held[k])), k
+
+
 # ----------------------------------------------------------------------- logits
 
 LOGITS = [
