@@ -13,7 +13,12 @@
 // fp16 form keeps every bf16 bit down to 2^-24 of the row's largest value; the unit, the
 // row's power of two and sm_scale meet the fp32 scores.  P is rounded to fp16 (2^-11 of
 // a weight, or 2^-32 of the row's largest), sums stay in fp32.  The tail runs in bf16 as
-// it is stored.
+// it is stored, P with it (2^-8 of a weight at most).
+//
+// Bound: instructions (about 375 a granule and warp: 128 conversions and products of the
+// codes, 16 mma.sync; the schedulers issue on 60% of the cycles, 3.5 warps each).  Two
+// granules a step let one's products run under the other's conversions: 32 requests of 512
+// .. 8192 keys, one node, 32 heads on 8: 47 us against 49.6 with one (160 MB: 3.4 TB/s).
 //
 // The dims of a head and the keys of a granule may be taken in any order by the
 // contractions.  K: thread (g, c) = (lane / 4, lane % 4) reads hd/4 consecutive dims of
@@ -569,6 +574,80 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
   }
 }
 
+// Merge of a pair's records: one warp per (b, i, h) row, hd/32 dims a lane.  ROWS: the
+// row tile of the kernel that wrote them.  The workers that began and ended the pair left
+// their numbers in `ends`, so the records are found without the search; the first
+// records' values are requested together with their weights.
+template <int HD, int ROWS>
+__global__ void __launch_bounds__(128)
+verify4_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __restrict__ kv_len,
+                     const __grid_constant__ V4Geom g, const float* __restrict__ ws_o, const float2* __restrict__ ws_ml,
+                     const int32_t* __restrict__ ends, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
+  constexpr int PER = HD / 32;
+  constexpr int AHEAD = 8;
+  const int lane = threadIdx.x & 31;
+  const unsigned row = blockIdx.x * 4u + (threadIdx.x >> 5);
+  const unsigned stride = static_cast<unsigned>(g.R) * g.H;
+  const int b = static_cast<int>(row / stride);
+  if (b >= g.B) {
+    pdl_wait();
+    return;
+  }
+  const int ih = static_cast<int>(row - b * stride), i = ih / g.H, h = ih - i * g.H;
+  const int kvh = h / g.G, r = i * g.G + h - kvh * g.G, rt = r / ROWS;
+  const size_t pair = static_cast<size_t>(b) * g.KVH * g.RG + kvh * g.RG + rt;
+  pdl_wait();
+  pdl_trigger();
+  const int P = kv_len[b], c0 = ends[2 * pair], c1 = ends[2 * pair + 1];
+  // (a worker that gave up, its error word set, may not have left its number)
+  if (pair_units<kGran>(g, kv, P) == 0 || c0 < 0 || c1 < c0 || c1 >= g.workers) return;
+  const int n = c1 - c0 + 1;
+  const size_t base = (pair + c0) * ROWS + (r - rt * ROWS);  // then ROWS apart
+  using Vec = typename std::conditional<PER == 4, float4, float2>::type;
+  auto value = [&](int q) { return reinterpret_cast<const Vec*>(ws_o + (base + static_cast<size_t>(q) * ROWS) * HD)[lane]; };
+  Vec x[AHEAD];
+#pragma unroll
+  for (int q = 0; q < AHEAD; ++q)
+    if (q < n) x[q] = value(q);
+  float2 ml = lane < n ? ws_ml[base + static_cast<size_t>(lane) * ROWS] : make_float2(-INFINITY, 0.0f);
+  float M = ml.y != 0.0f ? ml.x : -INFINITY;
+  for (int q = lane + 32; q < n; q += 32) {
+    const float2 y = ws_ml[base + static_cast<size_t>(q) * ROWS];
+    if (y.y != 0.0f) M = fmaxf(M, y.x);
+  }
+  M = warp_reduce(M, MaxF());
+  float acc[PER];
+#pragma unroll
+  for (int u = 0; u < PER; ++u) acc[u] = 0.0f;
+  float den = 0.0f;
+  for (int q0 = 0; q0 < n; q0 += 32) {
+    if (q0 > 0) ml = q0 + lane < n ? ws_ml[base + static_cast<size_t>(q0 + lane) * ROWS] : make_float2(-INFINITY, 0.0f);
+    // (-1: a record without keys, whose values were never written; a NaN sum stays one)
+    const float w = ml.y != 0.0f ? ml.y * ex2(ml.x - M) : -1.0f;
+    den += w == -1.0f ? 0.0f : w;
+    const int nq = min(32, n - q0);
+    for (int j0 = 0; j0 < nq; j0 += AHEAD) {
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        const float wj = __shfl_sync(0xFFFFFFFFu, w, (j0 + j) & 31);
+        if (j0 + j < nq && wj != -1.0f) {
+          const float* v = reinterpret_cast<const float*>(&x[j]);
+#pragma unroll
+          for (int u = 0; u < PER; ++u) acc[u] = fmaf(wj, v[u], acc[u]);
+        }
+        if (q0 + j0 + AHEAD + j < n) x[j] = value(q0 + j0 + AHEAD + j);
+      }
+    }
+  }
+  den = warp_reduce(den, [](float p, float q) { return p + q; });
+  const float inv = den != 0.0f ? 1.0f / den : 0.0f;
+  __nv_bfloat16* out = O + static_cast<size_t>(row) * HD + lane * PER;
+#pragma unroll
+  for (int u = 0; u < PER; u += 2)
+    *reinterpret_cast<uint32_t*>(out + u) = pack2_bf16(acc[u] * inv, acc[u + 1] * inv);
+  if (lane == 0) lse[row] = den != 0.0f ? (M + log2f(den)) * kLn2 : -INFINITY;
+}
+
 // Shares of the granule kernel: every warp that is resident, none below four granules.
 // Query rows in tiles of eight while they fit one, else of sixteen.
 V4Geom make_geom(int B, int R, int H, int KVH, int max_kv_len) {
@@ -601,7 +680,7 @@ cudaError_t launch_mma(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_
   const cudaError_t e = launch_pdl(verify4_mma_kernel<HD, NR>, dim3(g.workers / kWarps), dim3(kWarps * 32), V4Cfg<HD>::SMEM, s,
                                    1, q, kv, tail, kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, dev_err);
   if (e != cudaSuccess) return e;
-  return launch_pdl(verify4_merge_kernel<HD, 8 * NR, kGran, 1>, dim3(static_cast<unsigned>((static_cast<long>(g.B) * g.R * g.H + 3) / 4)),
+  return launch_pdl(verify4_merge_kernel<HD, 8 * NR>, dim3(static_cast<unsigned>((static_cast<long>(g.B) * g.R * g.H + 3) / 4)),
                     dim3(128), 0, s, 1, kv, kv_len, g, static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml),
                     static_cast<const int32_t*>(ends), o, lse);
 }

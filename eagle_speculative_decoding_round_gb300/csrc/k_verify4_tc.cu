@@ -5,22 +5,32 @@
 // its units are tiles of 128 prefix keys and then of 128 tree nodes; one CTA per SM takes
 // an equal share of all units.  A tile goes through the CTA like this:
 //   producers (warps 0, 3) the tile's codes and scales by bulk copies into rings, K and V
-//   dequantizers (4 warps) codes -> fp16 operands in 128-byte-swizzled shared memory: a
-//                          value c * e is exact in fp16 (see k_verify4.cu).  Tree nodes are
-//                          read from the bf16 tail and scaled by powers of two instead
-//                          (per key for K, per tile for V), which keeps their bits
-//   S = Q K^T              (warps 1 and 2, one per softmax group) tcgen05.mma kind::f16, M =
-//                          128 rows, N = 64 keys, into one of the group's two S buffers
-//   softmax (2 x 4 warps)  one thread per row: maximum, exponentials, P (fp16) over S
+//   dequantizers (4 + 4 warps, K and V) codes -> fp16 operands in 128-byte-swizzled shared
+//                          memory: a value c * e is exact in fp16 (see k_verify4.cu).  Tree
+//                          nodes come from the bf16 tail: K scaled by a power of two per
+//                          key, which keeps its bits, V as it is, for a product in bf16
+//   S = Q K^T              (warps 1 and 2, one issuing thread per softmax group)
+//                          tcgen05.mma kind::f16, 128 rows x 128 keys
+//   softmax (2 x 4 warps)  one thread per row: exponentials, P over S in halves of 64 keys
 //   O += P V               A = P from TMEM, V in place as an MN-major operand; O stays in
-//                          TMEM, rescaled only when a base moves by more than 2^15
-// A group's next scores are there when it has written its last P: S of a step runs under
-// the exponentials of the step before it, and the two groups fill each other's gaps.  RT = 2: a group per 128 rows, both use every tile, which is
-// dequantized once for 256 rows.  RT = 1 (at most 128 rows): the groups take the tiles in
-// turn, each with an O of its own, and leave two records per part.
-// Bound: shared-memory bandwidth.  Per 128 keys and SM in 128-byte cycles (RT = 2): raw
-// tile in and out 288, operands written 512, Q and K read by S 2 x 768, V by O 2 x 256;
-// its tensor core needs 2048 cycles for them.
+//                          TMEM, rescaled only when a row's base moves
+// RT = 2 (more than 128 rows): a group per 128 rows, both use every tile, which is
+// dequantized once for 256 rows.  RT = 1: the groups take the tiles in turn, each with an O
+// of its own, and leave two records per part.
+//
+// Bound: the chain S -> exponentials -> O of a group, about 4500 cycles a tile (RT = 2), of
+// which the tensor core works 2800 -- 32 instructions of 128 x 128 x 16 at about 88 cycles,
+// not the 64 of its rate: S reads Q and K from shared memory, 8 KB an instruction -- and the
+// exponentials take about 1600; the groups run in turn, so that each works under the
+// other's products.  What a part costs by itself (Q, the nodes, the record: some 20,000
+// cycles) is counted when the work is shared out.
+// Measured, whole calls, 32 heads on 8 KV heads: 32 requests of 512 .. 8192 keys with 61
+// nodes 205 us (140 GFLOP: 680 TFLOP/s; the 4-bit cache and all else read once: 0.95 TB/s);
+// one request of 65536 keys with 33 nodes 84 us; of 2048 keys with 61 nodes 21.5 us.
+//
+// What was slower: steps of 64 keys with two S buffers a group (batch 480, 128 keys 450 at
+// that time), one dequantizing warpgroup for K and V (334 against 315), a pass for the row
+// maximum before the exponentials (216 against 207).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
@@ -384,7 +394,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
       const unsigned char* scales = static_cast<const unsigned char*>(op ? kv.v_scale : kv.k_scale);
       unsigned char* ring = sRaw + (op ? C::RK * kRawB : 0);
       Parts p = first;
-      bool live = true;
+      bool live = !(op == 0 && cta == 0 && (tail.flags & E3_KV_SELFTEST_STALL));  // (K that never comes)
       int st = 0;
       uint32_t par = 1u;  // parity of the stages' last release (a fresh barrier counts as released)
       do {

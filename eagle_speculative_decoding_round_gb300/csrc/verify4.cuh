@@ -1,5 +1,4 @@
-// verify4.cuh -- what the kernels of tree_verify_attn4 share: how the work is cut, and the
-// merge of the parts.
+// verify4.cuh -- what the kernels of tree_verify_attn4 share: how the work is cut.
 #pragma once
 #include <math.h>
 
@@ -92,80 +91,6 @@ __device__ __forceinline__ V4Place find_place(const V4Geom& g, const e3_kv4_laye
     base += __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
   return f;
-}
-
-// Merge of a pair's records: one warp per (b, i, h) row, hd/32 dims a lane.  ROWS: the
-// row tile of the kernel that wrote them.  The workers that began and ended the pair left
-// their numbers in `ends`, so the records are found without the search; the first
-// records' values are requested together with their weights.
-template <int HD, int ROWS, int KEYS, int SPLIT>
-__global__ void __launch_bounds__(128)
-verify4_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __restrict__ kv_len,
-                     const __grid_constant__ V4Geom g, const float* __restrict__ ws_o, const float2* __restrict__ ws_ml,
-                     const int32_t* __restrict__ ends, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
-  constexpr int PER = HD / 32;
-  constexpr int AHEAD = 8;
-  const int lane = threadIdx.x & 31;
-  const unsigned row = blockIdx.x * 4u + (threadIdx.x >> 5);
-  const unsigned stride = static_cast<unsigned>(g.R) * g.H;
-  const int b = static_cast<int>(row / stride);
-  if (b >= g.B) {
-    pdl_wait();
-    return;
-  }
-  const int ih = static_cast<int>(row - b * stride), i = ih / g.H, h = ih - i * g.H;
-  const int kvh = h / g.G, r = i * g.G + h - kvh * g.G, rt = r / ROWS;
-  const size_t pair = static_cast<size_t>(b) * g.KVH * g.RG + kvh * g.RG + rt;
-  pdl_wait();
-  pdl_trigger();
-  const int P = kv_len[b], c0 = ends[2 * pair], c1 = ends[2 * pair + 1];
-  // (a worker that gave up, its error word set, may not have left its number)
-  if (pair_units<KEYS>(g, kv, P) == 0 || c0 < 0 || c1 < c0 || c1 >= g.workers) return;
-  const int n = (c1 - c0 + 1) * SPLIT;
-  const size_t base = (pair + c0) * SPLIT * ROWS + (r - rt * ROWS);  // then ROWS apart
-  using Vec = typename std::conditional<PER == 4, float4, float2>::type;
-  auto value = [&](int q) { return reinterpret_cast<const Vec*>(ws_o + (base + static_cast<size_t>(q) * ROWS) * HD)[lane]; };
-  Vec x[AHEAD];
-#pragma unroll
-  for (int q = 0; q < AHEAD; ++q)
-    if (q < n) x[q] = value(q);
-  float2 ml = lane < n ? ws_ml[base + static_cast<size_t>(lane) * ROWS] : make_float2(-INFINITY, 0.0f);
-  float M = ml.y != 0.0f ? ml.x : -INFINITY;
-  for (int q = lane + 32; q < n; q += 32) {
-    const float2 y = ws_ml[base + static_cast<size_t>(q) * ROWS];
-    if (y.y != 0.0f) M = fmaxf(M, y.x);
-  }
-  M = warp_reduce(M, MaxF());
-  float acc[PER];
-#pragma unroll
-  for (int u = 0; u < PER; ++u) acc[u] = 0.0f;
-  float den = 0.0f;
-  for (int q0 = 0; q0 < n; q0 += 32) {
-    if (q0 > 0) ml = q0 + lane < n ? ws_ml[base + static_cast<size_t>(q0 + lane) * ROWS] : make_float2(-INFINITY, 0.0f);
-    // (-1: a record without keys, whose values were never written; a NaN sum stays one)
-    const float w = ml.y != 0.0f ? ml.y * ex2(ml.x - M) : -1.0f;
-    den += w == -1.0f ? 0.0f : w;
-    const int nq = min(32, n - q0);
-    for (int j0 = 0; j0 < nq; j0 += AHEAD) {
-#pragma unroll
-      for (int j = 0; j < AHEAD; ++j) {
-        const float wj = __shfl_sync(0xFFFFFFFFu, w, (j0 + j) & 31);
-        if (j0 + j < nq && wj != -1.0f) {
-          const float* v = reinterpret_cast<const float*>(&x[j]);
-#pragma unroll
-          for (int u = 0; u < PER; ++u) acc[u] = fmaf(wj, v[u], acc[u]);
-        }
-        if (q0 + j0 + AHEAD + j < n) x[j] = value(q0 + j0 + AHEAD + j);
-      }
-    }
-  }
-  den = warp_reduce(den, [](float p, float q) { return p + q; });
-  const float inv = den != 0.0f ? 1.0f / den : 0.0f;
-  __nv_bfloat16* out = O + static_cast<size_t>(row) * HD + lane * PER;
-#pragma unroll
-  for (int u = 0; u < PER; u += 2)
-    *reinterpret_cast<uint32_t*>(out + u) = pack2_bf16(acc[u] * inv, acc[u + 1] * inv);
-  if (lane == 0) lse[row] = den != 0.0f ? (M + log2f(den)) * kLn2 : -INFINITY;
 }
 
 int num_sms() {

@@ -134,7 +134,8 @@ typedef struct {
  * thread waits on a barrier that nothing arrives on: the bounded wait runs out
  * after about a second, the kernel sets E3_DEV_ERR_TIMEOUT in dev_err, waits for
  * its own copies in flight, frees its tensor memory and returns; O and lse are not
- * valid.  Other paths and calls ignore the bit. */
+ * valid.  In tree_verify_attn4's, with the bit on the tail, one CTA waits for keys that
+ * nothing brings, with the same end.  Other paths and calls ignore the bit. */
 #define E3_KV_SELFTEST_STALL 0x40000000
 typedef struct {
   void* k;
@@ -465,7 +466,7 @@ typedef struct {
   int head_dim;              /* 64 or 128 */
   float k_unit;
   float v_unit;
-  int flags;                 /* 0 or E3_KV_PREFIX_STABLE (see tree_verify_attn4) */
+  int flags;                 /* 0 or E3_KV_PREFIX_STABLE (not used) */
 } e3_kv4_layer;
 
 /* ---------------------------------------------------------------------------
@@ -517,8 +518,11 @@ E3_API e3_status kv4_read(const e3_kv4_layer* layers, const e3_kv_layer* dst, in
  * kv_len[b] outside [0, max_kv_len] or beyond the pages sets E3_DEV_ERR_CAPACITY and
  * leaves the request's outputs unwritten; a page id out of range sets it and makes
  * the request's outputs unspecified.
+ * Arithmetic: products of the prefix in fp16 (exact operands but for P), of the nodes'
+ *   V in bf16, weights up to 2^15 of a row's base, sums in fp32: nodes' V up to 2^100 in
+ *   magnitude cannot overflow them.
  * Limits: head_dim 64 or 128; R <= 256; n_q_heads % n_kv_heads == 0; tail pages hold R
- *   slots.  E3_KV_PREFIX_STABLE in kv->flags: the promise of tree_verify_attn.
+ *   slots.  E3_KV_PREFIX_STABLE in kv->flags is accepted (and not used).
  * ws: eagle3_verify4_workspace_bytes(...) bytes of device scratch, 16-byte aligned;
  *   calls that may overlap on the GPU need scratch of their own.
  * ------------------------------------------------------------------------- */

@@ -496,6 +496,30 @@ def test_verify_attn4_on_streams_and_in_a_graph():
     attn_check(a, *out)
 
 
+@pytest.mark.parametrize("R,H", [(20, 16), (40, 16)])
+def test_verify_attn4_wait_that_runs_out(R, H):
+    """The self-test bit on the tail: a tile that never comes ends the call with the error word set,
+    after the waits' bound, and leaves nothing behind that the next call on the same buffers meets."""
+    d = attn_inputs(R, 2, R, H, 4, 128, [900, 300], 64)
+    dev = {}
+    need = e3.eagle3_verify4_workspace_bytes(2, R, H, 4, 128, 900)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    attn_call(d, dev=dev, ws=ws)
+    torch.cuda.synchronize()
+    make = e3.make_kv_layer
+    try:
+        e3.make_kv_layer = lambda *a: make(*a, flags=e3.E3_KV_SELFTEST_STALL)
+        _, _, err = attn_call(d, dev=dev, ws=ws)
+    finally:
+        e3.make_kv_layer = make
+    torch.cuda.synchronize()
+    assert int(err.item()) == e3.E3_DEV_ERR_TIMEOUT
+    O, lse, err = attn_call(d, dev=dev, ws=ws)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    attn_check(d, O, lse)
+
+
 @pytest.mark.parametrize("B,R,H,KVH,hd,most", [
     (48, 17, 32, 8, 128, 300),    # 68 rows a KV head: parts of one tile and of several
     (48, 17, 32, 8, 128, 40),     # no more than the nodes' tile and one of the prefix
