@@ -574,19 +574,21 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
   }
 }
 
-// Merge of a pair's records: one warp per (b, i, h) row, hd/32 dims a lane.  ROWS: the
-// row tile of the kernel that wrote them.  The workers that began and ended the pair left
-// their numbers in `ends`, so the records are found without the search; the first
-// records' values are requested together with their weights.
-template <int HD, int ROWS>
-__global__ void __launch_bounds__(128)
+// Merge of a pair's records: WPR warps per (b, i, h) row, each a run of the records, hd/32
+// dims a lane.  ROWS: the row tile of the kernel that wrote them.  The workers that began
+// and ended the pair left their numbers in `ends`, so the records are found without the
+// search; the first records' values are requested together with their weights.
+template <int HD, int ROWS, int WPR>
+__global__ void __launch_bounds__(WPR == 1 ? 128 : WPR * 32)
 verify4_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __restrict__ kv_len,
                      const __grid_constant__ V4Geom g, const float* __restrict__ ws_o, const float2* __restrict__ ws_ml,
                      const int32_t* __restrict__ ends, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
   constexpr int PER = HD / 32;
   constexpr int AHEAD = 8;
-  const int lane = threadIdx.x & 31;
-  const unsigned row = blockIdx.x * 4u + (threadIdx.x >> 5);
+  __shared__ float s_acc[WPR][HD];
+  __shared__ float2 s_md[WPR];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned row = WPR == 1 ? blockIdx.x * 4u + warp : blockIdx.x;
   const unsigned stride = static_cast<unsigned>(g.R) * g.H;
   const int b = static_cast<int>(row / stride);
   if (b >= g.B) {
@@ -601,8 +603,9 @@ verify4_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __r
   const int P = kv_len[b], c0 = ends[2 * pair], c1 = ends[2 * pair + 1];
   // (a worker that gave up, its error word set, may not have left its number)
   if (pair_units<kGran>(g, kv, P) == 0 || c0 < 0 || c1 < c0 || c1 >= g.workers) return;
-  const int n = c1 - c0 + 1;
-  const size_t base = (pair + c0) * ROWS + (r - rt * ROWS);  // then ROWS apart
+  const int all = c1 - c0 + 1, from = WPR == 1 ? 0 : warp * ((all + WPR - 1) / WPR);
+  const int n = WPR == 1 ? all : max(0, min(all - from, (all + WPR - 1) / WPR));
+  const size_t base = (pair + c0 + from) * ROWS + (r - rt * ROWS);  // then ROWS apart
   using Vec = typename std::conditional<PER == 4, float4, float2>::type;
   auto value = [&](int q) { return reinterpret_cast<const Vec*>(ws_o + (base + static_cast<size_t>(q) * ROWS) * HD)[lane]; };
   Vec x[AHEAD];
@@ -640,6 +643,28 @@ verify4_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __r
     }
   }
   den = warp_reduce(den, [](float p, float q) { return p + q; });
+  if (WPR > 1) {
+#pragma unroll
+    for (int u = 0; u < PER; ++u) s_acc[warp][lane * PER + u] = acc[u];
+    if (lane == 0) s_md[warp] = make_float2(M, den);
+    __syncthreads();
+    if (warp > 0) return;
+    M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w)
+      if (s_md[w].y != 0.0f) M = fmaxf(M, s_md[w].x);
+    den = 0.0f;
+#pragma unroll
+    for (int u = 0; u < PER; ++u) acc[u] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WPR; ++w) {
+      if (s_md[w].y == 0.0f) continue;  // (no keys)
+      const float f = ex2(s_md[w].x - M);
+      den += f * s_md[w].y;
+#pragma unroll
+      for (int u = 0; u < PER; ++u) acc[u] = fmaf(f, s_acc[w][lane * PER + u], acc[u]);
+    }
+  }
   const float inv = den != 0.0f ? 1.0f / den : 0.0f;
   __nv_bfloat16* out = O + static_cast<size_t>(row) * HD + lane * PER;
 #pragma unroll
@@ -680,9 +705,16 @@ cudaError_t launch_mma(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_
   const cudaError_t e = launch_pdl(verify4_mma_kernel<HD, NR>, dim3(g.workers / kWarps), dim3(kWarps * 32), V4Cfg<HD>::SMEM, s,
                                    1, q, kv, tail, kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, dev_err);
   if (e != cudaSuccess) return e;
-  return launch_pdl(verify4_merge_kernel<HD, 8 * NR>, dim3(static_cast<unsigned>((static_cast<long>(g.B) * g.R * g.H + 3) / 4)),
-                    dim3(128), 0, s, 1, kv, kv_len, g, static_cast<const float*>(ws_o), static_cast<const float2*>(ws_ml),
-                    static_cast<const int32_t*>(ends), o, lse);
+  const long rows = static_cast<long>(g.B) * g.R * g.H;
+  const float* co = ws_o;
+  const float2* cml = ws_ml;
+  const int32_t* ce = ends;
+  // eight warps a row where a row's records may be many
+  if (g.workers > 16l * g.B * g.KVH * g.RG)
+    return launch_pdl(verify4_merge_kernel<HD, 8 * NR, 8>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, s, 1, kv, kv_len, g, co,
+                      cml, ce, o, lse);
+  return launch_pdl(verify4_merge_kernel<HD, 8 * NR, 1>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, 1, kv, kv_len,
+                    g, co, cml, ce, o, lse);
 }
 
 }  // namespace

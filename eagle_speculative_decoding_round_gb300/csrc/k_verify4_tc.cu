@@ -1,5 +1,5 @@
 // k_verify4_tc.cu -- tree_verify_attn4 on the 5th-generation tensor cores (head_dim 128,
-// more than 16 query rows per KV head).
+// more than 32 query rows per KV head).
 //
 // Work is cut as in verify4.cuh: a pair is (request, KV head, tile of RT * 128 query rows),
 // its units are tiles of 128 prefix keys and then of 128 tree nodes; one CTA per SM takes
@@ -980,7 +980,11 @@ cudaError_t launch_tc(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_k
 
 }  // namespace
 
-bool verify4_uses_tc(int R, int H, int KVH, int hd) { return hd == kHD && H / KVH * R > 16; }
+// Up to 32 query rows per KV head the granule kernel's one or two tiles of 16 rows cost less,
+// beyond them it would read the cache once more for every 16.  32 heads on 8, us, granule
+// kernel / this one: 32 requests of 512 .. 8192 keys with 16, 32, 48 rows 66 / 145, 114 / 150,
+// 163 / 152; one request of 32768 keys with 16, 32 rows 33 / 47, 39 / 49.
+bool verify4_uses_tc(int R, int H, int KVH, int hd) { return hd == kHD && H / KVH * R > 32; }
 
 size_t verify4_tc_workspace_bytes(int B, int R, int H, int KVH, int max_kv_len) {
   const V4Geom g = make_geom_tc(B, R, H, KVH, max_kv_len);
