@@ -135,14 +135,15 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
   int b = at.b;
   if (b >= g.B) return;
   long long todo = at.share;
-  int units = pair_units<kGran>(g, kv, kv_len[b]);
+  int real = pair_units<kGran>(g, kv, kv_len[b]), units = real + at.extra;  // a pair's granules; with what a part costs
   int pq = static_cast<int>((at.share * worker - at.before) / units);  // the pair within the request
   int x0 = static_cast<int>(at.share * worker - at.before - static_cast<long long>(pq) * units);
   unsigned char* ring = smem + warp * kStages * C::STAGE;
-  for (;;) {
-    // one pair's part of this share: units [x0, x1)
+  for (;; x0 = 0) {
+    // one pair's part of this share: granules [x0, x1)
     const int P = kv_len[b];
-    const int x1 = static_cast<int>(min(static_cast<long long>(units), x0 + todo));
+    const int w1 = static_cast<int>(min(static_cast<long long>(units), x0 + todo)), x1 = min(w1, real);
+    if (x0 < real) {
     const int kvh = pq / g.RG, rg = pq - kvh * g.RG;
     const int NG = (P + kGran - 1) / kGran;
     const int ga = x0, ngran = max(0, min(x1, NG) - x0);  // the prefix granules
@@ -557,19 +558,20 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
     if (lane == 0) {
       int32_t* e = ends + 2 * (static_cast<size_t>(b) * Qn + pq);
       if (x0 == 0) e[0] = worker;
-      if (x1 == units) e[1] = worker;
+      if (x1 == real) e[1] = worker;
     }
+    }  // (a share may begin behind its first pair's granules)
     // the next pair of this share
-    todo -= x1 - x0;
+    todo -= w1 - x0;
     if (todo <= 0) break;
-    x0 = 0;
     if (++pq == Qn) {
       pq = 0;
       for (++b; b < g.B; ++b) {
-        units = pair_units<kGran>(g, kv, kv_len[b]);
-        if (units > 0) break;
+        real = pair_units<kGran>(g, kv, kv_len[b]);
+        if (real > 0) break;
       }
       if (b >= g.B) break;
+      units = real + at.extra;
     }
   }
 }
@@ -686,7 +688,8 @@ V4Geom make_geom(int B, int R, int H, int KVH, int max_kv_len) {
   g.RG = (g.G * R + g.rows - 1) / g.rows;
   g.max_kv_len = max_kv_len;
   g.workers = (g.rows == 8 ? 4 : 2) * num_sms() * kWarps;
-  g.min_share = 4;
+  g.min_share = 3;
+  g.extra = 4;
   return g;
 }
 

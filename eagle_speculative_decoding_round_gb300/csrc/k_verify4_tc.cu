@@ -943,6 +943,7 @@ V4Geom make_geom_tc(int B, int R, int H, int KVH, int max_kv_len) {
   // the shares where requests differ in length.  32 requests of 512 to 8192 keys, us: 298
   // without, 249, 241, 222, 221, 224 with 1, 2, 3, 4, 6.
   g.extra = 4;
+  g.extra_from = 8;
   return g;
 }
 

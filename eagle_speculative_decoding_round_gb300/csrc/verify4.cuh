@@ -34,7 +34,8 @@ struct V4Geom {
   int RG;       // row tiles of a KV head
   int workers;  // shares
   int min_share;
-  int extra;  // units that a pair counts beyond its own, for what a part costs by itself
+  int extra;  // units that a pair counts beyond its own, for what a part costs by itself,
+  int extra_from;  // where shares are of this many units or more
   int max_kv_len;
 };
 
@@ -64,7 +65,7 @@ __device__ __forceinline__ V4Place find_place(const V4Geom& g, const e3_kv4_laye
     live += __popc(__ballot_sync(0xFFFFFFFFu, u > 0));
   }
   V4Place f;
-  f.extra = total * Q >= 8ll * g.workers ? g.extra : 0;
+  f.extra = total * Q >= static_cast<long long>(g.extra_from) * g.workers ? g.extra : 0;
   total += static_cast<long long>(live) * f.extra;
   f.share = max((total * Q + g.workers - 1) / g.workers, static_cast<long long>(g.min_share));
   const long long at = f.share * worker;
