@@ -689,7 +689,10 @@ V4Geom make_geom(int B, int R, int H, int KVH, int max_kv_len) {
   g.max_kv_len = max_kv_len;
   g.workers = (g.rows == 8 ? 4 : 2) * num_sms() * kWarps;
   g.min_share = 3;
-  g.extra = 4;
+  // what a part costs by itself, in granules: 32 requests of 512 .. 8192 keys, one node, us:
+  // 47.5 without, 46.2, 44.3, 43.7, 45.4 with 4, 7, 10, 14; 3 requests of up to 1025 keys,
+  // 15 nodes, narrow heads: 21.5 without, 10.7
+  g.extra = 10;
   return g;
 }
 
