@@ -267,36 +267,40 @@ __device__ __forceinline__ void bring_rows(const __nv_bfloat16* from, int own, u
                  : "memory");
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
 }
-// magnitudes' bits: the larger of the even and of the odd elements
-__device__ __forceinline__ uint32_t max_bits(const uint4& y) {
-  return __vmaxu2(__vmaxu2(y.x & 0x7FFF7FFFu, y.y & 0x7FFF7FFFu), __vmaxu2(y.z & 0x7FFF7FFFu, y.w & 0x7FFF7FFFu));
-}
-// the slab's rows from bf16 to fp16 in place, each row's largest magnitude scaled to [1, 2)
-// (which keeps its bits down to 2^-24 of it); factor(row, its magnitude's bits, the power).  A
-// row with a NaN or an Inf becomes zeros.
-template <class F>
-__device__ __forceinline__ void rows_to_half(unsigned char* slab, int lane, F factor) {
+// largest magnitude of row `rr` as bf16 bits (a NaN: 0x7FFF).  A thread to a row: the
+// swizzle gives the eight lanes that read together banks of their own, and no shuffles are
+// needed (half a warp to a row, with them: 6000 cycles for 32 rows, so 1500).
+__device__ __forceinline__ uint32_t row_top(unsigned char* slab, int rr) {
+  __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
 #pragma unroll 4
-  for (int i = 0; i < 16; ++i) {
-    const int rr = 2 * i + (lane >> 4);
-    uint4* at = reinterpret_cast<uint4*>(row_chunk(slab, rr, lane & 15));
+  for (int c = 0; c < 16; ++c) {
+    const uint4 y = *reinterpret_cast<const uint4*>(row_chunk(slab, rr, c));
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&y);
+    m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3]))));
+  }
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
+  return max(w & 0xFFFFu, w >> 16);
+}
+// Row `rr` from bf16 to fp16 in place, its largest magnitude `top` scaled by a power of two,
+// whose exponent is returned, to [1, 2) ([2, 4) from 2^127 on), which keeps its bits down
+// to 2^-24 of it.  A row with a NaN or an Inf becomes zeros.
+__device__ __forceinline__ int row_to_half(unsigned char* slab, int rr, uint32_t top) {
+  const int ex = min(max(static_cast<int>(top >> 7), 1) - 127, 126);
+  const float f = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+  const bool bad = top >= 0x7F80u;
+#pragma unroll 4
+  for (int c = 0; c < 16; ++c) {
+    uint4* at = reinterpret_cast<uint4*>(row_chunk(slab, rr, c));
     const uint4 y = *at;
-    uint32_t am = max_bits(y);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) am = __vmaxu2(am, __shfl_xor_sync(0xFFFFFFFFu, am, o));
-    am = max(am & 0xFFFFu, am >> 16);
-    const int ex = max(static_cast<int>(am >> 7), 1) - 127;
-    if ((lane & 15) == 0) factor(rr, am, ex);
-    const int na = -ex / 2;
-    const float f0 = __uint_as_float(static_cast<uint32_t>(127 + na) << 23);
-    const float f1 = __uint_as_float(static_cast<uint32_t>(127 - ex - na) << 23);
     uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      w[k] = am < 0x7F80u ? h2u(__floats2half2_rn(__uint_as_float(w[k] << 16) * f0 * f1, __uint_as_float(w[k] & 0xFFFF0000u) * f0 * f1)) : 0u;
+      w[k] = bad ? 0u : h2u(__floats2half2_rn(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f));
     *at = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  return ex;
 }
 
 template <int RT>
@@ -564,22 +568,15 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           bring_rows(static_cast<const __nv_bfloat16*>(op ? tail.v : tail.k), own, slab, lane);
           // a node with a NaN or an Inf leaves the product: its scores get a NaN factor, rows
           // that see its V are marked
+          const uint32_t top = row_top(slab, lane);
           if (op == 0) {
-            rows_to_half(slab, lane, [&](int rr, uint32_t am, int ex) {
-              s_fac[slot * kKeys + dw * 32 + rr] = am >= 0x7F80u ? __int_as_float(0x7FC00000) : pow2f(ex);
-            });
+            const int ex = row_to_half(slab, lane, top);
+            s_fac[slot * kKeys + dw * 32 + lane] = top >= 0x7F80u ? __int_as_float(0x7FC00000) : pow2f(ex);
           } else {
-            uint32_t bad_v = 0u;
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-              uint4* at = reinterpret_cast<uint4*>(row_chunk(slab, 2 * i + (lane >> 4), lane & 15));
-              const uint32_t am = max_bits(*at);
-              const bool bad = max(am & 0xFFFFu, am >> 16) >= 0x7F80u;
-              if (bad) *at = make_uint4(0u, 0u, 0u, 0u);
-              const uint32_t hit = __ballot_sync(0xFFFFFFFFu, bad);
-              bad_v |= ((hit & 0xFFFFu) ? 1u << (2 * i) : 0u) | (hit >> 16 ? 2u << (2 * i) : 0u);
-            }
-            if (lane == 0) s_bad[slot * 4 + dw] = bad_v;
+            const uint32_t bad = __ballot_sync(0xFFFFFFFFu, top >= 0x7F80u);
+            if (lane == 0) s_bad[slot * 4 + dw] = bad;
+            if (top >= 0x7F80u)
+              for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(row_chunk(slab, lane, c)) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         fence_async_smem();  // generic-proxy writes -> tensor core
@@ -624,7 +621,9 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           bring_rows(Q + static_cast<size_t>(p.b) * g.R * g.H * kHD, row_ok ? node * g.H + head : -1, slab, lane);
           // (a row with a NaN or an Inf: a NaN factor.  Below 2^-64 a row's scores are as good
           // as zero, and their factor would underflow)
-          rows_to_half(slab, lane, [&](int rr, uint32_t am, int ex) { ex_rows[rr] = am >= 0x7F80u ? 128 : max(ex, -64); });
+          const uint32_t top = row_top(slab, lane);
+          const int ex = row_to_half(slab, lane, top);
+          ex_rows[lane] = top >= 0x7F80u ? 128 : max(ex, -64);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) bar_arrive(&q_full[grp]);
