@@ -258,7 +258,7 @@ __device__ __forceinline__ unsigned char* row_chunk(unsigned char* slab, int rr,
 // rows `own` (a lane's own row, -1: zeros) of `from` into the slab
 __device__ __forceinline__ void bring_rows(const __nv_bfloat16* from, int own, unsigned char* slab, int lane) {
   const int c = lane & 15;
-#pragma unroll 4
+#pragma unroll 8
   for (int i = 0; i < 16; ++i) {
     const int rr = 2 * i + (lane >> 4);
     const int at = __shfl_sync(0xFFFFFFFFu, own, rr);
@@ -274,7 +274,7 @@ __device__ __forceinline__ void bring_rows(const __nv_bfloat16* from, int own, u
 // needed (half a warp to a row, with them: 6000 cycles for 32 rows, so 1500).
 __device__ __forceinline__ uint32_t row_top(unsigned char* slab, int rr) {
   __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
-#pragma unroll 4
+#pragma unroll 8
   for (int c = 0; c < 16; ++c) {
     const uint4 y = *reinterpret_cast<const uint4*>(row_chunk(slab, rr, c));
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&y);
@@ -290,7 +290,7 @@ __device__ __forceinline__ int row_to_half(unsigned char* slab, int rr, uint32_t
   const int ex = min(max(static_cast<int>(top >> 7), 1) - 127, 126);
   const float f = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
   const bool bad = top >= 0x7F80u;
-#pragma unroll 4
+#pragma unroll 8
   for (int c = 0; c < 16; ++c) {
     uint4* at = reinterpret_cast<uint4*>(row_chunk(slab, rr, c));
     const uint4 y = *at;
