@@ -186,8 +186,17 @@ __device__ __forceinline__ void dequantize16(uint2 c, uint8_t e, float unit, uin
     const float2 f = __half22float2(h);
     o[i] = pack2_bf16(f.x * s, f.y * s);
   }
+  // Two neighbouring threads' groups are 64 bytes in a row: they swap the second piece of
+  // the first for the first of the second, so that each store fills whole sectors
+  const bool odd = threadIdx.x & 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = __shfl_xor_sync(3u << (threadIdx.x & 30), odd ? o[i] : o[4 + i], 1);
+    if (odd) o[i] = x; else o[4 + i] = x;
+  }
+  out -= odd ? 1 : 0;  // even: pieces 0 and 2 of the 64 bytes, odd: 1 and 3
   out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  out[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  out[2] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 __global__ void __launch_bounds__(kThreads)
