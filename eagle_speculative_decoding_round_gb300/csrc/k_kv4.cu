@@ -79,8 +79,8 @@ __device__ __forceinline__ uint2 quantize16(const uint32_t (&w)[8], float unit, 
       const float2 a = make_float2(x[2 * i], x[2 * i + 1]), rr = make_float2(r, r);
       const float2 q = __fmul2_rn(a, rr);
       const float2 d = __ffma2_rn(__ffma2_rn(q, make_float2(-s, -s), a), rr, q);
-      y[2 * i] = d.x == 0.0f ? a.x * 0.0f : d.x;  // (the sign of a zero value is kept)
-      y[2 * i + 1] = d.y == 0.0f ? a.y * 0.0f : d.y;
+      y[2 * i] = copysignf(d.x, a.x);  // (a zero value's sign would be lost)
+      y[2 * i + 1] = copysignf(d.y, a.y);
     }
   } else {  // a scale at its bound or of 0
     const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
