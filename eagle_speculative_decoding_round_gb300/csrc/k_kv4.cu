@@ -6,7 +6,10 @@
 // quantized once, when it becomes part of the prefix.
 //
 // A thread owns one group of 16 values: two 16-byte loads, one scale, eight bytes of
-// codes.  Bound: memory (2 + 9/16 bytes per value).
+// codes.  Bound: memory (2 + 9/16 bytes per value), and beside it the append's instructions
+// (190 a group, two thirds of the issue slots).  Two prompts of 8191 rows, four layers, 8
+// heads x 128: append and read 121 us (612 MB: 5.1 TB/s); the read 60 us, 72 when each
+// thread stored its own 32 bytes in two halves.
 #include <cuda_fp16.h>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>

@@ -22,11 +22,11 @@
 // which the tensor core works 2800 -- 32 instructions of 128 x 128 x 16 at about 88 cycles,
 // not the 64 of its rate: S reads Q and K from shared memory, 8 KB an instruction -- and the
 // exponentials take about 1600; the groups run in turn, so that each works under the
-// other's products.  What a part costs by itself (Q, the nodes, the record: some 20,000
+// other's products.  What a part costs by itself (Q, the nodes, the record: some 15,000
 // cycles) is counted when the work is shared out.
 // Measured, whole calls, 32 heads on 8 KV heads: 32 requests of 512 .. 8192 keys with 61
-// nodes 205 us (140 GFLOP: 680 TFLOP/s; the 4-bit cache and all else read once: 0.95 TB/s);
-// one request of 65536 keys with 33 nodes 84 us; of 2048 keys with 61 nodes 21.5 us.
+// nodes 180 us (140 GFLOP: 780 TFLOP/s; the 4-bit cache and all else read once: 1.1 TB/s);
+// one request of 65536 keys with 33 nodes 80 us; of 2048 keys with 61 nodes 17.5 us.
 //
 // What was slower: steps of 64 keys with two S buffers a group (batch 480, 128 keys 450 at
 // that time), one dequantizing warpgroup for K and V (334 against 315), a pass for the row
@@ -938,9 +938,10 @@ V4Geom make_geom_tc(int B, int R, int H, int KVH, int max_kv_len) {
   g.max_kv_len = max_kv_len;
   g.workers = num_sms();
   g.min_share = 1;
-  // A part costs about four tiles by itself (Q, the nodes, a record): counted, they even out
-  // the shares where requests differ in length.  32 requests of 512 to 8192 keys, us: 298
-  // without, 249, 241, 222, 221, 224 with 1, 2, 3, 4, 6.
+  // What a part costs by itself (Q, the nodes, a record), in tiles: counted, it evens out the
+  // shares where requests differ in length.  32 requests of 512 to 8192 keys, us: 202, 186,
+  // 185 with 2, 3, 4 (an earlier form of the kernel 298 without, 221 with 4).  Not where a
+  // share is a few tiles: it would leave SMs without any.
   g.extra = 4;
   g.extra_from = 8;
   return g;
