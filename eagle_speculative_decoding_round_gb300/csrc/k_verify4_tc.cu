@@ -940,10 +940,11 @@ V4Geom make_geom_tc(int B, int R, int H, int KVH, int max_kv_len) {
   g.min_share = 1;
   // What a part costs by itself (Q, the nodes, a record), in tiles: counted, it evens out the
   // shares where requests differ in length.  32 requests of 512 to 8192 keys, us: 202, 186,
-  // 185 with 2, 3, 4 (an earlier form of the kernel 298 without, 221 with 4).  Not where a
-  // share is a few tiles: it would leave SMs without any.
+  // 185 with 2, 3, 4 (an earlier form of the kernel 298 without, 221 with 4); of 300 keys 56
+  // against 62.  Not where a share is a few tiles, which it would make longer (16 of 512
+  // keys 39 against 36).
   g.extra = 4;
-  g.extra_from = 8;
+  g.extra_from = 5;
   return g;
 }
 
