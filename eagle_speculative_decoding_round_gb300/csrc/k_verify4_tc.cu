@@ -62,7 +62,7 @@ constexpr int kTailRing = 8;             // tiles of tree nodes whose factors ar
 // launch brings the sum.
 constexpr int kThreads = 640;
 constexpr int kSoftmax0 = 4, kDeq0 = 12;
-constexpr int kRegsIssue = 80, kRegsSoftmax = 120, kRegsDeq = 80;
+constexpr int kRegsIssue = 64, kRegsSoftmax = 128, kRegsDeq = 80;
 constexpr int kNodeExp = 24;  // > kTop: a node's weight times a row of V sums below 2^(15 - 24 + 8) of it
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
