@@ -22,7 +22,7 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kBatch = 8;  // pieces of a thread whose loads are in flight together
+constexpr int kBatch = 11;  // pieces of a thread whose loads are in flight together
 constexpr int kMaxBias = 1024;
 constexpr int kMaxR = E3_MAX_NODES + 1;
 constexpr int kPer = 16384;     // tokens of a CTA at three CTAs an SM (64 KB of the row each)
@@ -282,27 +282,30 @@ logits_process_kernel(LogitsArgs a) {
           x[u].y = (t + 64 < nv ? cnt[t + 64] : 0u) | (t + 96 < nv ? static_cast<uint32_t>(cnt[t + 96]) << 16 : 0u);
         }
       }
+      int n = 0;  // this lane's seen tokens, their place behind the lower lanes'
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        n += ((x[u].x & 0xFFFFu) != 0u) + (x[u].x >> 16 != 0u) + ((x[u].y & 0xFFFFu) != 0u) + (x[u].y >> 16 != 0u);
+      if (!__any_sync(0xFFFFFFFFu, n != 0)) continue;
+      int p = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xFFFFFFFFu, p, o);
+        if (lane >= o) p += y;
+      }
+      int base = 0;
+      if (lane == 31) base = atomicAdd(&s_nseen, p);
+      p += __shfl_sync(0xFFFFFFFFu, base, 31) - n;
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         const int t = k0 + 4 * kThreads * u + (VEC ? 4 * lane : lane);
         const uint32_t cw[4] = {x[u].x & 0xFFFFu, x[u].x >> 16, x[u].y & 0xFFFFu, x[u].y >> 16};
-        if (!__any_sync(0xFFFFFFFFu, (x[u].x | x[u].y) != 0u)) continue;
-        unsigned m[4];
-        int n = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          m[j] = __ballot_sync(0xFFFFFFFFu, cw[j] != 0u);
-          n += __popc(m[j]);
-        }
-        int base = 0;
-        if (lane == 0) base = atomicAdd(&s_nseen, n);
-        base = __shfl_sync(0xFFFFFFFFu, base, 0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int p = base + __popc(m[j] & ((1u << lane) - 1u));
-          if (cw[j] != 0u && p < kSeenCap) list[p] = (static_cast<uint32_t>(t + (VEC ? j : 32 * j)) << 16) | cw[j];
-          base += __popc(m[j]);
-        }
+        for (int j = 0; j < 4; ++j)
+          if (cw[j] != 0u) {
+            if (p < kSeenCap) list[p] = (static_cast<uint32_t>(t + (VEC ? j : 32 * j)) << 16) | cw[j];
+            ++p;
+          }
       }
     }
   }
