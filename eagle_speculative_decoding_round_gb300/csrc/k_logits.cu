@@ -6,7 +6,10 @@
 // what a request's sampling rules change about them has to be changed for every node
 // before the accept step, each node with the tokens of its own path.
 //
-// Bound: memory (the row in, the row out).
+// Bound: memory (the row in, the row out), and beside it the masses' instructions (13 a
+// token of about 25).  Measured: 32 requests of 61 nodes, V = 128256, 2.0 GB: 427 us (4.7
+// TB/s); one request 37 us with the caller's conversions, 25 of them this kernel, of which
+// 6 are the lists of seen tokens.
 #include <cooperative_groups.h>
 
 #include <algorithm>
