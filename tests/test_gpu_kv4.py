@@ -639,6 +639,8 @@ LOGITS = [
     (1, 3, 200000, 5, True, True, True, True, True),
     (1, 2, 262148, 9, True, True, True, True, False),   # wider than a cluster holds
     (40, 8, 2052, 2, True, True, True, True, False),    # many rows
+    (8, 40, 40000, 3, True, True, True, True, False),   # several rows to a cluster of several CTAs
+    (4, 23, 128256, 300, True, True, True, True, True),
 ]
 
 
