@@ -283,13 +283,16 @@ __device__ __forceinline__ uint32_t row_top(unsigned char* slab, int rr) {
   const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
   return max(w & 0xFFFFu, w >> 16);
 }
+__device__ __forceinline__ void row_clear(unsigned char* slab, int rr) {
+#pragma unroll 1
+  for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(row_chunk(slab, rr, c)) = make_uint4(0u, 0u, 0u, 0u);
+}
 // Row `rr` from bf16 to fp16 in place, its largest magnitude `top` scaled by a power of two,
 // whose exponent is returned, to [1, 2) ([2, 4) from 2^127 on), which keeps its bits down
 // to 2^-24 of it.  A row with a NaN or an Inf becomes zeros.
 __device__ __forceinline__ int row_to_half(unsigned char* slab, int rr, uint32_t top) {
   const int ex = min(max(static_cast<int>(top >> 7), 1) - 127, 126);
   const float f = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-  const bool bad = top >= 0x7F80u;
 #pragma unroll 8
   for (int c = 0; c < 16; ++c) {
     uint4* at = reinterpret_cast<uint4*>(row_chunk(slab, rr, c));
@@ -297,9 +300,11 @@ __device__ __forceinline__ int row_to_half(unsigned char* slab, int rr, uint32_t
     uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      w[k] = bad ? 0u : h2u(__floats2half2_rn(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f));
+      w[k] = h2u(__float22half2_rn(
+          __fmul2_rn(make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)), make_float2(f, f))));
     *at = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  if (top >= 0x7F80u) row_clear(slab, rr);
   return ex;
 }
 
@@ -575,8 +580,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           } else {
             const uint32_t bad = __ballot_sync(0xFFFFFFFFu, top >= 0x7F80u);
             if (lane == 0) s_bad[slot * 4 + dw] = bad;
-            if (top >= 0x7F80u)
-              for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(row_chunk(slab, lane, c)) = make_uint4(0u, 0u, 0u, 0u);
+            if (top >= 0x7F80u) row_clear(slab, lane);
           }
         }
         fence_async_smem();  // generic-proxy writes -> tensor core
