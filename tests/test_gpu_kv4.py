@@ -327,7 +327,7 @@ def attn_check(d, O, lse, requests=None):
         dead = ~d["see"][b].any(-1) if d["lens"][b] == 0 else np.zeros(R, bool)
         assert np.all(O[b][dead] == 0) and np.all(np.isneginf(lse[b][dead]))
         live = ~dead
-        assert np.all(np.abs(lse[b] - l)[live] <= (ds + 2.0 ** -21 * np.abs(l))[live]), np.abs(lse[b] - l)[live].max()
+        assert np.all(np.abs(lse[b][live] - l[live]) <= (ds + 2.0 ** -21 * np.abs(l))[live]), np.abs(lse[b][live] - l[live]).max()
         # weights off by a relative w leave o + e, |e| <= w mag; the output is then rounded by at
         # most half a step OF THAT VALUE: |e| + 2^-8 (|o| + |e|).  An fp16 weight below 2^-14 is
         # off by half its subnormal step, 2^-25, whatever its size: with the largest weight at
