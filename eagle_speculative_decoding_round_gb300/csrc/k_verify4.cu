@@ -203,19 +203,22 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
     // Q as the second operand: thread (gq, tq) holds row gq of each tile, dims [DK tq, DK (tq + 1))
     uint32_t qb[NR][KS][2];
     const int rows = g.G * g.R;
+    auto load_q = [&]() {
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-      const int r = rg * ROWS + 8 * nr + gq;
-      const bool in = r < rows;
-      const int node = in ? r / g.G : 0, head = kvh * g.G + (in ? r - node * g.G : 0);
-      const uint2* qp = reinterpret_cast<const uint2*>(Q + ((static_cast<size_t>(b) * g.R + node) * g.H + head) * HD + DK * tq);
+      for (int nr = 0; nr < NR; ++nr) {
+        const int r = rg * ROWS + 8 * nr + gq;
+        const bool in = r < rows;
+        const int node = in ? r / g.G : 0, head = kvh * g.G + (in ? r - node * g.G : 0);
+        const uint2* qp = reinterpret_cast<const uint2*>(Q + ((static_cast<size_t>(b) * g.R + node) * g.H + head) * HD + DK * tq);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const uint2 x = in ? qp[ks] : make_uint2(0u, 0u);
-        qb[nr][ks][0] = x.x;
-        qb[nr][ks][1] = x.y;
+        for (int ks = 0; ks < KS; ++ks) {
+          const uint2 x = in ? qp[ks] : make_uint2(0u, 0u);
+          qb[nr][ks][0] = x.x;
+          qb[nr][ks][1] = x.y;
+        }
       }
-    }
+    };
+    load_q();
     // O^T: tile j's accumulators are dims DV gq + 2j and + 1 (rows gq and gq + 8) of query
     // rows 2 tq and 2 tq + 1 of each row tile
     float o[NR][MT][4];
@@ -230,6 +233,14 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
       poison[nr][0] = poison[nr][1] = false;
     }
 
+    auto scale_o = [&](float f) {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nr][j][e] *= f;
+    };
     // running softmax over the scores of NGR granules (already scaled, -Inf where unseen):
     // sc[.][nr] holds keys gq (0, 1) and gq + 8 (2, 3) of query rows 2 tq, 2 tq + 1;
     // probabilities replace the scores; o and l follow the moved base
@@ -280,261 +291,270 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
         }
     };
 
-    // this part's granules of 16 tree nodes, in bf16
-    if (x1 > NG) {
-      const float c2 = sm_scale * kLog2e;
-      const int words = (g.R + 63) >> 6;
-      const __nv_bfloat16* tk = static_cast<const __nv_bfloat16*>(tail.k);
-      const __nv_bfloat16* tv = static_cast<const __nv_bfloat16*>(tail.v);
-      auto tail_row = [&](int j) -> long long {  // row of tail slot j, -1 beyond R or on a bad page
-        if (j >= g.R) return -1;
-        const int page = tail.page_table[static_cast<size_t>(b) * tail.max_pages + j / tail.page_size];
-        if (page < 0 || page >= tail.n_pages) {
-          dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
-          return -1;
+    const __nv_bfloat16* tk = static_cast<const __nv_bfloat16*>(tail.k);
+    const __nv_bfloat16* tv = static_cast<const __nv_bfloat16*>(tail.v);
+    auto tail_row = [&](int j) -> long long {  // row of tail slot j, -1 beyond R or on a bad page
+      if (j >= g.R) return -1;
+      const int page = tail.page_table[static_cast<size_t>(b) * tail.max_pages + j / tail.page_size];
+      if (page < 0 || page >= tail.n_pages) {
+        dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+        return -1;
+      }
+      return (static_cast<long long>(page) * g.KVH + kvh) * tail.page_size + j % tail.page_size;
+    };
+    // Nodes behind the prefix: the prefix sums in units of v_unit, in which a node's V may pass
+    // the range (2^100 at a unit of 2^-60); in values the prefix's sum is far below it.  Heads of
+    // 64 take the nodes first where the unit leaves room (256 weights of up to 2^15 and V of up
+    // to 2^100 have 2^4 of it to 2^127): their loads then pass under the first granules' (3
+    // requests of 15 nodes: 10.8 us, 11.2 behind).  Heads of 128 would pay with registers (32
+    // requests, one node: 44.2, 43.4 behind).
+    const bool nodes_first = HD == 64 && kv.v_unit >= 0.0625f;
+#pragma unroll(HD == 64 ? 1 : 2)
+    for (int turn = 0; turn < 2; ++turn) {
+      if (nodes_first == (turn == 0)) {
+        if (x1 <= NG) continue;
+        if (!nodes_first && ngran > 0) {
+          load_q();  // in bf16 again
+          scale_o(kv.v_unit);
         }
-        return (static_cast<long long>(page) * g.KVH + kvh) * tail.page_size + j % tail.page_size;
-      };
+        const float c2 = sm_scale * kLog2e;
+        const int words = (g.R + 63) >> 6;
 #pragma unroll 1
-      for (int j0 = (max(x0, NG) - NG) * kGran; j0 < (x1 - NG) * kGran; j0 += kGran) {
-        // (V is loaded after the scores: both at once would cost the main loop its registers)
-        uint2 kr[2][KS];
-        uint32_t raw[4][DV / 2];  // V of keys (tile 0: two, tile 1: two), DV dims each
-        uint64_t bits[NR][2];
+        for (int j0 = (max(x0, NG) - NG) * kGran; j0 < (x1 - NG) * kGran; j0 += kGran) {
+          // (V is loaded after the scores: both at once would cost the main loop its registers)
+          uint2 kr[2][KS];
+          uint32_t raw[4][DV / 2];  // V of keys (tile 0: two, tile 1: two), DV dims each
+          uint64_t bits[NR][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const long long row = tail_row(j0 + key_of(t, gq));
-          const uint2* kp = reinterpret_cast<const uint2*>(tk + max(row, 0ll) * HD + DK * tq);
+          for (int t = 0; t < 2; ++t) {
+            const long long row = tail_row(j0 + key_of(t, gq));
+            const uint2* kp = reinterpret_cast<const uint2*>(tk + max(row, 0ll) * HD + DK * tq);
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks) kr[t][ks] = row >= 0 ? kp[ks] : make_uint2(0u, 0u);
-        }
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // (a granule lies within one mask word)
-            const int r = rg * ROWS + 8 * nr + 2 * tq + e;
-            bits[nr][e] = r < rows ? mask[(static_cast<size_t>(b) * g.R + r / g.G) * words + (j0 >> 6)] >> (j0 & 63) : 0ull;
+            for (int ks = 0; ks < KS; ++ks) kr[t][ks] = row >= 0 ? kp[ks] : make_uint2(0u, 0u);
           }
-        float sc[1][NR][4];
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-          sc[0][nr][0] = sc[0][nr][1] = sc[0][nr][2] = sc[0][nr][3] = 0.0f;
-#pragma unroll
-          for (int ks = 0; ks < KS; ++ks) {
-            const uint32_t a[4] = {kr[0][ks].x, kr[1][ks].x, kr[0][ks].y, kr[1][ks].y};
-            mma_b16(sc[0][nr], a, qb[nr][ks][0], qb[nr][ks][1]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = key_of(e >> 1, gq);
-            const bool see = j0 + j < g.R && ((bits[nr][e & 1] >> j) & 1ull);
-            sc[0][nr][e] = see ? sc[0][nr][e] * c2 : -INFINITY;
-          }
-        }
-        softmax(sc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const long long row = tail_row(j0 + key_of(i >> 1, 2 * tq + (i & 1)));
-          const uint2* vp = reinterpret_cast<const uint2*>(tv + max(row, 0ll) * HD + DV * gq);
-#pragma unroll
-          for (int d = 0; d < DV / 4; ++d) {
-            const uint2 x = row >= 0 ? vp[d] : make_uint2(0u, 0u);
-            raw[i][2 * d] = x.x;
-            raw[i][2 * d + 1] = x.y;
-          }
-        }
-        uint32_t badk = 0u;  // keys of the granule with a non-finite V, as bits
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          bool bad = false;
-#pragma unroll
-          for (int d = 0; d < DV / 2; ++d)
-            bad |= (raw[i][d] & 0x7F80u) == 0x7F80u || (raw[i][d] & 0x7F800000u) == 0x7F800000u;
-          if (bad) badk |= 1u << key_of(i >> 1, 2 * tq + (i & 1));
-        }
-        badk = __reduce_or_sync(0xFFFFFFFFu, badk);
-        if (badk) {
-          // rows that do not see such a node must not meet it in 0 * Inf: it leaves the
-          // product (its dims sit in several threads), rows that see it get NaN below
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((badk >> key_of(i >> 1, 2 * tq + (i & 1))) & 1u)
-#pragma unroll
-              for (int d = 0; d < DV / 2; ++d) raw[i][d] = 0u;
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) poison[nr][e] |= (bits[nr][e] & badk) != 0ull;
-        }
+            for (int e = 0; e < 2; ++e) {  // (a granule lies within one mask word)
+              const int r = rg * ROWS + 8 * nr + 2 * tq + e;
+              bits[nr][e] = r < rows ? mask[(static_cast<size_t>(b) * g.R + r / g.G) * words + (j0 >> 6)] >> (j0 & 63) : 0ull;
+            }
+          float sc[1][NR][4];
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-          const uint32_t p0 = transpose8(pack2_bf16(sc[0][nr][0], sc[0][nr][1])), p1 = transpose8(pack2_bf16(sc[0][nr][2], sc[0][nr][3]));
+          for (int nr = 0; nr < NR; ++nr) {
+            sc[0][nr][0] = sc[0][nr][1] = sc[0][nr][2] = sc[0][nr][3] = 0.0f;
 #pragma unroll
-          for (int d = 0; d < DV / 2; ++d) {
-            const uint32_t a[4] = {__byte_perm(raw[0][d], raw[1][d], 0x5410), __byte_perm(raw[0][d], raw[1][d], 0x7632),
-                                   __byte_perm(raw[2][d], raw[3][d], 0x5410), __byte_perm(raw[2][d], raw[3][d], 0x7632)};
-            mma_b16(o[nr][d], a, p0, p1);
+            for (int ks = 0; ks < KS; ++ks) {
+              const uint32_t a[4] = {kr[0][ks].x, kr[1][ks].x, kr[0][ks].y, kr[1][ks].y};
+              mma_b16(sc[0][nr], a, qb[nr][ks][0], qb[nr][ks][1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = key_of(e >> 1, gq);
+              const bool see = j0 + j < g.R && ((bits[nr][e & 1] >> j) & 1ull);
+              sc[0][nr][e] = see ? sc[0][nr][e] * c2 : -INFINITY;
+            }
+          }
+          softmax(sc);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const long long row = tail_row(j0 + key_of(i >> 1, 2 * tq + (i & 1)));
+            const uint2* vp = reinterpret_cast<const uint2*>(tv + max(row, 0ll) * HD + DV * gq);
+#pragma unroll
+            for (int d = 0; d < DV / 4; ++d) {
+              const uint2 x = row >= 0 ? vp[d] : make_uint2(0u, 0u);
+              raw[i][2 * d] = x.x;
+              raw[i][2 * d + 1] = x.y;
+            }
+          }
+          uint32_t badk = 0u;  // keys of the granule with a non-finite V, as bits
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            bool bad = false;
+#pragma unroll
+            for (int d = 0; d < DV / 2; ++d)
+              bad |= (raw[i][d] & 0x7F80u) == 0x7F80u || (raw[i][d] & 0x7F800000u) == 0x7F800000u;
+            if (bad) badk |= 1u << key_of(i >> 1, 2 * tq + (i & 1));
+          }
+          badk = __reduce_or_sync(0xFFFFFFFFu, badk);
+          if (badk) {
+            // rows that do not see such a node must not meet it in 0 * Inf: it leaves the
+            // product (its dims sit in several threads), rows that see it get NaN below
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if ((badk >> key_of(i >> 1, 2 * tq + (i & 1))) & 1u)
+#pragma unroll
+                for (int d = 0; d < DV / 2; ++d) raw[i][d] = 0u;
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) poison[nr][e] |= (bits[nr][e] & badk) != 0ull;
+          }
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+            const uint32_t p0 = transpose8(pack2_bf16(sc[0][nr][0], sc[0][nr][1])), p1 = transpose8(pack2_bf16(sc[0][nr][2], sc[0][nr][3]));
+#pragma unroll
+            for (int d = 0; d < DV / 2; ++d) {
+              const uint32_t a[4] = {__byte_perm(raw[0][d], raw[1][d], 0x5410), __byte_perm(raw[0][d], raw[1][d], 0x7632),
+                                     __byte_perm(raw[2][d], raw[3][d], 0x5410), __byte_perm(raw[2][d], raw[3][d], 0x7632)};
+              mma_b16(o[nr][d], a, p0, p1);
+            }
           }
         }
-      }
-    }
-
-    // Q to fp16, each row's largest magnitude scaled to [1, 2); the scores' factor follows
-    float c2[NR][2];
+      } else if (ngran > 0) {
+        if (nodes_first && x1 > NG) scale_o(1.0f / kv.v_unit);
+        // Q to fp16, each row's largest magnitude scaled to [1, 2); the scores' factor follows
+        float c2[NR][2];
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
-      uint32_t am = 0u;  // largest magnitude of row gq as bf16 bits
+        for (int nr = 0; nr < NR; ++nr) {
+          uint32_t am = 0u;  // largest magnitude of row gq as bf16 bits
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+          for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) am = __vmaxu2(am, qb[nr][ks][x] & 0x7FFF7FFFu);
-      am = max(am & 0xFFFFu, am >> 16);
-      am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-      am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-      // exponent of the largest magnitude (below 2^-64 a row's scores are as good as zero)
-      const int ex = max(static_cast<int>(am >> 7) - 127, -64);
-      // 2^-ex in two factors (ex reaches 128 for Inf and NaN)
-      const float f0 = __uint_as_float(static_cast<uint32_t>(127 - ex / 2) << 23);
-      const float f1 = __uint_as_float(static_cast<uint32_t>(127 - (ex - ex / 2)) << 23);
+            for (int x = 0; x < 2; ++x) am = __vmaxu2(am, qb[nr][ks][x] & 0x7FFF7FFFu);
+          am = max(am & 0xFFFFu, am >> 16);
+          am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+          am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+          // exponent of the largest magnitude (below 2^-64 a row's scores are as good as zero)
+          const int ex = max(static_cast<int>(am >> 7) - 127, -64);
+          // 2^-ex in two factors (ex reaches 128 for Inf and NaN)
+          const float f0 = __uint_as_float(static_cast<uint32_t>(127 - ex / 2) << 23);
+          const float f1 = __uint_as_float(static_cast<uint32_t>(127 - (ex - ex / 2)) << 23);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+          for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const uint32_t w = qb[nr][ks][x];
-          const float lo = __uint_as_float(w << 16) * f0 * f1, hi = __uint_as_float(w & 0xFFFF0000u) * f0 * f1;
-          qb[nr][ks][x] = h2u(__floats2half2_rn(lo, hi));
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t w = qb[nr][ks][x];
+              const float lo = __uint_as_float(w << 16) * f0 * f1, hi = __uint_as_float(w & 0xFFFF0000u) * f0 * f1;
+              qb[nr][ks][x] = h2u(__floats2half2_rn(lo, hi));
+            }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {  // row 2 tq + e is held by lanes 4 (2 tq + e) ..
+            const int er = __shfl_sync(0xFFFFFFFFu, ex, 4 * (2 * tq + e));
+            c2[nr][e] = sm_scale * kLog2e * kv.k_unit * __uint_as_float(static_cast<uint32_t>(127 + er / 2) << 23) *
+                        __uint_as_float(static_cast<uint32_t>(127 + (er - er / 2)) << 23);
+          }
         }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {  // row 2 tq + e is held by lanes 4 (2 tq + e) ..
-        const int er = __shfl_sync(0xFFFFFFFFu, ex, 4 * (2 * tq + e));
-        c2[nr][e] = sm_scale * kLog2e * kv.k_unit * __uint_as_float(static_cast<uint32_t>(127 + er / 2) << 23) *
-                    __uint_as_float(static_cast<uint32_t>(127 + (er - er / 2)) << 23);
-      }
-    }
-    if (x1 > NG) {  // o holds V values in units of v_unit from here on
-      const float inv_vu = 1.0f / kv.v_unit;
-#pragma unroll
-      for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-        for (int j = 0; j < MT; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[nr][j][e] *= inv_vu;
-    }
 
-    // a step: kStep granules, whose products do not wait for one another.  (Keys beyond the
-    // prefix, and the granules that a last step lacks: -Inf for a score, 0 for V's scale.)
+        // a step: kStep granules, whose products do not wait for one another.  (Keys beyond the
+        // prefix, and the granules that a last step lacks: -Inf for a score, 0 for V's scale.)
 #pragma unroll 1
-    for (int i = 0; i < ngran; i += kStep) {
+        for (int i = 0; i < ngran; i += kStep) {
 #pragma unroll
-      for (int u = 0; u < kStep; ++u) load_granule((i + kStages - kStep + u) % kStages);
-      asm volatile("cp.async.wait_group %0;" ::"n"(kStages - kStep) : "memory");
-      __syncwarp();
-      float sc[kStep][NR][4];
-      const int left0 = min(P - (ga + i) * kGran, (ngran - i) * kGran);  // keys from the step's first
+          for (int u = 0; u < kStep; ++u) load_granule((i + kStages - kStep + u) % kStages);
+          asm volatile("cp.async.wait_group %0;" ::"n"(kStages - kStep) : "memory");
+          __syncwarp();
+          float sc[kStep][NR][4];
+          const int left0 = min(P - (ga + i) * kGran, (ngran - i) * kGran);  // keys from the step's first
 #pragma unroll
-      for (int u = 0; u < kStep; ++u) {
-        const unsigned char* st = ring + (i + u) % kStages * C::STAGE;
-        const int left = left0 - u * kGran;
+          for (int u = 0; u < kStep; ++u) {
+            const unsigned char* st = ring + (i + u) % kStages * C::STAGE;
+            const int left = left0 - u * kGran;
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr) sc[u][nr][0] = sc[u][nr][1] = sc[u][nr][2] = sc[u][nr][3] = 0.0f;
-        uint32_t w[2][DK / 8];
-        __half2 e2[2][DK / 16];  // the scale of each 16 dims, in both halves
+            for (int nr = 0; nr < NR; ++nr) sc[u][nr][0] = sc[u][nr][1] = sc[u][nr][2] = sc[u][nr][3] = 0.0f;
+            uint32_t w[2][DK / 8];
+            __half2 e2[2][DK / 16];  // the scale of each 16 dims, in both halves
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int key = key_of(t, gq);
-          const unsigned char* sp = st + 2 * C::CODES + key * C::SCB;
-          if (HD == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(st + code_off<HD>(key, tq));
-            w[t][0] = x.x, w[t][1] = x.y, w[t][DK / 8 - 2] = x.z, w[t][DK / 8 - 1] = x.w;
-            const uint32_t e = h2u(cvt8(*reinterpret_cast<const uint16_t*>(sp + 2 * tq)));
-            e2[t][0] = u2h(__byte_perm(e, e, 0x1010));
-            e2[t][DK / 16 - 1] = u2h(__byte_perm(e, e, 0x3232));
-          } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(st + key * C::ROWB + 8 * tq);
-            w[t][0] = x.x, w[t][1] = x.y;
-            const uint32_t e = h2u(cvt8(sp[tq]));
-            e2[t][0] = u2h(__byte_perm(e, e, 0x1010));
+            for (int t = 0; t < 2; ++t) {
+              const int key = key_of(t, gq);
+              const unsigned char* sp = st + 2 * C::CODES + key * C::SCB;
+              if (HD == 128) {
+                const uint4 x = *reinterpret_cast<const uint4*>(st + code_off<HD>(key, tq));
+                w[t][0] = x.x, w[t][1] = x.y, w[t][DK / 8 - 2] = x.z, w[t][DK / 8 - 1] = x.w;
+                const uint32_t e = h2u(cvt8(*reinterpret_cast<const uint16_t*>(sp + 2 * tq)));
+                e2[t][0] = u2h(__byte_perm(e, e, 0x1010));
+                e2[t][DK / 16 - 1] = u2h(__byte_perm(e, e, 0x3232));
+              } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(st + key * C::ROWB + 8 * tq);
+                w[t][0] = x.x, w[t][1] = x.y;
+                const uint32_t e = h2u(cvt8(sp[tq]));
+                e2[t][0] = u2h(__byte_perm(e, e, 0x1010));
+              }
+            }
+#pragma unroll
+            for (int k2 = 0; k2 < KS / 2; ++k2) {
+              __half2 x[4], y[4];
+              cvt4(w[0][k2], x);
+              cvt4(w[1][k2], y);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t a[4] = {h2u(__hmul2(x[2 * k], e2[0][k2 >> 1])), h2u(__hmul2(y[2 * k], e2[1][k2 >> 1])),
+                                       h2u(__hmul2(x[2 * k + 1], e2[0][k2 >> 1])), h2u(__hmul2(y[2 * k + 1], e2[1][k2 >> 1]))};
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) mma_f16(sc[u][nr], a, qb[nr][2 * k2 + k][0], qb[nr][2 * k2 + k][1]);
+              }
+            }
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sc[u][nr][e] = sc[u][nr][e] * c2[nr][e & 1];
+            if (left < kGran) {
+#pragma unroll
+              for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (key_of(e >> 1, gq) >= left) sc[u][nr][e] = -INFINITY;
+            }
           }
-        }
+          softmax(sc);
+          uint32_t pb[kStep][NR][2];
 #pragma unroll
-        for (int k2 = 0; k2 < KS / 2; ++k2) {
-          __half2 x[4], y[4];
-          cvt4(w[0][k2], x);
-          cvt4(w[1][k2], y);
+          for (int u = 0; u < kStep; ++u)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t a[4] = {h2u(__hmul2(x[2 * k], e2[0][k2 >> 1])), h2u(__hmul2(y[2 * k], e2[1][k2 >> 1])),
-                                   h2u(__hmul2(x[2 * k + 1], e2[0][k2 >> 1])), h2u(__hmul2(y[2 * k + 1], e2[1][k2 >> 1]))};
+            for (int nr = 0; nr < NR; ++nr) {
+              pb[u][nr][0] = transpose8(h2u(__floats2half2_rn(sc[u][nr][0], sc[u][nr][1])));
+              pb[u][nr][1] = transpose8(h2u(__floats2half2_rn(sc[u][nr][2], sc[u][nr][3])));
+            }
 #pragma unroll
-            for (int nr = 0; nr < NR; ++nr) mma_f16(sc[u][nr], a, qb[nr][2 * k2 + k][0], qb[nr][2 * k2 + k][1]);
+          for (int u = 0; u < kStep; ++u) {
+            // V: words of DV dims of the four keys, and the scale pair of each two keys (0 where
+            // the key is beyond the prefix: whatever its slot holds, it adds 0)
+            const unsigned char* st = ring + (i + u) % kStages * C::STAGE;
+            const int left = left0 - u * kGran;
+            uint32_t vw[4][DV / 8];
+            uint32_t ve[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int key = key_of(x >> 1, 2 * tq + (x & 1));
+              if (HD == 128) {
+                const uint2 y = *reinterpret_cast<const uint2*>(st + C::CODES + code_off<HD>(key, gq >> 1) + 8 * (gq & 1));
+                vw[x][0] = y.x, vw[x][DV / 8 - 1] = y.y;
+              } else {
+                vw[x][0] = *reinterpret_cast<const uint32_t*>(st + C::CODES + key * C::ROWB + 4 * gq);
+              }
+              ve[x] = st[2 * C::CODES + C::SCALES + key * C::SCB + (DV * gq) / 16];
+            }
+            if (left < kGran)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                if (key_of(x >> 1, 2 * tq + (x & 1)) >= left) ve[x] = 0u;
+            const __half2 e01 = cvt8(__byte_perm(ve[0], ve[1], 0x40)), e23 = cvt8(__byte_perm(ve[2], ve[3], 0x40));
+#pragma unroll
+            for (int x = 0; x < DV / 8; ++x) {
+              constexpr uint32_t kLo = 0x0F0F0F0Fu;
+              __half2 a0[4], a1[4], b0[4], b1[4];  // even and odd dims of the key pairs
+              cvt4((vw[0][x] & kLo) | ((vw[1][x] << 4) & ~kLo), a0);
+              cvt4(((vw[0][x] >> 4) & kLo) | (vw[1][x] & ~kLo), b0);
+              cvt4((vw[2][x] & kLo) | ((vw[3][x] << 4) & ~kLo), a1);
+              cvt4(((vw[2][x] >> 4) & kLo) | (vw[3][x] & ~kLo), b1);
+#pragma unroll
+              for (int d = 0; d < 4; ++d) {
+                const uint32_t a[4] = {h2u(__hmul2(a0[d], e01)), h2u(__hmul2(b0[d], e01)), h2u(__hmul2(a1[d], e23)),
+                                       h2u(__hmul2(b1[d], e23))};
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) mma_f16(o[nr][4 * x + d], a, pb[u][nr][0], pb[u][nr][1]);
+              }
+            }
           }
+          __syncwarp();  // the stages may be refilled
         }
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[u][nr][e] = sc[u][nr][e] * c2[nr][e & 1];
-        if (left < kGran) {
-#pragma unroll
-          for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (key_of(e >> 1, gq) >= left) sc[u][nr][e] = -INFINITY;
-        }
+
+        // this part's granules of 16 tree nodes, in bf16
       }
-      softmax(sc);
-      uint32_t pb[kStep][NR][2];
-#pragma unroll
-      for (int u = 0; u < kStep; ++u)
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr) {
-          pb[u][nr][0] = transpose8(h2u(__floats2half2_rn(sc[u][nr][0], sc[u][nr][1])));
-          pb[u][nr][1] = transpose8(h2u(__floats2half2_rn(sc[u][nr][2], sc[u][nr][3])));
-        }
-#pragma unroll
-      for (int u = 0; u < kStep; ++u) {
-        // V: words of DV dims of the four keys, and the scale pair of each two keys (0 where
-        // the key is beyond the prefix: whatever its slot holds, it adds 0)
-        const unsigned char* st = ring + (i + u) % kStages * C::STAGE;
-        const int left = left0 - u * kGran;
-        uint32_t vw[4][DV / 8];
-        uint32_t ve[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int key = key_of(x >> 1, 2 * tq + (x & 1));
-          if (HD == 128) {
-            const uint2 y = *reinterpret_cast<const uint2*>(st + C::CODES + code_off<HD>(key, gq >> 1) + 8 * (gq & 1));
-            vw[x][0] = y.x, vw[x][DV / 8 - 1] = y.y;
-          } else {
-            vw[x][0] = *reinterpret_cast<const uint32_t*>(st + C::CODES + key * C::ROWB + 4 * gq);
-          }
-          ve[x] = st[2 * C::CODES + C::SCALES + key * C::SCB + (DV * gq) / 16];
-        }
-        if (left < kGran)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (key_of(x >> 1, 2 * tq + (x & 1)) >= left) ve[x] = 0u;
-        const __half2 e01 = cvt8(__byte_perm(ve[0], ve[1], 0x40)), e23 = cvt8(__byte_perm(ve[2], ve[3], 0x40));
-#pragma unroll
-        for (int x = 0; x < DV / 8; ++x) {
-          constexpr uint32_t kLo = 0x0F0F0F0Fu;
-          __half2 a0[4], a1[4], b0[4], b1[4];  // even and odd dims of the key pairs
-          cvt4((vw[0][x] & kLo) | ((vw[1][x] << 4) & ~kLo), a0);
-          cvt4(((vw[0][x] >> 4) & kLo) | (vw[1][x] & ~kLo), b0);
-          cvt4((vw[2][x] & kLo) | ((vw[3][x] << 4) & ~kLo), a1);
-          cvt4(((vw[2][x] >> 4) & kLo) | (vw[3][x] & ~kLo), b1);
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const uint32_t a[4] = {h2u(__hmul2(a0[d], e01)), h2u(__hmul2(b0[d], e01)), h2u(__hmul2(a1[d], e23)),
-                                   h2u(__hmul2(b1[d], e23))};
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) mma_f16(o[nr][4 * x + d], a, pb[u][nr][0], pb[u][nr][1]);
-          }
-        }
-      }
-      __syncwarp();  // the stages may be refilled
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     // this part's record: o normalized by its own sum, the base and the sum
+    const float unit = (nodes_first ? ngran > 0 : x1 <= NG) ? kv.v_unit : 1.0f;  // o's
 #pragma unroll
     for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -547,7 +567,7 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
         if (rg * ROWS + rr < rows) {
           const size_t rec = (static_cast<size_t>(b) * Qn + pq + worker) * ROWS + rr;
           // (poison is the same in all threads of a row: one mask word and one badk per granule)
-          const float inv = poison[nr][e] ? __int_as_float(0x7FC00000) : s != 0.0f ? kv.v_unit / s : 0.0f;
+          const float inv = poison[nr][e] ? __int_as_float(0x7FC00000) : s != 0.0f ? unit / s : 0.0f;
           float* dst = ws_o + rec * HD + DV * gq;
 #pragma unroll
           for (int j = 0; j < MT; j += 2)

@@ -1,0 +1,88 @@
+"""The ends of the stated ranges of the verify pass over a 4-bit cache, against 64-bit forms.
+
+Tolerances of the attention, from the arithmetic (check_attn):
+  scores   fp32 sums of 128 products: 2^-18 of the largest sum |q||k| scale
+  weights  of prefix keys rounded to fp16, half a step 2^-11; of tree nodes to bf16, 2^-8;
+           each twice the score error on top
+  output   half a bf16 step of the value reached, 2^-8 of it
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv4_ref
+from eagle_speculative_decoding_round_gb300 import synth
+from gpu_util import host, to_dev
+from test_gpu_kv4 import attn_inputs, err_word, i32, mask_of
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from eagle_speculative_decoding_round_gb300 import eagle3 as e3
+
+
+def attn(d, scale):
+    B, R, H, KVH, hd = (d[k] for k in ("B", "R", "H", "KVH", "hd"))
+    q4 = [[to_dev(a) for a in w] for w in d["q4"]]
+    tail16 = [to_dev(t, torch.bfloat16) for t in d["tail"]]
+    pt, tpt, lens, mask, Q = i32(d["pt"]), i32(d["tpt"]), i32(d["lens"]), mask_of(d["see"]), to_dev(d["Q"], torch.bfloat16)
+    kv = e3.make_kv4_layer(q4[0][0], q4[1][0], q4[0][1], q4[1][1], pt, d["n"], d["page"], d["pt"].shape[1], KVH, hd, *d["units"])
+    tail = e3.make_kv_layer(*tail16, tpt, tail16[0].shape[0], d["tp"], d["tpt"].shape[1], KVH, hd, e3.E3_BF16)
+    need = e3.eagle3_verify4_workspace_bytes(B, R, H, KVH, hd, max(d["lens"]))
+    ws = torch.full((max(need, 16),), 255, dtype=torch.uint8, device="cuda")
+    O, lse, err = torch.full((B, R, H, hd), 55.0, dtype=torch.bfloat16, device="cuda"), torch.full((B, R, H), 55.0, device="cuda"), err_word()
+    e3.tree_verify_attn4(Q, kv, tail, lens, mask, B, R, H, max(d["lens"]), scale, O, lse, err, ws, need)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    return host(O).astype(np.float64), host(lse).astype(np.float64)
+
+
+def parts(d, b):
+    """K, V of request b's prefix and tail in 64 bits."""
+    t, j = np.arange(d["lens"][b]), np.arange(d["R"])
+    k, v = (kv4_ref.dequantize(d["q4"][w][0][d["pt"][b, t // d["page"]], :, t % d["page"]],
+                               d["q4"][w][1][d["pt"][b, t // d["page"]], :, t % d["page"]], d["units"][w]) for w in range(2))
+    tk, tv = (d["tail"][w][d["tpt"][b, j // d["tp"]], :, j % d["tp"]].astype(np.float64) for w in range(2))
+    return k, v, tk, tv
+
+
+def check_attn(d, O, lse, scale, skip=()):
+    for b in range(d["B"]):
+        k, v, tk, tv = parts(d, b)
+        Q, see, R = d["Q"][b].astype(np.float64), d["see"][b], d["R"]
+        o, l, _, big = kv4_ref.attend(Q, k, v, tk, tv, see, scale)
+        # sum p |v| over the prefix alone and over the nodes alone
+        _, _, mag_p, _ = kv4_ref.attend(Q, k, np.abs(v), tk, 0 * tv, see, scale)
+        _, _, mag_n, _ = kv4_ref.attend(Q, k, 0 * v, tk, np.abs(tv), see, scale)
+        ds = 2.0 ** -18 * (big + 1.0)
+        for i in range(R):
+            if (b, i) in skip:
+                continue
+            if not d["lens"][b] and not see[i].any():
+                assert np.all(O[b, i] == 0) and np.all(np.isneginf(lse[b, i])), (b, i)
+                continue
+            assert np.all(np.abs(lse[b, i] - l[i]) <= ds[i] + 2.0 ** -21 * np.abs(l[i])), (b, i, lse[b, i], l[i])
+            # an fp16 weight below 2^-14 is off by up to 2^-25 whatever its size: 2^-32 of the row's largest
+            G = d["H"] // d["KVH"]
+            tiny = 2.0 ** -32 * np.repeat(np.abs(v).sum(0), G, 0) if len(v) else 0.0
+            w = 2 * ds[i][:, None]
+            e = (2.0 ** -11 + w) * mag_p[i] + (2.0 ** -8 + w) * mag_n[i] + tiny
+            tol = e + 2.0 ** -8 * (np.abs(o[i]) + e) + 2.0 ** -126
+            bad = np.abs(O[b, i] - o[i]) - tol
+            assert np.all(bad <= 0), (b, i, bad.max(), np.abs(o[i]).max())
+
+
+SIDES = [(5, 4, 128), (40, 4, 128), (70, 4, 128), (5, 4, 64), (40, 4, 64)]  # R, query heads per KV head, head_dim
+
+
+@pytest.mark.parametrize("R,G,hd", SIDES)
+@pytest.mark.parametrize("v_unit,top", [(2.0 ** -60, 2.0 ** 97), (2.0 ** -30, 2.0 ** 92), (2.0 ** 60, 2.0 ** 97), (2.0 ** 60, 1.0), (2.0 ** -60, 1.0)])
+def test_large_nodes_beside_a_prefix_of_any_unit(R, G, hd, v_unit, top):
+    """Nodes' V up to 2^100 with the ends of v_unit: finite and right, also for rows that see the prefix alone."""
+    d = attn_inputs(R + G, 2, R, 2 * G, 2, hd, [150, 0], 16, units=(1.0, v_unit))
+    d["tail"][1] = synth.to_bf16_f32(d["tail"][1] * np.float32(top))  # |N(0, 1)| < 2^3
+    d["see"][:, R - 2] = False
+    scale = 1 / math.sqrt(hd)
+    check_attn(d, *attn(d, scale), scale)
