@@ -431,8 +431,10 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
 #pragma unroll
           for (int e = 0; e < 2; ++e) {  // row 2 tq + e is held by lanes 4 (2 tq + e) ..
             const int er = __shfl_sync(0xFFFFFFFFu, ex, 4 * (2 * tq + e));
-            c2[nr][e] = sm_scale * kLog2e * kv.k_unit * __uint_as_float(static_cast<uint32_t>(127 + er / 2) << 23) *
-                        __uint_as_float(static_cast<uint32_t>(127 + (er - er / 2)) << 23);
+            // (held below Inf, which would make NaN of a score of 0)
+            c2[nr][e] = fminf(sm_scale * kLog2e * kv.k_unit * __uint_as_float(static_cast<uint32_t>(127 + er / 2) << 23) *
+                                  __uint_as_float(static_cast<uint32_t>(127 + (er - er / 2)) << 23),
+                              3e38f);
           }
         }
 

@@ -636,7 +636,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         // while the other is a part behind)
         if (RT == 1 && grp == 1 && !warp_wait(&q_full[0], n_part & 1, abort)) live = false;
         const int q_ex = ex_rows[lane];
-        const float c2 = q_ex == 128 ? __int_as_float(0x7FC00000) : fmaxf(sm_scale * kLog2e * pow2f(q_ex), 1e-37f);
+        const float c2 = q_ex == 128 ? __int_as_float(0x7FC00000) : sm_scale * kLog2e * pow2f(q_ex);
         float m = -INFINITY, l = 0.0f;
         int ue = vu_exp, mine = 0;  // exponent of O's unit; this group's tiles of the part
         const int tail0 = ntail;
@@ -659,7 +659,8 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           // O's unit: the cache's under the prefix; the nodes' weights carry 2^-kNodeExp, so that
           // products with any finite V stay finite
           const int tile_ue = nodes ? kNodeExp : vu_exp;
-          const float c = nodes ? c2 : c2 * kv.k_unit;
+          // (a factor of 0 or Inf would make NaN of an unseen key's -Inf or of a score of 0)
+          const float c = q_ex == 128 ? c2 : fminf(fmaxf(nodes ? c2 : c2 * kv.k_unit, 1e-37f), 3e38f);
           if (!warp_wait(&s_full[grp], n_tile & 1, abort)) {
             live = false;
             break;

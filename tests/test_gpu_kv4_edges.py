@@ -86,3 +86,20 @@ def test_large_nodes_beside_a_prefix_of_any_unit(R, G, hd, v_unit, top):
     d["see"][:, R - 2] = False
     scale = 1 / math.sqrt(hd)
     check_attn(d, *attn(d, scale), scale)
+
+
+@pytest.mark.parametrize("R,G,hd", SIDES)
+def test_score_factors_that_leave_the_range(R, G, hd):
+    """The smallest k_unit with a small scale, rows of zeros among them: every score is nothing, the keys weigh alike."""
+    d = attn_inputs(R + G + 1, 2, R, 2 * G, 2, hd, [150, 3], 16, units=(2.0 ** -60, 1.0))
+    d["Q"][:, ::3] = 0.0
+    check_attn(d, *attn(d, 1e-9), 1e-9)
+
+
+@pytest.mark.parametrize("R,G,hd", SIDES)
+def test_score_factors_beyond_the_range(R, G, hd):
+    """The largest k_unit with a scale of 1e29 and keys of zeros: every score is 0."""
+    d = attn_inputs(R + G + 5, 2, R, 2 * G, 2, hd, [150, 3], 16, units=(2.0 ** 60, 1.0))
+    d["q4"][0][0][:] = 0
+    d["tail"][0][:] = 0.0
+    check_attn(d, *attn(d, 1e29), 1e29)
