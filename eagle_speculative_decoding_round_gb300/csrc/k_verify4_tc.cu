@@ -623,11 +623,10 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           if (RT == 1 && n_part > 0 && !warp_wait(q_free, (n_part - 1) & 1, abort)) live = false;
           unsigned char* slab = sQ + (RT == 2 ? grp : 0) * kOpB + quarter * 32 * 128;
           bring_rows(Q + static_cast<size_t>(p.b) * g.R * g.H * kHD, row_ok ? node * g.H + head : -1, slab, lane);
-          // (a row with a NaN or an Inf: a NaN factor.  Below 2^-64 a row's scores are as good
-          // as zero, and their factor would underflow)
+          // (a row with a NaN or an Inf: a NaN factor)
           const uint32_t top = row_top(slab, lane);
           const int ex = row_to_half(slab, lane, top);
-          ex_rows[lane] = top >= 0x7F80u ? 128 : max(ex, -64);
+          ex_rows[lane] = top >= 0x7F80u ? 128 : ex;
           fence_async_smem();
           __syncwarp();
           if (lane == 0) bar_arrive(&q_full[grp]);
@@ -636,7 +635,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         // while the other is a part behind)
         if (RT == 1 && grp == 1 && !warp_wait(&q_full[0], n_part & 1, abort)) live = false;
         const int q_ex = ex_rows[lane];
-        const float c2 = q_ex == 128 ? __int_as_float(0x7FC00000) : sm_scale * kLog2e * pow2f(q_ex);
+        const float q_pow = q_ex == 128 ? __int_as_float(0x7FC00000) : pow2f(q_ex);
         float m = -INFINITY, l = 0.0f;
         int ue = vu_exp, mine = 0;  // exponent of O's unit; this group's tiles of the part
         const int tail0 = ntail;
@@ -660,7 +659,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           // products with any finite V stay finite
           const int tile_ue = nodes ? kNodeExp : vu_exp;
           // (a factor of 0 or Inf would make NaN of an unseen key's -Inf or of a score of 0)
-          const float c = q_ex == 128 ? c2 : fminf(fmaxf(nodes ? c2 : c2 * kv.k_unit, 1e-37f), 3e38f);
+          const float c = q_ex == 128 ? q_pow : fminf(fmaxf(sm_scale * kLog2e * (nodes ? 1.0f : kv.k_unit) * q_pow, 1e-37f), 3e38f);
           if (!warp_wait(&s_full[grp], n_tile & 1, abort)) {
             live = false;
             break;

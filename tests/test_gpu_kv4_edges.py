@@ -103,3 +103,15 @@ def test_score_factors_beyond_the_range(R, G, hd):
     d["q4"][0][0][:] = 0
     d["tail"][0][:] = 0.0
     check_attn(d, *attn(d, 1e29), 1e29)
+
+
+@pytest.mark.parametrize("R,G,hd", SIDES)
+@pytest.mark.parametrize("nodes", [2.0 ** 60, 1.0])
+def test_small_queries_against_large_keys(R, G, hd, nodes):
+    """Rows of Q from 2^-72 to 2^-62 against keys of 2^60: scores of ordinary size."""
+    d = attn_inputs(R + G + 2, 2, R, 2 * G, 2, hd, [150, 20], 16, units=(2.0 ** 60, 1.0))
+    at = np.random.default_rng(R).integers(-72, -61, d["Q"].shape[:3])
+    d["Q"] = synth.to_bf16_f32(d["Q"] * np.exp2(at)[..., None].astype(np.float32))
+    d["Q"][0, 0] = 0.0
+    d["tail"][0] = synth.to_bf16_f32(d["tail"][0] * np.float32(nodes))
+    check_attn(d, *attn(d, 1.0), 1.0)
