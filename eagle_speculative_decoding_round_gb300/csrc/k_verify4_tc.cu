@@ -287,11 +287,10 @@ __device__ __forceinline__ void row_clear(unsigned char* slab, int rr) {
 #pragma unroll 1
   for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(row_chunk(slab, rr, c)) = make_uint4(0u, 0u, 0u, 0u);
 }
-// Row `rr` from bf16 to fp16 in place, its largest magnitude `top` scaled by a power of two,
-// whose exponent is returned, to [1, 2) ([2, 4) from 2^127 on), which keeps its bits down
-// to 2^-24 of it.  A row with a NaN or an Inf becomes zeros.
+// Row `rr` from bf16 to fp16 in place, its largest magnitude `top` scaled to [1, 4) by a power
+// of two, whose even exponent is returned, which keeps its bits down to 2^-24 of it.  A row with a NaN or an Inf becomes zeros.
 __device__ __forceinline__ int row_to_half(unsigned char* slab, int rr, uint32_t top) {
-  const int ex = min(max(static_cast<int>(top >> 7), 1) - 127, 126);
+  const int ex = (min(static_cast<int>(max(top >> 7, 1u)), 254) - 127) & ~1;
   const float f = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
 #pragma unroll 8
   for (int c = 0; c < 16; ++c) {
@@ -318,7 +317,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   unsigned char *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V, *sRaw = sm + C::RAW;
-  float* s_fac = reinterpret_cast<float*>(sm + C::FAC);  // [kTailRing][128] factor of each tree node's scores
+  float* s_fac = reinterpret_cast<float*>(sm + C::FAC);  // [kTailRing][128] root of the factor of each tree node's scores
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BARS);
   uint64_t* raw_full = bars;        // [K, V][3]
   uint64_t* raw_empty = bars + 6;   // [K, V][3]
@@ -576,7 +575,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           const uint32_t top = row_top(slab, lane);
           if (op == 0) {
             const int ex = row_to_half(slab, lane, top);
-            s_fac[slot * kKeys + dw * 32 + lane] = top >= 0x7F80u ? __int_as_float(0x7FC00000) : pow2f(ex);
+            s_fac[slot * kKeys + dw * 32 + lane] = top >= 0x7F80u ? __int_as_float(0x7FC00000) : pow2f(ex / 2);
           } else {
             const uint32_t bad = __ballot_sync(0xFFFFFFFFu, top >= 0x7F80u);
             if (lane == 0) s_bad[slot * 4 + dw] = bad;
@@ -635,7 +634,12 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
         // while the other is a part behind)
         if (RT == 1 && grp == 1 && !warp_wait(&q_full[0], n_part & 1, abort)) live = false;
         const int q_ex = ex_rows[lane];
+        // Factors of the scores.  The prefix's is held within the range: 0 or Inf would make NaN
+        // of an unseen key's -Inf or of a score of 0.  The nodes' meets a score between the two
+        // halves of the node's own, so that neither power alone carries it past the range.
         const float q_pow = q_ex == 128 ? __int_as_float(0x7FC00000) : pow2f(q_ex);
+        const float c_prefix = q_ex == 128 ? q_pow : fminf(fmaxf(sm_scale * kLog2e * kv.k_unit * q_pow, 1e-37f), 3e38f);
+        const float c_nodes = q_ex == 128 ? q_pow : fminf(sm_scale * kLog2e * q_pow, 3e38f);
         float m = -INFINITY, l = 0.0f;
         int ue = vu_exp, mine = 0;  // exponent of O's unit; this group's tiles of the part
         const int tail0 = ntail;
@@ -658,28 +662,34 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           // O's unit: the cache's under the prefix; the nodes' weights carry 2^-kNodeExp, so that
           // products with any finite V stay finite
           const int tile_ue = nodes ? kNodeExp : vu_exp;
-          // (a factor of 0 or Inf would make NaN of an unseen key's -Inf or of a score of 0)
-          const float c = q_ex == 128 ? q_pow : fminf(fmaxf(sm_scale * kLog2e * (nodes ? 1.0f : kv.k_unit) * q_pow, 1e-37f), 3e38f);
+          const float c = nodes ? 1.0f : c_prefix;
           if (!warp_wait(&s_full[grp], n_tile & 1, abort)) {
             live = false;
             break;
           }
           fence_after();
           if (!all) {  // the nodes' factors, and -Inf where unseen (whose exponential is 0)
+            const float2 cn = make_float2(c_nodes, c_nodes);
 #pragma unroll 1
             for (int d = 0; d < 4 * halves; ++d) {
               uint32_t y[16];
               tmem_ld16(tS + 16 * d, y);
               const uint32_t sb = static_cast<uint32_t>((d < 4 ? see[0] : see[1]) >> (16 * (d & 3)));
-              const float4* fac = reinterpret_cast<const float4*>(s_fac + slot * kKeys + 16 * d);
+              if (nodes) {
+                const float4* fac = reinterpret_cast<const float4*>(s_fac + slot * kKeys + 16 * d);
+                auto scaled = [&](uint32_t* s, float2 f) {
+                  const float2 v = __fmul2_rn(__fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(s[0]), __uint_as_float(s[1])), f), cn), f);
+                  s[0] = __float_as_uint(v.x), s[1] = __float_as_uint(v.y);
+                };
 #pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                const float4 f = nodes ? fac[j / 4] : make_float4(1.f, 1.f, 1.f, 1.f);
-                y[j] = sb & (1u << j) ? __float_as_uint(__uint_as_float(y[j]) * f.x) : 0xFF800000u;
-                y[j + 1] = sb & (2u << j) ? __float_as_uint(__uint_as_float(y[j + 1]) * f.y) : 0xFF800000u;
-                y[j + 2] = sb & (4u << j) ? __float_as_uint(__uint_as_float(y[j + 2]) * f.z) : 0xFF800000u;
-                y[j + 3] = sb & (8u << j) ? __float_as_uint(__uint_as_float(y[j + 3]) * f.w) : 0xFF800000u;
+                for (int j = 0; j < 16; j += 4) {
+                  const float4 f = fac[j / 4];
+                  scaled(y + j, make_float2(f.x, f.y));
+                  scaled(y + j + 2, make_float2(f.z, f.w));
+                }
               }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) y[j] = sb & (1u << j) ? y[j] : 0xFF800000u;
               tmem_st16(tS + 16 * d, y);
             }
             tmem_st_wait();

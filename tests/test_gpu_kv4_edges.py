@@ -115,3 +115,29 @@ def test_small_queries_against_large_keys(R, G, hd, nodes):
     d["Q"][0, 0] = 0.0
     d["tail"][0] = synth.to_bf16_f32(d["tail"][0] * np.float32(nodes))
     check_attn(d, *attn(d, 1.0), 1.0)
+
+
+@pytest.mark.parametrize("R,G,hd", SIDES)
+def test_the_largest_nodes_against_the_smallest_queries(R, G, hd):
+    """Nodes' K up to 2^127 with Q of 2^-121: scores of ordinary size.  (Values of Q below 2^-125 are left out.)"""
+    d = attn_inputs(R + G + 3, 2, R, 2 * G, 2, hd, [0, 20], 16)
+    q = d["Q"] * np.float32(2.0 ** -121)
+    d["Q"] = synth.to_bf16_f32(np.where(np.abs(q) < 2.0 ** -125, 0.0, q).astype(np.float32))
+    d["tail"][0] = synth.to_bf16_f32(d["tail"][0] * np.float32(2.0 ** 124))
+    check_attn(d, *attn(d, 0.1), 0.1)
+
+
+@pytest.mark.parametrize("R,G,hd", SIDES)
+def test_a_bad_query_row_that_sees_nothing(R, G, hd):
+    """NaN or Inf in a row of Q: 0 and -Inf where it sees no key, NaN where it sees one; other rows are not touched."""
+    d = attn_inputs(R + G + 4, 2, R, 2 * G, 2, hd, [0, 20], 16)
+    d["see"][0, 1:3] = False
+    good = d["Q"].copy()
+    bad = [(0, 1), (0, 2), (0, 3), (1, 4)]
+    d["Q"][0, 1], d["Q"][0, 2, :, 7], d["Q"][0, 3, :, 5], d["Q"][1, 4, :, 3] = np.nan, np.inf, np.nan, np.nan
+    O, lse = attn(d, 0.1)
+    assert np.all(O[0, 1:3] == 0) and np.all(np.isneginf(lse[0, 1:3]))
+    for b, i in bad[2:]:
+        assert np.all(np.isnan(O[b, i])) and np.all(np.isnan(lse[b, i]))
+    d["Q"] = good
+    check_attn(d, O, lse, 0.1, skip=bad)
