@@ -360,14 +360,16 @@ logits_process_kernel(LogitsArgs a) {
         if (32 * w < v0 + nv) s_ok[w - w0] = next_ok[k];
       }
     }
+    bool deep = false;  // (thread 0) the row's path has more than E3_MAX_DEPTH nodes
     if (tid == 0) {
-      int n = 0, u = a.tok ? i : 0;
-      while (u > 0 && u < a.R && n < E3_MAX_DEPTH) {
+      int n = 0, u = a.tok ? i : 0, depth = 0;
+      for (; u > 0 && u < a.R && depth < E3_MAX_DEPTH; ++depth) {
         const int t = s_tok[u] - v0;
         if (s_tok[u] >= 0 && t >= 0 && t < nv) s_path[n++] = t;
         u = s_par[u] < u ? s_par[u] : -1;  // parents come first
       }
       s_npath = n;
+      deep = u > 0;
       s_first = 0x7FFFFFFF;
       if (CL > 1) {
         expect_bytes(&xbar[par], 4u * CL);
@@ -430,7 +432,7 @@ logits_process_kernel(LogitsArgs a) {
     }
     __syncthreads();
     // grammar and maximum
-    float best = -INFINITY;
+    float best = deep ? __int_as_float(0x7FC00000) : -INFINITY;  // (too deep a path: a bad row)
 #pragma unroll 4
     for (int k = tid; 4 * k < nv; k += kThreads) {
       float4 x = reinterpret_cast<float4*>(zs)[k];
@@ -511,7 +513,7 @@ logits_process_kernel(LogitsArgs a) {
       }
       Q = sum.total();
     } else if (rank == 0 && tid == 0) {
-      dev_flag(a.dev_err, bad ? E3_DEV_ERR_NONFINITE : E3_DEV_ERR_MASKED);
+      dev_flag(a.dev_err, deep ? E3_DEV_ERR_CAPACITY : bad ? E3_DEV_ERR_NONFINITE : E3_DEV_ERR_MASKED);
     }
     Q = warp_reduce(static_cast<uint64_t>(Q), SumU64());
     if (lane == 0) s_sum[warp] = Q;
@@ -550,6 +552,7 @@ logits_process_kernel(LogitsArgs a) {
 __global__ void __launch_bounds__(kThreads)
 logits_process_wide_kernel(LogitsArgs a) {
   __shared__ int s_path[E3_MAX_DEPTH], s_npath;
+  __shared__ bool s_deep;
   __shared__ int btok[kMaxBias];
   __shared__ float bval[kMaxBias];
   __shared__ uint64_t red64[32];
@@ -565,6 +568,7 @@ logits_process_wide_kernel(LogitsArgs a) {
       u = p < u ? p : -1;
     }
     s_npath = n;
+    s_deep = u > 0;
   }
   for (int k = threadIdx.x; k < a.n_bias; k += kThreads) {
     btok[k] = a.bias_tok[static_cast<size_t>(b) * a.n_bias + k];
@@ -605,9 +609,9 @@ logits_process_wide_kernel(LogitsArgs a) {
   }
   bad = block_reduce(bad, OrI(), redi);
   best = block_reduce(best, MaxU64(), red64);
-  if (bad || best == 0ull) {
+  if (bad || best == 0ull || s_deep) {
     if (threadIdx.x == 0) {
-      dev_flag(a.dev_err, bad ? E3_DEV_ERR_NONFINITE : E3_DEV_ERR_MASKED);
+      dev_flag(a.dev_err, s_deep ? E3_DEV_ERR_CAPACITY : bad ? E3_DEV_ERR_NONFINITE : E3_DEV_ERR_MASKED);
       a.row_max[row] = __int_as_float(0x7FC00000);
       a.row_Q[row] = 0ull;
       a.row_argmax[row] = -1;

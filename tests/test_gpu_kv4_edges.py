@@ -13,9 +13,10 @@ import pytest
 import torch
 
 import kv4_ref
+import oracle
 from eagle_speculative_decoding_round_gb300 import synth
 from gpu_util import host, to_dev
-from test_gpu_kv4 import attn_inputs, err_word, i32, mask_of
+from test_gpu_kv4 import attn_inputs, err_word, i32, mask_of, ruled_out
 
 pytestmark = pytest.mark.gpu
 
@@ -141,3 +142,43 @@ def test_a_bad_query_row_that_sees_nothing(R, G, hd):
         assert np.all(np.isnan(O[b, i])) and np.all(np.isnan(lse[b, i]))
     d["Q"] = good
     check_attn(d, O, lse, 0.1, skip=bad)
+
+
+def logits_call(z, V, temp, counts=None, tok=None, par=None, pen=None, bias=None, allow=None, arow=None, B=1):
+    """(out, row_max, row_Q, row_argmax, error word) of tree_logits_process on host arrays, as host arrays."""
+    rows = len(z)
+    dev = lambda a, v=None: None if a is None else to_dev(a if v is None else a.view(v))  # noqa: E731
+    dz = to_dev(z)
+    out, mx = torch.full((rows, V), 9.0, device="cuda"), torch.zeros(rows, device="cuda")
+    Q, am = torch.ones(rows, dtype=torch.int64, device="cuda"), torch.zeros(rows, dtype=torch.int32, device="cuda")
+    err = err_word()
+    bt, bv = bias if bias is not None else (None, None)
+    keep = [dev(temp), dev(counts, np.int16), dev(tok), dev(par), dev(pen), dev(bt), dev(bv), dev(allow, np.int32), dev(arow)]
+    e3.tree_logits_process(dz, B, rows // B, V, *keep[:5], keep[5], keep[6], 0 if bt is None else bt.shape[1], keep[7], keep[8],
+                           0 if allow is None else len(allow), out, mx, Q, am, err)
+    torch.cuda.synchronize()
+    return host(out), host(mx), host(Q).view(np.uint64), host(am), int(err.item())
+
+
+def check_row(want, temp, mx, Q, am, row):
+    """Statistics of the processed row `want` against the oracle."""
+    ref = oracle.row_stats(ruled_out(want)[None], np.float32([temp]))
+    assert mx == ref[0][0] and am == int(ref[2][0]) and int(Q) == int(ref[1][0]), row
+
+
+@pytest.mark.parametrize("V", [500, 40000, 262148])
+def test_paths_beyond_the_depth_limit_are_flagged(V):
+    """A chain of nodes: rows whose path has at most 16 beside the root are exact, deeper ones carry the statistics of a bad row."""
+    R = 20
+    rng = np.random.default_rng(V)
+    z = rng.normal(size=(R, V)).astype(np.float32)
+    par = np.arange(-1, R - 1, dtype=np.int32)[None]
+    tok = rng.integers(0, V, (1, R)).astype(np.int32)
+    pen = np.float32([[1.3, 0.2, 0.1]])
+    out, mx, Q, am, err = logits_call(z, V, np.ones(R, np.float32), None, tok, par, pen)
+    for i in range(17):
+        want = kv4_ref.process(z[i], None, [int(t) for t in tok[0, 1:i + 1]], pen[0], [], [], None)
+        assert np.array_equal(out[i], want)
+        check_row(want, 1.0, mx[i], Q[i], am[i], i)
+    assert err == e3.E3_DEV_ERR_CAPACITY
+    assert np.isnan(mx[17:]).all() and not Q[17:].any() and np.all(am[17:] == -1)
