@@ -609,6 +609,8 @@ logits_process_wide_kernel(LogitsArgs a) {
   }
   bad = block_reduce(bad, OrI(), redi);
   best = block_reduce(best, MaxU64(), red64);
+  // (a maximum that the temperature carries to -Inf is past the range, too)
+  bad |= best != 0ull && unord_f32(static_cast<uint32_t>(best >> 32)) == -INFINITY;
   if (bad || best == 0ull || s_deep) {
     if (threadIdx.x == 0) {
       dev_flag(a.dev_err, s_deep ? E3_DEV_ERR_CAPACITY : bad ? E3_DEV_ERR_NONFINITE : E3_DEV_ERR_MASKED);

@@ -549,11 +549,11 @@ E3_API size_t eagle3_verify4_workspace_bytes(int B, int R, int n_q_heads, int n_
  *   z = -Inf where the grammar does not allow v.
  * out[row][v] = z, and with T = temp_per_row[row] (as lmhead_logits) s = z * (1/T):
  *   row_max, row_argmax (lowest id on ties), row_Q = sum floor(2^40 E(s - row_max)).
- * A -Inf logit means a token that is ruled out.  NaN or +Inf in a z sets
- * E3_DEV_ERR_NONFINITE, a row that is -Inf throughout E3_DEV_ERR_MASKED, a row whose path
- * has more than E3_MAX_DEPTH nodes beside the root E3_DEV_ERR_CAPACITY (only the deepest
- * E3_MAX_DEPTH count); each gives row_max = NaN, row_Q = 0, row_argmax = -1, which
- * spec_accept reports in status.
+ * A -Inf logit means a token that is ruled out.  NaN or +Inf in a z, or a row maximum
+ * that 1/T carries past the range, sets E3_DEV_ERR_NONFINITE, a row that is -Inf
+ * throughout E3_DEV_ERR_MASKED, a row whose path has more than E3_MAX_DEPTH nodes beside
+ * the root E3_DEV_ERR_CAPACITY (only the deepest E3_MAX_DEPTH count); each gives
+ * row_max = NaN, row_Q = 0, row_argmax = -1, which spec_accept reports in status.
  * counts [B][V] uint16, kept by token_counts_add (NULL: no token seen).  tok, parent:
  * [B][R] from tree_build_mask (NULL both: no paths, R independent rows); tokens
  * outside [0, V) are skipped.  pen: [B][3] fp32 {rep > 0, freq, pres} (NULL: 1, 0, 0).

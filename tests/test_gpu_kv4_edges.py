@@ -182,3 +182,16 @@ def test_paths_beyond_the_depth_limit_are_flagged(V):
         check_row(want, 1.0, mx[i], Q[i], am[i], i)
     assert err == e3.E3_DEV_ERR_CAPACITY
     assert np.isnan(mx[17:]).all() and not Q[17:].any() and np.all(am[17:] == -1)
+
+
+@pytest.mark.parametrize("V", [1000, 40000, 262148])
+def test_rows_that_a_small_temperature_carries_past_the_range(V):
+    """Finite logits whose quotient by the temperature overflows, either way: flagged, whichever kernel runs."""
+    z = np.full((3, V), -1000.0, np.float32)
+    z[1, 5] = 1000.0
+    z[2] = -np.float32(1.5)
+    out, mx, Q, am, err = logits_call(z, V, np.float32([1e-37, 1e-37, 0.5]))
+    assert np.array_equal(out, z)
+    assert err == e3.E3_DEV_ERR_NONFINITE
+    assert np.isnan(mx[:2]).all() and not Q[:2].any() and np.all(am[:2] == -1)
+    check_row(z[2], 0.5, mx[2], Q[2], am[2], 2)
