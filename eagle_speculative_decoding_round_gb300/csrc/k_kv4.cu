@@ -37,9 +37,9 @@ __device__ __forceinline__ long long slot_row(const int32_t* table, int max_page
 }
 
 // Rows request b appends, or -1 if they do not fit.
-__device__ __forceinline__ int append_count(int n, int max_rows, long long P, long long cap) {
+__device__ __forceinline__ int append_count(long long n, int max_rows, long long P, long long cap) {
   if (n <= 0) return 0;
-  return (n > max_rows || P < 0 || P + n > cap || P + n > 0x7FFFFFFFll) ? -1 : n;
+  return (n > max_rows || P < 0 || P + n > cap || P + n > 0x7FFFFFFFll) ? -1 : static_cast<int>(n);
 }
 
 // One group of 16 bf16 values -> 8 bytes of codes, the scale byte.  `unit` is a power
@@ -124,7 +124,7 @@ kv4_append_kernel(const __grid_constant__ Kv4Layers L4, e3_kv4_layer geo, const 
   pdl_trigger();
   const int b = blockIdx.z;
   const long long P = kv_len[b];
-  const int n = append_count(n_rows[b] + n_add, max_rows, P, static_cast<long long>(geo.max_pages) * geo.page_size);
+  const int n = append_count(static_cast<long long>(n_rows[b]) + n_add, max_rows, P, static_cast<long long>(geo.max_pages) * geo.page_size);
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) {
     if (n < 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
     if (kv_len_next) kv_len_next[b] = static_cast<int32_t>(P + max(n, 0));
@@ -176,7 +176,7 @@ __global__ void kv4_len_kernel(int B, int max_rows, const int32_t* __restrict__ 
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b < B) kv_len[b] += max(append_count(n_rows[b] + n_add, max_rows, kv_len[b], cap), 0);
+  if (b < B) kv_len[b] += max(append_count(static_cast<long long>(n_rows[b]) + n_add, max_rows, kv_len[b], cap), 0);
 }
 
 __device__ __forceinline__ void dequantize16(uint2 c, uint8_t e, float unit, uint4* out) {

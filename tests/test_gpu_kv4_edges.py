@@ -195,3 +195,20 @@ def test_rows_that_a_small_temperature_carries_past_the_range(V):
     assert err == e3.E3_DEV_ERR_NONFINITE
     assert np.isnan(mx[:2]).all() and not Q[:2].any() and np.all(am[:2] == -1)
     check_row(z[2], 0.5, mx[2], Q[2], am[2], 2)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_of_the_largest_row_count(in_place):
+    """n_rows + n_add past 31 bits is more rows than there are: flagged, the request as it was."""
+    KVH, hd, page = 1, 64, 16
+    src = torch.ones((2, KVH, page, hd), dtype=torch.bfloat16, device="cuda")
+    bufs = [torch.zeros((2, KVH, page, w), dtype=torch.uint8, device="cuda") for w in (hd // 2, hd // 2, hd // 16, hd // 16)]
+    pt = i32([[0], [1]])
+    l4 = e3.make_kv4_layer(*bufs, pt, 2, page, 1, KVH, hd)
+    l16 = e3.make_kv_layer(src, src, pt, 2, page, 1, KVH, hd, e3.E3_BF16)
+    lens, n, err = i32([3, 2]), i32([2 ** 31 - 1, 3]), err_word()
+    nxt = lens if in_place else torch.zeros_like(lens)
+    e3.kv4_append([l4], [l16], 2, 4, None, n, 1, lens, nxt, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == e3.E3_DEV_ERR_CAPACITY
+    assert host(nxt).tolist() == [3, 6] and not host(bufs[0])[0].any() and host(bufs[0])[1].any()
