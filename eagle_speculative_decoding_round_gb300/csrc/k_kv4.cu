@@ -210,15 +210,16 @@ kv4_read_kernel(const __grid_constant__ Kv4Layers L4, e3_kv4_layer geo, const __
   pdl_trigger();
   const int b = blockIdx.z;
   const int n = n_rows[b];
-  if (n > max_rows) {
+  const long long from = first ? first[b] : 0;
+  if (n > 0 && (n > max_rows || from < 0 || from + n > static_cast<long long>(geo.max_pages) * geo.page_size)) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
     return;
   }
   const RowItem it = row_item(geo, max_rows);
   if (it.kvh >= geo.n_kv_heads || it.j >= n) return;
-  const long long t = (first ? static_cast<long long>(first[b]) : 0ll) + it.j;
+  const long long t = from + it.j;
   const long long sr = slot_row(geo.page_table, geo.max_pages, geo.n_pages, geo.page_size, geo.n_kv_heads, b,
-                                t < 0 || t > 0x7FFFFFFF ? -1 : static_cast<int>(t));
+                                t > 0x7FFFFFFF ? -1 : static_cast<int>(t));
   const long long dr = slot_row(dgeo.page_table, dgeo.max_pages, dgeo.n_pages, dgeo.page_size, dgeo.n_kv_heads, b, it.j);
   if (sr < 0 || dr < 0) {
     dev_flag(dev_err, E3_DEV_ERR_CAPACITY);

@@ -498,7 +498,10 @@ E3_API e3_status kv4_append(const e3_kv4_layer* layers, const e3_kv_layer* src, 
  * kv4_read: rows of the 4-bit cache back to bf16 values (handing a request to a
  * bf16 cache): logical slots first[b] + j, j < n_rows[b] <= max_rows, of every layer
  * go to logical slots j of dst.  Exact (see e3_kv4_layer) where the value is a normal
- * bf16 number.  first NULL: from slot 0.  Errors as kv4_append.
+ * bf16 number.  first NULL: from slot 0.  n > max_rows, or rows outside the 4-bit cache's
+ * pages, set E3_DEV_ERR_CAPACITY and leave the request's part of dst as it was; a page id
+ * out of range (either side), or a row that dst's pages do not hold, sets it and skips
+ * that row.
  * ------------------------------------------------------------------------- */
 E3_API e3_status kv4_read(const e3_kv4_layer* layers, const e3_kv_layer* dst, int L, int B, int max_rows,
                           const int32_t* first, const int32_t* n_rows, int32_t* dev_err, e3_stream_t stream);

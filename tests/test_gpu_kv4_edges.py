@@ -212,3 +212,22 @@ def test_append_of_the_largest_row_count(in_place):
     torch.cuda.synchronize()
     assert int(err.item()) == e3.E3_DEV_ERR_CAPACITY
     assert host(nxt).tolist() == [3, 6] and not host(bufs[0])[0].any() and host(bufs[0])[1].any()
+
+
+@pytest.mark.parametrize("first,n", [(30, 3), (-1, 2), (2 ** 31 - 2, 4), (0, 33)])
+def test_read_beyond_the_pages_leaves_the_request(first, n):
+    """Rows that the 4-bit cache's pages do not hold: flagged, nothing of the request is written; the other request is."""
+    KVH, hd, page = 1, 64, 16
+    bufs = [torch.full((4, KVH, page, w), 0x38 if w == hd // 16 else 0x22, dtype=torch.uint8, device="cuda")
+            for w in (hd // 2, hd // 2, hd // 16, hd // 16)]
+    l4 = e3.make_kv4_layer(*bufs, i32([[0, 1], [2, 3]]), 4, page, 2, KVH, hd)
+    table = [i32([[0, 1], [2, 3]]), i32([[0, 1, 2], [3, 4, 5]])]
+    l4.page_table = table[0].data_ptr()
+    back = [torch.full((6, KVH, page, hd), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    l16 = e3.make_kv_layer(*back, table[1], 6, page, 3, KVH, hd, e3.E3_BF16)
+    starts, count, err = i32([first, 31]), i32([n, 1]), err_word()
+    e3.kv4_read([l4], [l16], 2, 40, starts, count, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == e3.E3_DEV_ERR_CAPACITY
+    for t in back:
+        assert torch.all(t[:3] == 9.0) and torch.all(t[3, 0, 0] == 1.0) and torch.all(t[3, 0, 1:] == 9.0) and torch.all(t[4:] == 9.0)
