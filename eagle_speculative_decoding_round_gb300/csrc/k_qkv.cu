@@ -37,13 +37,18 @@ struct QkvArgs {
 };
 
 // cos and sin of pair i at position pos.  The phase in units of 2^-64 turns is exact
-// modulo a turn; its top 32 bits, signed, are half-turns in [-1, 1) to 2^-31.
+// modulo a turn.  Its nearest quarter turn comes off as an integer, so that the float holds
+// 24 bits of what is left, in half-turns of [-1/4, 1/4], and a cosine or a sine close to 0
+// keeps its relative accuracy (24 bits of the whole phase left 2^-25 half-turns of error).
 __device__ __forceinline__ float2 rope_cs(const e3_rope& r, int i, int pos) {
   const uint64_t ph = r.turns[i] * static_cast<uint64_t>(static_cast<int64_t>(pos));
-  const float x = static_cast<float>(static_cast<int32_t>(ph >> 32)) * 0x1p-31f;
+  const uint32_t quarter = static_cast<uint32_t>((ph + (1ull << 61)) >> 62);
+  const float x = __ll2float_rn(static_cast<long long>(ph - (static_cast<uint64_t>(quarter) << 62))) * 0x1p-63f;
   float s, c;
   sincospif(x, &s, &c);
-  return make_float2(c * r.amp, s * r.amp);
+  const float a = (quarter & 1u) ? s : c, b = (quarter & 1u) ? c : s;  // cos and sin but for the signs
+  return make_float2(__uint_as_float(__float_as_uint(a * r.amp) ^ (((quarter + 1u) & 2u) << 30)),
+                     __uint_as_float(__float_as_uint(b * r.amp) ^ ((quarter & 2u) << 30)));
 }
 
 // Row of the cache (in heads x slots units of head_dim values, for KV head 0) of row r,

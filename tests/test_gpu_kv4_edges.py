@@ -231,3 +231,33 @@ def test_read_beyond_the_pages_leaves_the_request(first, n):
     assert int(err.item()) == e3.E3_DEV_ERR_CAPACITY
     for t in back:
         assert torch.all(t[:3] == 9.0) and torch.all(t[3, 0, 0] == 1.0) and torch.all(t[3, 0, 1:] == 9.0) and torch.all(t[4:] == 9.0)
+
+
+@pytest.mark.parametrize("rot,inter", [(64, False), (64, True), (24, False), (24, True)])
+def test_rotation_close_to_whole_quarter_turns(rot, inter):
+    """fp32 rows, unit vectors: cosine and sine are good to 2^-22 of themselves however close to 0 they are (half a
+    step of the reduced phase, 2^-25, and sincospif's one unit in the last place, 2^-23)."""
+    hd, R = 64, 96
+    rng = np.random.default_rng(3)
+    pos = np.concatenate([[0, 1, 355, 710, 103993, 104348, 208341, 312689, -355, 2 ** 31 - 1, -2 ** 31], rng.integers(-2 ** 31, 2 ** 31, R - 11)])
+    rope = e3.eagle3_rope_init(rot, 10000.0, interleaved=inter)
+    x = np.zeros((R, 3, hd), np.float32)
+    low, high = (np.arange(0, rot, 2), np.arange(1, rot, 2)) if inter else (np.arange(rot // 2), rot // 2 + np.arange(rot // 2))
+    x[:, :2, low] = 1.0
+    qkv = to_dev(x.reshape(R, -1))
+    K = torch.zeros((6, 1, 16, hd), device="cuda")
+    V, Q = torch.zeros_like(K), torch.zeros((R, hd), device="cuda")
+    pt, dpos, err = i32([list(range(6))]), i32(pos.astype(np.int64).astype(np.int32)), err_word()
+    kv = e3.make_kv_layer(K, V, pt, 6, 16, 6, 1, hd, e3.E3_F32)
+    e3.tree_qkv_append(qkv, 3 * hd, 1, R, None, 1, None, None, 0.0, rope, dpos, Q, kv, None, err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    hq, hk = host(Q), host(K)
+    for r in range(R):
+        for i in range(rot // 2):
+            ph = rope.turns[i] * int(pos[r]) % 2 ** 64
+            quarter, rest = (ph + 2 ** 61) >> 62, ((ph + 2 ** 61) & (2 ** 62 - 1)) - 2 ** 61
+            c, s = math.cos(rest * math.pi * 2.0 ** -63), math.sin(rest * math.pi * 2.0 ** -63)
+            c, s = [(c, s), (-s, c), (-c, -s), (s, -c)][quarter & 3]
+            for got in (hq[r], hk[r // 16, 0, r % 16]):
+                assert abs(got[low[i]] - c) <= 2.0 ** -22 * abs(c) and abs(got[high[i]] - s) <= 2.0 ** -22 * abs(s), (r, i)
