@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/eagle3.h"
+#include "per_device.h"
 
 namespace e3 {
 
@@ -74,6 +75,26 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     if (_e != cudaSuccess) return ::e3::cuda_status(_e, what);  \
     ::e3::note_launch();                                        \
   } while (0)
+
+// The current device's ordinal and its number of SMs (152, a GB300's, if it does not answer).
+inline int current_device() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+inline int num_sms() {
+  static NumberPerDevice known;
+  const int dev = current_device();
+  const int n = known.get(dev, [&] {
+    int x = 0;
+    return cudaDeviceGetAttribute(&x, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? x : 0;
+  });
+  return n > 0 ? n : 152;
+}
+// Kernel attributes, set before a kernel's first launch on a device.
+template <typename F>
+cudaError_t once_per_device(OncePerDevice<cudaError_t>& done, F&& f) {
+  return done.run(current_device(), f);
+}
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -798,10 +798,12 @@ accept_sampled_kernel(const int32_t* __restrict__ tok, const int32_t* __restrict
 int accept_cluster_size(int V) {
   static std::mutex mu;  // the cache below is read and refreshed as a unit
   const std::lock_guard<std::mutex> lock(mu);
-  static int cached_v = -1, cl = 8;
-  if (cached_v != V) {
+  static int cached_v = -1, cached_dev = -1, cl = 8;
+  const int dev = current_device();
+  if (cached_v != V || cached_dev != dev) {  // (the attribute is the device's)
     cl = 8;
     cached_v = V;
+    cached_dev = dev;
     if (cudaFuncSetAttribute(accept_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(16);
@@ -826,10 +828,12 @@ int accept_cluster_size(int V) {
 int accept_sampled_cluster_size(int V) {
   static std::mutex mu;  // the cache below is read and refreshed as a unit
   const std::lock_guard<std::mutex> lock(mu);
-  static int cached_v = -1, cl = 8;
-  if (cached_v != V) {
+  static int cached_v = -1, cached_dev = -1, cl = 8;
+  const int dev = current_device();
+  if (cached_v != V || cached_dev != dev) {  // (the attribute is the device's)
     cl = 8;
     cached_v = V;
+    cached_dev = dev;
     if (cudaFuncSetAttribute(accept_sampled_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
         cudaSuccess) {
       cudaLaunchConfig_t cfg = {};
@@ -859,10 +863,10 @@ e3_status launch_accept_sampled(const int32_t* tok, const int32_t* parent, const
                                 const int32_t* row_argmax, int V, const float* temp, const e3_qstat* q_stats,
                                 int q_cap, const uint32_t* u_acc, const uint32_t* u_bonus, int32_t* acc_len,
                                 int32_t* path, int32_t* out_tok, int32_t* status, cudaStream_t s) {
-  // one-time setup (a function-local static is initialised once, thread-safely)
-  static const bool attr_done =
-      (cudaFuncSetAttribute(accept_sampled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024), true);
-  (void)attr_done;
+  static OncePerDevice<cudaError_t> attrs;
+  once_per_device(attrs, [] {
+    return cudaFuncSetAttribute(accept_sampled_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  });
   const int CL = accept_sampled_cluster_size(V);
   const int per = (V + CL - 1) / CL;
   const size_t smem = static_cast<size_t>(per) * 8 + static_cast<size_t>((per + 31) / 32) * 4 + 16;
@@ -879,10 +883,10 @@ e3_status launch_accept(const int32_t* tok, const int32_t* parent, int B, int R,
                         const float* row_max, const uint64_t* row_Q, const int32_t* row_argmax, int V,
                         const float* temp, const uint32_t* u_acc, const uint32_t* u_bonus, int32_t* acc_len,
                         int32_t* path, int32_t* out_tok, int32_t* status, cudaStream_t s) {
-  // one-time setup (a function-local static is initialised once, thread-safely)
-  static const bool attr_done =
-      (cudaFuncSetAttribute(accept_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024), true);
-  (void)attr_done;
+  static OncePerDevice<cudaError_t> attrs;
+  once_per_device(attrs, [] {
+    return cudaFuncSetAttribute(accept_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  });
   const int CL = accept_cluster_size(V);
   const size_t smem = accept_smem_bytes((V + CL - 1) / CL);
   E3_REQUIRE(smem <= 200 * 1024, E3_ERR_SHAPE, "spec_accept: V=%d too large", V);

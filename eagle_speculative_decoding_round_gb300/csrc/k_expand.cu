@@ -462,8 +462,9 @@ template <int KMAX, bool SAMPLED>
 int cluster_size_for(int rows, int V, bool vec, int k) {
   static std::mutex mu;  // the cache below is read and refreshed as a unit
   const std::lock_guard<std::mutex> lock(mu);
-  static int cached_v = -1, cached_k = -1, max16 = 0;
-  if (cached_v != V || cached_k != k) {
+  static int cached_v = -1, cached_k = -1, cached_dev = -1, max16 = 0;
+  const int dev = current_device();
+  if (cached_v != V || cached_k != k || cached_dev != dev) {  // (the attribute is the device's)
     max16 = 0;
     if (cudaFuncSetAttribute(expand_rows_kernel<KMAX, SAMPLED>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
         cudaSuccess) {
@@ -484,6 +485,7 @@ int cluster_size_for(int rows, int V, bool vec, int k) {
     cudaGetLastError();
     cached_v = V;
     cached_k = k;
+    cached_dev = dev;
   }
   return rows <= max16 ? 16 : 8;
 }
@@ -492,11 +494,10 @@ template <int KMAX, bool SAMPLED>
 e3_status launch_rows(const float* logits, int rows, int F, int V, int k, float inv_temp, const float* parent_score,
                       const int32_t* parent_id, int depth, int cand_offset, const e3_cand& c, uint64_t seed,
                       e3_qstat* qs, int32_t* dev_err, cudaStream_t s) {
-  // one-time setup (a function-local static is initialised once, thread-safely)
-  static const bool attr_done = (cudaFuncSetAttribute(expand_rows_kernel<KMAX, SAMPLED>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024),
-                                 true);
-  (void)attr_done;
+  static OncePerDevice<cudaError_t> attrs;
+  once_per_device(attrs, [] {
+    return cudaFuncSetAttribute(expand_rows_kernel<KMAX, SAMPLED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  });
   const bool vec = (V % 4) == 0 && (reinterpret_cast<uintptr_t>(logits) & 15u) == 0;
   const int CL = cluster_size_for<KMAX, SAMPLED>(rows, V, vec, k);
   const int cand_cap = expand_cand_cap(V, vec, k, CL);

@@ -252,7 +252,7 @@ kv4_read_kernel(const __grid_constant__ Kv4Layers L4, e3_kv4_layer geo, const __
 dim3 row_grid(const e3_kv4_layer& geo, int L, int B, int max_rows, int* per) {
   const long long items = static_cast<long long>(geo.n_kv_heads) * max_rows * (geo.head_dim / 16);
   const long long x = (items + kThreads - 1) / kThreads;
-  *per = static_cast<int>(std::min<long long>(L, std::max<long long>(1, x * B * L / (8 * 152))));
+  *per = static_cast<int>(std::min<long long>(L, std::max<long long>(1, x * B * L / (8 * num_sms()))));
   return dim3(static_cast<unsigned>(x), (L + *per - 1) / *per, B);
 }
 

@@ -13,7 +13,6 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "e3_common.cuh"
 #include "e3_kernels.h"
@@ -674,7 +673,7 @@ e3_status launch_logits_process(const float* logits, int B, int R, int V, const 
   // CTAs of a row: as many as hold it, and more (down to 2048 tokens each) while the rows
   // leave SMs empty.  Rows of a cluster: several of one request, so that the request's lists are
   // built less often, as the rounds of clusters allow
-  const int sms = 152;
+  const int sms = num_sms();
   int CL = 1;
   while (CL < 8 && (CL * kPer < V || (static_cast<long>(B) * R * CL < sms && V > 2048 * CL))) CL *= 2;
   a.per = ((V + CL - 1) / CL + 3) / 4 * 4;
@@ -689,15 +688,13 @@ e3_status launch_logits_process(const float* logits, int B, int R, int V, const 
     }
   }
   const int smem = logits_smem(a.per, n_bias).total;
-  static std::atomic<bool> attr_done{false};
-  if (!attr_done.load(std::memory_order_acquire)) {
+  static OncePerDevice<cudaError_t> attrs;
+  const cudaError_t ea = once_per_device(attrs, [] {
     const int most = logits_smem(2 * kPer, kMaxBias).total;
-    cudaError_t e = cudaFuncSetAttribute(logits_process_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(logits_process_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-    if (e != cudaSuccess) return cuda_status(e, "logits_process_kernel smem attribute");
-    attr_done.store(true, std::memory_order_release);
-  }
+    const cudaError_t e0 = cudaFuncSetAttribute(logits_process_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    return e0 != cudaSuccess ? e0 : cudaFuncSetAttribute(logits_process_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  });
+  if (ea != cudaSuccess) return cuda_status(ea, "logits_process_kernel smem attribute");
   const bool vec = V % 4 == 0 && aligned16(logits) && aligned16(out) && (reinterpret_cast<uintptr_t>(counts) & 7u) == 0;
   const dim3 grid(static_cast<unsigned>(B) * ((R + a.rows - 1) / a.rows) * CL), block(kThreads);
   const cudaError_t e = vec ? launch_pdl(logits_process_kernel<true>, grid, block, smem, s, CL, a)

@@ -8,7 +8,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "e3_common.cuh"
 #include "e3_kernels.h"
@@ -321,17 +320,15 @@ constexpr size_t kSmemMost = 200 * 1024;
 
 template <typename T, int HD, bool INTER>
 cudaError_t launch_vec(const QkvArgs& a, const e3_rope& rope, cudaStream_t s) {
-  static std::atomic<bool> attr_done{false};
-  if (!attr_done.load(std::memory_order_acquire)) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(qkv_append_kernel<T, HD, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
-    if (e != cudaSuccess) return e;
-    attr_done.store(true, std::memory_order_release);
-  }
+  static OncePerDevice<cudaError_t> attrs;
+  const cudaError_t ea = once_per_device(attrs, [] {
+    return cudaFuncSetAttribute(qkv_append_kernel<T, HD, INTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+  });
+  if (ea != cudaSuccess) return ea;
   // one row per CTA while there are fewer than four for every place on the GPU (a row
   // alone has the shorter chain), then several
   int per = 1;
-  while (per < kMaxPer && a.rows >= 4 * per * 8 * 152) per *= 2;
+  while (per < kMaxPer && a.rows >= 4 * per * 8 * num_sms()) per *= 2;
   const size_t row_bytes = (static_cast<size_t>(a.H) + 2 * a.KVH) * HD * sizeof(T);
   int stages = std::min(per, kStages);
   while (stages > 1 && qkv_smem(row_bytes, stages, per, rope.rot_dim / 2) > kSmemMost) --stages;

@@ -21,7 +21,6 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "e3_common.cuh"
 #include "e3_kernels.h"
@@ -569,13 +568,11 @@ e3_status launch_fuse_bn(const CUtensorMap& a, const CUtensorMap& b0, const CUte
                          int Nw, int Mx, int kb_per_src, int kb_total, int splits, float* out, int32_t* dev_err,
                          cudaStream_t s) {
   using C = TcCfg<BN>;
-  static std::atomic<bool> attr_done{false};
-  if (!attr_done.load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(tc_gemm_kernel<BN, kModePartial>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return cuda_status(e, "tc_gemm_kernel smem attribute");
-    attr_done.store(true, std::memory_order_release);
-  }
+  static OncePerDevice<cudaError_t> attrs;
+  const cudaError_t ea = once_per_device(attrs, [] {
+    return cudaFuncSetAttribute(tc_gemm_kernel<BN, kModePartial>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (ea != cudaSuccess) return cuda_status(ea, "tc_gemm_kernel smem attribute");
   const int kb_per_split = (kb_total + splits - 1) / splits;  // callers pass splits with no empty split
   dim3 grid((Mx + BN - 1) / BN, (Nw + BM - 1) / BM, splits);
   const cudaError_t e = launch_pdl(tc_gemm_kernel<BN, kModePartial>, grid, dim3(192), C::SMEM, s, 1, a, b0, b1, b2, Nw,
@@ -676,23 +673,16 @@ e3_status launch_lmhead_bn(const CUtensorMap& a, const CUtensorMap& b, int V, in
                            unsigned long long* best, const float* temp, int32_t* dev_err, cudaStream_t s) {
   using C = LmCfg<BN>;
   static_assert(C::STAGES >= 2, "LM-head ring too small");
-  static std::atomic<bool> attr_done{false};
-  static std::atomic<int> n_sm{0};
-  if (!attr_done.load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(lmhead_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return cuda_status(e, "lmhead_kernel smem attribute");
-    int dev = 0;
-    cudaGetDevice(&dev);
-    int n = 0;
-    cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    n_sm.store(n < 1 ? 1 : n, std::memory_order_relaxed);
-    attr_done.store(true, std::memory_order_release);
-  }
+  static OncePerDevice<cudaError_t> attrs;
+  const cudaError_t ea = once_per_device(attrs, [] {
+    return cudaFuncSetAttribute(lmhead_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  });
+  if (ea != cudaSuccess) return cuda_status(ea, "lmhead_kernel smem attribute");
   const int n_mt = (M + BN - 1) / BN;
   const int n_vt = (V + BM - 1) / BM;
   const long n_tiles = static_cast<long>(n_mt) * n_vt;
   E3_REQUIRE(n_tiles < (1L << 31), E3_ERR_SHAPE, "lmhead_logits: %ld tiles", n_tiles);
-  const int grid = static_cast<int>(std::min<long>(n_tiles, n_sm.load(std::memory_order_relaxed)));
+  const int grid = static_cast<int>(std::min<long>(n_tiles, num_sms()));
   const cudaError_t e = launch_pdl(lmhead_kernel<BN>, dim3(grid), dim3(192), C::SMEM, s, 1, a, b, V, M, kb_total, n_mt,
                                    static_cast<int>(n_tiles), logits, best, temp, dev_err);
   if (e != cudaSuccess) return cuda_status(e, "lmhead_kernel");

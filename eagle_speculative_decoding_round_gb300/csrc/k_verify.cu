@@ -15,7 +15,6 @@
 // log2 domain into the workspace; a merge kernel combines the segments.
 #include <math.h>
 
-#include <atomic>
 
 #include "e3_common.cuh"
 #include "e3_kernels.h"
@@ -487,16 +486,6 @@ verify_merge_kernel(e3_kv_layer kv, const int32_t* __restrict__ kv_len, VerifyGe
   if (lane == 0) lse[row] = (M + log2f(den)) * kLn2;
 }
 
-int num_sms() {
-  static const int n_once = [] {  // queried once, thread-safely (152 on GB300 if the query fails)
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-    return n;
-  }();
-  return n_once;
-}
-
 VerifyGeom make_geom(int B, int R, int H, int KVH, int hd, int max_kv_len, bool mma) {
   VerifyGeom g{};
   g.B = B;
@@ -566,11 +555,10 @@ e3_status launch_verify(const void* Q, const e3_kv_layer& kv, const int32_t* kv_
 #define E3_MMA_CASE(HDV)                                                                           \
   do {                                                                                             \
     const int smem = MmaCfg<HDV>::SMEM;                                                            \
-    static std::atomic<bool> attr_done{false};                                                     \
-    if (!attr_done.load(std::memory_order_acquire)) {                                              \
-      cudaFuncSetAttribute(verify_mma_kernel<HDV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); \
-      attr_done.store(true, std::memory_order_release);                                            \
-    }                                                                                              \
+    static OncePerDevice<cudaError_t> attrs;                                                       \
+    once_per_device(attrs, [&] {                                                                   \
+      return cudaFuncSetAttribute(verify_mma_kernel<HDV>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem); \
+    });                                                                                            \
     verify_mma_kernel<HDV><<<grid, 256, smem, s>>>(static_cast<const __nv_bfloat16*>(Q), kv, kv_len, \
                                                    mask, g, sm_scale, ws_o, ws_ml, dev_err);       \
   } while (0)

@@ -32,7 +32,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "e3_common.cuh"
@@ -726,11 +725,11 @@ template <int HD, int NR>
 cudaError_t launch_mma(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
                        const uint64_t* mask, const V4Geom& g, float sm_scale, float* ws_o, float2* ws_ml, int32_t* ends,
                        __nv_bfloat16* o, float* lse, int32_t* dev_err, cudaStream_t s) {
-  static std::atomic<bool> attr_done{false};
-  if (!attr_done.load(std::memory_order_acquire)) {  // room for the rings of every resident CTA
-    cudaFuncSetAttribute(verify4_mma_kernel<HD, NR>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-    attr_done.store(true, std::memory_order_release);
-  }
+  static OncePerDevice<cudaError_t> attrs;
+  once_per_device(attrs, [] {  // room for the rings of every resident CTA
+    return cudaFuncSetAttribute(verify4_mma_kernel<HD, NR>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                cudaSharedmemCarveoutMaxShared);
+  });
   const cudaError_t e = launch_pdl(verify4_mma_kernel<HD, NR>, dim3(g.workers / kWarps), dim3(kWarps * 32), V4Cfg<HD>::SMEM, s,
                                    1, q, kv, tail, kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, dev_err);
   if (e != cudaSuccess) return e;

@@ -36,7 +36,6 @@
 #include <math.h>
 
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "e3_common.cuh"
@@ -971,17 +970,17 @@ template <int RT>
 cudaError_t launch_tc(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
                       const uint64_t* mask, const V4Geom& g, float sm_scale, float* ws_o, float2* ws_ml, int32_t* ends,
                       __nv_bfloat16* o, float* lse, int32_t* dev_err, cudaStream_t s) {
-  static std::atomic<bool> attr_done{false};
-  if (!attr_done.load(std::memory_order_acquire)) {
+  static OncePerDevice<cudaError_t> attrs;
+  const cudaError_t ea = once_per_device(attrs, [] {
     cudaError_t e = cudaFuncSetAttribute(verify4_tc_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<RT>::SMEM);
     if (e != cudaSuccess) return e;
     // a warpgroup that asked for registers which the launch did not bring would wait for ever
     cudaFuncAttributes fa;
     e = cudaFuncGetAttributes(&fa, verify4_tc_kernel<RT>);
     if (e != cudaSuccess) return e;
-    if (kThreads / 128 * fa.numRegs < kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsDeq) return cudaErrorLaunchOutOfResources;
-    attr_done.store(true, std::memory_order_release);
-  }
+    return kThreads / 128 * fa.numRegs < kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsDeq ? cudaErrorLaunchOutOfResources : cudaSuccess;
+  });
+  if (ea != cudaSuccess) return ea;
   const cudaError_t e = launch_pdl(verify4_tc_kernel<RT>, dim3(g.workers), dim3(kThreads), Cfg<RT>::SMEM, s, 1, q, kv, tail,
                                    kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, dev_err);
   if (e != cudaSuccess) return e;

@@ -1045,16 +1045,17 @@ e3_status launch_verify_tc(const void* Q, const e3_kv_layer& kv, const int32_t* 
   g.fold_tree = 0;
   g.prefix_stable = (kv.flags & E3_KV_PREFIX_STABLE) ? 1 : 0;
   g.stall = (kv.flags & E3_KV_SELFTEST_STALL) ? 1 : 0;
-  static std::atomic<bool> attr_done{false};
-  if (!attr_done.load(std::memory_order_acquire)) {
+  static OncePerDevice<cudaError_t> attrs;
+  const cudaError_t ea = once_per_device(attrs, [] {
     cudaError_t e = cudaFuncSetAttribute(verify_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(verify_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return cuda_status(e, "verify_tc_kernel smem attribute");
+    if (e != cudaSuccess) return e;
     cudaFuncSetAttribute(verify_tc_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     cudaGetLastError();
-    attr_done.store(true, std::memory_order_release);
-  }
+    return e;
+  });
+  if (ea != cudaSuccess) return cuda_status(ea, "verify_tc_kernel smem attribute");
   *merged = false;
   const int groups = g.RG * kv.n_kv_heads * B;
   const int Sc = pick_cluster_segments(groups, max_kv_len);

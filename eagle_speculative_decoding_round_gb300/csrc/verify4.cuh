@@ -94,16 +94,6 @@ __device__ __forceinline__ V4Place find_place(const V4Geom& g, const e3_kv4_laye
   return f;
 }
 
-int num_sms() {
-  static const int n_once = [] {  // queried once, thread-safely (152 on GB300 if the query fails)
-    int dev = 0, n = 0;
-    cudaGetDevice(&dev);
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
-    return n;
-  }();
-  return n_once;
-}
-
 }  // namespace
 
 }  // namespace e3
