@@ -26,6 +26,9 @@ static e3_status check_kv16(const e3_kv_layer* kv, const char* fn, const char* w
   return E3_OK;
 }
 
+// (a pointer off its elements' grid would fault in the paths for rows off the 16-byte grid)
+static bool on_grid(const void* p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
 static bool power_of_two(float u) {
   int ex = 0;
   return isfinite(u) && u > 0.0f && frexpf(u, &ex) == 0.5f && ex >= -59 && ex <= 61;
@@ -99,6 +102,8 @@ E3_API e3_status tree_qkv_append(const void* qkv, size_t ld, int B, int R, const
   const e3_status st = check_kv16(kv, fn, "kv");
   if (st != E3_OK) return st;
   E3_REQUIRE(qkv && Q, E3_ERR_INVALID_ARG, "%s: null pointer", fn);
+  const unsigned esz = kv->dt == E3_F32 ? 4 : 2;
+  E3_REQUIRE(on_grid(qkv, esz) && on_grid(Q, esz), E3_ERR_INVALID_ARG, "%s: qkv, Q not aligned to their elements", fn);
   E3_REQUIRE(!rope || pos, E3_ERR_INVALID_ARG, "%s: a rotation needs positions", fn);
   E3_REQUIRE(B >= 1 && R >= 1 && static_cast<long long>(B) * R <= 2147483647ll, E3_ERR_SHAPE, "%s: B=%d R=%d", fn, B, R);
   E3_REQUIRE(n_q_heads >= 1 && n_q_heads <= 65535 && kv->n_kv_heads <= 65535, E3_ERR_SHAPE, "%s: n_q_heads=%d", fn, n_q_heads);
@@ -181,6 +186,8 @@ E3_API e3_status tree_logits_process(const float* logits, int B, int R, int V, c
   clear_error();
   const char* fn = "tree_logits_process";
   E3_REQUIRE(logits && temp_per_row && out && row_max && row_Q && row_argmax, E3_ERR_INVALID_ARG, "%s: null pointer", fn);
+  E3_REQUIRE(on_grid(logits, 4) && on_grid(out, 4) && on_grid(counts, 2), E3_ERR_INVALID_ARG,
+             "%s: logits, out, counts not aligned to their elements", fn);
   E3_REQUIRE((tok == nullptr) == (parent == nullptr), E3_ERR_INVALID_ARG, "%s: tok and parent come together", fn);
   E3_REQUIRE(B >= 1 && R >= 1 && R <= E3_MAX_NODES + 1 && static_cast<long long>(B) * R <= 4000000, E3_ERR_SHAPE,
              "%s: B=%d R=%d", fn, B, R);

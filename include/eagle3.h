@@ -433,8 +433,8 @@ E3_API e3_status eagle3_rope_init(const e3_rope_spec* spec /* host */, e3_rope* 
  * Rows r >= n_rows[b] and their slots are left as they were.  A row whose slot has
  * no page (past max_pages, a page id out of range, kv_len[b] < 0) sets
  * E3_DEV_ERR_CAPACITY; its Q is written, its K and V are not.
- * qkv, Q: dtype kv->dt, 16-byte aligned rows take the vector path, others a
- * scalar one.  The output buffers must not overlap qkv.
+ * qkv, Q: dtype kv->dt, aligned to their elements; 16-byte aligned rows take the vector
+ * path, others a scalar one.  The output buffers must not overlap qkv.
  * Limits: rope->rot_dim <= head_dim; ld >= (n_q_heads + 2 n_kv_heads) head_dim;
  * B*R < 2^31; kv->flags 0 or E3_KV_PREFIX_STABLE (ignored).
  * ------------------------------------------------------------------------- */
@@ -565,7 +565,7 @@ E3_API size_t eagle3_verify4_workspace_bytes(int B, int R, int n_q_heads, int n_
  * allow: [n_allow][ceil(V/32)] uint32, bit v % 32 of word v / 32 (NULL: no grammar);
  * allow_row: [B][R], the row of allow that node follows, outside [0, n_allow): all
  * allowed (NULL: row b*R + i).
- * out may be logits itself.  With sampled drafts the accept step stays exact: it reads
+ * logits, out, counts: aligned to their elements; out may be logits itself.  With sampled drafts the accept step stays exact: it reads
  * the processed rows as the target's.
  * Limits: n_bias <= 1024; R <= 256; paths as above; V >= 1, V < 2^30.
  * ------------------------------------------------------------------------- */

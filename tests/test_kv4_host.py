@@ -180,3 +180,19 @@ def test_plain_quantizer():
     step = np.repeat(kv4_ref.E4M3[e] * 0.25, 16, 1)
     # half the widest grid gap, or clipping by the scale's own rounding (half of 2^-3 of 6 steps)
     assert np.all(np.abs(d - y) <= step * 1.0 + 1e-12)
+
+
+def test_pointers_off_their_elements_are_refused(e3):
+    """Rows may start anywhere on their elements' grid (the scalar paths take those), but not off it."""
+    def qkv(x=A, q=A, dt=None, hd=64):
+        e3.tree_qkv_append(x, 3 * hd + 1, 1, 1, None, 1, None, None, 0.0, None, None, q, kv16(e3, hd=hd, KVH=1, dt=dt), None, None,
+                           stream=0)
+
+    def logits(z=A, counts=None, out=A):
+        e3.tree_logits_process(z, 1, 1, 1000, A, counts, None, None, None, None, None, 0, None, None, 0, out, A, A, A, None, stream=0)
+    n0 = e3.launch_count()
+    for call, kw in ((qkv, dict(x=A + 1)), (qkv, dict(q=A + 1)), (qkv, dict(x=A + 2, dt=e3.E3_F32)), (qkv, dict(q=A + 2, dt=e3.E3_F32)),
+                     (logits, dict(z=A + 2)), (logits, dict(out=A + 1)), (logits, dict(counts=A + 1))):
+        with pytest.raises(e3.E3Error) as ei:
+            call(**kw)
+        assert ei.value.status == 1 and e3.launch_count() == n0, kw
