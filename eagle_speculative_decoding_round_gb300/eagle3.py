@@ -319,8 +319,12 @@ def _layer_arrays(fn, layers, others):
     if len(layers) != len(others):
         raise ValueError(f"{fn}: {len(layers)} 4-bit layers and {len(others)} 16-bit ones")
     # one copy of the descriptors' bytes (filling a ctypes array element by element takes longer than the launch)
-    return ((e3_kv4_layer * len(layers)).from_buffer_copy(b"".join(layers)),
-            (e3_kv_layer * len(others)).from_buffer_copy(b"".join(others)))
+    a4, a16 = b"".join(layers), b"".join(others)
+    n = len(layers)
+    # (their sizes differ, so a descriptor of the other kind shows in the sum)
+    if len(a4) != n * ctypes.sizeof(e3_kv4_layer) or len(a16) != n * ctypes.sizeof(e3_kv_layer):
+        raise TypeError(f"{fn}: e3_kv4_layer and e3_kv_layer descriptors wanted")
+    return (e3_kv4_layer * n).from_buffer_copy(a4), (e3_kv_layer * n).from_buffer_copy(a16)
 
 
 def kv4_append(layers, src, B, max_rows, rows, n_rows, n_add, kv_len, kv_len_next, dev_err=None, stream=None):

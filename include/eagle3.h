@@ -565,8 +565,8 @@ E3_API size_t eagle3_verify4_workspace_bytes(int B, int R, int n_q_heads, int n_
  * allow: [n_allow][ceil(V/32)] uint32, bit v % 32 of word v / 32 (NULL: no grammar);
  * allow_row: [B][R], the row of allow that node follows, outside [0, n_allow): all
  * allowed (NULL: row b*R + i).
- * logits, out, counts: aligned to their elements; out may be logits itself.  With sampled drafts the accept step stays exact: it reads
- * the processed rows as the target's.
+ * logits, out, counts: aligned to their elements; out may be logits itself.  With sampled
+ * drafts the accept step stays exact: it reads the processed rows as the target's.
  * Limits: n_bias <= 1024; R <= 256; paths as above; V >= 1, V < 2^30.
  * ------------------------------------------------------------------------- */
 E3_API e3_status tree_logits_process(const float* logits, int B, int R, int V, const float* temp_per_row,

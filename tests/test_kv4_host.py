@@ -196,3 +196,14 @@ def test_pointers_off_their_elements_are_refused(e3):
         with pytest.raises(e3.E3Error) as ei:
             call(**kw)
         assert ei.value.status == 1 and e3.launch_count() == n0, kw
+
+
+def test_layer_lists_of_the_wrong_kind_are_refused(e3):
+    """A descriptor of the other cache's kind would be read as pointers that it does not hold."""
+    for call in (lambda a, b: e3.kv4_append(a, b, 1, 1, None, A, 0, A, None, None, stream=0),
+                 lambda a, b: e3.kv4_read(a, b, 1, 1, None, A, None, stream=0)):
+        for a, b in (([kv4(e3)], [kv4(e3)]), ([kv16(e3)], [kv16(e3)]), ([kv16(e3)], [kv4(e3)]), ([kv4(e3), kv16(e3)], [kv16(e3)] * 2)):
+            n0 = e3.launch_count()
+            with pytest.raises(TypeError):
+                call(a, b)
+            assert e3.launch_count() == n0
