@@ -163,19 +163,27 @@ def ptr(x) -> int | None:
     return x.data_ptr()
 
 
-_torch_c = None
+_current_stream = None
+
+
+def _find_current_stream():
+    """How this torch tells its current stream's handle.  The call without the Stream object is
+    not a public one, but takes a thirtieth of torch.cuda.current_stream() (2.9 us, as long as a
+    small launch); a torch that lacks it is asked the public way."""
+    import torch
+    torch.cuda.current_stream()  # initializes CUDA on first use
+    device, raw = getattr(torch._C, "_cuda_getDevice", None), getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if device is None or raw is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
 
 
 def _stream(stream):
     if stream is None:
-        # torch's current stream as its handle; the call without the Stream object costs
-        # a thirtieth of torch.cuda.current_stream() (2.9 us, as long as a small launch)
-        global _torch_c
-        if _torch_c is None:
-            import torch
-            torch.cuda.current_stream()  # initializes CUDA on first use
-            _torch_c = torch._C
-        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -207,3 +207,20 @@ def test_layer_lists_of_the_wrong_kind_are_refused(e3):
             with pytest.raises(TypeError):
                 call(a, b)
             assert e3.launch_count() == n0
+
+
+@pytest.mark.parametrize("missing", [(), ("_cuda_getCurrentRawStream",), ("_cuda_getDevice",)])
+def test_current_stream_without_the_short_call(e3, monkeypatch, missing):
+    """The stream of a call: by torch's short call where torch has it, else by its public one."""
+    import sys
+    import types
+    fake = types.ModuleType("torch")
+    short = {"_cuda_getCurrentRawStream": lambda d: 100 + d, "_cuda_getDevice": lambda: 1}
+    fake._C = types.SimpleNamespace(**{k: v for k, v in short.items() if k not in missing})
+    fake.cuda = types.SimpleNamespace(current_stream=lambda *a: types.SimpleNamespace(cuda_stream=77))
+    monkeypatch.setitem(sys.modules, "torch", fake)
+    for name in ("_torch_c", "_current_stream"):  # what the first call leaves
+        if hasattr(e3, name):
+            monkeypatch.setattr(e3, name, None)
+    assert [e3._stream(None) for _ in range(2)] == ([77, 77] if missing else [101, 101])
+    assert e3._stream(5) == 5 and e3._stream(types.SimpleNamespace(cuda_stream=9)) == 9
