@@ -16,7 +16,7 @@ import kv4_ref
 import oracle
 from eagle_speculative_decoding_round_gb300 import synth
 from gpu_util import host, to_dev
-from test_gpu_kv4 import attn_inputs, err_word, i32, mask_of, ruled_out
+from test_gpu_kv4 import ATTN, attn_inputs, err_word, i32, mask_of, ruled_out
 
 pytestmark = pytest.mark.gpu
 
@@ -261,3 +261,65 @@ def test_rotation_close_to_whole_quarter_turns(rot, inter):
             c, s = [(c, s), (-s, c), (-c, -s), (s, -c)][quarter & 3]
             for got in (hq[r], hk[r // 16, 0, r % 16]):
                 assert abs(got[low[i]] - c) <= 2.0 ** -22 * abs(c) and abs(got[high[i]] - s) <= 2.0 ** -22 * abs(s), (r, i)
+
+
+@pytest.mark.parametrize("case", [c for c in ATTN if c[1] <= 64])
+def test_attention_with_a_bound_for_each_part(case):
+    """Prefix weights are good to fp16, the nodes' to bf16: the bounds of check_attn, which holds each part to its own."""
+    B, R, H, KVH, hd, page, lens = case
+    d = attn_inputs(R * 7 + H + hd + lens[0] + 1, B, R, H, KVH, hd, lens, page)
+    scale = 1 / math.sqrt(hd)
+    check_attn(d, *attn(d, scale), scale)
+
+
+@pytest.mark.parametrize("V", [1500, 2052, 40000, 40003, 262148])
+@pytest.mark.parametrize("seen", ["all", "list full", "list passed", "first part"])
+def test_more_seen_tokens_than_the_list_holds(V, seen):
+    """A part's list holds 1024 seen tokens: all seen, just as many, one more, and one part full while the others
+    are not; path and bias tokens among the seen ones and beside them."""
+    R, rng = 5, np.random.default_rng(V + len(seen))
+    counts = np.zeros((1, V), np.uint16)
+    hit = {"all": np.arange(V), "list full": np.arange(1024), "list passed": np.arange(1025),
+           "first part": np.concatenate([np.arange(min(V, 5000)), rng.integers(0, V, 20)])}[seen]
+    counts[0, hit] = rng.integers(1, 4, len(hit))
+    counts[0, hit[::3]] |= 32768
+    counts[0, hit[::5]] = 32768
+    z = (rng.normal(size=(R, V)) * 3).astype(np.float32)
+    par = np.int32([[-1, 0, 1, 1, 2]])
+    tok = np.int32([[3, 7, V - 1, 7, 1023]])
+    pen = np.float32([[1.3, 0.2, 0.1]])
+    bt = np.int32([[7, 1023, 7, V - 1, V // 2, 1100]])
+    bv = (rng.normal(size=bt.shape) * 2).astype(np.float32)
+    out, mx, Q, am, err = logits_call(z, V, np.full(R, 0.7, np.float32), counts, tok, par, pen, (bt, bv))
+    assert err == 0
+    for i in range(R):
+        path, u = [], i
+        while u > 0:
+            path.append(int(tok[0, u]))
+            u = par[0, u]
+        want = kv4_ref.process(z[i], counts[0], path, pen[0], bt[0], bv[0], None)
+        assert np.array_equal(out[i], want), (i, np.nonzero(out[i] != want)[0][:5])
+        check_row(want, 0.7, mx[i], Q[i], am[i], i)
+
+
+@pytest.mark.parametrize("V", [2052, 40000, 40003, 128256, 262148])
+def test_flagged_rows_of_wide_vocabularies(V):
+    """A masked row, a NaN in a masked place, a NaN in the last token, an Inf in the middle, a good row."""
+    R, W = 5, (V + 31) // 32
+    z = np.random.default_rng(V).normal(size=(R, V)).astype(np.float32)
+    z[1, V // 3] = np.nan
+    z[2, V - 1] = np.nan
+    z[3, V // 2] = np.inf
+    allow = np.full((R, W), 0xFFFFFFFF, np.uint32)
+    allow[0] = 0
+    allow[1, V // 3 // 32] &= ~np.uint32(1 << (V // 3 % 32))
+    out, mx, Q, am, err = logits_call(z, V, np.ones(R, np.float32), allow=allow, arow=np.arange(R, dtype=np.int32)[None])
+    assert err == e3.E3_DEV_ERR_MASKED | e3.E3_DEV_ERR_NONFINITE
+    assert np.isnan(mx[[0, 2, 3]]).all() and not Q[[0, 2, 3]].any() and np.all(am[[0, 2, 3]] == -1)
+    assert np.all(np.isneginf(out[0]))
+    for i in (1, 4):
+        want = z[i].copy()
+        if i == 1:
+            want[V // 3] = -np.inf
+        assert np.array_equal(out[i], want)
+        check_row(want, 1.0, mx[i], Q[i], am[i], i)
