@@ -13,7 +13,7 @@
 // fp16 form keeps every bf16 bit down to 2^-24 of the row's largest value; the unit, the
 // row's power of two and sm_scale meet the fp32 scores.  P is rounded to fp16 (2^-11 of
 // a weight, or 2^-32 of the row's largest), sums stay in fp32.  The tail runs in bf16 as
-// it is stored, P with it (2^-8 of a weight at most).
+// it is stored, P in two bf16 parts (2^-16 of a weight).
 //
 // Bound: instructions (about 375 a granule and warp: 128 conversions and products of the
 // codes, 16 mma.sync; the schedulers issue on 60% of the cycles, 3.5 warps each).  Two
@@ -391,12 +391,22 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
           }
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr) {
-            const uint32_t p0 = transpose8(pack2_bf16(sc[0][nr][0], sc[0][nr][1])), p1 = transpose8(pack2_bf16(sc[0][nr][2], sc[0][nr][3]));
+            // a weight in two bf16 parts (2^-16 of it is left out): one part alone would be the
+            // largest error of a row that sees mostly nodes
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const float* w = sc[0][nr] + 2 * x;
+              hi[x] = pack2_bf16(w[0], w[1]);
+              lo[x] = transpose8(pack2_bf16(w[0] - __uint_as_float(hi[x] << 16), w[1] - __uint_as_float(hi[x] & 0xFFFF0000u)));
+              hi[x] = transpose8(hi[x]);
+            }
 #pragma unroll
             for (int d = 0; d < DV / 2; ++d) {
               const uint32_t a[4] = {__byte_perm(raw[0][d], raw[1][d], 0x5410), __byte_perm(raw[0][d], raw[1][d], 0x7632),
                                      __byte_perm(raw[2][d], raw[3][d], 0x5410), __byte_perm(raw[2][d], raw[3][d], 0x7632)};
-              mma_b16(o[nr][d], a, p0, p1);
+              mma_b16(o[nr][d], a, hi[0], hi[1]);
+              mma_b16(o[nr][d], a, lo[0], lo[1]);
             }
           }
         }

@@ -521,9 +521,12 @@ E3_API e3_status kv4_read(const e3_kv4_layer* layers, const e3_kv_layer* dst, in
  * kv_len[b] outside [0, max_kv_len] or beyond the pages sets E3_DEV_ERR_CAPACITY and
  * leaves the request's outputs unwritten; a page id out of range sets it and makes
  * the request's outputs unspecified.
- * Arithmetic: products of the prefix in fp16 (exact operands but for P), of the nodes'
- *   V in bf16, weights up to 2^15 of a row's base, sums in fp32: nodes' V up to 2^100 in
- *   magnitude cannot overflow them.
+ * Arithmetic: products of the prefix in fp16 (exact operands but for the weights, which
+ *   are good to 2^-11), of the nodes' V in bf16 (their weights good to 2^-8, or, up to 32
+ *   query rows per KV head and for heads of 64, to 2^-16), weights up to 2^15 of a row's
+ *   base, sums in fp32: nodes' V up to 2^100 in magnitude cannot overflow them.  Q's values
+ *   below 2^-24 of their row's largest, and in the other case the nodes' K below 2^-24 of
+ *   theirs, lose bits.
  * Limits: head_dim 64 or 128; R <= 256; n_q_heads % n_kv_heads == 0; tail pages hold R
  *   slots.  E3_KV_PREFIX_STABLE in kv->flags is accepted (and not used).
  * ws: eagle3_verify4_workspace_bytes(...) bytes of device scratch, 16-byte aligned;

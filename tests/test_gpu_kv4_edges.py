@@ -2,7 +2,8 @@
 
 Tolerances of the attention, from the arithmetic (check_attn):
   scores   fp32 sums of 128 products: 2^-18 of the largest sum |q||k| scale
-  weights  of prefix keys rounded to fp16, half a step 2^-11; of tree nodes to bf16, 2^-8;
+  weights  of prefix keys rounded to fp16, half a step 2^-11; of tree nodes to bf16, 2^-8, or
+           up to 32 query rows per KV head and for heads of 64 to two bf16 parts, 2^-16;
            each twice the score error on top
   output   half a bf16 step of the value reached, 2^-8 of it
 """
@@ -49,7 +50,7 @@ def parts(d, b):
     return k, v, tk, tv
 
 
-def check_attn(d, O, lse, scale, skip=()):
+def check_attn(d, O, lse, scale, skip=(), node=2.0 ** -8):
     for b in range(d["B"]):
         k, v, tk, tv = parts(d, b)
         Q, see, R = d["Q"][b].astype(np.float64), d["see"][b], d["R"]
@@ -69,7 +70,7 @@ def check_attn(d, O, lse, scale, skip=()):
             G = d["H"] // d["KVH"]
             tiny = 2.0 ** -32 * np.repeat(np.abs(v).sum(0), G, 0) if len(v) else 0.0
             w = 2 * ds[i][:, None]
-            e = (2.0 ** -11 + w) * mag_p[i] + (2.0 ** -8 + w) * mag_n[i] + tiny
+            e = (2.0 ** -11 + w) * mag_p[i] + (node + w) * mag_n[i] + tiny
             tol = e + 2.0 ** -8 * (np.abs(o[i]) + e) + 2.0 ** -126
             bad = np.abs(O[b, i] - o[i]) - tol
             assert np.all(bad <= 0), (b, i, bad.max(), np.abs(o[i]).max())
@@ -323,3 +324,11 @@ def test_flagged_rows_of_wide_vocabularies(V):
             want[V // 3] = -np.inf
         assert np.array_equal(out[i], want)
         check_row(want, 1.0, mx[i], Q[i], am[i], i)
+
+
+@pytest.mark.parametrize("R,G,hd", [(15, 1, 64), (40, 4, 64), (8, 4, 128), (3, 2, 128)])
+def test_rows_of_nodes_alone(R, G, hd):
+    """No prefix: the nodes' weights are the row, and their two parts hold 2^-16 of it."""
+    d = attn_inputs(R + G + 6, 3, R, 2 * G, 2, hd, [0, 0, 0], 16)
+    scale = 1 / math.sqrt(hd)
+    check_attn(d, *attn(d, scale), scale, node=2.0 ** -16)
