@@ -144,7 +144,10 @@ E3_API e3_status kv4_read(const e3_kv4_layer* layers, const e3_kv_layer* dst, in
 }
 
 E3_API size_t eagle3_verify4_workspace_bytes(int B, int R, int n_q_heads, int n_kv_heads, int head_dim, int max_kv_len) {
-  if (B < 1 || R < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads != 0 || head_dim < 1 || max_kv_len < 0)
+  // (the bounds of the call itself)
+  if (B < 1 || B > 65535 || R < 1 || R > E3_MAX_NODES + 1 || n_q_heads < 1 || n_q_heads > 65535 || n_kv_heads < 1 ||
+      n_q_heads % n_kv_heads != 0 || static_cast<long long>(B) * R * n_q_heads >= (1ll << 31) ||
+      (head_dim != 64 && head_dim != 128) || max_kv_len < 0 || max_kv_len > (1 << 30))
     return 0;
   return verify4_workspace_bytes(B, R, n_q_heads, n_kv_heads, head_dim, max_kv_len);
 }

@@ -529,7 +529,8 @@ E3_API e3_status kv4_read(const e3_kv4_layer* layers, const e3_kv_layer* dst, in
  *   theirs, lose bits.
  * Limits: head_dim 64 or 128; R <= 256; n_q_heads % n_kv_heads == 0; tail pages hold R
  *   slots.  E3_KV_PREFIX_STABLE in kv->flags is accepted (and not used).
- * ws: eagle3_verify4_workspace_bytes(...) bytes of device scratch, 16-byte aligned;
+ * ws: eagle3_verify4_workspace_bytes(...) bytes of device scratch (0 for sizes that the
+ *   call refuses), 16-byte aligned;
  *   calls that may overlap on the GPU need scratch of their own.
  * ------------------------------------------------------------------------- */
 E3_API e3_status tree_verify_attn4(const void* Q, const e3_kv4_layer* kv /* host struct */,

@@ -224,3 +224,13 @@ def test_current_stream_without_the_short_call(e3, monkeypatch, missing):
             monkeypatch.setattr(e3, name, None)
     assert [e3._stream(None) for _ in range(2)] == ([77, 77] if missing else [101, 101])
     assert e3._stream(5) == 5 and e3._stream(types.SimpleNamespace(cuda_stream=9)) == 9
+
+
+def test_workspace_is_asked_for_calls_that_are_taken(e3):
+    """0 for what tree_verify_attn4 refuses, and no arithmetic that wraps on the way."""
+    ok = dict(B=2, R=61, H=32, KVH=8, hd=128, P=4096)
+    ask = lambda **kw: e3.eagle3_verify4_workspace_bytes(*(ok | kw).values())  # noqa: E731
+    assert ask() > 0 and ask(hd=64) > 0 and ask(R=256, P=0) > 0 and ask(B=65535, R=1) > 0
+    for kw in (dict(B=0), dict(B=65536), dict(R=0), dict(R=257), dict(R=70000, H=70000, KVH=1), dict(H=65536), dict(H=30), dict(KVH=0),
+               dict(hd=96), dict(hd=0), dict(P=-1), dict(P=(1 << 30) + 1), dict(B=65535, R=256, H=65535, KVH=1)):
+        assert ask(**kw) == 0, kw
