@@ -677,7 +677,10 @@ e3_status launch_logits_process(const float* logits, int B, int R, int V, const 
   int CL = 1;
   while (CL < 8 && (CL * kPer < V || (static_cast<long>(B) * R * CL < sms && V > 2048 * CL))) CL *= 2;
   a.per = ((V + CL - 1) / CL + 3) / 4 * 4;
-  const long places = std::max(1, 408 / CL);  // clusters that three CTAs an SM leave room for (51 of eight, as the occupancy query answers)
+  // clusters that three CTAs an SM leave room for (51 of eight, as the occupancy query answers).  Parts
+  // of more than 64 KB (V > 131072) fit twice or once, and the choice below counts too much room there:
+  // the results do not depend on it
+  const long places = std::max(1, 408 / CL);
   a.rows = 1;
   long cost = 0;
   for (int n = 1; n <= 16 && n <= R; ++n) {  // rounds of clusters x (their rows + the lists, about a row's time)

@@ -1,10 +1,10 @@
 // k_verify4.cu -- tree_verify_attn4: tree attention whose prefix is held in 4 bits.
 //
 // Segments as in k_verify.cu ("EAGLE-3 投机解码与 USP 长序列训练优化", USP 核心设计：
-// 三步走): the 4-bit prefix is split across CTAs, the tree nodes' bf16 tail joins the
-// last segment, partial (o, m, l) records are merged by their log-sum-exp.
+// 三步走): the 4-bit prefix and, behind it, the tree nodes' bf16 tail are split across
+// warps, partial (o, m, l) records are merged by their log-sum-exp.
 //
-// verify4_mma_kernel: a warp works alone on 16 query rows of one KV head and a run of
+// verify4_mma_kernel: a warp works alone on 8 or 16 query rows of one KV head and a run of
 // 16-key granules, whose codes and scales reach its ring in shared memory by cp.async.
 // Warps share nothing: one's waits pass under the others' arithmetic.  The
 // codes become fp16 matrix operands in registers: a value c * e (e2m1 times e4m3) has at
@@ -15,11 +15,11 @@
 // a weight, or 2^-32 of the row's largest), sums stay in fp32.  The tail runs in bf16 as
 // it is stored, P in two bf16 parts (2^-16 of a weight).
 //
-// Bound: instructions (about 375 a granule and warp: 128 conversions and products of the
-// codes, 16 mma.sync; the schedulers issue on 60% of the cycles, 3.5 warps each).  Two
+// Bound: instructions (about 360 a granule and warp: 128 conversions and products of the
+// codes, 16 mma.sync; the schedulers issue on 61% of the cycles, 3.5 warps each).  Two
 // granules a step let one's products run under the other's conversions (47 us against 49.6).
-// Measured, whole calls: 32 requests of 512 .. 8192 keys, one node, 32 heads on 8: 43.7 us
-// (160 MB: 3.7 TB/s); one request of 32768 keys, one node, 29 us; of 2048 keys, 16 us.
+// Measured, whole calls: 32 requests of 512 .. 8192 keys, one node, 32 heads on 8: 43.6 us
+// (160 MB: 3.7 TB/s); one request of 32768 keys, one node, 25 us; of 2048 keys, 10.4 us.
 //
 // The dims of a head and the keys of a granule may be taken in any order by the
 // contractions.  K: thread (g, c) = (lane / 4, lane % 4) reads hd/4 consecutive dims of
@@ -306,7 +306,7 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
     // 64 take the nodes first where the unit leaves room (256 weights of up to 2^15 and V of up
     // to 2^100 have 2^4 of it to 2^127): their loads then pass under the first granules' (3
     // requests of 15 nodes: 10.8 us, 11.2 behind).  Heads of 128 would pay with registers (32
-    // requests, one node: 44.2, 43.4 behind).
+    // requests, one node: 44.2, 43.6 behind).
     const bool nodes_first = HD == 64 && kv.v_unit >= 0.0625f;
 #pragma unroll(HD == 64 ? 1 : 2)
     for (int turn = 0; turn < 2; ++turn) {
@@ -707,7 +707,7 @@ verify4_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __r
   if (lane == 0) lse[row] = den != 0.0f ? (M + log2f(den)) * kLn2 : -INFINITY;
 }
 
-// Shares of the granule kernel: every warp that is resident, none below four granules.
+// Shares of the granule kernel: one for every warp that is resident, of three granules at least.
 // Query rows in tiles of eight while they fit one, else of sixteen.
 V4Geom make_geom(int B, int R, int H, int KVH, int max_kv_len) {
   V4Geom g{};

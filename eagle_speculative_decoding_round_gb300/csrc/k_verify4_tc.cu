@@ -8,7 +8,9 @@
 //   dequantizers (4 + 4 warps, K and V) codes -> fp16 operands in 128-byte-swizzled shared
 //                          memory: a value c * e is exact in fp16 (see k_verify4.cu).  Tree
 //                          nodes come from the bf16 tail: K scaled by a power of two per
-//                          key, which keeps its bits, V as it is, for a product in bf16
+//                          key, which keeps its bits, V as it is, for a product in bf16 (a
+//                          node's weight is good to 2^-8; a second part of it would be half
+//                          of a node tile's products again and more columns of P)
 //   S = Q K^T              (warps 1 and 2, one issuing thread per softmax group)
 //                          tcgen05.mma kind::f16, 128 rows x 128 keys
 //   softmax (2 x 4 warps)  one thread per row: exponentials, P over S in halves of 64 keys
@@ -25,8 +27,8 @@
 // other's products.  What a part costs by itself (Q, the nodes, the record: some 15,000
 // cycles) is counted when the work is shared out.
 // Measured, whole calls, 32 heads on 8 KV heads: 32 requests of 512 .. 8192 keys with 61
-// nodes 180 us (140 GFLOP: 780 TFLOP/s; the 4-bit cache and all else read once: 1.1 TB/s);
-// one request of 65536 keys with 33 nodes 80 us; of 2048 keys with 61 nodes 17.5 us.
+// nodes 178 us (140 GFLOP: 787 TFLOP/s; the 4-bit cache and all else read once: 1.1 TB/s);
+// one request of 65536 keys with 33 nodes 79 us; of 2048 keys with 61 nodes 17.7 us.
 //
 // What was slower: steps of 64 keys with two S buffers a group (batch 480, 128 keys 450 at
 // that time), one dequantizing warpgroup for K and V (334 against 315), a pass for the row
@@ -556,7 +558,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
             }
           }
         } else {
-          // tree nodes: K to fp16, each key's largest magnitude scaled to [1, 2) (its scores
+          // tree nodes: K to fp16, each key's largest magnitude scaled to [1, 4) (its scores
           // get the factor back); V as it is stored, its product runs in bf16
           int own = -1;  // this lane's row of the warp's 32
           if (dw * 32 + lane < left) {
@@ -997,8 +999,8 @@ cudaError_t launch_tc(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_k
 
 // Up to 32 query rows per KV head the granule kernel's one or two tiles of 16 rows cost less,
 // beyond them it would read the cache once more for every 16.  32 heads on 8, us, granule
-// kernel / this one: 32 requests of 512 .. 8192 keys with 16, 32, 48 rows 66 / 145, 114 / 150,
-// 163 / 152; one request of 32768 keys with 16, 32 rows 33 / 47, 39 / 49.
+// kernel / this one: 32 requests of 512 .. 8192 keys with 16, 32, 48 rows 55 / 105, 98 / 106,
+// 141 / 108; one request of 32768 keys 25 / 35, 33 / 35, 41 / 36.
 bool verify4_uses_tc(int R, int H, int KVH, int hd) { return hd == kHD && H / KVH * R > 32; }
 
 size_t verify4_tc_workspace_bytes(int B, int R, int H, int KVH, int max_kv_len) {
