@@ -382,7 +382,7 @@ extern "C" E3_API e3_status eagle3_rope_init(const e3_rope_spec* spec, e3_rope* 
   E3_REQUIRE(isfinite(spec->amp) && spec->amp >= 0.0 && spec->amp < 1e30, E3_ERR_INVALID_ARG, "%s: amp", fn);
   const int kind = spec->scaling;
   if (kind != E3_ROPE_PLAIN)
-    E3_REQUIRE(isfinite(spec->factor) && spec->factor >= 1e-6, E3_ERR_INVALID_ARG, "%s: factor must be > 0", fn);
+    E3_REQUIRE(isfinite(spec->factor) && spec->factor >= 1e-6, E3_ERR_INVALID_ARG, "%s: factor must be >= 1e-6", fn);
   const bool ramp = kind == E3_ROPE_WAVELEN || kind == E3_ROPE_YARN;
   if (ramp)
     E3_REQUIRE(isfinite(spec->high) && isfinite(spec->orig_len) && spec->low > 0.0 && spec->low < spec->high &&

@@ -401,7 +401,7 @@ typedef struct {
   int interleaved;
   int scaling;     /* e3_rope_scaling */
   double base;     /* > 1 */
-  double factor;   /* > 0; scalings other than PLAIN */
+  double factor;   /* >= 1e-6; scalings other than PLAIN */
   double low;      /* turns; WAVELEN and YARN, 0 < low < high */
   double high;
   double orig_len; /* trained length; WAVELEN and YARN, > 0 */
