@@ -18,8 +18,8 @@
 // Bound: instructions (about 360 a granule and warp: 128 conversions and products of the
 // codes, 16 mma.sync; the schedulers issue on 61% of the cycles, 3.5 warps each).  Two
 // granules a step let one's products run under the other's conversions (47 us against 49.6).
-// Measured, whole calls: 32 requests of 512 .. 8192 keys, one node, 32 heads on 8: 43.6 us
-// (160 MB: 3.7 TB/s); one request of 32768 keys, one node, 25 us; of 2048 keys, 10.4 us.
+// Measured, whole calls: 32 requests of 512 .. 8192 keys, one node, 32 heads on 8: 43.4 us
+// (160 MB: 3.7 TB/s); one request of 32768 keys, one node, 25 us; of 2048 keys, 10.6 us.
 //
 // The dims of a head and the keys of a granule may be taken in any order by the
 // contractions.  K: thread (g, c) = (lane / 4, lane % 4) reads hd/4 consecutive dims of
@@ -302,13 +302,15 @@ verify4_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
       return (static_cast<long long>(page) * g.KVH + kvh) * tail.page_size + j % tail.page_size;
     };
     // Nodes behind the prefix: the prefix sums in units of v_unit, in which a node's V may pass
-    // the range (2^100 at a unit of 2^-60); in values the prefix's sum is far below it.  Heads of
-    // 64 take the nodes first where the unit leaves room (256 weights of up to 2^15 and V of up
-    // to 2^100 have 2^4 of it to 2^127): their loads then pass under the first granules' (3
-    // requests of 15 nodes: 10.8 us, 11.2 behind).  Heads of 128 would pay with registers (32
-    // requests, one node: 44.2, 43.6 behind).
-    const bool nodes_first = HD == 64 && kv.v_unit >= 0.0625f;
-#pragma unroll(HD == 64 ? 1 : 2)
+    // the range (2^100 at a unit of 2^-60); in values the prefix's sum is far below it.  Where
+    // the unit leaves room (256 weights of up to 2^15 and V of up to 2^100 have 2^4 of it to
+    // 2^127) the nodes come first, so that their loads pass under the first granules' (3
+    // requests of 15 nodes, heads of 64: 10.8 us, 11.2 behind; 32 requests of four nodes, heads
+    // of 128: 54.4, 55.6 behind).  Heads of 128 in one tile of rows would pay for it with
+    // registers (32 requests, one node: 44.2, 43.4 behind).
+    constexpr bool kBoth = HD == 64 || NR == 2;
+    const bool nodes_first = kBoth && kv.v_unit >= 0.0625f;
+#pragma unroll(kBoth ? 1 : 2)
     for (int turn = 0; turn < 2; ++turn) {
       if (nodes_first == (turn == 0)) {
         if (x1 <= NG) continue;

@@ -999,8 +999,8 @@ cudaError_t launch_tc(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_k
 
 // Up to 32 query rows per KV head the granule kernel's one or two tiles of 16 rows cost less,
 // beyond them it would read the cache once more for every 16.  32 heads on 8, us, granule
-// kernel / this one: 32 requests of 512 .. 8192 keys with 16, 32, 48 rows 55 / 105, 98 / 106,
-// 141 / 108; one request of 32768 keys 25 / 35, 33 / 35, 41 / 36.
+// kernel / this one: 32 requests of 512 .. 8192 keys with 16, 32, 48 rows 55 / 105, 97 / 106,
+// 139 / 108; one request of 32768 keys 25 / 35, 33 / 35, 41 / 36.
 bool verify4_uses_tc(int R, int H, int KVH, int hd) { return hd == kHD && H / KVH * R > 32; }
 
 size_t verify4_tc_workspace_bytes(int B, int R, int H, int KVH, int max_kv_len) {
