@@ -76,7 +76,7 @@ def check_attn(d, O, lse, scale, skip=(), node=2.0 ** -8):
             assert np.all(bad <= 0), (b, i, bad.max(), np.abs(o[i]).max())
 
 
-SIDES = [(5, 4, 128), (40, 4, 128), (70, 4, 128), (5, 4, 64), (40, 4, 64)]  # R, query heads per KV head, head_dim
+SIDES = [(5, 1, 128), (5, 4, 128), (40, 4, 128), (70, 4, 128), (5, 1, 64), (5, 4, 64), (40, 4, 64)]  # R, query heads per KV head, head_dim
 
 
 @pytest.mark.parametrize("R,G,hd", SIDES)
