@@ -4,30 +4,10 @@
 #include <math.h>
 #include <string.h>
 
-#include "e3_common.cuh"
+#include "capi_checks.cuh"
 #include "e3_kernels.h"
 
 namespace e3 {
-
-static e3_status check_kv16(const e3_kv_layer* kv, const char* fn, const char* what) {
-  E3_REQUIRE(kv != nullptr, E3_ERR_INVALID_ARG, "%s: null %s descriptor", fn, what);
-  E3_REQUIRE(kv->k && kv->v && kv->page_table, E3_ERR_INVALID_ARG, "%s: null %s k/v/page_table", fn, what);
-  E3_REQUIRE(kv->dt == E3_F32 || kv->dt == E3_BF16, E3_ERR_INVALID_ARG, "%s: bad %s dtype %d", fn, what,
-             static_cast<int>(kv->dt));
-  E3_REQUIRE(kv->n_pages > 0 && kv->max_pages > 0 && kv->n_kv_heads > 0, E3_ERR_SHAPE,
-             "%s: %s n_pages, max_pages, n_kv_heads must be positive", fn, what);
-  E3_REQUIRE(kv->page_size > 0 && kv->page_size % 16 == 0, E3_ERR_SHAPE, "%s: %s page_size %d not a multiple of 16", fn,
-             what, kv->page_size);
-  E3_REQUIRE(kv->head_dim >= 32 && kv->head_dim <= 256 && kv->head_dim % 32 == 0, E3_ERR_SHAPE,
-             "%s: %s head_dim %d must be a multiple of 32 in [32, 256]", fn, what, kv->head_dim);
-  E3_REQUIRE(aligned16(kv->k) && aligned16(kv->v), E3_ERR_INVALID_ARG, "%s: %s k/v not 16-byte aligned", fn, what);
-  E3_REQUIRE((kv->flags & ~(E3_KV_PREFIX_STABLE | E3_KV_SELFTEST_STALL)) == 0, E3_ERR_INVALID_ARG,
-             "%s: unknown %s flags %#x", fn, what, kv->flags);
-  return E3_OK;
-}
-
-// (a pointer off its elements' grid would fault in the paths for rows off the 16-byte grid)
-static bool on_grid(const void* p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 static bool power_of_two(float u) {
   int ex = 0;
@@ -144,11 +124,7 @@ E3_API e3_status kv4_read(const e3_kv4_layer* layers, const e3_kv_layer* dst, in
 }
 
 E3_API size_t eagle3_verify4_workspace_bytes(int B, int R, int n_q_heads, int n_kv_heads, int head_dim, int max_kv_len) {
-  // (the bounds of the call itself)
-  if (B < 1 || B > 65535 || R < 1 || R > E3_MAX_NODES + 1 || n_q_heads < 1 || n_q_heads > 65535 || n_kv_heads < 1 ||
-      n_q_heads % n_kv_heads != 0 || static_cast<long long>(B) * R * n_q_heads >= (1ll << 31) ||
-      (head_dim != 64 && head_dim != 128) || max_kv_len < 0 || max_kv_len > (1 << 30))
-    return 0;
+  if (!verify_quant_sizes_ok(B, R, n_q_heads, n_kv_heads, head_dim, max_kv_len)) return 0;
   return verify4_workspace_bytes(B, R, n_q_heads, n_kv_heads, head_dim, max_kv_len);
 }
 
@@ -159,23 +135,8 @@ E3_API e3_status tree_verify_attn4(const void* Q, const e3_kv4_layer* kv, const 
   clear_error();
   const char* fn = "tree_verify_attn4";
   e3_status st = check_kv4(kv, fn);
-  if (st == E3_OK) st = check_kv16(tail, fn, "tail");
+  if (st == E3_OK) st = check_verify_quant(fn, Q, kv, tail, kv_len, mask, B, R, n_q_heads, max_kv_len, sm_scale, O, lse, ws);
   if (st != E3_OK) return st;
-  E3_REQUIRE(Q && kv_len && mask && O && lse && ws, E3_ERR_INVALID_ARG, "%s: null pointer", fn);
-  E3_REQUIRE(tail->dt == E3_BF16, E3_ERR_UNSUPPORTED, "%s: the tail must be bf16", fn);
-  E3_REQUIRE(tail->n_kv_heads == kv->n_kv_heads && tail->head_dim == kv->head_dim, E3_ERR_SHAPE,
-             "%s: heads or head_dim of cache and tail differ", fn);
-  E3_REQUIRE(B >= 1 && B <= 65535 && R >= 1 && R <= E3_MAX_NODES + 1, E3_ERR_SHAPE, "%s: B=%d R=%d", fn, B, R);
-  E3_REQUIRE(n_q_heads >= 1 && n_q_heads <= 65535 && n_q_heads % kv->n_kv_heads == 0, E3_ERR_SHAPE,
-             "%s: n_q_heads %d not a multiple of n_kv_heads %d", fn, n_q_heads, kv->n_kv_heads);
-  E3_REQUIRE(static_cast<long long>(B) * R * n_q_heads < (1ll << 31), E3_ERR_SHAPE, "%s: B*R*n_q_heads too large", fn);
-  E3_REQUIRE(max_kv_len >= 0 && max_kv_len <= (1 << 30), E3_ERR_SHAPE, "%s: max_kv_len=%d", fn, max_kv_len);
-  E3_REQUIRE(max_kv_len <= static_cast<long long>(kv->max_pages) * kv->page_size, E3_ERR_CAPACITY,
-             "%s: max_kv_len %d exceeds the pages", fn, max_kv_len);
-  E3_REQUIRE(R <= static_cast<long long>(tail->max_pages) * tail->page_size, E3_ERR_CAPACITY,
-             "%s: tail pages do not hold R=%d slots", fn, R);
-  E3_REQUIRE(sm_scale > 0.0f && sm_scale < 1e30f, E3_ERR_INVALID_ARG, "%s: sm_scale must be > 0", fn);
-  E3_REQUIRE(aligned16(Q) && aligned16(O) && aligned16(ws), E3_ERR_INVALID_ARG, "%s: Q, O, ws must be 16-byte aligned", fn);
   return launch_verify4(Q, *kv, *tail, kv_len, mask, B, R, n_q_heads, max_kv_len, sm_scale, O, lse, dev_err, ws, ws_bytes,
                         reinterpret_cast<cudaStream_t>(stream));
 }

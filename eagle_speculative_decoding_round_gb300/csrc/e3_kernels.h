@@ -23,6 +23,12 @@ struct Kv4Layers {
   float v_unit[E3_MAX_LAYERS];
 };
 
+// Per-layer pointers of an 8-bit cache (kernel parameter).
+struct Kv8Layers {
+  void* c[2][E3_MAX_LAYERS];  // codes of K, of V
+  int8_t* e[2][E3_MAX_LAYERS];
+};
+
 e3_status launch_expand(const float* logits, int B, int F, int V, int k, int W, float inv_temp,
                         const float* parent_score, const int32_t* parent_id, int depth, int cand_offset,
                         const e3_cand& c, int32_t* next_id, float* next_score, bool sampled, uint64_t seed,
@@ -104,6 +110,17 @@ size_t verify4_tc_workspace_bytes(int B, int R, int H, int KVH, int max_kv_len);
 e3_status launch_verify4_tc(const void* Q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
                             const uint64_t* mask, int B, int R, int H, int max_kv_len, float sm_scale, void* O, float* lse,
                             int32_t* dev_err, void* ws, cudaStream_t s);
+e3_status launch_kv8_append(const Kv8Layers& l8, const e3_kv8_layer& geo, const CompactLayers& src,
+                            const e3_kv_layer& sgeo, int L, int B, int max_rows, const int32_t* rows,
+                            const int32_t* n_rows, int n_add, const int32_t* kv_len, int32_t* kv_len_next,
+                            int32_t* dev_err, cudaStream_t s);
+e3_status launch_kv8_read(const Kv8Layers& l8, const e3_kv8_layer& geo, const CompactLayers& dst,
+                          const e3_kv_layer& dgeo, int L, int B, int max_rows, const int32_t* first,
+                          const int32_t* n_rows, int32_t* dev_err, cudaStream_t s);
+size_t verify8_workspace_bytes(int B, int R, int H, int KVH, int hd, int max_kv_len);
+e3_status launch_verify8(const void* Q, const e3_kv8_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
+                         const uint64_t* mask, int B, int R, int H, int max_kv_len, float sm_scale, void* O, float* lse,
+                         int32_t* dev_err, void* ws, size_t ws_bytes, cudaStream_t s);
 e3_status launch_logits_process(const float* logits, int B, int R, int V, const float* temp, const uint16_t* counts,
                                 const int32_t* tok, const int32_t* parent, const float* pen, const int32_t* bias_tok,
                                 const float* bias_val, int n_bias, const uint32_t* allow, const int32_t* allow_row,

@@ -18,29 +18,13 @@
 
 #include "e3_common.cuh"
 #include "e3_kernels.h"
+#include "kv_rows.cuh"
 
 namespace e3 {
 
 namespace {
 
 constexpr int kThreads = 128;
-
-// index of (page, head 0, slot) of logical slot t in rows, or -1
-__device__ __forceinline__ long long slot_row(const int32_t* table, int max_pages, int n_pages, int page_size, int KVH,
-                                              int b, int t) {
-  if (t < 0) return -1;
-  const int pi = t / page_size;
-  if (pi >= max_pages) return -1;
-  const int page = table[static_cast<size_t>(b) * max_pages + pi];
-  if (page < 0 || page >= n_pages) return -1;
-  return static_cast<long long>(page) * KVH * page_size + (t - pi * page_size);
-}
-
-// Rows request b appends, or -1 if they do not fit.
-__device__ __forceinline__ int append_count(long long n, int max_rows, long long P, long long cap) {
-  if (n <= 0) return 0;
-  return (n > max_rows || P < 0 || P + n > cap || P + n > 0x7FFFFFFFll) ? -1 : static_cast<int>(n);
-}
 
 // One group of 16 bf16 values -> 8 bytes of codes, the scale byte.  `unit` is a power
 // of two, so e * unit and 6 * unit are exact.  A quotient x / (e unit) lies either
@@ -170,15 +154,6 @@ kv4_append_kernel(const __grid_constant__ Kv4Layers L4, e3_kv4_layer geo, const 
   if (bad) dev_flag(dev_err, E3_DEV_ERR_NONFINITE);
 }
 
-// kv_len in place: after every CTA of the append has read it
-__global__ void kv4_len_kernel(int B, int max_rows, const int32_t* __restrict__ n_rows, int n_add, long long cap,
-                               int32_t* kv_len) {
-  pdl_wait();
-  pdl_trigger();
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
-  if (b < B) kv_len[b] += max(append_count(static_cast<long long>(n_rows[b]) + n_add, max_rows, kv_len[b], cap), 0);
-}
-
 __device__ __forceinline__ void dequantize16(uint2 c, uint8_t e, float unit, uint4* out) {
   const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(e, __NV_E4M3))) * unit;
   uint32_t o[8];
@@ -189,17 +164,7 @@ __device__ __forceinline__ void dequantize16(uint2 c, uint8_t e, float unit, uin
     const float2 f = __half22float2(h);
     o[i] = pack2_bf16(f.x * s, f.y * s);
   }
-  // Two neighbouring threads' groups are 64 bytes in a row: they swap the second piece of
-  // the first for the first of the second, so that each store fills whole sectors
-  const bool odd = threadIdx.x & 1;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t x = __shfl_xor_sync(3u << (threadIdx.x & 30), odd ? o[i] : o[4 + i], 1);
-    if (odd) o[i] = x; else o[4 + i] = x;
-  }
-  out -= odd ? 1 : 0;  // even: pieces 0 and 2 of the 64 bytes, odd: 1 and 3
-  out[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  out[2] = make_uint4(o[4], o[5], o[6], o[7]);
+  store_pair(o, out);
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -269,9 +234,9 @@ e3_status launch_kv4_append(const Kv4Layers& l4, const e3_kv4_layer& geo, const 
                              n_rows, n_add, kv_len, in_place ? nullptr : kv_len_next, dev_err);
   if (e != cudaSuccess) return cuda_status(e, "kv4_append_kernel");
   if (in_place) {
-    e = launch_pdl(kv4_len_kernel, dim3((B + 255) / 256), dim3(256), 0, s, 1, B, max_rows, n_rows, n_add,
+    e = launch_pdl(kv_len_add_kernel, dim3((B + 255) / 256), dim3(256), 0, s, 1, B, max_rows, n_rows, n_add,
                    static_cast<long long>(geo.max_pages) * geo.page_size, kv_len_next);
-    if (e != cudaSuccess) return cuda_status(e, "kv4_len_kernel");
+    if (e != cudaSuccess) return cuda_status(e, "kv_len_add_kernel");
   }
   return E3_OK;
 }

@@ -220,7 +220,7 @@ struct Parts {
   // keys of tile x that exist (more than 128 where it is not the last of its kind)
   __device__ __forceinline__ int left(const V4Geom& g, int x) const { return x >= NT ? g.R - (x - NT) * kKeys : P - x * kKeys; }
   // the next part; false at the end of the share
-  __device__ __forceinline__ bool next(const V4Geom& g, const e3_kv4_layer& kv, const int32_t* kv_len) {
+  __device__ __forceinline__ bool next(const V4Geom& g, const int32_t* kv_len) {
     todo -= w1 - x0;
     if (todo <= 0) return false;
     x0 = 0;
@@ -228,7 +228,7 @@ struct Parts {
       pq = 0;
       for (++b; b < g.B; ++b) {
         P = kv_len[b];
-        real = pair_units<kKeys>(g, kv, P);
+        real = pair_units<kKeys>(g, P);
         if (real > 0) break;
       }
       if (b >= g.B) return false;
@@ -369,21 +369,21 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   pdl_wait();
   if (cta == 0)  // requests whose length is out of bounds
     for (int b = threadIdx.x; b < g.B; b += kThreads)
-      if (pair_units<kKeys>(g, kv, kv_len[b]) == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
-  const V4Place at = find_place<kKeys>(g, kv, kv_len, cta);
+      if (pair_units<kKeys>(g, kv_len[b]) == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+  const V4Place at = find_place<kKeys>(g, kv_len, cta);
   bool work = at.b < g.B;
   Parts first{};
   if (work) {
     first.b = at.b;
     first.P = kv_len[at.b];
     first.todo = at.share;
-    first.real = pair_units<kKeys>(g, kv, first.P);
+    first.real = pair_units<kKeys>(g, first.P);
     first.extra = at.extra;
     const long long off = at.share * cta - at.before;
     first.pq = static_cast<int>(off / (first.real + at.extra));
     first.x0 = static_cast<int>(off - static_cast<long long>(first.pq) * (first.real + at.extra));
     first.take();
-    if (first.x1 <= first.x0) work = first.next(g, kv, kv_len);
+    if (first.x1 <= first.x0) work = first.next(g, kv_len);
   }
   fence_before();
   __syncthreads();
@@ -449,7 +449,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
             par ^= 1u;
           }
         }
-      } while (live && p.next(g, kv, kv_len));
+      } while (live && p.next(g, kv_len));
     }
     // One issuing thread per softmax group: neither group's products wait behind the other
     // group's barriers.
@@ -511,7 +511,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           umma_commit(&o_done[w]);
           umma_commit(&v_empty[st]);
         }
-      } while (live && p.next(g, kv, kv_len));
+      } while (live && p.next(g, kv_len));
     }
   } else if (warp >= kDeq0) {
     regs_dec<kRegsDeq>();
@@ -595,7 +595,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           raw_par ^= 1u;
         }
         if (++x == p.x1) {
-          if (!p.next(g, kv, kv_len)) break;
+          if (!p.next(g, kv_len)) break;
           x = p.x0;
         }
       }
@@ -841,7 +841,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
           if (p.x1 == p.real) e[1] = cta;
         }
         ++n_part;
-      } while (p.next(g, kv, kv_len));
+      } while (p.next(g, kv_len));
     }
   }
   fence_before();
@@ -872,7 +872,7 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
 // NQ = 1 21.3 and 314, NQ = 2 24.7 and 296.
 template <int RT, int NQ>
 __global__ void __launch_bounds__(256 / NQ)
-verify4_tc_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* __restrict__ kv_len,
+verify4_tc_merge_kernel(const int32_t* __restrict__ kv_len,
                         const __grid_constant__ V4Geom g, const float* __restrict__ ws_o, const float2* __restrict__ ws_ml,
                         const int32_t* __restrict__ ends, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
   constexpr int ROWS = RT * kRows, SPLIT = RT == 1 ? 2 : 1, AHEAD = 8 / NQ;
@@ -888,7 +888,7 @@ verify4_tc_merge_kernel(const __grid_constant__ e3_kv4_layer kv, const int32_t* 
   pdl_trigger();
   const int c0 = ends[2 * pair], c1 = ends[2 * pair + 1];
   // (a worker that gave up, its error word set, may not have left its number)
-  if (pair_units<kKeys>(g, kv, kv_len[b]) == 0 || c0 < 0 || c1 < c0 || c1 >= g.workers) return;
+  if (pair_units<kKeys>(g, kv_len[b]) == 0 || c0 < 0 || c1 < c0 || c1 >= g.workers) return;
   const int n = ok ? (c1 - c0 + 1) * SPLIT : 0;
   const size_t rec = (pair + c0) * SPLIT;
   const float2* ml = ws_ml + rec * ROWS + (r - rt * ROWS);
@@ -991,8 +991,8 @@ cudaError_t launch_tc(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_k
   const float2* cml = ws_ml;
   const int32_t* ce = ends;
   if (blocks > 4u * g.workers)
-    return launch_pdl(verify4_tc_merge_kernel<RT, 2>, dim3(blocks), dim3(128), 0, s, 1, kv, kv_len, g, co, cml, ce, o, lse);
-  return launch_pdl(verify4_tc_merge_kernel<RT, 1>, dim3(blocks), dim3(256), 0, s, 1, kv, kv_len, g, co, cml, ce, o, lse);
+    return launch_pdl(verify4_tc_merge_kernel<RT, 2>, dim3(blocks), dim3(128), 0, s, 1, kv_len, g, co, cml, ce, o, lse);
+  return launch_pdl(verify4_tc_merge_kernel<RT, 1>, dim3(blocks), dim3(256), 0, s, 1, kv_len, g, co, cml, ce, o, lse);
 }
 
 }  // namespace
@@ -1012,7 +1012,8 @@ size_t verify4_tc_workspace_bytes(int B, int R, int H, int KVH, int max_kv_len) 
 e3_status launch_verify4_tc(const void* Q, const e3_kv4_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
                             const uint64_t* mask, int B, int R, int H, int max_kv_len, float sm_scale, void* O, float* lse,
                             int32_t* dev_err, void* ws, cudaStream_t s) {
-  const V4Geom g = make_geom_tc(B, R, H, kv.n_kv_heads, max_kv_len);
+  V4Geom g = make_geom_tc(B, R, H, kv.n_kv_heads, max_kv_len);
+  g.cap = static_cast<long long>(kv.max_pages) * kv.page_size;
   float* ws_o = static_cast<float*>(ws);
   float2* ws_ml = reinterpret_cast<float2*>(ws_o + record_rows(g) * kHD);
   int32_t* ends = reinterpret_cast<int32_t*>(ws_ml + record_rows(g));

@@ -1,4 +1,4 @@
-// verify4.cuh -- what the kernels of tree_verify_attn4 share: how the work is cut.
+// verify4.cuh -- what the kernels of tree_verify_attn4 and tree_verify_attn8 share: how the work is cut.
 #pragma once
 #include <math.h>
 
@@ -37,12 +37,13 @@ struct V4Geom {
   int extra;  // units that a pair counts beyond its own, for what a part costs by itself,
   int extra_from;  // where shares are of this many units or more
   int max_kv_len;
+  long long cap;  // slots that a request's pages hold
 };
 
 // Units of request b's pairs, 0 if its length is out of bounds.
 template <int KEYS>
-__device__ __forceinline__ int pair_units(const V4Geom& g, const e3_kv4_layer& kv, int P) {
-  if (P < 0 || P > g.max_kv_len || P > static_cast<long long>(kv.max_pages) * kv.page_size) return 0;
+__device__ __forceinline__ int pair_units(const V4Geom& g, int P) {
+  if (P < 0 || P > g.max_kv_len || P > g.cap) return 0;
   return (P + KEYS - 1) / KEYS + (g.R + KEYS - 1) / KEYS;
 }
 
@@ -54,13 +55,13 @@ struct V4Place {
   int extra;                // a pair's further units: none where shares are small
 };
 template <int KEYS>
-__device__ __forceinline__ V4Place find_place(const V4Geom& g, const e3_kv4_layer& kv, const int32_t* kv_len, int worker) {
+__device__ __forceinline__ V4Place find_place(const V4Geom& g, const int32_t* kv_len, int worker) {
   const int lane = threadIdx.x & 31;
   const long long Q = static_cast<long long>(g.KVH) * g.RG;
   long long total = 0;
   int live = 0;
   for (int b0 = 0; b0 < g.B; b0 += 32) {
-    const int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv, kv_len[b0 + lane]) : 0;
+    const int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv_len[b0 + lane]) : 0;
     total += __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(u));
     live += __popc(__ballot_sync(0xFFFFFFFFu, u > 0));
   }
@@ -73,7 +74,7 @@ __device__ __forceinline__ V4Place find_place(const V4Geom& g, const e3_kv4_laye
   f.b = g.B;
   f.before = total * Q;
   for (int b0 = 0; b0 < g.B; b0 += 32) {
-    int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv, kv_len[b0 + lane]) : 0;
+    int u = b0 + lane < g.B ? pair_units<KEYS>(g, kv_len[b0 + lane]) : 0;
     if (u > 0) u += f.extra;
     unsigned incl = static_cast<unsigned>(u);
 #pragma unroll

@@ -27,7 +27,8 @@ SYMBOLS = ["eagle3_fuse", "eagle3_fuse_workspace_bytes", "eagle3_fuse_noalloc",
            "tree_verify_attn", "eagle3_verify_workspace_bytes", "lmhead_logits", "spec_accept",
            "spec_accept_sampled", "kv_compact", "eagle3_draft_step", "eagle3_draft_workspace_bytes",
            "eagle3_rope_init", "tree_qkv_append", "kv4_append", "kv4_read", "tree_verify_attn4",
-           "eagle3_verify4_workspace_bytes", "tree_logits_process", "token_counts_add",
+           "eagle3_verify4_workspace_bytes", "kv8_append", "kv8_read", "tree_verify_attn8",
+           "eagle3_verify8_workspace_bytes", "tree_logits_process", "token_counts_add",
            "eagle3_budget_init", "eagle3_budget_update", "eagle3_last_error",
            "eagle3_abi_version", "eagle3_launch_count"]
 MAX_BUDGET_LEVELS = 16
@@ -65,6 +66,13 @@ class e3_kv4_layer(ctypes.Structure):
                 ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
                 ("head_dim", ctypes.c_int), ("k_unit", ctypes.c_float), ("v_unit", ctypes.c_float),
                 ("flags", ctypes.c_int)]
+
+
+class e3_kv8_layer(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("n_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("block", ctypes.c_int), ("flags", ctypes.c_int)]
 
 
 class e3_rope_spec(ctypes.Structure):
@@ -132,6 +140,11 @@ def _load() -> ctypes.CDLL:
         "tree_verify_attn4": (I, [P, ctypes.POINTER(e3_kv4_layer), ctypes.POINTER(e3_kv_layer), P, P, I, I, I, I, F, P, P,
                                   P, P, S, P]),
         "eagle3_verify4_workspace_bytes": (S, [I, I, I, I, I, I]),
+        "kv8_append": (I, [ctypes.POINTER(e3_kv8_layer), ctypes.POINTER(e3_kv_layer), I, I, I, P, P, I, P, P, P, P]),
+        "kv8_read": (I, [ctypes.POINTER(e3_kv8_layer), ctypes.POINTER(e3_kv_layer), I, I, I, P, P, P, P]),
+        "tree_verify_attn8": (I, [P, ctypes.POINTER(e3_kv8_layer), ctypes.POINTER(e3_kv_layer), P, P, I, I, I, I, F, P, P,
+                                  P, P, S, P]),
+        "eagle3_verify8_workspace_bytes": (S, [I, I, I, I, I, I]),
         "tree_logits_process": (I, [P, I, I, I, P, P, P, P, P, P, P, I, P, P, I, P, P, P, P, P, P]),
         "token_counts_add": (I, [P, I, I, P, P, I, I, I, P]),
         "eagle3_budget_init": (I, [ctypes.POINTER(e3_budget_policy), P, I]),
@@ -207,6 +220,12 @@ def make_kv4_layer(k, v, k_scale, v_scale, page_table, n_pages, page_size, max_p
                    v_unit=1.0, flags=0) -> e3_kv4_layer:
     return e3_kv4_layer(ptr(k), ptr(v), ptr(k_scale), ptr(v_scale), ptr(page_table), n_pages, page_size, max_pages,
                         n_kv_heads, head_dim, k_unit, v_unit, flags)
+
+
+def make_kv8_layer(k, v, k_exp, v_exp, page_table, n_pages, page_size, max_pages, n_kv_heads, head_dim, block,
+                   flags=0) -> e3_kv8_layer:
+    return e3_kv8_layer(ptr(k), ptr(v), ptr(k_exp), ptr(v_exp), ptr(page_table), n_pages, page_size, max_pages,
+                        n_kv_heads, head_dim, block, flags)
 
 
 def abi_version() -> int:
@@ -323,16 +342,15 @@ def tree_qkv_append(qkv, ld, B, R, n_rows, n_q_heads, q_norm, k_norm, eps, rope:
                                 ptr(kv_len), ptr(dev_err), _stream(stream)))
 
 
-def _layer_arrays(fn, layers, others):
+def _layer_arrays(fn, layers, others, kind=e3_kv4_layer):
     if len(layers) != len(others):
-        raise ValueError(f"{fn}: {len(layers)} 4-bit layers and {len(others)} 16-bit ones")
+        raise ValueError(f"{fn}: {len(layers)} quantized layers and {len(others)} 16-bit ones")
     # one copy of the descriptors' bytes (filling a ctypes array element by element takes longer than the launch)
-    a4, a16 = b"".join(layers), b"".join(others)
+    a, a16 = b"".join(layers), b"".join(others)
     n = len(layers)
-    # (their sizes differ, so a descriptor of the other kind shows in the sum)
-    if len(a4) != n * ctypes.sizeof(e3_kv4_layer) or len(a16) != n * ctypes.sizeof(e3_kv_layer):
-        raise TypeError(f"{fn}: e3_kv4_layer and e3_kv_layer descriptors wanted")
-    return (e3_kv4_layer * n).from_buffer_copy(a4), (e3_kv_layer * n).from_buffer_copy(a16)
+    if n and ({*map(type, layers)} != {kind} or {*map(type, others)} != {e3_kv_layer}):
+        raise TypeError(f"{fn}: {kind.__name__} and e3_kv_layer descriptors wanted")
+    return (kind * n).from_buffer_copy(a), (e3_kv_layer * n).from_buffer_copy(a16)
 
 
 def kv4_append(layers, src, B, max_rows, rows, n_rows, n_add, kv_len, kv_len_next, dev_err=None, stream=None):
@@ -357,6 +375,32 @@ def tree_verify_attn4(Q, kv: e3_kv4_layer, tail: e3_kv_layer, kv_len, mask, B, R
                       lse, dev_err=None, ws=None, ws_bytes=0, stream=None):
     _check("tree_verify_attn4",
            _lib.tree_verify_attn4(ptr(Q), ctypes.byref(kv), ctypes.byref(tail), ptr(kv_len), ptr(mask), B, R, n_q_heads,
+                                  max_kv_len, sm_scale, ptr(O), ptr(lse), ptr(dev_err), ptr(ws), ws_bytes,
+                                  _stream(stream)))
+
+
+def kv8_append(layers, src, B, max_rows, rows, n_rows, n_add, kv_len, kv_len_next, dev_err=None, stream=None):
+    """layers/src: sequences of e3_kv8_layer / bf16 e3_kv_layer, one per layer."""
+    a8, a16 = _layer_arrays("kv8_append", layers, src, e3_kv8_layer)
+    _check("kv8_append", _lib.kv8_append(a8, a16, len(a8), B, max_rows, ptr(rows), ptr(n_rows), n_add, ptr(kv_len),
+                                         ptr(kv_len_next), ptr(dev_err), _stream(stream)))
+
+
+def kv8_read(layers, dst, B, max_rows, first, n_rows, dev_err=None, stream=None):
+    """layers/dst: sequences of e3_kv8_layer / bf16 e3_kv_layer, one per layer."""
+    a8, a16 = _layer_arrays("kv8_read", layers, dst, e3_kv8_layer)
+    _check("kv8_read", _lib.kv8_read(a8, a16, len(a8), B, max_rows, ptr(first), ptr(n_rows), ptr(dev_err),
+                                     _stream(stream)))
+
+
+def eagle3_verify8_workspace_bytes(B, R, n_q_heads, n_kv_heads, head_dim, max_kv_len) -> int:
+    return int(_lib.eagle3_verify8_workspace_bytes(B, R, n_q_heads, n_kv_heads, head_dim, max_kv_len))
+
+
+def tree_verify_attn8(Q, kv: e3_kv8_layer, tail: e3_kv_layer, kv_len, mask, B, R, n_q_heads, max_kv_len, sm_scale, O,
+                      lse, dev_err=None, ws=None, ws_bytes=0, stream=None):
+    _check("tree_verify_attn8",
+           _lib.tree_verify_attn8(ptr(Q), ctypes.byref(kv), ctypes.byref(tail), ptr(kv_len), ptr(mask), B, R, n_q_heads,
                                   max_kv_len, sm_scale, ptr(O), ptr(lse), ptr(dev_err), ptr(ws), ws_bytes,
                                   _stream(stream)))
 

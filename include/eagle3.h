@@ -541,6 +541,86 @@ E3_API e3_status tree_verify_attn4(const void* Q, const e3_kv4_layer* kv /* host
 E3_API size_t eagle3_verify4_workspace_bytes(int B, int R, int n_q_heads, int n_kv_heads, int head_dim,
                                              int max_kv_len);
 
+/* One layer's paged KV cache held in 8 bits.  Each block of `block` consecutive tokens
+ * of a KV head shares one exponent e in [-100, 120] and holds fp8 codes c (e4m3: 0,
+ * +-2^-9 .. +-448); the value is c * 2^e, exact in bf16.  The scale is a power of two so
+ * that rows already in a block can follow when its scale grows (kv8_append), losing bits
+ * only where a code falls into e4m3's subnormal range.
+ * k, v: [n_pages][n_kv_heads][page_size][head_dim] bytes; k_exp, v_exp: [n_pages]
+ *   [n_kv_heads][page_size / block] int8.  Slots as in e3_kv_layer; block j of a page
+ *   holds its slots j*block .. (j+1)*block - 1. */
+typedef struct {
+  void* k;
+  void* v;
+  int8_t* k_exp;
+  int8_t* v_exp;
+  const int32_t* page_table; /* [B][max_pages], device */
+  int n_pages;
+  int page_size;             /* a multiple of block */
+  int max_pages;
+  int n_kv_heads;
+  int head_dim;              /* 64 or 128 */
+  int block;                 /* 16, 32, 64 or 128 */
+  int flags;                 /* 0 or E3_KV_PREFIX_STABLE (not used) */
+} e3_kv8_layer;
+
+/* ---------------------------------------------------------------------------
+ * kv8_append: rows of a bf16 cache to the end of the 8-bit cache, all layers -- the
+ * commit of a round whose tree K/V live in a bf16 tail, or of a prompt (kv4_append's
+ * counterpart; arguments, rows and lengths as there).
+ * Request b appends n = n_rows[b] + n_add rows (n <= 0: none): row j < n is logical
+ * slot rows[b*max_rows + j] of src (rows NULL: slot j) and goes to logical slot
+ * kv_len[b] + j of the 8-bit cache; kv_len_next[b] = kv_len[b] + max(n, 0)
+ * (kv_len_next NULL: not written; it may be kv_len itself).
+ * A block that receives rows gets  e = max(e of its rows that are there already, the
+ *   smallest e with max|x| <= 448 * 2^e over the new rows x), within [-100, 120] (-100
+ *   where all are 0); what the exponent of a block without rows was before does not
+ *   matter.  New rows are stored as the nearest e4m3 value to x / 2^e, rows that were
+ *   there as the nearest to their value / 2^e (exact but for subnormal codes); ties to
+ *   the even code.  Slots behind the last row are left as they were.
+ * NaN is stored as 0 and magnitudes beyond 240 * 2^120 (bf16 holds up to 255 * 2^120)
+ *   as that; NaN and +-Inf set E3_DEV_ERR_NONFINITE.
+ * n > max_rows, or rows beyond the 8-bit cache's pages, set E3_DEV_ERR_CAPACITY and
+ * leave the request as it was (its length too); a page id out of range sets it and
+ * skips the row (src) or the rows of that page (the 8-bit cache).
+ * layers, src: host arrays of L descriptors of one geometry each; src bf16.  The two
+ * caches must not overlap, and no block that receives rows belongs to two requests.
+ * Limits: 1 <= L <= E3_MAX_LAYERS, 1 <= B <= 65535, max_rows >= 1,
+ *   n_kv_heads * max_rows * head_dim / 16 < 2^31, n_add 0 or 1.
+ * ------------------------------------------------------------------------- */
+E3_API e3_status kv8_append(const e3_kv8_layer* layers, const e3_kv_layer* src, int L, int B, int max_rows,
+                            const int32_t* rows, const int32_t* n_rows, int n_add, const int32_t* kv_len,
+                            int32_t* kv_len_next, int32_t* dev_err, e3_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * kv8_read: the inverse: logical slots first[b] .. first[b] + n_rows[b] - 1 of the 8-bit
+ * cache (first NULL: 0) to logical slots 0 .. n_rows[b] - 1 of dst (bf16), all layers; the
+ * values are exact.  n_rows[b] > max_rows, or slots that the 8-bit cache's pages do not
+ * hold, set E3_DEV_ERR_CAPACITY and leave the request as it was; a row on a page out of
+ * range (either side), or that dst's pages do not hold, sets it and skips that row.
+ * ------------------------------------------------------------------------- */
+E3_API e3_status kv8_read(const e3_kv8_layer* layers, const e3_kv_layer* dst, int L, int B, int max_rows,
+                          const int32_t* first, const int32_t* n_rows, int32_t* dev_err, e3_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * tree_verify_attn8: tree_verify_attn over a prefix held in 8 bits; arguments, tail,
+ * masks, rows without a key and errors as tree_verify_attn4.
+ * Arithmetic: products exact but for the weights, which are good to 2^-8, sums in fp32.
+ *   Values of V up to 2^100 in magnitude cannot overflow them.  Q's values below 2^-24 of
+ *   their row's largest lose bits, and so do weights below 2^-21 of their row's largest in
+ *   units of the largest V scale of the request: blocks whose V scale is 2^20 below it
+ *   count less exactly.
+ * Scratch: eagle3_verify8_workspace_bytes(...) bytes (0 for sizes that the call refuses),
+ *   16-byte aligned; calls that may overlap on the GPU need scratch of their own.
+ * ------------------------------------------------------------------------- */
+E3_API e3_status tree_verify_attn8(const void* Q, const e3_kv8_layer* kv /* host struct */,
+                                   const e3_kv_layer* tail /* host struct */, const int32_t* kv_len,
+                                   const uint64_t* mask, int B, int R, int n_q_heads, int max_kv_len, float sm_scale,
+                                   void* O, float* lse, int32_t* dev_err, void* ws, size_t ws_bytes,
+                                   e3_stream_t stream);
+E3_API size_t eagle3_verify8_workspace_bytes(int B, int R, int n_q_heads, int n_kv_heads, int head_dim,
+                                             int max_kv_len);
+
 /* ---------------------------------------------------------------------------
  * tree_logits_process: penalties, biases and grammar masks on the node logits, and
  * the statistics that spec_accept reads; between lmhead_logits and spec_accept.
