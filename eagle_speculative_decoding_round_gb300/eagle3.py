@@ -28,7 +28,7 @@ SYMBOLS = ["eagle3_fuse", "eagle3_fuse_workspace_bytes", "eagle3_fuse_noalloc",
            "spec_accept_sampled", "kv_compact", "eagle3_draft_step", "eagle3_draft_workspace_bytes",
            "eagle3_rope_init", "tree_qkv_append", "kv4_append", "kv4_read", "tree_verify_attn4",
            "eagle3_verify4_workspace_bytes", "kv8_append", "kv8_read", "tree_verify_attn8",
-           "eagle3_verify8_workspace_bytes", "tree_logits_process", "token_counts_add",
+           "eagle3_verify8_workspace_bytes", "prompt_attn", "eagle3_prompt_workspace_bytes", "tree_logits_process", "token_counts_add",
            "eagle3_budget_init", "eagle3_budget_update", "eagle3_last_error",
            "eagle3_abi_version", "eagle3_launch_count"]
 MAX_BUDGET_LEVELS = 16
@@ -145,6 +145,8 @@ def _load() -> ctypes.CDLL:
         "tree_verify_attn8": (I, [P, ctypes.POINTER(e3_kv8_layer), ctypes.POINTER(e3_kv_layer), P, P, I, I, I, I, F, P, P,
                                   P, P, S, P]),
         "eagle3_verify8_workspace_bytes": (S, [I, I, I, I, I, I]),
+        "prompt_attn": (I, [P, P, P, ctypes.POINTER(e3_kv_layer), P, I, I, I, I, I, F, P, P, P, P, S, P]),
+        "eagle3_prompt_workspace_bytes": (S, [I, I, I, I, I, I, I, I]),
         "tree_logits_process": (I, [P, I, I, I, P, P, P, P, P, P, P, I, P, P, I, P, P, P, P, P, P]),
         "token_counts_add": (I, [P, I, I, P, P, I, I, I, P]),
         "eagle3_budget_init": (I, [ctypes.POINTER(e3_budget_policy), P, I]),
@@ -403,6 +405,19 @@ def tree_verify_attn8(Q, kv: e3_kv8_layer, tail: e3_kv_layer, kv_len, mask, B, R
            _lib.tree_verify_attn8(ptr(Q), ctypes.byref(kv), ctypes.byref(tail), ptr(kv_len), ptr(mask), B, R, n_q_heads,
                                   max_kv_len, sm_scale, ptr(O), ptr(lse), ptr(dev_err), ptr(ws), ws_bytes,
                                   _stream(stream)))
+
+
+def eagle3_prompt_workspace_bytes(B, n_total, max_rows, n_q_heads, n_kv_heads, head_dim, max_kv_len, dt) -> int:
+    return int(_lib.eagle3_prompt_workspace_bytes(B, n_total, max_rows, n_q_heads, n_kv_heads, head_dim, max_kv_len, dt))
+
+
+def prompt_attn(Q, row_start, n_rows, kv: e3_kv_layer, kv_len, B, n_total, max_rows, n_q_heads, max_kv_len, sm_scale, O,
+                lse, dev_err=None, ws=None, ws_bytes=0, stream=None):
+    """row_start None: request b's rows begin at b * max_rows; n_rows None: max_rows each; kv_len None: whole prompts."""
+    _check("prompt_attn",
+           _lib.prompt_attn(ptr(Q), ptr(row_start), ptr(n_rows), ctypes.byref(kv), ptr(kv_len), B, n_total, max_rows,
+                            n_q_heads, max_kv_len, sm_scale, ptr(O), ptr(lse), ptr(dev_err), ptr(ws), ws_bytes,
+                            _stream(stream)))
 
 
 def tree_logits_process(logits, B, R, V, temp_per_row, counts, tok, parent, pen, bias_tok, bias_val, n_bias, allow,

@@ -622,6 +622,42 @@ E3_API size_t eagle3_verify8_workspace_bytes(int B, int R, int n_q_heads, int n_
                                              int max_kv_len);
 
 /* ---------------------------------------------------------------------------
+ * prompt_attn: causal attention of prompts over the paged cache -- how the prefix that a
+ * round verifies against comes about, layer by layer: tree_qkv_append puts a prompt's
+ * K and V into the cache, this call gives the layer's attention output.  Whole prompts
+ * (kv_len NULL or 0), or the next pieces of longer ones (kv_len keys are cached before
+ * them); sequences of different lengths in one call.
+ * Request b has n_rows[b] rows (n_rows NULL: max_rows), which are rows row_start[b] ..
+ * row_start[b] + n_rows[b] - 1 of Q, O and lse (row_start NULL: b*max_rows, the layout
+ * that tree_qkv_append writes).  Row r, query head h < n_q_heads, sees the cache's logical
+ * slots t = 0 .. kv_len[b] + r:
+ *   o = softmax(sm_scale * q . k_t) v_t,  lse = ln(sum exp(sm_scale * q . k_t)).
+ * The caller has written the rows' own K/V at logical slots kv_len[b] + r.  Query head h
+ * reads KV head h / (n_q_heads / n_kv_heads).
+ * Q: [n_total][n_q_heads][head_dim] dtype kv->dt; O: same shape and dtype; lse: [n_total]
+ * [n_q_heads] fp32.  Rows of Q, O and lse that belong to no request are left as they were.
+ * Slots that a row does not see have no effect on it, whatever they hold; a row that sees a
+ * NaN or an Inf in V gets NaN or Inf in o, in that dimension at least.
+ * n_rows[b] outside [0, max_rows], kv_len[b] outside [0, max_kv_len], rows outside
+ * [0, n_total), or slots beyond max_pages set E3_DEV_ERR_CAPACITY and leave the request's
+ * outputs unwritten; a page id out of range sets it and makes them unspecified.
+ * Arithmetic: bf16: products in bf16 with fp32 sums, weights good to 2^-9 and summed
+ *   before that rounding; fp32: fp32 throughout.
+ * Limits: head_dim 64 or 128 (fp32: any multiple of 32 up to 256); n_q_heads %
+ *   n_kv_heads == 0; page_size % 16 == 0; 1 <= B <= 65535; 1 <= max_rows;
+ *   1 <= n_total, n_total * n_q_heads < 2^31; max_kv_len + max_rows <= 2^30.  Q, O 16-byte
+ *   aligned; kv->flags 0 or E3_KV_PREFIX_STABLE (not used).
+ * ws: eagle3_prompt_workspace_bytes(...) bytes of device scratch (may be 0, ws then NULL),
+ *   16-byte aligned; calls that may overlap on the GPU need scratch of their own.
+ * ------------------------------------------------------------------------- */
+E3_API e3_status prompt_attn(const void* Q, const int32_t* row_start, const int32_t* n_rows,
+                             const e3_kv_layer* kv /* host struct */, const int32_t* kv_len, int B, int n_total,
+                             int max_rows, int n_q_heads, int max_kv_len, float sm_scale, void* O, float* lse,
+                             int32_t* dev_err, void* ws, size_t ws_bytes, e3_stream_t stream);
+E3_API size_t eagle3_prompt_workspace_bytes(int B, int n_total, int max_rows, int n_q_heads, int n_kv_heads,
+                                            int head_dim, int max_kv_len, e3_dtype dt);
+
+/* ---------------------------------------------------------------------------
  * tree_logits_process: penalties, biases and grammar masks on the node logits, and
  * the statistics that spec_accept reads; between lmhead_logits and spec_accept.
  * Row i of request b predicts the token after node i, so the tokens of its path
