@@ -26,16 +26,11 @@ struct SimtCfg {
 };
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 ld4(const __nv_bfloat16* p) {
-  const uint2 w = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                     __uint_as_float(w.y & 0xFFFF0000u));
-}
 
-template <typename T, int HD>
+template <int HD>
 __global__ void __launch_bounds__(256)
-prompt_simt_kernel(const T* __restrict__ Q, const __grid_constant__ e3_kv_layer kv, const __grid_constant__ PromptGeom g,
-                   float sm_scale, T* __restrict__ O, float* __restrict__ lse, int32_t* dev_err) {
+prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_layer kv, const __grid_constant__ PromptGeom g,
+                   float sm_scale, float* __restrict__ O, float* __restrict__ lse, int32_t* dev_err) {
   using C = SimtCfg<HD>;
   constexpr int ND = HD / 16;
   extern __shared__ __align__(16) float sm[];
@@ -62,7 +57,7 @@ prompt_simt_kernel(const T* __restrict__ Q, const __grid_constant__ e3_kv_layer 
       *reinterpret_cast<float4*>(sQ + r * C::PITCH + d) = x;
     }
     // 64 keys (or their values) from t0 on; zeros behind the last key that the tile sees
-    auto load_tile = [&](const T* base, int t0) {
+    auto load_tile = [&](const float* base, int t0) {
       for (int i = threadIdx.x; i < 64 * (HD / 4); i += 256) {
         const int r = i / (HD / 4), d = 4 * (i % (HD / 4)), t = t0 + r;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -88,7 +83,7 @@ prompt_simt_kernel(const T* __restrict__ Q, const __grid_constant__ e3_kv_layer 
     }
     for (int t0 = 0; t0 < keys; t0 += kKeys) {
       __syncthreads();
-      load_tile(static_cast<const T*>(kv.k), t0);
+      load_tile(static_cast<const float*>(kv.k), t0);
       __syncthreads();
       float s[4][4] = {};
 #pragma unroll 4
@@ -129,7 +124,7 @@ prompt_simt_kernel(const T* __restrict__ Q, const __grid_constant__ e3_kv_layer 
         }
       }
       __syncthreads();
-      load_tile(static_cast<const T*>(kv.v), t0);
+      load_tile(static_cast<const float*>(kv.v), t0);
       __syncthreads();
       // keys that every row of the tile sees, then those that only some do: a row must not meet
       // another's in 0 * Inf
@@ -156,7 +151,7 @@ prompt_simt_kernel(const T* __restrict__ Q, const __grid_constant__ e3_kv_layer 
         const int f = f0 + r, row = f / g.G, h = it.kvh * g.G + f - row * g.G;
         const size_t at = static_cast<size_t>(q.start + row) * g.H + h;
 #pragma unroll
-        for (int k = 0; k < ND; ++k) st_elem(O, at * HD + tx + 16 * k, o[i][k] / l[i]);
+        for (int k = 0; k < ND; ++k) O[at * HD + tx + 16 * k] = o[i][k] / l[i];
         if (tx == 0) lse[at] = m[i] + logf(l[i]);
       }
     }
@@ -164,17 +159,17 @@ prompt_simt_kernel(const T* __restrict__ Q, const __grid_constant__ e3_kv_layer 
   }
 }
 
-template <typename T, int HD>
+template <int HD>
 cudaError_t launch_simt(const void* Q, const e3_kv_layer& kv, const PromptGeom& g, float sm_scale, void* O, float* lse,
                         int32_t* dev_err, cudaStream_t s) {
   static OncePerDevice<cudaError_t> attrs;
   const cudaError_t e = once_per_device(attrs, [] {
-    return cudaFuncSetAttribute(prompt_simt_kernel<T, HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, SimtCfg<HD>::SMEM);
+    return cudaFuncSetAttribute(prompt_simt_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, SimtCfg<HD>::SMEM);
   });
   if (e != cudaSuccess) return e;
   const long long items = prompt_items_bound(g), most = 8ll * num_sms();
-  return launch_pdl(prompt_simt_kernel<T, HD>, dim3(static_cast<unsigned>(items < most ? items : most)), dim3(256),
-                    SimtCfg<HD>::SMEM, s, 1, static_cast<const T*>(Q), kv, g, sm_scale, static_cast<T*>(O), lse, dev_err);
+  return launch_pdl(prompt_simt_kernel<HD>, dim3(static_cast<unsigned>(items < most ? items : most)), dim3(256),
+                    SimtCfg<HD>::SMEM, s, 1, static_cast<const float*>(Q), kv, g, sm_scale, static_cast<float*>(O), lse, dev_err);
 }
 
 }  // namespace
@@ -201,20 +196,16 @@ e3_status launch_prompt(const void* Q, const int32_t* row_start, const int32_t* 
   g.cap = static_cast<long long>(kv.max_pages) * kv.page_size;
   g.L = (g.max_kv_len + max_rows + 127) / 128;
   cudaError_t e = cudaErrorInvalidValue;
-  if (kv.dt == E3_BF16) {
-    e = kv.head_dim == 128 ? launch_simt<__nv_bfloat16, 128>(Q, kv, g, sm_scale, O, lse, dev_err, s)
-                           : launch_simt<__nv_bfloat16, 64>(Q, kv, g, sm_scale, O, lse, dev_err, s);
-  } else {
-    switch (kv.head_dim) {
-      case 32: e = launch_simt<float, 32>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
-      case 64: e = launch_simt<float, 64>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
-      case 96: e = launch_simt<float, 96>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
-      case 128: e = launch_simt<float, 128>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
-      case 160: e = launch_simt<float, 160>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
-      case 192: e = launch_simt<float, 192>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
-      case 224: e = launch_simt<float, 224>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
-      case 256: e = launch_simt<float, 256>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
-    }
+  if (kv.dt == E3_BF16) return launch_prompt_tc(Q, kv, g, sm_scale, O, lse, dev_err, s);
+  switch (kv.head_dim) {
+    case 32: e = launch_simt<32>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
+    case 64: e = launch_simt<64>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
+    case 96: e = launch_simt<96>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
+    case 128: e = launch_simt<128>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
+    case 160: e = launch_simt<160>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
+    case 192: e = launch_simt<192>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
+    case 224: e = launch_simt<224>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
+    case 256: e = launch_simt<256>(Q, kv, g, sm_scale, O, lse, dev_err, s); break;
   }
   return e == cudaSuccess ? E3_OK : cuda_status(e, "prompt kernels");
 }

@@ -1,0 +1,586 @@
+// k_prompt_tc.cu -- prompt_attn in bf16 on the 5th-generation tensor cores (head_dim 64, 128).
+//
+// An item is 256 flat query rows of one request and KV head (prompt.cuh: row by row, head by
+// head, so that a group's heads share the keys and a diagonal is short); one CTA per SM works
+// through items, the longest first.  Two softmax groups take 128 rows each, one thread to a
+// row; both use every tile of 128 keys:
+//   producer (warp 0)  finds the next item, brings K and V tiles by TMA into two stages each
+//   issuer (warp 1)    S = Q K^T, then O += P V with P from tensor memory, for the groups in
+//                      turn, so that each group's softmax runs under the other's products
+//   warps 2 and 3      the items' rows of Q; V tiles with keys that some rows do not see: rows of
+//                      V that hold a NaN or an Inf, or nothing yet, leave the product (0 * Inf would
+//                      reach the rows that do not see them), rows that see them get NaN
+//   softmax (2 x 4 warps)  exponentials against the base so far, P (bf16) over S in halves of 64
+//                      keys.  No pass for the maximum but on an item's first tile: where a half's
+//                      sum passes 2^kTop, or is NaN, the maximum is looked for, the base moved and
+//                      the half done again.  The diagonal's tiles take -Inf where unseen.
+// O stays in tensor memory until the item's end; its rows are written from there.
+#include <algorithm>
+
+#include "e3_common.cuh"
+#include "e3_kernels.h"
+#include "prompt.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.cuh"
+
+namespace e3 {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kRows = 128;       // query rows of a softmax group
+constexpr int kKeys = 128;       // keys of a tile
+constexpr int kStep = 64;        // keys of a half
+constexpr int kHalfB = 16384;    // bytes of 64 dims of a tile: [128 rows][128 B], 128-byte swizzle
+constexpr int kThreads = 384;
+constexpr int kSoftmax0 = 4;     // first softmax warp
+constexpr float kTop = 32768.0f;
+
+template <int HD>
+struct TcCfg {
+  static constexpr int HALVES = HD / 64;          // of an operand's dims
+  static constexpr int OP = HALVES * kHalfB;      // bytes of an operand tile
+  static constexpr int Q = 0, K = 2 * OP, V = K + 2 * OP, BARS = V + 2 * OP;
+  static constexpr int SMEM = BARS + 1024 + 1024;  // (base rounded up to 1024)
+};
+static_assert(TcCfg<128>::SMEM <= 232448, "shared memory of a CTA");
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint64_t* b) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(su32(b))
+               : "memory");
+}
+
+struct Item {  // what the producer tells the other roles (b < 0: no more)
+  int b, kvh, f0, start, n, c;
+};
+// Sizes of an item that every role derives from it.
+struct Sizes {
+  int keys[2];  // keys that group g's rows reach (0: the group has no rows)
+  int tiles;    // key tiles of the item
+  int common;   // keys that all its rows see
+  __device__ __forceinline__ Sizes(const Item& it, int G) {
+    const int flat = it.n * G;
+    common = it.c + it.f0 / G + 1;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const int first = it.f0 + g * kRows;
+      keys[g] = first < flat ? it.c + (min(first + kRows, flat) - 1) / G + 1 : 0;
+    }
+    tiles = (max(keys[0], keys[1]) + kKeys - 1) / kKeys;
+  }
+  __device__ __forceinline__ int tiles_of(int g) const { return (keys[g] + kKeys - 1) / kKeys; }
+  // halves of tile t that group g computes
+  __device__ __forceinline__ int halves(int g, int t) const { return keys[g] - t * kKeys > kStep ? 2 : 1; }
+  // some row of the item does not see all of tile t's keys
+  __device__ __forceinline__ bool masked(int t) const { return (t + 1) * kKeys > common; }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const __grid_constant__ e3_kv_layer kv, const __grid_constant__ PromptGeom g, int box, float sm_scale,
+                 __nv_bfloat16* __restrict__ O, float* __restrict__ lse, int32_t* dev_err) {
+  using C = TcCfg<HD>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BARS);
+  uint64_t* k_full = bars;          // [stage], as the following
+  uint64_t* k_empty = bars + 2;
+  uint64_t* v_full = bars + 4;      // tiles that every row sees
+  uint64_t* v_raw = bars + 6;       // tiles that warps 2 and 3 look through first,
+  uint64_t* v_ok = bars + 8;        // and have
+  uint64_t* v_empty = bars + 10;
+  uint64_t* s_full = bars + 12;     // [softmax group]
+  uint64_t* p_full = bars + 14;     // [softmax group][half]
+  uint64_t* o_half = bars + 18;     // [softmax group] the product with the tile's first half
+  uint64_t* o_done = bars + 20;     // [softmax group] the item's last
+  uint64_t* q_full = bars + 22;     // [softmax group]
+  uint64_t* q_empty = bars + 24;
+  uint64_t* item_full = bars + 26;  // [2]
+  uint64_t* item_empty = bars + 28;
+  Item* s_item = reinterpret_cast<Item*>(bars + 30);                // [2]
+  uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_item + 2);        // [2 items][4 masked tiles][4] keys whose V is not finite
+  uint32_t* tmem_slot = s_bad + 32;
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&k_full[i], 1);
+      bar_init(&k_empty[i], 1);
+      bar_init(&v_full[i], 1);
+      bar_init(&v_raw[i], 1);
+      bar_init(&v_ok[i], 2);
+      bar_init(&v_empty[i], 1);
+      bar_init(&s_full[i], 1);
+      bar_init(&p_full[2 * i], 4);
+      bar_init(&p_full[2 * i + 1], 4);
+      bar_init(&o_half[i], 1);
+      bar_init(&o_done[i], 1);
+      bar_init(&q_full[i], 1);
+      bar_init(&q_empty[i], 1);
+      bar_init(&item_full[i], 1);
+      bar_init(&item_empty[i], 11);  // every warp but the producer
+    }
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  if (blockIdx.x == 0)  // requests whose sizes are out of bounds
+    for (int b = threadIdx.x; b < g.B; b += kThreads)
+      if (!prompt_req(g, b).ok) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  pdl_trigger();
+  const uint32_t tmem = *tmem_slot;  // columns: S of group g at 128 g (its P over the first half), O at 256 + HD g
+  // the item in slot k % 2, or the end; the slot is given back with item_done
+  auto next_item = [&](uint32_t k, Item* it) {
+    if (!warp_wait(&item_full[k & 1], (k >> 1) & 1, abort)) return false;
+    *it = s_item[k & 1];
+    return it->b >= 0;
+  };
+  auto item_done = [&](uint32_t k) {
+    __syncwarp();
+    if (lane == 0) bar_arrive(&item_empty[k & 1]);
+  };
+  // (after a wait that ran out: the phases that the copies in flight complete)
+  // bit st: the stage has been loaded, the parity of its last load; of V also whether to v_raw
+  uint32_t any_k = 0, par_k = 0, any_v = 0, par_v = 0, raw_v = 0;
+
+  if (warp == 0) {
+    uint32_t T = 0, use_full = 0, use_raw = 0;  // tiles; bit st: parity of the stage's next use of v_full, v_raw
+    bool live = true;
+    for (uint32_t k = 0; live; ++k) {
+      const long long row = static_cast<long long>(k) * gridDim.x;
+      const PromptItem at = find_prompt_item(g, row + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
+      Item it{-1, 0, 0, 0, 0, 0};
+      if (at.b < g.B) {
+        const PromptReq q = prompt_req(g, at.b);
+        it = Item{at.b, at.kvh, at.tile * 2 * kRows, q.start, q.n, q.c};
+      }
+      if (!warp_wait(&item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort)) break;
+      if (lane == 0) {
+        s_item[k & 1] = it;
+        bar_arrive(&item_full[k & 1]);
+      }
+      __syncwarp();
+      if (it.b < 0 || ((kv.flags & E3_KV_SELFTEST_STALL) && blockIdx.x == 0)) break;  // (keys that never come)
+      const Sizes z(it, g.G);
+      const int keys = max(z.keys[0], z.keys[1]);
+      const int32_t* table = kv.page_table + static_cast<size_t>(it.b) * kv.max_pages;
+      // lane i brings keys [i box, (i + 1) box) of a tile; the row of its first one, -1: none
+      auto box_row = [&](int t) {
+        const int key = t * kKeys + lane * box;
+        if (lane * box >= kKeys || key >= keys) return -1;
+        const int pi = key / kv.page_size;
+        int page = table[pi];
+        if (page < 0 || page >= kv.n_pages) {
+          dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+          page = 0;
+        }
+        return (page * g.KVH + it.kvh) * kv.page_size + (key - pi * kv.page_size);
+      };
+      int r = box_row(0);
+      for (int t = 0; t < z.tiles; ++t, ++T) {
+        const int st = T & 1, r_next = t + 1 < z.tiles ? box_row(t + 1) : -1;
+        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, r >= 0)) * static_cast<uint32_t>(box) * HD * 2;
+        auto load = [&](uint64_t* full, unsigned char* dst, const CUtensorMap* map) {
+          if (lane == 0) bar_expect(full, bytes);
+          __syncwarp();
+          if (r >= 0)
+#pragma unroll
+            for (int h = 0; h < C::HALVES; ++h) tma2d(su32(dst + st * C::OP + h * kHalfB) + lane * box * 128, map, h * 64, r, full);
+        };
+        if (!warp_wait(&k_empty[st], ((T >> 1) & 1) ^ 1, abort)) {
+          live = false;
+          break;
+        }
+        load(&k_full[st], sK, &tmK);
+        any_k |= 1u << st;
+        par_k = (par_k & ~(1u << st)) | (((T >> 1) & 1u) << st);
+        if (!warp_wait(&v_empty[st], ((T >> 1) & 1) ^ 1, abort)) {
+          live = false;
+          break;
+        }
+        const bool raw = z.masked(t);
+        load(raw ? &v_raw[st] : &v_full[st], sV, &tmV);
+        uint32_t& use = raw ? use_raw : use_full;
+        any_v |= 1u << st;
+        par_v = (par_v & ~(1u << st)) | (use & (1u << st));
+        raw_v = (raw_v & ~(1u << st)) | ((raw ? 1u : 0u) << st);
+        use ^= 1u << st;
+        r = r_next;
+      }
+    }
+  } else if (warp == 1) {
+    const uint64_t q_desc = desc_sw128(su32(sQ), 16, 1024), k_desc = desc_sw128(su32(sK), 16, 1024);
+    const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
+    uint32_t T = 0, use_full = 0, use_ok = 0, use_p = 0, use_q = 0;  // (bits: parities of the next uses)
+    Item it;
+    bool live = true;
+    for (uint32_t k = 0; live && next_item(k, &it); ++k) {
+      const Sizes z(it, g.G);
+      item_done(k);
+      if (lane == 0) {
+        const int nt[2] = {z.tiles_of(0), z.tiles_of(1)};
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if (nt[w] > 0) {
+            live = live && bar_wait(&q_full[w], (use_q >> w) & 1, abort);
+            use_q ^= 1u << w;
+          }
+        // step t: each group's product with V of tile t - 1, then its scores of tile t
+        for (int t = 0; live && t <= z.tiles; ++t) {
+          const uint32_t st = (T + t) & 1, pst = st ^ 1;
+          if (t < z.tiles) live = bar_wait(&k_full[st], ((T + t) >> 1) & 1, abort);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const uint32_t tS = tmem + w * kRows, tO = tmem + 256 + w * HD;
+            if (live && t > 0 && t - 1 < nt[w]) {
+              if (w == 0 || nt[0] < t) {  // the first group to use V of tile t - 1
+                if (z.masked(t - 1)) {
+                  live = bar_wait(&v_ok[pst], (use_ok >> pst) & 1, abort);
+                  use_ok ^= 1u << pst;
+                } else {
+                  live = bar_wait(&v_full[pst], (use_full >> pst) & 1, abort);
+                  use_full ^= 1u << pst;
+                }
+              }
+              const int halves = z.halves(w, t - 1);
+              const uint64_t vd = v_desc + static_cast<uint64_t>((pst * C::OP) >> 4);
+              for (int h = 0; live && h < halves; ++h) {
+                live = bar_wait(&p_full[2 * w + h], (use_p >> (2 * w + h)) & 1, abort);
+                use_p ^= 1u << (2 * w + h);
+                if (!live) break;
+                fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  umma_ts(tO, tS + h * 32 + kk * 8, vd + static_cast<uint64_t>(((h * kStep + kk * 16) * 128) >> 4), idesc_16(HD, 1, true),
+                          h + kk > 0 || t > 1 ? 1u : 0u);
+                if (h == 0 && halves == 2) umma_commit(&o_half[w]);
+              }
+              if (live && (w == 1 || nt[1] < t)) umma_commit(&v_empty[pst]);
+              if (live && t == nt[w]) umma_commit(&o_done[w]);
+            }
+            if (live && t < nt[w]) {
+              // over the P that the product before reads: products of one thread run in the order of issue
+              const uint64_t qd = q_desc + static_cast<uint64_t>((w * C::OP) >> 4), kd = k_desc + static_cast<uint64_t>((st * C::OP) >> 4);
+              const uint32_t id = z.halves(w, t) == 2 ? idesc_16(kKeys, 0, true) : idesc_16(kStep, 0, true);
+#pragma unroll
+              for (int kk = 0; kk < HD / 16; ++kk) {
+                const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kHalfB >> 4) + (kk & 3) * 2);
+                umma(tS, qd + off, kd + off, id, kk > 0 ? 1u : 0u);
+              }
+              umma_commit(&s_full[w]);
+              if (w == 1 || nt[1] <= t) umma_commit(&k_empty[st]);
+              if (t == nt[w] - 1) umma_commit(&q_empty[w]);
+            }
+          }
+        }
+        T += z.tiles;
+      }
+      live = __shfl_sync(0xFFFFFFFFu, live ? 1 : 0, 0) != 0;
+    }
+  } else if (warp < kSoftmax0) {
+    const int w = warp - 2;
+    uint32_t use_raw = 0, T = 0, n_q = 0;
+    Item it;
+    bool live = true;
+    for (uint32_t k = 0; live && next_item(k, &it); ++k) {
+      const Sizes z(it, g.G);
+      // Q of group w: 128 rows of the 256
+      if (z.keys[w] > 0) {
+        if (!warp_wait(&q_empty[w], (n_q & 1) ^ 1, abort)) break;
+        ++n_q;
+        constexpr int LPR = HD / 8;          // lanes (16-byte pieces) of a row
+        const int flat = it.n * g.G, c = lane % LPR;
+        unsigned char* slab = sQ + w * C::OP;
+#pragma unroll 1
+        for (int r0 = 0; r0 < kRows; r0 += 32) {
+          const int f = it.f0 + w * kRows + r0 + lane, row = f / g.G;
+          const int own = f < flat ? (it.start + row) * g.H + it.kvh * g.G + f - row * g.G : -1;
+#pragma unroll 8
+          for (int i = 0; i < LPR; ++i) {
+            const int rr = r0 + i * (32 / LPR) + lane / LPR;
+            const int at = __shfl_sync(0xFFFFFFFFu, own, rr - r0);
+            const __nv_bfloat16* src = Q + static_cast<size_t>(max(at, 0)) * HD + c * 8;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             su32(slab + (c >> 3) * kHalfB + rr * 128 + (((c & 7) ^ (rr & 7)) << 4))),
+                         "l"(src), "r"(at >= 0 ? 16 : 0)
+                         : "memory");
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&q_full[w]);
+      }
+      // V tiles with keys that some rows do not see
+      const int keys = max(z.keys[0], z.keys[1]), t0 = z.common / kKeys;
+      for (int t = t0; t < z.tiles; ++t) {
+        const int st = (T + t) & 1;
+        if (!warp_wait(&v_raw[st], (use_raw >> st) & 1, abort)) {
+          live = false;
+          break;
+        }
+        use_raw ^= 1u << st;
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          const int rr = w * 64 + i * 32 + lane, key = t * kKeys + rr;
+          bool bad = false;
+          if (key >= z.common) {
+            unsigned char* at = sV + st * C::OP + rr * 128;
+            if (key < keys) {
+              __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
+#pragma unroll 8
+              for (int c = 0; c < 8 * C::HALVES; ++c) {
+                const uint4 y = *reinterpret_cast<const uint4*>(at + (c >> 3) * kHalfB + (((c + lane) & 7) << 4));
+                const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&y);
+                m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3]))));
+              }
+              const uint32_t b = *reinterpret_cast<const uint32_t*>(&m);
+              bad = max(b & 0xFFFFu, b >> 16) >= 0x7F80u;
+            }
+            if (bad || key >= keys)
+#pragma unroll 1
+              for (int c = 0; c < 8 * C::HALVES; ++c)
+                *reinterpret_cast<uint4*>(at + (c >> 3) * kHalfB + (((c + lane) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          const uint32_t word = __ballot_sync(0xFFFFFFFFu, bad);
+          if (lane == 0) s_bad[((k & 1) * 4 + t - t0) * 4 + 2 * w + i] = word;
+        }
+        fence_async_smem();  // generic-proxy writes -> tensor core
+        __syncwarp();
+        if (lane == 0) bar_arrive(&v_ok[st]);
+      }
+      T += z.tiles;
+      item_done(k);
+    }
+  } else {
+    // softmax: warp w of group grp reads TMEM lane quarter warp % 4 (rows 32 quarter ..)
+    const int grp = (warp - kSoftmax0) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + grp * kRows + lane_base, tO = tmem + 256 + grp * HD + lane_base;
+    const float c = sm_scale * kLog2e;
+    const float2 cv = make_float2(c, c);
+    uint32_t n_tile = 0, n_half = 0, n_done = 0;
+    Item it;
+    bool live = true;
+    for (uint32_t k = 0; live && next_item(k, &it); ++k) {
+      const Sizes z(it, g.G);
+      const int mine = z.tiles_of(grp);
+      if (mine == 0) {
+        item_done(k);
+        continue;
+      }
+      const int f = it.f0 + grp * kRows + r, row = f / g.G;
+      const bool row_ok = f < it.n * g.G;
+      const int see = row_ok ? it.c + row + 1 : z.keys[grp];  // keys that the row sees
+      float m = -INFINITY, l = 0.0f;
+      auto scale_o = [&](float x) {  // O times x
+#pragma unroll 1
+        for (int d = 0; d < HD / 16; ++d) {
+          uint32_t y[16];
+          tmem_ld16(tO + 16 * d, y);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * x);
+          tmem_st16(tO + 16 * d, y);
+        }
+        tmem_st_wait();
+      };
+      for (int t = 0; t < mine; ++t) {
+        const int halves = z.halves(grp, t);
+        if (!warp_wait(&s_full[grp], n_tile & 1, abort)) {
+          live = false;
+          break;
+        }
+        ++n_tile;
+        fence_after();
+#pragma unroll 1
+        for (int h = 0; h < halves; ++h) {
+          const int vis = see - t * kKeys - h * kStep;  // keys of the half that the row sees
+          const bool masked = __any_sync(0xFFFFFFFFu, vis < kStep);
+          bool look = t + h == 0;  // for the maximum
+          uint32_t pk[2][16];
+          float s;
+#pragma unroll 1
+          for (;;) {
+            if (look) {
+              float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll 1
+              for (int d = 0; d < 4; ++d) {
+                uint32_t y[16];
+                tmem_ld16(tS + kStep * h + 16 * d, y);
+                if (masked)
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) y[j] = 16 * d + j < vis ? y[j] : 0xFF800000u;
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                  a0 = fmax3f(a0, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                  a1 = fmax3f(a1, __uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
+                }
+              }
+              const float nm = fmaxf(m, fmaxf(a0, a1) * c);
+              if (t + h > 0) {
+                const float corr = ex2(m - nm);
+                l *= corr;
+                if (h == 1 && !warp_wait(&o_half[grp], n_half & 1, abort)) {
+                  live = false;
+                  break;
+                }
+                fence_after();
+                scale_o(corr);
+              }
+              m = nm;
+            }
+            const float2 nv = make_float2(-m, -m);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            uint32_t y[2][32];
+            auto exps = [&](auto hide) {
+              tmem_ld32(tS + kStep * h, y[0]);
+              tmem_wait32(y[0]);
+              tmem_ld32(tS + kStep * h + 32, y[1]);
+#pragma unroll
+              for (int q = 0; q < 2; ++q) {
+                if (q == 1) tmem_wait32(y[1]);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  float2 a = __ffma2_rn(make_float2(__uint_as_float(y[q][2 * j]), __uint_as_float(y[q][2 * j + 1])), cv, nv);
+                  hide(a, 32 * q + 2 * j);
+                  const float2 e = make_float2(ex2(a.x), ex2(a.y));
+                  sum[j & 1] = __fadd2_rn(sum[j & 1], e);
+                  pk[q][j] = pack2_bf16(e.x, e.y);
+                }
+              }
+            };
+            if (masked)
+              exps([&](float2& a, int j) {
+                a.x = j < vis ? a.x : -INFINITY;
+                a.y = j + 1 < vis ? a.y : -INFINITY;
+              });
+            else
+              exps([](float2&, int) {});
+            const float2 s2 = __fadd2_rn(sum[0], sum[1]);
+            s = s2.x + s2.y;
+            if (look || !__any_sync(0xFFFFFFFFu, !(s <= kTop))) break;
+            look = true;
+          }
+          if (!live) break;
+          l += s;
+          tmem_st16(tS + 32 * h, pk[0]);
+          tmem_st16(tS + 32 * h + 16, pk[1]);
+          tmem_st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&p_full[2 * grp + h]);
+        }
+        if (!live) break;
+        if (halves == 2) ++n_half;
+      }
+      if (!live || !warp_wait(&o_done[grp], n_done & 1, abort)) break;
+      ++n_done;
+      __syncwarp();
+      fence_after();
+      // a row that sees a V which was taken out gets NaN (the marks are complete: the products are)
+      bool poison = false;
+      for (int t = z.common / kKeys; t < mine; ++t) {
+        const uint32_t* bad = s_bad + ((k & 1) * 4 + t - z.common / kKeys) * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int vis = see - t * kKeys - 32 * i;
+          if (vis > 0) poison |= (bad[i] & (vis >= 32 ? ~0u : (1u << vis) - 1u)) != 0u;
+        }
+      }
+      const size_t at = (static_cast<size_t>(it.start) + row) * g.H + it.kvh * g.G + (f - row * g.G);
+      const float inv = poison ? __int_as_float(0x7FC00000) : 1.0f / l;
+      uint4* dst = reinterpret_cast<uint4*>(O + at * HD);
+#pragma unroll 1
+      for (int h = 0; h < HD / 32; ++h) {
+        uint32_t y[32];
+        tmem_ld32(tO + 32 * h, y);
+        tmem_wait32(y);
+        if (row_ok) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t x[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              x[q] = pack2_bf16(__uint_as_float(y[8 * j + 2 * q]) * inv, __uint_as_float(y[8 * j + 2 * q + 1]) * inv);
+            dst[4 * h + j] = make_uint4(x[0], x[1], x[2], x[3]);
+          }
+        }
+      }
+      fence_before();
+      if (row_ok) lse[at] = (m + log2f(l)) * kLn2;
+      item_done(k);
+    }
+  }
+  fence_before();
+  if (__syncthreads_or(*abort != 0)) {
+    // after a wait that ran out, the copies still in flight land (bounded) before the
+    // shared memory goes
+    if (warp == 0) {
+      const uint64_t t0 = gtimer();
+      for (int st = 0; st < 2; ++st) {
+        if ((any_k >> st) & 1u)
+          while (!bar_try(&k_full[st], (par_k >> st) & 1u) && gtimer() - t0 < kWaitNs) {
+          }
+        if ((any_v >> st) & 1u)
+          while (!bar_try((raw_v >> st) & 1u ? &v_raw[st] : &v_full[st], (par_v >> st) & 1u) && gtimer() - t0 < kWaitNs) {
+          }
+      }
+      while (gtimer() - t0 < 50000) {  // and so have the products
+      }
+      if (lane == 0) dev_flag(dev_err, E3_DEV_ERR_TIMEOUT);
+    }
+    __syncthreads();
+  }
+  fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+template <int HD>
+cudaError_t launch_tc(const void* Q, const CUtensorMap& mk, const CUtensorMap& mv, const e3_kv_layer& kv, const PromptGeom& g, int box,
+                      float sm_scale, void* O, float* lse, int32_t* dev_err, cudaStream_t s) {
+  static OncePerDevice<cudaError_t> attrs;
+  const cudaError_t e = once_per_device(attrs, [] {
+    return cudaFuncSetAttribute(prompt_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<HD>::SMEM);
+  });
+  if (e != cudaSuccess) return e;
+  const long long items = prompt_items_bound(g);
+  return launch_pdl(prompt_tc_kernel<HD>, dim3(static_cast<unsigned>(std::min<long long>(items, num_sms()))), dim3(kThreads),
+                    TcCfg<HD>::SMEM, s, 1, static_cast<const __nv_bfloat16*>(Q), mk, mv, kv, g, box, sm_scale,
+                    static_cast<__nv_bfloat16*>(O), lse, dev_err);
+}
+
+}  // namespace
+
+e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, float sm_scale, void* O, float* lse,
+                           int32_t* dev_err, cudaStream_t s) {
+  g.tile = 2 * kRows;
+  int box = 16;  // keys of a TMA box: what divides a page, as far as a tile has
+  while (box < kKeys && kv.page_size % (2 * box) == 0) box *= 2;
+  const unsigned long long rows = static_cast<unsigned long long>(kv.n_pages) * kv.n_kv_heads * kv.page_size;
+  E3_REQUIRE(rows < (1ull << 31), E3_ERR_SHAPE, "prompt_attn: %llu rows of K", rows);
+  CUtensorMap mk, mv;
+  E3_REQUIRE(encode_rows_map(&mk, kv.k, rows, kv.head_dim, box) && encode_rows_map(&mv, kv.v, rows, kv.head_dim, box),
+             E3_ERR_INVALID_ARG, "prompt_attn: cuTensorMapEncodeTiled rejected K or V");
+  const cudaError_t e = kv.head_dim == 128 ? launch_tc<128>(Q, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, s)
+                                           : launch_tc<64>(Q, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, s);
+  return e == cudaSuccess ? E3_OK : cuda_status(e, "prompt_tc_kernel");
+}
+
+}  // namespace e3

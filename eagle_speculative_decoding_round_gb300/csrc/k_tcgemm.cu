@@ -24,6 +24,7 @@
 
 #include "e3_common.cuh"
 #include "e3_kernels.h"
+#include "tensor_map.cuh"
 
 namespace e3 {
 
@@ -535,34 +536,6 @@ row_q_kernel(const float* __restrict__ logits, int V, const float* __restrict__ 
 // host side
 // ---------------------------------------------------------------------------
 
-// The driver's tensor-map encoder, looked up through the runtime so that the
-// library does not link libcuda (it must load on machines without a driver).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {  // looked up once, thread-safely
-    PFN_cuTensorMapEncodeTiled_v12000 found = nullptr;
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      found = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    return found;
-  }();
-  return fn;
-}
-
-bool make_map(CUtensorMap* map, const void* base, int rows, int cols, int box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  if (!encode) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(BK), static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-                                      strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 template <int BN>
 e3_status launch_fuse_bn(const CUtensorMap& a, const CUtensorMap& b0, const CUtensorMap& b1, const CUtensorMap& b2,
                          int Nw, int Mx, int kb_per_src, int kb_total, int splits, float* out, int32_t* dev_err,
@@ -630,8 +603,8 @@ e3_status launch_linear_tc(const void* W, const void* const* src, int n_src, int
              "linear: n_src=%d K=%d M=%d N=%d", n_src, K, M, N);
   const int bn = pick_bn(M);
   CUtensorMap a, b[3];
-  bool ok = make_map(&a, W, N, n_src * K, BM);
-  for (int i = 0; i < n_src; ++i) ok = ok && make_map(&b[i], src[i], M, K, bn);
+  bool ok = encode_rows_map(&a, W, N, n_src * K, BM);
+  for (int i = 0; i < n_src; ++i) ok = ok && encode_rows_map(&b[i], src[i], M, K, bn);
   E3_REQUIRE(ok, E3_ERR_INVALID_ARG, "linear: cuTensorMapEncodeTiled rejected an operand");
   for (int i = n_src; i < 3; ++i) b[i] = b[0];
   *splits = linear_splits_impl(M, n_src * K, N);
@@ -652,8 +625,8 @@ e3_status launch_fuse_tc(const void* h_low, const void* h_mid, const void* h_hig
              ws_bytes);
   const int bn = pick_bn(M);
   CUtensorMap a, b0, b1, b2;
-  E3_REQUIRE(make_map(&a, W_f, d_out, 3 * d, BM) && make_map(&b0, h_low, M, d, bn) && make_map(&b1, h_mid, M, d, bn) &&
-                 make_map(&b2, h_high, M, d, bn),
+  E3_REQUIRE(encode_rows_map(&a, W_f, d_out, 3 * d, BM) && encode_rows_map(&b0, h_low, M, d, bn) && encode_rows_map(&b1, h_mid, M, d, bn) &&
+                 encode_rows_map(&b2, h_high, M, d, bn),
              E3_ERR_INVALID_ARG, "eagle3_fuse: cuTensorMapEncodeTiled rejected an operand");
   const int splits = fuse_splits(M, d, d_out);
   float* part = static_cast<float*>(ws);
@@ -693,7 +666,7 @@ e3_status launch_lmhead_tc(const void* h, const void* W_lm, int M, int d, int V,
                            float* row_max, uint64_t* row_Q, int32_t* row_argmax, int32_t* dev_err, cudaStream_t s) {
   const int bn = std::max(32, pick_bn(M));  // the epilogue reads the accumulator 32 columns at a time
   CUtensorMap a, b;
-  E3_REQUIRE(make_map(&a, W_lm, V, d, BM) && make_map(&b, h, M, d, bn), E3_ERR_INVALID_ARG,
+  E3_REQUIRE(encode_rows_map(&a, W_lm, V, d, BM) && encode_rows_map(&b, h, M, d, bn), E3_ERR_INVALID_ARG,
              "lmhead_logits: cuTensorMapEncodeTiled rejected an operand");
   cudaError_t e = cudaMemsetAsync(row_Q, 0, static_cast<size_t>(M) * sizeof(uint64_t), s);
   if (e != cudaSuccess) return cuda_status(e, "lmhead_logits memset");

@@ -40,6 +40,7 @@
 
 #include "e3_common.cuh"
 #include "e3_kernels.h"
+#include "tensor_map.cuh"
 
 namespace e3 {
 
@@ -939,19 +940,6 @@ verify_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {  // looked up once, thread-safely
-    PFN_cuTensorMapEncodeTiled_v12000 found = nullptr;
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      found = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    return found;
-  }();
-  return fn;
-}
-
 // How many clusters of S verify CTAs (one per SM) can be resident at once
 // (0 if such clusters cannot be launched).
 int max_active_clusters(int S) {
@@ -1002,7 +990,7 @@ bool verify_tc_supported(const e3_kv_layer& kv, int H) {
 e3_status launch_verify_tc(const void* Q, const e3_kv_layer& kv, const int32_t* kv_len, const uint64_t* mask, int B,
                            int R, int H, int max_kv_len, float sm_scale, VerifySplit* split, float* ws_o,
                            float2* ws_ml, void* O, float* lse, bool* merged, int32_t* dev_err, cudaStream_t s) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   E3_REQUIRE(enc != nullptr, E3_ERR_CUDA, "tree_verify_attn: tensor-map encoder unavailable");
   const int G = H / kv.n_kv_heads;
   CUtensorMap mq, mk, mv;

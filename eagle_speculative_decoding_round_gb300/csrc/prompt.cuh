@@ -6,8 +6,6 @@
 
 namespace e3 {
 
-namespace {
-
 // The query rows of one request and KV head, row by row and head by head: flat row f is row
 // f / G of the request, query head kvh * G + f % G.  They are cut into tiles of `tile` flat
 // rows; a tile's keys end behind its last row's position.
@@ -19,6 +17,8 @@ struct PromptGeom {
   long long cap;  // slots that a request's pages hold
   int L;          // most key tiles of 128 that a tile can have
 };
+
+namespace {
 
 struct PromptReq {
   int start, n, c;  // first row, rows (0 where the request's sizes are out of bounds), keys before them
@@ -116,5 +116,8 @@ inline long long prompt_items_bound(const PromptGeom& g) {
 }
 
 }  // namespace
+
+e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, float sm_scale, void* O, float* lse,
+                           int32_t* dev_err, cudaStream_t s);
 
 }  // namespace e3

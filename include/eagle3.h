@@ -134,8 +134,9 @@ typedef struct {
  * thread waits on a barrier that nothing arrives on: the bounded wait runs out
  * after about a second, the kernel sets E3_DEV_ERR_TIMEOUT in dev_err, waits for
  * its own copies in flight, frees its tensor memory and returns; O and lse are not
- * valid.  In tree_verify_attn4's, with the bit on the tail, one CTA waits for keys that
- * nothing brings, with the same end.  Other paths and calls ignore the bit. */
+ * valid.  In tree_verify_attn4's, with the bit on the tail, and in prompt_attn's bf16
+ * kernel, one CTA waits for keys that nothing brings, with the same end.  Other paths and
+ * calls ignore the bit. */
 #define E3_KV_SELFTEST_STALL 0x40000000
 typedef struct {
   void* k;
@@ -646,7 +647,7 @@ E3_API size_t eagle3_verify8_workspace_bytes(int B, int R, int n_q_heads, int n_
  * Limits: head_dim 64 or 128 (fp32: any multiple of 32 up to 256); n_q_heads %
  *   n_kv_heads == 0; page_size % 16 == 0; 1 <= B <= 65535; 1 <= max_rows;
  *   1 <= n_total, n_total * n_q_heads < 2^31; max_kv_len + max_rows <= 2^30.  Q, O 16-byte
- *   aligned; kv->flags 0 or E3_KV_PREFIX_STABLE (not used).
+ *   aligned; E3_KV_PREFIX_STABLE in kv->flags is accepted (and not used).
  * ws: eagle3_prompt_workspace_bytes(...) bytes of device scratch (may be 0, ws then NULL),
  *   16-byte aligned; calls that may overlap on the GPU need scratch of their own.
  * ------------------------------------------------------------------------- */

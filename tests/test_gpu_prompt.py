@@ -284,3 +284,19 @@ def test_prompt_attn_many_requests():
     assert int(err.item()) == 0
     check(d, O, lse)
     assert torch.equal(O, O2) and torch.equal(lse, lse2)
+
+
+def test_prompt_attn_wait_that_runs_out():
+    """The self-test bit: keys that never come end the call with the error word set, after the waits' bound, and leave
+    nothing behind that the next call on the same buffers meets."""
+    d = inputs(6, 16, 4, 128, [700, 300], [0, 200], 64)
+    dev = {}
+    call(d, dev=dev)
+    torch.cuda.synchronize()
+    _, _, err = call(d, dev=dev, flags=e3.E3_KV_SELFTEST_STALL)
+    torch.cuda.synchronize()
+    assert int(err.item()) == e3.E3_DEV_ERR_TIMEOUT
+    O, lse, err = call(d, dev=dev)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(d, O, lse)

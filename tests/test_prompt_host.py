@@ -28,7 +28,7 @@ def test_prompt_refusals(e3):  # noqa: F811
     refused(e3, 2, call, H=0)
     refused(e3, 2, call, kv=kv16(e3, hd=96))            # bf16 heads of 96
     refused(e3, 2, call, kv=kv16(e3, page=24))
-    refused(e3, 1, call, kv=kv16(e3, flags=e3.E3_KV_SELFTEST_STALL | 2))
+    refused(e3, 1, call, kv=kv16(e3, flags=2))
     refused(e3, 1, call, kv=kv16(e3, k=A + 4))
     refused(e3, 1, call, kv=kv16(e3, dt=7))
     refused(e3, 1, call, scale=0.0)
