@@ -5,9 +5,9 @@
 // through items, the longest first.  Two softmax groups take 128 rows each, one thread to a
 // row; both use every tile of 128 keys:
 //   producer (warp 0)  finds the next item, brings K and V tiles by TMA into two stages each
-//   issuer (warp 1)    S = Q K^T, then O += P V with P from tensor memory, for the groups in
-//                      turn, so that each group's softmax runs under the other's products
-//   warps 2 and 3      the items' rows of Q; V tiles with keys that some rows do not see: rows of
+//   issuers (warps 1, 2; one per group)  S = Q K^T, then O += P V with P from tensor memory; each
+//                      group's softmax runs under the other's products
+//   warps 3 and 12     the items' rows of Q; V tiles with keys that some rows do not see: rows of
 //                      V that hold a NaN or an Inf, or nothing yet, leave the product (0 * Inf would
 //                      reach the rows that do not see them), rows that see them get NaN
 //   softmax (2 x 4 warps)  exponentials against the base so far, P (bf16) over S in halves of 64
@@ -33,7 +33,7 @@ constexpr int kRows = 128;       // query rows of a softmax group
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kStep = 64;        // keys of a half
 constexpr int kHalfB = 16384;    // bytes of 64 dims of a tile: [128 rows][128 B], 128-byte swizzle
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
 constexpr int kSoftmax0 = 4;     // first softmax warp
 constexpr float kTop = 32768.0f;
 
@@ -95,7 +95,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   uint64_t* k_full = bars;          // [stage], as the following
   uint64_t* k_empty = bars + 2;
   uint64_t* v_full = bars + 4;      // tiles that every row sees
-  uint64_t* v_raw = bars + 6;       // tiles that warps 2 and 3 look through first,
+  uint64_t* v_raw = bars + 6;       // tiles that warps 3 and 12 look through first,
   uint64_t* v_ok = bars + 8;        // and have
   uint64_t* v_empty = bars + 10;
   uint64_t* s_full = bars + 12;     // [softmax group]
@@ -115,11 +115,11 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       bar_init(&k_full[i], 1);
-      bar_init(&k_empty[i], 1);
+      bar_init(&k_empty[i], 2);
       bar_init(&v_full[i], 1);
       bar_init(&v_raw[i], 1);
       bar_init(&v_ok[i], 2);
-      bar_init(&v_empty[i], 1);
+      bar_init(&v_empty[i], 2);
       bar_init(&s_full[i], 1);
       bar_init(&p_full[2 * i], 4);
       bar_init(&p_full[2 * i + 1], 4);
@@ -128,7 +128,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       bar_init(&q_full[i], 1);
       bar_init(&q_empty[i], 1);
       bar_init(&item_full[i], 1);
-      bar_init(&item_empty[i], 11);  // every warp but the producer
+      bar_init(&item_empty[i], 12);  // every warp but the producer
     }
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -225,77 +225,85 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         r = r_next;
       }
     }
-  } else if (warp == 1) {
-    const uint64_t q_desc = desc_sw128(su32(sQ), 16, 1024), k_desc = desc_sw128(su32(sK), 16, 1024);
+  } else if (warp <= 2) {
+    // One issuing warp per softmax group: what one waits for passes under the other's products.
+    // (The issue of a product stalls while the tensor core has some in hand, and a wait on a
+    // barrier takes some 200 cycles even where its phase is over.)
+    const int w = warp - 1;
+    const uint64_t q_desc = desc_sw128(su32(sQ + w * C::OP), 16, 1024), k_desc = desc_sw128(su32(sK), 16, 1024);
     const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
+    const uint32_t tS = tmem + w * kRows, tO = tmem + 256 + w * HD;
     uint32_t T = 0, use_full = 0, use_ok = 0, use_p = 0, use_q = 0;  // (bits: parities of the next uses)
+    const uint32_t lead = elect_lane();
     Item it;
     bool live = true;
     for (uint32_t k = 0; live && next_item(k, &it); ++k) {
       const Sizes z(it, g.G);
       item_done(k);
-      if (lane == 0) {
-        const int nt[2] = {z.tiles_of(0), z.tiles_of(1)};
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          if (nt[w] > 0) {
-            live = live && bar_wait(&q_full[w], (use_q >> w) & 1, abort);
-            use_q ^= 1u << w;
-          }
-        // step t: each group's product with V of tile t - 1, then its scores of tile t
-        for (int t = 0; live && t <= z.tiles; ++t) {
-          const uint32_t st = (T + t) & 1, pst = st ^ 1;
-          if (t < z.tiles) live = bar_wait(&k_full[st], ((T + t) >> 1) & 1, abort);
-#pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            const uint32_t tS = tmem + w * kRows, tO = tmem + 256 + w * HD;
-            if (live && t > 0 && t - 1 < nt[w]) {
-              if (w == 0 || nt[0] < t) {  // the first group to use V of tile t - 1
-                if (z.masked(t - 1)) {
-                  live = bar_wait(&v_ok[pst], (use_ok >> pst) & 1, abort);
-                  use_ok ^= 1u << pst;
-                } else {
-                  live = bar_wait(&v_full[pst], (use_full >> pst) & 1, abort);
-                  use_full ^= 1u << pst;
-                }
-              }
-              const int halves = z.halves(w, t - 1);
-              const uint64_t vd = v_desc + static_cast<uint64_t>((pst * C::OP) >> 4);
-              for (int h = 0; live && h < halves; ++h) {
-                live = bar_wait(&p_full[2 * w + h], (use_p >> (2 * w + h)) & 1, abort);
-                use_p ^= 1u << (2 * w + h);
-                if (!live) break;
-                fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  umma_ts(tO, tS + h * 32 + kk * 8, vd + static_cast<uint64_t>(((h * kStep + kk * 16) * 128) >> 4), idesc_16(HD, 1, true),
-                          h + kk > 0 || t > 1 ? 1u : 0u);
-                if (h == 0 && halves == 2) umma_commit(&o_half[w]);
-              }
-              if (live && (w == 1 || nt[1] < t)) umma_commit(&v_empty[pst]);
-              if (live && t == nt[w]) umma_commit(&o_done[w]);
-            }
-            if (live && t < nt[w]) {
-              // over the P that the product before reads: products of one thread run in the order of issue
-              const uint64_t qd = q_desc + static_cast<uint64_t>((w * C::OP) >> 4), kd = k_desc + static_cast<uint64_t>((st * C::OP) >> 4);
-              const uint32_t id = z.halves(w, t) == 2 ? idesc_16(kKeys, 0, true) : idesc_16(kStep, 0, true);
-#pragma unroll
-              for (int kk = 0; kk < HD / 16; ++kk) {
-                const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kHalfB >> 4) + (kk & 3) * 2);
-                umma(tS, qd + off, kd + off, id, kk > 0 ? 1u : 0u);
-              }
-              umma_commit(&s_full[w]);
-              if (w == 1 || nt[1] <= t) umma_commit(&k_empty[st]);
-              if (t == nt[w] - 1) umma_commit(&q_empty[w]);
-            }
-          }
-        }
-        T += z.tiles;
+      const int mine = z.tiles_of(w);
+      if (mine > 0) {
+        live = warp_wait(&q_full[w], use_q, abort);
+        use_q ^= 1u;
       }
-      live = __shfl_sync(0xFFFFFFFFu, live ? 1 : 0, 0) != 0;
+      // scores of tile t; a stage that the group does not use is given back when it has come
+      auto scores = [&](int t) {
+        const uint32_t st = (T + t) & 1;
+        if (!warp_wait(&k_full[st], ((T + t) >> 1) & 1, abort)) return false;
+        if (t >= mine) {
+          if (lane == 0) bar_arrive(&k_empty[st]);
+          return true;
+        }
+        const uint64_t kd = k_desc + static_cast<uint64_t>((st * C::OP) >> 4);
+        const uint32_t id = z.halves(w, t) == 2 ? idesc_16(kKeys, 0, true) : idesc_16(kStep, 0, true);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kHalfB >> 4) + (kk & 3) * 2);
+          umma_lead(lead, tS, q_desc + off, kd + off, id, kk > 0 ? 1u : 0u);
+        }
+        umma_commit_lead(lead, &s_full[w]);
+        umma_commit_lead(lead, &k_empty[st]);
+        if (t == mine - 1) umma_commit_lead(lead, &q_empty[w]);
+        return true;
+      };
+      live = live && scores(0);
+      for (int t = 0; live && t < z.tiles; ++t) {
+        const uint32_t st = (T + t) & 1;
+        if (z.masked(t)) {
+          live = warp_wait(&v_ok[st], (use_ok >> st) & 1, abort);
+          use_ok ^= 1u << st;
+        } else {
+          live = warp_wait(&v_full[st], (use_full >> st) & 1, abort);
+          use_full ^= 1u << st;
+        }
+        if (t < mine) {
+          const int halves = z.halves(w, t);
+          const uint64_t vd = v_desc + static_cast<uint64_t>((st * C::OP) >> 4);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (!live || h >= halves) break;
+            live = warp_wait(&p_full[2 * w + h], (use_p >> h) & 1, abort);
+            use_p ^= 1u << h;
+            if (!live) break;
+            fence_after();
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_ts_lead(lead, tO, tS + h * 32 + kk * 8, vd + static_cast<uint64_t>(((h * kStep + kk * 16) * 128) >> 4),
+                           idesc_16(HD, 1, true), h + kk > 0 || t > 0 ? 1u : 0u);
+            if (h == 0 && halves == 2) umma_commit_lead(lead, &o_half[w]);
+          }
+          if (!live) break;
+          umma_commit_lead(lead, &v_empty[st]);
+          if (t == mine - 1) umma_commit_lead(lead, &o_done[w]);
+        } else if (live && lane == 0) {
+          bar_arrive(&v_empty[st]);
+        }
+        // (over the P that the product reads: products of one thread run in the order of issue)
+        if (t + 1 < z.tiles) live = live && scores(t + 1);
+      }
+      T += z.tiles;
     }
-  } else if (warp < kSoftmax0) {
-    const int w = warp - 2;
+  } else if (warp == 3 || warp == kSoftmax0 + 8) {
+    const int w = warp == 3 ? 0 : 1;
     uint32_t use_raw = 0, T = 0, n_q = 0;
     Item it;
     bool live = true;

@@ -79,6 +79,30 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b,
   asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::
                    "r"(d), "r"(a_tmem), "l"(b), "r"(id), "r"(acc));
 }
+// The same for a warp that stays together, `lead` != 0 in the one lane that issues: the operands
+// are the warp's, so that they reach the uniform registers that the instruction reads once and
+// not for every product (in a branch of one lane each product took about 130 cycles to issue).
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t x;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(x));
+  return x;
+}
+__device__ __forceinline__ void umma_lead(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::
+          "r"(d), "l"(a), "l"(b), "r"(id), "r"(acc), "r"(lead));
+}
+__device__ __forceinline__ void umma_ts_lead(uint32_t lead, uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::
+          "r"(d), "r"(a_tmem), "l"(b), "r"(id), "r"(acc), "r"(lead));
+}
+__device__ __forceinline__ void umma_commit_lead(uint32_t lead, uint64_t* b) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(su32(b)),
+      "r"(lead)
+      : "memory");
+}
 __device__ __forceinline__ void umma_commit(uint64_t* b) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(su32(b)) : "memory");
 }
