@@ -78,6 +78,11 @@ struct Sizes {
   __device__ __forceinline__ int tiles_of(int g) const { return (keys[g] + kKeys - 1) / kKeys; }
   // halves of tile t that group g computes
   __device__ __forceinline__ int halves(int g, int t) const { return keys[g] - t * kKeys > kStep ? 2 : 1; }
+  // The groups' scores come in turn: group 0's of tile t when the other has those of tile t - 1,
+  // group 1's when the other has those of tile t (as far as both have tiles).
+  __device__ __forceinline__ bool in_turn(int g, int t) const {
+    return keys[1] > 0 && t < tiles_of(0) && (g == 0 ? t > 0 : true);
+  }
   // some row of the item does not see all of tile t's keys
   __device__ __forceinline__ bool masked(int t) const { return (t + 1) * kKeys > common; }
 };
@@ -106,7 +111,8 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   uint64_t* q_empty = bars + 24;
   uint64_t* item_full = bars + 26;  // [2]
   uint64_t* item_empty = bars + 28;
-  Item* s_item = reinterpret_cast<Item*>(bars + 30);                // [2]
+  uint64_t* turn = bars + 30;       // [softmax group] the group has its scores
+  Item* s_item = reinterpret_cast<Item*>(bars + 32);                // [2]
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_item + 2);        // [2 items][4 masked tiles][4] keys whose V is not finite
   uint32_t* tmem_slot = s_bad + 32;
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -128,6 +134,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       bar_init(&q_full[i], 1);
       bar_init(&q_empty[i], 1);
       bar_init(&item_full[i], 1);
+      bar_init(&turn[i], 4);
       bar_init(&item_empty[i], 12);  // every warp but the producer
     }
     *abort = 0;
@@ -233,7 +240,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
     const uint64_t q_desc = desc_sw128(su32(sQ + w * C::OP), 16, 1024), k_desc = desc_sw128(su32(sK), 16, 1024);
     const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
     const uint32_t tS = tmem + w * kRows, tO = tmem + 256 + w * HD;
-    uint32_t T = 0, use_full = 0, use_ok = 0, use_p = 0, use_q = 0;  // (bits: parities of the next uses)
+    uint32_t T = 0, use_full = 0, use_ok = 0, use_p = 0, use_q = 0, use_turn = 0;  // (bits: parities of the next uses)
     const uint32_t lead = elect_lane();
     Item it;
     bool live = true;
@@ -252,6 +259,11 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         if (t >= mine) {
           if (lane == 0) bar_arrive(&k_empty[st]);
           return true;
+        }
+        // left alone the groups fall into step, and the tensor core idles under their softmax
+        if (z.in_turn(w, t)) {
+          if (!warp_wait(&turn[w ^ 1], use_turn, abort)) return false;
+          use_turn ^= 1u;
         }
         const uint64_t kd = k_desc + static_cast<uint64_t>((st * C::OP) >> 4);
         const uint32_t id = z.halves(w, t) == 2 ? idesc_16(kKeys, 0, true) : idesc_16(kStep, 0, true);
@@ -416,6 +428,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
           break;
         }
         ++n_tile;
+        if (lane == 0 && z.in_turn(grp ^ 1, grp == 0 ? t : t + 1)) bar_arrive(&turn[grp]);
         fence_after();
 #pragma unroll 1
         for (int h = 0; h < halves; ++h) {
