@@ -10,10 +10,10 @@
 //   warps 3 and 12     the items' rows of Q; V tiles with keys that some rows do not see: rows of
 //                      V that hold a NaN or an Inf, or nothing yet, leave the product (0 * Inf would
 //                      reach the rows that do not see them), rows that see them get NaN
-//   softmax (2 x 4 warps)  exponentials against the base so far, P (bf16) over S in halves of 64
-//                      keys.  No pass for the maximum but on an item's first tile: where a half's
-//                      sum passes 2^kTop, or is NaN, the maximum is looked for, the base moved and
-//                      the half done again.  The diagonal's tiles take -Inf where unseen.
+//   softmax (2 x 4 warps)  steps of 64 keys in two buffers of tensor memory: exponentials against
+//                      the base so far, P (bf16) over S.  No pass for the maximum but on an item's first tile: where a step's
+//                      sum passes kTop, or is NaN, the maximum is looked for, the base moved and
+//                      the step done again.  The diagonal's tiles take -Inf where unseen.
 // O stays in tensor memory until the item's end; its rows are written from there.
 #include <algorithm>
 
@@ -31,7 +31,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kRows = 128;       // query rows of a softmax group
 constexpr int kKeys = 128;       // keys of a tile
-constexpr int kStep = 64;        // keys of a half
+constexpr int kStep = 64;        // keys of a step
 constexpr int kHalfB = 16384;    // bytes of 64 dims of a tile: [128 rows][128 B], 128-byte swizzle
 constexpr int kThreads = 416;
 constexpr int kSoftmax0 = 4;     // first softmax warp
@@ -75,14 +75,7 @@ struct Sizes {
     }
     tiles = (max(keys[0], keys[1]) + kKeys - 1) / kKeys;
   }
-  __device__ __forceinline__ int tiles_of(int g) const { return (keys[g] + kKeys - 1) / kKeys; }
-  // halves of tile t that group g computes
-  __device__ __forceinline__ int halves(int g, int t) const { return keys[g] - t * kKeys > kStep ? 2 : 1; }
-  // The groups' scores come in turn: group 0's of tile t when the other has those of tile t - 1,
-  // group 1's when the other has those of tile t (as far as both have tiles).
-  __device__ __forceinline__ bool in_turn(int g, int t) const {
-    return keys[1] > 0 && t < tiles_of(0) && (g == 0 ? t > 0 : true);
-  }
+  __device__ __forceinline__ int steps_of(int g) const { return (keys[g] + kStep - 1) / kStep; }
   // some row of the item does not see all of tile t's keys
   __device__ __forceinline__ bool masked(int t) const { return (t + 1) * kKeys > common; }
 };
@@ -103,15 +96,14 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   uint64_t* v_raw = bars + 6;       // tiles that warps 3 and 12 look through first,
   uint64_t* v_ok = bars + 8;        // and have
   uint64_t* v_empty = bars + 10;
-  uint64_t* s_full = bars + 12;     // [softmax group]
-  uint64_t* p_full = bars + 14;     // [softmax group][half]
-  uint64_t* o_half = bars + 18;     // [softmax group] the product with the tile's first half
-  uint64_t* o_done = bars + 20;     // [softmax group] the item's last
+  uint64_t* s_full = bars + 12;     // [softmax group][buffer]
+  uint64_t* p_full = bars + 16;     // [softmax group][buffer]
+  uint64_t* o_step = bars + 20;     // [softmax group] the product with a step's V
   uint64_t* q_full = bars + 22;     // [softmax group]
   uint64_t* q_empty = bars + 24;
   uint64_t* item_full = bars + 26;  // [2]
   uint64_t* item_empty = bars + 28;
-  uint64_t* turn = bars + 30;       // [softmax group] the group has its scores
+  uint64_t* o_done = bars + 30;     // [softmax group] the item's last product
   Item* s_item = reinterpret_cast<Item*>(bars + 32);                // [2]
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_item + 2);        // [2 items][4 masked tiles][4] keys whose V is not finite
   uint32_t* tmem_slot = s_bad + 32;
@@ -126,15 +118,15 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       bar_init(&v_raw[i], 1);
       bar_init(&v_ok[i], 2);
       bar_init(&v_empty[i], 2);
-      bar_init(&s_full[i], 1);
+      bar_init(&s_full[2 * i], 1);
+      bar_init(&s_full[2 * i + 1], 1);
       bar_init(&p_full[2 * i], 4);
       bar_init(&p_full[2 * i + 1], 4);
-      bar_init(&o_half[i], 1);
+      bar_init(&o_step[i], 1);
       bar_init(&o_done[i], 1);
       bar_init(&q_full[i], 1);
       bar_init(&q_empty[i], 1);
       bar_init(&item_full[i], 1);
-      bar_init(&turn[i], 4);
       bar_init(&item_empty[i], 12);  // every warp but the producer
     }
     *abort = 0;
@@ -240,79 +232,75 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
     const uint64_t q_desc = desc_sw128(su32(sQ + w * C::OP), 16, 1024), k_desc = desc_sw128(su32(sK), 16, 1024);
     const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
     const uint32_t tS = tmem + w * kRows, tO = tmem + 256 + w * HD;
-    uint32_t T = 0, use_full = 0, use_ok = 0, use_p = 0, use_q = 0, use_turn = 0;  // (bits: parities of the next uses)
+    uint32_t T = 0, n_step = 0, use_full = 0, use_ok = 0, use_q = 0;  // tiles; steps; (bits: parities of the next uses)
     const uint32_t lead = elect_lane();
     Item it;
     bool live = true;
     for (uint32_t k = 0; live && next_item(k, &it); ++k) {
       const Sizes z(it, g.G);
       item_done(k);
-      const int mine = z.tiles_of(w);
+      const int mine = z.steps_of(w);
       if (mine > 0) {
         live = warp_wait(&q_full[w], use_q, abort);
         use_q ^= 1u;
       }
-      // scores of tile t; a stage that the group does not use is given back when it has come
-      auto scores = [&](int t) {
-        const uint32_t st = (T + t) & 1;
-        if (!warp_wait(&k_full[st], ((T + t) >> 1) & 1, abort)) return false;
-        if (t >= mine) {
-          if (lane == 0) bar_arrive(&k_empty[st]);
-          return true;
-        }
-        // left alone the groups fall into step, and the tensor core idles under their softmax
-        if (z.in_turn(w, t)) {
-          if (!warp_wait(&turn[w ^ 1], use_turn, abort)) return false;
-          use_turn ^= 1u;
-        }
-        const uint64_t kd = k_desc + static_cast<uint64_t>((st * C::OP) >> 4);
-        const uint32_t id = z.halves(w, t) == 2 ? idesc_16(kKeys, 0, true) : idesc_16(kStep, 0, true);
+      // scores of step u, into buffer u % 2 (the item's steps begin in turn with either)
+      auto scores = [&](int u) {
+        const uint32_t st = (T + (u >> 1)) & 1, bf = (n_step + u) & 1;
+        if (!(u & 1) && !warp_wait(&k_full[st], ((T + (u >> 1)) >> 1) & 1, abort)) return false;
+        const uint64_t kd = k_desc + static_cast<uint64_t>((st * C::OP + (u & 1) * (kStep * 128)) >> 4);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint64_t off = static_cast<uint64_t>((kk >> 2) * (kHalfB >> 4) + (kk & 3) * 2);
-          umma_lead(lead, tS, q_desc + off, kd + off, id, kk > 0 ? 1u : 0u);
+          umma_lead(lead, tS + bf * kStep, q_desc + off, kd + off, idesc_16(kStep, 0, true), kk > 0 ? 1u : 0u);
         }
-        umma_commit_lead(lead, &s_full[w]);
-        umma_commit_lead(lead, &k_empty[st]);
-        if (t == mine - 1) umma_commit_lead(lead, &q_empty[w]);
+        umma_commit_lead(lead, &s_full[2 * w + bf]);
+        if ((u & 1) || u == mine - 1) umma_commit_lead(lead, &k_empty[st]);
+        if (u == mine - 1) umma_commit_lead(lead, &q_empty[w]);
         return true;
       };
-      live = live && scores(0);
-      for (int t = 0; live && t < z.tiles; ++t) {
+      for (int u = 0; u < min(2, mine); ++u) live = live && scores(u);
+      for (int u = 0; live && u < mine; ++u) {
+        const uint32_t st = (T + (u >> 1)) & 1, bf = (n_step + u) & 1;
+        if (!(u & 1)) {
+          if (z.masked(u >> 1)) {
+            live = warp_wait(&v_ok[st], (use_ok >> st) & 1, abort);
+            use_ok ^= 1u << st;
+          } else {
+            live = warp_wait(&v_full[st], (use_full >> st) & 1, abort);
+            use_full ^= 1u << st;
+          }
+        }
+        live = live && warp_wait(&p_full[2 * w + bf], ((n_step + u) >> 1) & 1, abort);
+        if (!live) break;
+        fence_after();
+        const uint64_t vd = v_desc + static_cast<uint64_t>((st * C::OP + (u & 1) * (kStep * 128)) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ts_lead(lead, tO, tS + bf * kStep + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), idesc_16(HD, 1, true),
+                       kk > 0 || u > 0 ? 1u : 0u);
+        umma_commit_lead(lead, &o_step[w]);
+        if ((u & 1) || u == mine - 1) umma_commit_lead(lead, &v_empty[st]);
+        if (u == mine - 1) umma_commit_lead(lead, &o_done[w]);
+        // over the P that the product reads: products of one thread run in the order of issue
+        if (u + 2 < mine) live = scores(u + 2);
+      }
+      // stages that the group does not use are given back when they have come
+      for (int t = (mine + 1) / 2; live && t < z.tiles; ++t) {
         const uint32_t st = (T + t) & 1;
+        live = warp_wait(&k_full[st], ((T + t) >> 1) & 1, abort);
+        if (live && lane == 0) bar_arrive(&k_empty[st]);
         if (z.masked(t)) {
-          live = warp_wait(&v_ok[st], (use_ok >> st) & 1, abort);
+          live = live && warp_wait(&v_ok[st], (use_ok >> st) & 1, abort);
           use_ok ^= 1u << st;
         } else {
-          live = warp_wait(&v_full[st], (use_full >> st) & 1, abort);
+          live = live && warp_wait(&v_full[st], (use_full >> st) & 1, abort);
           use_full ^= 1u << st;
         }
-        if (t < mine) {
-          const int halves = z.halves(w, t);
-          const uint64_t vd = v_desc + static_cast<uint64_t>((st * C::OP) >> 4);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (!live || h >= halves) break;
-            live = warp_wait(&p_full[2 * w + h], (use_p >> h) & 1, abort);
-            use_p ^= 1u << h;
-            if (!live) break;
-            fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              umma_ts_lead(lead, tO, tS + h * 32 + kk * 8, vd + static_cast<uint64_t>(((h * kStep + kk * 16) * 128) >> 4),
-                           idesc_16(HD, 1, true), h + kk > 0 || t > 0 ? 1u : 0u);
-            if (h == 0 && halves == 2) umma_commit_lead(lead, &o_half[w]);
-          }
-          if (!live) break;
-          umma_commit_lead(lead, &v_empty[st]);
-          if (t == mine - 1) umma_commit_lead(lead, &o_done[w]);
-        } else if (live && lane == 0) {
-          bar_arrive(&v_empty[st]);
-        }
-        // (over the P that the product reads: products of one thread run in the order of issue)
-        if (t + 1 < z.tiles) live = live && scores(t + 1);
+        if (live && lane == 0) bar_arrive(&v_empty[st]);
       }
       T += z.tiles;
+      n_step += mine;
     }
   } else if (warp == 3 || warp == kSoftmax0 + 8) {
     const int w = warp == 3 ? 0 : 1;
@@ -395,13 +383,13 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t tS = tmem + grp * kRows + lane_base, tO = tmem + 256 + grp * HD + lane_base;
     const float c = sm_scale * kLog2e;
-    const float2 cv = make_float2(c, c);
-    uint32_t n_tile = 0, n_half = 0, n_done = 0;
+    const unsigned long long cv = pair(c, c);
+    uint32_t n_step = 0, n_item = 0;
     Item it;
     bool live = true;
     for (uint32_t k = 0; live && next_item(k, &it); ++k) {
       const Sizes z(it, g.G);
-      const int mine = z.tiles_of(grp);
+      const int mine = z.steps_of(grp);
       if (mine == 0) {
         item_done(k);
         continue;
@@ -410,114 +398,95 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       const bool row_ok = f < it.n * g.G;
       const int see = row_ok ? it.c + row + 1 : z.keys[grp];  // keys that the row sees
       float m = -INFINITY, l = 0.0f;
-      auto scale_o = [&](float x) {  // O times x
-#pragma unroll 1
-        for (int d = 0; d < HD / 16; ++d) {
-          uint32_t y[16];
-          tmem_ld16(tO + 16 * d, y);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * x);
-          tmem_st16(tO + 16 * d, y);
-        }
-        tmem_st_wait();
-      };
-      for (int t = 0; t < mine; ++t) {
-        const int halves = z.halves(grp, t);
-        if (!warp_wait(&s_full[grp], n_tile & 1, abort)) {
+      for (int u = 0; u < mine; ++u, ++n_step) {
+        const uint32_t bf = n_step & 1, tB = tS + bf * kStep;
+        if (!warp_wait(&s_full[2 * grp + bf], (n_step >> 1) & 1, abort)) {
           live = false;
           break;
         }
-        ++n_tile;
-        if (lane == 0 && z.in_turn(grp ^ 1, grp == 0 ? t : t + 1)) bar_arrive(&turn[grp]);
         fence_after();
+        const int vis = see - u * kStep;  // keys of the step that the row sees
+        const bool masked = __any_sync(0xFFFFFFFFu, vis < kStep);
+        bool look = u == 0;  // for the maximum
+        uint32_t pk[32];
+        float s;
 #pragma unroll 1
-        for (int h = 0; h < halves; ++h) {
-          const int vis = see - t * kKeys - h * kStep;  // keys of the half that the row sees
-          const bool masked = __any_sync(0xFFFFFFFFu, vis < kStep);
-          bool look = t + h == 0;  // for the maximum
-          uint32_t pk[2][16];
-          float s;
+        for (;;) {
+          if (look) {
+            float a0 = -INFINITY, a1 = -INFINITY;
 #pragma unroll 1
-          for (;;) {
-            if (look) {
-              float a0 = -INFINITY, a1 = -INFINITY;
-#pragma unroll 1
-              for (int d = 0; d < 4; ++d) {
-                uint32_t y[16];
-                tmem_ld16(tS + kStep * h + 16 * d, y);
-                if (masked)
+            for (int d = 0; d < 4; ++d) {
+              uint32_t y[16];
+              tmem_ld16(tB + 16 * d, y);
+              if (masked)
 #pragma unroll
-                  for (int j = 0; j < 16; ++j) y[j] = 16 * d + j < vis ? y[j] : 0xFF800000u;
+                for (int j = 0; j < 16; ++j) y[j] = 16 * d + j < vis ? y[j] : 0xFF800000u;
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                  a0 = fmax3f(a0, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
-                  a1 = fmax3f(a1, __uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
-                }
+              for (int j = 0; j < 16; j += 4) {
+                a0 = fmax3f(a0, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
+                a1 = fmax3f(a1, __uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
               }
-              const float nm = fmaxf(m, fmaxf(a0, a1) * c);
-              if (t + h > 0) {
-                const float corr = ex2(m - nm);
-                l *= corr;
-                if (h == 1 && !warp_wait(&o_half[grp], n_half & 1, abort)) {
-                  live = false;
-                  break;
-                }
-                fence_after();
-                scale_o(corr);
-              }
-              m = nm;
             }
-            const float2 nv = make_float2(-m, -m);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            uint32_t y[2][32];
-            auto exps = [&](auto hide) {
-              tmem_ld32(tS + kStep * h, y[0]);
-              tmem_wait32(y[0]);
-              tmem_ld32(tS + kStep * h + 32, y[1]);
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                if (q == 1) tmem_wait32(y[1]);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  float2 a = __ffma2_rn(make_float2(__uint_as_float(y[q][2 * j]), __uint_as_float(y[q][2 * j + 1])), cv, nv);
-                  hide(a, 32 * q + 2 * j);
-                  const float2 e = make_float2(ex2(a.x), ex2(a.y));
-                  sum[j & 1] = __fadd2_rn(sum[j & 1], e);
-                  pk[q][j] = pack2_bf16(e.x, e.y);
-                }
+            const float nm = fmaxf(m, fmaxf(a0, a1) * c);
+            if (u > 0) {
+              const float corr = ex2(m - nm);
+              l *= corr;
+              // (the scores of this step came behind the product of the step before the last)
+              if (!warp_wait(&o_step[grp], (n_step - 1) & 1, abort)) {
+                live = false;
+                break;
               }
-            };
-            if (masked)
-              exps([&](float2& a, int j) {
-                a.x = j < vis ? a.x : -INFINITY;
-                a.y = j + 1 < vis ? a.y : -INFINITY;
-              });
-            else
-              exps([](float2&, int) {});
-            const float2 s2 = __fadd2_rn(sum[0], sum[1]);
-            s = s2.x + s2.y;
-            if (look || !__any_sync(0xFFFFFFFFu, !(s <= kTop))) break;
-            look = true;
+              fence_after();
+#pragma unroll 1
+              for (int d = 0; d < HD / 16; ++d) {
+                uint32_t y[16];
+                tmem_ld16(tO + 16 * d, y);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
+                tmem_st16(tO + 16 * d, y);
+              }
+              tmem_st_wait();
+            }
+            m = nm;
           }
-          if (!live) break;
-          l += s;
-          tmem_st16(tS + 32 * h, pk[0]);
-          tmem_st16(tS + 32 * h + 16, pk[1]);
-          tmem_st_wait();
-          fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&p_full[2 * grp + h]);
+          const unsigned long long nv = pair(-m, -m);
+          unsigned long long sum[2] = {0ull, 0ull};
+          unsigned long long y[32];
+          tmem_ld64_pairs(tB, y);
+          auto exps = [&](auto hide) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const unsigned long long a = fma2(y[j], cv, nv);
+              const float e0 = ex2(hide(lo_of(a), 2 * j)), e1 = ex2(hide(hi_of(a), 2 * j + 1));
+              sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
+              pk[j] = pack2_bf16(e0, e1);
+            }
+          };
+          if (masked)
+            exps([&](float a, int j) { return j < vis ? a : -INFINITY; });
+          else
+            exps([](float a, int) { return a; });
+          sum[0] = add2(sum[0], sum[1]);
+          s = lo_of(sum[0]) + hi_of(sum[0]);
+          if (look || !__any_sync(0xFFFFFFFFu, !(s <= kTop))) break;
+          look = true;
         }
         if (!live) break;
-        if (halves == 2) ++n_half;
+        l += s;
+        tmem_st32(tB, pk);
+        tmem_st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&p_full[2 * grp + bf]);
       }
-      if (!live || !warp_wait(&o_done[grp], n_done & 1, abort)) break;
-      ++n_done;
+      live = live && warp_wait(&o_done[grp], n_item & 1, abort);
+      if (!live) break;
+      ++n_item;
       __syncwarp();
       fence_after();
       // a row that sees a V which was taken out gets NaN (the marks are complete: the products are)
       bool poison = false;
-      for (int t = z.common / kKeys; t < mine; ++t) {
+      for (int t = z.common / kKeys; t * kKeys < see; ++t) {
         const uint32_t* bad = s_bad + ((k & 1) * 4 + t - z.common / kKeys) * 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -141,6 +141,71 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
       "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
+// 64 consecutive 32-bit TMEM columns of this thread's lane as 32 register pairs (fp32x2
+// operands need pairs: put together from single registers they cost a move a value)
+__device__ __forceinline__ void tmem_ld64_pairs(uint32_t taddr, unsigned long long (&q)[32]) {
+  asm volatile(
+      "{\n .reg .b32 t<64>;\n"
+      " tcgen05.ld.sync.aligned.32x32b.x64.b32 {t0,t1,t2,t3,t4,t5,t6,t7,t8,t9,t10,t11,t12,t13,t14,t15,t16,t17,t18,t19,t20,t21,t22,t23,t24,t25,t26,t27,t28,t29,t30,t31,t32,t33,t34,t35,t36,t37,t38,t39,t40,t41,t42,t43,t44,t45,t46,t47,t48,t49,t50,t51,t52,t53,t54,t55,t56,t57,t58,t59,t60,t61,t62,t63}, [%32];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      " mov.b64 %0, {t0, t1};\n"
+      " mov.b64 %1, {t2, t3};\n"
+      " mov.b64 %2, {t4, t5};\n"
+      " mov.b64 %3, {t6, t7};\n"
+      " mov.b64 %4, {t8, t9};\n"
+      " mov.b64 %5, {t10, t11};\n"
+      " mov.b64 %6, {t12, t13};\n"
+      " mov.b64 %7, {t14, t15};\n"
+      " mov.b64 %8, {t16, t17};\n"
+      " mov.b64 %9, {t18, t19};\n"
+      " mov.b64 %10, {t20, t21};\n"
+      " mov.b64 %11, {t22, t23};\n"
+      " mov.b64 %12, {t24, t25};\n"
+      " mov.b64 %13, {t26, t27};\n"
+      " mov.b64 %14, {t28, t29};\n"
+      " mov.b64 %15, {t30, t31};\n"
+      " mov.b64 %16, {t32, t33};\n"
+      " mov.b64 %17, {t34, t35};\n"
+      " mov.b64 %18, {t36, t37};\n"
+      " mov.b64 %19, {t38, t39};\n"
+      " mov.b64 %20, {t40, t41};\n"
+      " mov.b64 %21, {t42, t43};\n"
+      " mov.b64 %22, {t44, t45};\n"
+      " mov.b64 %23, {t46, t47};\n"
+      " mov.b64 %24, {t48, t49};\n"
+      " mov.b64 %25, {t50, t51};\n"
+      " mov.b64 %26, {t52, t53};\n"
+      " mov.b64 %27, {t54, t55};\n"
+      " mov.b64 %28, {t56, t57};\n"
+      " mov.b64 %29, {t58, t59};\n"
+      " mov.b64 %30, {t60, t61};\n"
+      " mov.b64 %31, {t62, t63};\n"
+      "}\n"
+      : "=l"(q[0]), "=l"(q[1]), "=l"(q[2]), "=l"(q[3]), "=l"(q[4]), "=l"(q[5]), "=l"(q[6]), "=l"(q[7]), "=l"(q[8]), "=l"(q[9]), "=l"(q[10]), "=l"(q[11]), "=l"(q[12]), "=l"(q[13]), "=l"(q[14]), "=l"(q[15]), "=l"(q[16]), "=l"(q[17]), "=l"(q[18]), "=l"(q[19]), "=l"(q[20]), "=l"(q[21]), "=l"(q[22]), "=l"(q[23]), "=l"(q[24]), "=l"(q[25]), "=l"(q[26]), "=l"(q[27]), "=l"(q[28]), "=l"(q[29]), "=l"(q[30]), "=l"(q[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};\n" ::"r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31]),
+      "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ unsigned long long pair(float x, float y) {
+  return static_cast<unsigned long long>(__float_as_uint(x)) | (static_cast<unsigned long long>(__float_as_uint(y)) << 32);
+}
+__device__ __forceinline__ float lo_of(unsigned long long p) { return __uint_as_float(static_cast<uint32_t>(p)); }
+__device__ __forceinline__ float hi_of(unsigned long long p) { return __uint_as_float(static_cast<uint32_t>(p >> 32)); }
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void regs_inc() {
