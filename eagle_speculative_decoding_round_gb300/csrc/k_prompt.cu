@@ -17,7 +17,7 @@ namespace e3 {
 
 namespace {
 
-constexpr int kTile = 64, kKeys = 64;
+constexpr int kShift = 6, kTile = 1 << kShift, kKeys = 64;
 
 template <int HD>
 struct SimtCfg {
@@ -41,8 +41,9 @@ prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_la
   if (blockIdx.x == 0)  // requests whose sizes are out of bounds
     for (int b = threadIdx.x; b < g.B; b += 256)
       if (!prompt_req(g, b).ok) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+  const PromptReq own = prompt_req(g, threadIdx.x & 31);
   for (long long rank = blockIdx.x;; rank += gridDim.x) {
-    const PromptItem it = find_prompt_item(g, rank);
+    const PromptItem it = find_prompt_item(g, own, rank);
     if (it.b >= g.B) break;
     const PromptReq q = prompt_req(g, it.b);
     const int f0 = it.tile * kTile, rows = min(kTile, q.n * g.G - f0);
@@ -189,7 +190,7 @@ e3_status launch_prompt(const void* Q, const int32_t* row_start, const int32_t* 
   g.H = H;
   g.KVH = kv.n_kv_heads;
   g.G = H / g.KVH;
-  g.tile = kTile;
+  g.shift = kShift;
   g.n_total = n_total;
   g.max_rows = max_rows;
   g.max_kv_len = kv_len ? max_kv_len : 0;

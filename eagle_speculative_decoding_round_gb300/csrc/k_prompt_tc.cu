@@ -4,7 +4,8 @@
 // head, so that a group's heads share the keys and a diagonal is short); one CTA per SM works
 // through items, the longest first.  Two softmax groups take 128 rows each, one thread to a
 // row; both use every tile of 128 keys:
-//   producer (warp 0)  finds the next item, brings K and V tiles by TMA into two stages each
+//   warp 13            finds the next item
+//   producer (warp 0)  brings K and V tiles by TMA into two stages each
 //   issuers (warps 1, 2; one per group)  S = Q K^T, then O += P V with P from tensor memory; each
 //                      group's softmax runs under the other's products
 //   warps 3 and 12     the items' rows of Q; V tiles with keys that some rows do not see: rows of
@@ -33,7 +34,7 @@ constexpr int kRows = 128;       // query rows of a softmax group
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kStep = 64;        // keys of a step
 constexpr int kHalfB = 16384;    // bytes of 64 dims of a tile: [128 rows][128 B], 128-byte swizzle
-constexpr int kThreads = 416;
+constexpr int kThreads = 448;
 constexpr int kSoftmax0 = 4;     // first softmax warp
 constexpr float kTop = 32768.0f;
 
@@ -41,7 +42,7 @@ template <int HD>
 struct TcCfg {
   static constexpr int HALVES = HD / 64;          // of an operand's dims
   static constexpr int OP = HALVES * kHalfB;      // bytes of an operand tile
-  static constexpr int Q = 0, K = 2 * OP, V = K + 2 * OP, BARS = V + 2 * OP;
+  static constexpr int Q = 0, K = 2 * OP, V = K + 2 * OP, OUT = V + 2 * OP, BARS = OUT + 8 * 4096;
   static constexpr int SMEM = BARS + 1024 + 1024;  // (base rounded up to 1024)
 };
 static_assert(TcCfg<128>::SMEM <= 232448, "shared memory of a CTA");
@@ -88,7 +89,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   using C = TcCfg<HD>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  unsigned char *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V;
+  unsigned char *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V, *sOut = sm + C::OUT;
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BARS);
   uint64_t* k_full = bars;          // [stage], as the following
   uint64_t* k_empty = bars + 2;
@@ -127,7 +128,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       bar_init(&q_full[i], 1);
       bar_init(&q_empty[i], 1);
       bar_init(&item_full[i], 1);
-      bar_init(&item_empty[i], 12);  // every warp but the producer
+      bar_init(&item_empty[i], 13);  // every warp but the one that finds the items
     }
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -162,22 +163,11 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   if (warp == 0) {
     uint32_t T = 0, use_full = 0, use_raw = 0;  // tiles; bit st: parity of the stage's next use of v_full, v_raw
     bool live = true;
-    for (uint32_t k = 0; live; ++k) {
-      const long long row = static_cast<long long>(k) * gridDim.x;
-      const PromptItem at = find_prompt_item(g, row + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
-      Item it{-1, 0, 0, 0, 0, 0};
-      if (at.b < g.B) {
-        const PromptReq q = prompt_req(g, at.b);
-        it = Item{at.b, at.kvh, at.tile * 2 * kRows, q.start, q.n, q.c};
-      }
-      if (!warp_wait(&item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort)) break;
-      if (lane == 0) {
-        s_item[k & 1] = it;
-        bar_arrive(&item_full[k & 1]);
-      }
-      __syncwarp();
-      if (it.b < 0 || ((kv.flags & E3_KV_SELFTEST_STALL) && blockIdx.x == 0)) break;  // (keys that never come)
+    Item it;
+    for (uint32_t k = 0; live && next_item(k, &it); ++k) {
       const Sizes z(it, g.G);
+      item_done(k);
+      if ((kv.flags & E3_KV_SELFTEST_STALL) && blockIdx.x == 0) break;  // (keys that never come)
       const int keys = max(z.keys[0], z.keys[1]);
       const int32_t* table = kv.page_table + static_cast<size_t>(it.b) * kv.max_pages;
       // lane i brings keys [i box, (i + 1) box) of a tile; the row of its first one, -1: none
@@ -223,6 +213,25 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         use ^= 1u << st;
         r = r_next;
       }
+    }
+  } else if (warp == kSoftmax0 + 9) {
+    // finds the items, one ahead of the others' work
+    const PromptReq own = prompt_req(g, lane);
+    for (uint32_t k = 0;; ++k) {
+      const long long row = static_cast<long long>(k) * gridDim.x;
+      const PromptItem at = find_prompt_item(g, own, row + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
+      Item it{-1, 0, 0, 0, 0, 0};
+      if (at.b < g.B) {
+        const PromptReq q = prompt_req(g, at.b);
+        it = Item{at.b, at.kvh, at.tile * 2 * kRows, q.start, q.n, q.c};
+      }
+      if (!warp_wait(&item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort)) break;
+      if (lane == 0) {
+        s_item[k & 1] = it;
+        bar_arrive(&item_full[k & 1]);
+      }
+      __syncwarp();
+      if (it.b < 0) break;
     }
   } else if (warp <= 2) {
     // One issuing warp per softmax group: what one waits for passes under the other's products.
@@ -320,7 +329,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         for (int r0 = 0; r0 < kRows; r0 += 32) {
           const int f = it.f0 + w * kRows + r0 + lane, row = f / g.G;
           const int own = f < flat ? (it.start + row) * g.H + it.kvh * g.G + f - row * g.G : -1;
-#pragma unroll 8
+#pragma unroll
           for (int i = 0; i < LPR; ++i) {
             const int rr = r0 + i * (32 / LPR) + lane / LPR;
             const int at = __shfl_sync(0xFFFFFFFFu, own, rr - r0);
@@ -347,7 +356,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         use_raw ^= 1u << st;
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
-          const int rr = w * 64 + i * 32 + lane, key = t * kKeys + rr;
+          const int rr = i * 64 + w * 32 + lane, key = t * kKeys + rr;
           bool bad = false;
           if (key >= z.common) {
             unsigned char* at = sV + st * C::OP + rr * 128;
@@ -363,12 +372,12 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
               bad = max(b & 0xFFFFu, b >> 16) >= 0x7F80u;
             }
             if (bad || key >= keys)
-#pragma unroll 1
+#pragma unroll 8
               for (int c = 0; c < 8 * C::HALVES; ++c)
                 *reinterpret_cast<uint4*>(at + (c >> 3) * kHalfB + (((c + lane) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
           }
           const uint32_t word = __ballot_sync(0xFFFFFFFFu, bad);
-          if (lane == 0) s_bad[((k & 1) * 4 + t - t0) * 4 + 2 * w + i] = word;
+          if (lane == 0) s_bad[((k & 1) * 4 + t - t0) * 4 + 2 * i + w] = word;
         }
         fence_async_smem();  // generic-proxy writes -> tensor core
         __syncwarp();
@@ -496,22 +505,35 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       }
       const size_t at = (static_cast<size_t>(it.start) + row) * g.H + it.kvh * g.G + (f - row * g.G);
       const float inv = poison ? __int_as_float(0x7FC00000) : 1.0f / l;
-      uint4* dst = reinterpret_cast<uint4*>(O + at * HD);
+      // 64 dims of the warp's rows go through its 4 KB of shared memory (16-byte pieces, swizzled),
+      // so that a store takes whole lines: a thread's own row would cost a line for each 16 bytes
+      unsigned char* stage = sOut + (warp - kSoftmax0) * 4096;
+      const int own = row_ok ? static_cast<int>(at) : -1;
 #pragma unroll 1
-      for (int h = 0; h < HD / 32; ++h) {
-        uint32_t y[32];
-        tmem_ld32(tO + 32 * h, y);
-        tmem_wait32(y);
-        if (row_ok) {
+      for (int h = 0; h < HD / 64; ++h) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t y[32];
+          tmem_ld32(tO + 64 * h + 32 * q, y);
+          tmem_wait32(y);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t x[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              x[q] = pack2_bf16(__uint_as_float(y[8 * j + 2 * q]) * inv, __uint_as_float(y[8 * j + 2 * q + 1]) * inv);
-            dst[4 * h + j] = make_uint4(x[0], x[1], x[2], x[3]);
+            for (int e = 0; e < 4; ++e)
+              x[e] = pack2_bf16(__uint_as_float(y[8 * j + 2 * e]) * inv, __uint_as_float(y[8 * j + 2 * e + 1]) * inv);
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + j) ^ (lane & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
           }
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // four rows a store
+          const int rr = 4 * i + (lane >> 3);
+          const int to = __shfl_sync(0xFFFFFFFFu, own, rr);
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4*>(O + static_cast<size_t>(to) * HD + 64 * h + 8 * (lane & 7)) = x;
+        }
+        __syncwarp();
       }
       fence_before();
       if (row_ok) lse[at] = (m + log2f(l)) * kLn2;
@@ -560,7 +582,7 @@ cudaError_t launch_tc(const void* Q, const CUtensorMap& mk, const CUtensorMap& m
 
 e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, float sm_scale, void* O, float* lse,
                            int32_t* dev_err, cudaStream_t s) {
-  g.tile = 2 * kRows;
+  g.shift = 8;  // 2 * kRows
   int box = 16;  // keys of a TMA box: what divides a page, as far as a tile has
   while (box < kKeys && kv.page_size % (2 * box) == 0) box *= 2;
   const unsigned long long rows = static_cast<unsigned long long>(kv.n_pages) * kv.n_kv_heads * kv.page_size;
