@@ -195,7 +195,6 @@ e3_status launch_prompt(const void* Q, const int32_t* row_start, const int32_t* 
   g.max_rows = max_rows;
   g.max_kv_len = kv_len ? max_kv_len : 0;
   g.cap = static_cast<long long>(kv.max_pages) * kv.page_size;
-  g.L = (g.max_kv_len + max_rows + 127) / 128;
   cudaError_t e = cudaErrorInvalidValue;
   if (kv.dt == E3_BF16) return launch_prompt_tc(Q, kv, g, sm_scale, O, lse, dev_err, s);
   switch (kv.head_dim) {
