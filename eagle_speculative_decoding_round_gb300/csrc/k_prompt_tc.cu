@@ -58,6 +58,13 @@ __device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* m, int x,
                : "memory");
 }
 
+__device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint64_t* b) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(su32(b))
+      : "memory");
+}
+
 struct Item {  // what the producer tells the other roles (b < 0: no more)
   int b, kvh, f0, start, n, c;
 };
@@ -83,8 +90,8 @@ struct Sizes {
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
-prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                 const __grid_constant__ e3_kv_layer kv, const __grid_constant__ PromptGeom g, int box, float sm_scale,
+prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                 const __grid_constant__ e3_kv_layer kv, const __grid_constant__ PromptGeom g, int box, bool q_box, float sm_scale,
                  __nv_bfloat16* __restrict__ O, float* __restrict__ lse, int32_t* dev_err) {
   using C = TcCfg<HD>;
   extern __shared__ unsigned char smem_raw[];
@@ -159,6 +166,8 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   // (after a wait that ran out: the phases that the copies in flight complete)
   // bit st: the stage has been loaded, the parity of its last load; of V also whether to v_raw
   uint32_t any_k = 0, par_k = 0, any_v = 0, par_v = 0, raw_v = 0;
+  bool any_q = false;  // (of warps 3 and 12, their group's Q)
+  uint32_t par_q = 0;
 
   if (warp == 0) {
     uint32_t T = 0, use_full = 0, use_raw = 0;  // tiles; bit st: parity of the stage's next use of v_full, v_raw
@@ -322,28 +331,40 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       if (z.keys[w] > 0) {
         if (!warp_wait(&q_empty[w], (n_q & 1) ^ 1, abort)) break;
         ++n_q;
-        constexpr int LPR = HD / 8;          // lanes (16-byte pieces) of a row
-        const int flat = it.n * g.G, c = lane % LPR;
-        unsigned char* slab = sQ + w * C::OP;
-#pragma unroll 1
-        for (int r0 = 0; r0 < kRows; r0 += 32) {
-          const int f = it.f0 + w * kRows + r0 + lane, row = f / g.G;
-          const int own = f < flat ? (it.start + row) * g.H + it.kvh * g.G + f - row * g.G : -1;
+        if (q_box) {
+          // (rows behind the request's last are another's or zeros: nothing is done with them)
+          if (lane == 0) {
+            bar_expect(&q_full[w], C::OP);
 #pragma unroll
-          for (int i = 0; i < LPR; ++i) {
-            const int rr = r0 + i * (32 / LPR) + lane / LPR;
-            const int at = __shfl_sync(0xFFFFFFFFu, own, rr - r0);
-            const __nv_bfloat16* src = Q + static_cast<size_t>(max(at, 0)) * HD + c * 8;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             su32(slab + (c >> 3) * kHalfB + rr * 128 + (((c & 7) ^ (rr & 7)) << 4))),
-                         "l"(src), "r"(at >= 0 ? 16 : 0)
-                         : "memory");
+            for (int h = 0; h < C::HALVES; ++h)
+              tma3d(su32(sQ + w * C::OP + h * kHalfB), &tmQ, h * 64, it.kvh * g.G, it.start + (it.f0 + w * kRows) / g.G, &q_full[w]);
+            any_q = true;
+            par_q = (n_q - 1) & 1;
           }
+        } else {
+          constexpr int LPR = HD / 8;  // lanes (16-byte pieces) of a row
+          const int flat = it.n * g.G, c = lane % LPR;
+          unsigned char* slab = sQ + w * C::OP;
+#pragma unroll 1
+          for (int r0 = 0; r0 < kRows; r0 += 32) {
+            const int f = it.f0 + w * kRows + r0 + lane, row = f / g.G;
+            const int own = f < flat ? (it.start + row) * g.H + it.kvh * g.G + f - row * g.G : -1;
+#pragma unroll 4
+            for (int i = 0; i < LPR; ++i) {
+              const int rr = r0 + i * (32 / LPR) + lane / LPR;
+              const int at = __shfl_sync(0xFFFFFFFFu, own, rr - r0);
+              const __nv_bfloat16* src = Q + static_cast<size_t>(max(at, 0)) * HD + c * 8;
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                               su32(slab + (c >> 3) * kHalfB + rr * 128 + (((c & 7) ^ (rr & 7)) << 4))),
+                           "l"(src), "r"(at >= 0 ? 16 : 0)
+                           : "memory");
+            }
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&q_full[w]);
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&q_full[w]);
       }
       // V tiles with keys that some rows do not see
       const int keys = max(z.keys[0], z.keys[1]), t0 = z.common / kKeys;
@@ -477,7 +498,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
             exps([](float a, int) { return a; });
           sum[0] = add2(sum[0], sum[1]);
           s = lo_of(sum[0]) + hi_of(sum[0]);
-          if (look || !__any_sync(0xFFFFFFFFu, !(s <= kTop))) break;
+          if (look || !__any_sync(0xFFFFFFFFu, row_ok && !(s <= kTop))) break;
           look = true;
         }
         if (!live) break;
@@ -509,24 +530,24 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       // so that a store takes whole lines: a thread's own row would cost a line for each 16 bytes
       unsigned char* stage = sOut + (warp - kSoftmax0) * 4096;
       const int own = row_ok ? static_cast<int>(at) : -1;
+      // (Loops of few instructions: what runs once an item comes from the L2, not the caches.)
 #pragma unroll 1
       for (int h = 0; h < HD / 64; ++h) {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t y[16];
+          tmem_ld16(tO + 64 * h + 16 * q, y);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t y[32];
-          tmem_ld32(tO + 64 * h + 32 * q, y);
-          tmem_wait32(y);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             uint32_t x[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               x[e] = pack2_bf16(__uint_as_float(y[8 * j + 2 * e]) * inv, __uint_as_float(y[8 * j + 2 * e + 1]) * inv);
-            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * q + j) ^ (lane & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((2 * q + j) ^ (lane & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
           }
         }
         __syncwarp();
-#pragma unroll
+#pragma unroll 2
         for (int i = 0; i < 8; ++i) {  // four rows a store
           const int rr = 4 * i + (lane >> 3);
           const int to = __shfl_sync(0xFFFFFFFFu, own, rr);
@@ -544,6 +565,11 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   if (__syncthreads_or(*abort != 0)) {
     // after a wait that ran out, the copies still in flight land (bounded) before the
     // shared memory goes
+    if (any_q) {
+      const uint64_t t0 = gtimer();
+      while (!bar_try(&q_full[warp == 3 ? 0 : 1], par_q) && gtimer() - t0 < kWaitNs) {
+      }
+    }
     if (warp == 0) {
       const uint64_t t0 = gtimer();
       for (int st = 0; st < 2; ++st) {
@@ -565,7 +591,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
 }
 
 template <int HD>
-cudaError_t launch_tc(const void* Q, const CUtensorMap& mk, const CUtensorMap& mv, const e3_kv_layer& kv, const PromptGeom& g, int box,
+cudaError_t launch_tc(const void* Q, const CUtensorMap& mq, bool q_box, const CUtensorMap& mk, const CUtensorMap& mv, const e3_kv_layer& kv, const PromptGeom& g, int box,
                       float sm_scale, void* O, float* lse, int32_t* dev_err, cudaStream_t s) {
   static OncePerDevice<cudaError_t> attrs;
   const cudaError_t e = once_per_device(attrs, [] {
@@ -574,7 +600,7 @@ cudaError_t launch_tc(const void* Q, const CUtensorMap& mk, const CUtensorMap& m
   if (e != cudaSuccess) return e;
   const long long items = prompt_items_bound(g);
   return launch_pdl(prompt_tc_kernel<HD>, dim3(static_cast<unsigned>(std::min<long long>(items, num_sms()))), dim3(kThreads),
-                    TcCfg<HD>::SMEM, s, 1, static_cast<const __nv_bfloat16*>(Q), mk, mv, kv, g, box, sm_scale,
+                    TcCfg<HD>::SMEM, s, 1, static_cast<const __nv_bfloat16*>(Q), mq, mk, mv, kv, g, box, q_box, sm_scale,
                     static_cast<__nv_bfloat16*>(O), lse, dev_err);
 }
 
@@ -590,8 +616,21 @@ e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, f
   CUtensorMap mk, mv;
   E3_REQUIRE(encode_rows_map(&mk, kv.k, rows, kv.head_dim, box) && encode_rows_map(&mv, kv.v, rows, kv.head_dim, box),
              E3_ERR_INVALID_ARG, "prompt_attn: cuTensorMapEncodeTiled rejected K or V");
-  const cudaError_t e = kv.head_dim == 128 ? launch_tc<128>(Q, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, s)
-                                           : launch_tc<64>(Q, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, s);
+  // Q of a softmax group as one box where its rows are whole rows of the request
+  const bool q_box = kRows % g.G == 0;
+  CUtensorMap mq{};
+  if (q_box) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kv.head_dim), static_cast<cuuint64_t>(g.H), static_cast<cuuint64_t>(g.n_total)};
+    const cuuint64_t str[2] = {static_cast<cuuint64_t>(kv.head_dim) * 2, static_cast<cuuint64_t>(g.H) * kv.head_dim * 2};
+    const cuuint32_t qb[3] = {64, static_cast<cuuint32_t>(g.G), static_cast<cuuint32_t>(kRows / g.G)};
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r = encode(&mq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(Q), dims, str, qb, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    E3_REQUIRE(r == CUDA_SUCCESS, E3_ERR_INVALID_ARG, "prompt_attn: cuTensorMapEncodeTiled rejected Q (%d)", static_cast<int>(r));
+  }
+  const cudaError_t e = kv.head_dim == 128 ? launch_tc<128>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, s)
+                                           : launch_tc<64>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, s);
   return e == cudaSuccess ? E3_OK : cuda_status(e, "prompt_tc_kernel");
 }
 
