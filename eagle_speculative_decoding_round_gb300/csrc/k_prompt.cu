@@ -190,6 +190,7 @@ e3_status launch_prompt(const void* Q, const int32_t* row_start, const int32_t* 
   g.H = H;
   g.KVH = kv.n_kv_heads;
   g.G = H / g.KVH;
+  g.inv_G = 1.0f / static_cast<float>(g.G);
   g.shift = kShift;
   g.n_total = n_total;
   g.max_rows = max_rows;

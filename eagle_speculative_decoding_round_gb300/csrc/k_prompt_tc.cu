@@ -4,11 +4,10 @@
 // head, so that a group's heads share the keys and a diagonal is short); one CTA per SM works
 // through items, the longest first.  Two softmax groups take 128 rows each, one thread to a
 // row; both use every tile of 128 keys:
-//   warp 13            finds the next item
 //   producer (warp 0)  brings K and V tiles by TMA into two stages each
 //   issuers (warps 1, 2; one per group)  S = Q K^T, then O += P V with P from tensor memory; each
 //                      group's softmax runs under the other's products
-//   warps 3 and 12     the items' rows of Q; V tiles with keys that some rows do not see: rows of
+//   warp 3             finds the next item; the items' rows of Q; V tiles with keys that some rows do not see: rows of
 //                      V that hold a NaN or an Inf, or nothing yet, leave the product (0 * Inf would
 //                      reach the rows that do not see them), rows that see them get NaN
 //   softmax (2 x 4 warps)  steps of 64 keys in two buffers of tensor memory: exponentials against
@@ -34,7 +33,7 @@ constexpr int kRows = 128;       // query rows of a softmax group
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kStep = 64;        // keys of a step
 constexpr int kHalfB = 16384;    // bytes of 64 dims of a tile: [128 rows][128 B], 128-byte swizzle
-constexpr int kThreads = 448;
+constexpr int kThreads = 384;
 constexpr int kSoftmax0 = 4;     // first softmax warp
 constexpr float kTop = 32768.0f;
 
@@ -65,28 +64,24 @@ __device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* m, int x,
       : "memory");
 }
 
-struct Item {  // what the producer tells the other roles (b < 0: no more)
-  int b, kvh, f0, start, n, c;
-};
-// Sizes of an item that every role derives from it.
-struct Sizes {
-  int keys[2];  // keys that group g's rows reach (0: the group has no rows)
-  int tiles;    // key tiles of the item
-  int common;   // keys that all its rows see
-  __device__ __forceinline__ Sizes(const Item& it, int G) {
-    const int flat = it.n * G;
-    common = it.c + it.f0 / G + 1;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int first = it.f0 + g * kRows;
-      keys[g] = first < flat ? it.c + (min(first + kRows, flat) - 1) / G + 1 : 0;
-    }
-    tiles = (max(keys[0], keys[1]) + kKeys - 1) / kKeys;
-  }
-  __device__ __forceinline__ int steps_of(int g) const { return (keys[g] + kStep - 1) / kStep; }
+// What the warp that finds the items tells the other roles.
+struct Item {
+  int b, kvh;     // request (-1: no more), KV head
+  int start;      // row of Q of the request's first
+  int row, rem;   // the item's first flat row: row of the request, head of the group
+  int flat;       // flat rows from there to the request's end
+  int c;          // keys before the request's rows
+  int keys0, keys1;  // keys that the groups' rows reach (0: the group has no rows)
+  int common;     // keys that all rows see
+  __device__ __forceinline__ int all_keys() const { return max(keys0, keys1); }
+  __device__ __forceinline__ int keys_of(int g) const { return g ? keys1 : keys0; }
+  __device__ __forceinline__ int tiles() const { return (all_keys() + kKeys - 1) / kKeys; }
+  __device__ __forceinline__ int steps_of(int g) const { return (keys_of(g) + kStep - 1) / kStep; }
   // some row of the item does not see all of tile t's keys
   __device__ __forceinline__ bool masked(int t) const { return (t + 1) * kKeys > common; }
 };
+// x / G for x < G + 256: the quotient is at least 1 / 2G off an integer, the product far less
+__device__ __forceinline__ int small_div(int x, float inv_g) { return static_cast<int>((static_cast<float>(x) + 0.5f) * inv_g); }
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -101,7 +96,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   uint64_t* k_full = bars;          // [stage], as the following
   uint64_t* k_empty = bars + 2;
   uint64_t* v_full = bars + 4;      // tiles that every row sees
-  uint64_t* v_raw = bars + 6;       // tiles that warps 3 and 12 look through first,
+  uint64_t* v_raw = bars + 6;       // tiles that warp 3 looks through first,
   uint64_t* v_ok = bars + 8;        // and have
   uint64_t* v_empty = bars + 10;
   uint64_t* s_full = bars + 12;     // [softmax group][buffer]
@@ -124,7 +119,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       bar_init(&k_empty[i], 2);
       bar_init(&v_full[i], 1);
       bar_init(&v_raw[i], 1);
-      bar_init(&v_ok[i], 2);
+      bar_init(&v_ok[i], 1);
       bar_init(&v_empty[i], 2);
       bar_init(&s_full[2 * i], 1);
       bar_init(&s_full[2 * i + 1], 1);
@@ -135,7 +130,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       bar_init(&q_full[i], 1);
       bar_init(&q_empty[i], 1);
       bar_init(&item_full[i], 1);
-      bar_init(&item_empty[i], 13);  // every warp but the one that finds the items
+      bar_init(&item_empty[i], 11);  // every warp but the one that finds the items
     }
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -154,10 +149,10 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;  // columns: S of group g at 128 g (its P over the first half), O at 256 + HD g
   // the item in slot k % 2, or the end; the slot is given back with item_done
-  auto next_item = [&](uint32_t k, Item* it) {
+  auto next_item = [&](uint32_t k, Item& it) {
     if (!warp_wait(&item_full[k & 1], (k >> 1) & 1, abort)) return false;
-    *it = s_item[k & 1];
-    return it->b >= 0;
+    it = s_item[k & 1];
+    return it.b >= 0;
   };
   auto item_done = [&](uint32_t k) {
     __syncwarp();
@@ -166,18 +161,16 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   // (after a wait that ran out: the phases that the copies in flight complete)
   // bit st: the stage has been loaded, the parity of its last load; of V also whether to v_raw
   uint32_t any_k = 0, par_k = 0, any_v = 0, par_v = 0, raw_v = 0;
-  bool any_q = false;  // (of warps 3 and 12, their group's Q)
-  uint32_t par_q = 0;
+  uint32_t any_q = 0, par_q = 0;  // bit w: group w's Q
 
   if (warp == 0) {
     uint32_t T = 0, use_full = 0, use_raw = 0;  // tiles; bit st: parity of the stage's next use of v_full, v_raw
     bool live = true;
     Item it;
-    for (uint32_t k = 0; live && next_item(k, &it); ++k) {
-      const Sizes z(it, g.G);
+    for (uint32_t k = 0; live && next_item(k, it); ++k) {
       item_done(k);
       if ((kv.flags & E3_KV_SELFTEST_STALL) && blockIdx.x == 0) break;  // (keys that never come)
-      const int keys = max(z.keys[0], z.keys[1]);
+      const int keys = it.all_keys(), tiles = it.tiles();
       const int32_t* table = kv.page_table + static_cast<size_t>(it.b) * kv.max_pages;
       // lane i brings keys [i box, (i + 1) box) of a tile; the row of its first one, -1: none
       auto box_row = [&](int t) {
@@ -192,8 +185,8 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         return (page * g.KVH + it.kvh) * kv.page_size + (key - pi * kv.page_size);
       };
       int r = box_row(0);
-      for (int t = 0; t < z.tiles; ++t, ++T) {
-        const int st = T & 1, r_next = t + 1 < z.tiles ? box_row(t + 1) : -1;
+      for (int t = 0; t < tiles; ++t, ++T) {
+        const int st = T & 1, r_next = t + 1 < tiles ? box_row(t + 1) : -1;
         const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, r >= 0)) * static_cast<uint32_t>(box) * HD * 2;
         auto load = [&](uint64_t* full, unsigned char* dst, const CUtensorMap* map) {
           if (lane == 0) bar_expect(full, bytes);
@@ -213,7 +206,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
           live = false;
           break;
         }
-        const bool raw = z.masked(t);
+        const bool raw = it.masked(t);
         load(raw ? &v_raw[st] : &v_full[st], sV, &tmV);
         uint32_t& use = raw ? use_raw : use_full;
         any_v |= 1u << st;
@@ -222,25 +215,6 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         use ^= 1u << st;
         r = r_next;
       }
-    }
-  } else if (warp == kSoftmax0 + 9) {
-    // finds the items, one ahead of the others' work
-    const PromptReq own = prompt_req(g, lane);
-    for (uint32_t k = 0;; ++k) {
-      const long long row = static_cast<long long>(k) * gridDim.x;
-      const PromptItem at = find_prompt_item(g, own, row + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
-      Item it{-1, 0, 0, 0, 0, 0};
-      if (at.b < g.B) {
-        const PromptReq q = prompt_req(g, at.b);
-        it = Item{at.b, at.kvh, at.tile * 2 * kRows, q.start, q.n, q.c};
-      }
-      if (!warp_wait(&item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort)) break;
-      if (lane == 0) {
-        s_item[k & 1] = it;
-        bar_arrive(&item_full[k & 1]);
-      }
-      __syncwarp();
-      if (it.b < 0) break;
     }
   } else if (warp <= 2) {
     // One issuing warp per softmax group: what one waits for passes under the other's products.
@@ -254,10 +228,9 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
     const uint32_t lead = elect_lane();
     Item it;
     bool live = true;
-    for (uint32_t k = 0; live && next_item(k, &it); ++k) {
-      const Sizes z(it, g.G);
+    for (uint32_t k = 0; live && next_item(k, it); ++k) {
       item_done(k);
-      const int mine = z.steps_of(w);
+      const int mine = it.steps_of(w), tiles = it.tiles();
       if (mine > 0) {
         live = warp_wait(&q_full[w], use_q, abort);
         use_q ^= 1u;
@@ -281,7 +254,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       for (int u = 0; live && u < mine; ++u) {
         const uint32_t st = (T + (u >> 1)) & 1, bf = (n_step + u) & 1;
         if (!(u & 1)) {
-          if (z.masked(u >> 1)) {
+          if (it.masked(u >> 1)) {
             live = warp_wait(&v_ok[st], (use_ok >> st) & 1, abort);
             use_ok ^= 1u << st;
           } else {
@@ -304,11 +277,11 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         if (u + 2 < mine) live = scores(u + 2);
       }
       // stages that the group does not use are given back when they have come
-      for (int t = (mine + 1) / 2; live && t < z.tiles; ++t) {
+      for (int t = (mine + 1) / 2; live && t < tiles; ++t) {
         const uint32_t st = (T + t) & 1;
         live = warp_wait(&k_full[st], ((T + t) >> 1) & 1, abort);
         if (live && lane == 0) bar_arrive(&k_empty[st]);
-        if (z.masked(t)) {
+        if (it.masked(t)) {
           live = live && warp_wait(&v_ok[st], (use_ok >> st) & 1, abort);
           use_ok ^= 1u << st;
         } else {
@@ -317,46 +290,79 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         }
         if (live && lane == 0) bar_arrive(&v_empty[st]);
       }
-      T += z.tiles;
+      T += tiles;
       n_step += mine;
     }
-  } else if (warp == 3 || warp == kSoftmax0 + 8) {
-    const int w = warp == 3 ? 0 : 1;
-    uint32_t use_raw = 0, T = 0, n_q = 0;
-    Item it;
+  } else if (warp == 3) {
+    uint32_t use_raw = 0, T = 0, use_q = 3u;  // (bits: parities of the next uses; a fresh barrier counts as released)
     bool live = true;
-    for (uint32_t k = 0; live && next_item(k, &it); ++k) {
-      const Sizes z(it, g.G);
-      // Q of group w: 128 rows of the 256
-      if (z.keys[w] > 0) {
-        if (!warp_wait(&q_empty[w], (n_q & 1) ^ 1, abort)) break;
-        ++n_q;
+    const PromptReq own = prompt_req(g, lane);
+    Item it, next;
+    // finds item k and tells the others
+    auto publish = [&](uint32_t k) {
+      const long long row = static_cast<long long>(k) * gridDim.x;
+      const PromptItem at = find_prompt_item(g, own, row + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
+      next.b = -1;
+      if (at.b < g.B) {
+        const PromptReq q = prompt_req(g, at.b);
+        const int f0 = at.tile * 2 * kRows;
+        next.b = at.b;
+        next.kvh = at.kvh;
+        next.start = q.start;
+        next.row = f0 / g.G;
+        next.rem = f0 - next.row * g.G;
+        next.flat = q.n * g.G - f0;
+        next.c = q.c;
+        next.common = q.c + next.row + 1;
+        next.keys0 = q.c + (f0 + min(kRows, next.flat) - 1) / g.G + 1;
+        next.keys1 = kRows < next.flat ? q.c + (f0 + min(2 * kRows, next.flat) - 1) / g.G + 1 : 0;
+      }
+      if (!warp_wait(&item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort)) return false;
+      if (lane == 0) {
+        s_item[k & 1] = next;
+        bar_arrive(&item_full[k & 1]);
+      }
+      __syncwarp();
+      return true;
+    };
+    live = publish(0);
+    for (uint32_t k = 0; live && next.b >= 0; ++k) {
+      it = next;
+      // Q: 128 rows of each group
+#pragma unroll 1
+      for (int w = 0; live && w < 2; ++w) {
+        if (it.keys_of(w) == 0) continue;
+        if (!warp_wait(&q_empty[w], (use_q >> w) & 1, abort)) {
+          live = false;
+          break;
+        }
+        use_q ^= 1u << w;
         if (q_box) {
           // (rows behind the request's last are another's or zeros: nothing is done with them)
           if (lane == 0) {
             bar_expect(&q_full[w], C::OP);
 #pragma unroll
             for (int h = 0; h < C::HALVES; ++h)
-              tma3d(su32(sQ + w * C::OP + h * kHalfB), &tmQ, h * 64, it.kvh * g.G, it.start + (it.f0 + w * kRows) / g.G, &q_full[w]);
-            any_q = true;
-            par_q = (n_q - 1) & 1;
+              tma3d(su32(sQ + w * C::OP + h * kHalfB), &tmQ, h * 64, it.kvh * g.G, it.start + it.row + small_div(w * kRows, g.inv_G), &q_full[w]);
           }
+          any_q |= 1u << w;
+          par_q = (par_q & ~(1u << w)) | (use_q & (1u << w));  // (the phase that this load completes)
         } else {
           constexpr int LPR = HD / 8;  // lanes (16-byte pieces) of a row
-          const int flat = it.n * g.G, c = lane % LPR;
+          const int c = lane % LPR;
           unsigned char* slab = sQ + w * C::OP;
 #pragma unroll 1
           for (int r0 = 0; r0 < kRows; r0 += 32) {
-            const int f = it.f0 + w * kRows + r0 + lane, row = f / g.G;
-            const int own = f < flat ? (it.start + row) * g.H + it.kvh * g.G + f - row * g.G : -1;
+            const int f = w * kRows + r0 + lane, over = small_div(it.rem + f, g.inv_G);
+            const int at = f < it.flat ? (it.start + it.row + over) * g.H + it.kvh * g.G + it.rem + f - over * g.G : -1;
 #pragma unroll 4
             for (int i = 0; i < LPR; ++i) {
               const int rr = r0 + i * (32 / LPR) + lane / LPR;
-              const int at = __shfl_sync(0xFFFFFFFFu, own, rr - r0);
-              const __nv_bfloat16* src = Q + static_cast<size_t>(max(at, 0)) * HD + c * 8;
+              const int from = __shfl_sync(0xFFFFFFFFu, at, rr - r0);
+              const __nv_bfloat16* src = Q + static_cast<size_t>(max(from, 0)) * HD + c * 8;
               asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                                su32(slab + (c >> 3) * kHalfB + rr * 128 + (((c & 7) ^ (rr & 7)) << 4))),
-                           "l"(src), "r"(at >= 0 ? 16 : 0)
+                           "l"(src), "r"(from >= 0 ? 16 : 0)
                            : "memory");
             }
           }
@@ -366,9 +372,11 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
           if (lane == 0) bar_arrive(&q_full[w]);
         }
       }
+      live = live && publish(k + 1);
+      if (!live) break;
       // V tiles with keys that some rows do not see
-      const int keys = max(z.keys[0], z.keys[1]), t0 = z.common / kKeys;
-      for (int t = t0; t < z.tiles; ++t) {
+      const int keys = it.all_keys(), tiles = it.tiles(), t0 = it.common / kKeys;
+      for (int t = t0; t < tiles; ++t) {
         const int st = (T + t) & 1;
         if (!warp_wait(&v_raw[st], (use_raw >> st) & 1, abort)) {
           live = false;
@@ -376,10 +384,10 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         }
         use_raw ^= 1u << st;
 #pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          const int rr = i * 64 + w * 32 + lane, key = t * kKeys + rr;
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 32 + lane, key = t * kKeys + rr;
           bool bad = false;
-          if (key >= z.common) {
+          if (key >= it.common) {
             unsigned char* at = sV + st * C::OP + rr * 128;
             if (key < keys) {
               __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
@@ -398,14 +406,13 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
                 *reinterpret_cast<uint4*>(at + (c >> 3) * kHalfB + (((c + lane) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
           }
           const uint32_t word = __ballot_sync(0xFFFFFFFFu, bad);
-          if (lane == 0) s_bad[((k & 1) * 4 + t - t0) * 4 + 2 * i + w] = word;
+          if (lane == 0) s_bad[((k & 1) * 4 + t - t0) * 4 + i] = word;
         }
         fence_async_smem();  // generic-proxy writes -> tensor core
         __syncwarp();
         if (lane == 0) bar_arrive(&v_ok[st]);
       }
-      T += z.tiles;
-      item_done(k);
+      T += tiles;
     }
   } else {
     // softmax: warp w of group grp reads TMEM lane quarter warp % 4 (rows 32 quarter ..)
@@ -417,16 +424,15 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
     uint32_t n_step = 0, n_item = 0;
     Item it;
     bool live = true;
-    for (uint32_t k = 0; live && next_item(k, &it); ++k) {
-      const Sizes z(it, g.G);
-      const int mine = z.steps_of(grp);
+    for (uint32_t k = 0; live && next_item(k, it); ++k) {
+      const int mine = it.steps_of(grp);
       if (mine == 0) {
         item_done(k);
         continue;
       }
-      const int f = it.f0 + grp * kRows + r, row = f / g.G;
-      const bool row_ok = f < it.n * g.G;
-      const int see = row_ok ? it.c + row + 1 : z.keys[grp];  // keys that the row sees
+      const int f = grp * kRows + r, over = small_div(it.rem + f, g.inv_G), row = it.row + over;
+      const bool row_ok = f < it.flat;
+      const int see = row_ok ? it.c + row + 1 : it.keys_of(grp);  // keys that the row sees
       float m = -INFINITY, l = 0.0f;
       for (int u = 0; u < mine; ++u, ++n_step) {
         const uint32_t bf = n_step & 1, tB = tS + bf * kStep;
@@ -440,24 +446,18 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         bool look = u == 0;  // for the maximum
         uint32_t pk[32];
         float s;
+        unsigned long long y[32];
+        tmem_ld64_pairs(tB, y);
+        if (masked)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) y[j] = pair(2 * j < vis ? lo_of(y[j]) : -INFINITY, 2 * j + 1 < vis ? hi_of(y[j]) : -INFINITY);
 #pragma unroll 1
         for (;;) {
           if (look) {
-            float a0 = -INFINITY, a1 = -INFINITY;
-#pragma unroll 1
-            for (int d = 0; d < 4; ++d) {
-              uint32_t y[16];
-              tmem_ld16(tB + 16 * d, y);
-              if (masked)
+            float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = 16 * d + j < vis ? y[j] : 0xFF800000u;
-#pragma unroll
-              for (int j = 0; j < 16; j += 4) {
-                a0 = fmax3f(a0, __uint_as_float(y[j]), __uint_as_float(y[j + 1]));
-                a1 = fmax3f(a1, __uint_as_float(y[j + 2]), __uint_as_float(y[j + 3]));
-              }
-            }
-            const float nm = fmaxf(m, fmaxf(a0, a1) * c);
+            for (int j = 0; j < 32; ++j) a[j & 3] = fmax3f(a[j & 3], lo_of(y[j]), hi_of(y[j]));
+            const float nm = fmaxf(m, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * c);
             if (u > 0) {
               const float corr = ex2(m - nm);
               l *= corr;
@@ -469,11 +469,11 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
               fence_after();
 #pragma unroll 1
               for (int d = 0; d < HD / 16; ++d) {
-                uint32_t y[16];
-                tmem_ld16(tO + 16 * d, y);
+                uint32_t x[16];
+                tmem_ld16(tO + 16 * d, x);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * corr);
-                tmem_st16(tO + 16 * d, y);
+                for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * corr);
+                tmem_st16(tO + 16 * d, x);
               }
               tmem_st_wait();
             }
@@ -481,21 +481,13 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
           }
           const unsigned long long nv = pair(-m, -m);
           unsigned long long sum[2] = {0ull, 0ull};
-          unsigned long long y[32];
-          tmem_ld64_pairs(tB, y);
-          auto exps = [&](auto hide) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const unsigned long long a = fma2(y[j], cv, nv);
-              const float e0 = ex2(hide(lo_of(a), 2 * j)), e1 = ex2(hide(hi_of(a), 2 * j + 1));
-              sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
-              pk[j] = pack2_bf16(e0, e1);
-            }
-          };
-          if (masked)
-            exps([&](float a, int j) { return j < vis ? a : -INFINITY; });
-          else
-            exps([](float a, int) { return a; });
+          for (int j = 0; j < 32; ++j) {
+            const unsigned long long a = fma2(y[j], cv, nv);
+            const float e0 = ex2(lo_of(a)), e1 = ex2(hi_of(a));
+            sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
+            pk[j] = pack2_bf16(e0, e1);
+          }
           sum[0] = add2(sum[0], sum[1]);
           s = lo_of(sum[0]) + hi_of(sum[0]);
           if (look || !__any_sync(0xFFFFFFFFu, row_ok && !(s <= kTop))) break;
@@ -516,15 +508,15 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       fence_after();
       // a row that sees a V which was taken out gets NaN (the marks are complete: the products are)
       bool poison = false;
-      for (int t = z.common / kKeys; t * kKeys < see; ++t) {
-        const uint32_t* bad = s_bad + ((k & 1) * 4 + t - z.common / kKeys) * 4;
+      for (int t = it.common / kKeys; t * kKeys < see; ++t) {
+        const uint32_t* bad = s_bad + ((k & 1) * 4 + t - it.common / kKeys) * 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int vis = see - t * kKeys - 32 * i;
           if (vis > 0) poison |= (bad[i] & (vis >= 32 ? ~0u : (1u << vis) - 1u)) != 0u;
         }
       }
-      const size_t at = (static_cast<size_t>(it.start) + row) * g.H + it.kvh * g.G + (f - row * g.G);
+      const size_t at = (static_cast<size_t>(it.start) + row) * g.H + it.kvh * g.G + (it.rem + f - over * g.G);
       const float inv = poison ? __int_as_float(0x7FC00000) : 1.0f / l;
       // 64 dims of the warp's rows go through its 4 KB of shared memory (16-byte pieces, swizzled),
       // so that a store takes whole lines: a thread's own row would cost a line for each 16 bytes
@@ -565,10 +557,12 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   if (__syncthreads_or(*abort != 0)) {
     // after a wait that ran out, the copies still in flight land (bounded) before the
     // shared memory goes
-    if (any_q) {
+    if (warp == 3) {
       const uint64_t t0 = gtimer();
-      while (!bar_try(&q_full[warp == 3 ? 0 : 1], par_q) && gtimer() - t0 < kWaitNs) {
-      }
+      for (int w = 0; w < 2; ++w)
+        if ((any_q >> w) & 1u)
+          while (!bar_try(&q_full[w], (par_q >> w) & 1u) && gtimer() - t0 < kWaitNs) {
+          }
     }
     if (warp == 0) {
       const uint64_t t0 = gtimer();

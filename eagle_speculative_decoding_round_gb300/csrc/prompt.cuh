@@ -12,6 +12,7 @@ namespace e3 {
 struct PromptGeom {
   const int32_t *row_start, *n_rows, *kv_len;  // null: b * max_rows, max_rows, 0
   int B, H, KVH, G;
+  float inv_G;
   int shift;       // a tile has 1 << shift flat rows
   int n_total, max_rows, max_kv_len;
   long long cap;  // slots that a request's pages hold
