@@ -121,6 +121,11 @@ size_t verify8_workspace_bytes(int B, int R, int H, int KVH, int hd, int max_kv_
 e3_status launch_verify8(const void* Q, const e3_kv8_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
                          const uint64_t* mask, int B, int R, int H, int max_kv_len, float sm_scale, void* O, float* lse,
                          int32_t* dev_err, void* ws, size_t ws_bytes, cudaStream_t s);
+bool verify8_uses_tc(int R, int H, int KVH, int hd);
+size_t verify8_tc_workspace_bytes(int B, int R, int H, int KVH, int max_kv_len);
+e3_status launch_verify8_tc(const void* Q, const e3_kv8_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
+                            const uint64_t* mask, int B, int R, int H, int max_kv_len, float sm_scale, void* O, float* lse,
+                            int32_t* dev_err, void* ws, cudaStream_t s);
 size_t prompt_workspace_bytes(int B, int n_total, int max_rows, int H, int KVH, int hd, int max_kv_len, e3_dtype dt);
 e3_status launch_prompt(const void* Q, const int32_t* row_start, const int32_t* n_rows, const e3_kv_layer& kv,
                         const int32_t* kv_len, int B, int n_total, int max_rows, int H, int max_kv_len, float sm_scale,

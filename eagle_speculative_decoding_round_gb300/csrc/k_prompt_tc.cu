@@ -444,7 +444,6 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         const int vis = see - u * kStep;  // keys of the step that the row sees
         const bool masked = __any_sync(0xFFFFFFFFu, vis < kStep);
         bool look = u == 0;  // for the maximum
-        uint32_t pk[32];
         float s;
         unsigned long long y[32];
         tmem_ld64_pairs(tB, y);
@@ -482,11 +481,16 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
           const unsigned long long nv = pair(-m, -m);
           unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const unsigned long long a = fma2(y[j], cv, nv);
-            const float e0 = ex2(lo_of(a)), e1 = ex2(hi_of(a));
-            sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
-            pk[j] = pack2_bf16(e0, e1);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t pk[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const unsigned long long a = fma2(y[8 * i + j], cv, nv);
+              const float e0 = ex2(lo_of(a)), e1 = ex2(hi_of(a));
+              sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
+              pk[j] = pack2_bf16(e0, e1);
+            }
+            tmem_st8(tB + 8 * i, pk);  // (the scores are in registers, for a step that is done again too)
           }
           sum[0] = add2(sum[0], sum[1]);
           s = lo_of(sum[0]) + hi_of(sum[0]);
@@ -495,7 +499,6 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         }
         if (!live) break;
         l += s;
-        tmem_st32(tB, pk);
         tmem_st_wait();
         fence_before();
         __syncwarp();

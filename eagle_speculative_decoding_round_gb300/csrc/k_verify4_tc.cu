@@ -42,19 +42,12 @@
 
 #include "e3_common.cuh"
 #include "e3_kernels.h"
-#include "tcgen05.cuh"
-#include "verify4.cuh"
+#include "verify_tc.cuh"
 
 namespace e3 {
 
 namespace {
 
-constexpr int kRows = 128;   // query rows of a softmax group
-constexpr int kKeys = 128;   // keys of a tile
-constexpr int kStep = 64;    // keys of a step
-constexpr int kHD = 128;
-constexpr int kHalfB = 16384;            // bytes of a 64-dim half of an operand: [128 rows][128 B]
-constexpr int kOpB = 2 * kHalfB;         // bytes of an operand
 constexpr int kCodeB = kKeys * kHD / 2;  // bytes of a tile's codes, per operand
 constexpr int kScaleB = kKeys * kHD / 16;
 constexpr int kRawB = kCodeB + kScaleB;  // of one operand
@@ -65,7 +58,6 @@ constexpr int kTailRing = 8;             // tiles of tree nodes whose factors ar
 constexpr int kThreads = 640;
 constexpr int kSoftmax0 = 4, kDeq0 = 12;
 constexpr int kRegsIssue = 64, kRegsSoftmax = 128, kRegsDeq = 80;
-constexpr int kNodeExp = 24;  // > kTop: a node's weight times a row of V sums below 2^(15 - 24 + 8) of it
 
 template <int RT>
 struct Cfg {
@@ -75,46 +67,6 @@ struct Cfg {
   static constexpr int SMEM = END + 1024;  // (base rounded up to 1024)
 };
 static_assert(Cfg<1>::SMEM <= 232448 && Cfg<2>::SMEM <= 232448, "shared memory of a CTA");
-
-__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
-// 2^e for any int e a float's exponent can meet here (|e| <= 252), as a product of two normals
-__device__ __forceinline__ float pow2f(int e) {
-  const int a = e / 2;
-  return __uint_as_float(static_cast<uint32_t>(127 + a) << 23) * __uint_as_float(static_cast<uint32_t>(127 + e - a) << 23);
-}
-
-// The parts of one CTA's share, one after another; every role walks the same list.
-struct Parts {
-  long long todo;
-  int b, pq, x0, x1;  // the pair; the part's tiles
-  int real, w1;       // the pair's tiles; the end of the part in units, where a pair has `extra` more of them
-  int P, NT, extra;   // the request's length, its prefix tiles
-  __device__ __forceinline__ void take() {
-    w1 = static_cast<int>(min(static_cast<long long>(real + extra), x0 + todo));
-    x1 = min(w1, real);
-    NT = (P + kKeys - 1) / kKeys;
-  }
-  // keys of tile x that exist (more than 128 where it is not the last of its kind)
-  __device__ __forceinline__ int left(const V4Geom& g, int x) const { return x >= NT ? g.R - (x - NT) * kKeys : P - x * kKeys; }
-  // the next part; false at the end of the share
-  __device__ __forceinline__ bool next(const V4Geom& g, const int32_t* kv_len) {
-    todo -= w1 - x0;
-    if (todo <= 0) return false;
-    x0 = 0;
-    if (++pq == g.KVH * g.RG) {
-      pq = 0;
-      for (++b; b < g.B; ++b) {
-        P = kv_len[b];
-        real = pair_units<kKeys>(g, P);
-        if (real > 0) break;
-      }
-      if (b >= g.B) return false;
-    }
-    take();
-    return true;
-  }
-};
 
 // 4-bit values of four words (32 dims of a key) -> fp16 pairs, eight per call: word w, scale e
 __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 e) {
@@ -128,44 +80,6 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, __half2 e) {
                     h2u(__hmul2(u2h(r[3]), e)));
 }
 
-// 32 rows of 256 bytes in a swizzled operand (the first row a multiple of 8): half a warp to
-// a row, lane % 16 the 16-byte piece.  (Loops, not straight code: an instruction that runs
-// once a part costs its fetch.)
-__device__ __forceinline__ unsigned char* row_chunk(unsigned char* slab, int rr, int c) {
-  return slab + (c >> 3) * kHalfB + rr * 128 + (((c & 7) ^ (rr & 7)) << 4);
-}
-// rows `own` (a lane's own row, -1: zeros) of `from` into the slab
-__device__ __forceinline__ void bring_rows(const __nv_bfloat16* from, int own, unsigned char* slab, int lane) {
-  const int c = lane & 15;
-#pragma unroll 8
-  for (int i = 0; i < 16; ++i) {
-    const int rr = 2 * i + (lane >> 4);
-    const int at = __shfl_sync(0xFFFFFFFFu, own, rr);
-    const __nv_bfloat16* src = from + static_cast<size_t>(max(at, 0)) * kHD + c * 8;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(su32(row_chunk(slab, rr, c))), "l"(src), "r"(at >= 0 ? 16 : 0)
-                 : "memory");
-  }
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncwarp();
-}
-// largest magnitude of row `rr` as bf16 bits (a NaN: 0x7FFF).  A thread to a row: the
-// swizzle gives the eight lanes that read together banks of their own, and no shuffles are
-// needed (half a warp to a row, with them: 6000 cycles for 32 rows, so 1500).
-__device__ __forceinline__ uint32_t row_top(unsigned char* slab, int rr) {
-  __nv_bfloat162 m = __float2bfloat162_rn(0.0f);
-#pragma unroll 8
-  for (int c = 0; c < 16; ++c) {
-    const uint4 y = *reinterpret_cast<const uint4*>(row_chunk(slab, rr, c));
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&y);
-    m = __hmax2_nan(m, __hmax2_nan(__hmax2_nan(__habs2(h[0]), __habs2(h[1])), __hmax2_nan(__habs2(h[2]), __habs2(h[3]))));
-  }
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(&m);
-  return max(w & 0xFFFFu, w >> 16);
-}
-__device__ __forceinline__ void row_clear(unsigned char* slab, int rr) {
-#pragma unroll 1
-  for (int c = 0; c < 16; ++c) *reinterpret_cast<uint4*>(row_chunk(slab, rr, c)) = make_uint4(0u, 0u, 0u, 0u);
-}
 // Row `rr` from bf16 to fp16 in place, its largest magnitude `top` scaled to [1, 4) by a power
 // of two, whose even exponent is returned, which keeps its bits down to 2^-24 of it.  A row with a NaN or an Inf becomes zeros.
 __device__ __forceinline__ int row_to_half(unsigned char* slab, int rr, uint32_t top) {
@@ -742,83 +656,6 @@ verify4_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ e
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
-// Merge of a pair's records.  A record holds its values as [dims / 4][rows][4], so that the
-// threads of the kernel above, a row each, write whole lines; here a block takes 8 rows of a
-// pair, a warp NQ * 16 dims of each: lane % 8 is the row, lane / 8 the four dims (the second
-// four 16 dims on).  NQ = 1 has more loads in flight where a pair has many records, NQ = 2
-// less to set up where there are many rows: 1 and 32 requests' 61 nodes, whole calls, us:
-// NQ = 1 21.3 and 314, NQ = 2 24.7 and 296.
-template <int RT, int NQ>
-__global__ void __launch_bounds__(256 / NQ)
-verify4_tc_merge_kernel(const int32_t* __restrict__ kv_len,
-                        const __grid_constant__ V4Geom g, const float* __restrict__ ws_o, const float2* __restrict__ ws_ml,
-                        const int32_t* __restrict__ ends, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
-  constexpr int ROWS = RT * kRows, SPLIT = RT == 1 ? 2 : 1, AHEAD = 8 / NQ;
-  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) * (4 * NQ) + (lane >> 3);
-  const int strips = (g.G * g.R + 7) / 8;  // of a KV head (8 divides ROWS: none crosses a tile)
-  const int b = blockIdx.x / (g.KVH * strips), in = blockIdx.x - b * (g.KVH * strips), kvh = in / strips;
-  const int r = (in - kvh * strips) * 8 + (lane & 7), rt = r / ROWS;  // row of the KV head
-  const bool ok = r < g.G * g.R;
-  const size_t pair = (static_cast<size_t>(b) * g.KVH + kvh) * g.RG + rt;
-  const int i = ok ? r / g.G : 0;
-  const size_t row = (static_cast<size_t>(b) * g.R + i) * g.H + kvh * g.G + (ok ? r - i * g.G : 0);
-  pdl_wait();
-  pdl_trigger();
-  const int c0 = ends[2 * pair], c1 = ends[2 * pair + 1];
-  // (a worker that gave up, its error word set, may not have left its number)
-  if (pair_units<kKeys>(g, kv_len[b]) == 0 || c0 < 0 || c1 < c0 || c1 >= g.workers) return;
-  const int n = ok ? (c1 - c0 + 1) * SPLIT : 0;
-  const size_t rec = (pair + c0) * SPLIT;
-  const float2* ml = ws_ml + rec * ROWS + (r - rt * ROWS);
-  const float4* val = reinterpret_cast<const float4*>(ws_o + rec * (ROWS * kHD)) + quad * ROWS + (r - rt * ROWS);
-  // the weights are kept relative to the largest base so far
-  float M = -INFINITY, acc[4 * NQ], den = 0.0f;
-#pragma unroll
-  for (int u = 0; u < 4 * NQ; ++u) acc[u] = 0.0f;
-  for (int q0 = 0; q0 < n; q0 += AHEAD) {
-    float2 y[AHEAD];
-    float4 x[AHEAD][NQ];
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      y[u] = make_float2(-INFINITY, 0.0f);
-      if (q0 + u < n) {
-        y[u] = ml[(q0 + u) * ROWS];
-#pragma unroll
-        for (int k = 0; k < NQ; ++k) x[u][k] = val[static_cast<size_t>(q0 + u) * (ROWS * kHD / 4) + 4 * k * ROWS];
-      }
-    }
-    float top = M;
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u)
-      if (y[u].y != 0.0f) top = fmaxf(top, y[u].x);
-    if (top > M) {
-      const float f = ex2(M - top);
-      M = top;
-      den *= f;
-#pragma unroll
-      for (int u = 0; u < 4 * NQ; ++u) acc[u] *= f;
-    }
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u)
-      if (y[u].y != 0.0f) {  // (0: a record without keys, whose values were never written; a NaN sum stays one)
-        const float w = y[u].y * ex2(y[u].x - M);
-        den += w;
-#pragma unroll
-        for (int k = 0; k < NQ; ++k) {
-          acc[4 * k] = fmaf(w, x[u][k].x, acc[4 * k]), acc[4 * k + 1] = fmaf(w, x[u][k].y, acc[4 * k + 1]);
-          acc[4 * k + 2] = fmaf(w, x[u][k].z, acc[4 * k + 2]), acc[4 * k + 3] = fmaf(w, x[u][k].w, acc[4 * k + 3]);
-        }
-      }
-  }
-  if (!ok) return;
-  const float inv = den != 0.0f ? 1.0f / den : 0.0f;
-#pragma unroll
-  for (int k = 0; k < NQ; ++k)
-    reinterpret_cast<uint2*>(O + row * kHD)[quad + 4 * k] =
-        make_uint2(pack2_bf16(acc[4 * k] * inv, acc[4 * k + 1] * inv), pack2_bf16(acc[4 * k + 2] * inv, acc[4 * k + 3] * inv));
-  if (quad == 0) lse[row] = den != 0.0f ? (M + log2f(den)) * kLn2 : -INFINITY;
-}
-
 V4Geom make_geom_tc(int B, int R, int H, int KVH, int max_kv_len) {
   V4Geom g{};
   g.B = B;
@@ -864,13 +701,7 @@ cudaError_t launch_tc(const __nv_bfloat16* q, const e3_kv4_layer& kv, const e3_k
   const cudaError_t e = launch_pdl(verify4_tc_kernel<RT>, dim3(g.workers), dim3(kThreads), Cfg<RT>::SMEM, s, 1, q, kv, tail,
                                    kv_len, mask, g, sm_scale, ws_o, ws_ml, ends, dev_err);
   if (e != cudaSuccess) return e;
-  const unsigned blocks = static_cast<unsigned>(g.B) * g.KVH * ((g.G * g.R + 7) / 8);
-  const float* co = ws_o;
-  const float2* cml = ws_ml;
-  const int32_t* ce = ends;
-  if (blocks > 4u * g.workers)
-    return launch_pdl(verify4_tc_merge_kernel<RT, 2>, dim3(blocks), dim3(128), 0, s, 1, kv_len, g, co, cml, ce, o, lse);
-  return launch_pdl(verify4_tc_merge_kernel<RT, 1>, dim3(blocks), dim3(256), 0, s, 1, kv_len, g, co, cml, ce, o, lse);
+  return launch_tc_merge<RT, RT == 1 ? 2 : 1>(kv_len, g, ws_o, ws_ml, ends, o, lse, s);
 }
 
 }  // namespace

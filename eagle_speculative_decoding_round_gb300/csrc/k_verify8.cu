@@ -584,6 +584,7 @@ cudaError_t launch_mma(const __nv_bfloat16* q, const e3_kv8_layer& kv, const e3_
 }  // namespace
 
 size_t verify8_workspace_bytes(int B, int R, int H, int KVH, int hd, int max_kv_len) {
+  if (verify8_uses_tc(R, H, KVH, hd)) return verify8_tc_workspace_bytes(B, R, H, KVH, max_kv_len);
   const V4Geom g = make_geom(B, R, H, KVH, hd, max_kv_len);
   return records(g) * g.rows * (hd * sizeof(float) + sizeof(float2)) + pairs(g) * 2 * sizeof(int32_t);
 }
@@ -594,6 +595,8 @@ e3_status launch_verify8(const void* Q, const e3_kv8_layer& kv, const e3_kv_laye
   const size_t need = verify8_workspace_bytes(B, R, H, kv.n_kv_heads, kv.head_dim, max_kv_len);
   E3_REQUIRE(ws_bytes >= need, E3_ERR_CAPACITY, "tree_verify_attn8: workspace of %zu bytes needed, %zu given", need,
              ws_bytes);
+  if (verify8_uses_tc(R, H, kv.n_kv_heads, kv.head_dim))
+    return launch_verify8_tc(Q, kv, tail, kv_len, mask, B, R, H, max_kv_len, sm_scale, O, lse, dev_err, ws, s);
   V4Geom g = make_geom(B, R, H, kv.n_kv_heads, kv.head_dim, max_kv_len);
   g.cap = static_cast<long long>(kv.max_pages) * kv.page_size;
   float* ws_o = static_cast<float*>(ws);

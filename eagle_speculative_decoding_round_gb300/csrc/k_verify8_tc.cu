@@ -1,0 +1,747 @@
+// k_verify8_tc.cu -- tree_verify_attn8 on the 5th-generation tensor cores (head_dim 128, more
+// than 32 query rows per KV head).
+//
+// Work is cut as in verify4.cuh: a pair is (request, KV head, tile of RT * 128 query rows),
+// its units are tiles of 128 prefix keys and then of 128 tree nodes; one CTA per SM takes
+// an equal share of all units.  RT softmax groups of 128 rows each use every tile:
+//   producer (warp 0)      K's codes by TMA into two stages, as the products read them; V's codes
+//                          into one; the blocks' exponents
+//   issuers (warps 1, 2; one per group)  S = Q K^T in steps of 64 keys, into two buffers of tensor
+//                          memory, then O += P V with P from tensor memory
+//   dequantizers (4 warps) V's codes -> fp16 (exact) in 128-byte-swizzled shared memory; the
+//                          tree nodes' rows
+//   softmax (RT x 4 warps) one thread per row: exponentials against the base so far, P over S
+// K is never converted: codes are the operand.  A row of Q, scaled by a power of two to [2^6, 2^8),
+// is the sum of two e4m3 parts, exactly down to 2^-10 of its largest value (a bf16 value has
+// eight significant bits, a part four; below that to 2^-18 of it): S = (q1 + q2) K is two
+// products at twice the rate of 16-bit ones.  Nodes' K is split the same way, four products.
+// K's exponents and Q's power meet the scores, V's exponents the weights: O is kept in units of
+// the largest V exponent of the part so far, a step's weights carry 2^(their block's exponent -
+// that one), which goes into the exponential's argument and comes back out of the row's sum.
+// Nodes' V runs in bf16 as it is, their weights good to 2^-8 with 2^-kNodeExp on them.
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "e3_common.cuh"
+#include "e3_kernels.h"
+#include "tensor_map.cuh"
+#include "verify_tc.cuh"
+
+namespace e3 {
+
+namespace {
+
+constexpr int kCodeB = kKeys * kHD;   // bytes of a tile's codes, per operand
+constexpr int kTailRing = 4;          // tiles of tree nodes whose factors are kept (three are in flight at most)
+constexpr int kExpRing = 8;           // tiles whose exponents are kept
+constexpr int kMinShift = -60;        // of a block's weights: below it they are zeros in fp16 anyhow
+// Warpgroups: 0 = producer and issuers, 1 and 2 = softmax, 3 = dequantizers.  Registers move from
+// the others to the softmax groups; launch_tc checks that the launch brings the sum.
+constexpr int kThreads = 512;
+constexpr int kSoftmax0 = 4, kDeq0 = 12;
+constexpr int kRegsIssue = 96, kRegsSoftmax = 160, kRegsDeq = 96;
+
+template <int RT>
+struct Cfg {
+  // Q: two parts of each group; K: two stages, a second half for the nodes' second parts; V: two stages
+  static constexpr int Q = 0, K = RT * 2 * kCodeB, V = K + 2 * 2 * kCodeB, RAW = V + 2 * kOpB, FAC = RAW + kCodeB;
+  static constexpr int BARS = FAC + kTailRing * kKeys * 4, END = BARS + 2048;
+  static constexpr int SMEM = END + 1024;  // (base rounded up to 1024)
+};
+static_assert(Cfg<2>::SMEM <= 232448, "shared memory of a CTA");
+
+__device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint64_t* b) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(su32(b))
+               : "memory");
+}
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float pow2n(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// A row of bf16 values (16-byte pieces at `src`, null: zeros) in two e4m3 parts, row `rr` of `hi` and `lo`, its largest
+// magnitude scaled to [2^6, 2^8) by a power of two with an even exponent: returns the exponent that takes it back, or
+// 1000 for a row with a NaN or an Inf, which becomes zeros.
+__device__ __forceinline__ int row_to_parts(const uint4* src, unsigned char* hi, unsigned char* lo, int rr) {
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  uint32_t top = 0u;
+#pragma unroll 4
+  for (int c = 0; c < 16; ++c) {
+    const uint4 x = src ? src[c] : none;
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+  }
+  top = max(top & 0xFFFFu, top >> 16);
+  const bool odd = top >= 0x7F80u;
+  const int ex = (min(static_cast<int>(max(top >> 7, 1u)), 254) - 127) & ~1;
+  const float f0 = pow2n((6 - ex) / 2), f1 = pow2n(6 - ex - (6 - ex) / 2);  // (2^132 for a row of zeros)
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {  // 16 values
+    const uint4 x[2] = {src ? src[2 * c] : none, src ? src[2 * c + 1] : none};
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint4& y = x[q >> 1];
+      const uint32_t w[2] = {q & 1 ? y.z : y.x, q & 1 ? y.w : y.y};
+      uint32_t a[2], b[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float2 v = __fmul2_rn(make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)), make_float2(f0, f0));
+        v = odd ? make_float2(0.0f, 0.0f) : __fmul2_rn(v, make_float2(f1, f1));
+        a[e] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+        const float2 g = __half22float2(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(a[e]), __NV_E4M3))));
+        b[e] = __nv_cvt_float2_to_fp8x2(make_float2(v.x - g.x, v.y - g.y), __NV_SATFINITE, __NV_E4M3);
+      }
+      h[q] = a[0] | (a[1] << 16);
+      l[q] = b[0] | (b[1] << 16);
+    }
+    const int at = rr * 128 + ((c ^ (rr & 7)) << 4);
+    *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+  }
+  return odd ? 1000 : ex - 6;
+}
+
+// The steps of a part's tiles: 64 keys each, one for a tile with 64 keys or fewer.
+struct Step {
+  int x, h;
+  __device__ __forceinline__ void next(const Parts& p, const V4Geom& g) {
+    if (h == 0 && p.left(g, x) > kStep)
+      h = 1;
+    else
+      h = 0, ++x;
+  }
+  __device__ __forceinline__ bool last_of_tile(const Parts& p, const V4Geom& g) const { return h == 1 || p.left(g, x) <= kStep; }
+};
+
+template <int RT>
+__global__ void __launch_bounds__(kThreads, 1)
+verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                  const __grid_constant__ e3_kv8_layer kv, const __grid_constant__ e3_kv_layer tail, const int32_t* __restrict__ kv_len,
+                  const uint64_t* __restrict__ mask, const __grid_constant__ V4Geom g, int box, float sm_scale,
+                  float* __restrict__ ws_o, float2* __restrict__ ws_ml, int32_t* __restrict__ ends, int32_t* dev_err) {
+  using C = Cfg<RT>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V, *sRaw = sm + C::RAW;
+  float* s_fac = reinterpret_cast<float*>(sm + C::FAC);  // [kTailRing][128] root of the factor of each tree node's scores
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BARS);
+  uint64_t* k_full = bars;         // [stage] prefix codes
+  uint64_t* n_full = bars + 2;     // [stage] tree nodes' K
+  uint64_t* k_empty = bars + 4;    // [stage]
+  uint64_t* raw_full = bars + 6;   // V's codes (nothing where the tile is of nodes)
+  uint64_t* raw_empty = bars + 7;
+  uint64_t* v_full = bars + 8;     // [stage]
+  uint64_t* v_empty = bars + 10;   // [stage]
+  uint64_t* s_full = bars + 12;    // [softmax group][buffer]
+  uint64_t* p_full = bars + 16;    // [softmax group][buffer]
+  uint64_t* o_step = bars + 20;    // [softmax group] the product with a step's V
+  uint64_t* o_done = bars + 22;    // [softmax group] the part's last
+  uint64_t* q_full = bars + 24;    // [softmax group]
+  uint64_t* q_empty = bars + 26;   // [softmax group]
+  int8_t* s_exp = reinterpret_cast<int8_t*>(bars + 28);            // [kExpRing][K, V][8 x 16 keys]
+  uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_exp + kExpRing * 16);  // [kTailRing][4] nodes with a non-finite V
+  uint32_t* tmem_slot = s_bad + 4 * kTailRing;
+  volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&k_full[i], 1);
+      bar_init(&n_full[i], 4);
+      bar_init(&k_empty[i], RT);
+      bar_init(&v_full[i], 4);
+      bar_init(&v_empty[i], RT);
+      bar_init(&s_full[2 * i], 1);
+      bar_init(&s_full[2 * i + 1], 1);
+      bar_init(&p_full[2 * i], 4);
+      bar_init(&p_full[2 * i + 1], 4);
+      bar_init(&o_step[i], 1);
+      bar_init(&o_done[i], 1);
+      bar_init(&q_full[i], 4);
+      bar_init(&q_empty[i], 1);
+    }
+    bar_init(raw_full, 1);
+    bar_init(raw_empty, 4);
+    *abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(su32(tmem_slot)), "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  if (cta == 0)  // requests whose length is out of bounds
+    for (int b = threadIdx.x; b < g.B; b += kThreads)
+      if (pair_units<kKeys>(g, kv_len[b]) == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+  const V4Place at = find_place<kKeys>(g, kv_len, cta);
+  bool work = at.b < g.B;
+  Parts first{};
+  if (work) {
+    first.b = at.b;
+    first.P = kv_len[at.b];
+    first.todo = at.share;
+    first.real = pair_units<kKeys>(g, first.P);
+    first.extra = at.extra;
+    const long long off = at.share * cta - at.before;
+    first.pq = static_cast<int>(off / (first.real + at.extra));
+    first.x0 = static_cast<int>(off - static_cast<long long>(first.pq) * (first.real + at.extra));
+    first.take();
+    if (first.x1 <= first.x0) work = first.next(g, kv_len);
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  pdl_trigger();
+  const uint32_t tmem = *tmem_slot;  // columns: S buffer i of group w at 128 w + 64 i (its P over the first half), O at 256 + 128 w
+  const int Qn = g.KVH * g.RG;
+  uint32_t any_k = 0, par_k = 0, n_raw = 0;  // (producer) bit st: the stage has been loaded, its last load's parity; raw loads
+
+  if (warp < kSoftmax0) {
+    regs_dec<kRegsIssue>();
+    if (warp == 0 && work) {
+      Parts p = first;
+      bool live = !(cta == 0 && (tail.flags & E3_KV_SELFTEST_STALL));  // (keys that never come)
+      uint32_t T = 0, use_k = 0;  // tiles; bit st: parity of the stage's next use of k_full
+      const int log_block = __ffs(kv.block) - 1;
+      do {
+        const int kvh = p.pq / g.RG;
+        const int32_t* table = kv.page_table + static_cast<size_t>(p.b) * kv.max_pages;
+        // lane i brings keys [i box, (i + 1) box) of a tile: the row of its first one, -1: none
+        auto key_row = [&](int key) {
+          const int pi = key / kv.page_size;
+          int page = table[pi];
+          if (page < 0 || page >= kv.n_pages) {
+            dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+            page = 0;
+          }
+          return (page * g.KVH + kvh) * kv.page_size + (key - pi * kv.page_size);
+        };
+        auto box_row = [&](int x) {
+          const int key = x * kKeys + lane * box;
+          return lane * box < kKeys && key < p.P ? key_row(key) : -1;
+        };
+        // lanes 0 .. 7 (K) and 8 .. 15 (V): the exponent of 16 keys of the tile (those behind the prefix: the first's)
+        auto exponent = [&](int x) {
+          if (lane >= 16) return 0;
+          int key = x * kKeys + 16 * (lane & 7);
+          if (key >= p.P) key = x * kKeys;
+          return static_cast<int>((lane < 8 ? kv.k_exp : kv.v_exp)[key_row(key) >> log_block]);
+        };
+        int r = p.x0 < p.NT ? box_row(p.x0) : -1, e = p.x0 < p.NT ? exponent(p.x0) : 0;
+        for (int x = p.x0; live && x < p.x1; ++x, ++T) {
+          const int st = T & 1;
+          const bool nodes = x >= p.NT;
+          const int r_next = x + 1 < min(p.x1, p.NT) ? box_row(x + 1) : -1, e_next = x + 1 < min(p.x1, p.NT) ? exponent(x + 1) : 0;
+          if (!warp_wait(&k_empty[st], ((T >> 1) & 1) ^ 1, abort)) {
+            live = false;
+            break;
+          }
+          const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, r >= 0)) * static_cast<uint32_t>(box) * kHD;
+          if (!nodes) {
+            // (tile T - kExpRing's exponents have been read: its steps' weights came before the scores of tile T - 4)
+            if (lane < 16) s_exp[(T % kExpRing) * 16 + lane] = static_cast<int8_t>(e);
+            __syncwarp();
+            if (lane == 0) bar_expect(&k_full[st], bytes);
+            __syncwarp();
+            if (r >= 0) tma2d(su32(sK + st * 2 * kCodeB) + lane * box * 128, &tmK, 0, r, &k_full[st]);
+            any_k |= 1u << st;
+            par_k = (par_k & ~(1u << st)) | (use_k & (1u << st));
+            use_k ^= 1u << st;
+          }
+          if (!warp_wait(raw_empty, (T & 1) ^ 1, abort)) {
+            live = false;
+            break;
+          }
+          if (!nodes) {
+            if (lane == 0) bar_expect(raw_full, bytes);
+            __syncwarp();
+            if (r >= 0) tma2d(su32(sRaw) + lane * box * 128, &tmV, 0, r, raw_full);
+          } else if (lane == 0) {
+            bar_arrive(raw_full);  // (K's stage is free, too)
+          }
+          ++n_raw;
+          r = r_next;
+          e = e_next;
+        }
+      } while (live && p.next(g, kv_len));
+    }
+    if ((warp == 1 || (RT == 2 && warp == 2)) && work) {
+      // One issuing warp per softmax group, kept together (see k_prompt_tc.cu)
+      const int w = warp - 1;
+      const uint64_t q_desc = desc_sw128(su32(sQ + w * 2 * kCodeB), 16, 1024), k_desc = desc_sw128(su32(sK), 16, 1024);
+      const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
+      const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
+      const uint32_t lead = elect_lane();
+      uint32_t T = 0, n_step = 0, n_part = 0, use_k = 0, use_n = 0;  // (bits: parities of the next uses)
+      Parts p = first;
+      bool live = true;
+      do {
+        live = warp_wait(&q_full[w], n_part++ & 1, abort);
+        // scores run two steps ahead of the products with V
+        Step s{p.x0, 0}, v{p.x0, 0};
+        uint32_t n_s = n_step;
+        auto scores = [&]() {
+          const uint32_t st = (T + (s.x - p.x0)) & 1, bf = n_s & 1;
+          const bool nodes = s.x >= p.NT;
+          if (s.h == 0) {
+            if (nodes) {
+              if (!warp_wait(&n_full[st], (use_n >> st) & 1, abort)) return false;
+              use_n ^= 1u << st;
+            } else {
+              if (!warp_wait(&k_full[st], (use_k >> st) & 1, abort)) return false;
+              use_k ^= 1u << st;
+            }
+          }
+          const uint64_t kd = k_desc + static_cast<uint64_t>((st * 2 * kCodeB + s.h * (kStep * 128)) >> 4);
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma8_lead(lead, tS + bf * kStep, q_desc + static_cast<uint64_t>((part * kCodeB + kk * 32) >> 4),
+                         kd + static_cast<uint64_t>((kk * 32) >> 4), idesc_e4m3(kStep), part + kk > 0 ? 1u : 0u);
+          if (nodes)
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma8_lead(lead, tS + bf * kStep, q_desc + static_cast<uint64_t>((part * kCodeB + kk * 32) >> 4),
+                           kd + static_cast<uint64_t>((kCodeB + kk * 32) >> 4), idesc_e4m3(kStep), 1u);
+          umma_commit_lead(lead, &s_full[2 * w + bf]);
+          const bool tile_end = s.last_of_tile(p, g);
+          if (tile_end) umma_commit_lead(lead, &k_empty[st]);
+          if (tile_end && s.x + 1 == p.x1) umma_commit_lead(lead, &q_empty[w]);
+          s.next(p, g);
+          ++n_s;
+          return true;
+        };
+        for (int i = 0; i < 2; ++i)
+          if (live && s.x < p.x1) live = scores();
+        while (live && v.x < p.x1) {
+          const uint32_t tile = T + (v.x - p.x0), st = tile & 1, bf = n_step & 1;
+          if (v.h == 0) live = warp_wait(&v_full[st], (tile >> 1) & 1, abort);
+          live = live && warp_wait(&p_full[2 * w + bf], (n_step >> 1) & 1, abort);
+          if (!live) break;
+          fence_after();
+          const uint64_t vd = v_desc + static_cast<uint64_t>((st * kOpB + v.h * (kStep * 128)) >> 4);
+          const uint32_t id = v.x >= p.NT ? idesc_16(kHD, 1, true) : idesc_16(kHD, 1, false);  // tree nodes' V stays bf16
+          const bool start = v.x == p.x0 && v.h == 0;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            umma_ts_lead(lead, tO, tS + bf * kStep + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id, kk > 0 || !start ? 1u : 0u);
+          umma_commit_lead(lead, &o_step[w]);
+          const bool tile_end = v.last_of_tile(p, g);
+          if (tile_end) umma_commit_lead(lead, &v_empty[st]);
+          if (tile_end && v.x + 1 == p.x1) umma_commit_lead(lead, &o_done[w]);
+          v.next(p, g);
+          ++n_step;
+          // over the P that the product reads: products of one thread run in the order of issue
+          if (s.x < p.x1) live = scores();
+        }
+        T += p.x1 - p.x0;
+      } while (live && p.next(g, kv_len));
+    }
+  } else if (warp >= kDeq0) {
+    regs_dec<kRegsDeq>();
+    if (work) {
+      const int dw = warp & 3;
+      Parts p = first;
+      int x = p.x0, ntail = 0;
+      for (uint32_t T = 0;; ++T) {
+        const uint32_t st = T & 1;
+        const bool nodes = x >= p.NT;
+        if (!warp_wait(raw_full, T & 1, abort)) break;
+        if (!warp_wait(&v_empty[st], ((T >> 1) & 1) ^ 1, abort)) break;
+        unsigned char* dst = sV + st * kOpB;
+        const int left = p.left(g, x);
+        if (!nodes) {
+          // eight lanes to a key, 16 dims each.  The lanes of the second half's dims store their two
+          // 16-byte pieces in the other order, so that the banks of the eight lanes that store
+          // together differ
+          const int j = lane & 7, kr = lane >> 3, flip = j >> 2;
+          const uint32_t codes = su32(sRaw) + (dw * 32 + kr) * 128 + j * 16;
+          const uint32_t out = su32(dst) + flip * kHalfB + (dw * 32 + kr) * 128 + (((2 * (j & 3) + flip) ^ kr) << 4);
+          const int lim = left - (dw * 32 + kr);
+#pragma unroll 4
+          for (int i = 0; i < 8; ++i) {  // keys 4 i on; their rows' swizzle: 4 (i % 2) more
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(codes + i * 512));
+            uint32_t y[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const uint32_t c = q & 1 ? w[q >> 1] >> 16 : w[q >> 1] & 0xFFFFu;
+              y[q] = h2u(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3))));
+              if (4 * i >= lim) y[q] = 0u;  // beyond the prefix: adds 0 whatever the slot holds
+            }
+            const uint32_t at = (out ^ ((i & 1) << 6)) + i * 512;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(flip ? y[4] : y[0]), "r"(flip ? y[5] : y[1]),
+                         "r"(flip ? y[6] : y[2]), "r"(flip ? y[7] : y[3]) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16u), "r"(flip ? y[0] : y[4]), "r"(flip ? y[1] : y[5]),
+                         "r"(flip ? y[2] : y[6]), "r"(flip ? y[3] : y[7]) : "memory");
+          }
+        } else {
+          const int slot = ntail % kTailRing, kvh = p.pq / g.RG;
+          int own = -1;  // this lane's row of the warp's 32
+          if (dw * 32 + lane < left) {
+            const int j = (x - p.NT) * kKeys + dw * 32 + lane, pi = j / tail.page_size;
+            const int page = tail.page_table[static_cast<size_t>(p.b) * tail.max_pages + pi];
+            if (page >= 0 && page < tail.n_pages)
+              own = (page * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size);
+            else
+              dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
+          }
+          // a node with a NaN or an Inf leaves the product: its scores get a NaN factor, rows
+          // that see its V are marked
+          unsigned char* k0 = sK + st * 2 * kCodeB;
+          const __nv_bfloat16* krow = static_cast<const __nv_bfloat16*>(tail.k) + static_cast<size_t>(max(own, 0)) * kHD;
+          const int ex = row_to_parts(own >= 0 ? reinterpret_cast<const uint4*>(krow) : nullptr, k0, k0 + kCodeB, dw * 32 + lane);
+          s_fac[slot * kKeys + dw * 32 + lane] = ex == 1000 ? __int_as_float(0x7FC00000) : pow2f(ex / 2);
+          unsigned char* slab = dst + dw * 32 * 128;
+          bring_rows(static_cast<const __nv_bfloat16*>(tail.v), own, slab, lane);
+          const uint32_t top = row_top(slab, lane);
+          const uint32_t bad = __ballot_sync(0xFFFFFFFFu, top >= 0x7F80u);
+          if (lane == 0) s_bad[slot * 4 + dw] = bad;
+          if (top >= 0x7F80u) row_clear(slab, lane);
+          ++ntail;
+        }
+        fence_async_smem();  // generic-proxy writes -> tensor core
+        __syncwarp();
+        if (lane == 0) {
+          if (nodes) bar_arrive(&n_full[st]);
+          bar_arrive(&v_full[st]);
+          bar_arrive(raw_empty);
+        }
+        if (++x == p.x1) {
+          if (!p.next(g, kv_len)) break;
+          x = p.x0;
+        }
+      }
+    }
+  } else {
+    regs_inc<kRegsSoftmax>();
+    // softmax: warp w of group grp reads TMEM lane quarter warp % 4 (rows 32 quarter ..)
+    const int grp = (warp - kSoftmax0) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t tS = tmem + grp * 128 + lane_base, tO = tmem + 256 + grp * 128 + lane_base;
+    if (grp < RT && work) {
+      Parts p = first;
+      uint32_t T = 0, n_step = 0, n_part = 0;
+      int ntail = 0;
+      bool live = true;
+      do {
+        const int kvh = p.pq / g.RG, rg = p.pq - kvh * g.RG;
+        const int gr = (rg * RT + grp) * kRows + r;  // row of the KV head
+        const bool row_ok = gr < g.G * g.R;
+        const int node = row_ok ? gr / g.G : 0, head = kvh * g.G + (row_ok ? gr - node * g.G : 0);
+        if (!warp_wait(&q_empty[grp], (n_part & 1) ^ 1, abort)) {
+          live = false;
+          break;
+        }
+        unsigned char* q0 = sQ + grp * 2 * kCodeB;
+        const __nv_bfloat16* qrow = Q + ((static_cast<size_t>(p.b) * g.R + node) * g.H + head) * kHD;
+        const int q_ex = row_to_parts(row_ok ? reinterpret_cast<const uint4*>(qrow) : nullptr, q0, q0 + kCodeB, r);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&q_full[grp]);
+        // Factors of the scores.  The nodes' meets a score between the two halves of the node's own, the
+        // prefix's takes Q's and K's exponents in one power, so that neither alone carries it past the
+        // range; held within the range: 0 or Inf would make NaN of an unseen key's -Inf or of a score of 0.
+        const float nan = __int_as_float(0x7FC00000);
+        const float c0 = sm_scale * kLog2e;
+        const float c_nodes = q_ex == 1000 ? nan : fminf(sm_scale * kLog2e * pow2f(q_ex), 3e38f);
+        float m = -INFINITY, l = 0.0f;
+        int unit = 0;  // O's unit, as an exponent
+        const int tail0 = ntail;
+        const int words = (g.R + 63) >> 6;
+        const uint64_t* mrow = mask + (static_cast<size_t>(p.b) * g.R + node) * words;
+        bool begun = false;
+        for (int x = p.x0; live && x < p.x1; ++x, ++T) {
+          const bool nodes = x >= p.NT;
+          const int left = p.left(g, x), halves = left > kStep ? 2 : 1;
+          const int slot = ntail % kTailRing;
+#pragma unroll 1
+          for (int h = 0; h < halves; ++h, ++n_step) {
+            const uint32_t bf = n_step & 1, tB = tS + bf * kStep;
+            // keys the row sees: those that exist, or the ancestors among the nodes
+            const int here = left - h * kStep;
+            uint64_t see = here >= 64 ? ~0ull : (1ull << here) - 1ull;
+            if (nodes) {
+              const int wd = 2 * (x - p.NT) + h;
+              see &= row_ok && wd < words ? mrow[wd] : 0ull;
+            }
+            if (!warp_wait(&s_full[2 * grp + bf], (n_step >> 1) & 1, abort)) {
+              live = false;
+              break;
+            }
+            fence_after();
+            unsigned long long y[32];
+            tmem_ld64_pairs(tB, y);
+            // a factor for the scores of each 16 keys, and what is added to their exponents
+            float c[4];
+            int d[4];
+            int top = kNodeExp;
+            if (nodes) {
+              const float4* fac = reinterpret_cast<const float4*>(s_fac + slot * kKeys + h * kStep);
+              const unsigned long long cn = pair(c_nodes, c_nodes);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float4 f = fac[j];
+                const unsigned long long f0 = pair(f.x, f.y), f1 = pair(f.z, f.w), zero = pair(0.0f, 0.0f);
+                y[2 * j] = fma2(fma2(fma2(y[2 * j], f0, zero), cn, zero), f0, zero);
+                y[2 * j + 1] = fma2(fma2(fma2(y[2 * j + 1], f1, zero), cn, zero), f1, zero);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) c[i] = 1.0f, d[i] = -kNodeExp;
+            } else {
+              const int8_t* ex = s_exp + (T % kExpRing) * 16 + 4 * h;
+              const char4 ke = *reinterpret_cast<const char4*>(ex), ve = *reinterpret_cast<const char4*>(ex + 8);
+              const int kx[4] = {ke.x, ke.y, ke.z, ke.w};
+              d[0] = ve.x, d[1] = ve.y, d[2] = ve.z, d[3] = ve.w;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                c[i] = fminf(fmaxf(c0 * pow2n(min(max((q_ex == 1000 ? 0 : q_ex) + kx[i], -126), 126)), 1e-37f), 3e38f);
+              if (q_ex == 1000) c[0] = c[1] = c[2] = c[3] = nan;  // (the bounds would drop it)
+              top = max(max(d[0], d[1]), max(d[2], d[3]));
+            }
+            // O's unit grows with V's exponents, and becomes the nodes' behind the prefix
+            float o_f = 1.0f;
+            bool rescale = false;
+            if (!begun || (nodes && unit != kNodeExp) || (!nodes && top > unit)) {
+              if (begun) {
+                o_f = pow2f(min(max(unit - top, -126), 126));
+                rescale = true;
+              }
+              unit = top;
+            }
+            if (!nodes)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) d[i] = max(d[i] - unit, kMinShift);
+            if (!__all_sync(0xFFFFFFFFu, see == ~0ull)) {
+              const uint32_t s0 = static_cast<uint32_t>(see), s1 = static_cast<uint32_t>(see >> 32);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const uint32_t s = j < 16 ? s0 : s1;
+                y[j] = pair(s & (1u << ((2 * j) & 31)) ? lo_of(y[j]) : -INFINITY, s & (1u << ((2 * j + 1) & 31)) ? hi_of(y[j]) : -INFINITY);
+              }
+            }
+            // Exponentials against the base so far.  Where a row's sum passes 2^kTop (or it has no
+            // base yet) its maximum is looked for, the base moved and the step done again.
+            bool look = !begun;
+            float s;
+#pragma unroll 1
+            for (;;) {
+              if (look) {
+                float nm = m;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  float a = -INFINITY;
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) a = fmax3f(a, lo_of(y[8 * i + j]), hi_of(y[8 * i + j]));
+                  nm = fmaxf(nm, a * c[i] - kHead);
+                }
+                if (nm != m) {
+                  const float corr = ex2(m - nm);
+                  l *= corr;
+                  o_f *= corr;
+                  m = nm;
+                }
+                rescale = rescale || begun;
+              }
+              const float base = m == -INFINITY ? 0.0f : m;  // (a row that has seen no key: weights of 0)
+              float total = 0.0f;
+              auto exps = [&](auto pack) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const unsigned long long cv = pair(c[i], c[i]);
+                  const float n = static_cast<float>(d[i]) - base;
+                  const unsigned long long nv = pair(n, n);
+                  unsigned long long sum = 0ull;
+                  uint32_t pk[8];
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    const unsigned long long a = fma2(y[8 * i + j], cv, nv);
+                    const float e0 = ex2(lo_of(a)), e1 = ex2(hi_of(a));
+                    sum = add2(sum, pair(e0, e1));
+                    pk[j] = pack(e0, e1);
+                  }
+                  tmem_st8(tB + 8 * i, pk);  // (the scores are in registers, for a step that is done again too)
+                  total = fmaf(lo_of(sum) + hi_of(sum), pow2n(-d[i]), total);
+                }
+              };
+              if (nodes)
+                exps([](float a, float b) { return pack2_bf16(a, b); });
+              else
+                exps([](float a, float b) { return h2u(__floats2half2_rn(a, b)); });
+              s = total;
+              if (look || !__any_sync(0xFFFFFFFFu, !(s <= 32768.0f) || (m == -INFINITY && see != 0ull))) break;
+              look = true;
+            }
+            l += s;
+            if (rescale) {
+              // (the scores of this step came behind the product of the step before the last)
+              if (!warp_wait(&o_step[grp], (n_step - 1) & 1, abort)) {
+                live = false;
+                break;
+              }
+              fence_after();
+#pragma unroll 1
+              for (int k = 0; k < 8; ++k) {
+                uint32_t z[16];
+                tmem_ld16(tO + 16 * k, z);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[j] = __float_as_uint(__uint_as_float(z[j]) * o_f);
+                tmem_st16(tO + 16 * k, z);
+              }
+              tmem_st_wait();
+            }
+            tmem_st_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&p_full[2 * grp + bf]);
+            begun = true;
+          }
+          if (nodes) ++ntail;
+        }
+        if (!live || !warp_wait(&o_done[grp], n_part & 1, abort)) {
+          live = false;
+          break;
+        }
+        ++n_part;
+        __syncwarp();
+        fence_after();
+        // a row that sees a node with a non-finite V gets NaN (the marks are complete: the
+        // products with V are)
+        bool poison = false;
+        for (int x = max(p.x0, p.NT); x < p.x1; ++x) {
+          const uint32_t* bad = s_bad + (tail0 + x - max(p.x0, p.NT)) % kTailRing * 4;
+          const int wd = 2 * (x - p.NT);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (row_ok && wd + h < words)
+              poison |= (mrow[wd + h] & (bad[2 * h] | (static_cast<uint64_t>(bad[2 * h + 1]) << 32))) != 0ull;
+        }
+        // the part's record: o normalized by its own sum, the base and the sum
+        const size_t rec = static_cast<size_t>(p.b) * Qn + p.pq + cta;
+        const int rrow = grp * kRows + r;
+        const float inv = poison ? nan : l != 0.0f ? 1.0f / l : 0.0f, o_unit = pow2f(unit);
+        float4* dst = reinterpret_cast<float4*>(ws_o + rec * (RT * kRows * kHD)) + rrow;
+#pragma unroll 1
+        for (int h = 0; h < 8; ++h) {
+          uint32_t z[16];
+          tmem_ld16(tO + 16 * h, z);
+          if (row_ok) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              dst[(4 * h + j) * (RT * kRows)] =
+                  make_float4(__uint_as_float(z[4 * j]) * inv * o_unit, __uint_as_float(z[4 * j + 1]) * inv * o_unit,
+                              __uint_as_float(z[4 * j + 2]) * inv * o_unit, __uint_as_float(z[4 * j + 3]) * inv * o_unit);
+          }
+        }
+        fence_before();
+        if (row_ok) ws_ml[rec * (RT * kRows) + rrow] = make_float2(m, l);
+        if (grp == 0 && r == 0) {
+          int32_t* e = ends + 2 * (static_cast<size_t>(p.b) * Qn + p.pq);
+          if (p.x0 == 0) e[0] = cta;
+          if (p.x1 == p.real) e[1] = cta;
+        }
+      } while (p.next(g, kv_len));
+    }
+  }
+  fence_before();
+  if (__syncthreads_or(*abort != 0)) {
+    // after a wait that ran out, the copies still in flight land (bounded) before the
+    // shared memory goes
+    if (warp == 0) {
+      const uint64_t t0 = gtimer();
+      for (int st = 0; st < 2; ++st)
+        if ((any_k >> st) & 1u)
+          while (!bar_try(&k_full[st], (par_k >> st) & 1u) && gtimer() - t0 < kWaitNs) {
+          }
+      if (n_raw > 0)
+        while (!bar_try(raw_full, (n_raw - 1) & 1u) && gtimer() - t0 < kWaitNs) {
+        }
+      while (gtimer() - t0 < 50000) {  // and so have the products
+      }
+      if (lane == 0) dev_flag(dev_err, E3_DEV_ERR_TIMEOUT);
+    }
+    __syncthreads();
+  }
+  fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+V4Geom make_geom_tc(int B, int R, int H, int KVH, int max_kv_len) {
+  V4Geom g{};
+  g.B = B;
+  g.R = R;
+  g.H = H;
+  g.KVH = KVH;
+  g.G = H / KVH;
+  g.rows = g.G * R <= kRows ? kRows : 2 * kRows;
+  g.RG = (g.G * R + g.rows - 1) / g.rows;
+  g.max_kv_len = max_kv_len;
+  g.workers = num_sms();
+  g.min_share = 1;
+  // what a part costs by itself (Q, the nodes, a record), in tiles, where shares are long enough
+  g.extra = 4;
+  g.extra_from = 5;
+  return g;
+}
+
+size_t record_rows(const V4Geom& g) { return (static_cast<size_t>(g.B) * g.KVH * g.RG + g.workers) * g.rows; }
+
+template <int RT>
+cudaError_t launch_tc(const __nv_bfloat16* q, const CUtensorMap& mk, const CUtensorMap& mv, const e3_kv8_layer& kv, const e3_kv_layer& tail,
+                      const int32_t* kv_len, const uint64_t* mask, const V4Geom& g, int box, float sm_scale, float* ws_o, float2* ws_ml,
+                      int32_t* ends, __nv_bfloat16* o, float* lse, int32_t* dev_err, cudaStream_t s) {
+  static OncePerDevice<cudaError_t> attrs;
+  const cudaError_t ea = once_per_device(attrs, [] {
+    cudaError_t e = cudaFuncSetAttribute(verify8_tc_kernel<RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<RT>::SMEM);
+    if (e != cudaSuccess) return e;
+    // a warpgroup that asked for registers which the launch did not bring would wait for ever
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, verify8_tc_kernel<RT>);
+    if (e != cudaSuccess) return e;
+    return kThreads / 128 * fa.numRegs < kRegsIssue + 2 * kRegsSoftmax + kRegsDeq ? cudaErrorLaunchOutOfResources : cudaSuccess;
+  });
+  if (ea != cudaSuccess) return ea;
+  const cudaError_t e = launch_pdl(verify8_tc_kernel<RT>, dim3(g.workers), dim3(kThreads), Cfg<RT>::SMEM, s, 1, q, mk, mv, kv, tail,
+                                   kv_len, mask, g, box, sm_scale, ws_o, ws_ml, ends, dev_err);
+  if (e != cudaSuccess) return e;
+  return launch_tc_merge<RT, 1>(kv_len, g, ws_o, ws_ml, ends, o, lse, s);
+}
+
+}  // namespace
+
+// Up to 32 query rows per KV head the granule kernel's one or two tiles of 16 rows cost less.
+bool verify8_uses_tc(int R, int H, int KVH, int hd) { return hd == kHD && H / KVH * R > 32; }
+
+size_t verify8_tc_workspace_bytes(int B, int R, int H, int KVH, int max_kv_len) {
+  const V4Geom g = make_geom_tc(B, R, H, KVH, max_kv_len);
+  return record_rows(g) * (kHD * sizeof(float) + sizeof(float2)) +
+         static_cast<size_t>(g.B) * g.KVH * g.RG * 2 * sizeof(int32_t);
+}
+
+e3_status launch_verify8_tc(const void* Q, const e3_kv8_layer& kv, const e3_kv_layer& tail, const int32_t* kv_len,
+                            const uint64_t* mask, int B, int R, int H, int max_kv_len, float sm_scale, void* O, float* lse,
+                            int32_t* dev_err, void* ws, cudaStream_t s) {
+  V4Geom g = make_geom_tc(B, R, H, kv.n_kv_heads, max_kv_len);
+  g.cap = static_cast<long long>(kv.max_pages) * kv.page_size;
+  int box = 16;  // keys of a TMA box: what divides a page, as far as a tile has
+  while (box < kKeys && kv.page_size % (2 * box) == 0) box *= 2;
+  const unsigned long long rows = static_cast<unsigned long long>(kv.n_pages) * kv.n_kv_heads * kv.page_size;
+  E3_REQUIRE(rows < (1ull << 31), E3_ERR_SHAPE, "tree_verify_attn8: %llu rows of K", rows);
+  CUtensorMap mk, mv;
+  E3_REQUIRE(encode_bytes_map(&mk, kv.k, rows, box, true) && encode_bytes_map(&mv, kv.v, rows, box, false), E3_ERR_INVALID_ARG,
+             "tree_verify_attn8: cuTensorMapEncodeTiled rejected K or V");
+  float* ws_o = static_cast<float*>(ws);
+  float2* ws_ml = reinterpret_cast<float2*>(ws_o + record_rows(g) * kHD);
+  int32_t* ends = reinterpret_cast<int32_t*>(ws_ml + record_rows(g));
+  const auto launch = g.rows == kRows ? launch_tc<1> : launch_tc<2>;
+  const cudaError_t e = launch(static_cast<const __nv_bfloat16*>(Q), mk, mv, kv, tail, kv_len, mask, g, box, sm_scale, ws_o, ws_ml, ends,
+                               static_cast<__nv_bfloat16*>(O), lse, dev_err, s);
+  return e == cudaSuccess ? E3_OK : cuda_status(e, "verify8_tc kernels");
+}
+
+}  // namespace e3

@@ -134,8 +134,8 @@ typedef struct {
  * thread waits on a barrier that nothing arrives on: the bounded wait runs out
  * after about a second, the kernel sets E3_DEV_ERR_TIMEOUT in dev_err, waits for
  * its own copies in flight, frees its tensor memory and returns; O and lse are not
- * valid.  In tree_verify_attn4's, with the bit on the tail, and in prompt_attn's bf16
- * kernel, one CTA waits for keys that nothing brings, with the same end.  Other paths and
+ * valid.  In tree_verify_attn4's and tree_verify_attn8's, with the bit on the tail, and in
+ * prompt_attn's bf16 kernel, one CTA waits for keys that nothing brings, with the same end.  Other paths and
  * calls ignore the bit. */
 #define E3_KV_SELFTEST_STALL 0x40000000
 typedef struct {

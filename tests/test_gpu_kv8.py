@@ -445,3 +445,22 @@ def test_verify_attn8_many_requests_of_differing_length(B, R, H, KVH, hd, most):
     assert torch.equal(O, O2) and torch.equal(lse, lse2)
     assert not torch.any(O == 55.0) and not torch.any(lse == 55.0)
     attn_check(d, O, lse, requests=[0, 1, 2, B // 2, B - 1])
+
+
+@pytest.mark.parametrize("R,H", [(20, 16), (40, 16)])
+def test_verify_attn8_wait_that_runs_out(R, H):
+    """The self-test bit on the tail: a tile that never comes ends the call with the error word set,
+    after the waits' bound, and leaves nothing behind that the next call on the same buffers meets."""
+    d = attn_inputs(R, 2, R, H, 4, 128, [900, 300], 64, 32)
+    dev = {}
+    need = e3.eagle3_verify8_workspace_bytes(2, R, H, 4, 128, 900)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    attn_call(d, dev=dev, ws=ws)
+    torch.cuda.synchronize()
+    _, _, err = attn_call(d, dev=dev, ws=ws, tail_flags=e3.E3_KV_SELFTEST_STALL)
+    torch.cuda.synchronize()
+    assert int(err.item()) == e3.E3_DEV_ERR_TIMEOUT
+    O, lse, err = attn_call(d, dev=dev, ws=ws)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    attn_check(d, O, lse)
