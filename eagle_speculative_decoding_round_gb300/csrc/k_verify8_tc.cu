@@ -8,17 +8,16 @@
 //                          into one; the blocks' exponents
 //   issuers (warps 1, 2; one per group)  S = Q K^T in steps of 64 keys, into two buffers of tensor
 //                          memory, then O += P V with P from tensor memory
-//   dequantizers (4 warps) V's codes -> fp16 (exact) in 128-byte-swizzled shared memory; the
+//   dequantizers (4 warps) V's codes -> bf16 in 128-byte-swizzled shared memory; the
 //                          tree nodes' rows
 //   softmax (RT x 4 warps) one thread per row: exponentials against the base so far, P over S
 // K is never converted: codes are the operand.  A row of Q, scaled by a power of two to [2^6, 2^8),
 // is the sum of two e4m3 parts, exactly down to 2^-10 of its largest value (a bf16 value has
 // eight significant bits, a part four; below that to 2^-18 of it): S = (q1 + q2) K is two
 // products at twice the rate of 16-bit ones.  Nodes' K is split the same way, four products.
-// K's exponents and Q's power meet the scores, V's exponents the weights: O is kept in units of
-// the largest V exponent of the part so far, a step's weights carry 2^(their block's exponent -
-// that one), which goes into the exponential's argument and comes back out of the row's sum.
-// Nodes' V runs in bf16 as it is, their weights good to 2^-8 with 2^-kNodeExp on them.
+// K's exponents and Q's power meet the scores.  V's codes become bf16 values, exactly, with their
+// scale on them, as the nodes' V is: a shift and one product by a power of two for each pair; the
+// weights are good to 2^-8 (bf16).
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -36,12 +35,11 @@ namespace {
 constexpr int kCodeB = kKeys * kHD;   // bytes of a tile's codes, per operand
 constexpr int kTailRing = 4;          // tiles of tree nodes whose factors are kept (three are in flight at most)
 constexpr int kExpRing = 8;           // tiles whose exponents are kept
-constexpr int kMinShift = -60;        // of a block's weights: below it they are zeros in fp16 anyhow
 // Warpgroups: 0 = producer and issuers, 1 and 2 = softmax, 3 = dequantizers.  Registers move from
 // the others to the softmax groups; launch_tc checks that the launch brings the sum.
 constexpr int kThreads = 512;
 constexpr int kSoftmax0 = 4, kDeq0 = 12;
-constexpr int kRegsIssue = 96, kRegsSoftmax = 160, kRegsDeq = 96;
+constexpr int kRegsIssue = 96, kRegsSoftmax = 152, kRegsDeq = 112;
 
 template <int RT>
 struct Cfg {
@@ -59,6 +57,11 @@ __device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* m, int x,
 }
 // 2^e for e in [-126, 127]
 __device__ __forceinline__ float pow2n(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+__device__ __forceinline__ uint32_t b2u(__nv_bfloat162 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __nv_bfloat162 u2b(uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); }
+// 2^e in both halves, e in [-126, 127]
+__device__ __forceinline__ __nv_bfloat162 power(int e) { return u2b(static_cast<uint32_t>(127 + e) * 0x00800080u); }
 
 // A row of bf16 values (16-byte pieces at `src`, null: zeros) in two e4m3 parts, row `rr` of `hi` and `lo`, its largest
 // magnitude scaled to [2^6, 2^8) by a power of two with an even exponent: returns the exponent that takes it back, or
@@ -139,8 +142,9 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
   uint64_t* o_done = bars + 22;    // [softmax group] the part's last
   uint64_t* q_full = bars + 24;    // [softmax group]
   uint64_t* q_empty = bars + 26;   // [softmax group]
-  int8_t* s_exp = reinterpret_cast<int8_t*>(bars + 28);            // [kExpRing][K, V][8 x 16 keys]
-  uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_exp + kExpRing * 16);  // [kTailRing][4] nodes with a non-finite V
+  float* s_k2 = reinterpret_cast<float*>(bars + 28);          // [kExpRing][8] K's scale of 16 keys each
+  int* s_ve = reinterpret_cast<int*>(s_k2 + kExpRing * 8);    // [kExpRing][8] V's exponent
+  uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_ve + kExpRing * 8);  // [kTailRing][4] nodes with a non-finite V
   uint32_t* tmem_slot = s_bad + 4 * kTailRing;
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -222,18 +226,21 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           const int key = x * kKeys + lane * box;
           return lane * box < kKeys && key < p.P ? key_row(key) : -1;
         };
-        // lanes 0 .. 7 (K) and 8 .. 15 (V): the exponent of 16 keys of the tile (those behind the prefix: the first's)
+        // lanes 0 .. 7: K's scale and V's exponent of 16 keys of the tile (those behind the prefix: the first's)
         auto exponent = [&](int x) {
-          if (lane >= 16) return 0;
-          int key = x * kKeys + 16 * (lane & 7);
+          if (lane >= 8) return make_int2(0, 0);
+          int key = x * kKeys + 16 * lane;
           if (key >= p.P) key = x * kKeys;
-          return static_cast<int>((lane < 8 ? kv.k_exp : kv.v_exp)[key_row(key) >> log_block]);
+          const int at = key_row(key) >> log_block;
+          return make_int2(kv.k_exp[at], kv.v_exp[at]);
         };
-        int r = p.x0 < p.NT ? box_row(p.x0) : -1, e = p.x0 < p.NT ? exponent(p.x0) : 0;
+        int r = p.x0 < p.NT ? box_row(p.x0) : -1;
+        int2 e = p.x0 < p.NT ? exponent(p.x0) : make_int2(0, 0);
         for (int x = p.x0; live && x < p.x1; ++x, ++T) {
           const int st = T & 1;
           const bool nodes = x >= p.NT;
-          const int r_next = x + 1 < min(p.x1, p.NT) ? box_row(x + 1) : -1, e_next = x + 1 < min(p.x1, p.NT) ? exponent(x + 1) : 0;
+          const int r_next = x + 1 < min(p.x1, p.NT) ? box_row(x + 1) : -1;
+          const int2 e_next = x + 1 < min(p.x1, p.NT) ? exponent(x + 1) : make_int2(0, 0);
           if (!warp_wait(&k_empty[st], ((T >> 1) & 1) ^ 1, abort)) {
             live = false;
             break;
@@ -241,7 +248,7 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, r >= 0)) * static_cast<uint32_t>(box) * kHD;
           if (!nodes) {
             // (tile T - kExpRing's exponents have been read: its steps' weights came before the scores of tile T - 4)
-            if (lane < 16) s_exp[(T % kExpRing) * 16 + lane] = static_cast<int8_t>(e);
+            if (lane < 8) s_k2[(T % kExpRing) * 8 + lane] = pow2n(max(e.x, -126)), s_ve[(T % kExpRing) * 8 + lane] = e.y;
             __syncwarp();
             if (lane == 0) bar_expect(&k_full[st], bytes);
             __syncwarp();
@@ -325,11 +332,11 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           if (!live) break;
           fence_after();
           const uint64_t vd = v_desc + static_cast<uint64_t>((st * kOpB + v.h * (kStep * 128)) >> 4);
-          const uint32_t id = v.x >= p.NT ? idesc_16(kHD, 1, true) : idesc_16(kHD, 1, false);  // tree nodes' V stays bf16
           const bool start = v.x == p.x0 && v.h == 0;
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_ts_lead(lead, tO, tS + bf * kStep + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4), id, kk > 0 || !start ? 1u : 0u);
+            umma_ts_lead(lead, tO, tS + bf * kStep + kk * 8, vd + static_cast<uint64_t>((kk * 16 * 128) >> 4),
+                         idesc_16(kHD, 1, true), kk > 0 || !start ? 1u : 0u);
           umma_commit_lead(lead, &o_step[w]);
           const bool tile_end = v.last_of_tile(p, g);
           if (tile_end) umma_commit_lead(lead, &v_empty[st]);
@@ -356,29 +363,38 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
         unsigned char* dst = sV + st * kOpB;
         const int left = p.left(g, x);
         if (!nodes) {
-          // eight lanes to a key, 16 dims each.  The lanes of the second half's dims store their two
-          // 16-byte pieces in the other order, so that the banks of the eight lanes that store
+          // eight lanes to a key, 16 dims each.  The lanes of the second half's dims take their two
+          // pieces in the other order, so that the banks of the eight lanes that store
           // together differ
           const int j = lane & 7, kr = lane >> 3, flip = j >> 2;
-          const uint32_t codes = su32(sRaw) + (dw * 32 + kr) * 128 + j * 16;
+          const uint32_t codes = su32(sRaw) + (dw * 32 + kr) * 128 + j * 16 + 8 * flip;
           const uint32_t out = su32(dst) + flip * kHalfB + (dw * 32 + kr) * 128 + (((2 * (j & 3) + flip) ^ kr) << 4);
           const int lim = left - (dw * 32 + kr);
+          // the warp's 32 keys lie in two of the tile's eight parts of 16
+          const int2 ve = *reinterpret_cast<const int2*>(s_ve + (T % kExpRing) * 8 + 2 * dw);
+          const bool big = max(ve.x, ve.y) > 7;
+          const __nv_bfloat162 f0 = power(min(120 + ve.x, 127)), f1 = power(min(120 + ve.y, 127));
+          const __nv_bfloat162 g0 = power(max(ve.x - 7, 0)), g1 = power(max(ve.y - 7, 0));
 #pragma unroll 4
           for (int i = 0; i < 8; ++i) {  // keys 4 i on; their rows' swizzle: 4 (i % 2) more
             uint32_t w[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(codes + i * 512));
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(codes + i * 512));
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[2]), "=r"(w[3]) : "r"((codes ^ 8u) + i * 512));
+            if (4 * i >= lim) w[0] = w[1] = w[2] = w[3] = 0u;  // beyond the prefix: adds 0 whatever the slot holds
             uint32_t y[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-              const uint32_t c = q & 1 ? w[q >> 1] >> 16 : w[q >> 1] & 0xFFFFu;
-              y[q] = h2u(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3))));
-              if (4 * i >= lim) y[q] = 0u;  // beyond the prefix: adds 0 whatever the slot holds
+              // two codes to the upper bytes of two bf16, four bits down: the value times 2^-120
+              const uint32_t c = __byte_perm(w[q >> 1], 0u, q & 1 ? 0x3424 : 0x1404);
+              const uint32_t v = ((c >> 4) & 0x07F007F0u) | (c & 0x80008000u);
+              y[q] = b2u(__hmul2(u2b(v), i < 4 ? f0 : f1));
             }
+            if (big)  // a scale above 2^7 takes a second factor
+#pragma unroll
+              for (int q = 0; q < 8; ++q) y[q] = b2u(__hmul2(u2b(y[q]), i < 4 ? g0 : g1));
             const uint32_t at = (out ^ ((i & 1) << 6)) + i * 512;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(flip ? y[4] : y[0]), "r"(flip ? y[5] : y[1]),
-                         "r"(flip ? y[6] : y[2]), "r"(flip ? y[7] : y[3]) : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16u), "r"(flip ? y[0] : y[4]), "r"(flip ? y[1] : y[5]),
-                         "r"(flip ? y[2] : y[6]), "r"(flip ? y[3] : y[7]) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16u), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
           }
         } else {
           const int slot = ntail % kTailRing, kvh = p.pq / g.RG;
@@ -444,14 +460,14 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
         fence_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(&q_full[grp]);
-        // Factors of the scores.  The nodes' meets a score between the two halves of the node's own, the
-        // prefix's takes Q's and K's exponents in one power, so that neither alone carries it past the
-        // range; held within the range: 0 or Inf would make NaN of an unseen key's -Inf or of a score of 0.
-        const float nan = __int_as_float(0x7FC00000);
-        const float c0 = sm_scale * kLog2e;
-        const float c_nodes = q_ex == 1000 ? nan : fminf(sm_scale * kLog2e * pow2f(q_ex), 3e38f);
+        // Factors of the scores.  The nodes' meets a score between the two halves of the node's own, K's
+        // scale those of Q's power, so that neither alone carries it past the range; held within the range:
+        // 0 or Inf would make NaN of an unseen key's -Inf or of a score of 0.  (A row of Q with a NaN
+        // or an Inf has parts of 0; it gets its NaN at the end.)
+        const bool q_bad = q_ex == 1000;
+        const float q_a = sm_scale * kLog2e * pow2n((q_bad ? 0 : q_ex) / 2), q_b = pow2n(q_bad ? 0 : q_ex - q_ex / 2);
+        const float c_nodes = fminf(q_a * q_b, 3e38f);
         float m = -INFINITY, l = 0.0f;
-        int unit = 0;  // O's unit, as an exponent
         const int tail0 = ntail;
         const int words = (g.R + 63) >> 6;
         const uint64_t* mrow = mask + (static_cast<size_t>(p.b) * g.R + node) * words;
@@ -459,16 +475,20 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
         for (int x = p.x0; live && x < p.x1; ++x, ++T) {
           const bool nodes = x >= p.NT;
           const int left = p.left(g, x), halves = left > kStep ? 2 : 1;
+          const bool all = !nodes && left >= kKeys;  // every row sees all of the tile
           const int slot = ntail % kTailRing;
 #pragma unroll 1
           for (int h = 0; h < halves; ++h, ++n_step) {
             const uint32_t bf = n_step & 1, tB = tS + bf * kStep;
-            // keys the row sees: those that exist, or the ancestors among the nodes
-            const int here = left - h * kStep;
-            uint64_t see = here >= 64 ? ~0ull : (1ull << here) - 1ull;
-            if (nodes) {
-              const int wd = 2 * (x - p.NT) + h;
-              see &= row_ok && wd < words ? mrow[wd] : 0ull;
+            uint64_t see = ~0ull;
+            if (!all) {
+              // keys the row sees: those that exist, or the ancestors among the nodes
+              const int here = left - h * kStep;
+              if (here < 64) see = (1ull << here) - 1ull;
+              if (nodes) {
+                const int wd = 2 * (x - p.NT) + h;
+                see &= row_ok && wd < words ? mrow[wd] : 0ull;
+              }
             }
             if (!warp_wait(&s_full[2 * grp + bf], (n_step >> 1) & 1, abort)) {
               live = false;
@@ -477,47 +497,25 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
             fence_after();
             unsigned long long y[32];
             tmem_ld64_pairs(tB, y);
-            // a factor for the scores of each 16 keys, and what is added to their exponents
-            float c[4];
-            int d[4];
-            int top = kNodeExp;
+            float c[4];  // the scores' factor of each 16 keys
             if (nodes) {
               const float4* fac = reinterpret_cast<const float4*>(s_fac + slot * kKeys + h * kStep);
-              const unsigned long long cn = pair(c_nodes, c_nodes);
+              const unsigned long long cn = pair(c_nodes, c_nodes), zero = pair(0.0f, 0.0f);
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
                 const float4 f = fac[j];
-                const unsigned long long f0 = pair(f.x, f.y), f1 = pair(f.z, f.w), zero = pair(0.0f, 0.0f);
+                const unsigned long long f0 = pair(f.x, f.y), f1 = pair(f.z, f.w);
                 y[2 * j] = fma2(fma2(fma2(y[2 * j], f0, zero), cn, zero), f0, zero);
                 y[2 * j + 1] = fma2(fma2(fma2(y[2 * j + 1], f1, zero), cn, zero), f1, zero);
               }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) c[i] = 1.0f, d[i] = -kNodeExp;
+              c[0] = c[1] = c[2] = c[3] = 1.0f;
             } else {
-              const int8_t* ex = s_exp + (T % kExpRing) * 16 + 4 * h;
-              const char4 ke = *reinterpret_cast<const char4*>(ex), ve = *reinterpret_cast<const char4*>(ex + 8);
-              const int kx[4] = {ke.x, ke.y, ke.z, ke.w};
-              d[0] = ve.x, d[1] = ve.y, d[2] = ve.z, d[3] = ve.w;
+              const float4 e = reinterpret_cast<const float4*>(s_k2 + (T % kExpRing) * 8)[h];
+              c[0] = e.x, c[1] = e.y, c[2] = e.z, c[3] = e.w;
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                c[i] = fminf(fmaxf(c0 * pow2n(min(max((q_ex == 1000 ? 0 : q_ex) + kx[i], -126), 126)), 1e-37f), 3e38f);
-              if (q_ex == 1000) c[0] = c[1] = c[2] = c[3] = nan;  // (the bounds would drop it)
-              top = max(max(d[0], d[1]), max(d[2], d[3]));
+              for (int i = 0; i < 4; ++i) c[i] = fminf(fmaxf(q_a * c[i] * q_b, 1e-37f), 3e38f);
             }
-            // O's unit grows with V's exponents, and becomes the nodes' behind the prefix
-            float o_f = 1.0f;
-            bool rescale = false;
-            if (!begun || (nodes && unit != kNodeExp) || (!nodes && top > unit)) {
-              if (begun) {
-                o_f = pow2f(min(max(unit - top, -126), 126));
-                rescale = true;
-              }
-              unit = top;
-            }
-            if (!nodes)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) d[i] = max(d[i] - unit, kMinShift);
-            if (!__all_sync(0xFFFFFFFFu, see == ~0ull)) {
+            if (!all && !__all_sync(0xFFFFFFFFu, see == ~0ull)) {
               const uint32_t s0 = static_cast<uint32_t>(see), s1 = static_cast<uint32_t>(see >> 32);
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
@@ -528,7 +526,7 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
             // Exponentials against the base so far.  Where a row's sum passes 2^kTop (or it has no
             // base yet) its maximum is looked for, the base moved and the step done again.
             bool look = !begun;
-            float s;
+            float o_f = 1.0f, s;
 #pragma unroll 1
             for (;;) {
               if (look) {
@@ -538,47 +536,37 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
                   float a = -INFINITY;
 #pragma unroll
                   for (int j = 0; j < 8; ++j) a = fmax3f(a, lo_of(y[8 * i + j]), hi_of(y[8 * i + j]));
-                  nm = fmaxf(nm, a * c[i] - kHead);
+                  nm = fmaxf(nm, a * c[i]);
                 }
                 if (nm != m) {
-                  const float corr = ex2(m - nm);
-                  l *= corr;
-                  o_f *= corr;
+                  o_f = ex2(m - nm);
+                  l *= o_f;
                   m = nm;
                 }
-                rescale = rescale || begun;
               }
               const float base = m == -INFINITY ? 0.0f : m;  // (a row that has seen no key: weights of 0)
-              float total = 0.0f;
-              auto exps = [&](auto pack) {
+              const unsigned long long nv = pair(-base, -base);
+              unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const unsigned long long cv = pair(c[i], c[i]);
-                  const float n = static_cast<float>(d[i]) - base;
-                  const unsigned long long nv = pair(n, n);
-                  unsigned long long sum = 0ull;
-                  uint32_t pk[8];
+              for (int i = 0; i < 4; ++i) {
+                const unsigned long long cv = pair(c[i], c[i]);
+                uint32_t pk[8];
 #pragma unroll
-                  for (int j = 0; j < 8; ++j) {
-                    const unsigned long long a = fma2(y[8 * i + j], cv, nv);
-                    const float e0 = ex2(lo_of(a)), e1 = ex2(hi_of(a));
-                    sum = add2(sum, pair(e0, e1));
-                    pk[j] = pack(e0, e1);
-                  }
-                  tmem_st8(tB + 8 * i, pk);  // (the scores are in registers, for a step that is done again too)
-                  total = fmaf(lo_of(sum) + hi_of(sum), pow2n(-d[i]), total);
+                for (int j = 0; j < 8; ++j) {
+                  const unsigned long long a = fma2(y[8 * i + j], cv, nv);
+                  const float e0 = ex2(lo_of(a)), e1 = ex2(hi_of(a));
+                  sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
+                  pk[j] = pack2_bf16(e0, e1);
                 }
-              };
-              if (nodes)
-                exps([](float a, float b) { return pack2_bf16(a, b); });
-              else
-                exps([](float a, float b) { return h2u(__floats2half2_rn(a, b)); });
-              s = total;
+                tmem_st8(tB + 8 * i, pk);  // (the scores are in registers, for a step that is done again too)
+              }
+              sum[0] = add2(sum[0], sum[1]);
+              s = lo_of(sum[0]) + hi_of(sum[0]);
               if (look || !__any_sync(0xFFFFFFFFu, !(s <= 32768.0f) || (m == -INFINITY && see != 0ull))) break;
               look = true;
             }
             l += s;
-            if (rescale) {
+            if (look && begun) {
               // (the scores of this step came behind the product of the step before the last)
               if (!warp_wait(&o_step[grp], (n_step - 1) & 1, abort)) {
                 live = false;
@@ -593,7 +581,6 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
                 for (int j = 0; j < 16; ++j) z[j] = __float_as_uint(__uint_as_float(z[j]) * o_f);
                 tmem_st16(tO + 16 * k, z);
               }
-              tmem_st_wait();
             }
             tmem_st_wait();
             fence_before();
@@ -624,7 +611,8 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
         // the part's record: o normalized by its own sum, the base and the sum
         const size_t rec = static_cast<size_t>(p.b) * Qn + p.pq + cta;
         const int rrow = grp * kRows + r;
-        const float inv = poison ? nan : l != 0.0f ? 1.0f / l : 0.0f, o_unit = pow2f(unit);
+        if (q_bad) l = __int_as_float(0x7FC00000);
+        const float inv = poison ? __int_as_float(0x7FC00000) : l != 0.0f ? 1.0f / l : 0.0f;
         float4* dst = reinterpret_cast<float4*>(ws_o + rec * (RT * kRows * kHD)) + rrow;
 #pragma unroll 1
         for (int h = 0; h < 8; ++h) {
@@ -634,8 +622,8 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               dst[(4 * h + j) * (RT * kRows)] =
-                  make_float4(__uint_as_float(z[4 * j]) * inv * o_unit, __uint_as_float(z[4 * j + 1]) * inv * o_unit,
-                              __uint_as_float(z[4 * j + 2]) * inv * o_unit, __uint_as_float(z[4 * j + 3]) * inv * o_unit);
+                  make_float4(__uint_as_float(z[4 * j]) * inv, __uint_as_float(z[4 * j + 1]) * inv, __uint_as_float(z[4 * j + 2]) * inv,
+                              __uint_as_float(z[4 * j + 3]) * inv);
           }
         }
         fence_before();
