@@ -4,8 +4,8 @@
 // Work is cut as in verify4.cuh: a pair is (request, KV head, tile of RT * 128 query rows),
 // its units are tiles of 128 prefix keys and then of 128 tree nodes; one CTA per SM takes
 // an equal share of all units.  RT softmax groups of 128 rows each use every tile:
-//   producer (warp 0)      K's codes by TMA into two stages, as the products read them; V's codes
-//                          into one; the blocks' exponents
+//   producer (warp 0)      K's codes by TMA into three slots, as the products read them; V's codes
+//                          into two stages; the blocks' exponents
 //   issuers (warps 1, 2; one per group)  S = Q K^T in steps of 64 keys, into two buffers of tensor
 //                          memory, then O += P V with P from tensor memory
 //   dequantizers (4 warps) V's codes -> bf16 in 128-byte-swizzled shared memory; the
@@ -33,6 +33,7 @@ namespace e3 {
 namespace {
 
 constexpr int kCodeB = kKeys * kHD;   // bytes of a tile's codes, per operand
+constexpr int kSlots = 3;              // tiles of K's codes in shared memory
 constexpr int kTailRing = 4;          // tiles of tree nodes whose factors are kept (three are in flight at most)
 constexpr int kExpRing = 8;           // tiles whose exponents are kept
 // Warpgroups: 0 = producer and issuers, 1 and 2 = softmax, 3 = dequantizers.  Registers move from
@@ -43,8 +44,8 @@ constexpr int kRegsIssue = 96, kRegsSoftmax = 152, kRegsDeq = 112;
 
 template <int RT>
 struct Cfg {
-  // Q: two parts of each group; K: two stages, a second half for the nodes' second parts; V: two stages
-  static constexpr int Q = 0, K = RT * 2 * kCodeB, V = K + 2 * 2 * kCodeB, RAW = V + 2 * kOpB, FAC = RAW + kCodeB;
+  // Q: two parts of each group; K: three slots, two for a tile of nodes; V: two stages; its codes: two
+  static constexpr int Q = 0, K = RT * 2 * kCodeB, V = K + kSlots * kCodeB, RAW = V + 2 * kOpB, FAC = RAW + 2 * kCodeB;
   static constexpr int BARS = FAC + kTailRing * kKeys * 4, END = BARS + 2048;
   static constexpr int SMEM = END + 1024;  // (base rounded up to 1024)
 };
@@ -129,20 +130,20 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
   unsigned char *sQ = sm + C::Q, *sK = sm + C::K, *sV = sm + C::V, *sRaw = sm + C::RAW;
   float* s_fac = reinterpret_cast<float*>(sm + C::FAC);  // [kTailRing][128] root of the factor of each tree node's scores
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::BARS);
-  uint64_t* k_full = bars;         // [stage] prefix codes
-  uint64_t* n_full = bars + 2;     // [stage] tree nodes' K
-  uint64_t* k_empty = bars + 4;    // [stage]
-  uint64_t* raw_full = bars + 6;   // V's codes (nothing where the tile is of nodes)
-  uint64_t* raw_empty = bars + 7;
-  uint64_t* v_full = bars + 8;     // [stage]
+  uint64_t* k_full = bars;         // [slot] prefix codes
+  uint64_t* k_empty = bars + 3;    // [slot]
+  uint64_t* raw_full = bars + 6;   // [stage] V's codes (nothing where the tile is of nodes)
+  uint64_t* raw_empty = bars + 8;  // [stage]
+  uint64_t* v_full = bars + 28;    // [stage]
   uint64_t* v_empty = bars + 10;   // [stage]
+  uint64_t* n_full = bars + 30;    // tree nodes' K
   uint64_t* s_full = bars + 12;    // [softmax group][buffer]
   uint64_t* p_full = bars + 16;    // [softmax group][buffer]
   uint64_t* o_step = bars + 20;    // [softmax group] the product with a step's V
   uint64_t* o_done = bars + 22;    // [softmax group] the part's last
   uint64_t* q_full = bars + 24;    // [softmax group]
   uint64_t* q_empty = bars + 26;   // [softmax group]
-  float* s_k2 = reinterpret_cast<float*>(bars + 28);          // [kExpRing][8] K's scale of 16 keys each
+  float* s_k2 = reinterpret_cast<float*>(bars + 32);          // [kExpRing][8] K's scale of 16 keys each
   int* s_ve = reinterpret_cast<int*>(s_k2 + kExpRing * 8);    // [kExpRing][8] V's exponent
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_ve + kExpRing * 8);  // [kTailRing][4] nodes with a non-finite V
   uint32_t* tmem_slot = s_bad + 4 * kTailRing;
@@ -152,9 +153,8 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
   const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      bar_init(&k_full[i], 1);
-      bar_init(&n_full[i], 4);
-      bar_init(&k_empty[i], RT);
+      bar_init(&raw_full[i], 1);
+      bar_init(&raw_empty[i], 4);
       bar_init(&v_full[i], 4);
       bar_init(&v_empty[i], RT);
       bar_init(&s_full[2 * i], 1);
@@ -166,8 +166,11 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
       bar_init(&q_full[i], 4);
       bar_init(&q_empty[i], 1);
     }
-    bar_init(raw_full, 1);
-    bar_init(raw_empty, 4);
+    for (int i = 0; i < kSlots; ++i) {
+      bar_init(&k_full[i], 1);
+      bar_init(&k_empty[i], RT);
+    }
+    bar_init(n_full, 4);
     *abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -200,14 +203,15 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;  // columns: S buffer i of group w at 128 w + 64 i (its P over the first half), O at 256 + 128 w
   const int Qn = g.KVH * g.RG;
-  uint32_t any_k = 0, par_k = 0, n_raw = 0;  // (producer) bit st: the stage has been loaded, its last load's parity; raw loads
+  // (producer) bit i: the slot has been loaded, its last load's parity; tiles whose V has been asked for
+  uint32_t any_k = 0, par_k = 0, n_raw = 0;
 
   if (warp < kSoftmax0) {
     regs_dec<kRegsIssue>();
     if (warp == 0 && work) {
       Parts p = first;
       bool live = !(cta == 0 && (tail.flags & E3_KV_SELFTEST_STALL));  // (keys that never come)
-      uint32_t T = 0, use_k = 0;  // tiles; bit st: parity of the stage's next use of k_full
+      uint32_t T = 0, slot = 0, use_k = 0, free_k = 7u;  // tiles; the next slot; bit i: parity of k_full's and k_empty's next use
       const int log_block = __ffs(kv.block) - 1;
       do {
         const int kvh = p.pq / g.RG;
@@ -241,32 +245,33 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           const bool nodes = x >= p.NT;
           const int r_next = x + 1 < min(p.x1, p.NT) ? box_row(x + 1) : -1;
           const int2 e_next = x + 1 < min(p.x1, p.NT) ? exponent(x + 1) : make_int2(0, 0);
-          if (!warp_wait(&k_empty[st], ((T >> 1) & 1) ^ 1, abort)) {
-            live = false;
-            break;
-          }
           const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, r >= 0)) * static_cast<uint32_t>(box) * kHD;
-          if (!nodes) {
-            // (tile T - kExpRing's exponents have been read: its steps' weights came before the scores of tile T - 4)
-            if (lane < 8) s_k2[(T % kExpRing) * 8 + lane] = pow2n(max(e.x, -126)), s_ve[(T % kExpRing) * 8 + lane] = e.y;
-            __syncwarp();
-            if (lane == 0) bar_expect(&k_full[st], bytes);
-            __syncwarp();
-            if (r >= 0) tma2d(su32(sK + st * 2 * kCodeB) + lane * box * 128, &tmK, 0, r, &k_full[st]);
-            any_k |= 1u << st;
-            par_k = (par_k & ~(1u << st)) | (use_k & (1u << st));
-            use_k ^= 1u << st;
+          for (int i = 0; live && i < (nodes ? 2 : 1); ++i) {
+            live = warp_wait(&k_empty[slot], (free_k >> slot) & 1, abort);
+            free_k ^= 1u << slot;
+            if (live && !nodes) {
+              // (tile T - kExpRing's exponents have been read: its steps' weights came before the scores of tile T - 5)
+              if (lane < 8) s_k2[(T % kExpRing) * 8 + lane] = pow2n(max(e.x, -126)), s_ve[(T % kExpRing) * 8 + lane] = e.y;
+              __syncwarp();
+              if (lane == 0) bar_expect(&k_full[slot], bytes);
+              __syncwarp();
+              if (r >= 0) tma2d(su32(sK + slot * kCodeB) + lane * box * 128, &tmK, 0, r, &k_full[slot]);
+              any_k |= 1u << slot;
+              par_k = (par_k & ~(1u << slot)) | (use_k & (1u << slot));
+              use_k ^= 1u << slot;
+            }
+            slot = slot == kSlots - 1 ? 0 : slot + 1;
           }
-          if (!warp_wait(raw_empty, (T & 1) ^ 1, abort)) {
+          if (!live || !warp_wait(&raw_empty[st], ((T >> 1) & 1) ^ 1, abort)) {
             live = false;
             break;
           }
           if (!nodes) {
-            if (lane == 0) bar_expect(raw_full, bytes);
+            if (lane == 0) bar_expect(&raw_full[st], bytes);
             __syncwarp();
-            if (r >= 0) tma2d(su32(sRaw) + lane * box * 128, &tmV, 0, r, raw_full);
+            if (r >= 0) tma2d(su32(sRaw + st * kCodeB) + lane * box * 128, &tmV, 0, r, &raw_full[st]);
           } else if (lane == 0) {
-            bar_arrive(raw_full);  // (K's stage is free, too)
+            bar_arrive(&raw_full[st]);  // (K's slots are free, too)
           }
           ++n_raw;
           r = r_next;
@@ -281,7 +286,7 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
       const uint64_t v_desc = desc_sw128(su32(sV), kHalfB, 1024);
       const uint32_t tS = tmem + w * 128, tO = tmem + 256 + w * 128;
       const uint32_t lead = elect_lane();
-      uint32_t T = 0, n_step = 0, n_part = 0, use_k = 0, use_n = 0;  // (bits: parities of the next uses)
+      uint32_t T = 0, n_step = 0, n_part = 0, slot = 0, use_k = 0, use_n = 0;  // (bits: parities of the next uses)
       Parts p = first;
       bool live = true;
       do {
@@ -290,18 +295,18 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
         Step s{p.x0, 0}, v{p.x0, 0};
         uint32_t n_s = n_step;
         auto scores = [&]() {
-          const uint32_t st = (T + (s.x - p.x0)) & 1, bf = n_s & 1;
+          const uint32_t bf = n_s & 1, second = slot == kSlots - 1 ? 0 : slot + 1;  // (the nodes' second parts)
           const bool nodes = s.x >= p.NT;
           if (s.h == 0) {
             if (nodes) {
-              if (!warp_wait(&n_full[st], (use_n >> st) & 1, abort)) return false;
-              use_n ^= 1u << st;
+              if (!warp_wait(n_full, use_n, abort)) return false;
+              use_n ^= 1u;
             } else {
-              if (!warp_wait(&k_full[st], (use_k >> st) & 1, abort)) return false;
-              use_k ^= 1u << st;
+              if (!warp_wait(&k_full[slot], (use_k >> slot) & 1, abort)) return false;
+              use_k ^= 1u << slot;
             }
           }
-          const uint64_t kd = k_desc + static_cast<uint64_t>((st * 2 * kCodeB + s.h * (kStep * 128)) >> 4);
+          const uint64_t kd = k_desc + static_cast<uint64_t>((slot * kCodeB + s.h * (kStep * 128)) >> 4);
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -314,10 +319,14 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 umma8_lead(lead, tS + bf * kStep, q_desc + static_cast<uint64_t>((part * kCodeB + kk * 32) >> 4),
-                           kd + static_cast<uint64_t>((kCodeB + kk * 32) >> 4), idesc_e4m3(kStep), 1u);
+                           k_desc + static_cast<uint64_t>((second * kCodeB + s.h * (kStep * 128) + kk * 32) >> 4), idesc_e4m3(kStep), 1u);
           umma_commit_lead(lead, &s_full[2 * w + bf]);
           const bool tile_end = s.last_of_tile(p, g);
-          if (tile_end) umma_commit_lead(lead, &k_empty[st]);
+          if (tile_end) {
+            umma_commit_lead(lead, &k_empty[slot]);
+            if (nodes) umma_commit_lead(lead, &k_empty[second]);
+            slot = nodes ? (second == kSlots - 1 ? 0 : second + 1) : second;
+          }
           if (tile_end && s.x + 1 == p.x1) umma_commit_lead(lead, &q_empty[w]);
           s.next(p, g);
           ++n_s;
@@ -355,10 +364,11 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
       const int dw = warp & 3;
       Parts p = first;
       int x = p.x0, ntail = 0;
+      uint32_t slot = 0;  // of K, as the others count
       for (uint32_t T = 0;; ++T) {
-        const uint32_t st = T & 1;
+        const uint32_t st = T & 1, second = slot == kSlots - 1 ? 0 : slot + 1;
         const bool nodes = x >= p.NT;
-        if (!warp_wait(raw_full, T & 1, abort)) break;
+        if (!warp_wait(&raw_full[st], (T >> 1) & 1, abort)) break;
         if (!warp_wait(&v_empty[st], ((T >> 1) & 1) ^ 1, abort)) break;
         unsigned char* dst = sV + st * kOpB;
         const int left = p.left(g, x);
@@ -367,7 +377,7 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           // pieces in the other order, so that the banks of the eight lanes that store
           // together differ
           const int j = lane & 7, kr = lane >> 3, flip = j >> 2;
-          const uint32_t codes = su32(sRaw) + (dw * 32 + kr) * 128 + j * 16 + 8 * flip;
+          const uint32_t codes = su32(sRaw + st * kCodeB) + (dw * 32 + kr) * 128 + j * 16 + 8 * flip;
           const uint32_t out = su32(dst) + flip * kHalfB + (dw * 32 + kr) * 128 + (((2 * (j & 3) + flip) ^ kr) << 4);
           const int lim = left - (dw * 32 + kr);
           // the warp's 32 keys lie in two of the tile's eight parts of 16
@@ -397,7 +407,7 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ 16u), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7]) : "memory");
           }
         } else {
-          const int slot = ntail % kTailRing, kvh = p.pq / g.RG;
+          const int fac = ntail % kTailRing, kvh = p.pq / g.RG;
           int own = -1;  // this lane's row of the warp's 32
           if (dw * 32 + lane < left) {
             const int j = (x - p.NT) * kKeys + dw * 32 + lane, pi = j / tail.page_size;
@@ -409,25 +419,26 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           }
           // a node with a NaN or an Inf leaves the product: its scores get a NaN factor, rows
           // that see its V are marked
-          unsigned char* k0 = sK + st * 2 * kCodeB;
           const __nv_bfloat16* krow = static_cast<const __nv_bfloat16*>(tail.k) + static_cast<size_t>(max(own, 0)) * kHD;
-          const int ex = row_to_parts(own >= 0 ? reinterpret_cast<const uint4*>(krow) : nullptr, k0, k0 + kCodeB, dw * 32 + lane);
-          s_fac[slot * kKeys + dw * 32 + lane] = ex == 1000 ? __int_as_float(0x7FC00000) : pow2f(ex / 2);
+          const int ex = row_to_parts(own >= 0 ? reinterpret_cast<const uint4*>(krow) : nullptr, sK + slot * kCodeB, sK + second * kCodeB,
+                                      dw * 32 + lane);
+          s_fac[fac * kKeys + dw * 32 + lane] = ex == 1000 ? __int_as_float(0x7FC00000) : pow2f(ex / 2);
           unsigned char* slab = dst + dw * 32 * 128;
           bring_rows(static_cast<const __nv_bfloat16*>(tail.v), own, slab, lane);
           const uint32_t top = row_top(slab, lane);
           const uint32_t bad = __ballot_sync(0xFFFFFFFFu, top >= 0x7F80u);
-          if (lane == 0) s_bad[slot * 4 + dw] = bad;
+          if (lane == 0) s_bad[fac * 4 + dw] = bad;
           if (top >= 0x7F80u) row_clear(slab, lane);
           ++ntail;
         }
         fence_async_smem();  // generic-proxy writes -> tensor core
         __syncwarp();
         if (lane == 0) {
-          if (nodes) bar_arrive(&n_full[st]);
+          if (nodes) bar_arrive(n_full);
           bar_arrive(&v_full[st]);
-          bar_arrive(raw_empty);
+          bar_arrive(&raw_empty[st]);
         }
+        slot = nodes ? (second == kSlots - 1 ? 0 : second + 1) : second;
         if (++x == p.x1) {
           if (!p.next(g, kv_len)) break;
           x = p.x0;
@@ -642,12 +653,12 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
     // shared memory goes
     if (warp == 0) {
       const uint64_t t0 = gtimer();
-      for (int st = 0; st < 2; ++st)
-        if ((any_k >> st) & 1u)
-          while (!bar_try(&k_full[st], (par_k >> st) & 1u) && gtimer() - t0 < kWaitNs) {
+      for (int i = 0; i < kSlots; ++i)
+        if ((any_k >> i) & 1u)
+          while (!bar_try(&k_full[i], (par_k >> i) & 1u) && gtimer() - t0 < kWaitNs) {
           }
-      if (n_raw > 0)
-        while (!bar_try(raw_full, (n_raw - 1) & 1u) && gtimer() - t0 < kWaitNs) {
+      for (uint32_t t = n_raw > 2 ? n_raw - 2 : 0; t < n_raw; ++t)
+        while (!bar_try(&raw_full[t & 1], (t >> 1) & 1u) && gtimer() - t0 < kWaitNs) {
         }
       while (gtimer() - t0 < 50000) {  // and so have the products
       }
