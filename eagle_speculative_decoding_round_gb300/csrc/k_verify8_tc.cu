@@ -506,34 +506,36 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
               break;
             }
             fence_after();
-            unsigned long long y[32];
-            tmem_ld64_pairs(tB, y);
-            float c[4];  // the scores' factor of each 16 keys
-            if (nodes) {
-              const float4* fac = reinterpret_cast<const float4*>(s_fac + slot * kKeys + h * kStep);
-              const unsigned long long cn = pair(c_nodes, c_nodes), zero = pair(0.0f, 0.0f);
+            if (!all) {  // the nodes' factors, and -Inf where unseen (whose exponential is 0), in place
+              const float2 cn = make_float2(c_nodes, c_nodes);
+#pragma unroll 1
+              for (int d = 0; d < 4; ++d) {
+                uint32_t z[16];
+                tmem_ld16(tB + 16 * d, z);
+                if (nodes) {
+                  const float2* fac = reinterpret_cast<const float2*>(s_fac + slot * kKeys + h * kStep + 16 * d);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const float4 f = fac[j];
-                const unsigned long long f0 = pair(f.x, f.y), f1 = pair(f.z, f.w);
-                y[2 * j] = fma2(fma2(fma2(y[2 * j], f0, zero), cn, zero), f0, zero);
-                y[2 * j + 1] = fma2(fma2(fma2(y[2 * j + 1], f1, zero), cn, zero), f1, zero);
+                  for (int j = 0; j < 8; ++j) {
+                    const float2 v = __fmul2_rn(__fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1])), fac[j]), cn), fac[j]);
+                    z[2 * j] = __float_as_uint(v.x), z[2 * j + 1] = __float_as_uint(v.y);
+                  }
+                }
+                const uint32_t sb = static_cast<uint32_t>(see >> (16 * d));
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[j] = sb & (1u << j) ? z[j] : 0xFF800000u;
+                tmem_st16(tB + 16 * d, z);
               }
-              c[0] = c[1] = c[2] = c[3] = 1.0f;
-            } else {
+              tmem_st_wait();
+            }
+            float c[4] = {1.0f, 1.0f, 1.0f, 1.0f};  // the scores' factor of each 16 keys
+            if (!nodes) {
               const float4 e = reinterpret_cast<const float4*>(s_k2 + (T % kExpRing) * 8)[h];
               c[0] = e.x, c[1] = e.y, c[2] = e.z, c[3] = e.w;
 #pragma unroll
               for (int i = 0; i < 4; ++i) c[i] = fminf(fmaxf(q_a * c[i] * q_b, 1e-37f), 3e38f);
             }
-            if (!all && !__all_sync(0xFFFFFFFFu, see == ~0ull)) {
-              const uint32_t s0 = static_cast<uint32_t>(see), s1 = static_cast<uint32_t>(see >> 32);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const uint32_t s = j < 16 ? s0 : s1;
-                y[j] = pair(s & (1u << ((2 * j) & 31)) ? lo_of(y[j]) : -INFINITY, s & (1u << ((2 * j + 1) & 31)) ? hi_of(y[j]) : -INFINITY);
-              }
-            }
+            unsigned long long y[32];
+            tmem_ld64_pairs(tB, y);
             // Exponentials against the base so far.  Where a row's sum passes 2^kTop (or it has no
             // base yet) its maximum is looked for, the base moved and the step done again.
             bool look = !begun;
