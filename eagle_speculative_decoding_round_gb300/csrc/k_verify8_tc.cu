@@ -64,46 +64,49 @@ __device__ __forceinline__ __nv_bfloat162 u2b(uint32_t u) { return *reinterpret_
 // 2^e in both halves, e in [-126, 127]
 __device__ __forceinline__ __nv_bfloat162 power(int e) { return u2b(static_cast<uint32_t>(127 + e) * 0x00800080u); }
 
-// A row of bf16 values (16-byte pieces at `src`, null: zeros) in two e4m3 parts, row `rr` of `hi` and `lo`, its largest
-// magnitude scaled to [2^6, 2^8) by a power of two with an even exponent: returns the exponent that takes it back, or
-// 1000 for a row with a NaN or an Inf, which becomes zeros.
-__device__ __forceinline__ int row_to_parts(const uint4* src, unsigned char* hi, unsigned char* lo, int rr) {
-  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-  uint32_t top = 0u;
-#pragma unroll 4
-  for (int c = 0; c < 16; ++c) {
-    const uint4 x = src ? src[c] : none;
-    top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
-  }
-  top = max(top & 0xFFFFu, top >> 16);
-  const bool odd = top >= 0x7F80u;
-  const int ex = (min(static_cast<int>(max(top >> 7, 1u)), 254) - 127) & ~1;
-  const float f0 = pow2n((6 - ex) / 2), f1 = pow2n(6 - ex - (6 - ex) / 2);  // (2^132 for a row of zeros)
+// A warp's 32 rows of bf16 values (row `own` of `from` for each lane, -1: zeros) in two e4m3 parts, rows row0 + lane of
+// `hi` and `lo`, each row's largest magnitude scaled to [2^6, 2^8) by a power of two with an even exponent: returns the
+// exponent that takes the lane's row back, or 1000 for a row with a NaN or an Inf, which becomes zeros.  Half a warp to a
+// row, so that the loads take whole lines (a thread to a row, its pieces 256 bytes from the next thread's: 6 us for
+// 256 rows).
+__device__ __forceinline__ int rows_to_parts(const __nv_bfloat16* from, int own, unsigned char* hi, unsigned char* lo, int row0, int lane) {
+  const int c = lane & 15;  // the 16-byte piece
+  int mine = 0;
 #pragma unroll 1
-  for (int c = 0; c < 8; ++c) {  // 16 values
-    const uint4 x[2] = {src ? src[2 * c] : none, src ? src[2 * c + 1] : none};
-    uint32_t h[4], l[4];
+  for (int i0 = 0; i0 < 16; i0 += 4) {
+    uint4 x[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4& y = x[q >> 1];
-      const uint32_t w[2] = {q & 1 ? y.z : y.x, q & 1 ? y.w : y.y};
-      uint32_t a[2], b[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float2 v = __fmul2_rn(make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)), make_float2(f0, f0));
-        v = odd ? make_float2(0.0f, 0.0f) : __fmul2_rn(v, make_float2(f1, f1));
-        a[e] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-        const float2 g = __half22float2(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(a[e]), __NV_E4M3))));
-        b[e] = __nv_cvt_float2_to_fp8x2(make_float2(v.x - g.x, v.y - g.y), __NV_SATFINITE, __NV_E4M3);
-      }
-      h[q] = a[0] | (a[1] << 16);
-      l[q] = b[0] | (b[1] << 16);
+    for (int i = 0; i < 4; ++i) {
+      const int at = __shfl_sync(0xFFFFFFFFu, own, 2 * (i0 + i) + (lane >> 4));
+      x[i] = at >= 0 ? reinterpret_cast<const uint4*>(from + static_cast<size_t>(at) * kHD)[c] : make_uint4(0u, 0u, 0u, 0u);
     }
-    const int at = rr * 128 + ((c ^ (rr & 7)) << 4);
-    *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+      top = max(top & 0xFFFFu, top >> 16);
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+      const bool odd = top >= 0x7F80u;
+      const int ex = (min(static_cast<int>(max(top >> 7, 1u)), 254) - 127) & ~1;
+      const float f0 = pow2n((6 - ex) / 2), f1 = pow2n(6 - ex - (6 - ex) / 2);  // (2^132 for a row of zeros)
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float2 v = __fmul2_rn(make_float2(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xFFFF0000u)), make_float2(f0, f0));
+        v = odd ? make_float2(0.0f, 0.0f) : __fmul2_rn(v, make_float2(f1, f1));
+        h[q] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+        const float2 g = __half22float2(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h[q]), __NV_E4M3))));
+        l[q] = __nv_cvt_float2_to_fp8x2(make_float2(v.x - g.x, v.y - g.y), __NV_SATFINITE, __NV_E4M3);
+      }
+      const int rr = row0 + 2 * (i0 + i) + (lane >> 4), at = rr * 128 + (((c >> 1) ^ (rr & 7)) << 4) + 8 * (c & 1);
+      *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+      *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
+      const int e = __shfl_sync(0xFFFFFFFFu, odd ? 1000 : ex - 6, (lane & 1) * 16);
+      if (lane >> 1 == i0 + i) mine = e;
+    }
   }
-  return odd ? 1000 : ex - 6;
+  return mine;
 }
 
 // The steps of a part's tiles: 64 keys each, one for a tile with 64 keys or fewer.
@@ -385,7 +388,7 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           const bool big = max(ve.x, ve.y) > 7;
           const __nv_bfloat162 f0 = power(min(120 + ve.x, 127)), f1 = power(min(120 + ve.y, 127));
           const __nv_bfloat162 g0 = power(max(ve.x - 7, 0)), g1 = power(max(ve.y - 7, 0));
-#pragma unroll 4
+#pragma unroll 2  // (unrolled further it takes the instruction caches from the softmax: batch 194 us, by 4 202, by 8 225)
           for (int i = 0; i < 8; ++i) {  // keys 4 i on; their rows' swizzle: 4 (i % 2) more
             uint32_t w[4];
             asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(codes + i * 512));
@@ -419,9 +422,7 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           }
           // a node with a NaN or an Inf leaves the product: its scores get a NaN factor, rows
           // that see its V are marked
-          const __nv_bfloat16* krow = static_cast<const __nv_bfloat16*>(tail.k) + static_cast<size_t>(max(own, 0)) * kHD;
-          const int ex = row_to_parts(own >= 0 ? reinterpret_cast<const uint4*>(krow) : nullptr, sK + slot * kCodeB, sK + second * kCodeB,
-                                      dw * 32 + lane);
+          const int ex = rows_to_parts(static_cast<const __nv_bfloat16*>(tail.k), own, sK + slot * kCodeB, sK + second * kCodeB, dw * 32, lane);
           s_fac[fac * kKeys + dw * 32 + lane] = ex == 1000 ? __int_as_float(0x7FC00000) : pow2f(ex / 2);
           unsigned char* slab = dst + dw * 32 * 128;
           bring_rows(static_cast<const __nv_bfloat16*>(tail.v), own, slab, lane);
@@ -466,8 +467,8 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           break;
         }
         unsigned char* q0 = sQ + grp * 2 * kCodeB;
-        const __nv_bfloat16* qrow = Q + ((static_cast<size_t>(p.b) * g.R + node) * g.H + head) * kHD;
-        const int q_ex = row_to_parts(row_ok ? reinterpret_cast<const uint4*>(qrow) : nullptr, q0, q0 + kCodeB, r);
+        const int q_ex = rows_to_parts(Q + static_cast<size_t>(p.b) * g.R * g.H * kHD, row_ok ? node * g.H + head : -1, q0, q0 + kCodeB,
+                                       quarter * 32, lane);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(&q_full[grp]);
