@@ -64,37 +64,60 @@ __device__ __forceinline__ __nv_bfloat162 u2b(uint32_t u) { return *reinterpret_
 // 2^e in both halves, e in [-126, 127]
 __device__ __forceinline__ __nv_bfloat162 power(int e) { return u2b(static_cast<uint32_t>(127 + e) * 0x00800080u); }
 
-// A warp's 32 rows of bf16 values (row `own` of `from` for each lane, -1: zeros) in two e4m3 parts, rows row0 + lane of
-// `hi` and `lo`, each row's largest magnitude scaled to [2^6, 2^8) by a power of two with an even exponent: returns the
-// exponent that takes the lane's row back, or 1000 for a row with a NaN or an Inf, which becomes zeros.  Half a warp to a
-// row, so that the loads take whole lines (a thread to a row, its pieces 256 bytes from the next thread's: 6 us for
-// 256 rows).
-__device__ __forceinline__ int rows_to_parts(const __nv_bfloat16* from, int own, unsigned char* hi, unsigned char* lo, int row0, int lane) {
+// A warp's 32 rows of bf16 values (row `own` of `from` for each lane, -1: zeros) on their way to rows row0 + lane of two
+// tiles, the first 64 dims of each into `hi`, the others into `lo`, where rows_to_parts takes them up.
+__device__ __forceinline__ void ask_rows(const __nv_bfloat16* from, int own, unsigned char* hi, unsigned char* lo, int row0, int lane) {
   const int c = lane & 15;  // the 16-byte piece
-  int mine = 0;
+#pragma unroll 4
+  for (int i = 0; i < 16; ++i) {
+    const int rr = row0 + 2 * i + (lane >> 4);
+    const int at = __shfl_sync(0xFFFFFFFFu, own, 2 * i + (lane >> 4));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(su32((c < 8 ? hi : lo) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4))),
+                 "l"(from + static_cast<size_t>(max(at, 0)) * kHD + c * 8), "r"(at >= 0 ? 16 : 0)
+                 : "memory");
+  }
+}
+// Those rows in two e4m3 parts, in place (half a warp has a whole row in hand), each row's largest magnitude scaled to
+// [2^6, 2^8) by a power of two with an even exponent: returns the exponent that takes the lane's row back, or 1000 for a
+// row with a NaN or an Inf, which becomes zeros.
+__device__ __forceinline__ int rows_to_parts(unsigned char* hi, unsigned char* lo, int row0, int lane) {
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  const int c = lane & 15;
+  // a thread to a row for the largest magnitude (the swizzle gives eight lanes banks of their own)
+  uint32_t top = 0u;
+  {
+    const int rr = row0 + lane;
+#pragma unroll 4
+    for (int k = 0; k < 16; ++k) {
+      const uint4 x = *reinterpret_cast<const uint4*>((k < 8 ? hi : lo) + rr * 128 + (((k & 7) ^ (rr & 7)) << 4));
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu), __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu)));
+    }
+    top = max(top & 0xFFFFu, top >> 16);
+  }
+  const bool odd = top >= 0x7F80u;
+  const int ex = (min(static_cast<int>(max(top >> 7, 1u)), 254) - 127) & ~1;
+  // half a warp to a row for the parts; 2^(6 - ex) in two factors (it reaches 2^132 for a row of zeros)
 #pragma unroll 1
   for (int i0 = 0; i0 < 16; i0 += 4) {
     uint4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int at = __shfl_sync(0xFFFFFFFFu, own, 2 * (i0 + i) + (lane >> 4));
-      x[i] = at >= 0 ? reinterpret_cast<const uint4*>(from + static_cast<size_t>(at) * kHD)[c] : make_uint4(0u, 0u, 0u, 0u);
+      const int rr = row0 + 2 * (i0 + i) + (lane >> 4);
+      x[i] = *reinterpret_cast<const uint4*>((c < 8 ? hi : lo) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
     }
+    __syncwarp();  // (the rows have been read)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const int e = __shfl_sync(0xFFFFFFFFu, odd ? 1000 : 6 - ex, 2 * (i0 + i) + (lane >> 4)), e0 = e / 2;
+      const float f0 = pow2n(e == 1000 ? 0 : e0), f1 = pow2n(e == 1000 ? 0 : e - e0);
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu), __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
-      top = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-      const bool odd = top >= 0x7F80u;
-      const int ex = (min(static_cast<int>(max(top >> 7, 1u)), 254) - 127) & ~1;
-      const float f0 = pow2n((6 - ex) / 2), f1 = pow2n(6 - ex - (6 - ex) / 2);  // (2^132 for a row of zeros)
       uint32_t h[4], l[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         float2 v = __fmul2_rn(make_float2(__uint_as_float(w[q] << 16), __uint_as_float(w[q] & 0xFFFF0000u)), make_float2(f0, f0));
-        v = odd ? make_float2(0.0f, 0.0f) : __fmul2_rn(v, make_float2(f1, f1));
+        v = __fmul2_rn(v, make_float2(f1, f1));
+        if (e == 1000) v = make_float2(0.0f, 0.0f);
         h[q] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
         const float2 g = __half22float2(__half2(__half2_raw(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(h[q]), __NV_E4M3))));
         l[q] = __nv_cvt_float2_to_fp8x2(make_float2(v.x - g.x, v.y - g.y), __NV_SATFINITE, __NV_E4M3);
@@ -102,11 +125,9 @@ __device__ __forceinline__ int rows_to_parts(const __nv_bfloat16* from, int own,
       const int rr = row0 + 2 * (i0 + i) + (lane >> 4), at = rr * 128 + (((c >> 1) ^ (rr & 7)) << 4) + 8 * (c & 1);
       *reinterpret_cast<uint2*>(hi + at) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
       *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
-      const int e = __shfl_sync(0xFFFFFFFFu, odd ? 1000 : ex - 6, (lane & 1) * 16);
-      if (lane >> 1 == i0 + i) mine = e;
     }
   }
-  return mine;
+  return odd ? 1000 : ex - 6;
 }
 
 // The steps of a part's tiles: 64 keys each, one for a tile with 64 keys or fewer.
@@ -422,10 +443,11 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           }
           // a node with a NaN or an Inf leaves the product: its scores get a NaN factor, rows
           // that see its V are marked
-          const int ex = rows_to_parts(static_cast<const __nv_bfloat16*>(tail.k), own, sK + slot * kCodeB, sK + second * kCodeB, dw * 32, lane);
-          s_fac[fac * kKeys + dw * 32 + lane] = ex == 1000 ? __int_as_float(0x7FC00000) : pow2f(ex / 2);
+          ask_rows(static_cast<const __nv_bfloat16*>(tail.k), own, sK + slot * kCodeB, sK + second * kCodeB, dw * 32, lane);
           unsigned char* slab = dst + dw * 32 * 128;
           bring_rows(static_cast<const __nv_bfloat16*>(tail.v), own, slab, lane);
+          const int ex = rows_to_parts(sK + slot * kCodeB, sK + second * kCodeB, dw * 32, lane);
+          s_fac[fac * kKeys + dw * 32 + lane] = ex == 1000 ? __int_as_float(0x7FC00000) : pow2f(ex / 2);
           const uint32_t top = row_top(slab, lane);
           const uint32_t bad = __ballot_sync(0xFFFFFFFFu, top >= 0x7F80u);
           if (lane == 0) s_bad[fac * 4 + dw] = bad;
@@ -456,19 +478,25 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
       Parts p = first;
       uint32_t T = 0, n_step = 0, n_part = 0;
       int ntail = 0;
-      bool live = true;
+      bool live = true, more = true;
+      unsigned char* q0 = sQ + grp * 2 * kCodeB;
+      // this thread's row of a part: node and query head (-1: none)
+      auto row_of = [&](const Parts& q, int* node) {
+        const int kvh = q.pq / g.RG, gr = ((q.pq - kvh * g.RG) * RT + grp) * kRows + r;  // row of the KV head
+        const bool ok = gr < g.G * g.R;
+        *node = ok ? gr / g.G : 0;
+        return ok ? kvh * g.G + gr - *node * g.G : -1;
+      };
+      auto ask_q = [&](const Parts& q) {
+        int node;
+        const int head = row_of(q, &node);
+        ask_rows(Q + static_cast<size_t>(q.b) * g.R * g.H * kHD, head >= 0 ? node * g.H + head : -1, q0, q0 + kCodeB, quarter * 32, lane);
+      };
+      ask_q(p);
       do {
-        const int kvh = p.pq / g.RG, rg = p.pq - kvh * g.RG;
-        const int gr = (rg * RT + grp) * kRows + r;  // row of the KV head
-        const bool row_ok = gr < g.G * g.R;
-        const int node = row_ok ? gr / g.G : 0, head = kvh * g.G + (row_ok ? gr - node * g.G : 0);
-        if (!warp_wait(&q_empty[grp], (n_part & 1) ^ 1, abort)) {
-          live = false;
-          break;
-        }
-        unsigned char* q0 = sQ + grp * 2 * kCodeB;
-        const int q_ex = rows_to_parts(Q + static_cast<size_t>(p.b) * g.R * g.H * kHD, row_ok ? node * g.H + head : -1, q0, q0 + kCodeB,
-                                       quarter * 32, lane);
+        int node;
+        const bool row_ok = row_of(p, &node) >= 0;
+        const int q_ex = rows_to_parts(q0, q0 + kCodeB, quarter * 32, lane);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(&q_full[grp]);
@@ -604,6 +632,17 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           }
           if (nodes) ++ntail;
         }
+        // the part's products with Q are done before its last product with V: the next part's rows
+        // may come while this one's record is written
+        const Parts done = p;
+        more = live && p.next(g, kv_len);
+        if (more) {
+          if (!warp_wait(&q_empty[grp], n_part & 1, abort)) {
+            live = false;
+            break;
+          }
+          ask_q(p);
+        }
         if (!live || !warp_wait(&o_done[grp], n_part & 1, abort)) {
           live = false;
           break;
@@ -614,28 +653,29 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
         // a row that sees a node with a non-finite V gets NaN (the marks are complete: the
         // products with V are)
         bool poison = false;
-        for (int x = max(p.x0, p.NT); x < p.x1; ++x) {
-          const uint32_t* bad = s_bad + (tail0 + x - max(p.x0, p.NT)) % kTailRing * 4;
-          const int wd = 2 * (x - p.NT);
+        for (int x = max(done.x0, done.NT); x < done.x1; ++x) {
+          const uint32_t* bad = s_bad + (tail0 + x - max(done.x0, done.NT)) % kTailRing * 4;
+          const int wd = 2 * (x - done.NT);
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             if (row_ok && wd + h < words)
               poison |= (mrow[wd + h] & (bad[2 * h] | (static_cast<uint64_t>(bad[2 * h + 1]) << 32))) != 0ull;
         }
         // the part's record: o normalized by its own sum, the base and the sum
-        const size_t rec = static_cast<size_t>(p.b) * Qn + p.pq + cta;
+        const size_t rec = static_cast<size_t>(done.b) * Qn + done.pq + cta;
         const int rrow = grp * kRows + r;
         if (q_bad) l = __int_as_float(0x7FC00000);
         const float inv = poison ? __int_as_float(0x7FC00000) : l != 0.0f ? 1.0f / l : 0.0f;
         float4* dst = reinterpret_cast<float4*>(ws_o + rec * (RT * kRows * kHD)) + rrow;
 #pragma unroll 1
-        for (int h = 0; h < 8; ++h) {
-          uint32_t z[16];
-          tmem_ld16(tO + 16 * h, z);
+        for (int h = 0; h < 4; ++h) {
+          uint32_t z[32];
+          tmem_ld32(tO + 32 * h, z);
+          tmem_wait32(z);
           if (row_ok) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              dst[(4 * h + j) * (RT * kRows)] =
+            for (int j = 0; j < 8; ++j)
+              dst[(8 * h + j) * (RT * kRows)] =
                   make_float4(__uint_as_float(z[4 * j]) * inv, __uint_as_float(z[4 * j + 1]) * inv, __uint_as_float(z[4 * j + 2]) * inv,
                               __uint_as_float(z[4 * j + 3]) * inv);
           }
@@ -643,17 +683,18 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
         fence_before();
         if (row_ok) ws_ml[rec * (RT * kRows) + rrow] = make_float2(m, l);
         if (grp == 0 && r == 0) {
-          int32_t* e = ends + 2 * (static_cast<size_t>(p.b) * Qn + p.pq);
-          if (p.x0 == 0) e[0] = cta;
-          if (p.x1 == p.real) e[1] = cta;
+          int32_t* e = ends + 2 * (static_cast<size_t>(done.b) * Qn + done.pq);
+          if (done.x0 == 0) e[0] = cta;
+          if (done.x1 == done.real) e[1] = cta;
         }
-      } while (p.next(g, kv_len));
+      } while (more);
     }
   }
   fence_before();
   if (__syncthreads_or(*abort != 0)) {
     // after a wait that ran out, the copies still in flight land (bounded) before the
     // shared memory goes
+    asm volatile("cp.async.wait_all;" ::: "memory");
     if (warp == 0) {
       const uint64_t t0 = gtimer();
       for (int i = 0; i < kSlots; ++i)
