@@ -363,4 +363,7 @@ __device__ __forceinline__ void block_bitonic_desc(uint64_t* s, int n) {
   }
 }
 
+// 2^e for e in [-126, 127]
+__device__ __forceinline__ float pow2n(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
 }  // namespace e3

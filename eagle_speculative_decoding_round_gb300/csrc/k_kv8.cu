@@ -11,7 +11,10 @@
 // nothing, so a value is rounded once, when it is stored, unless its code later falls into
 // e4m3's subnormal range.
 //
-// Bound: memory (two bytes read and one written a value).
+// Bound: memory (two bytes read and one written a value).  Measured on a GB300: two prompts of
+// 8191 rows, 4 layers, 8 heads of 128: append 74.6 us, 5.4 TB/s (80% of the copy rate), read 64.5
+// us, 6.2 TB/s.  32 paths of 1 to 7 rows, 32 layers: append 18.7 us (a chain of dependent loads:
+// length, page, exponent, rows; where the scale grows, the block's rows), read 38.1 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -28,8 +31,6 @@ namespace {
 constexpr int kExpMin = -100;      // of a block's scale; at most 120, which the largest magnitude below gives
 constexpr uint32_t kTopBits = 0x7F70u;  // 240 * 2^120 in bf16, the largest magnitude that is stored
 constexpr int kHold = 8;           // 16-byte pieces of new rows that a lane holds
-
-__device__ __forceinline__ float pow2f(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // The smallest e with the bf16 magnitude m <= 448 * 2^e (448 = 1.75 * 2^8), at least kExpMin.
 __device__ __forceinline__ int block_exp(uint32_t m) {
@@ -93,7 +94,9 @@ kv8_append_kernel(const __grid_constant__ Kv8Layers L8, e3_kv8_layer geo, const 
   const long long blk = P / geo.block + static_cast<int>(at - static_cast<unsigned>(kvh) * nblk);
   const long long tok0 = max(P, blk * geo.block);
   int m = n > 0 && kvh < geo.n_kv_heads ? static_cast<int>(max(0ll, min(P + n, (blk + 1) * geo.block) - tok0)) : 0;
-  const long long d0 = m > 0 ? slot_row(geo.page_table, geo.max_pages, geo.n_pages, geo.page_size, geo.n_kv_heads, b, static_cast<int>(tok0)) : 0;
+  const long long d0 = m > 0 ? slot_row(geo.page_table, geo.max_pages, geo.n_pages, geo.page_size, geo.n_kv_heads, b,
+                                        static_cast<int>(tok0))
+                             : 0;
   if (d0 < 0) {
     if (t == 0) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
     m = 0;
@@ -157,13 +160,13 @@ kv8_append_kernel(const __grid_constant__ Kv8Layers L8, e3_kv8_layer geo, const 
     }
     const int e = max(block_exp(top), e_held);
     unsigned char* codes = static_cast<unsigned char*>(L8.c[w][l]);
-    const float f = pow2f(-e);
+    const float f = pow2n(-e);
     uint2* out = reinterpret_cast<uint2*>(codes) + (drow << sh);
 #pragma unroll
     for (int i = 0; i < kHold; ++i)
       if (from[i] >= 0) out[i * T + t] = encode8(y[i], f);
     if (held > 0 && e > e_held) {
-      const float g = pow2f(max(e_held - e, -60));
+      const float g = pow2n(max(e_held - e, -60));
       uint4* old = reinterpret_cast<uint4*>(codes + ((drow - held) << (sh + 3)));
       for (int i = t; i < held << (sh - 1); i += T) {
         const uint4 c = old[i];
@@ -176,7 +179,7 @@ kv8_append_kernel(const __grid_constant__ Kv8Layers L8, e3_kv8_layer geo, const 
 }
 
 __device__ __forceinline__ void decode16(uint4 c, int e, uint4* out) {
-  const float f = pow2f(max(e, -126));
+  const float f = pow2n(max(e, -126));
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
   uint32_t o[8];
 #pragma unroll

@@ -7,14 +7,24 @@
 //   producer (warp 0)  brings K and V tiles by TMA into two stages each
 //   issuers (warps 1, 2; one per group)  S = Q K^T, then O += P V with P from tensor memory; each
 //                      group's softmax runs under the other's products
-//   warp 3             finds the next item; the items' rows of Q; V tiles with keys that some rows do not see: rows of
-//                      V that hold a NaN or an Inf, or nothing yet, leave the product (0 * Inf would
-//                      reach the rows that do not see them), rows that see them get NaN
+//   warp 3             finds the next item; the items' rows of Q; V tiles with keys that some rows
+//                      do not see: rows of V that hold a NaN or an Inf, or nothing yet, leave the
+//                      product (0 * Inf would reach the rows that do not see them), rows that see
+//                      them get NaN
 //   softmax (2 x 4 warps)  steps of 64 keys in two buffers of tensor memory: exponentials against
-//                      the base so far, P (bf16) over S.  No pass for the maximum but on an item's first tile: where a step's
-//                      sum passes kTop, or is NaN, the maximum is looked for, the base moved and
-//                      the step done again.  The diagonal's tiles take -Inf where unseen.
+//                      the base so far, P (bf16) over S.  No pass for the maximum but on an item's
+//                      first tile: where a step's sum passes kTop, or is NaN, the maximum is looked
+//                      for, the base moved and the step done again.  The diagonal's tiles take -Inf
+//                      where unseen.
 // O stays in tensor memory until the item's end; its rows are written from there.
+//
+// Bound: the tensor cores, with the exponentials (one a product's 2 * 64 multiply-adds) close
+// behind, and under a long load the power limit.  Measured on a GB300, 32 query and 8 KV heads of
+// 128: 32768 rows 5.54 ms, 1.59 PFLOP/s (82% of a library product's burst rate; 1.82 GHz under the
+// power cap); 16 prompts of 512 to 8192 rows 2.25 ms; 2048 rows 34 us; 4 pieces of 100 to 257 rows
+// behind 11000 to 16384 keys, 64 query heads, 304 us.  What the design gained, at 32768 rows: one
+// issuing warp for both groups 8.60 ms, one for each 6.70; S of one tile in flight 6.37, steps of
+// 64 keys in two buffers 5.64; P stored piece by piece under the exponentials 5.54.
 #include <algorithm>
 
 #include "e3_common.cuh"
@@ -51,18 +61,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint64_t* b) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(su32(b))
-               : "memory");
-}
-
-__device__ __forceinline__ void tma3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint64_t* b) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(su32(b))
-      : "memory");
-}
 
 // What the warp that finds the items tells the other roles.
 struct Item {
@@ -85,7 +83,8 @@ __device__ __forceinline__ int small_div(int x, float inv_g) { return static_cas
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
-prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CUtensorMap tmQ,
+                 const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ e3_kv_layer kv, const __grid_constant__ PromptGeom g, int box, bool q_box, float sm_scale,
                  __nv_bfloat16* __restrict__ O, float* __restrict__ lse, int32_t* dev_err) {
   using C = TcCfg<HD>;
@@ -588,7 +587,8 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
 }
 
 template <int HD>
-cudaError_t launch_tc(const void* Q, const CUtensorMap& mq, bool q_box, const CUtensorMap& mk, const CUtensorMap& mv, const e3_kv_layer& kv, const PromptGeom& g, int box,
+cudaError_t launch_tc(const void* Q, const CUtensorMap& mq, bool q_box, const CUtensorMap& mk, const CUtensorMap& mv,
+                      const e3_kv_layer& kv, const PromptGeom& g, int box,
                       float sm_scale, void* O, float* lse, int32_t* dev_err, cudaStream_t s) {
   static OncePerDevice<cudaError_t> attrs;
   const cudaError_t e = once_per_device(attrs, [] {

@@ -48,6 +48,7 @@ namespace e3 {
 
 namespace {
 
+constexpr int kNodeExp = 24;  // > kTop: a node's weight times a row of V sums below 2^(15 - 24 + 8) of it
 constexpr int kCodeB = kKeys * kHD / 2;  // bytes of a tile's codes, per operand
 constexpr int kScaleB = kKeys * kHD / 16;
 constexpr int kRawB = kCodeB + kScaleB;  // of one operand

@@ -18,6 +18,15 @@
 // K's exponents and Q's power meet the scores.  V's codes become bf16 values, exactly, with their
 // scale on them, as the nodes' V is: a shift and one product by a power of two for each pair; the
 // weights are good to 2^-8 (bf16).
+//
+// Bound: not memory (a tile's codes are 32 KB in some 2 us) but the chain of a step: S, its
+// exponentials, P, O, each handed on by a barrier; and, for a short prefix, a part's own cost of
+// about 20 us (Q, its record, the merge).  Measured on a GB300, 32 query and 8 KV heads of 128:
+// 32 requests of 512 to 8192 keys with 61 nodes 172 us (the codes: 285 MB), one
+// request of 65536 keys with 33 nodes 74 us, one of 2048 keys with 61 nodes 19.4 us.  What the
+// design gained: the granule kernel alone 872, 185 and 30 us; V in fp16 with a unit that follows
+// the largest scale 232, 90 and 22; K in two slots 213 and 87 (batch, long); masks and factors
+// found between the softmax's steps 213 and 82; Q read row by row, a row to a thread, 211 and 80.
 #include <cuda_fp8.h>
 #include <math.h>
 
@@ -51,13 +60,6 @@ struct Cfg {
 };
 static_assert(Cfg<2>::SMEM <= 232448, "shared memory of a CTA");
 
-__device__ __forceinline__ void tma2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint64_t* b) {
-  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(su32(b))
-               : "memory");
-}
-// 2^e for e in [-126, 127]
-__device__ __forceinline__ float pow2n(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 __device__ __forceinline__ uint32_t b2u(__nv_bfloat162 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __nv_bfloat162 u2b(uint32_t u) { return *reinterpret_cast<__nv_bfloat162*>(&u); }
@@ -545,7 +547,8 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
                   const float2* fac = reinterpret_cast<const float2*>(s_fac + slot * kKeys + h * kStep + 16 * d);
 #pragma unroll
                   for (int j = 0; j < 8; ++j) {
-                    const float2 v = __fmul2_rn(__fmul2_rn(__fmul2_rn(make_float2(__uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1])), fac[j]), cn), fac[j]);
+                    const float2 u = make_float2(__uint_as_float(z[2 * j]), __uint_as_float(z[2 * j + 1]));
+                    const float2 v = __fmul2_rn(__fmul2_rn(__fmul2_rn(u, fac[j]), cn), fac[j]);
                     z[2 * j] = __float_as_uint(v.x), z[2 * j + 1] = __float_as_uint(v.y);
                   }
                 }
@@ -725,6 +728,7 @@ V4Geom make_geom_tc(int B, int R, int H, int KVH, int max_kv_len) {
   g.RG = (g.G * R + g.rows - 1) / g.rows;
   g.max_kv_len = max_kv_len;
   g.workers = num_sms();
+  // (one request of 2048 keys with 61 nodes: 20.6 us; shares of 2, 3, 4 tiles at least: 26.9, 28.4, 31.0)
   g.min_share = 1;
   // what a part costs by itself (Q, the nodes, a record), in tiles, where shares are long enough
   g.extra = 4;
@@ -757,7 +761,9 @@ cudaError_t launch_tc(const __nv_bfloat16* q, const CUtensorMap& mk, const CUten
 
 }  // namespace
 
-// Up to 32 query rows per KV head the granule kernel's one or two tiles of 16 rows cost less.
+// Up to 32 query rows per KV head the granule kernel's one or two tiles of 16 rows cost less, beyond that its further
+// passes over the keys more.  (32 requests of 512 to 8192 keys, granule kernel and this one: 16 rows 59.8 and 124.0 us, 32
+// rows 99.2 and 123.2, 48 rows 144.0 and 125.2; one request of 32768 keys: 24.0 and 36.5, 31.8 and 36.3, 39.3 and 36.1.)
 bool verify8_uses_tc(int R, int H, int KVH, int hd) { return hd == kHD && H / KVH * R > 32; }
 
 size_t verify8_tc_workspace_bytes(int B, int R, int H, int KVH, int max_kv_len) {

@@ -17,7 +17,6 @@ constexpr int kStep = 64;    // keys of a step
 constexpr int kHD = 128;
 constexpr int kHalfB = 16384;            // bytes of a 64-dim half of an operand: [128 rows][128 B]
 constexpr int kOpB = 2 * kHalfB;         // bytes of an operand
-constexpr int kNodeExp = 24;  // > kTop: a node's weight times a row of V sums below 2^(15 - 24 + 8) of it
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 // 2^e for any int e a float's exponent can meet here (|e| <= 252), as a product of two normals

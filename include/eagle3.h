@@ -419,8 +419,8 @@ E3_API e3_status eagle3_rope_init(const e3_rope_spec* spec /* host */, e3_rope* 
 /* ---------------------------------------------------------------------------
  * tree_qkv_append: from one layer's projected rows to its attention's inputs --
  * norms of each query and key head, rotary positions, and the append of K and V
- * to the paged cache, in one pass.  It writes what tree_verify_attn and
- * tree_verify_attn4 read ("Thinking Budget 与 EAGLE-3", 一棵候选树怎样被验证: the
+ * to the paged cache, in one pass.  It writes what tree_verify_attn, tree_verify_attn4,
+ * tree_verify_attn8 and prompt_attn read ("Thinking Budget 与 EAGLE-3", 一棵候选树怎样被验证: the
  * nodes' K/V are temporary entries behind the prefix; "EAGLE 系列与 DFlash", §二
  * 关键新增步骤①: a node's position follows from its depth).
  * Row r < n_rows[b] of request b (n_rows NULL: all R; values are clamped to
@@ -607,10 +607,12 @@ E3_API e3_status kv8_read(const e3_kv8_layer* layers, const e3_kv_layer* dst, in
  * tree_verify_attn8: tree_verify_attn over a prefix held in 8 bits; arguments, tail,
  * masks, rows without a key and errors as tree_verify_attn4.
  * Arithmetic: products exact but for the weights, which are good to 2^-8, sums in fp32.
- *   Values of V up to 2^100 in magnitude cannot overflow them.  Q's values below 2^-24 of
- *   their row's largest lose bits, and so do weights below 2^-21 of their row's largest in
- *   units of the largest V scale of the request: blocks whose V scale is 2^20 below it
- *   count less exactly.
+ *   Values of V up to 2^100 in magnitude cannot overflow them.  Up to 32 query rows per KV
+ *   head, and for heads of 64: Q's values below 2^-24 of their row's largest lose bits, and
+ *   so do weights below 2^-21 of their row's largest in units of the largest V scale of the
+ *   request: blocks whose V scale is 2^20 below it count less exactly.  With more rows: Q's
+ *   values below 2^-10 of their row's largest, and the nodes' K below 2^-10 of theirs, lose
+ *   bits: they are good to 2^-18 of that largest value; V's scales lose none.
  * Scratch: eagle3_verify8_workspace_bytes(...) bytes (0 for sizes that the call refuses),
  *   16-byte aligned; calls that may overlap on the GPU need scratch of their own.
  * ------------------------------------------------------------------------- */
@@ -641,7 +643,8 @@ E3_API size_t eagle3_verify8_workspace_bytes(int B, int R, int n_q_heads, int n_
  * NaN or an Inf in V gets NaN or Inf in o, in that dimension at least.
  * n_rows[b] outside [0, max_rows], kv_len[b] outside [0, max_kv_len], rows outside
  * [0, n_total), or slots beyond max_pages set E3_DEV_ERR_CAPACITY and leave the request's
- * outputs unwritten; a page id out of range sets it and makes them unspecified.
+ * outputs unwritten; a page id out of range sets it and makes them unspecified.  Rows of
+ * two requests must not overlap.
  * Arithmetic: bf16: products in bf16 with fp32 sums, weights good to 2^-9 and summed
  *   before that rounding; fp32: fp32 throughout.
  * Limits: head_dim 64 or 128 (fp32: any multiple of 32 up to 256); n_q_heads %
