@@ -18,11 +18,15 @@
 //                      where unseen.
 // O stays in tensor memory until the item's end; its rows are written from there.
 //
+// Calls of few items behind long contexts (prompt_splits) are cut into equal shares, one for each
+// CTA, whose borders may lie between any two tiles of an item's keys: the parts leave fp32 records (O,
+// base, sum), which prompt_merge_kernel joins in the order of the keys.
+//
 // Bound: the tensor cores, with the exponentials (one a product's 2 * 64 multiply-adds) close
 // behind, and under a long load the power limit.  Measured on a GB300, 32 query and 8 KV heads of
 // 128: 32768 rows 5.54 ms, 1.59 PFLOP/s (82% of a library product's burst rate; 1.82 GHz under the
 // power cap); 16 prompts of 512 to 8192 rows 2.25 ms; 2048 rows 34 us; 4 pieces of 100 to 257 rows
-// behind 11000 to 16384 keys, 64 query heads, 304 us.  What the design gained, at 32768 rows: one
+// behind 12288 to 16384 keys, 64 query heads, 286 us (306 without shares).  What the design gained, at 32768 rows: one
 // issuing warp for both groups 8.60 ms, one for each 6.70; S of one tile in flight 6.37, steps of
 // 64 keys in two buffers 5.64; P stored piece by piece under the exponentials 5.54.
 #include <algorithm>
@@ -46,6 +50,7 @@ constexpr int kHalfB = 16384;    // bytes of 64 dims of a tile: [128 rows][128 B
 constexpr int kThreads = 384;
 constexpr int kSoftmax0 = 4;     // first softmax warp
 constexpr float kTop = 32768.0f;
+constexpr int kShift = 8;        // an item has 2 * kRows flat rows
 
 template <int HD>
 struct TcCfg {
@@ -71,10 +76,15 @@ struct Item {
   int c;          // keys before the request's rows
   int keys0, keys1;  // keys that the groups' rows reach (0: the group has no rows)
   int common;     // keys that all rows see
+  int t0, t1;     // tiles of keys that this CTA takes
+  int rec;        // number of the record that they leave (-1: all of the item's, no record)
   __device__ __forceinline__ int all_keys() const { return max(keys0, keys1); }
   __device__ __forceinline__ int keys_of(int g) const { return g ? keys1 : keys0; }
-  __device__ __forceinline__ int tiles() const { return (all_keys() + kKeys - 1) / kKeys; }
-  __device__ __forceinline__ int steps_of(int g) const { return (keys_of(g) + kStep - 1) / kStep; }
+  __device__ __forceinline__ int key0() const { return t0 * kKeys; }
+  __device__ __forceinline__ int tiles() const { return t1 - t0; }
+  __device__ __forceinline__ int steps_of(int g) const {
+    return max(0, (min(keys_of(g), t1 * kKeys) - key0() + kStep - 1) / kStep);
+  }
   // some row of the item does not see all of tile t's keys
   __device__ __forceinline__ bool masked(int t) const { return (t + 1) * kKeys > common; }
 };
@@ -86,7 +96,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CUtensorMap tmQ,
                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ e3_kv_layer kv, const __grid_constant__ PromptGeom g, int box, bool q_box, float sm_scale,
-                 __nv_bfloat16* __restrict__ O, float* __restrict__ lse, int32_t* dev_err) {
+                 __nv_bfloat16* __restrict__ O, float* __restrict__ lse, float* __restrict__ ws_o, float2* __restrict__ ws_ml,
+                 int32_t* dev_err) {
   using C = TcCfg<HD>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -169,7 +180,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
     for (uint32_t k = 0; live && next_item(k, it); ++k) {
       item_done(k);
       if ((kv.flags & E3_KV_SELFTEST_STALL) && blockIdx.x == 0) break;  // (keys that never come)
-      const int keys = it.all_keys(), tiles = it.tiles();
+      const int keys = it.all_keys();
       const int32_t* table = kv.page_table + static_cast<size_t>(it.b) * kv.max_pages;
       // lane i brings keys [i box, (i + 1) box) of a tile; the row of its first one, -1: none
       auto box_row = [&](int t) {
@@ -183,9 +194,9 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         }
         return (page * g.KVH + it.kvh) * kv.page_size + (key - pi * kv.page_size);
       };
-      int r = box_row(0);
-      for (int t = 0; t < tiles; ++t, ++T) {
-        const int st = T & 1, r_next = t + 1 < tiles ? box_row(t + 1) : -1;
+      int r = box_row(it.t0);
+      for (int t = it.t0; t < it.t1; ++t, ++T) {
+        const int st = T & 1, r_next = t + 1 < it.t1 ? box_row(t + 1) : -1;
         const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, r >= 0)) * static_cast<uint32_t>(box) * HD * 2;
         auto load = [&](uint64_t* full, unsigned char* dst, const CUtensorMap* map) {
           if (lane == 0) bar_expect(full, bytes);
@@ -253,7 +264,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       for (int u = 0; live && u < mine; ++u) {
         const uint32_t st = (T + (u >> 1)) & 1, bf = (n_step + u) & 1;
         if (!(u & 1)) {
-          if (it.masked(u >> 1)) {
+          if (it.masked(it.t0 + (u >> 1))) {
             live = warp_wait(&v_ok[st], (use_ok >> st) & 1, abort);
             use_ok ^= 1u << st;
           } else {
@@ -280,7 +291,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         const uint32_t st = (T + t) & 1;
         live = warp_wait(&k_full[st], ((T + t) >> 1) & 1, abort);
         if (live && lane == 0) bar_arrive(&k_empty[st]);
-        if (it.masked(t)) {
+        if (it.masked(it.t0 + t)) {
           live = live && warp_wait(&v_ok[st], (use_ok >> st) & 1, abort);
           use_ok ^= 1u << st;
         } else {
@@ -297,13 +308,40 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
     bool live = true;
     const PromptReq own = prompt_req(g, lane);
     Item it, next;
+    long long cost_at = 0, cost_end = 0;  // the CTA's share
+    if (g.split) {
+      const PromptShares s = prompt_shares(g, own, gridDim.x);
+      cost_at = blockIdx.x * s.share;
+      cost_end = min(s.total, cost_at + s.share);
+    }
     // finds item k and tells the others
     auto publish = [&](uint32_t k) {
-      const long long row = static_cast<long long>(k) * gridDim.x;
-      const PromptItem at = find_prompt_item(g, own, row + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
+      PromptItem at;
+      PromptPlace place;
+      bool cut = false;
       next.b = -1;
+      if (!g.split) {
+        const long long row = static_cast<long long>(k) * gridDim.x;
+        at = find_prompt_item(g, own, row + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
+      } else {
+        // the next part of the CTA's share that has a tile of keys
+        at.b = g.B;
+        while (cost_at < cost_end) {
+          place = prompt_place(g, own, cost_at);
+          const int last = min((place.it.tile + 1) << g.shift, place.q.n * g.G) - 1;
+          const int nt = (place.q.c + last / g.G + kKeys) / kKeys;
+          next.t0 = cut_tile(place.in, place.cost, nt);
+          next.t1 = cut_tile(place.in + (cost_end - cost_at), place.cost, nt);
+          cost_at += place.cost - place.in;
+          if (next.t1 > next.t0) {
+            at = place.it;
+            cut = next.t1 - next.t0 < nt;
+            break;
+          }
+        }
+      }
       if (at.b < g.B) {
-        const PromptReq q = prompt_req(g, at.b);
+        const PromptReq q = g.split ? place.q : prompt_req(g, at.b);
         const int f0 = at.tile * 2 * kRows;
         next.b = at.b;
         next.kvh = at.kvh;
@@ -315,6 +353,12 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         next.common = q.c + next.row + 1;
         next.keys0 = q.c + (f0 + min(kRows, next.flat) - 1) / g.G + 1;
         next.keys1 = kRows < next.flat ? q.c + (f0 + min(2 * kRows, next.flat) - 1) / g.G + 1 : 0;
+        if (!g.split) {
+          next.t0 = 0;
+          next.t1 = (next.all_keys() + kKeys - 1) / kKeys;
+        }
+        // (a CTA's share begins within one item at most, and ends within one)
+        next.rec = !cut ? -1 : 2 * blockIdx.x + (next.t0 > 0 ? 0 : 1);
       }
       if (!warp_wait(&item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort)) return false;
       if (lane == 0) {
@@ -330,7 +374,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       // Q: 128 rows of each group
 #pragma unroll 1
       for (int w = 0; live && w < 2; ++w) {
-        if (it.keys_of(w) == 0) continue;
+        if (it.steps_of(w) == 0) continue;
         if (!warp_wait(&q_empty[w], (use_q >> w) & 1, abort)) {
           live = false;
           break;
@@ -374,9 +418,9 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       live = live && publish(k + 1);
       if (!live) break;
       // V tiles with keys that some rows do not see
-      const int keys = it.all_keys(), tiles = it.tiles(), t0 = it.common / kKeys;
-      for (int t = t0; t < tiles; ++t) {
-        const int st = (T + t) & 1;
+      const int keys = it.all_keys(), t0 = it.common / kKeys;
+      for (int t = max(t0, it.t0); t < it.t1; ++t) {
+        const int st = (T + t - it.t0) & 1;
         if (!warp_wait(&v_raw[st], (use_raw >> st) & 1, abort)) {
           live = false;
           break;
@@ -411,7 +455,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         __syncwarp();
         if (lane == 0) bar_arrive(&v_ok[st]);
       }
-      T += tiles;
+      T += it.tiles();
     }
   } else {
     // softmax: warp w of group grp reads TMEM lane quarter warp % 4 (rows 32 quarter ..)
@@ -432,7 +476,8 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       const int f = grp * kRows + r, over = small_div(it.rem + f, g.inv_G), row = it.row + over;
       const bool row_ok = f < it.flat;
       const int see = row_ok ? it.c + row + 1 : it.keys_of(grp);  // keys that the row sees
-      float m = -INFINITY, l = 0.0f;
+      // (a row that sees none of the part's keys sees none in any step: every weight is 0, whatever the base)
+      float m = see > it.key0() ? -INFINITY : 0.0f, l = 0.0f;
       for (int u = 0; u < mine; ++u, ++n_step) {
         const uint32_t bf = n_step & 1, tB = tS + bf * kStep;
         if (!warp_wait(&s_full[2 * grp + bf], (n_step >> 1) & 1, abort)) {
@@ -440,7 +485,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
           break;
         }
         fence_after();
-        const int vis = see - u * kStep;  // keys of the step that the row sees
+        const int vis = see - it.key0() - u * kStep;  // keys of the step that the row sees
         const bool masked = __any_sync(0xFFFFFFFFu, vis < kStep);
         bool look = u == 0;  // for the maximum
         float s;
@@ -510,13 +555,34 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       fence_after();
       // a row that sees a V which was taken out gets NaN (the marks are complete: the products are)
       bool poison = false;
-      for (int t = it.common / kKeys; t * kKeys < see; ++t) {
+      for (int t = max(it.t0, it.common / kKeys); t < it.t1 && t * kKeys < see; ++t) {
         const uint32_t* bad = s_bad + ((k & 1) * 4 + t - it.common / kKeys) * 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int vis = see - t * kKeys - 32 * i;
           if (vis > 0) poison |= (bad[i] & (vis >= 32 ? ~0u : (1u << vis) - 1u)) != 0u;
         }
+      }
+      if (it.rec >= 0) {
+        // a part's record: sums against the base m, quad of dims by quad, rows side by side
+        const bool counts = row_ok && see > it.key0();
+        const float taint = poison ? __int_as_float(0x7FC00000) : 0.0f;
+        float4* to = reinterpret_cast<float4*>(ws_o) + static_cast<size_t>(it.rec) * (HD / 4 * 2 * kRows) + grp * kRows + r;
+#pragma unroll 1
+        for (int q = 0; q < HD / 16; ++q) {
+          uint32_t y[16];
+          tmem_ld16(tO + 16 * q, y);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (counts)
+              to[(4 * q + j) * (2 * kRows)] =
+                  make_float4(__uint_as_float(y[4 * j]) + taint, __uint_as_float(y[4 * j + 1]) + taint,
+                              __uint_as_float(y[4 * j + 2]) + taint, __uint_as_float(y[4 * j + 3]) + taint);
+        }
+        fence_before();
+        if (counts) ws_ml[static_cast<size_t>(it.rec) * (2 * kRows) + grp * kRows + r] = make_float2(m, l);
+        item_done(k);
+        continue;
       }
       const size_t at = (static_cast<size_t>(it.start) + row) * g.H + it.kvh * g.G + (it.rem + f - over * g.G);
       const float inv = poison ? __int_as_float(0x7FC00000) : 1.0f / l;
@@ -586,26 +652,131 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
+// The items that borders between shares cut: their parts' records, joined in the order of the keys.  A CTA takes 32 rows
+// of the item that border w lies in, where that is the item's first border.
+constexpr int kMergeRows = 32;
+
+template <int HD>
+__global__ void __launch_bounds__(256)
+prompt_merge_kernel(const __grid_constant__ PromptGeom g, int workers, const float* __restrict__ ws_o,
+                    const float2* __restrict__ ws_ml, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
+  constexpr int CHUNKS = 2 * kRows / kMergeRows, NQ = HD / 32, AHEAD = 4;  // NQ: quads of dims of a thread
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w = 1 + blockIdx.x / CHUNKS, chunk = blockIdx.x % CHUNKS;
+  const PromptReq own = prompt_req(g, lane);
+  const PromptShares s = prompt_shares(g, own, workers);
+  const long long border = w * s.share;
+  if (border >= s.total) return;
+  const PromptPlace p = prompt_place(g, own, border);
+  if (p.in == 0 || p.in > s.share) return;
+  const PromptReq q = p.q;
+  const int f0 = p.it.tile << g.shift, flat = q.n * g.G, r = chunk * kMergeRows + lane, f = f0 + r;
+  if (f0 + chunk * kMergeRows >= flat) return;
+  const bool ok = f < flat;
+  const int row = (ok ? f : flat - 1) / g.G, head = (ok ? f : flat - 1) - row * g.G, see = q.c + row + 1;
+  const int nt = (q.c + (min(f0 + 2 * kRows, flat) - 1) / g.G + kKeys) / kKeys;
+  // part j is CTA w - 1 + j's: of the item's cost, what lies before the border, then a share each
+  const int parts = static_cast<int>((p.cost - p.in + s.share - 1) / s.share) + 1;
+  float M = -INFINITY, den = 0.0f, acc[4 * NQ];
+#pragma unroll
+  for (int i = 0; i < 4 * NQ; ++i) acc[i] = 0.0f;
+  for (int j0 = 0; j0 < parts; j0 += AHEAD) {
+    float2 y[AHEAD];
+    float4 x[AHEAD][NQ];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) {
+      const int j = j0 + u;
+      y[u] = make_float2(-INFINITY, 0.0f);
+      if (j >= parts) continue;
+      const int t0 = j == 0 ? 0 : cut_tile(p.in + (j - 1) * s.share, p.cost, nt), t1 = cut_tile(p.in + j * s.share, p.cost, nt);
+      if (t0 == 0 && t1 == nt) return;  // (one CTA has all of its tiles: O is written)
+      if (t1 <= t0 || see <= t0 * kKeys) continue;
+      const size_t rec = 2 * static_cast<size_t>(w - 1 + j) + (t0 > 0 ? 0 : 1);
+      y[u] = ws_ml[rec * (2 * kRows) + r];
+      const float4* from = reinterpret_cast<const float4*>(ws_o) + rec * (HD / 4 * 2 * kRows) + r;
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) x[u][i] = from[(warp + 8 * i) * (2 * kRows)];
+    }
+    float top = M;
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) top = fmaxf(top, y[u].x);
+    if (top > M) {
+      const float c = ex2(M - top);
+      M = top;
+      den *= c;
+#pragma unroll
+      for (int i = 0; i < 4 * NQ; ++i) acc[i] *= c;
+    }
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u)
+      if (y[u].y != 0.0f) {  // (a part that the row sees has a sum of 1 at least, or NaN)
+        const float c = ex2(y[u].x - M);
+        den = fmaf(y[u].y, c, den);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          acc[4 * i] = fmaf(x[u][i].x, c, acc[4 * i]), acc[4 * i + 1] = fmaf(x[u][i].y, c, acc[4 * i + 1]);
+          acc[4 * i + 2] = fmaf(x[u][i].z, c, acc[4 * i + 2]), acc[4 * i + 3] = fmaf(x[u][i].w, c, acc[4 * i + 3]);
+        }
+      }
+  }
+  if (!ok) return;
+  const size_t at = (static_cast<size_t>(q.start) + row) * g.H + p.it.kvh * g.G + head;
+  const float inv = 1.0f / den;
+#pragma unroll
+  for (int i = 0; i < NQ; ++i)
+    reinterpret_cast<uint2*>(O + at * HD)[warp + 8 * i] =
+        make_uint2(pack2_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack2_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
+  if (warp == 0) lse[at] = (M + log2f(den)) * kLn2;
+}
+
+// Whether the call is cut into equal shares: where that saves more tiles of keys (some 1.2 us each) than the records and
+// the second kernel cost: 8, and 12 more where items have all of their rows.  By the call's bounds.  Measured, whole items and
+// equal shares, 32 query and 8 KV heads of 128: 16 rows behind 30000 keys 266 and 45 us, 8 requests of 64 rows behind 8192 keys
+// 101 and 72, 4 of 1 row behind 2048 keys 26.4 and 24.0; where whole items stay: 4 of 1 row behind 1024 keys 17.7 and 21.4, 512
+// rows behind 2048 keys 37.1 and 42.2, 1000 rows 20.7 and 37.1.
+bool prompt_splits(const PromptGeom& g, int max_kv_len) {
+  const long long items = prompt_items_bound(g), sms = num_sms();
+  if (items > 16 * sms) return false;
+  const double ctx = static_cast<double>(max_kv_len) / kKeys, own = static_cast<double>(g.max_rows) / kKeys;
+  const double share = items * (0.75 * ctx + own / 2) / sms;  // (contexts differ)
+  const double whole = items <= sms ? ctx + own : ((items + sms - 1) / sms) * ctx + items * own / (2 * sms);
+  return whole - share > 8.0 + 12.0 * std::min(1.0, static_cast<double>(g.max_rows) * g.G / (2 * kRows));
+}
+size_t record_rows() { return static_cast<size_t>(2) * num_sms() * 2 * kRows; }
+
 template <int HD>
 cudaError_t launch_tc(const void* Q, const CUtensorMap& mq, bool q_box, const CUtensorMap& mk, const CUtensorMap& mv,
-                      const e3_kv_layer& kv, const PromptGeom& g, int box,
-                      float sm_scale, void* O, float* lse, int32_t* dev_err, cudaStream_t s) {
+                      const e3_kv_layer& kv, const PromptGeom& g, int box, float sm_scale, void* O, float* lse, int32_t* dev_err,
+                      float* ws_o, float2* ws_ml, cudaStream_t s) {
   static OncePerDevice<cudaError_t> attrs;
   const cudaError_t e = once_per_device(attrs, [] {
     return cudaFuncSetAttribute(prompt_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<HD>::SMEM);
   });
   if (e != cudaSuccess) return e;
-  const long long items = prompt_items_bound(g);
-  return launch_pdl(prompt_tc_kernel<HD>, dim3(static_cast<unsigned>(std::min<long long>(items, num_sms()))), dim3(kThreads),
-                    TcCfg<HD>::SMEM, s, 1, static_cast<const __nv_bfloat16*>(Q), mq, mk, mv, kv, g, box, q_box, sm_scale,
-                    static_cast<__nv_bfloat16*>(O), lse, dev_err);
+  const int workers = g.split ? num_sms() : static_cast<int>(std::min<long long>(prompt_items_bound(g), num_sms()));
+  const cudaError_t el =
+      launch_pdl(prompt_tc_kernel<HD>, dim3(workers), dim3(kThreads), TcCfg<HD>::SMEM, s, 1, static_cast<const __nv_bfloat16*>(Q), mq, mk,
+                 mv, kv, g, box, q_box, sm_scale, static_cast<__nv_bfloat16*>(O), lse, ws_o, ws_ml, dev_err);
+  if (el != cudaSuccess || !g.split) return el;
+  return launch_pdl(prompt_merge_kernel<HD>, dim3((workers - 1) * (2 * kRows / kMergeRows)), dim3(256), 0, s, 1, g, workers, ws_o, ws_ml,
+                    static_cast<__nv_bfloat16*>(O), lse);
 }
 
 }  // namespace
 
-e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, float sm_scale, void* O, float* lse,
-                           int32_t* dev_err, cudaStream_t s) {
-  g.shift = 8;  // 2 * kRows
+size_t prompt_tc_workspace_bytes(PromptGeom g, int hd, int max_kv_len) {
+  g.shift = kShift;
+  return prompt_splits(g, max_kv_len) ? record_rows() * (hd * sizeof(float) + sizeof(float2)) : 0;
+}
+
+e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, int max_kv_len, float sm_scale, void* O, float* lse,
+                           int32_t* dev_err, void* ws, cudaStream_t s) {
+  g.shift = kShift;
+  g.split = prompt_splits(g, max_kv_len);
+  float* ws_o = static_cast<float*>(ws);
+  float2* ws_ml = g.split ? reinterpret_cast<float2*>(ws_o + record_rows() * kv.head_dim) : nullptr;
   int box = 16;  // keys of a TMA box: what divides a page, as far as a tile has
   while (box < kKeys && kv.page_size % (2 * box) == 0) box *= 2;
   const unsigned long long rows = static_cast<unsigned long long>(kv.n_pages) * kv.n_kv_heads * kv.page_size;
@@ -626,9 +797,9 @@ e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, f
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     E3_REQUIRE(r == CUDA_SUCCESS, E3_ERR_INVALID_ARG, "prompt_attn: cuTensorMapEncodeTiled rejected Q (%d)", static_cast<int>(r));
   }
-  const cudaError_t e = kv.head_dim == 128 ? launch_tc<128>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, s)
-                                           : launch_tc<64>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, s);
-  return e == cudaSuccess ? E3_OK : cuda_status(e, "prompt_tc_kernel");
+  const cudaError_t e = kv.head_dim == 128 ? launch_tc<128>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, ws_o, ws_ml, s)
+                                           : launch_tc<64>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, ws_o, ws_ml, s);
+  return e == cudaSuccess ? E3_OK : cuda_status(e, "prompt_tc kernels");
 }
 
 }  // namespace e3

@@ -14,11 +14,14 @@ struct PromptGeom {
   int B, H, KVH, G;
   float inv_G;
   int shift;       // a tile has 1 << shift flat rows
+  int split;       // the call is cut into equal shares, items along their keys
   int n_total, max_rows, max_kv_len;
   long long cap;  // slots that a request's pages hold
 };
 
 namespace {
+
+constexpr int kLeastKeys = 512;  // of a share, beside what an item costs by itself
 
 struct PromptReq {
   int start, n, c;  // first row, rows (0 where the request's sizes are out of bounds), keys before them
@@ -101,6 +104,85 @@ __device__ __forceinline__ PromptItem find_prompt_item(const PromptGeom& g, cons
   return it;
 }
 
+// What an item costs, in 1 / G keys: its rows' keys (a tile of rows taken as whole), and what it costs by itself.
+constexpr int kItemKeys = 256;
+__device__ __forceinline__ long long item_cost(const PromptGeom& g, const PromptReq& q, int tile) {
+  return (static_cast<long long>(q.c) + kItemKeys) * g.G + (static_cast<long long>(tile + 1) << g.shift);
+}
+// of a request's last n tiles, all KV heads
+__device__ __forceinline__ long long last_cost(const PromptGeom& g, const PromptReq& q, int tiles, long long n) {
+  return g.KVH * (n * (static_cast<long long>(q.c) + kItemKeys) * g.G + ((n * (2ll * tiles - n + 1) / 2) << g.shift));
+}
+// The call's cost in equal shares, one for each CTA.
+struct PromptShares {
+  long long total, share;
+};
+__device__ __forceinline__ PromptShares prompt_shares(const PromptGeom& g, const PromptReq& own, int workers) {
+  const int lane = threadIdx.x & 31;
+  long long cost = 0;
+  for (int b0 = 0; b0 < g.B; b0 += 32) {
+    const PromptReq q = b0 == 0 ? own : prompt_req(g, b0 + lane);
+    const int tiles = prompt_tiles(g, q);
+    cost += last_cost(g, q, tiles, tiles);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) cost += __shfl_xor_sync(0xFFFFFFFFu, cost, o);
+  const long long least = static_cast<long long>(kItemKeys + kLeastKeys) * g.G;
+  return {cost, max((cost + workers - 1) / workers, least)};
+}
+// The item at cost `at` < total, and where in its cost that is.  The items' order: request by request, the last tiles first,
+// KV heads side by side.
+struct PromptPlace {
+  PromptItem it;
+  PromptReq q;
+  long long in, cost;
+};
+__device__ __forceinline__ PromptPlace prompt_place(const PromptGeom& g, const PromptReq& own, long long at) {
+  const int lane = threadIdx.x & 31;
+  PromptPlace p;
+  p.it.b = g.B;
+  for (int b0 = 0; b0 < g.B; b0 += 32) {
+    const PromptReq q = b0 == 0 ? own : prompt_req(g, b0 + lane);
+    const int tiles = prompt_tiles(g, q);
+    const long long u = last_cost(g, q, tiles, tiles);
+    long long incl = u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, incl > at);
+    if (hit) {
+      const int k = __ffs(hit) - 1;
+      p.it.b = b0 + k;
+      at -= __shfl_sync(0xFFFFFFFFu, incl - u, k);
+      break;
+    }
+    at -= __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  p.q = prompt_req(g, p.it.b);
+  const int tiles = prompt_tiles(g, p.q);
+  int a = 0, z = tiles;  // tiles from the request's last: last_cost(a) <= at < last_cost(z)
+  while (z - a > 1) {
+    const int mid = (a + z) >> 1;
+    if (last_cost(g, p.q, tiles, mid) <= at)
+      a = mid;
+    else
+      z = mid;
+  }
+  at -= last_cost(g, p.q, tiles, a);
+  p.it.tile = tiles - 1 - a;
+  p.cost = item_cost(g, p.q, p.it.tile);
+  p.it.kvh = static_cast<int>(at / p.cost);
+  p.in = at - p.it.kvh * p.cost;
+  return p;
+}
+// The tile of keys, of nt, that an item is cut at for a border at `in` of its cost (never falls as `in` grows).
+__device__ __forceinline__ int cut_tile(long long in, long long cost, int nt) {
+  if (in >= cost) return nt;
+  return in <= 0 ? 0 : min(nt, static_cast<int>(__fdiv_rn(__fmul_rn(static_cast<float>(in), static_cast<float>(nt)), static_cast<float>(cost))));
+}
+
 // An upper bound of the items of a call.
 inline long long prompt_items_bound(const PromptGeom& g) {
   const long long by_rows = ((static_cast<long long>(g.n_total) * g.G) >> g.shift) + g.B;
@@ -110,7 +192,9 @@ inline long long prompt_items_bound(const PromptGeom& g) {
 
 }  // namespace
 
-e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, float sm_scale, void* O, float* lse,
-                           int32_t* dev_err, cudaStream_t s);
+// bf16: shift, split are set here; max_kv_len as the call's (its scratch goes by it)
+size_t prompt_tc_workspace_bytes(PromptGeom g, int hd, int max_kv_len);
+e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, int max_kv_len, float sm_scale, void* O, float* lse,
+                           int32_t* dev_err, void* ws, cudaStream_t s);
 
 }  // namespace e3

@@ -300,3 +300,144 @@ def test_prompt_attn_wait_that_runs_out():
     torch.cuda.synchronize()
     assert int(err.item()) == 0
     check(d, O, lse)
+
+
+SPLIT = [
+    # H, KVH, hd, rows, ctx, page: few items behind long contexts, which are cut along their keys
+    (8, 1, 128, [5], [20000], 16),                                      # one item in many parts
+    (64, 8, 128, [100, 152, 204, 257], [3000, 2800, 2500, 2300], 64),   # more items than SMs
+    (8, 8, 64, [1] * 5, [4000, 0, 2999, 129, 2500], 16),
+    (5, 1, 128, [300, 52], [9000, 100], 48),                            # tiles end inside a row
+    (2, 2, 128, [700, 1], [1500, 5000], 128),                           # diagonals in the last parts
+    (40, 8, 128, [3, 0, 64], [2176, 5000, 2175], 64),
+]
+
+
+@pytest.mark.parametrize("H,KVH,hd,rows,ctx,page", SPLIT)
+def test_prompt_attn_split_along_the_keys(H, KVH, hd, rows, ctx, page):
+    d = inputs(11 + H + rows[0], H, KVH, hd, rows, ctx, page, gap=1)
+    records = e3.eagle3_prompt_workspace_bytes(d["B"], d["total"], max(rows), H, KVH, hd, max(ctx), e3.E3_BF16)
+    assert records > 0
+    O, lse, err = call(d)
+    O2, lse2, _ = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    check(d, O, lse)
+
+
+def test_prompt_attn_split_with_many_requests_and_a_loose_bound():
+    """More requests than lanes, lengths from none to far apart, the bounds above all of them."""
+    rng = np.random.default_rng(14)
+    rows = [int(x) for x in np.where(rng.random(45) < 0.3, 0, rng.integers(1, 60, 45))]
+    ctx = [int(x) for x in np.where(rng.random(45) < 0.5, 0, rng.integers(1, 3000, 45))]
+    ctx[7], rows[7], ctx[33], rows[33] = 6000, 0, 5000, 130
+    d = inputs(14, 8, 2, 128, rows, ctx, 16, gap=1)
+    assert e3.eagle3_prompt_workspace_bytes(45, d["total"], 200, 8, 2, 128, 9000, e3.E3_BF16) > 0
+    O, lse, err = call(d, max_rows=200, max_ctx=9000)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(d, O, lse)
+
+
+def test_prompt_attn_split_sharp_rows():
+    """Parts whose bases differ widely, late maxima, rows of zeros."""
+    d = inputs(15, 8, 2, 128, [40, 9], [4000, 2500], 64)
+    rng = np.random.default_rng(3)
+    d["Q"] *= np.exp2(rng.integers(-12, 5, d["Q"].shape[:2]))[..., None].astype(np.float32)
+    d["Q"][d["start"][0] + 5] = 0.0
+    t = np.arange(4000)
+    late = d["k"][d["pt"][0, t // 64], :, t % 64] * np.linspace(0.1, 6.0, 4000)[:, None, None]
+    d["k"][d["pt"][0, t // 64], :, t % 64] = synth.to_bf16_f32(late.astype(np.float32))
+    O, lse, err = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(d, O, lse)
+
+
+@pytest.mark.parametrize("bad,which,x", [(3010, "v", np.nan), (3001, "v", np.inf), (3039, "k", np.nan), (1234, "v", -np.inf)])
+def test_prompt_attn_split_unseen_keys_have_no_effect(bad, which, x):
+    """As above, with the items cut along their keys: in a part that some of the rows see, and in one that all see."""
+    n, c = 50, 3000
+    d = inputs(bad, 8, 2, 128, [n], [c], 16)
+    clean = dict(d, k=d["k"].copy(), v=d["v"].copy())
+    d[which][d["pt"][0, bad // 16], :, bad % 16, 3] = x
+    O, lse, err = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    below = np.arange(0, max(0, bad - c))
+    if len(below):
+        check(clean, O, lse, requests=[0], rows_of=lambda n: below)
+    o = host(O)[d["start"][0] + np.arange(max(0, bad - c), n)]
+    assert not np.isfinite(o[..., 3]).any()
+
+
+def test_prompt_attn_split_in_a_graph_and_with_bad_requests():
+    """A captured split call replayed on other inputs and lengths; a request out of bounds beside ones that are cut."""
+    a = inputs(21, 16, 4, 128, [30, 70], [3000, 1500], 64)
+    dev = {}
+    O, lse, err = call(a, dev=dev, max_rows=70, max_ctx=3000)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(a, O, lse)
+    need = e3.eagle3_prompt_workspace_bytes(2, a["total"], 70, 16, 4, 128, 3000, e3.E3_BF16)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    out = (torch.full((100, 16, 128), 55.0, dtype=torch.bfloat16, device="cuda"), torch.full((100, 16), 55.0, device="cuda"))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(a, dev=dev, ws=ws, out=out, err=err, max_rows=70, max_ctx=3000)
+    # the same pages cut elsewhere: 70 rows of the first request behind 2960 keys, 30 of the second behind 1540
+    rows = dict(a, rows=[70, 30], start=np.array([30, 0]), ctx=[2960, 1540])
+    for key in ("rows", "start", "ctx"):
+        dev[key].copy_(i32(rows[key]))
+    g.replay()
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(rows, *out)
+    dev["ctx"].copy_(i32([3001, 1540]))
+    out[0].fill_(55.0), out[1].fill_(55.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert int(err.item()) == e3.E3_DEV_ERR_CAPACITY
+    assert torch.all(out[0][30:] == 55.0) and torch.all(out[1][30:] == 55.0)
+    check(rows, *out, requests=[1])
+
+
+def test_prompt_attn_split_wait_that_runs_out():
+    d = inputs(23, 16, 4, 128, [40, 30], [3000, 200], 64)
+    dev = {}
+    call(d, dev=dev)
+    torch.cuda.synchronize()
+    _, _, err = call(d, dev=dev, flags=e3.E3_KV_SELFTEST_STALL)
+    torch.cuda.synchronize()
+    assert int(err.item()) == e3.E3_DEV_ERR_TIMEOUT
+    O, lse, err = call(d, dev=dev)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(d, O, lse)
+
+
+@pytest.mark.parametrize("H,KVH,hd,rows,ctx", [
+    (8, 8, 64, [1300], [0]), (16, 4, 128, [500, 620], [70, 0]), (160, 160, 32, [5], [9]), (40, 20, 96, [300], [10]), (80, 80, 160, [33, 70], [65, 0]),
+    (80, 80, 192, [70], [3]), (160, 160, 224, [17], [64]), (80, 80, 256, [70, 65], [0, 128])])
+def test_prompt_attn_fp32_enough_rows_for_every_sm(H, KVH, hd, rows, ctx):
+    """Tiles of 64 rows."""
+    d = inputs(H + hd, H, KVH, hd, rows, ctx, 16, "f32", gap=1)
+    O, lse, err = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(d, O, lse, rows_of=None if hd < 128 else lambda n: np.unique(np.concatenate([np.arange(0, n, 7), [n - 1]])))
+
+
+def test_prompt_attn_fp32_large_tiles_unseen_keys():
+    """A NaN in V behind a row's position, with tiles of 64 rows."""
+    n, c, bad = 700, 50, 330
+    d = inputs(77, 16, 16, 64, [n], [c], 16, "f32")
+    clean = dict(d, k=d["k"].copy(), v=d["v"].copy())
+    d["v"][d["pt"][0, bad // 16], :, bad % 16, 3] = np.nan
+    O, lse, err = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    below = np.arange(0, bad - c)
+    check(clean, O, lse, requests=[0], rows_of=lambda m: below)
+    assert not np.isfinite(host(O)[d["start"][0] + np.arange(bad - c, n)][..., 3]).any()
