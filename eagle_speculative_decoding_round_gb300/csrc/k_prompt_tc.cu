@@ -26,7 +26,7 @@
 // behind, and under a long load the power limit.  Measured on a GB300, 32 query and 8 KV heads of
 // 128: 32768 rows 5.54 ms, 1.59 PFLOP/s (82% of a library product's burst rate; 1.82 GHz under the
 // power cap); 16 prompts of 512 to 8192 rows 2.25 ms; 2048 rows 34 us; 4 pieces of 100 to 257 rows
-// behind 12288 to 16384 keys, 64 query heads, 286 us (306 without shares).  What the design gained, at 32768 rows: one
+// behind 12288 to 16384 keys, 64 query heads, 268 us (306 without shares).  What the design gained, at 32768 rows: one
 // issuing warp for both groups 8.60 ms, one for each 6.70; S of one tile in flight 6.37, steps of
 // 64 keys in two buffers 5.64; P stored piece by piece under the exponentials 5.54.
 #include <algorithm>
@@ -88,6 +88,12 @@ struct Item {
   // some row of the item does not see all of tile t's keys
   __device__ __forceinline__ bool masked(int t) const { return (t + 1) * kKeys > common; }
 };
+// Where a CTA's share begins, left for the kernel that joins the records: the item (request -1: no share), what of its cost
+// lies before, its cost, a share's.
+struct Border {
+  int b, tile, kvh;
+  long long in, cost, share;
+};
 // x / G for x < G + 256: the quotient is at least 1 / 2G off an integer, the product far less
 __device__ __forceinline__ int small_div(int x, float inv_g) { return static_cast<int>((static_cast<float>(x) + 0.5f) * inv_g); }
 
@@ -97,7 +103,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                  const __grid_constant__ e3_kv_layer kv, const __grid_constant__ PromptGeom g, int box, bool q_box, float sm_scale,
                  __nv_bfloat16* __restrict__ O, float* __restrict__ lse, float* __restrict__ ws_o, float2* __restrict__ ws_ml,
-                 int32_t* dev_err) {
+                 Border* __restrict__ ws_border, int32_t* dev_err) {
   using C = TcCfg<HD>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -308,26 +314,36 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
     bool live = true;
     const PromptReq own = prompt_req(g, lane);
     Item it, next;
-    long long cost_at = 0, cost_end = 0;  // the CTA's share
+    long long cost_at = 0, cost_end = 0;  // the CTA's share, behind so many whole items
+    uint32_t waves = 0;
+    PromptPlace place;  // where the share's next part begins
     if (g.split) {
       const PromptShares s = prompt_shares(g, own, gridDim.x);
-      cost_at = blockIdx.x * s.share;
+      waves = s.waves;
+      cost_at = s.from + blockIdx.x * s.share;
       cost_end = min(s.total, cost_at + s.share);
+      Border at{-1, 0, 0, 0, 0, s.share};
+      if (cost_at < cost_end) {
+        place = prompt_place(g, own, cost_at);
+        at = Border{place.it.b, place.it.tile, place.it.kvh, place.in, place.cost, s.share};
+      }
+      if (lane == 0) ws_border[blockIdx.x] = at;
     }
     // finds item k and tells the others
     auto publish = [&](uint32_t k) {
       PromptItem at;
-      PromptPlace place;
       bool cut = false;
       next.b = -1;
       if (!g.split) {
         const long long row = static_cast<long long>(k) * gridDim.x;
         at = find_prompt_item(g, own, row + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
+      } else if (k < waves) {
+        long long before;
+        at = numbered_item(g, own, static_cast<long long>(k) * gridDim.x + blockIdx.x, &before);
       } else {
         // the next part of the CTA's share that has a tile of keys
         at.b = g.B;
-        while (cost_at < cost_end) {
-          place = prompt_place(g, own, cost_at);
+        while (at.b == g.B && cost_at < cost_end) {
           const int last = min((place.it.tile + 1) << g.shift, place.q.n * g.G) - 1;
           const int nt = (place.q.c + last / g.G + kKeys) / kKeys;
           next.t0 = cut_tile(place.in, place.cost, nt);
@@ -336,12 +352,12 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
           if (next.t1 > next.t0) {
             at = place.it;
             cut = next.t1 - next.t0 < nt;
-            break;
           }
+          if (cost_at < cost_end) place = prompt_place(g, own, cost_at);
         }
       }
       if (at.b < g.B) {
-        const PromptReq q = g.split ? place.q : prompt_req(g, at.b);
+        const PromptReq q = prompt_req(g, at.b);
         const int f0 = at.tile * 2 * kRows;
         next.b = at.b;
         next.kvh = at.kvh;
@@ -353,12 +369,12 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         next.common = q.c + next.row + 1;
         next.keys0 = q.c + (f0 + min(kRows, next.flat) - 1) / g.G + 1;
         next.keys1 = kRows < next.flat ? q.c + (f0 + min(2 * kRows, next.flat) - 1) / g.G + 1 : 0;
-        if (!g.split) {
+        if (!g.split || k < waves) {
           next.t0 = 0;
           next.t1 = (next.all_keys() + kKeys - 1) / kKeys;
         }
         // (a CTA's share begins within one item at most, and ends within one)
-        next.rec = !cut ? -1 : 2 * blockIdx.x + (next.t0 > 0 ? 0 : 1);
+        next.rec = !cut ? -1 : 2 * static_cast<int>(blockIdx.x) + (next.t0 > 0 ? 0 : 1);
       }
       if (!warp_wait(&item_empty[k & 1], ((k >> 1) & 1) ^ 1, abort)) return false;
       if (lane == 0) {
@@ -652,89 +668,93 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
-// The items that borders between shares cut: their parts' records, joined in the order of the keys.  A CTA takes 32 rows
-// of the item that border w lies in, where that is the item's first border.
-constexpr int kMergeRows = 32;
+// The items that borders between shares cut: their parts' records, joined in the order of the keys.  Border w's CTAs take
+// the item that it lies in, where that is the item's first border: every kMergeCtas-th 32 of its rows, a row to a lane.  What
+// the parts are is worked out once a CTA, so that the records' loads wait for nothing but one another's batch (by itself,
+// where every border cuts an item: 25 us with the parts found in the loop, 13 so).
+constexpr int kMergeCtas = 4, kMergeWarps = 16;
 
 template <int HD>
-__global__ void __launch_bounds__(256)
-prompt_merge_kernel(const __grid_constant__ PromptGeom g, int workers, const float* __restrict__ ws_o,
+__global__ void __launch_bounds__(kMergeWarps * 32, 2)
+prompt_merge_kernel(const __grid_constant__ PromptGeom g, const Border* __restrict__ ws_border, const float* __restrict__ ws_o,
                     const float2* __restrict__ ws_ml, __nv_bfloat16* __restrict__ O, float* __restrict__ lse) {
-  constexpr int CHUNKS = 2 * kRows / kMergeRows, NQ = HD / 32, AHEAD = 4;  // NQ: quads of dims of a thread
+  constexpr int NQ = HD / 4 / kMergeWarps, AHEAD = 4;  // NQ: quads of dims of a thread
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int w = 1 + blockIdx.x / CHUNKS, chunk = blockIdx.x % CHUNKS;
-  const PromptReq own = prompt_req(g, lane);
-  const PromptShares s = prompt_shares(g, own, workers);
-  const long long border = w * s.share;
-  if (border >= s.total) return;
-  const PromptPlace p = prompt_place(g, own, border);
-  if (p.in == 0 || p.in > s.share) return;
-  const PromptReq q = p.q;
-  const int f0 = p.it.tile << g.shift, flat = q.n * g.G, r = chunk * kMergeRows + lane, f = f0 + r;
-  if (f0 + chunk * kMergeRows >= flat) return;
-  const bool ok = f < flat;
-  const int row = (ok ? f : flat - 1) / g.G, head = (ok ? f : flat - 1) - row * g.G, see = q.c + row + 1;
+  const int w = 1 + blockIdx.x / kMergeCtas;
+  const Border p = ws_border[w];
+  if (p.b < 0 || p.in == 0 || p.in > p.share) return;
+  const PromptReq q = prompt_req(g, p.b);
+  const int f0 = p.tile << g.shift, flat = q.n * g.G;
   const int nt = (q.c + (min(f0 + 2 * kRows, flat) - 1) / g.G + kKeys) / kKeys;
   // part j is CTA w - 1 + j's: of the item's cost, what lies before the border, then a share each
-  const int parts = static_cast<int>((p.cost - p.in + s.share - 1) / s.share) + 1;
-  float M = -INFINITY, den = 0.0f, acc[4 * NQ];
-#pragma unroll
-  for (int i = 0; i < 4 * NQ; ++i) acc[i] = 0.0f;
-  for (int j0 = 0; j0 < parts; j0 += AHEAD) {
-    float2 y[AHEAD];
-    float4 x[AHEAD][NQ];
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) {
-      const int j = j0 + u;
-      y[u] = make_float2(-INFINITY, 0.0f);
-      if (j >= parts) continue;
-      const int t0 = j == 0 ? 0 : cut_tile(p.in + (j - 1) * s.share, p.cost, nt), t1 = cut_tile(p.in + j * s.share, p.cost, nt);
-      if (t0 == 0 && t1 == nt) return;  // (one CTA has all of its tiles: O is written)
-      if (t1 <= t0 || see <= t0 * kKeys) continue;
-      const size_t rec = 2 * static_cast<size_t>(w - 1 + j) + (t0 > 0 ? 0 : 1);
-      y[u] = ws_ml[rec * (2 * kRows) + r];
-      const float4* from = reinterpret_cast<const float4*>(ws_o) + rec * (HD / 4 * 2 * kRows) + r;
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) x[u][i] = from[(warp + 8 * i) * (2 * kRows)];
-    }
-    float top = M;
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u) top = fmaxf(top, y[u].x);
-    if (top > M) {
-      const float c = ex2(M - top);
-      M = top;
-      den *= c;
-#pragma unroll
-      for (int i = 0; i < 4 * NQ; ++i) acc[i] *= c;
-    }
-#pragma unroll
-    for (int u = 0; u < AHEAD; ++u)
-      if (y[u].y != 0.0f) {  // (a part that the row sees has a sum of 1 at least, or NaN)
-        const float c = ex2(y[u].x - M);
-        den = fmaf(y[u].y, c, den);
-#pragma unroll
-        for (int i = 0; i < NQ; ++i) {
-          acc[4 * i] = fmaf(x[u][i].x, c, acc[4 * i]), acc[4 * i + 1] = fmaf(x[u][i].y, c, acc[4 * i + 1]);
-          acc[4 * i + 2] = fmaf(x[u][i].z, c, acc[4 * i + 2]), acc[4 * i + 3] = fmaf(x[u][i].w, c, acc[4 * i + 3]);
-        }
-      }
+  const int parts = static_cast<int>((p.cost - p.in + p.share - 1) / p.share) + 1;
+  extern __shared__ int2 s_part[];  // record, first key (beyond all keys: the part has none)
+  bool whole = false;
+  for (int j = threadIdx.x; j < parts; j += kMergeWarps * 32) {
+    const int t0 = j == 0 ? 0 : cut_tile(p.in + (j - 1) * p.share, p.cost, nt), t1 = cut_tile(p.in + j * p.share, p.cost, nt);
+    s_part[j] = make_int2(2 * (w - 1 + j) + (t0 > 0 ? 0 : 1), t1 > t0 ? t0 * kKeys : 0x7FFFFFFF);
+    whole |= t0 == 0 && t1 == nt;
   }
-  if (!ok) return;
-  const size_t at = (static_cast<size_t>(q.start) + row) * g.H + p.it.kvh * g.G + head;
-  const float inv = 1.0f / den;
+  if (__syncthreads_or(whole)) return;  // (one CTA had all of its tiles: O is written)
+#pragma unroll 1
+  for (int r = (blockIdx.x % kMergeCtas) * 32 + lane; r - lane < min(2 * kRows, flat - f0); r += 32 * kMergeCtas) {
+    const bool ok = f0 + r < flat;
+    const int f = ok ? f0 + r : flat - 1, row = f / g.G, head = f - row * g.G, see = q.c + row + 1;
+    float M = -INFINITY, den = 0.0f, acc[4 * NQ];
 #pragma unroll
-  for (int i = 0; i < NQ; ++i)
-    reinterpret_cast<uint2*>(O + at * HD)[warp + 8 * i] =
-        make_uint2(pack2_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack2_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
-  if (warp == 0) lse[at] = (M + log2f(den)) * kLn2;
+    for (int i = 0; i < 4 * NQ; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < parts; j0 += AHEAD) {
+      // (loads of parts that the row does not see stay in the records, and are not used)
+      float2 y[AHEAD];
+      float4 x[AHEAD][NQ];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int2 part = s_part[min(j0 + u, parts - 1)];
+        y[u] = ws_ml[static_cast<size_t>(part.x) * (2 * kRows) + r];
+        const float4* from = reinterpret_cast<const float4*>(ws_o) + static_cast<size_t>(part.x) * (HD / 4 * 2 * kRows) + r;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) x[u][i] = from[(warp + kMergeWarps * i) * (2 * kRows)];
+        if (j0 + u >= parts || see <= part.y) y[u] = make_float2(-INFINITY, 0.0f);
+      }
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) top = fmaxf(top, y[u].x);
+      if (top > M) {
+        const float c = ex2(M - top);
+        M = top;
+        den *= c;
+#pragma unroll
+        for (int i = 0; i < 4 * NQ; ++i) acc[i] *= c;
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u)
+        if (y[u].y != 0.0f) {  // (a part that the row sees has a sum of 1 at least, or NaN)
+          const float c = ex2(y[u].x - M);
+          den = fmaf(y[u].y, c, den);
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) {
+            acc[4 * i] = fmaf(x[u][i].x, c, acc[4 * i]), acc[4 * i + 1] = fmaf(x[u][i].y, c, acc[4 * i + 1]);
+            acc[4 * i + 2] = fmaf(x[u][i].z, c, acc[4 * i + 2]), acc[4 * i + 3] = fmaf(x[u][i].w, c, acc[4 * i + 3]);
+          }
+        }
+    }
+    if (!ok) break;
+    const size_t at = (static_cast<size_t>(q.start) + row) * g.H + p.kvh * g.G + head;
+    const float inv = 1.0f / den;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+      reinterpret_cast<uint2*>(O + at * HD)[warp + kMergeWarps * i] =
+          make_uint2(pack2_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv), pack2_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
+    if (warp == 0) lse[at] = (M + log2f(den)) * kLn2;
+  }
 }
 
 // Whether the call is cut into equal shares: where that saves more tiles of keys (some 1.2 us each) than the records and
 // the second kernel cost: 8, and 12 more where items have all of their rows.  By the call's bounds.  Measured, whole items and
-// equal shares, 32 query and 8 KV heads of 128: 16 rows behind 30000 keys 266 and 45 us, 8 requests of 64 rows behind 8192 keys
-// 101 and 72, 4 of 1 row behind 2048 keys 26.4 and 24.0; where whole items stay: 4 of 1 row behind 1024 keys 17.7 and 21.4, 512
+// equal shares, 32 query and 8 KV heads of 128: 16 rows behind 30000 keys 266 and 44 us, 8 requests of 64 rows behind 8192 keys
+// 101 and 69, 4 of 1 row behind 2048 keys 26.4 and 21.0; where whole items stay: 4 of 1 row behind 1024 keys 17.7 and 21.4, 512
 // rows behind 2048 keys 37.1 and 42.2, 1000 rows 20.7 and 37.1.
 bool prompt_splits(const PromptGeom& g, int max_kv_len) {
   const long long items = prompt_items_bound(g), sms = num_sms();
@@ -749,7 +769,7 @@ size_t record_rows() { return static_cast<size_t>(2) * num_sms() * 2 * kRows; }
 template <int HD>
 cudaError_t launch_tc(const void* Q, const CUtensorMap& mq, bool q_box, const CUtensorMap& mk, const CUtensorMap& mv,
                       const e3_kv_layer& kv, const PromptGeom& g, int box, float sm_scale, void* O, float* lse, int32_t* dev_err,
-                      float* ws_o, float2* ws_ml, cudaStream_t s) {
+                      float* ws_o, float2* ws_ml, Border* ws_border, cudaStream_t s) {
   static OncePerDevice<cudaError_t> attrs;
   const cudaError_t e = once_per_device(attrs, [] {
     return cudaFuncSetAttribute(prompt_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<HD>::SMEM);
@@ -758,9 +778,9 @@ cudaError_t launch_tc(const void* Q, const CUtensorMap& mq, bool q_box, const CU
   const int workers = g.split ? num_sms() : static_cast<int>(std::min<long long>(prompt_items_bound(g), num_sms()));
   const cudaError_t el =
       launch_pdl(prompt_tc_kernel<HD>, dim3(workers), dim3(kThreads), TcCfg<HD>::SMEM, s, 1, static_cast<const __nv_bfloat16*>(Q), mq, mk,
-                 mv, kv, g, box, q_box, sm_scale, static_cast<__nv_bfloat16*>(O), lse, ws_o, ws_ml, dev_err);
+                 mv, kv, g, box, q_box, sm_scale, static_cast<__nv_bfloat16*>(O), lse, ws_o, ws_ml, ws_border, dev_err);
   if (el != cudaSuccess || !g.split) return el;
-  return launch_pdl(prompt_merge_kernel<HD>, dim3((workers - 1) * (2 * kRows / kMergeRows)), dim3(256), 0, s, 1, g, workers, ws_o, ws_ml,
+  return launch_pdl(prompt_merge_kernel<HD>, dim3((workers - 1) * kMergeCtas), dim3(kMergeWarps * 32), workers * sizeof(int2), s, 1, g, ws_border, ws_o, ws_ml,
                     static_cast<__nv_bfloat16*>(O), lse);
 }
 
@@ -768,7 +788,7 @@ cudaError_t launch_tc(const void* Q, const CUtensorMap& mq, bool q_box, const CU
 
 size_t prompt_tc_workspace_bytes(PromptGeom g, int hd, int max_kv_len) {
   g.shift = kShift;
-  return prompt_splits(g, max_kv_len) ? record_rows() * (hd * sizeof(float) + sizeof(float2)) : 0;
+  return prompt_splits(g, max_kv_len) ? record_rows() * (hd * sizeof(float) + sizeof(float2)) + num_sms() * sizeof(Border) : 0;
 }
 
 e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, int max_kv_len, float sm_scale, void* O, float* lse,
@@ -777,6 +797,7 @@ e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, i
   g.split = prompt_splits(g, max_kv_len);
   float* ws_o = static_cast<float*>(ws);
   float2* ws_ml = g.split ? reinterpret_cast<float2*>(ws_o + record_rows() * kv.head_dim) : nullptr;
+  Border* ws_border = g.split ? reinterpret_cast<Border*>(ws_ml + record_rows()) : nullptr;
   int box = 16;  // keys of a TMA box: what divides a page, as far as a tile has
   while (box < kKeys && kv.page_size % (2 * box) == 0) box *= 2;
   const unsigned long long rows = static_cast<unsigned long long>(kv.n_pages) * kv.n_kv_heads * kv.page_size;
@@ -797,8 +818,8 @@ e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, i
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     E3_REQUIRE(r == CUDA_SUCCESS, E3_ERR_INVALID_ARG, "prompt_attn: cuTensorMapEncodeTiled rejected Q (%d)", static_cast<int>(r));
   }
-  const cudaError_t e = kv.head_dim == 128 ? launch_tc<128>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, ws_o, ws_ml, s)
-                                           : launch_tc<64>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, ws_o, ws_ml, s);
+  const cudaError_t e = kv.head_dim == 128 ? launch_tc<128>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, ws_o, ws_ml, ws_border, s)
+                              : launch_tc<64>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, ws_o, ws_ml, ws_border, s);
   return e == cudaSuccess ? E3_OK : cuda_status(e, "prompt_tc kernels");
 }
 
