@@ -54,8 +54,9 @@ prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_la
     for (int b = threadIdx.x; b < g.B; b += 256)
       if (!prompt_req(g, b).ok) dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
   const PromptReq own = prompt_req(g, threadIdx.x & 31);
+  PromptSeen seen{0, 0};
   for (long long rank = blockIdx.x;; rank += gridDim.x) {
-    const PromptItem it = find_prompt_item(g, own, rank);
+    const PromptItem it = g.B <= 32 ? find_prompt_item(g, own, rank) : next_prompt_item(g, rank, seen);
     if (it.b >= g.B) break;
     const PromptReq q = prompt_req(g, it.b);
     const int f0 = it.tile * C::TILE, rows = min(C::TILE, q.n * g.G - f0);

@@ -316,6 +316,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
     Item it, next;
     long long cost_at = 0, cost_end = 0;  // the CTA's share, behind so many whole items
     uint32_t waves = 0;
+    PromptSeen seen{0, 0};
     PromptPlace place;  // where the share's next part begins
     if (g.split) {
       const PromptShares s = prompt_shares(g, own, gridDim.x);
@@ -336,7 +337,8 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       next.b = -1;
       if (!g.split) {
         const long long row = static_cast<long long>(k) * gridDim.x;
-        at = find_prompt_item(g, own, row + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x));
+        const long long rank = row + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        at = g.B <= 32 ? find_prompt_item(g, own, rank) : next_prompt_item(g, rank, seen);
       } else if (k < waves) {
         long long before;
         at = numbered_item(g, own, static_cast<long long>(k) * gridDim.x + blockIdx.x, &before);

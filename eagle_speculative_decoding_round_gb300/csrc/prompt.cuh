@@ -51,25 +51,17 @@ __device__ __forceinline__ int prompt_tiles(const PromptGeom& g, const PromptReq
 // (16 prompts of 512 .. 8192 rows, items ordered by their keys over all requests: 2.43 ms).
 // Item `rank` (every lane of a warp calls and gets the same answer; b = B: there is none): with
 // it the request is found by bisection over the numbers of keys, no list is kept.  `own` is the
-// request of the lane's number, read once by the caller.
+// request of the lane's number, read once by the caller; there are 32 at most.
 struct PromptItem {
   int b, tile, kvh;
 };
 __device__ __forceinline__ PromptItem find_prompt_item(const PromptGeom& g, const PromptReq& own, long long rank) {
-  const int lane = threadIdx.x & 31;
+  const int tiles = prompt_tiles(g, own), most = own.c + own.n;
   const long long at = rank / g.KVH;  // among the tiles of one KV head
-  PromptItem it;
-  it.kvh = static_cast<int>(rank - at * g.KVH);
+  PromptItem it{g.B, 0, static_cast<int>(rank - at * g.KVH)};
   auto before = [&](int keys) {  // tiles of the requests with more keys
-    long long total = 0;
-    for (int b0 = 0; b0 < g.B; b0 += 32) {
-      const PromptReq q = b0 == 0 ? own : prompt_req(g, b0 + lane);
-      total += __reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(q.c + q.n > keys ? prompt_tiles(g, q) : 0));
-    }
-    return total;
+    return static_cast<long long>(__reduce_add_sync(0xFFFFFFFFu, static_cast<unsigned>(most > keys ? tiles : 0)));
   };
-  it.b = g.B;
-  it.tile = 0;
   if (at >= before(0)) return it;
   int lo = 0, hi = g.max_kv_len + g.max_rows;  // before(lo) > at >= before(hi)
   long long first = 0;
@@ -82,24 +74,44 @@ __device__ __forceinline__ PromptItem find_prompt_item(const PromptGeom& g, cons
       hi = mid, first = n;
   }
   // the requests with exactly hi keys, one by one
-  long long left = at - first;
-  for (int b0 = 0; b0 < g.B; b0 += 32) {
-    const PromptReq q = b0 == 0 ? own : prompt_req(g, b0 + lane);
-    const int u = q.c + q.n == hi ? prompt_tiles(g, q) : 0;
-    unsigned incl = static_cast<unsigned>(u);
+  const int left = static_cast<int>(at - first), lane = threadIdx.x & 31;
+  unsigned incl = static_cast<unsigned>(most == hi ? tiles : 0);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  it.b = __ffs(__ballot_sync(0xFFFFFFFFu, static_cast<int>(incl) > left)) - 1;
+  it.tile = __shfl_sync(0xFFFFFFFFu, static_cast<int>(incl) - 1 - left, it.b);
+  return it;
+}
+// The same for calls of more requests than a warp has lanes, which are taken as they come: a search by keys would read all of
+// them again for each bit of a length (2000 requests of one row 3.85 ms, so 0.43; 64 of 100 to 900 rows 256 us, so 215).
+// `rank` grows from call to call, and `seen` goes with it.
+struct PromptSeen {
+  int b0;          // the requests from here on have not been passed
+  long long tiles;  // of one KV head, of those before
+};
+__device__ __forceinline__ PromptItem next_prompt_item(const PromptGeom& g, long long rank, PromptSeen& seen) {
+  const int lane = threadIdx.x & 31;
+  const long long at = rank / g.KVH;
+  PromptItem it{g.B, 0, static_cast<int>(rank - at * g.KVH)};
+  for (; seen.b0 < g.B; seen.b0 += 32) {
+    const int tiles = prompt_tiles(g, prompt_req(g, seen.b0 + lane));
+    int incl = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += y;
     }
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, static_cast<long long>(incl) > left);
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, seen.tiles + incl > at);
     if (hit) {
       const int k = __ffs(hit) - 1;
-      it.b = b0 + k;
-      it.tile = __shfl_sync(0xFFFFFFFFu, static_cast<int>(incl) - 1 - static_cast<int>(left), k);
-      return it;
+      it.b = seen.b0 + k;
+      it.tile = static_cast<int>(seen.tiles + __shfl_sync(0xFFFFFFFFu, incl, k) - 1 - at);
+      break;
     }
-    left -= __shfl_sync(0xFFFFFFFFu, incl, 31);
+    seen.tiles += __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
   return it;
 }
