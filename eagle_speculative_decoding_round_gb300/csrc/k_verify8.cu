@@ -407,26 +407,60 @@ verify8_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
       const float node_f = pow2n(-unit);
       const float c2 = sm_scale * kLog2e;
       const int words = (g.R + 63) >> 6;
+      // rows of the tail: lane i < 16 holds that of node i of the granule, looked up a granule ahead
+      auto rows_at = [&](int j) -> long long { return lane < kGran ? tail_row(j + lane) : -1; };
+      // what the thread's rows see of a granule (which lies within one mask word)
+      uint32_t bits[NR][2];
+      auto bits_at = [&](int j) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = rg * ROWS + 8 * nr + 2 * tq + e;
+            bits[nr][e] = r < rows && j < g.R
+                              ? static_cast<uint32_t>(mask[(static_cast<size_t>(b) * g.R + r / g.G) * words + (j >> 6)] >> (j & 63)) &
+                                    ((1u << min(kGran, g.R - j)) - 1u)
+                              : 0u;
+          }
+      };
+      const int j_first = (max(x0, NG) - NG) * kGran;
+      long long at = rows_at(j_first);
+      bits_at(j_first);
 #pragma unroll 1
-      for (int j0 = (max(x0, NG) - NG) * kGran; j0 < (x1 - NG) * kGran; j0 += kGran) {
-        // (V is loaded after the scores: both at once would cost the main loop its registers)
+      for (int j0 = j_first; j0 < (x1 - NG) * kGran; j0 += kGran) {
+        // A tree's rows see few of its nodes: granules that no row of the tile sees are passed over (31 trees of 197 nodes, 6
+        // query and 2 KV heads of 64, short prefixes: 94.5 us, so 76.2).  Where there is one granule, K need not wait for the masks.
+        bool any = false;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) any |= (bits[nr][0] | bits[nr][1]) != 0u;
+        if (g.R > kGran && !__any_sync(0xFFFFFFFFu, any)) {
+          at = rows_at(j0 + kGran);
+          bits_at(j0 + kGran);
+          continue;
+        }
         uint2 kr[2][KS];
         uint32_t raw[4][DV / 2];  // V of keys (tile 0: two, tile 1: two), DV dims each
-        uint64_t bits[NR][2];
+        auto load_v = [&] {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const long long row = __shfl_sync(0xFFFFFFFFu, at, key_of(i >> 1, 2 * tq + (i & 1)));
+            const uint2* vp = reinterpret_cast<const uint2*>(tv + max(row, 0ll) * HD + DV * gq);
+#pragma unroll
+            for (int d = 0; d < DV / 4; ++d) {
+              const uint2 x = row >= 0 ? vp[d] : make_uint2(0u, 0u);
+              raw[i][2 * d] = x.x;
+              raw[i][2 * d + 1] = x.y;
+            }
+          }
+        };
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const long long row = tail_row(j0 + key_of(t, gq));
+          const long long row = __shfl_sync(0xFFFFFFFFu, at, key_of(t, gq));
           const uint2* kp = reinterpret_cast<const uint2*>(tk + max(row, 0ll) * HD + DK * tq);
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) kr[t][ks] = row >= 0 ? kp[ks] : make_uint2(0u, 0u);
         }
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {  // (a granule lies within one mask word)
-            const int r = rg * ROWS + 8 * nr + 2 * tq + e;
-            bits[nr][e] = r < rows ? mask[(static_cast<size_t>(b) * g.R + r / g.G) * words + (j0 >> 6)] >> (j0 & 63) : 0ull;
-          }
+        if (HD == 64) load_v();  // (heads of 128 wait for the scores: both at once would cost the main loop its registers)
         float sc[1][NR][4];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
@@ -439,22 +473,13 @@ verify8_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int j = key_of(e >> 1, gq);
-            const bool see = j0 + j < g.R && ((bits[nr][e & 1] >> j) & 1ull);
+            const bool see = (bits[nr][e & 1] >> j) & 1u;
             sc[0][nr][e] = see ? sc[0][nr][e] * c2 : -INFINITY;
           }
         }
         softmax(sc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const long long row = tail_row(j0 + key_of(i >> 1, 2 * tq + (i & 1)));
-          const uint2* vp = reinterpret_cast<const uint2*>(tv + max(row, 0ll) * HD + DV * gq);
-#pragma unroll
-          for (int d = 0; d < DV / 4; ++d) {
-            const uint2 x = row >= 0 ? vp[d] : make_uint2(0u, 0u);
-            raw[i][2 * d] = x.x;
-            raw[i][2 * d + 1] = x.y;
-          }
-        }
+        if (HD != 64) load_v();
+        at = rows_at(j0 + kGran);
         uint32_t badk = 0u;  // keys of the granule with a non-finite V, as bits
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -476,8 +501,9 @@ verify8_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
 #pragma unroll
           for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) poison[nr][e] |= (bits[nr][e] & badk) != 0ull;
+            for (int e = 0; e < 2; ++e) poison[nr][e] |= (bits[nr][e] & badk) != 0u;
         }
+        bits_at(j0 + kGran);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
           // a weight in two bf16 parts (2^-16 of it is left out): one part alone would be the
