@@ -8,7 +8,7 @@ static bool prompt_sizes_ok(int B, int n_total, int max_rows, int n_q_heads, int
                             e3_dtype dt) {
   return B >= 1 && B <= 65535 && n_total >= 1 && max_rows >= 1 && n_q_heads >= 1 && n_q_heads <= 65535 && n_kv_heads >= 1 &&
          n_q_heads % n_kv_heads == 0 && static_cast<long long>(n_total) * n_q_heads < (1ll << 31) && max_kv_len >= 0 &&
-         static_cast<long long>(max_kv_len) + max_rows <= (1ll << 30) &&
+         static_cast<long long>(max_kv_len) + max_rows <= (dt == E3_BF16 ? 1ll << 25 : 1ll << 30) &&
          static_cast<long long>(max_rows) * (n_q_heads / n_kv_heads) < (1ll << 31) - 1024 &&
          (dt == E3_BF16 ? head_dim == 64 || head_dim == 128
                         : dt == E3_F32 && head_dim >= 32 && head_dim <= 256 && head_dim % 32 == 0);

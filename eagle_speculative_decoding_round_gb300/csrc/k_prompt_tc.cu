@@ -820,8 +820,8 @@ e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, i
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     E3_REQUIRE(r == CUDA_SUCCESS, E3_ERR_INVALID_ARG, "prompt_attn: cuTensorMapEncodeTiled rejected Q (%d)", static_cast<int>(r));
   }
-  const cudaError_t e = kv.head_dim == 128 ? launch_tc<128>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, ws_o, ws_ml, ws_border, s)
-                              : launch_tc<64>(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, ws_o, ws_ml, ws_border, s);
+  const auto launch = kv.head_dim == 128 ? launch_tc<128> : launch_tc<64>;
+  const cudaError_t e = launch(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, ws_o, ws_ml, ws_border, s);
   return e == cudaSuccess ? E3_OK : cuda_status(e, "prompt_tc kernels");
 }
 

@@ -441,3 +441,43 @@ def test_prompt_attn_fp32_large_tiles_unseen_keys():
     below = np.arange(0, bad - c)
     check(clean, O, lse, requests=[0], rows_of=lambda m: below)
     assert not np.isfinite(host(O)[d["start"][0] + np.arange(bad - c, n)][..., 3]).any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_prompt_attn_thousands_of_requests(dt):
+    """Short requests, many of them empty, far more than CTAs."""
+    rng = np.random.default_rng(9)
+    rows = [int(x) for x in rng.integers(0, 4, 3000)]
+    ctx = [int(x) for x in np.where(rng.random(3000) < 0.8, 0, rng.integers(1, 40, 3000))]
+    rows[1711] = 300
+    d = inputs(9, 2, 1, 64, rows, ctx, 16, dt, gap=1)
+    O, lse, err = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(d, O, lse)
+
+
+def test_prompt_attn_split_on_two_streams_over_shared_pages():
+    """Two split calls at once, each with scratch of its own; requests whose tables name the same pages."""
+    a = inputs(31, 16, 4, 128, [20, 20], [3000, 3000], 64)
+    k, v = a["k"], a["v"]
+    for x in (k, v):  # both requests' contexts are the first one's pages; their own rows stay apart
+        last = x[a["pt"][1, 3000 // 64]].copy()
+        last[:, :3000 % 64] = x[a["pt"][0, 3000 // 64], :, :3000 % 64]
+        x[a["pt"][1, 3000 // 64]] = last
+    a["pt"][1, :3000 // 64] = a["pt"][0, :3000 // 64]
+    dev = {}
+    call(a, dev=dev)
+    torch.cuda.synchronize()
+    outs, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                outs.append(call(a, dev=dev, stream=s))
+    torch.cuda.synchronize()
+    for O, lse, err in outs:
+        assert int(err.item()) == 0
+        assert torch.equal(O, outs[0][0]) and torch.equal(lse, outs[0][1])
+    check(a, *outs[0][:2])

@@ -24,6 +24,7 @@ def test_prompt_refusals(e3):  # noqa: F811
     refused(e3, 2, call, P=-1)
     refused(e3, 2, call, P=1 << 30)
     refused(e3, 2, call, most=1 << 30, P=1)
+    refused(e3, 2, call, P=(1 << 25) - 63)              # bf16: 2^25 keys
     refused(e3, 2, call, H=30)                          # not a multiple of the KV heads
     refused(e3, 2, call, H=0)
     refused(e3, 2, call, kv=kv16(e3, hd=96))            # bf16 heads of 96
