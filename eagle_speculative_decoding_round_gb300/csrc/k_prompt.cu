@@ -12,7 +12,7 @@
 // cores would round the operands to tf32.
 //
 // Bound: FMAs, and for small prompts the latency of a tile's chain (loads, S, softmax, O).
-// Measured on a GB300: 3 prompts of 15 to 131 rows behind up to 128 keys, 4 heads of 64: 21.2 us
+// Measured on a GB300: 3 prompts of 15 to 131 rows behind up to 128 keys, 4 heads of 64: 18 us
 // (tiles of 64 rows only, K and V in one buffer: 39); 1000 rows, 32 query heads of 128: 259 us, 32
 // TFLOP/s.
 #include <type_traits>

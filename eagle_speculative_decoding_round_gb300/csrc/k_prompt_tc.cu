@@ -25,10 +25,11 @@
 // Bound: the tensor cores, with the exponentials (one a product's 2 * 64 multiply-adds) close
 // behind, and under a long load the power limit.  Measured on a GB300, 32 query and 8 KV heads of
 // 128: 32768 rows 5.54 ms, 1.59 PFLOP/s (82% of a library product's burst rate; 1.82 GHz under the
-// power cap); 16 prompts of 512 to 8192 rows 2.25 ms; 2048 rows 34 us; 4 pieces of 100 to 257 rows
-// behind 12288 to 16384 keys, 64 query heads, 268 us (306 without shares).  What the design gained, at 32768 rows: one
-// issuing warp for both groups 8.60 ms, one for each 6.70; S of one tile in flight 6.37, steps of
-// 64 keys in two buffers 5.64; P stored piece by piece under the exponentials 5.54.
+// power cap); 16 prompts of 512 to 8192 rows 2.25 ms; 2048 rows 33 us; 4 pieces of 100 to 257 rows
+// behind 12288 to 16384 keys, 64 query heads, 262 to 277 us (306 without shares).  What the design
+// gained, at 32768 rows: one issuing warp for both groups 8.60 ms, one for each 6.70; S of one tile in
+// flight 6.37, steps of 64 keys in two buffers 5.64; P stored piece by piece under the exponentials
+// 5.54.
 #include <algorithm>
 
 #include "e3_common.cuh"
