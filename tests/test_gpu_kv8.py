@@ -464,3 +464,29 @@ def test_verify_attn8_wait_that_runs_out(R, H):
     torch.cuda.synchronize()
     assert int(err.item()) == 0
     attn_check(d, O, lse)
+
+
+@pytest.mark.parametrize("R,H,KVH,hd", [(40, 4, 4, 64), (100, 6, 2, 64), (197, 6, 2, 64), (31, 8, 8, 128), (256, 2, 1, 64)])
+def test_verify_attn8_granules_of_nodes_that_no_row_sees(R, H, KVH, hd):
+    """Few rows per tile and many nodes: deep and shallow trees, tiles whose rows see no node at all (beside a prefix and
+    without one), a NaN in V of a node that one row sees."""
+    d = attn_inputs(R + hd, 3, R, H, KVH, hd, [0, 130, 517], 64, 16)
+    d["see"][0, 16:32] = False             # no key at all
+    d["see"][1, :] = np.eye(R, dtype=bool)  # each node itself alone
+    d["see"][2, R // 2:] = False            # the prefix alone
+    d["see"][2, R - 1, R - 1] = True
+    O, lse, err = attn_call(d)
+    O2, lse2, _ = attn_call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    attn_check(d, O, lse)
+    bad = R - 1
+    d["tail"][1][d["tpt"][2, bad // 64], :, bad % 64, 5] = np.nan
+    O3, lse3, _ = attn_call(d)
+    torch.cuda.synchronize()
+    assert torch.isnan(O3[2, bad]).all() and torch.equal(lse3, lse)
+    keep = torch.ones((3, R), dtype=torch.bool, device="cuda")
+    keep[2, bad] = False
+    if not d["see"][2, :bad, bad].any():
+        assert torch.equal(O3[keep], O[keep])

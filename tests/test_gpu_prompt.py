@@ -481,3 +481,12 @@ def test_prompt_attn_split_on_two_streams_over_shared_pages():
         assert int(err.item()) == 0
         assert torch.equal(O, outs[0][0]) and torch.equal(lse, outs[0][1])
     check(a, *outs[0][:2])
+
+
+@pytest.mark.parametrize("ctx,dt", [([0, 3], "bf16"), ([5000, 0], "bf16"), ([9, 0], "f32")])
+def test_prompt_attn_without_rows(ctx, dt):
+    """Every request empty: nothing is written, nothing is flagged."""
+    d = inputs(1, 8, 2, 64, [0, 0], ctx, 16, dt)
+    O, lse, err = call(d, max_rows=30)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.all(O == 55.0) and torch.all(lse == 55.0)
