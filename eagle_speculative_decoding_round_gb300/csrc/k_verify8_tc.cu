@@ -505,7 +505,7 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
         // Factors of the scores.  The nodes' meets a score between the two halves of the node's own, K's
         // scale those of Q's power, so that neither alone carries it past the range; held within the range:
         // 0 or Inf would make NaN of an unseen key's -Inf or of a score of 0.  (A row of Q with a NaN
-        // or an Inf has parts of 0; it gets its NaN at the end.)
+        // or an Inf has parts of 0, so each key that it sees weighs 1; it gets its NaN at the end.)
         const bool q_bad = q_ex == 1000;
         const float q_a = sm_scale * kLog2e * pow2n((q_bad ? 0 : q_ex) / 2), q_b = pow2n(q_bad ? 0 : q_ex - q_ex / 2);
         const float c_nodes = fminf(q_a * q_b, 3e38f);
@@ -667,7 +667,7 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
         // the part's record: o normalized by its own sum, the base and the sum
         const size_t rec = static_cast<size_t>(done.b) * Qn + done.pq + cta;
         const int rrow = grp * kRows + r;
-        if (q_bad) l = __int_as_float(0x7FC00000);
+        if (q_bad && l != 0.0f) l = __int_as_float(0x7FC00000);  // (0: it has seen no key of the part, which leaves none)
         const float inv = poison ? __int_as_float(0x7FC00000) : l != 0.0f ? 1.0f / l : 0.0f;
         float4* dst = reinterpret_cast<float4*>(ws_o + rec * (RT * kRows * kHD)) + rrow;
 #pragma unroll 1
