@@ -144,15 +144,16 @@ prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_la
         }
 #pragma unroll
         for (int w = 1; w < 16; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
-        const float nm = fmaxf(m[i], top);  // (finite from the first tile on: every row sees key 0)
-        const float corr = expf(m[i] - nm);
+        const float nm = fmaxf(m[i], top);
+        const float base = nm == -INFINITY ? 0.0f : nm;  // (scores of -Inf alone so far: weights of 0)
+        const float corr = expf(m[i] - base);
         m[i] = nm;
         l[i] *= corr;
 #pragma unroll
         for (int k = 0; k < ND; ++k) o[i][k].x *= corr, o[i][k].y *= corr;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float p = expf(s[i][j] - nm);
+          const float p = expf(s[i][j] - base);
           l[i] += p;
           sP[(RPT * ty + i) * C::P_PITCH + tx + 16 * j] = p;
         }
@@ -210,9 +211,10 @@ prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_la
       if (r < rows) {
         const int f = f0 + r, row = f / g.G, h = it.kvh * g.G + f - row * g.G;
         const size_t at = static_cast<size_t>(q.start + row) * g.H + h;
+        const float den = l[i] != 0.0f ? l[i] : 1.0f;  // (0: every score was -Inf)
 #pragma unroll
         for (int k = 0; k < ND; ++k)
-          *reinterpret_cast<float2*>(O + at * HD + 2 * tx + 32 * k) = make_float2(o[i][k].x / l[i], o[i][k].y / l[i]);
+          *reinterpret_cast<float2*>(O + at * HD + 2 * tx + 32 * k) = make_float2(o[i][k].x / den, o[i][k].y / den);
         if (tx == 0) lse[at] = m[i] + logf(l[i]);
       }
     }

@@ -1,0 +1,71 @@
+"""GPU parity of prompt_attn at the edges of its inputs: scores of -Inf, long sums.
+
+Tolerances as in test_gpu_prompt, with what a test adds to them derived beside it.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import host
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from test_gpu_prompt import call, inputs
+
+
+def check_inf(d, O, lse):
+    """As check() of test_gpu_prompt, with keys whose score is -Inf: they weigh 0, and a row that has no others gets 0 and -Inf."""
+    O, lse = host(O).astype(np.float64), host(lse).astype(np.float64)
+    G, page, scale = d["H"] // d["KVH"], d["page"], 1 / math.sqrt(d["hd"])
+    w_err, half = (2.0 ** -8, 2.0 ** -8) if d["dt"] == "bf16" else (2.0 ** -20, 2.0 ** -24)
+    for b in range(d["B"]):
+        n, c = d["rows"][b], d["ctx"][b]
+        t, r = np.arange(c + n), np.arange(n)
+        k, v = (x[d["pt"][b, t // page], :, t % page].astype(np.float64) for x in (d["k"], d["v"]))
+        at = d["start"][b] + r
+        for h in range(d["H"]):
+            q, kh, vh = d["Q"][at, h].astype(np.float64), k[:, h // G], v[:, h // G]
+            kh0 = np.where(np.isinf(kh), 0.0, kh)
+            seen = (t[None] <= c + r[:, None]) & ~np.isinf(kh).any(1)[None]
+            s = np.where(seen, q @ kh0.T * scale, -np.inf)
+            big = np.where(seen, np.abs(q) @ np.abs(kh0).T * scale, 0.0).max(1)
+            none = ~seen.any(1)
+            m = np.where(none, 0.0, s.max(1))[:, None]
+            p = np.exp(s - m)
+            z = p.sum(1, keepdims=True) + none[:, None]
+            o, mag, l = p @ vh / z, p @ np.abs(vh) / z, (m + np.log(z))[:, 0]
+            assert np.all(O[at[none], h] == 0) and np.all(np.isneginf(lse[at[none], h])), (b, h)
+            some = ~none
+            ds = 2.0 ** -18 * (big + 1.0)
+            assert np.all((np.abs(lse[at, h] - l) <= ds + 2.0 ** -21 * np.abs(l))[some]), (b, h)
+            e = (w_err + 2 * ds[:, None]) * mag
+            bad = np.abs(O[at, h] - o) - (e + half * (np.abs(o) + e) + 2.0 ** -126)
+            assert np.all(bad[some] <= 0), (b, h, bad[some].max())
+
+
+def inf_keys(d, where):
+    """Q positive in dim 0, K there -Inf for the keys that where(t, request) names: their scores are -Inf."""
+    d["Q"][..., 0] = np.abs(d["Q"][..., 0]) + 0.5
+    for b in range(d["B"]):
+        t = np.arange(d["rows"][b] + d["ctx"][b])
+        gone = t[where(t, b)]
+        d["k"][d["pt"][b, gone // d["page"]], :, gone % d["page"], 0] = -np.inf
+    return d
+
+
+WHERE = {"first 64": lambda t, b: t < 64, "first 130": lambda t, b: t < 130, "a stretch": lambda t, b: (t >= 40) & (t < 300),
+         "all but one": lambda t, b: t != 200, "all": lambda t, b: t >= 0}
+
+
+@pytest.mark.parametrize("where", WHERE)
+@pytest.mark.parametrize("H,KVH,hd,rows,ctx", [(4, 2, 64, [300, 5], [0, 250]), (32, 32, 128, [150], [100]), (2, 1, 96, [20], [220])])
+def test_prompt_attn_fp32_scores_of_minus_inf(H, KVH, hd, rows, ctx, where):
+    """Tiles of 16 and of 64 rows; rows with no other score in their first tiles, in later ones, in all."""
+    d = inf_keys(inputs(H + hd, H, KVH, hd, rows, ctx, 16, "f32"), WHERE[where])
+    O, lse, err = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check_inf(d, O, lse)
