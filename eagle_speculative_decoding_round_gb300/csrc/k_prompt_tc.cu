@@ -13,9 +13,9 @@
 //                      them get NaN
 //   softmax (2 x 4 warps)  steps of 64 keys in two buffers of tensor memory: exponentials against
 //                      the base so far, P (bf16) over S.  No pass for the maximum but on an item's
-//                      first tile: where a step's sum passes kTop, or is NaN, the maximum is looked
-//                      for, the base moved and the step done again.  The diagonal's tiles take -Inf
-//                      where unseen.
+//                      first step: where a step's sum passes kTop, or is NaN, or a row has met scores
+//                      of -Inf alone, the maximum is looked for, the base moved and the step done
+//                      again.  The diagonal's tiles take -Inf where unseen.
 // O stays in tensor memory until the item's end; its rows are written from there.
 //
 // Calls of few items behind long contexts (prompt_splits) are cut into equal shares, one for each
@@ -521,7 +521,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
             for (int j = 0; j < 32; ++j) a[j & 3] = fmax3f(a[j & 3], lo_of(y[j]), hi_of(y[j]));
             const float nm = fmaxf(m, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * c);
             if (u > 0) {
-              const float corr = ex2(m - nm);
+              const float corr = nm == -INFINITY ? 1.0f : ex2(m - nm);
               l *= corr;
               // (the scores of this step came behind the product of the step before the last)
               if (!warp_wait(&o_step[grp], (n_step - 1) & 1, abort)) {
@@ -541,7 +541,8 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
             }
             m = nm;
           }
-          const unsigned long long nv = pair(-m, -m);
+          const float base = m == -INFINITY ? 0.0f : m;  // (scores of -Inf alone so far: weights of 0)
+          const unsigned long long nv = pair(-base, -base);
           unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -557,7 +558,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
           }
           sum[0] = add2(sum[0], sum[1]);
           s = lo_of(sum[0]) + hi_of(sum[0]);
-          if (look || !__any_sync(0xFFFFFFFFu, row_ok && !(s <= kTop))) break;
+          if (look || !__any_sync(0xFFFFFFFFu, row_ok && (!(s <= kTop) || m == -INFINITY))) break;
           look = true;
         }
         if (!live) break;
@@ -604,7 +605,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
         continue;
       }
       const size_t at = (static_cast<size_t>(it.start) + row) * g.H + it.kvh * g.G + (it.rem + f - over * g.G);
-      const float inv = poison ? __int_as_float(0x7FC00000) : 1.0f / l;
+      const float inv = poison ? __int_as_float(0x7FC00000) : l != 0.0f ? 1.0f / l : 0.0f;  // (0: every score was -Inf)
       // 64 dims of the warp's rows go through its 4 KB of shared memory (16-byte pieces, swizzled),
       // so that a store takes whole lines: a thread's own row would cost a line for each 16 bytes
       unsigned char* stage = sOut + (warp - kSoftmax0) * 4096;
@@ -719,7 +720,7 @@ prompt_merge_kernel(const __grid_constant__ PromptGeom g, const Border* __restri
         const float4* from = reinterpret_cast<const float4*>(ws_o) + static_cast<size_t>(part.x) * (HD / 4 * 2 * kRows) + r;
 #pragma unroll
         for (int i = 0; i < NQ; ++i) x[u][i] = from[(warp + kMergeWarps * i) * (2 * kRows)];
-        if (j0 + u >= parts || see <= part.y) y[u] = make_float2(-INFINITY, 0.0f);
+        if (j0 + u >= parts || see <= part.y) y[u] = make_float2(-INFINITY, -1.0f);  // (no sum is below 0)
       }
       float top = M;
 #pragma unroll
@@ -733,8 +734,8 @@ prompt_merge_kernel(const __grid_constant__ PromptGeom g, const Border* __restri
       }
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u)
-        if (y[u].y != 0.0f) {  // (a part that the row sees has a sum of 1 at least, or NaN)
-          const float c = ex2(y[u].x - M);
+        if (y[u].y != -1.0f) {
+          const float c = ex2(y[u].x - (M == -INFINITY ? 0.0f : M));  // (a part whose scores were all -Inf: 0)
           den = fmaf(y[u].y, c, den);
 #pragma unroll
           for (int i = 0; i < NQ; ++i) {
@@ -745,7 +746,7 @@ prompt_merge_kernel(const __grid_constant__ PromptGeom g, const Border* __restri
     }
     if (!ok) break;
     const size_t at = (static_cast<size_t>(q.start) + row) * g.H + p.kvh * g.G + head;
-    const float inv = 1.0f / den;
+    const float inv = den != 0.0f ? 1.0f / den : 0.0f;
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
       reinterpret_cast<uint2*>(O + at * HD)[warp + kMergeWarps * i] =

@@ -641,7 +641,8 @@ E3_API size_t eagle3_verify8_workspace_bytes(int B, int R, int n_q_heads, int n_
  * Q: [n_total][n_q_heads][head_dim] dtype kv->dt; O: same shape and dtype; lse: [n_total]
  * [n_q_heads] fp32.  Rows of Q, O and lse that belong to no request are left as they were.
  * Slots that a row does not see have no effect on it, whatever they hold; a row that sees a
- * NaN or an Inf in V gets NaN or Inf in o, in that dimension at least.
+ * NaN or an Inf in V gets NaN or Inf in o, in that dimension at least.  Keys whose score is
+ * -Inf weigh 0; a row that sees no others gets 0 in o and -Inf in lse.
  * n_rows[b] outside [0, max_rows], kv_len[b] outside [0, max_kv_len], rows outside
  * [0, n_total), or slots beyond max_pages set E3_DEV_ERR_CAPACITY and leave the request's
  * outputs unwritten; a page id out of range sets it and makes them unspecified.  Rows of

@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+from eagle_speculative_decoding_round_gb300 import synth
 from gpu_util import host
 
 pytestmark = pytest.mark.gpu
@@ -49,6 +50,8 @@ def check_inf(d, O, lse):
 def inf_keys(d, where):
     """Q positive in dim 0, K there -Inf for the keys that where(t, request) names: their scores are -Inf."""
     d["Q"][..., 0] = np.abs(d["Q"][..., 0]) + 0.5
+    if d["dt"] == "bf16":
+        d["Q"] = synth.to_bf16_f32(d["Q"])  # what the device holds
     for b in range(d["B"]):
         t = np.arange(d["rows"][b] + d["ctx"][b])
         gone = t[where(t, b)]
@@ -69,3 +72,27 @@ def test_prompt_attn_fp32_scores_of_minus_inf(H, KVH, hd, rows, ctx, where):
     torch.cuda.synchronize()
     assert int(err.item()) == 0
     check_inf(d, O, lse)
+
+
+@pytest.mark.parametrize("where", WHERE)
+@pytest.mark.parametrize("H,KVH,hd,rows,ctx", [
+    (4, 2, 64, [300, 5], [0, 250]), (8, 2, 128, [400], [100]), (5, 1, 128, [103, 300], [77, 0]),
+    (8, 2, 128, [9, 130], [4000, 2500]), (16, 1, 64, [1], [20000])])  # (the last two are cut along their keys)
+def test_prompt_attn_bf16_scores_of_minus_inf(H, KVH, hd, rows, ctx, where):
+    """Rows with no other score in their first steps, in whole parts of a cut item, in all."""
+    d = inf_keys(inputs(H + hd, H, KVH, hd, rows, ctx, 16), WHERE[where])
+    O, lse, err = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check_inf(d, O, lse)
+
+
+@pytest.mark.parametrize("dt,ctx", [("bf16", 130), ("bf16", 4000), ("f32", 130)])
+def test_prompt_attn_bad_values_beside_scores_of_minus_inf(dt, ctx):
+    """V with a NaN where the score is -Inf: the rows that see it get NaN (0 times NaN), whichever part holds it."""
+    d = inf_keys(inputs(ctx, 8, 2, 64, [20], [ctx], 16, dt), WHERE["first 130"])
+    d["v"][d["pt"][0, 7 // 16], :, 7 % 16, 3] = np.nan
+    O, lse, err = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    assert np.isnan(host(O)[d["start"][0]:d["start"][0] + 20][..., 3]).all() and not np.isnan(host(lse)).any()
