@@ -103,7 +103,7 @@ prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_la
     int see[RPT];  // keys that the thread's rows see
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      m[i] = -INFINITY;
+      m[i] = -3.402823466e38f;
       l[i] = 0.0f;
       see[i] = q.c + (f0 + RPT * ty + i) / g.G + 1;
 #pragma unroll
@@ -144,16 +144,15 @@ prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_la
         }
 #pragma unroll
         for (int w = 1; w < 16; w <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, w));
-        const float nm = fmaxf(m[i], top);
-        const float base = nm == -INFINITY ? 0.0f : nm;  // (scores of -Inf alone so far: weights of 0)
-        const float corr = expf(m[i] - base);
+        const float nm = fmaxf(m[i], top);  // (finite, so that scores of -Inf weigh 0 where there has been no other)
+        const float corr = expf(m[i] - nm);
         m[i] = nm;
         l[i] *= corr;
 #pragma unroll
         for (int k = 0; k < ND; ++k) o[i][k].x *= corr, o[i][k].y *= corr;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float p = expf(s[i][j] - base);
+          const float p = expf(s[i][j] - nm);
           l[i] += p;
           sP[(RPT * ty + i) * C::P_PITCH + tx + 16 * j] = p;
         }

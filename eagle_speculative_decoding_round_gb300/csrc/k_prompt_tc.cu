@@ -13,9 +13,9 @@
 //                      them get NaN
 //   softmax (2 x 4 warps)  steps of 64 keys in two buffers of tensor memory: exponentials against
 //                      the base so far, P (bf16) over S.  No pass for the maximum but on an item's
-//                      first step: where a step's sum passes kTop, or is NaN, or a row has met scores
-//                      of -Inf alone, the maximum is looked for, the base moved and the step done
-//                      again.  The diagonal's tiles take -Inf where unseen.
+//                      first step: where a step's sum passes kTop, or is NaN, the maximum is looked
+//                      for, the base moved and the step done again.  The diagonal's tiles take -Inf
+//                      where unseen.
 // O stays in tensor memory until the item's end; its rows are written from there.
 //
 // Calls of few items behind long contexts (prompt_splits) are cut into equal shares, one for each
@@ -51,6 +51,7 @@ constexpr int kHalfB = 16384;    // bytes of 64 dims of a tile: [128 rows][128 B
 constexpr int kThreads = 384;
 constexpr int kSoftmax0 = 4;     // first softmax warp
 constexpr float kTop = 32768.0f;
+constexpr float kLowest = -3.402823466e38f;
 constexpr int kShift = 8;        // an item has 2 * kRows flat rows
 
 template <int HD>
@@ -495,8 +496,9 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       const int f = grp * kRows + r, over = small_div(it.rem + f, g.inv_G), row = it.row + over;
       const bool row_ok = f < it.flat;
       const int see = row_ok ? it.c + row + 1 : it.keys_of(grp);  // keys that the row sees
-      // (a row that sees none of the part's keys sees none in any step: every weight is 0, whatever the base)
-      float m = see > it.key0() ? -INFINITY : 0.0f, l = 0.0f;
+      // The base is finite from the start: scores of -Inf, unseen or not, weigh 0 against it, and the sum of a step with
+      // the first other score passes kTop.
+      float m = kLowest, l = 0.0f;
       for (int u = 0; u < mine; ++u, ++n_step) {
         const uint32_t bf = n_step & 1, tB = tS + bf * kStep;
         if (!warp_wait(&s_full[2 * grp + bf], (n_step >> 1) & 1, abort)) {
@@ -521,7 +523,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
             for (int j = 0; j < 32; ++j) a[j & 3] = fmax3f(a[j & 3], lo_of(y[j]), hi_of(y[j]));
             const float nm = fmaxf(m, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * c);
             if (u > 0) {
-              const float corr = nm == -INFINITY ? 1.0f : ex2(m - nm);
+              const float corr = ex2(m - nm);
               l *= corr;
               // (the scores of this step came behind the product of the step before the last)
               if (!warp_wait(&o_step[grp], (n_step - 1) & 1, abort)) {
@@ -541,8 +543,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
             }
             m = nm;
           }
-          const float base = m == -INFINITY ? 0.0f : m;  // (scores of -Inf alone so far: weights of 0)
-          const unsigned long long nv = pair(-base, -base);
+          const unsigned long long nv = pair(-m, -m);
           unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -558,7 +559,7 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
           }
           sum[0] = add2(sum[0], sum[1]);
           s = lo_of(sum[0]) + hi_of(sum[0]);
-          if (look || !__any_sync(0xFFFFFFFFu, row_ok && (!(s <= kTop) || m == -INFINITY))) break;
+          if (look || !__any_sync(0xFFFFFFFFu, row_ok && !(s <= kTop))) break;
           look = true;
         }
         if (!live) break;
@@ -735,7 +736,7 @@ prompt_merge_kernel(const __grid_constant__ PromptGeom g, const Border* __restri
 #pragma unroll
       for (int u = 0; u < AHEAD; ++u)
         if (y[u].y != -1.0f) {
-          const float c = ex2(y[u].x - (M == -INFINITY ? 0.0f : M));  // (a part whose scores were all -Inf: 0)
+          const float c = ex2(y[u].x - M);
           den = fmaf(y[u].y, c, den);
 #pragma unroll
           for (int i = 0; i < NQ; ++i) {
