@@ -8,8 +8,9 @@
 // prompt_simt_kernel: a block of 16 x 16 threads takes a tile of 16 RPT flat rows (prompt.cuh) and
 // walks its keys in tiles of 64: S = Q K^T with RPT x 4 values a thread, a running maximum and sum
 // per row, O += P V with RPT rows and HD / 16 dims a thread.  RPT 4: one buffer for K and V, so that two
-// blocks share an SM.  RPT 1: a buffer each, loaded under the other's products.  Everything in fp32 FMAs: tensor
-// cores would round the operands to tf32.
+// blocks share an SM (heads up to 96).  RPT 1: a buffer each, loaded under the other's products.  Everything in fp32
+// FMAs: tensor cores would round the operands to tf32.  A tile's keys are summed by themselves before they join O: added one
+// by one to the sum of all before them, 131072 keys of one sign lost 2^-12.5 of it.
 //
 // Bound: FMAs, and for small prompts the latency of a tile's chain (loads, S, softmax, O).
 // Measured on a GB300: 3 prompts of 15 to 131 rows behind up to 128 keys, 4 heads of 64: 18 us
@@ -39,7 +40,7 @@ struct SimtCfg {
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 
 template <int HD, int RPT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, RPT == 1 || HD <= 96 ? 2 : 1)
 prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_layer kv, const __grid_constant__ PromptGeom g,
                    float sm_scale, float* __restrict__ O, float* __restrict__ lse, int32_t* dev_err) {
   using C = SimtCfg<HD, RPT>;
@@ -101,14 +102,46 @@ prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_la
     float m[RPT], l[RPT];
     float2 o[RPT][ND];
     int see[RPT];  // keys that the thread's rows see
+    // Long sums in three levels, none of more than about the square root of the tiles (from 64 on): a tile's keys, `span`
+    // tiles' partial sums in o and l, and these in the row's own place in O and in fl, against the base fm.
+    const int tiles = (keys + kKeys - 1) / kKeys, span = max(64, 1 << ((33 - __clz(tiles - 1)) / 2));
+    float fm[RPT], fl[RPT];
+    bool folded = false;
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
       m[i] = -3.402823466e38f;
-      l[i] = 0.0f;
+      l[i] = fl[i] = fm[i] = 0.0f;
       see[i] = q.c + (f0 + RPT * ty + i) / g.G + 1;
 #pragma unroll
       for (int k = 0; k < ND; ++k) o[i][k] = make_float2(0.0f, 0.0f);
     }
+    // place of row i of the thread's in lse (O: times HD), -1: no row
+    auto place_of = [&](int i) -> long long {
+      const int r = RPT * ty + i;
+      if (r >= rows) return -1;
+      const int f = f0 + r, row = f / g.G, h = it.kvh * g.G + f - row * g.G;
+      return static_cast<long long>(q.start + row) * g.H + h;
+    };
+    auto pair_of = [&](long long place, int k) { return reinterpret_cast<float2*>(O + place * HD + 2 * tx + 32 * k); };
+    // o and l join the sums in O and fl (`more`: there are some), and begin again
+    auto fold = [&](bool more) {
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const long long place = place_of(i);
+        const float f = more ? expf(fm[i] - m[i]) : 0.0f;
+        fl[i] = fmaf(fl[i], f, l[i]);
+        fm[i] = m[i];
+        l[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < ND; ++k) {
+          if (place >= 0) {
+            const float2 x = more ? *pair_of(place, k) : make_float2(0.0f, 0.0f);
+            *pair_of(place, k) = make_float2(fmaf(x.x, f, o[i][k].x), fmaf(x.y, f, o[i][k].y));
+          }
+          o[i][k] = make_float2(0.0f, 0.0f);
+        }
+      }
+    };
     if (threadIdx.x < kKeys) s_row[0][threadIdx.x] = row_of(threadIdx.x);
     __syncthreads();
     load_tile(kv.k, sK, 0);
@@ -147,15 +180,14 @@ prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_la
         const float nm = fmaxf(m[i], top);  // (finite, so that scores of -Inf weigh 0 where there has been no other)
         const float corr = expf(m[i] - nm);
         m[i] = nm;
-        l[i] *= corr;
 #pragma unroll
         for (int k = 0; k < ND; ++k) o[i][k].x *= corr, o[i][k].y *= corr;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float p = expf(s[i][j] - nm);
-          l[i] += p;
-          sP[(RPT * ty + i) * C::P_PITCH + tx + 16 * j] = p;
+          s[i][j] = expf(s[i][j] - nm);
+          sP[(RPT * ty + i) * C::P_PITCH + tx + 16 * j] = s[i][j];
         }
+        l[i] = fmaf(l[i], corr, (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]));
       }
       if (threadIdx.x < kKeys) s_row[(t0 / kKeys + 1) & 1][threadIdx.x] = row_next;
       __syncthreads();  // (K is read, P is written)
@@ -171,6 +203,7 @@ prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_la
       // keys that every row of the tile sees, then those that only some do: a row must not meet
       // another's in 0 * Inf
       const int n = min(kKeys, keys - t0), common = min(n, max(0, q.c + f0 / g.G + 1 - t0));
+      float2 part[RPT][ND] = {};
       int t = 0;
       for (; t + 4 <= common; t += 4) {
         float4 p[RPT];
@@ -183,8 +216,8 @@ prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_la
           for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const float2*>(sV + (t + e) * C::PITCH + 2 * tx + 32 * k);
 #pragma unroll
           for (int i = 0; i < RPT; ++i) {
-            o[i][k].x = fmaf(p[i].w, v[3].x, fmaf(p[i].z, v[2].x, fmaf(p[i].y, v[1].x, fmaf(p[i].x, v[0].x, o[i][k].x))));
-            o[i][k].y = fmaf(p[i].w, v[3].y, fmaf(p[i].z, v[2].y, fmaf(p[i].y, v[1].y, fmaf(p[i].x, v[0].y, o[i][k].y))));
+            part[i][k].x = fmaf(p[i].w, v[3].x, fmaf(p[i].z, v[2].x, fmaf(p[i].y, v[1].x, fmaf(p[i].x, v[0].x, part[i][k].x))));
+            part[i][k].y = fmaf(p[i].w, v[3].y, fmaf(p[i].z, v[2].y, fmaf(p[i].y, v[1].y, fmaf(p[i].x, v[0].y, part[i][k].y))));
           }
         }
       }
@@ -196,25 +229,35 @@ prompt_simt_kernel(const float* __restrict__ Q, const __grid_constant__ e3_kv_la
 #pragma unroll
             for (int k = 0; k < ND; ++k) {
               const float2 v = *reinterpret_cast<const float2*>(sV + t * C::PITCH + 2 * tx + 32 * k);
-              o[i][k].x = fmaf(p, v.x, o[i][k].x), o[i][k].y = fmaf(p, v.y, o[i][k].y);
+              part[i][k].x = fmaf(p, v.x, part[i][k].x), part[i][k].y = fmaf(p, v.y, part[i][k].y);
             }
           }
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int k = 0; k < ND; ++k) o[i][k].x += part[i][k].x, o[i][k].y += part[i][k].y;
+      if ((t0 / kKeys + 1) % span == 0 && t0 + kKeys < keys) {
+        fold(folded);
+        folded = true;
+      }
       __syncthreads();
       if (t0 + kKeys < keys) load_tile(C::BUFS == 1 ? kv.k : kv.v, sV, t0 + kKeys);
     }
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
+      const float f = folded ? expf(fm[i] - m[i]) : 0.0f;
+      l[i] = fmaf(fl[i], f, l[i]);
 #pragma unroll
       for (int w = 1; w < 16; w <<= 1) l[i] += __shfl_xor_sync(0xFFFFFFFFu, l[i], w);
-      const int r = RPT * ty + i;
-      if (r < rows) {
-        const int f = f0 + r, row = f / g.G, h = it.kvh * g.G + f - row * g.G;
-        const size_t at = static_cast<size_t>(q.start + row) * g.H + h;
+      const long long place = place_of(i);
+      if (place >= 0) {
         const float den = l[i] != 0.0f ? l[i] : 1.0f;  // (0: every score was -Inf)
 #pragma unroll
-        for (int k = 0; k < ND; ++k)
-          *reinterpret_cast<float2*>(O + at * HD + 2 * tx + 32 * k) = make_float2(o[i][k].x / den, o[i][k].y / den);
-        if (tx == 0) lse[at] = m[i] + logf(l[i]);
+        for (int k = 0; k < ND; ++k) {
+          const float2 x = folded ? *pair_of(place, k) : make_float2(0.0f, 0.0f);
+          *pair_of(place, k) = make_float2(fmaf(x.x, f, o[i][k].x) / den, fmaf(x.y, f, o[i][k].y) / den);
+        }
+        if (tx == 0) lse[place] = m[i] + logf(l[i]);
       }
     }
     __syncthreads();

@@ -96,3 +96,70 @@ def test_prompt_attn_bad_values_beside_scores_of_minus_inf(dt, ctx):
     torch.cuda.synchronize()
     assert int(err.item()) == 0
     assert np.isnan(host(O)[d["start"][0]:d["start"][0] + 20][..., 3]).all() and not np.isnan(host(lse)).any()
+
+
+def long_inputs(seed, H, KVH, hd, rows, ctx, dt, page=64, n=5, zeros=True):
+    """Contexts of any length over n pages that the tables name again and again; V of one sign, so that nothing of what a
+    sum loses is lost in cancellation; rows of zeros in Q (equal weights), or ordinary ones."""
+    rng = np.random.default_rng(seed)
+    d = inputs(seed, H, KVH, hd, rows, [0] * len(rows), page, dt)
+    rnd = (lambda a: synth.to_bf16_f32(a.astype(np.float32))) if dt == "bf16" else (lambda a: a.astype(np.float32))
+    most = max(r + c for r, c in zip(rows, ctx))
+    d.update(ctx=list(ctx), n=n, pt=np.stack([(np.arange(-(-most // page)) + b) % n for b in range(len(rows))]).astype(np.int32),
+             k=rnd(rng.normal(size=(n, KVH, page, hd))), v=rnd(rng.uniform(0.5, 1.0, (n, KVH, page, hd))))
+    if zeros:
+        d["Q"][:] = 0.0
+    return d
+
+
+def check_long(d, O, lse, adds, heads=None):
+    """64-bit softmax over the pages' slots, each counted as often as a row sees it.  `adds(keys)` bounds the error of a sum of
+    one sign, relative: it is added to the tolerance of test_gpu_prompt, once for the values' sum and once for the weights'."""
+    O, lse = host(O).astype(np.float64), host(lse).astype(np.float64)
+    G, page, scale = d["H"] // d["KVH"], d["page"], 1 / math.sqrt(d["hd"])
+    w_err, half = (2.0 ** -8, 2.0 ** -8) if d["dt"] == "bf16" else (2.0 ** -20, 2.0 ** -24)
+    worst = 0.0
+    for b in range(d["B"]):
+        for r in range(d["rows"][b]):
+            keys = d["ctx"][b] + r + 1
+            full, rest = divmod(keys, page)
+            count = np.bincount(d["pt"][b, :full], minlength=d["n"])[:, None] * np.ones(page)
+            if rest:
+                count[d["pt"][b, full], :rest] += 1
+            at, count = d["start"][b] + r, count.ravel()
+            for h in range(d["H"]) if heads is None else heads:
+                k, v = (x[:, h // G].reshape(-1, d["hd"]).astype(np.float64) for x in (d["k"], d["v"]))
+                q = d["Q"][at, h].astype(np.float64)
+                s, big = k @ q * scale, (np.abs(k) @ np.abs(q) * scale).max()
+                m = s[count > 0].max()
+                p = count * np.exp(s - m)
+                z = p.sum()
+                o, l = p @ v / z, m + np.log(z)
+                ds, lost = 2.0 ** -18 * (big + 1.0), adds(keys)
+                assert abs(lse[at, h] - l) <= ds + lost + 2.0 ** -21 * abs(l), (b, r, h, lse[at, h] - l)
+                e = (w_err + 2 * ds + 2 * lost) * o
+                bad = np.abs(O[at, h] - o) - (e + half * (o + e))
+                worst = max(worst, (np.abs(O[at, h] - o) / o).max())
+                assert np.all(bad <= 0), (b, r, h, worst, lost)
+    return worst
+
+
+def adds_fp32(keys):
+    """64 keys of a tile one after another, then up to 2.5 sqrt(tiles) partial sums in two levels (64 or more in the first): 2^-24 each."""
+    tiles = -(-keys // 64)
+    span = max(64, 2 ** (((tiles - 1).bit_length() + 1) // 2))
+    return (64 + min(tiles, span) + tiles // span) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("H,KVH,hd,rows,ctx,zeros", [
+    (4, 2, 64, [3], [20000], True), (4, 2, 64, [3], [20000], False), (2, 2, 128, [1], [1 << 20], True), (2, 1, 256, [2, 1], [70001, 4095], False),
+    (160, 160, 32, [2], [40000], True), (160, 160, 128, [1], [30000], False), (2, 1, 96, [1], [131072], True), (80, 80, 192, [70], [4200], True),
+    (160, 160, 64, [1], [12345], True), (160, 160, 160, [1], [8200], False), (160, 160, 224, [1], [9000], True), (160, 160, 256, [1], [9000], True)])
+def test_prompt_attn_fp32_long_sums(H, KVH, hd, rows, ctx, zeros):
+    """Tens of thousands of keys of one sign, tiles of 16 and of 64 rows: the sums do not lose what is added late."""
+    d = long_inputs(H + hd, H, KVH, hd, rows, ctx, "f32", zeros=zeros)
+    O, lse, err = call(d)
+    O2, lse2, _ = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(O, O2) and torch.equal(lse, lse2)
+    check_long(d, O, lse, adds_fp32, heads=None if H < 10 else (0, 7, H - 1))
