@@ -16,7 +16,8 @@
 //                      first step: where a step's sum passes kTop, or is NaN, the maximum is looked
 //                      for, the base moved and the step done again.  The diagonal's tiles take -Inf
 //                      where unseen.
-// O stays in tensor memory until the item's end; its rows are written from there.
+// O stays in tensor memory until the item's end (kFold: of long items, until 32768 keys are summed); its rows are written
+// from there.
 //
 // Calls of few items behind long contexts (prompt_splits) are cut into equal shares, one for each
 // CTA, whose borders may lie between any two tiles of an item's keys: the parts leave fp32 records (O,
@@ -53,6 +54,10 @@ constexpr int kSoftmax0 = 4;     // first softmax warp
 constexpr float kTop = 32768.0f;
 constexpr float kLowest = -3.402823466e38f;
 constexpr int kShift = 8;        // an item has 2 * kRows flat rows
+// Steps whose products tensor memory sums up.  The tensor core cuts a sum off where it adds to it: 4194304 keys with V of
+// one sign lost 2.5% so, which is 2^-12 for 32768.  Longer sums go on in fp32 in the CTA's record (one row of 152 heads of
+// 128 behind 131072 keys: 1.22 ms whole, 1.27 so; behind 4194304 36.0 and 37.5).
+constexpr int kFold = 512;
 
 template <int HD>
 struct TcCfg {
@@ -99,7 +104,8 @@ struct Border {
 // x / G for x < G + 256: the quotient is at least 1 / 2G off an integer, the product far less
 __device__ __forceinline__ int small_div(int x, float inv_g) { return static_cast<int>((static_cast<float>(x) + 0.5f) * inv_g); }
 
-template <int HD>
+// FOLDS: an item may have more than kFold steps
+template <int HD, bool FOLDS>
 __global__ void __launch_bounds__(kThreads, 1)
 prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CUtensorMap tmQ,
                  const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
@@ -499,81 +505,127 @@ prompt_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ CU
       // The base is finite from the start: scores of -Inf, unseen or not, weigh 0 against it, and the sum of a step with
       // the first other score passes kTop.
       float m = kLowest, l = 0.0f;
-      for (int u = 0; u < mine; ++u, ++n_step) {
-        const uint32_t bf = n_step & 1, tB = tS + bf * kStep;
-        if (!warp_wait(&s_full[2 * grp + bf], (n_step >> 1) & 1, abort)) {
-          live = false;
-          break;
+      // The row's sums so far go to the CTA's record, with their base and the weights' sum, and begin again; at the item's end
+      // what has gone there comes back.
+      auto fold = [&](int u, bool end) {
+        const size_t slot = it.rec >= 0 ? it.rec : 2 * blockIdx.x + 1;
+        float4* sum = reinterpret_cast<float4*>(ws_o) + slot * (HD / 4 * 2 * kRows) + grp * kRows + r;
+        float2* ml = ws_ml + slot * (2 * kRows) + grp * kRows + r;
+        const bool more = end || u > kFold;
+        const float2 old = more ? *ml : make_float2(m, 0.0f);
+        const float f = ex2(old.x - m);
+        l = fmaf(old.y, f, l);
+        if (!end) {
+          *ml = make_float2(m, l);
+          l = 0.0f;
         }
-        fence_after();
-        const int vis = see - it.key0() - u * kStep;  // keys of the step that the row sees
-        const bool masked = __any_sync(0xFFFFFFFFu, vis < kStep);
-        bool look = u == 0;  // for the maximum
-        float s;
-        unsigned long long y[32];
-        tmem_ld64_pairs(tB, y);
-        if (masked)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) y[j] = pair(2 * j < vis ? lo_of(y[j]) : -INFINITY, 2 * j + 1 < vis ? hi_of(y[j]) : -INFINITY);
 #pragma unroll 1
-        for (;;) {
-          if (look) {
-            float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        for (int q = 0; q < HD / 16; ++q) {
+          uint32_t x[16];
+          tmem_ld16(tO + 16 * q, x);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) a[j & 3] = fmax3f(a[j & 3], lo_of(y[j]), hi_of(y[j]));
-            const float nm = fmaxf(m, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * c);
-            if (u > 0) {
-              const float corr = ex2(m - nm);
-              l *= corr;
-              // (the scores of this step came behind the product of the step before the last)
-              if (!warp_wait(&o_step[grp], (n_step - 1) & 1, abort)) {
-                live = false;
-                break;
-              }
-              fence_after();
-#pragma unroll 1
-              for (int d = 0; d < HD / 16; ++d) {
-                uint32_t x[16];
-                tmem_ld16(tO + 16 * d, x);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * corr);
-                tmem_st16(tO + 16 * d, x);
-              }
-              tmem_st_wait();
+          for (int j = 0; j < 4; ++j) {
+            float4& to = sum[(4 * q + j) * (2 * kRows)];
+            float4 y = more ? to : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            y = make_float4(fmaf(y.x, f, __uint_as_float(x[4 * j])), fmaf(y.y, f, __uint_as_float(x[4 * j + 1])),
+                            fmaf(y.z, f, __uint_as_float(x[4 * j + 2])), fmaf(y.w, f, __uint_as_float(x[4 * j + 3])));
+            if (!end) {
+              to = y;
+              y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             }
-            m = nm;
+            x[4 * j] = __float_as_uint(y.x), x[4 * j + 1] = __float_as_uint(y.y);
+            x[4 * j + 2] = __float_as_uint(y.z), x[4 * j + 3] = __float_as_uint(y.w);
           }
-          const unsigned long long nv = pair(-m, -m);
-          unsigned long long sum[2] = {0ull, 0ull};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t pk[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const unsigned long long a = fma2(y[8 * i + j], cv, nv);
-              const float e0 = ex2(lo_of(a)), e1 = ex2(hi_of(a));
-              sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
-              pk[j] = pack2_bf16(e0, e1);
-            }
-            tmem_st8(tB + 8 * i, pk);  // (the scores are in registers, for a step that is done again too)
-          }
-          sum[0] = add2(sum[0], sum[1]);
-          s = lo_of(sum[0]) + hi_of(sum[0]);
-          if (look || !__any_sync(0xFFFFFFFFu, row_ok && !(s <= kTop))) break;
-          look = true;
+          tmem_st16(tO + 16 * q, x);
         }
-        if (!live) break;
-        l += s;
         tmem_st_wait();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&p_full[2 * grp + bf]);
+      };
+      int u = 0;
+#pragma unroll 1
+      for (int until = FOLDS ? min(mine, kFold) : mine;; until = min(mine, until + kFold)) {
+        for (; u < until; ++u, ++n_step) {
+          const uint32_t bf = n_step & 1, tB = tS + bf * kStep;
+          if (!warp_wait(&s_full[2 * grp + bf], (n_step >> 1) & 1, abort)) {
+            live = false;
+            break;
+          }
+          fence_after();
+          const int vis = see - it.key0() - u * kStep;  // keys of the step that the row sees
+          const bool masked = __any_sync(0xFFFFFFFFu, vis < kStep);
+          bool look = u == 0;  // for the maximum
+          float s;
+          unsigned long long y[32];
+          tmem_ld64_pairs(tB, y);
+          if (masked)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) y[j] = pair(2 * j < vis ? lo_of(y[j]) : -INFINITY, 2 * j + 1 < vis ? hi_of(y[j]) : -INFINITY);
+#pragma unroll 1
+          for (;;) {
+            if (look) {
+              float a[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int j = 0; j < 32; ++j) a[j & 3] = fmax3f(a[j & 3], lo_of(y[j]), hi_of(y[j]));
+              const float nm = fmaxf(m, fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3])) * c);
+              if (u > 0) {
+                const float corr = ex2(m - nm);
+                l *= corr;
+                // (the scores of this step came behind the product of the step before the last)
+                if (!warp_wait(&o_step[grp], (n_step - 1) & 1, abort)) {
+                  live = false;
+                  break;
+                }
+                fence_after();
+#pragma unroll 1
+                for (int d = 0; d < HD / 16; ++d) {
+                  uint32_t x[16];
+                  tmem_ld16(tO + 16 * d, x);
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * corr);
+                  tmem_st16(tO + 16 * d, x);
+                }
+                tmem_st_wait();
+              }
+              m = nm;
+            }
+            const unsigned long long nv = pair(-m, -m);
+            unsigned long long sum[2] = {0ull, 0ull};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t pk[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const unsigned long long a = fma2(y[8 * i + j], cv, nv);
+                const float e0 = ex2(lo_of(a)), e1 = ex2(hi_of(a));
+                sum[j & 1] = add2(sum[j & 1], pair(e0, e1));
+                pk[j] = pack2_bf16(e0, e1);
+              }
+              tmem_st8(tB + 8 * i, pk);  // (the scores are in registers, for a step that is done again too)
+            }
+            sum[0] = add2(sum[0], sum[1]);
+            s = lo_of(sum[0]) + hi_of(sum[0]);
+            if (look || !__any_sync(0xFFFFFFFFu, row_ok && !(s <= kTop))) break;
+            look = true;
+          }
+          if (!live) break;
+          l += s;
+          tmem_st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(&p_full[2 * grp + bf]);
+        }
+        if (!FOLDS || !live || u == mine) break;
+        // (the next step's scores came behind the product of the step before the last, of which o_step's phase tells then)
+        live = warp_wait(&s_full[2 * grp + (n_step & 1)], (n_step >> 1) & 1, abort) && warp_wait(&o_step[grp], (n_step - 1) & 1, abort);
+        if (!live) break;
+        fence_after();
+        fold(u, false);
       }
       live = live && warp_wait(&o_done[grp], n_item & 1, abort);
       if (!live) break;
       ++n_item;
       __syncwarp();
       fence_after();
+      if (FOLDS && mine > kFold) fold(mine, true);
       // a row that sees a V which was taken out gets NaN (the marks are complete: the products are)
       bool poison = false;
       for (int t = max(it.t0, it.common / kKeys); t < it.t1 && t * kKeys < see; ++t) {
@@ -769,20 +821,23 @@ bool prompt_splits(const PromptGeom& g, int max_kv_len) {
   const double whole = items <= sms ? ctx + own : ((items + sms - 1) / sms) * ctx + items * own / (2 * sms);
   return whole - share > 8.0 + 12.0 * std::min(1.0, static_cast<double>(g.max_rows) * g.G / (2 * kRows));
 }
+// Whether an item may have more keys than tensor memory sums up.  Where it may not the kernel leaves that out of its loop: 16
+// prompts of 512 to 8192 rows 2254 us, with it 2280.
+bool prompt_folds(const PromptGeom& g, int max_kv_len) { return static_cast<long long>(max_kv_len) + g.max_rows > kFold * kStep; }
 size_t record_rows() { return static_cast<size_t>(2) * num_sms() * 2 * kRows; }
 
-template <int HD>
+template <int HD, bool FOLDS>
 cudaError_t launch_tc(const void* Q, const CUtensorMap& mq, bool q_box, const CUtensorMap& mk, const CUtensorMap& mv,
                       const e3_kv_layer& kv, const PromptGeom& g, int box, float sm_scale, void* O, float* lse, int32_t* dev_err,
                       float* ws_o, float2* ws_ml, Border* ws_border, cudaStream_t s) {
   static OncePerDevice<cudaError_t> attrs;
   const cudaError_t e = once_per_device(attrs, [] {
-    return cudaFuncSetAttribute(prompt_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<HD>::SMEM);
+    return cudaFuncSetAttribute(prompt_tc_kernel<HD, FOLDS>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<HD>::SMEM);
   });
   if (e != cudaSuccess) return e;
   const int workers = g.split ? num_sms() : static_cast<int>(std::min<long long>(prompt_items_bound(g), num_sms()));
   const cudaError_t el =
-      launch_pdl(prompt_tc_kernel<HD>, dim3(workers), dim3(kThreads), TcCfg<HD>::SMEM, s, 1, static_cast<const __nv_bfloat16*>(Q), mq, mk,
+      launch_pdl(prompt_tc_kernel<HD, FOLDS>, dim3(workers), dim3(kThreads), TcCfg<HD>::SMEM, s, 1, static_cast<const __nv_bfloat16*>(Q), mq, mk,
                  mv, kv, g, box, q_box, sm_scale, static_cast<__nv_bfloat16*>(O), lse, ws_o, ws_ml, ws_border, dev_err);
   if (el != cudaSuccess || !g.split) return el;
   return launch_pdl(prompt_merge_kernel<HD>, dim3((workers - 1) * kMergeCtas), dim3(kMergeWarps * 32), workers * sizeof(int2), s, 1, g, ws_border, ws_o, ws_ml,
@@ -793,7 +848,8 @@ cudaError_t launch_tc(const void* Q, const CUtensorMap& mq, bool q_box, const CU
 
 size_t prompt_tc_workspace_bytes(PromptGeom g, int hd, int max_kv_len) {
   g.shift = kShift;
-  return prompt_splits(g, max_kv_len) ? record_rows() * (hd * sizeof(float) + sizeof(float2)) + num_sms() * sizeof(Border) : 0;
+  if (!prompt_splits(g, max_kv_len) && !prompt_folds(g, max_kv_len)) return 0;
+  return record_rows() * (hd * sizeof(float) + sizeof(float2)) + num_sms() * sizeof(Border);
 }
 
 e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, int max_kv_len, float sm_scale, void* O, float* lse,
@@ -801,8 +857,9 @@ e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, i
   g.shift = kShift;
   g.split = prompt_splits(g, max_kv_len);
   float* ws_o = static_cast<float*>(ws);
-  float2* ws_ml = g.split ? reinterpret_cast<float2*>(ws_o + record_rows() * kv.head_dim) : nullptr;
-  Border* ws_border = g.split ? reinterpret_cast<Border*>(ws_ml + record_rows()) : nullptr;
+  const bool folds = prompt_folds(g, max_kv_len), records = g.split || folds;
+  float2* ws_ml = records ? reinterpret_cast<float2*>(ws_o + record_rows() * kv.head_dim) : nullptr;
+  Border* ws_border = records ? reinterpret_cast<Border*>(ws_ml + record_rows()) : nullptr;
   int box = 16;  // keys of a TMA box: what divides a page, as far as a tile has
   while (box < kKeys && kv.page_size % (2 * box) == 0) box *= 2;
   const unsigned long long rows = static_cast<unsigned long long>(kv.n_pages) * kv.n_kv_heads * kv.page_size;
@@ -823,7 +880,8 @@ e3_status launch_prompt_tc(const void* Q, const e3_kv_layer& kv, PromptGeom g, i
                               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     E3_REQUIRE(r == CUDA_SUCCESS, E3_ERR_INVALID_ARG, "prompt_attn: cuTensorMapEncodeTiled rejected Q (%d)", static_cast<int>(r));
   }
-  const auto launch = kv.head_dim == 128 ? launch_tc<128> : launch_tc<64>;
+  const auto launch = kv.head_dim == 128 ? (folds ? launch_tc<128, true> : launch_tc<128, false>)
+                                         : (folds ? launch_tc<64, true> : launch_tc<64, false>);
   const cudaError_t e = launch(Q, mq, q_box, mk, mv, kv, g, box, sm_scale, O, lse, dev_err, ws_o, ws_ml, ws_border, s);
   return e == cudaSuccess ? E3_OK : cuda_status(e, "prompt_tc kernels");
 }

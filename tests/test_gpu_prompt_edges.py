@@ -112,12 +112,15 @@ def long_inputs(seed, H, KVH, hd, rows, ctx, dt, page=64, n=5, zeros=True):
     return d
 
 
-def check_long(d, O, lse, adds, heads=None):
+def check_long(d, O, lse, adds, heads=None, exact=False):
     """64-bit softmax over the pages' slots, each counted as often as a row sees it.  `adds(keys)` bounds the error of a sum of
-    one sign, relative: it is added to the tolerance of test_gpu_prompt, once for the values' sum and once for the weights'."""
+    one sign, relative: it is added to the tolerance of test_gpu_prompt, once for the values' sum and once for the weights'.
+    exact: the weights are 1, which no rounding changes."""
     O, lse = host(O).astype(np.float64), host(lse).astype(np.float64)
     G, page, scale = d["H"] // d["KVH"], d["page"], 1 / math.sqrt(d["hd"])
     w_err, half = (2.0 ** -8, 2.0 ** -8) if d["dt"] == "bf16" else (2.0 ** -20, 2.0 ** -24)
+    if exact:
+        w_err = 0.0
     worst = 0.0
     for b in range(d["B"]):
         for r in range(d["rows"][b]):
@@ -163,3 +166,50 @@ def test_prompt_attn_fp32_long_sums(H, KVH, hd, rows, ctx, zeros):
     torch.cuda.synchronize()
     assert int(err.item()) == 0 and torch.equal(O, O2) and torch.equal(lse, lse2)
     check_long(d, O, lse, adds_fp32, heads=None if H < 10 else (0, 7, H - 1))
+
+
+def adds_bf16(keys):
+    """The tensor core sums 32768 keys at most, 16 a product, and cuts the sum off with each of up to four additions of a
+    product, by one unit 2^-23 at most; then fp32 sums of these and of the steps' weights."""
+    steps = -(-keys // 64)
+    return (min(steps, 512) * 16 + min(steps, 512) // 2 + steps // 512) * 2.0 ** -23 if steps else 0.0
+
+
+@pytest.mark.parametrize("H,KVH,hd,rows,ctx,zeros", [
+    (152, 152, 128, [1], [1 << 20], True),             # whole items in a call that is cut
+    (152, 152, 64, [3], [1 << 22], True),
+    (152, 152, 128, [300], [33000], False),            # two waves, diagonals behind what has left tensor memory
+    (2433, 2433, 64, [1], [40000], True),              # a call that is not cut
+    (2433, 2433, 64, [1], [70000], False),
+    (8, 1, 128, [5], [152 * 40000], True),             # one item in 152 parts, each longer than 32768 keys
+    (8, 2, 128, [5, 40], [152 * 30000, 90001], False),
+    (16, 2, 64, [1, 1], [40000, 20000], False)])
+def test_prompt_attn_bf16_long_sums(H, KVH, hd, rows, ctx, zeros):
+    """Contexts of tens of thousands to millions of keys, V of one sign."""
+    d = long_inputs(H + hd, H, KVH, hd, rows, ctx, "bf16", zeros=zeros)
+    O, lse, err = call(d)
+    O2, lse2, _ = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(O, O2) and torch.equal(lse, lse2)
+    if max(rows) > 50:  # (a sample of the rows)
+        d = dict(d, start=d["start"] + rows[0] - 5, ctx=[ctx[0] + rows[0] - 5], rows=[5], B=1)
+    check_long(d, O, lse, adds_bf16, heads=None if H < 10 else (0, 7, H - 1), exact=zeros)
+
+
+@pytest.mark.parametrize("H,KVH,hd,ctx", [(152, 152, 64, 70000), (2433, 2433, 64, 40000), (4, 1, 128, 152 * 33000)])
+def test_prompt_attn_bf16_long_sums_keep_what_they_have_met(H, KVH, hd, ctx):
+    """A NaN in V of an early key reaches o behind the folded sums; late maxima move the base over them."""
+    d = long_inputs(H, H, KVH, hd, [2], [ctx], "bf16", n=8)
+    d["Q"][:] = 1.0
+    d["pt"][0] = np.minimum(np.arange(d["pt"].shape[1]) * 8 // d["pt"].shape[1], 7)  # the pages one after another, repeated
+    d["k"] = synth.to_bf16_f32((np.linspace(-1.0, 1.0, 8)[:, None, None, None] + 0.05 * d["k"]).astype(np.float32))
+    O, lse, err = call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check_long(d, O, lse, adds_bf16, heads=None if H < 10 else (0, 7, H - 1))
+    d["v"][0, :, 5, 3] = np.nan
+    O2, lse2, _ = call(d)
+    torch.cuda.synchronize()
+    o = host(O2)
+    assert np.isnan(o[..., 3]).all() and torch.equal(lse, lse2)
+    assert np.array_equal(np.delete(o, 3, -1), np.delete(host(O), 3, -1))
