@@ -45,6 +45,9 @@ constexpr int kCodeB = kKeys * kHD;   // bytes of a tile's codes, per operand
 constexpr int kSlots = 3;              // tiles of K's codes in shared memory
 constexpr int kTailRing = 4;          // tiles of tree nodes whose factors are kept (three are in flight at most)
 constexpr int kExpRing = 8;           // tiles whose exponents are kept
+// Tiles of a part whose products tensor memory sums up.  The tensor core cuts a sum off where it adds to it: V of one sign
+// lost 0.6% of o in a part of 1048576 keys, 2.6% in one of 4194304.  Longer sums go on in fp32 in the part's record.
+constexpr int kFold = 256;
 // Warpgroups: 0 = producer and issuers, 1 and 2 = softmax, 3 = dequantizers.  Registers move from
 // the others to the softmax groups; launch_tc checks that the launch brings the sum.
 constexpr int kThreads = 512;
@@ -514,7 +517,49 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
         const int words = (g.R + 63) >> 6;
         const uint64_t* mrow = mask + (static_cast<size_t>(p.b) * g.R + node) * words;
         bool begun = false;
+        const size_t rec = static_cast<size_t>(p.b) * Qn + p.pq + cta;  // the part's record
+        const int rrow = grp * kRows + r;
+        // The row's sums so far go to the record, with their base and the weights' sum, and begin again; at the part's end
+        // what has gone there comes back.
+        auto fold = [&](bool more, bool end) {
+          float4* sum = reinterpret_cast<float4*>(ws_o + rec * (RT * kRows * kHD)) + rrow;
+          float2* ml = ws_ml + rec * (RT * kRows) + rrow;
+          const float2 old = more ? *ml : make_float2(m, 0.0f);
+          const float f = old.y != 0.0f ? ex2(old.x - m) : 0.0f;  // (0: no key so far)
+          l = fmaf(old.y, f, l);
+          if (!end) {
+            *ml = make_float2(m, l);
+            l = 0.0f;
+          }
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {
+            uint32_t z[16];
+            tmem_ld16(tO + 16 * k, z);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              float4& to = sum[(4 * k + j) * (RT * kRows)];
+              float4 y = more ? to : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              y = make_float4(fmaf(y.x, f, __uint_as_float(z[4 * j])), fmaf(y.y, f, __uint_as_float(z[4 * j + 1])),
+                              fmaf(y.z, f, __uint_as_float(z[4 * j + 2])), fmaf(y.w, f, __uint_as_float(z[4 * j + 3])));
+              if (!end) {
+                to = y;
+                y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              }
+              z[4 * j] = __float_as_uint(y.x), z[4 * j + 1] = __float_as_uint(y.y);
+              z[4 * j + 2] = __float_as_uint(y.z), z[4 * j + 3] = __float_as_uint(y.w);
+            }
+            tmem_st16(tO + 16 * k, z);
+          }
+          tmem_st_wait();
+        };
         for (int x = p.x0; live && x < p.x1; ++x, ++T) {
+          if (x > p.x0 && (x - p.x0) % kFold == 0) {
+            // (the next step's scores came behind the product of the step before the last, of which o_step's phase tells then)
+            live = warp_wait(&s_full[2 * grp + (n_step & 1)], (n_step >> 1) & 1, abort) && warp_wait(&o_step[grp], (n_step - 1) & 1, abort);
+            if (!live) break;
+            fence_after();
+            fold(x - p.x0 > kFold, false);
+          }
           const bool nodes = x >= p.NT;
           const int left = p.left(g, x), halves = left > kStep ? 2 : 1;
           const bool all = !nodes && left >= kKeys;  // every row sees all of the tile
@@ -664,9 +709,8 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
             if (row_ok && wd + h < words)
               poison |= (mrow[wd + h] & (bad[2 * h] | (static_cast<uint64_t>(bad[2 * h + 1]) << 32))) != 0ull;
         }
+        if (done.x1 - done.x0 > kFold) fold(true, true);
         // the part's record: o normalized by its own sum, the base and the sum
-        const size_t rec = static_cast<size_t>(done.b) * Qn + done.pq + cta;
-        const int rrow = grp * kRows + r;
         if (q_bad && l != 0.0f) l = __int_as_float(0x7FC00000);  // (0: it has seen no key of the part, which leaves none)
         const float inv = poison ? __int_as_float(0x7FC00000) : l != 0.0f ? 1.0f / l : 0.0f;
         float4* dst = reinterpret_cast<float4*>(ws_o + rec * (RT * kRows * kHD)) + rrow;

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import kv8_ref
 from gpu_util import host
 
 pytestmark = pytest.mark.gpu
@@ -36,3 +37,76 @@ def test_verify_attn8_bad_query_row_that_sees_nothing(R, G, hd):
     for b, i in bad[2:]:
         O[b, i], lse[b, i] = host(O2)[b, i], host(lse2)[b, i]
     attn_check(d, torch.from_numpy(O), torch.from_numpy(lse))
+
+
+def long_inputs(seed, B, R, H, KVH, hd, lens, page=64, n=5, late=False):
+    """Prefixes of any length over n pages that the tables name again and again; V of one sign, so that nothing of what a sum
+    loses is lost in cancellation.  late: the pages one after another, with ever larger scores."""
+    rng = np.random.default_rng(seed)
+    d = attn_inputs(seed, B, R, H, KVH, hd, [1] * B, page, 16, spread=0.5)
+    k = (rng.integers(0x20, 0x38, (n, KVH, page, hd)) + 128 * rng.integers(0, 2, (n, KVH, page, hd))).astype(np.uint8)
+    v = rng.integers(0x38, 0x40, (n, KVH, page, hd)).astype(np.uint8)
+    exps = [rng.integers(-1, 2, (n, KVH, page // 16)).astype(np.int8) for _ in range(2)]
+    m = -(-max(lens) // page)
+    at = np.arange(m)[None] + np.arange(B)[:, None]
+    pt = np.minimum(np.arange(m) * n // m, n - 1)[None].repeat(B, 0) if late else at % n
+    if late:  # K along Q's rows, which are positive, from page to page
+        d["Q"] = np.abs(d["Q"])
+        k = (rng.integers(0x28, 0x30, (n, KVH, page, hd)) + 128 * (np.arange(n) < n // 2)[:, None, None, None]).astype(np.uint8)
+        exps[0] = np.broadcast_to(np.abs(np.arange(n) - n // 2)[:, None, None] // 2, exps[0].shape).astype(np.int8).copy()
+    d.update(lens=list(lens), n=n, pt=pt.astype(np.int32), kv=[(k, exps[0]), (v, exps[1])], tail=[d["tail"][0], np.abs(d["tail"][1])])
+    return d
+
+
+def check_long(d, O, lse, adds, heads, rows):
+    """64-bit softmax over the pages' slots, each counted as often as a row sees it, and the nodes.  `adds(keys)` bounds the
+    errors of the values' and of the weights' sums, relative, which join the tolerances of test_gpu_kv8."""
+    O, lse = host(O).astype(np.float64), host(lse).astype(np.float64)
+    page, R, G, scale = d["page"], d["R"], d["H"] // d["KVH"], 1 / np.sqrt(d["hd"])
+    for b in range(d["B"]):
+        keys = d["lens"][b]
+        full, rest = divmod(keys, page)
+        count = np.bincount(d["pt"][b, :full], minlength=d["n"])[:, None] * np.ones(page)
+        if rest:
+            count[d["pt"][b, full], :rest] += 1
+        j = np.arange(R)
+        lost_o, lost_l = adds(keys)
+        for h in heads:
+            k, v = (kv8_ref.decode(c[:, h // G], np.repeat(e[:, h // G].astype(np.float64), d["block"], -1)[..., None]).reshape(-1, d["hd"])
+                    for c, e in d["kv"])
+            tk, tv = (t[d["tpt"][b, j // page], h // G, j % page].astype(np.float64) for t in d["tail"])
+            k, v = np.concatenate([k, tk]), np.concatenate([v, tv])
+            for r in rows:
+                q = d["Q"][b, r, h].astype(np.float64)
+                c = np.concatenate([count.ravel(), d["see"][b, r].astype(float)])
+                s, big = k @ q * scale, (np.abs(k) @ np.abs(q) * scale)[c > 0].max()
+                m = s[c > 0].max()
+                p = c * np.exp(s - m)
+                z = p.sum()
+                o, l = p @ v / z, m + np.log(z)
+                ds = 2.0 ** -18 * (big + 1.0)
+                assert abs(lse[b, r, h] - l) <= ds + lost_l + 2.0 ** -21 * abs(l), (b, r, h, lse[b, r, h] - l)
+                e = (2.0 ** -8 + 2 * ds + lost_o + lost_l) * o
+                bad = np.abs(O[b, r, h] - o) - (e + 2.0 ** -8 * (o + e))
+                assert np.all(bad <= 0), (b, r, h, (np.abs(O[b, r, h] - o) / o).max())
+
+
+def adds_tc(keys):
+    """32768 keys at most in tensor memory, 16 a product, each cutting the sum off up to four times by at most a unit 2^-23;
+    the weights' sum in steps of 64 keys; then fp32 sums of these."""
+    n = min(keys, 32768)
+    return (n / 4 + keys / 32768) * 2.0 ** -23, (n / 64 + keys / 32768) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("B,R,H,KVH,lens,late", [
+    (1, 33, 152, 152, [1 << 20], False), (1, 200, 152, 152, [1 << 22], False),     # a part of every CTA; both widths of the tile
+    (1, 33, 152, 152, [100001], True), (1, 150, 152, 152, [70000], True),          # late maxima over what has left tensor memory
+    (2, 61, 32, 8, [2000000, 1300011], False),                                     # parts that begin and end inside a prefix
+    (3, 40, 160, 80, [33000, 0, 90000], False)])
+def test_verify_attn8_many_rows_long_sums(B, R, H, KVH, lens, late):
+    d = long_inputs(R + H, B, R, H, KVH, 128, lens, late=late)
+    O, lse, err = attn_call(d)
+    O2, lse2, _ = attn_call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(O, O2) and torch.equal(lse, lse2)
+    check_long(d, O, lse, adds_tc, heads=(0, H // 3, H - 1), rows=(0, R // 2, R - 1))
