@@ -39,6 +39,9 @@ namespace {
 
 constexpr int kStages = 4;  // granules in a warp's ring
 constexpr int kStep = 2;    // granules of a step
+// Granules of a part that are summed up in the accumulators.  The tensor core cuts a sum off where it adds to it: V of one sign
+// lost 0.6% of o in a part of 1048576 keys.  Longer sums go on in the part's record.
+constexpr int kFold = 2048;
 
 template <int HD>
 struct V8Cfg {
@@ -194,6 +197,47 @@ verify8_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
         for (int j = 0; j < MT; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[nr][j][e] *= f;
+    };
+    // The part's record: o normalized by its own sum, the base and the sum.  more: it holds the sums of earlier granules.
+    auto leave = [&](bool more) {
+      const float o_unit = pow2n(unit);
+      float2 old[NR][2];
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int rr = 8 * nr + 2 * tq + e;
+          old[nr][e] = make_float2(0.0f, 0.0f);
+          if (more && rg * ROWS + rr < g.G * g.R) old[nr][e] = ws_ml[(static_cast<size_t>(b) * Qn + pq + worker) * ROWS + rr];
+        }
+      __syncwarp();
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float s = l[nr][e];
+          s += __shfl_xor_sync(0xFFFFFFFFu, s, 4);
+          s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
+          s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
+          const int rr = 8 * nr + 2 * tq + e;
+          if (rg * ROWS + rr < g.G * g.R) {
+            const size_t rec = (static_cast<size_t>(b) * Qn + pq + worker) * ROWS + rr;
+            const float before = old[nr][e].y != 0.0f ? old[nr][e].y * ex2(old[nr][e].x - m[nr][e]) : 0.0f;
+            s += before;
+            // (poison is the same in all threads of a row: one mask word and one badk per granule)
+            const float inv = poison[nr][e] ? __int_as_float(0x7FC00000) : s != 0.0f ? 1.0f / s : 0.0f, f = before * inv;
+            float* dst = ws_o + rec * HD + DV * gq;
+#pragma unroll
+            for (int j = 0; j < MT; j += 2) {
+              float4* to = reinterpret_cast<float4*>(dst + 2 * j);
+              const float4 x = more ? *to : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              *to = make_float4(fmaf(x.x, f, o[nr][j][e] * inv * o_unit), fmaf(x.y, f, o[nr][j][2 + e] * inv * o_unit),
+                                fmaf(x.z, f, o[nr][j + 1][e] * inv * o_unit), fmaf(x.w, f, o[nr][j + 1][2 + e] * inv * o_unit));
+            }
+            if (gq == 0) ws_ml[rec] = make_float2(m[nr][e], s);
+          }
+        }
+      __syncwarp();
     };
     // running softmax over the scores of NGR granules (already scaled, -Inf where unseen):
     // sc[.][nr] holds keys gq (0, 1) and gq + 8 (2, 3) of query rows 2 tq, 2 tq + 1;
@@ -382,6 +426,15 @@ verify8_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
         __syncwarp();  // the stages may be refilled
 #pragma unroll
         for (int u = 0; u < kStep; ++u) ke[u] = ke_next[u], ve[u] = ve_next[u];
+        if ((i + kStep) % kFold == 0 && i + kStep < ngran) {
+          leave(i >= kFold);
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j) o[nr][j][0] = o[nr][j][1] = o[nr][j][2] = o[nr][j][3] = 0.0f;
+            l[nr][0] = l[nr][1] = 0.0f;
+          }
+        }
       }
     }
 
@@ -527,30 +580,7 @@ verify8_mma_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ 
       }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
-    // this part's record: o normalized by its own sum, the base and the sum
-    const float o_unit = pow2n(unit);
-#pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float s = l[nr][e];
-        s += __shfl_xor_sync(0xFFFFFFFFu, s, 4);
-        s += __shfl_xor_sync(0xFFFFFFFFu, s, 8);
-        s += __shfl_xor_sync(0xFFFFFFFFu, s, 16);
-        const int rr = 8 * nr + 2 * tq + e;
-        if (rg * ROWS + rr < rows) {
-          const size_t rec = (static_cast<size_t>(b) * Qn + pq + worker) * ROWS + rr;
-          // (poison is the same in all threads of a row: one mask word and one badk per granule)
-          const float inv = poison[nr][e] ? __int_as_float(0x7FC00000) : s != 0.0f ? 1.0f / s : 0.0f;
-          float* dst = ws_o + rec * HD + DV * gq;
-#pragma unroll
-          for (int j = 0; j < MT; j += 2)
-            *reinterpret_cast<float4*>(dst + 2 * j) =
-                make_float4(o[nr][j][e] * inv * o_unit, o[nr][j][2 + e] * inv * o_unit, o[nr][j + 1][e] * inv * o_unit,
-                            o[nr][j + 1][2 + e] * inv * o_unit);
-          if (gq == 0) ws_ml[rec] = make_float2(m[nr][e], s);
-        }
-      }
+    leave(ngran > kFold);
     if (lane == 0) {
       int32_t* e = ends + 2 * (static_cast<size_t>(b) * Qn + pq);
       if (x0 == 0) e[0] = worker;

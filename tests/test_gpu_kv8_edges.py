@@ -110,3 +110,23 @@ def test_verify_attn8_many_rows_long_sums(B, R, H, KVH, lens, late):
     torch.cuda.synchronize()
     assert int(err.item()) == 0 and torch.equal(O, O2) and torch.equal(lse, lse2)
     check_long(d, O, lse, adds_tc, heads=(0, H // 3, H - 1), rows=(0, R // 2, R - 1))
+
+
+def adds_granules(keys):
+    """The same in the granule kernel; a lane sums its two keys of 16 one after another."""
+    n = min(keys, 32768)
+    return (n / 4 + keys / 32768) * 2.0 ** -23, (n / 8 + keys / 32768) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("B,R,H,KVH,hd,lens,late", [
+    (1, 1, 1824, 1824, 128, [1 << 20], False), (1, 16, 1216, 1216, 128, [1 << 20], False),     # a part of every warp
+    (1, 1, 2432, 2432, 64, [1 << 20], False), (1, 40, 304, 304, 64, [1 << 20], False),
+    (1, 1, 1824, 1824, 128, [100001], True), (1, 9, 1216, 1216, 128, [70000], True), (1, 2, 2432, 2432, 64, [100000], True),
+    (2, 5, 480, 80, 128, [1000000, 777777], False), (3, 3, 800, 400, 64, [400000, 0, 290000], False)])  # parts that begin and end inside
+def test_verify_attn8_few_rows_long_sums(B, R, H, KVH, hd, lens, late):
+    d = long_inputs(R + H, B, R, H, KVH, hd, lens, late=late)
+    O, lse, err = attn_call(d)
+    O2, lse2, _ = attn_call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and torch.equal(O, O2) and torch.equal(lse, lse2)
+    check_long(d, O, lse, adds_granules, heads=(0, H // 3, H - 1), rows=sorted({0, R // 2, R - 1}))
