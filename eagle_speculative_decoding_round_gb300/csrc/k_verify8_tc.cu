@@ -11,10 +11,12 @@
 //   dequantizers (4 warps) V's codes -> bf16 in 128-byte-swizzled shared memory; the
 //                          tree nodes' rows
 //   softmax (RT x 4 warps) one thread per row: exponentials against the base so far, P over S
-// K is never converted: codes are the operand.  A row of Q, scaled by a power of two to [2^6, 2^8),
-// is the sum of two e4m3 parts, exactly down to 2^-10 of its largest value (a bf16 value has
-// eight significant bits, a part four; below that to 2^-18 of it): S = (q1 + q2) K is two
-// products at twice the rate of 16-bit ones.  Nodes' K is split the same way, four products.
+// K is never converted: codes are the operand.  A row of Q, scaled by a power of two so that its
+// largest value lies in (224, 448], is the sum of two e4m3 parts: a bf16 value has eight significant
+// bits, a part four, and the second's last is 2^-9, so that values from 2^-2 on, 2^-9 of the largest,
+// are exact, and smaller ones are off by 2^-10, 2^-17 of it.  S = (q1 + q2) K is two products at
+// twice the rate of 16-bit ones.  Nodes' K is split the same way, four products; its power is even (its
+// root meets a score twice, below), so that the largest is above 112: 2^-8 and 2^-16 of it.
 // K's exponents and Q's power meet the scores.  V's codes become bf16 values, exactly, with their
 // scale on them, as the nodes' V is: a shift and one product by a power of two for each pair; the
 // weights are good to 2^-8 (bf16).
@@ -82,9 +84,10 @@ __device__ __forceinline__ void ask_rows(const __nv_bfloat16* from, int own, uns
                  : "memory");
   }
 }
-// Those rows in two e4m3 parts, in place (half a warp has a whole row in hand), each row's largest magnitude scaled to
-// [2^6, 2^8) by a power of two with an even exponent: returns the exponent that takes the lane's row back, or 1000 for a
-// row with a NaN or an Inf, which becomes zeros.
+// Those rows in two e4m3 parts, in place (half a warp has a whole row in hand), each row divided by the smallest power of
+// two, EVEN: with an even exponent, that leaves its largest magnitude within 448.  Returns the lane's row's exponent, or 1000
+// for a row with a NaN or an Inf, which becomes zeros.
+template <bool EVEN>
 __device__ __forceinline__ int rows_to_parts(unsigned char* hi, unsigned char* lo, int row0, int lane) {
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
@@ -101,8 +104,9 @@ __device__ __forceinline__ int rows_to_parts(unsigned char* hi, unsigned char* l
     top = max(top & 0xFFFFu, top >> 16);
   }
   const bool odd = top >= 0x7F80u;
-  const int ex = (min(static_cast<int>(max(top >> 7, 1u)), 254) - 127) & ~1;
-  // half a warp to a row for the parts; 2^(6 - ex) in two factors (it reaches 2^132 for a row of zeros)
+  int ex = min(static_cast<int>(max(top >> 7, 1u)), 254) - 127 - 8 + ((top & 0x7Fu) > 0x60u ? 1 : 0);  // (448 = 1.75 * 2^8)
+  if (EVEN) ex = (ex + 1) & ~1;
+  // half a warp to a row for the parts; 2^-ex in two factors (it reaches 2^134 for a row of zeros)
 #pragma unroll 1
   for (int i0 = 0; i0 < 16; i0 += 4) {
     uint4 x[4];
@@ -114,7 +118,7 @@ __device__ __forceinline__ int rows_to_parts(unsigned char* hi, unsigned char* l
     __syncwarp();  // (the rows have been read)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int e = __shfl_sync(0xFFFFFFFFu, odd ? 1000 : 6 - ex, 2 * (i0 + i) + (lane >> 4)), e0 = e / 2;
+      const int e = __shfl_sync(0xFFFFFFFFu, odd ? 1000 : -ex, 2 * (i0 + i) + (lane >> 4)), e0 = e / 2;
       const float f0 = pow2n(e == 1000 ? 0 : e0), f1 = pow2n(e == 1000 ? 0 : e - e0);
       const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
       uint32_t h[4], l[4];
@@ -132,7 +136,7 @@ __device__ __forceinline__ int rows_to_parts(unsigned char* hi, unsigned char* l
       *reinterpret_cast<uint2*>(lo + at) = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
     }
   }
-  return odd ? 1000 : ex - 6;
+  return odd ? 1000 : ex;
 }
 
 // The steps of a part's tiles: 64 keys each, one for a tile with 64 keys or fewer.
@@ -451,7 +455,7 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
           ask_rows(static_cast<const __nv_bfloat16*>(tail.k), own, sK + slot * kCodeB, sK + second * kCodeB, dw * 32, lane);
           unsigned char* slab = dst + dw * 32 * 128;
           bring_rows(static_cast<const __nv_bfloat16*>(tail.v), own, slab, lane);
-          const int ex = rows_to_parts(sK + slot * kCodeB, sK + second * kCodeB, dw * 32, lane);
+          const int ex = rows_to_parts<true>(sK + slot * kCodeB, sK + second * kCodeB, dw * 32, lane);
           s_fac[fac * kKeys + dw * 32 + lane] = ex == 1000 ? __int_as_float(0x7FC00000) : pow2f(ex / 2);
           const uint32_t top = row_top(slab, lane);
           const uint32_t bad = __ballot_sync(0xFFFFFFFFu, top >= 0x7F80u);
@@ -501,7 +505,7 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
       do {
         int node;
         const bool row_ok = row_of(p, &node) >= 0;
-        const int q_ex = rows_to_parts(q0, q0 + kCodeB, quarter * 32, lane);
+        const int q_ex = rows_to_parts<false>(q0, q0 + kCodeB, quarter * 32, lane);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) bar_arrive(&q_full[grp]);

@@ -607,13 +607,14 @@ E3_API e3_status kv8_read(const e3_kv8_layer* layers, const e3_kv_layer* dst, in
  * tree_verify_attn8: tree_verify_attn over a prefix held in 8 bits; arguments, tail,
  * masks, rows without a key and errors as tree_verify_attn4.
  * Arithmetic: products exact but for the weights, which are good to 2^-8, sums in fp32, off by
- *   at most 2^-10 of the magnitudes' (the tensor core cuts off what it adds up).  Values of V up to 2^85 in magnitude cannot overflow them (up to 2^100 where max_kv_len is
- *   below 2^18).  Up to 32 query rows per KV
- *   head, and for heads of 64: Q's values below 2^-24 of their row's largest lose bits, and
- *   so do weights below 2^-21 of their row's largest in units of the largest V scale of the
- *   request: blocks whose V scale is 2^20 below it count less exactly.  With more rows: Q's
- *   values below 2^-10 of their row's largest, and the nodes' K below 2^-10 of theirs, lose
- *   bits: they are good to 2^-18 of that largest value; V's scales lose none.
+ *   at most 2^-10 of the magnitudes' (the tensor core cuts off what it adds up).
+ *   Values of V up to 2^85 in magnitude cannot overflow them (up to 2^100 where max_kv_len is
+ *   below 2^18).  Up to 32 query rows per KV head, and for heads of 64: Q's values below 2^-24
+ *   of their row's largest lose bits, and so do weights below 2^-21 of their row's largest in
+ *   units of the largest V scale of the request: blocks whose V scale is 2^20 below it count
+ *   less exactly.  With more rows: Q's values below 2^-9 of their row's largest are good to
+ *   2^-17 of it, and the nodes' K below 2^-8 of theirs to 2^-16; larger ones, and V's scales,
+ *   lose nothing.
  * Scratch: eagle3_verify8_workspace_bytes(...) bytes (0 for sizes that the call refuses),
  *   16-byte aligned; calls that may overlap on the GPU need scratch of their own.
  * ------------------------------------------------------------------------- */

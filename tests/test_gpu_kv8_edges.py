@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import kv8_ref
+from eagle_speculative_decoding_round_gb300 import synth
 from gpu_util import host
 
 pytestmark = pytest.mark.gpu
@@ -130,3 +131,54 @@ def test_verify_attn8_few_rows_long_sums(B, R, H, KVH, hd, lens, late):
     torch.cuda.synchronize()
     assert int(err.item()) == 0 and torch.equal(O, O2) and torch.equal(lse, lse2)
     check_long(d, O, lse, adds_granules, heads=(0, H // 3, H - 1), rows=sorted({0, R // 2, R - 1}))
+
+
+@pytest.mark.parametrize("top", [1.0, 1.75, 1.7578125, 1.9921875])
+@pytest.mark.parametrize("R,G", [(40, 1), (40, 4), (6, 4)])
+def test_verify_attn8_rows_of_uneven_values(R, G, top):
+    """Q and the nodes' K with one large dim and the others far below it, each against keys, or queries, that are large in the
+    others.  With more than 32 rows Q's values below 2^-9 of their row's largest are off by up to 2^-17 of it, the nodes' K
+    below 2^-8 of theirs by 2^-16: times what they meet, that joins the scores' error.  Q's others from 2^-9 on are exact."""
+    P, hd = 150, 128
+    for f in (6, 7, 8, 9, 10, 12, 14):
+        d = attn_inputs(R + f, 1, R, 2 * G, 2, hd, [P], 64, 16)
+        rng = np.random.default_rng(f)
+        q = rng.uniform(1.0, 1.99, d["Q"].shape) * 2.0 ** -f
+        q[..., 0] = top
+        d["Q"] = synth.to_bf16_f32(q.astype(np.float32))
+        d["kv"][0][0][..., 0] = 0                                    # (K's codes positive, none in Q's large dim)
+        d["kv"][0][0][..., 1:] = np.minimum(d["kv"][0][0][..., 1:] & 0x7F, 0x70)
+        d["kv"][0][1][:] = f - 10
+        tk = rng.uniform(-1.99, 1.99, d["tail"][0].shape) * 2.0 ** -f
+        tk[..., 1] = top
+        d["tail"][0] = synth.to_bf16_f32(tk.astype(np.float32))
+        O, lse, err = attn_call(d)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        O, lse = host(O).astype(np.float64), host(lse).astype(np.float64)
+        t, j, scale = np.arange(P), np.arange(R), 1 / np.sqrt(hd)
+        pg = d["pt"][0, t // 64]
+        k, v = (kv8_ref.decode(d["kv"][w][0][pg, :, t % 64], d["kv"][w][1][pg, :, t % 64 // 16].astype(np.float64)[..., None])
+                for w in range(2))
+        k, v = (np.concatenate([a, n[d["tpt"][0, j // 64], :, j % 64].astype(np.float64)]) for a, n in zip((k, v), d["tail"]))
+        many = R * G > 32
+        for h in range(2 * G):
+            q, kh, vh = d["Q"][0, :, h].astype(np.float64), k[:, h // G], v[:, h // G]
+            seen = np.concatenate([np.ones((R, P), bool), d["see"][0]], 1)
+            qm, km = np.abs(q).max(1, keepdims=True), np.abs(kh).max(1, keepdims=True)
+            eq = np.where(many & (np.abs(q) < 2.0 ** -9 * qm), 2.0 ** -17 * qm, 0.0)
+            ek = np.where(many & (np.abs(kh) < 2.0 ** -8 * km) & (np.arange(P + R) >= P)[:, None], 2.0 ** -16 * km, 0.0)
+            s = np.where(seen, q @ kh.T * scale, -np.inf)
+            big = np.where(seen, np.abs(q) @ np.abs(kh).T * scale, 0.0).max(1)
+            off = np.where(seen, (eq @ np.abs(kh).T + (np.abs(q) + eq) @ ek.T) * scale, 0.0).max(1)
+            m = s.max(1, keepdims=True)
+            p = np.exp(s - m)
+            z = p.sum(1, keepdims=True)
+            o, mag, l = p @ vh / z, p @ np.abs(vh) / z, (m + np.log(z))[:, 0]
+            ds = 2.0 ** -18 * (big + 1.0) + off
+            assert np.all(np.abs(lse[0, :, h] - l) <= ds + 2.0 ** -21 * np.abs(l)), (f, h, (np.abs(lse[0, :, h] - l) / ds).max())
+            grow = np.expm1(2 * ds)[:, None]  # (the scores' error is not small against 1 everywhere)
+            codes = np.abs(vh[:P]) * 2.0 ** (d["kv"][1][1].max() - d["kv"][1][1][pg, h // G, t % 64 // 16].astype(np.float64))[:, None]
+            e = (2.0 ** -8 + grow) * mag + 2.0 ** -32 * codes.sum(0)[None]
+            bad = np.abs(O[0, :, h] - o) - (e + 2.0 ** -8 * (np.abs(o) + e))
+            assert np.all(bad <= 0), (f, h, bad.max())
