@@ -648,7 +648,7 @@ E3_API size_t eagle3_verify8_workspace_bytes(int B, int R, int n_q_heads, int n_
  * [0, n_total), or slots beyond max_pages set E3_DEV_ERR_CAPACITY and leave the request's
  * outputs unwritten; a page id out of range sets it and makes them unspecified.  Rows of
  * two requests must not overlap.
- * Arithmetic: bf16: products in bf16 with fp32 sums, weights good to 2^-9 and summed
+ * Arithmetic: bf16: products in bf16 with fp32 sums, weights good to 2^-8 and summed
  *   before that rounding, V up to 2^90 in magnitude cannot overflow the sums, which are off
  *   by at most 2^-10 of the magnitudes' (the tensor core cuts off what it adds up); fp32: fp32
  *   throughout, a sum over n keys off by at most (128 + sqrt(n) / 2) 2^-24 of that of the magnitudes.
