@@ -1,8 +1,20 @@
 // capi_checks.cuh -- argument checks that several files of C entry points share.
 #pragma once
+#include <initializer_list>
+
 #include "e3_common.cuh"
 
 namespace e3 {
+
+// (a pointer off its elements' grid would fault on the device)
+inline bool on_grid(const void* p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+// Arrays of 32-bit elements: lengths, row numbers, page tables, statistics, the error word (null ones pass).
+inline bool words_on_grid(std::initializer_list<const void*> arrays) {
+  for (const void* p : arrays)
+    if (!on_grid(p, 4)) return false;
+  return true;
+}
 
 inline e3_status check_kv16(const e3_kv_layer* kv, const char* fn, const char* what) {
   E3_REQUIRE(kv != nullptr, E3_ERR_INVALID_ARG, "%s: null %s descriptor", fn, what);
@@ -16,13 +28,11 @@ inline e3_status check_kv16(const e3_kv_layer* kv, const char* fn, const char* w
   E3_REQUIRE(kv->head_dim >= 32 && kv->head_dim <= 256 && kv->head_dim % 32 == 0, E3_ERR_SHAPE,
              "%s: %s head_dim %d must be a multiple of 32 in [32, 256]", fn, what, kv->head_dim);
   E3_REQUIRE(aligned16(kv->k) && aligned16(kv->v), E3_ERR_INVALID_ARG, "%s: %s k/v not 16-byte aligned", fn, what);
+  E3_REQUIRE(words_on_grid({kv->page_table}), E3_ERR_INVALID_ARG, "%s: %s page_table not 4-byte aligned", fn, what);
   E3_REQUIRE((kv->flags & ~(E3_KV_PREFIX_STABLE | E3_KV_SELFTEST_STALL)) == 0, E3_ERR_INVALID_ARG,
              "%s: unknown %s flags %#x", fn, what, kv->flags);
   return E3_OK;
 }
-
-// (a pointer off its elements' grid would fault in the paths for rows off the 16-byte grid)
-inline bool on_grid(const void* p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
 // B, R, heads and lengths of a tree attention call over a quantized prefix (the bounds of the call itself).
 inline bool verify_quant_sizes_ok(int B, int R, int n_q_heads, int n_kv_heads, int head_dim, int max_kv_len) {
@@ -35,7 +45,7 @@ inline bool verify_quant_sizes_ok(int B, int R, int n_q_heads, int n_kv_heads, i
 template <class Layer>
 e3_status check_verify_quant(const char* fn, const void* Q, const Layer* kv, const e3_kv_layer* tail, const int32_t* kv_len,
                              const uint64_t* mask, int B, int R, int n_q_heads, int max_kv_len, float sm_scale, const void* O,
-                             const float* lse, const void* ws) {
+                             const float* lse, const int32_t* dev_err, const void* ws) {
   const e3_status st = check_kv16(tail, fn, "tail");
   if (st != E3_OK) return st;
   E3_REQUIRE(Q && kv_len && mask && O && lse && ws, E3_ERR_INVALID_ARG, "%s: null pointer", fn);
@@ -53,6 +63,8 @@ e3_status check_verify_quant(const char* fn, const void* Q, const Layer* kv, con
              "%s: tail pages do not hold R=%d slots", fn, R);
   E3_REQUIRE(sm_scale > 0.0f && sm_scale < 1e30f, E3_ERR_INVALID_ARG, "%s: sm_scale must be > 0", fn);
   E3_REQUIRE(aligned16(Q) && aligned16(O) && aligned16(ws), E3_ERR_INVALID_ARG, "%s: Q, O, ws must be 16-byte aligned", fn);
+  E3_REQUIRE(on_grid(mask, 8) && words_on_grid({kv_len, lse, dev_err}), E3_ERR_INVALID_ARG,
+             "%s: mask, kv_len, lse or dev_err not aligned to its elements", fn);
   return E3_OK;
 }
 

@@ -20,6 +20,7 @@ static e3_status check_kv4(const e3_kv4_layer* kv, const char* fn) {
              "%s: null k/v/scale/page_table", fn);
   E3_REQUIRE(aligned16(kv->k) && aligned16(kv->v) && aligned16(kv->k_scale) && aligned16(kv->v_scale),
              E3_ERR_INVALID_ARG, "%s: 4-bit k/v/scales not 16-byte aligned", fn);
+  E3_REQUIRE(words_on_grid({kv->page_table}), E3_ERR_INVALID_ARG, "%s: page_table not 4-byte aligned", fn);
   E3_REQUIRE(kv->n_pages > 0 && kv->max_pages > 0 && kv->n_kv_heads > 0 && kv->n_kv_heads <= 65535, E3_ERR_SHAPE,
              "%s: n_pages, max_pages, n_kv_heads must be positive", fn);
   E3_REQUIRE(kv->page_size > 0 && kv->page_size % 16 == 0, E3_ERR_SHAPE, "%s: page_size %d not a multiple of 16", fn,
@@ -84,6 +85,8 @@ E3_API e3_status tree_qkv_append(const void* qkv, size_t ld, int B, int R, const
   E3_REQUIRE(qkv && Q, E3_ERR_INVALID_ARG, "%s: null pointer", fn);
   const unsigned esz = kv->dt == E3_F32 ? 4 : 2;
   E3_REQUIRE(on_grid(qkv, esz) && on_grid(Q, esz), E3_ERR_INVALID_ARG, "%s: qkv, Q not aligned to their elements", fn);
+  E3_REQUIRE(words_on_grid({n_rows, q_norm, k_norm, pos, kv_len, dev_err}), E3_ERR_INVALID_ARG,
+             "%s: n_rows, norms, pos, kv_len or dev_err not 4-byte aligned", fn);
   E3_REQUIRE(!rope || pos, E3_ERR_INVALID_ARG, "%s: a rotation needs positions", fn);
   E3_REQUIRE(B >= 1 && R >= 1 && static_cast<long long>(B) * R <= 2147483647ll, E3_ERR_SHAPE, "%s: B=%d R=%d", fn, B, R);
   E3_REQUIRE(n_q_heads >= 1 && n_q_heads <= 65535 && kv->n_kv_heads <= 65535, E3_ERR_SHAPE, "%s: n_q_heads=%d", fn, n_q_heads);
@@ -102,6 +105,8 @@ E3_API e3_status kv4_append(const e3_kv4_layer* layers, const e3_kv_layer* src, 
                             int32_t* kv_len_next, int32_t* dev_err, e3_stream_t stream) {
   clear_error();
   E3_REQUIRE(layers && src && n_rows && kv_len, E3_ERR_INVALID_ARG, "kv4_append: null pointer");
+  E3_REQUIRE(words_on_grid({rows, n_rows, kv_len, kv_len_next, dev_err}), E3_ERR_INVALID_ARG,
+             "kv4_append: rows, n_rows, kv_len, kv_len_next or dev_err not 4-byte aligned");
   E3_REQUIRE(n_add >= 0 && n_add <= 1, E3_ERR_SHAPE, "kv4_append: n_add=%d (0 or 1)", n_add);
   Kv4Layers l4;
   CompactLayers l16;
@@ -115,6 +120,7 @@ E3_API e3_status kv4_read(const e3_kv4_layer* layers, const e3_kv_layer* dst, in
                           const int32_t* first, const int32_t* n_rows, int32_t* dev_err, e3_stream_t stream) {
   clear_error();
   E3_REQUIRE(layers && dst && n_rows, E3_ERR_INVALID_ARG, "kv4_read: null pointer");
+  E3_REQUIRE(words_on_grid({first, n_rows, dev_err}), E3_ERR_INVALID_ARG, "kv4_read: first, n_rows or dev_err not 4-byte aligned");
   Kv4Layers l4;
   CompactLayers l16;
   const e3_status st = gather_layers("kv4_read", layers, dst, L, B, max_rows, &l4, &l16);
@@ -135,7 +141,7 @@ E3_API e3_status tree_verify_attn4(const void* Q, const e3_kv4_layer* kv, const 
   clear_error();
   const char* fn = "tree_verify_attn4";
   e3_status st = check_kv4(kv, fn);
-  if (st == E3_OK) st = check_verify_quant(fn, Q, kv, tail, kv_len, mask, B, R, n_q_heads, max_kv_len, sm_scale, O, lse, ws);
+  if (st == E3_OK) st = check_verify_quant(fn, Q, kv, tail, kv_len, mask, B, R, n_q_heads, max_kv_len, sm_scale, O, lse, dev_err, ws);
   if (st != E3_OK) return st;
   return launch_verify4(Q, *kv, *tail, kv_len, mask, B, R, n_q_heads, max_kv_len, sm_scale, O, lse, dev_err, ws, ws_bytes,
                         reinterpret_cast<cudaStream_t>(stream));

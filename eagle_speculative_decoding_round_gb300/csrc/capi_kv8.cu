@@ -12,6 +12,7 @@ static e3_status check_kv8(const e3_kv8_layer* kv, const char* fn) {
   E3_REQUIRE(kv->k && kv->v && kv->k_exp && kv->v_exp && kv->page_table, E3_ERR_INVALID_ARG,
              "%s: null k/v/exponents/page_table", fn);
   E3_REQUIRE(aligned16(kv->k) && aligned16(kv->v), E3_ERR_INVALID_ARG, "%s: 8-bit k/v not 16-byte aligned", fn);
+  E3_REQUIRE(words_on_grid({kv->page_table}), E3_ERR_INVALID_ARG, "%s: page_table not 4-byte aligned", fn);
   E3_REQUIRE(kv->n_pages > 0 && kv->max_pages > 0 && kv->n_kv_heads > 0 && kv->n_kv_heads <= 65535, E3_ERR_SHAPE,
              "%s: n_pages, max_pages, n_kv_heads must be positive", fn);
   E3_REQUIRE(kv->block == 16 || kv->block == 32 || kv->block == 64 || kv->block == 128, E3_ERR_SHAPE,
@@ -68,6 +69,8 @@ E3_API e3_status kv8_append(const e3_kv8_layer* layers, const e3_kv_layer* src, 
                             int32_t* kv_len_next, int32_t* dev_err, e3_stream_t stream) {
   clear_error();
   E3_REQUIRE(layers && src && n_rows && kv_len, E3_ERR_INVALID_ARG, "kv8_append: null pointer");
+  E3_REQUIRE(words_on_grid({rows, n_rows, kv_len, kv_len_next, dev_err}), E3_ERR_INVALID_ARG,
+             "kv8_append: rows, n_rows, kv_len, kv_len_next or dev_err not 4-byte aligned");
   E3_REQUIRE(n_add >= 0 && n_add <= 1, E3_ERR_SHAPE, "kv8_append: n_add=%d (0 or 1)", n_add);
   Kv8Layers l8;
   CompactLayers l16;
@@ -81,6 +84,7 @@ E3_API e3_status kv8_read(const e3_kv8_layer* layers, const e3_kv_layer* dst, in
                           const int32_t* first, const int32_t* n_rows, int32_t* dev_err, e3_stream_t stream) {
   clear_error();
   E3_REQUIRE(layers && dst && n_rows, E3_ERR_INVALID_ARG, "kv8_read: null pointer");
+  E3_REQUIRE(words_on_grid({first, n_rows, dev_err}), E3_ERR_INVALID_ARG, "kv8_read: first, n_rows or dev_err not 4-byte aligned");
   Kv8Layers l8;
   CompactLayers l16;
   const e3_status st = gather_layers8("kv8_read", layers, dst, L, B, max_rows, &l8, &l16);
@@ -101,7 +105,7 @@ E3_API e3_status tree_verify_attn8(const void* Q, const e3_kv8_layer* kv, const 
   clear_error();
   const char* fn = "tree_verify_attn8";
   e3_status st = check_kv8(kv, fn);
-  if (st == E3_OK) st = check_verify_quant(fn, Q, kv, tail, kv_len, mask, B, R, n_q_heads, max_kv_len, sm_scale, O, lse, ws);
+  if (st == E3_OK) st = check_verify_quant(fn, Q, kv, tail, kv_len, mask, B, R, n_q_heads, max_kv_len, sm_scale, O, lse, dev_err, ws);
   if (st != E3_OK) return st;
   return launch_verify8(Q, *kv, *tail, kv_len, mask, B, R, n_q_heads, max_kv_len, sm_scale, O, lse, dev_err, ws, ws_bytes,
                         reinterpret_cast<cudaStream_t>(stream));

@@ -35,7 +35,9 @@ E3_API e3_status prompt_attn(const void* Q, const int32_t* row_start, const int3
   const e3_status st = check_kv16(kv, fn, "kv");
   if (st != E3_OK) return st;
   E3_REQUIRE(Q && O && lse, E3_ERR_INVALID_ARG, "%s: null pointer", fn);
-  E3_REQUIRE(aligned16(Q) && aligned16(O) && on_grid(lse, 4), E3_ERR_INVALID_ARG, "%s: Q, O must be 16-byte aligned", fn);
+  E3_REQUIRE(aligned16(Q) && aligned16(O), E3_ERR_INVALID_ARG, "%s: Q, O must be 16-byte aligned", fn);
+  E3_REQUIRE(words_on_grid({row_start, n_rows, kv_len, lse, dev_err}), E3_ERR_INVALID_ARG,
+             "%s: row_start, n_rows, kv_len, lse or dev_err not 4-byte aligned", fn);
   E3_REQUIRE(kv->dt == E3_F32 || kv->head_dim == 64 || kv->head_dim == 128, E3_ERR_SHAPE, "%s: head_dim %d (64 or 128 in bf16)",
              fn, kv->head_dim);
   E3_REQUIRE(n_q_heads >= 1 && n_q_heads <= 65535 && n_q_heads % kv->n_kv_heads == 0, E3_ERR_SHAPE,
