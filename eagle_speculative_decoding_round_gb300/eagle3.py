@@ -350,8 +350,10 @@ def _layer_arrays(fn, layers, others, kind=e3_kv4_layer):
     # one copy of the descriptors' bytes (filling a ctypes array element by element takes longer than the launch)
     a, a16 = b"".join(layers), b"".join(others)
     n = len(layers)
-    if n and ({*map(type, layers)} != {kind} or {*map(type, others)} != {e3_kv_layer}):
-        raise TypeError(f"{fn}: {kind.__name__} and e3_kv_layer descriptors wanted")
+    # (by type, subclasses among them: e3_kv4_layer and e3_kv8_layer are of one size)
+    for kinds, want, raw in (({*map(type, layers)}, kind, a), ({*map(type, others)}, e3_kv_layer, a16)):
+        if not all(issubclass(t, want) for t in kinds) or len(raw) != n * ctypes.sizeof(want):
+            raise TypeError(f"{fn}: {kind.__name__} and e3_kv_layer descriptors wanted")
     return (kind * n).from_buffer_copy(a), (e3_kv_layer * n).from_buffer_copy(a16)
 
 
