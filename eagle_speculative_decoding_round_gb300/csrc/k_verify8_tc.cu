@@ -139,6 +139,18 @@ __device__ __forceinline__ int rows_to_parts(unsigned char* hi, unsigned char* l
   return odd ? 1000 : ex;
 }
 
+// q . k of a node whose K holds a NaN or an Inf.
+__device__ __forceinline__ float odd_score(const __nv_bfloat16* q, const __nv_bfloat16* k) {
+  float s = 0.0f;
+#pragma unroll 1
+  for (int d = 0; d < kHD; d += 2) {
+    const uint32_t a = *reinterpret_cast<const uint32_t*>(q + d), b = *reinterpret_cast<const uint32_t*>(k + d);
+    s = fmaf(__uint_as_float(a << 16), __uint_as_float(b << 16), s);
+    s = fmaf(__uint_as_float(a & 0xFFFF0000u), __uint_as_float(b & 0xFFFF0000u), s);
+  }
+  return s;
+}
+
 // The steps of a part's tiles: 64 keys each, one for a tile with 64 keys or fewer.
 struct Step {
   int x, h;
@@ -179,7 +191,8 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
   float* s_k2 = reinterpret_cast<float*>(bars + 32);          // [kExpRing][8] K's scale of 16 keys each
   int* s_ve = reinterpret_cast<int*>(s_k2 + kExpRing * 8);    // [kExpRing][8] V's exponent
   uint32_t* s_bad = reinterpret_cast<uint32_t*>(s_ve + kExpRing * 8);  // [kTailRing][4] nodes with a non-finite V
-  uint32_t* tmem_slot = s_bad + 4 * kTailRing;
+  uint32_t* s_odd = s_bad + 4 * kTailRing;                             // [kTailRing][4] nodes with a non-finite K
+  uint32_t* tmem_slot = s_odd + 4 * kTailRing;
   volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -450,13 +463,15 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
             else
               dev_flag(dev_err, E3_DEV_ERR_CAPACITY);
           }
-          // a node with a NaN or an Inf leaves the product: its scores get a NaN factor, rows
-          // that see its V are marked
+          // a node with a NaN or an Inf leaves the products: the scores of its K are worked out by the rows that see it,
+          // rows that see its V are marked
           ask_rows(static_cast<const __nv_bfloat16*>(tail.k), own, sK + slot * kCodeB, sK + second * kCodeB, dw * 32, lane);
           unsigned char* slab = dst + dw * 32 * 128;
           bring_rows(static_cast<const __nv_bfloat16*>(tail.v), own, slab, lane);
           const int ex = rows_to_parts<true>(sK + slot * kCodeB, sK + second * kCodeB, dw * 32, lane);
-          s_fac[fac * kKeys + dw * 32 + lane] = ex == 1000 ? __int_as_float(0x7FC00000) : pow2f(ex / 2);
+          s_fac[fac * kKeys + dw * 32 + lane] = ex == 1000 ? 0.0f : pow2f(ex / 2);
+          const uint32_t odd = __ballot_sync(0xFFFFFFFFu, ex == 1000);
+          if (lane == 0) s_odd[fac * 4 + dw] = odd;
           const uint32_t top = row_top(slab, lane);
           const uint32_t bad = __ballot_sync(0xFFFFFFFFu, top >= 0x7F80u);
           if (lane == 0) s_bad[fac * 4 + dw] = bad;
@@ -605,6 +620,26 @@ verify8_tc_kernel(const __nv_bfloat16* __restrict__ Q, const __grid_constant__ C
 #pragma unroll
                 for (int j = 0; j < 16; ++j) z[j] = sb & (1u << j) ? z[j] : 0xFF800000u;
                 tmem_st16(tB + 16 * d, z);
+              }
+              if (nodes && (s_odd[slot * 4 + 2 * h] | s_odd[slot * 4 + 2 * h + 1])) {
+                tmem_st_wait();  // (the scores below go over these)
+#pragma unroll 1
+                for (int w = 0; w < 2; ++w)
+#pragma unroll 1
+                  for (uint32_t odd = s_odd[slot * 4 + 2 * h + w]; odd != 0u; odd &= odd - 1u) {
+                    const int col = 32 * w + __ffs(odd) - 1;
+                    float score = -INFINITY;
+                    if (row_ok && ((see >> col) & 1ull)) {
+                      const int kvh = p.pq / g.RG, head = kvh * g.G + (((p.pq - kvh * g.RG) * RT + grp) * kRows + r) - node * g.G;
+                      const int j = (x - p.NT) * kKeys + h * kStep + col, pi = j / tail.page_size;
+                      const int page = tail.page_table[static_cast<size_t>(p.b) * tail.max_pages + pi];  // (a good one: its row was read)
+                      score = odd_score(Q + ((static_cast<size_t>(p.b) * g.R + node) * g.H + head) * kHD,
+                                        static_cast<const __nv_bfloat16*>(tail.k) +
+                                            ((static_cast<size_t>(page) * g.KVH + kvh) * tail.page_size + (j - pi * tail.page_size)) * kHD) *
+                              (sm_scale * kLog2e);
+                    }
+                    tmem_st1(tB + col, __float_as_uint(score));
+                  }
               }
               tmem_st_wait();
             }

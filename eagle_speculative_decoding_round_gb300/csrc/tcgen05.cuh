@@ -208,6 +208,9 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
 }
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(v) : "memory");
+}
 __device__ __forceinline__ unsigned long long pair(float x, float y) {
   return static_cast<unsigned long long>(__float_as_uint(x)) | (static_cast<unsigned long long>(__float_as_uint(y)) << 32);
 }

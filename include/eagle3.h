@@ -605,7 +605,8 @@ E3_API e3_status kv8_read(const e3_kv8_layer* layers, const e3_kv_layer* dst, in
 
 /* ---------------------------------------------------------------------------
  * tree_verify_attn8: tree_verify_attn over a prefix held in 8 bits; arguments, tail,
- * masks, rows without a key and errors as tree_verify_attn4.
+ * masks, rows without a key and errors as tree_verify_attn4.  A node whose score is -Inf (an Inf
+ * in its K) weighs 0.
  * Arithmetic: products exact but for the weights, which are good to 2^-8, sums in fp32, off by
  *   at most 2^-10 of the magnitudes' (the tensor core cuts off what it adds up).
  *   Values of V up to 2^85 in magnitude cannot overflow them (up to 2^100 where max_kv_len is

@@ -182,3 +182,33 @@ def test_verify_attn8_rows_of_uneven_values(R, G, top):
             e = (2.0 ** -8 + grow) * mag + 2.0 ** -32 * codes.sum(0)[None]
             bad = np.abs(O[0, :, h] - o) - (e + 2.0 ** -8 * (np.abs(o) + e))
             assert np.all(bad <= 0), (f, h, bad.max())
+
+
+@pytest.mark.parametrize("R,G,hd,page", [(6, 4, 128, 64), (40, 1, 128, 16), (40, 4, 128, 64), (70, 2, 128, 16), (200, 1, 128, 64), (256, 2, 128, 128),
+                                         (90, 2, 64, 64)])
+def test_verify_attn8_nodes_with_scores_of_minus_inf(R, G, hd, page):
+    """-Inf in nodes' K where Q is positive: those nodes weigh 0, a row that sees no other key gets 0 and -Inf.  +Inf, a NaN: rows
+    that see such a node get NaN, the others are exact.  Both kernels, both widths of the larger one's tile."""
+    d = attn_inputs(R + G, 3, R, 2 * G, 2, hd, [0, 20, 300], page, 16)
+    d["Q"] = np.abs(d["Q"])
+    gone = np.zeros((3, R), bool)
+    gone[0, :2], gone[1, [0, R // 2, R - 1]], gone[2] = True, True, np.arange(R) % 3 == 0
+    d["see"][0, 2] = False
+    d["see"][0, 2, :2] = True                          # (what it sees is gone)
+    for b in range(3):
+        for j in np.flatnonzero(gone[b]):
+            d["tail"][0][d["tpt"][b, j // page], :, j % page, (5 * j) % hd] = -np.inf
+    O, lse, err = attn_call(d)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    want = dict(d, see=d["see"] & ~gone[:, None], tail=[np.where(np.isinf(d["tail"][0]), 0.0, d["tail"][0]), d["tail"][1]])
+    attn_check(want, O, lse)
+    assert not want["see"][0, :3].any() and torch.all(O[0, :3] == 0)
+    j = R - 2  # one node more, with scores that are no numbers' neighbours
+    for value in (np.inf, np.nan):
+        d["tail"][0][d["tpt"][2, j // page], :, j % page, 7] = value
+        O2, lse2, _ = attn_call(d)
+        torch.cuda.synchronize()
+        see = torch.from_numpy(d["see"][2, :, j]).cuda()
+        assert torch.isnan(O2[2][see]).all() and torch.isnan(lse2[2][see]).all() and see.any()
+        assert torch.equal(O2[2][~see], O[2][~see]) and torch.equal(O2[:2], O[:2])
