@@ -13,6 +13,7 @@ from gpu_util import host
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
+    from eagle_speculative_decoding_round_gb300 import eagle3 as e3
     from test_gpu_kv8 import attn_call, attn_check, attn_inputs
 
 
@@ -212,3 +213,31 @@ def test_verify_attn8_nodes_with_scores_of_minus_inf(R, G, hd, page):
         see = torch.from_numpy(d["see"][2, :, j]).cuda()
         assert torch.isnan(O2[2][see]).all() and torch.isnan(lse2[2][see]).all() and see.any()
         assert torch.equal(O2[2][~see], O[2][~see]) and torch.equal(O2[:2], O[:2])
+
+
+@pytest.mark.parametrize("R,KVH", [(33, 152), (140, 152), (1, 1824), (9, 1216)])
+@pytest.mark.parametrize("P", [32640, 32768, 32769, 65536, 65600])
+def test_verify_attn8_long_sums_borders(R, KVH, P):
+    """Prefixes that end where the sums leave the accumulators, with the nodes behind: a fold before a tile of nodes, none, one more.
+    The same call in a graph that was captured on a short prefix."""
+    d = long_inputs(R + P, 1, R, KVH, KVH, 128, [P])
+    dev = {}
+    O, lse, err = attn_call(d, dev=dev)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    adds, at = adds_tc if R > 32 else adds_granules, dict(heads=(0, KVH - 1), rows=sorted({0, R - 1}))
+    check_long(d, O, lse, adds, **at)
+    need = e3.eagle3_verify8_workspace_bytes(1, R, KVH, KVH, 128, P)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    out = (torch.full_like(O, 55.0), torch.full_like(lse, 55.0))
+    dev["lens"].fill_(70)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        attn_call(d, dev=dev, ws=ws, out=out, err=err)
+    for keys in (70, P):
+        dev["lens"].fill_(keys)
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        check_long(dict(d, lens=[keys]), *out, adds, **at)
+    assert torch.equal(out[0], O) and torch.equal(out[1], lse)

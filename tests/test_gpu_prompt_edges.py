@@ -14,7 +14,8 @@ from gpu_util import host
 pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
-    from test_gpu_prompt import call, inputs
+    from eagle_speculative_decoding_round_gb300 import eagle3 as e3
+    from test_gpu_prompt import call, check, inputs
 
 
 def check_inf(d, O, lse):
@@ -213,3 +214,56 @@ def test_prompt_attn_bf16_long_sums_keep_what_they_have_met(H, KVH, hd, ctx):
     o = host(O2)
     assert np.isnan(o[..., 3]).all() and torch.equal(lse, lse2)
     assert np.array_equal(np.delete(o, 3, -1), np.delete(host(O), 3, -1))
+
+
+def test_prompt_attn_bounds_of_long_contexts_over_short_ones():
+    """A bound above 32768 keys takes the kernel for long items: on short requests (one call cut along its keys, one not) it answers the
+    same, in a graph too, whose replay meets a long context; a wait that runs out in it ends the call."""
+    for H, KVH, rows, ctx in ((16, 4, [70, 0, 3, 300], [10, 0, 2000, 0]), (8, 8, [20] * 320, [5] * 320)):
+        d = inputs(H, H, KVH, 64, rows, ctx, 16, gap=1)
+        dev = {}
+        O, lse, err = call(d, dev=dev)
+        O2, lse2, err2 = call(d, dev=dev, max_ctx=40000)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0 and int(err2.item()) == 0
+        check(d, O2, lse2)
+    _, _, err = call(d, dev=dev, max_ctx=40000, flags=e3.E3_KV_SELFTEST_STALL)
+    torch.cuda.synchronize()
+    assert int(err.item()) == e3.E3_DEV_ERR_TIMEOUT
+    d = long_inputs(5, 152, 152, 64, [2], [40000], "bf16", zeros=False)
+    dev = {}
+    O, lse, err = call(d, dev=dev)
+    need = e3.eagle3_prompt_workspace_bytes(1, d["total"], 2, 152, 152, 64, 40000, e3.E3_BF16)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    out = (torch.full_like(O, 55.0), torch.full_like(lse, 55.0))
+    dev["ctx"].fill_(100)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(d, dev=dev, ws=ws, out=out, err=err)
+    for ctx in (100, 40000, 32766, 32768, 700):
+        dev["ctx"].fill_(ctx)
+        g.replay()
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        check_long(dict(d, ctx=[ctx]), *out, adds_bf16, heads=(0, 151))
+        if ctx == 40000:
+            assert torch.equal(out[0], O) and torch.equal(out[1], lse)
+
+
+def test_prompt_attn_long_sums_on_two_streams():
+    """Two long calls at once, each with scratch of its own; fp32 beside them."""
+    a = long_inputs(6, 152, 152, 64, [1], [70000], "bf16", zeros=False)
+    b = long_inputs(7, 4, 2, 128, [2], [20000], "f32", zeros=False)
+    da, db = {}, {}
+    call(a, dev=da)
+    call(b, dev=db)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(3)], []
+    for _ in range(2):
+        for s, d, dev in zip(streams, (a, a, b), (da, da, db)):
+            with torch.cuda.stream(s):
+                outs.append((d, call(d, dev=dev, stream=s)))
+    torch.cuda.synchronize()
+    for d, (O, lse, err) in outs:
+        assert int(err.item()) == 0
+        check_long(d, O, lse, adds_bf16 if d is a else adds_fp32, heads=(0, d["H"] - 1))
