@@ -14,8 +14,7 @@
 //
 // Bound: FMAs, and for small prompts the latency of a tile's chain (loads, S, softmax, O).
 // Measured on a GB300: 3 prompts of 15 to 131 rows behind up to 128 keys, 4 heads of 64: 18 us
-// (tiles of 64 rows only, K and V in one buffer: 39); 1000 rows, 32 query heads of 128: 259 us, 32
-// TFLOP/s.
+// (tiles of 64 rows only: 31); 1000 rows, 32 query heads of 128: 286 us, 29 TFLOP/s.
 #include <type_traits>
 
 #include "e3_common.cuh"
@@ -278,7 +277,7 @@ cudaError_t launch_rows(const void* Q, const e3_kv_layer& kv, const PromptGeom& 
 }
 
 // Tiles of 64 rows where those are an item for every SM, else of 16.  (32 query and 8 KV heads of 128, tiles of 64 and 16:
-// 1000 rows 259 and 573 us, 200 rows 42.0 and 43.8; 4 heads of 64, one row behind 5000 keys 426 and 309 us.)
+// 1000 rows 286 and 555 us, 300 rows 53 and 64, 200 rows 40 and 38; 4 heads of 64, one row behind 5000 keys 438 and 283 us.)
 template <int HD>
 cudaError_t launch_simt(const void* Q, const e3_kv_layer& kv, PromptGeom g, float sm_scale, void* O, float* lse, int32_t* dev_err,
                         cudaStream_t s) {

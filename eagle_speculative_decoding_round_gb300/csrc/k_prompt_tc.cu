@@ -25,9 +25,10 @@
 //
 // Bound: the tensor cores, with the exponentials (one a product's 2 * 64 multiply-adds) close
 // behind, and under a long load the power limit.  Measured on a GB300, 32 query and 8 KV heads of
-// 128: 32768 rows 5.54 ms, 1.59 PFLOP/s (82% of a library product's burst rate; 1.82 GHz under the
+// 128: 32768 rows 5.46 to 5.60 ms, 1.6 PFLOP/s (82% of a library product's burst rate; 1.82 GHz under the
 // power cap); 16 prompts of 512 to 8192 rows 2.25 ms; 2048 rows 33 us; 4 pieces of 100 to 257 rows
-// behind 12288 to 16384 keys, 64 query heads, 262 to 277 us (306 without shares).  What the design
+// behind 12288 to 16384 keys, 64 query heads, 277 us (306 without shares).  Heads of 64, half the products
+// for as many exponentials: 32768 rows 4.28 ms, 8192 rows 0.30 ms.  What the design
 // gained, at 32768 rows: one issuing warp for both groups 8.60 ms, one for each 6.70; S of one tile in
 // flight 6.37, steps of 64 keys in two buffers 5.64; P stored piece by piece under the exponentials
 // 5.54.
@@ -56,7 +57,7 @@ constexpr float kLowest = -3.402823466e38f;
 constexpr int kShift = 8;        // an item has 2 * kRows flat rows
 // Steps whose products tensor memory sums up.  The tensor core cuts a sum off where it adds to it: 4194304 keys with V of
 // one sign lost 2.5% so, which is 2^-12 for 32768.  Longer sums go on in fp32 in the CTA's record (one row of 152 heads of
-// 128 behind 131072 keys: 1.22 ms whole, 1.27 so; behind 4194304 36.0 and 37.5).
+// 128 behind 131072 keys: 1.22 ms whole, 1.27 so; behind 4194304 36.0 and 37.5; 40000 rows 7.92 and 8.10).
 constexpr int kFold = 512;
 
 template <int HD>

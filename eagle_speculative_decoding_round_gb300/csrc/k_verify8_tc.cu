@@ -25,7 +25,7 @@
 // exponentials, P, O, each handed on by a barrier; and, for a short prefix, a part's own cost of
 // about 20 us (Q, its record, the merge).  Measured on a GB300, 32 query and 8 KV heads of 128:
 // 32 requests of 512 to 8192 keys with 61 nodes 172 us (the codes: 285 MB), one
-// request of 65536 keys with 33 nodes 74 us, one of 2048 keys with 61 nodes 19.4 us.  What the
+// request of 65536 keys with 33 nodes 72 us, one of 2048 keys with 61 nodes 19.4 us.  What the
 // design gained: the granule kernel alone 872, 185 and 30 us; V in fp16 with a unit that follows
 // the largest scale 232, 90 and 22; K in two slots 213 and 87 (batch, long); masks and factors
 // found between the softmax's steps 213 and 82; Q read row by row, a row to a thread, 211 and 80.

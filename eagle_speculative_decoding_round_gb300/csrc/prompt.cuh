@@ -86,7 +86,9 @@ __device__ __forceinline__ PromptItem find_prompt_item(const PromptGeom& g, cons
   return it;
 }
 // The same for calls of more requests than a warp has lanes, which are taken as they come: a search by keys would read all of
-// them again for each bit of a length (2000 requests of one row 3.85 ms, so 0.43; 64 of 100 to 900 rows 256 us, so 215).
+// them again for each bit of a length (2000 requests of one row 3.85 ms, so 0.43; 64 of 100 to 900 rows 256 us, so 215).  What
+// that costs: a long request that comes last begins last (33 of them, 32 of 200 rows and one of 8000: 357 us where it comes
+// first, 420 where last; 32 of 1000 and one of 4000: 351 and 365).
 // `rank` grows from call to call, and `seen` goes with it.
 struct PromptSeen {
   int b0;          // the requests from here on have not been passed
@@ -165,9 +167,10 @@ __device__ __forceinline__ PromptItem numbered_item(const PromptGeom& g, const P
 }
 // How a call is cut: equal shares of the cost from `from` on, one for each CTA.  Where the requests' keys are about as many, the
 // items before that, as many full waves of CTAs as there are, go to the CTAs whole: tiles of rows that read the same keys then
-// read them at the same time.  (Four pieces of 100 to 257 rows behind 12288 to 16384 keys 263 us, without whole waves 278 and
-// 1.28 GB of DRAM reads; three of 250 rows behind 12000 keys 205 and 220; four of 200 rows behind 500 to 20000 keys 188 without
-// and 273 with them, behind 10000 to 20000 keys 294 and 314.)
+// read them at the same time.  (Four pieces of 100 to 257 rows behind 12288 to 16384 keys, call after call: 277 us, without
+// whole waves 309, with four times the DRAM reads (331 MB, 1.28 GB); a call by itself, the card idle before it, takes the same
+// with and without, 286 and 284.  Three of 250 rows behind 12000 keys, by itself: 210 and 223.  Where the keys are not alike:
+// four of 200 rows behind 500 to 20000 keys 188 without and 273 with them, behind 10000 to 20000 keys 294 and 314.)
 struct PromptShares {
   int waves;
   long long from, total, share;
