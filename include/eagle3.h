@@ -607,8 +607,8 @@ E3_API e3_status kv8_read(const e3_kv8_layer* layers, const e3_kv_layer* dst, in
  * tree_verify_attn8: tree_verify_attn over a prefix held in 8 bits; arguments, tail,
  * masks, rows without a key and errors as tree_verify_attn4.  A node whose score is -Inf (an Inf
  * in its K) weighs 0.
- * Arithmetic: products exact but for the weights, which are good to 2^-8, sums in fp32, off by
- *   at most 2^-10 of the magnitudes' (the tensor core cuts off what it adds up).
+ * Arithmetic: products exact but for the weights, which are good to 2^-8, sums in fp32, over n
+ *   keys off by at most 2^-10 + n 2^-37 of the magnitudes' (the tensor core cuts off what it adds up).
  *   Values of V up to 2^85 in magnitude cannot overflow them (up to 2^100 where max_kv_len is
  *   below 2^18).  Up to 32 query rows per KV head, and for heads of 64: Q's values below 2^-24
  *   of their row's largest lose bits, and so do weights below 2^-21 of their row's largest in
@@ -650,14 +650,14 @@ E3_API size_t eagle3_verify8_workspace_bytes(int B, int R, int n_q_heads, int n_
  * outputs unwritten; a page id out of range sets it and makes them unspecified.  Rows of
  * two requests must not overlap.
  * Arithmetic: bf16: products in bf16 with fp32 sums, weights good to 2^-8 and summed
- *   before that rounding, V up to 2^90 in magnitude cannot overflow the sums, which are off
- *   by at most 2^-10 of the magnitudes' (the tensor core cuts off what it adds up); fp32: fp32
- *   throughout, a sum over n keys off by at most (128 + sqrt(n) / 2) 2^-24 of that of the magnitudes.
+ *   before that rounding, V up to 2^90 in magnitude cannot overflow the sums, which over n
+ *   keys are off by at most 2^-10 + n 2^-37 of the magnitudes' (the tensor core cuts off what it
+ *   adds up); fp32: fp32 throughout, such a sum off by at most (128 + sqrt(n) / 2) 2^-24.
  * Limits: head_dim 64 or 128 (fp32: any multiple of 32 up to 256); n_q_heads %
  *   n_kv_heads == 0; page_size % 16 == 0; 1 <= B <= 65535; 1 <= max_rows;
  *   1 <= n_total, n_total * n_q_heads < 2^31; max_kv_len + max_rows <= 2^30 (bf16:
  *   2^25, some 0.4 s for one tile of rows, within the bound of the kernel's waits).  Q, O 16-byte
- *   aligned; E3_KV_PREFIX_STABLE in kv->flags is accepted (and not used).
+ *   aligned, other arrays to their elements; E3_KV_PREFIX_STABLE in kv->flags is accepted (and not used).
  * ws: eagle3_prompt_workspace_bytes(...) bytes of device scratch (may be 0, ws then NULL),
  *   16-byte aligned; calls that may overlap on the GPU need scratch of their own.
  * ------------------------------------------------------------------------- */
